@@ -404,6 +404,242 @@ int verify_attn_accept(const float *target_logits, const float *draft_logits,
                        int T, int vocab, uint64_t seed, void *workspace, int32_t *out_tokens,
                        int32_t *num_accepted, void *stream);
 
+/* Element type of a tensor outside the cache. */
+typedef enum {
+    VA_FLOAT_BF16 = 0,
+    VA_FLOAT_FP16 = 1,
+    VA_FLOAT_FP32 = 2
+} va_float_type;
+
+/* Rotary positions with several axes.  Text has one running position; a token
+ * of an image or a video has several (time, row, column).  The first 2 P
+ * elements of a head (P = num_pairs) are P pairs, and pair i is turned by the
+ * position on its own axis:
+ *     (a, b)  = (x[i], x[i + P])          adjacent = 0 (the two halves)
+ *               (x[2 i], x[2 i + 1])      adjacent = 1
+ *     theta_i = position[axis[i]] * inv_freq[i]
+ *     a' = scale (a cos theta_i - b sin theta_i)
+ *     b' = scale (b cos theta_i + a sin theta_i)
+ * Elements from 2 P on are left as they are.  The inverse turns by -theta_i
+ * with the same scale: the transposed map, so it takes the gradient of the
+ * rotated tensor to the gradient of the tensor.
+ *
+ * va_rope describes the rotation; it is host data, filled by
+ * verify_attn_rope_init and copied into every launch, so it may be changed or
+ * freed as soon as a call has returned.  turn[i] is inv_freq[i] / (2 pi), the
+ * part of a full turn that one step of position makes, times 2^64 and modulo
+ * 2^64: position * turn[i] modulo 2^64 is then the angle's part of a turn
+ * without a rounding that grows with the position, for every int32 position. */
+#define VA_ROPE_MAX_PAIRS 128
+#define VA_ROPE_MAX_AXES 4
+typedef struct {
+    uint64_t turn[VA_ROPE_MAX_PAIRS];
+    uint8_t axis[VA_ROPE_MAX_PAIRS];
+    int32_t num_pairs, num_axes, adjacent;
+    float scale;
+} va_rope;
+
+/* Fill *rope (host only).  inv_freq [num_pairs] (finite, magnitude at most
+ * 2^20) and axis [num_pairs] (each in [0, num_axes); NULL: all 0) are host
+ * arrays; 1 <= num_pairs <= VA_ROPE_MAX_PAIRS, 1 <= num_axes <=
+ * VA_ROPE_MAX_AXES, scale finite.  VA_ERR_INVALID_ARGUMENT otherwise. */
+int verify_attn_rope_init(va_rope *rope, const double *inv_freq, const int32_t *axis,
+                          int num_pairs, int num_axes, int adjacent, float scale);
+
+/* Heads of a batch, [num_seqs, T, num_heads, head_dim]: strides in elements,
+ * head_dim contiguous, so a slice of a fused projection or a [num_seqs,
+ * num_heads, T, head_dim] tensor is passed as it lies. */
+typedef struct {
+    void *data;
+    int64_t stride_seq, stride_token, stride_head;
+    int num_heads;
+} va_heads;
+
+/* Positions, int32 on the device: that of axis a, sequence b, token t is
+ * data[a * stride_axis + b * stride_seq + t * stride_token] (strides in
+ * elements, 0 to share one among them). */
+typedef struct {
+    const int32_t *data;
+    int64_t stride_axis, stride_seq, stride_token;
+} va_positions;
+
+/* Rotate q and k (k and k_out may both be NULL) of one batch in one launch.
+ * Each output is its input's own memory with the same strides (in place), or
+ * memory that overlaps neither input; its elements must not overlap each
+ * other.  head_dim >= 2 * num_pairs, any size up to 1024; num_seqs, T >= 0 (nothing
+ * is launched for 0).  Arithmetic in binary32, one rounding to the type.
+ * Returns VA_OK when enqueued, VA_ERR_INVALID_ARGUMENT, VA_ERR_UNSUPPORTED
+ * for an unknown type, VA_ERR_CUDA. */
+int verify_attn_rope(const va_rope *rope, const va_positions *positions, va_float_type type,
+                     int num_seqs, int T, int head_dim, const va_heads *q,
+                     const va_heads *q_out, const va_heads *k, const va_heads *k_out,
+                     int inverse, void *stream);
+
+/* Rotate q and k and append k and v to the paged cache, in one launch: the
+ * step before verify attention.  q, k_new, v_new bf16 with num_heads =
+ * num_q_heads, num_kv_heads, num_kv_heads (q and q_out may both be NULL).
+ * q_out bf16, contiguous [num_seqs, T, num_q_heads, head_dim] on a 16-byte
+ * boundary, receives the rotated q (it may be q's own memory where q is
+ * contiguous).  The cache receives what verify_attn_kv_append stores, with
+ * its rule applied to the rotated k in binary32: the scale and the codes are
+ * taken from the unrounded rotated row (a bf16 cache: one rounding), not from
+ * a bf16 copy of it.  v is stored as verify_attn_kv_append stores it.
+ * positions NULL: every axis is the token's place in its sequence,
+ * L_b - T + t.  Cache, block table, seq_lens, num_pages and flags as for
+ * verify_attn_kv_append; rows whose block lies outside the block table's row
+ * are skipped and flagged as well.  head_dim in {64, 128, 256}; num_pairs a
+ * multiple of head_dim / 32 unless the pairs are adjacent; q, k_new and v_new
+ * start on a 16-byte boundary and their strides are multiples of 8.  Returns
+ * as verify_attn_kv_append. */
+int verify_attn_rope_append(const va_rope *rope, const va_positions *positions, int num_seqs, int T,
+                            int head_dim, const va_heads *q, void *q_out, const va_heads *k_new,
+                            const va_heads *v_new, va_kv_dtype kv_dtype, void *k_pages,
+                            void *v_pages, float *k_scale, float *v_scale,
+                            const int32_t *block_table, int block_table_stride,
+                            const int32_t *seq_lens, int num_pages, int *flags, void *stream);
+
+/* A row of probabilities per (sequence, position): element i of position t of
+ * sequence b is data[b * stride_seq + t * stride_pos + i]. */
+typedef struct {
+    const void *data;
+    int64_t stride_seq, stride_pos;
+} va_rows;
+
+/* Speculative acceptance from given probabilities and given random numbers.
+ * verify_attn_accept starts from raw logits and draws its own numbers; this
+ * entry takes the distributions as the caller made them (after top-k, top-p,
+ * penalties or masks) and the caller's uniforms, so a caller with a generator
+ * of its own, or one that replays a recorded run, decides exactly what it
+ * would decide.  For sequence b with n_b = draft_lens[b] drafts (T when
+ * draft_lens is NULL; clamped to [0, T]), p = target_probs, q = draft_probs:
+ *   draft t is accepted while u_accept[b, t] * q_t(d_t) < p_t(d_t) (the exact
+ *     product; q_t(d_t) = 1 when draft_probs is NULL, a point-mass proposal;
+ *     a token outside [0, vocab) or a NaN is rejected);
+ *   at the first rejection t = n the weights are w_i = max(0, p_n(i) -
+ *     q_n(i)) (the proposal's point mass when draft_probs is NULL), or p_n(i)
+ *     where those are all zero; when all n_b drafts are accepted n = n_b and
+ *     w_i = p_n(i);
+ *   the emitted token is the smallest i with w_0 + .. + w_i > u_emit[b] * W,
+ *     W the sum of all w (inversion of the cumulative distribution).
+ * The weights need not sum to one.  Each p and q counts as a number in [0, 1]
+ * (NaN and negative values as 0, larger ones as 1), cut to a multiple of
+ * 2^-62; the sums are exact in 128-bit integers, so the token does not depend
+ * on how the work is split.  u_emit counts as in [0, 1 - 2^-24] (NaN as 0).
+ * A row with no weight at all emits -1.
+ * Outputs as verify_attn_accept: out_tokens[b, 0 .. n-1] = the accepted
+ * drafts, out_tokens[b, n] = the emitted token, -1 after it; num_accepted[b]
+ * = n.
+ * Layouts (device): target_probs [num_seqs, T + 1, vocab] and draft_probs
+ * [num_seqs, T, vocab] (data NULL or the pointer NULL: point mass) of one
+ * `type`, rows contiguous; draft_tokens int32 [num_seqs, T], draft_lens int32
+ * [num_seqs] or NULL, u_accept fp32 [num_seqs, T], u_emit fp32 [num_seqs],
+ * out_tokens int32 [num_seqs, T + 1], num_accepted int32 [num_seqs].
+ * T >= 0 (0: one sample of p_0 per sequence; draft_tokens and u_accept may
+ * then be NULL), 1 <= num_seqs <= 65535, vocab >= 1.  No workspace.  Returns
+ * VA_OK when enqueued, VA_ERR_INVALID_ARGUMENT, VA_ERR_UNSUPPORTED for an
+ * unknown type, VA_ERR_CUDA. */
+int verify_attn_accept_probs(const va_rows *target_probs, const va_rows *draft_probs,
+                             va_float_type type, const int32_t *draft_tokens,
+                             const int32_t *draft_lens, const float *u_accept, const float *u_emit,
+                             int num_seqs, int T, int vocab, int32_t *out_tokens,
+                             int32_t *num_accepted, void *stream);
+
+/* The pages of a paged cache: which are free, who holds which, and their
+ * care between verify steps.  The block table and seq_lens are the ones that
+ * verify_attn, verify_attn_kv_append and verify_attn_rope_append read.  All
+ * pointers but `buffers` are device memory owned by the caller:
+ *     block_table int32 [num_seqs, block_table_stride]; sequence b holds its
+ *                 entries 0 .. ceil(seq_lens[b] / 16) - 1
+ *     seq_lens    int32 [num_seqs]; 0 for a slot that holds nothing
+ *     ref_count   int32 [num_pages]  how many block-table entries hold a page
+ *     free_list   int32 [num_pages]  a stack of the free pages: entries 0 ..
+ *                 num_free - 1, the last one taken first; the entries above
+ *                 keep what they held
+ *     num_free    int32 [1]
+ *     flags       int32 [1] or NULL; the calls only OR bits into it:
+ *                   VA_PAGES_BAD_ENTRY   a block-table or free-list entry
+ *                                        outside [0, num_pages): skipped
+ *                   VA_PAGES_EXHAUSTED   too few free pages: the sequence (or
+ *                                        fork) is as it was
+ *                   VA_PAGES_BAD_REQUEST a length outside [0, 16 *
+ *                                        block_table_stride], a sequence
+ *                                        index outside [0, num_seqs), a fork
+ *                                        into a slot that is not empty or
+ *                                        that an earlier fork of the call has
+ *                                        taken: not carried out
+ *                   VA_PAGES_BAD_COUNT   a held page with no references, or a
+ *                                        num_free that disagrees with them
+ *     buffers     host array of the pools that the pages lie in: page p of
+ *                 buffer i is page_bytes bytes at data + p * page_bytes (the K
+ *                 pages, V pages and scales of every layer; 16-byte aligned,
+ *                 page_bytes a multiple of 16); all are copied alike
+ *     workspace   at least verify_attn_pages_workspace_bytes(num_seqs,
+ *                 num_pages) bytes, 16-byte aligned; needs no initialisation
+ * A pool starts with ref_count and seq_lens 0, free_list any permutation of
+ * the pages and num_free = num_pages.  Calls on one pool, and those that read
+ * its block table, must be ordered on one stream.  Results do not depend on
+ * timing: whole numbers, counted and ordered by page and sequence.
+ * Limits: num_seqs and num_forks <= VA_PAGES_MAX_SEQS, num_pages <= 2^24,
+ * num_seqs * block_table_stride < 2^31.  Every call returns VA_OK when enqueued,
+ * VA_ERR_INVALID_ARGUMENT for null or misaligned pointers and sizes out of
+ * range, VA_ERR_CUDA if a launch fails. */
+#define VA_PAGES_MAX_SEQS 8192
+#define VA_PAGES_BAD_ENTRY 1
+#define VA_PAGES_EXHAUSTED 8
+#define VA_PAGES_BAD_REQUEST 16
+#define VA_PAGES_BAD_COUNT 32
+
+typedef struct {
+    void *data;
+    size_t page_bytes;
+} va_page_buffer;
+
+typedef struct {
+    int32_t *block_table, *seq_lens, *ref_count, *free_list, *num_free, *flags;
+    int block_table_stride, num_seqs, num_pages, num_buffers;
+    const va_page_buffer *buffers;
+    void *workspace;
+} va_page_pool;
+
+/* 0 for sizes that the calls reject. */
+size_t verify_attn_pages_workspace_bytes(int num_seqs, int num_pages);
+
+/* Change the sequences' lengths to new_lens [num_seqs] (device; a negative
+ * entry leaves its sequence alone): give pages back, take pages.
+ *   1. A sequence that shrinks (to 0: is freed) drops its pages from
+ *      ceil(new / 16) on and those table entries become -1.  Pages that
+ *      nobody holds any more go onto the free list, in ascending order.
+ *   2. Growing sequences are then served in order b = 0, 1, ..: each takes
+ *      the pages of its new blocks, one after the other from the top of the
+ *      list.  One whose partly filled last page is also held by others (it
+ *      was cut back into a page that a fork shares) first takes a page for a
+ *      copy of its own, since its next tokens will be written there.  From
+ *      the first sequence on for which the list is too short, all that need
+ *      a page are refused.
+ *   3. Shared pages that all their holders replaced in step 2 are then given
+ *      back, in ascending order.
+ * So the call after a verify step is new_lens[b] = accepted length + the next
+ * block's tokens. */
+int verify_attn_pages_resize(const va_page_pool *pool, const int32_t *new_lens, void *stream);
+
+/* Fork sequences: fork f makes the empty slot children[f] a copy of the first
+ * lens[f] tokens (lens NULL: all) of parents[f], for samples, beams or a
+ * prefix kept for later requests.  share != 0: the full pages are held in
+ * common (ref_count + 1) and a partly filled last page is copied; share = 0:
+ * every page is copied.  Pages are taken in order f = 0, 1, .. and block
+ * order; from the first fork on for which the list is too short, all that
+ * need a page are refused.  parents, children, lens: device, [num_forks];
+ * num_forks >= 0.  The lengths are those before the call. */
+int verify_attn_pages_fork(const va_page_pool *pool, const int32_t *parents, const int32_t *children,
+                           const int32_t *lens, int num_forks, int share, void *stream);
+
+/* Move the held pages to the front of the pool: with n pages held, the k-th
+ * held page at or above n (ascending) goes to the k-th free place below n;
+ * block tables and counts follow.  The free list becomes num_pages - 1, ..,
+ * n, so that the lowest free page is taken next and the pages above the n-th
+ * can be given to something else. */
+int verify_attn_pages_compact(const va_page_pool *pool, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

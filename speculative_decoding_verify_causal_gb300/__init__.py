@@ -12,6 +12,12 @@ Layouts (see ``include/verify_attn.h``):
   bf16 / fp8-e4m3 (uint8 storage) / int8; k_scale / v_scale fp32
   [num_pages, 16, Hkv]; block_table int32 [B, stride]; seq_lens int32 [B];
   out bf16 [B, T, Hq, D]; lse fp32 [B, T, Hq].
+
+Around the verify step: ``verify_attn_rope`` and ``verify_attn_rope_append``
+(rotary positions with several axes, alone and with the KV append),
+``verify_attn_accept_probs`` (acceptance from given probabilities and random
+numbers) and ``PagePool`` with ``verify_attn_pages_resize`` / ``_fork`` /
+``_compact`` (the pages behind the block table).
 """
 from __future__ import annotations
 
@@ -29,6 +35,10 @@ KV_DTYPE_CODES = {"bf16": VA_BF16, "fp8_e4m3": VA_FP8_E4M3, "int8": VA_INT8, "in
 VA_PATH_AUTO, VA_PATH_WARP, VA_PATH_MMA = 0, 1, 2
 PATH_CODES = {"auto": VA_PATH_AUTO, "warp": VA_PATH_WARP, "mma": VA_PATH_MMA}
 PAGE_SIZE = 16
+VA_FLOAT_BF16, VA_FLOAT_FP16, VA_FLOAT_FP32 = 0, 1, 2
+ROPE_MAX_PAIRS, ROPE_MAX_AXES = 128, 4
+# bits of a page pool's flag word
+VA_PAGES_BAD_ENTRY, VA_PAGES_EXHAUSTED, VA_PAGES_BAD_REQUEST, VA_PAGES_BAD_COUNT = 1, 8, 16, 32
 
 STATUS_NAMES = {
     0: "VA_OK", -1: "VA_ERR_INVALID_ARGUMENT", -2: "VA_ERR_UNSUPPORTED",
@@ -61,6 +71,36 @@ class PlanInfo(ctypes.Structure):
 
     def as_dict(self):
         return {n: getattr(self, n) for n, _ in self._fields_}
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("turn", ctypes.c_uint64 * ROPE_MAX_PAIRS), ("axis", ctypes.c_uint8 * ROPE_MAX_PAIRS),
+                ("num_pairs", ctypes.c_int32), ("num_axes", ctypes.c_int32), ("adjacent", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_seq", ctypes.c_int64), ("stride_token", ctypes.c_int64),
+                ("stride_head", ctypes.c_int64), ("num_heads", ctypes.c_int)]
+
+
+class _Positions(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_axis", ctypes.c_int64), ("stride_seq", ctypes.c_int64),
+                ("stride_token", ctypes.c_int64)]
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_seq", ctypes.c_int64), ("stride_pos", ctypes.c_int64)]
+
+
+class _PageBuffer(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("page_bytes", ctypes.c_size_t)]
+
+
+class _PagePool(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("block_table", "seq_lens", "ref_count", "free_list", "num_free", "flags")
+                ] + [(n, ctypes.c_int) for n in ("block_table_stride", "num_seqs", "num_pages", "num_buffers")
+                     ] + [("buffers", ctypes.POINTER(_PageBuffer)), ("workspace", ctypes.c_void_p)]
 
 
 _lib = None
@@ -110,6 +150,18 @@ def _load():
         lib.verify_attn_accept.restype = I
         lib.verify_attn_validate_host.argtypes = [P, I, I, P, I, I, ctypes.POINTER(I), ctypes.POINTER(I)]
         lib.verify_attn_validate_host.restype = I
+        lib.verify_attn_rope_init.argtypes = [P, P, P, I, I, I, ctypes.c_float]
+        lib.verify_attn_rope.argtypes = [P, P, I, I, I, I, P, P, P, P, I, P]
+        lib.verify_attn_rope_append.argtypes = [P, P, I, I, I, P, P, P, P, I, P, P, P, P, P, I, P, I, P, P]
+        lib.verify_attn_accept_probs.argtypes = [P, P, I, P, P, P, P, I, I, I, P, P, P]
+        lib.verify_attn_pages_workspace_bytes.argtypes = [I, I]
+        lib.verify_attn_pages_workspace_bytes.restype = ctypes.c_size_t
+        lib.verify_attn_pages_resize.argtypes = [P, P, P]
+        lib.verify_attn_pages_fork.argtypes = [P, P, P, P, I, I, P]
+        lib.verify_attn_pages_compact.argtypes = [P, P]
+        for f in ("verify_attn_rope_init", "verify_attn_rope", "verify_attn_rope_append", "verify_attn_accept_probs",
+                  "verify_attn_pages_resize", "verify_attn_pages_fork", "verify_attn_pages_compact"):
+            getattr(lib, f).restype = I
         for f in ("verify_attn_plan", "verify_attn_plan_ex", "verify_attn", "verify_attn_with_plan",
                   "verify_attn_plan_get_info", "verify_attn_plan_describe", "verify_attn_plan_device_flags"):
             getattr(lib, f).restype = I
@@ -472,7 +524,377 @@ def verify_attn_accept(target_logits, draft_tokens, temperature, seed, draft_log
     return out, nacc
 
 
+def _float_code(t, name):
+    import torch
+    code = {torch.bfloat16: VA_FLOAT_BF16, torch.float16: VA_FLOAT_FP16, torch.float32: VA_FLOAT_FP32}.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected bfloat16, float16 or float32")
+    return code
+
+
+def _launch_on(device, stream):
+    """(stream handle, guard): a call runs on the tensors' device and on ``stream`` there (a
+    torch stream or a raw handle; default: torch's current stream of that device).  What the
+    call allocates is allocated inside the guard, so it belongs to that stream."""
+    import contextlib
+
+    import torch
+    if stream is None:
+        handle = torch.cuda.current_stream(device).cuda_stream
+        if torch.cuda.current_device() == device.index:
+            return handle, contextlib.nullcontext()
+        return handle, torch.cuda.device(device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    elif stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    return stream.cuda_stream, torch.cuda.stream(stream)
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _shaped(t, name, dtypes, shape):
+    """Device pointer of a contiguous CUDA tensor of that shape."""
+    p = _dev_ptr(t, name, dtypes)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return p
+
+
+def _heads(t, name, dtype, shape=None):
+    """A [B, T, H, D] tensor, any strides but a contiguous last dimension, as a ``va_heads``."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 4:
+        raise ValueError(f"{name} must be a CUDA tensor [B, T, H, D]")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    s = t.stride()
+    if s[3] != 1 and t.shape[3] > 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return _Heads(t.data_ptr(), s[0], s[1], s[2], t.shape[2])
+
+
+def _positions(t, rope, B, T):
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32:
+        raise ValueError("positions must be an int32 CUDA tensor")
+    if tuple(t.shape) != (rope.num_axes, B, T):
+        raise ValueError(f"positions must be [{rope.num_axes}, {B}, {T}], got {list(t.shape)}")
+    s = t.stride()
+    return _Positions(t.data_ptr(), s[0], s[1], s[2])
+
+
+class Rope:
+    """A rotation (``va_rope``): host data, made by ``verify_attn_rope_spec``."""
+
+    def __init__(self, struct):
+        self._struct = struct
+        self._ref = ctypes.byref(struct)
+
+    num_pairs = property(lambda self: self._struct.num_pairs)
+    num_axes = property(lambda self: self._struct.num_axes)
+    axis = property(lambda self: list(self._struct.axis[:self._struct.num_pairs]))
+
+
+def verify_attn_rope_spec(rotary_dim, base=1.0e6, inv_freq=None, sections=None, layout="blocked", pairing="half",
+                          scale=1.0) -> Rope:
+    """Describe a rotation of the first ``rotary_dim`` elements of each head.
+    ``inv_freq``: the ``rotary_dim / 2`` frequencies (default ``base ** (-i /
+    pairs)``).  ``sections``: how many pairs turn by each axis's position
+    (default: all by one axis); ``layout`` "blocked" puts the axes' pairs one
+    after the other, "dealt" deals pairs round to the axes that have some
+    left.  ``pairing`` "half" pairs element i with i + rotary_dim / 2,
+    "adjacent" 2 i with 2 i + 1.  ``scale`` multiplies the rotated elements."""
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even and at least 2")
+    pairs = int(rotary_dim) // 2
+    if pairs > ROPE_MAX_PAIRS:
+        raise ValueError(f"rotary_dim must be at most {2 * ROPE_MAX_PAIRS}")
+    if inv_freq is None:
+        inv_freq = float(base) ** (-np.arange(pairs, dtype=np.float64) / pairs)
+    freq = np.ascontiguousarray(np.asarray(inv_freq, np.float64).reshape(-1))
+    if freq.size != pairs:
+        raise ValueError(f"inv_freq must have {pairs} entries")
+    sections = [pairs] if sections is None else [int(n) for n in sections]
+    if not 1 <= len(sections) <= ROPE_MAX_AXES or min(sections) < 0 or sum(sections) != pairs:
+        raise ValueError(f"sections must be 1 to {ROPE_MAX_AXES} counts that sum to {pairs}")
+    if layout not in ("blocked", "dealt") or pairing not in ("half", "adjacent"):
+        raise ValueError("layout is 'blocked' or 'dealt', pairing 'half' or 'adjacent'")
+    if layout == "blocked":
+        axis = [a for a, n in enumerate(sections) for _ in range(n)]
+    else:
+        left, axis = list(sections), []
+        while any(left):
+            for a, n in enumerate(left):
+                if n:
+                    left[a] -= 1
+                    axis.append(a)
+    axis = np.asarray(axis, np.int32)
+    r = _Rope()
+    _check(_load().verify_attn_rope_init(ctypes.byref(r), freq.ctypes.data, axis.ctypes.data, pairs, len(sections),
+                                         int(pairing == "adjacent"), float(scale)), "verify_attn_rope_spec")
+    return Rope(r)
+
+
+def verify_attn_rope(rope: Rope, positions, q, k=None, q_out=None, k_out=None, inverse=False, stream=None):
+    """Rotate ``q`` and ``k`` (``[B, T, H, D]`` bf16, fp16 or fp32, any strides
+    with a contiguous last dimension) by ``positions`` (int32 ``[axes, B, T]``,
+    any strides).  ``q_out`` / ``k_out`` default to new contiguous tensors; pass
+    ``q`` / ``k`` themselves to work in place, otherwise outputs must not overlap
+    inputs.  ``inverse=True`` rotates back, which is also the gradient's way.
+    Returns (q_out, k_out), k_out None without ``k``."""
+    import torch
+    code = _float_code(q, "q")
+    hq = _heads(q, "q", q.dtype)
+    B, T, _, D = q.shape
+    hk = None if k is None else _heads(k, "k", q.dtype, (B, T, k.shape[2] if k.dim() == 4 else -1, D))
+    pos = _positions(positions, rope, B, T)
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    device = q.device
+    _same_device(device, positions=positions, k=k, q_out=q_out, k_out=k_out)
+    st, guard = _launch_on(device, stream)
+    with guard:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=q.dtype, device=device)
+        oq = _heads(q_out, "q_out", q.dtype, q.shape)
+        ok = None if k is None else _heads(k_out, "k_out", q.dtype, k.shape)
+        ref = ctypes.byref
+        rc = _load().verify_attn_rope(rope._ref, ref(pos), code, B, T, D, ref(hq), ref(oq),
+                                      None if hk is None else ref(hk), None if ok is None else ref(ok),
+                                      int(bool(inverse)), st)
+    _check(rc, "verify_attn_rope")
+    return q_out, k_out
+
+
+def verify_attn_rope_append(rope: Rope, positions, q, k_new, v_new, k_pages, v_pages, k_scale, v_scale, block_table,
+                            seq_lens, kv_dtype, q_out=None, num_pages=0, flags=None, stream=None):
+    """Rotate ``q`` and ``k_new`` and append ``k_new`` / ``v_new`` to the paged
+    cache in one launch (``[B, T, heads, D]`` bf16, any strides with a
+    contiguous last dimension, for instance slices of a fused projection).
+    Cache arguments, ``num_pages`` and ``flags`` as for
+    ``verify_attn_kv_append``; the cache gets the rotated keys, quantised from
+    their unrounded values.  ``positions`` None: every axis is the token's
+    place in its sequence, ``seq_lens[b] - T + t``.  ``q`` may be None.  Returns
+    the rotated q, contiguous bf16."""
+    import torch
+    code = _dtype_code(kv_dtype)
+    bf16 = torch.bfloat16
+    hk = _heads(k_new, "k_new", bf16)
+    B, T, Hkv, D = k_new.shape
+    hv = _heads(v_new, "v_new", bf16, k_new.shape)
+    hq = None if q is None else _heads(q, "q", bf16, (B, T, q.shape[2] if q.dim() == 4 else -1, D))
+    pos = None if positions is None else _positions(positions, rope, B, T)
+    kvd = _kv_dtypes(code)
+    bits = {VA_BF16: 16, VA_INT4: 4, VA_INT2: 2}.get(code, 8)
+    width = D if code in (VA_BF16, VA_FP8_E4M3, VA_INT8) else D * bits // 8
+    cache = []
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        cache.append(_dev_ptr(t, name, kvd))
+        if t.dim() != 4 or tuple(t.shape[1:]) != (PAGE_SIZE, Hkv, width):
+            raise ValueError(f"{name} must be [num_pages, {PAGE_SIZE}, {Hkv}, {width}], got {list(t.shape)}")
+    pages = min(k_pages.shape[0], v_pages.shape[0])
+    if num_pages > pages:
+        raise ValueError(f"num_pages is {num_pages}, the cache has {pages}")
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        cache.append(_dev_ptr(t, name, (torch.float32,), allow_none=code == VA_BF16))
+        if t is not None and (t.numel() < pages * PAGE_SIZE * Hkv):
+            raise ValueError(f"{name} must be [num_pages, {PAGE_SIZE}, {Hkv}]")
+    bt = _dev_ptr(block_table, "block_table", (torch.int32,))
+    if block_table.dim() != 2 or block_table.shape[0] < B:
+        raise ValueError("block_table must be [B, stride]")
+    sl = _dev_ptr(seq_lens, "seq_lens", (torch.int32,))
+    if seq_lens.numel() < B:
+        raise ValueError("seq_lens must be [B]")
+    fl = _dev_ptr(flags, "flags", (torch.int32,), allow_none=True)
+    device = k_new.device
+    _same_device(device, q=q, q_out=q_out, v_new=v_new, positions=positions, k_pages=k_pages, v_pages=v_pages,
+                 k_scale=k_scale, v_scale=v_scale, block_table=block_table, seq_lens=seq_lens, flags=flags)
+    st, guard = _launch_on(device, stream)
+    with guard:
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=bf16, device=device)
+        oq = None if q is None else _shaped(q_out, "q_out", (bf16,), q.shape)
+        ref = ctypes.byref
+        rc = _load().verify_attn_rope_append(
+            rope._ref, None if pos is None else ref(pos), B, T, D, None if hq is None else ref(hq), oq, ref(hk),
+            ref(hv), code, *cache, bt, block_table.shape[1], sl, int(num_pages) or pages, fl, st)
+    _check(rc, "verify_attn_rope_append")
+    return q_out
+
+
+def verify_attn_accept_probs(target_probs, draft_tokens, u_accept, u_emit, draft_probs=None, draft_lens=None,
+                             out_tokens=None, num_accepted=None, stream=None):
+    """Speculative acceptance from given probabilities and random numbers:
+    ``target_probs`` ``[B, T+1, V]`` and ``draft_probs`` ``[B, T, V]`` (None: point-mass
+    proposals) of one type (fp32, bf16 or fp16; any strides with a contiguous
+    last dimension, for instance padded vocabularies), ``draft_tokens`` int32 ``[B,
+    T]``, ``draft_lens`` int32 ``[B]`` (None: T each), uniforms ``u_accept`` fp32
+    ``[B, T]`` (one per draft) and ``u_emit`` fp32 ``[B]`` (for the emitted
+    token).  Definition in ``include/verify_attn.h``.  Returns (out_tokens int32
+    ``[B, T+1]`` with -1 after the emitted token, num_accepted int32 ``[B]``)."""
+    import torch
+    f32, i32 = (torch.float32,), (torch.int32,)
+    code = _float_code(target_probs, "target_probs")
+
+    def rows(t, name, shape):
+        if not t.is_cuda or t.dtype != target_probs.dtype:
+            raise ValueError(f"{name} must be a CUDA tensor of type {target_probs.dtype}")
+        if t.dim() != 3 or tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        s = t.stride()
+        if s[2] != 1 and t.shape[2] > 1:
+            raise ValueError(f"{name} must be contiguous in its last dimension")
+        return _Rows(t.data_ptr(), s[0], s[1])
+
+    if target_probs.dim() != 3 or target_probs.shape[1] < 1:
+        raise ValueError("target_probs must be [B, T+1, V]")
+    B, T1, V = target_probs.shape
+    T = T1 - 1
+    p = rows(target_probs, "target_probs", (B, T1, V))
+    q = None if draft_probs is None or T == 0 else rows(draft_probs, "draft_probs", (B, T, V))
+    device = target_probs.device
+    d = _shaped(draft_tokens, "draft_tokens", i32, (B, T)) if T else None
+    ua = _shaped(u_accept, "u_accept", f32, (B, T)) if T else None
+    ue = _shaped(u_emit, "u_emit", f32, (B,))
+    dl = None if draft_lens is None else _shaped(draft_lens, "draft_lens", i32, (B,))
+    _same_device(device, draft_probs=draft_probs, draft_tokens=draft_tokens if T else None,
+                 u_accept=u_accept if T else None, u_emit=u_emit, draft_lens=draft_lens, out_tokens=out_tokens,
+                 num_accepted=num_accepted)
+    st, guard = _launch_on(device, stream)
+    with guard:
+        if out_tokens is None:
+            out_tokens = torch.empty((B, T1), dtype=torch.int32, device=device)
+        if num_accepted is None:
+            num_accepted = torch.empty((B,), dtype=torch.int32, device=device)
+        ot = _shaped(out_tokens, "out_tokens", i32, (B, T1))
+        na = _shaped(num_accepted, "num_accepted", i32, (B,))
+        rc = _load().verify_attn_accept_probs(ctypes.byref(p), None if q is None else ctypes.byref(q), code, d, dl, ua,
+                                              ue, B, T, V, ot, na, st)
+    _check(rc, "verify_attn_accept_probs")
+    return out_tokens, num_accepted
+
+
+class PagePool:
+    """The pages of a paged cache (``va_page_pool``): the tensors of the block
+    table and the free list, the pools that the pages lie in, and the
+    workspace.  ``PagePool.create`` makes an empty one; the constructor takes
+    tensors that exist (int32, contiguous, on one device): ``block_table``
+    ``[num_seqs, stride]``, ``seq_lens`` ``[num_seqs]``, ``ref_count`` and
+    ``free_list`` ``[num_pages]``, ``num_free`` ``[1]``, ``flags`` ``[1]`` or None
+    (made).  ``buffers``: tensors whose first dimension is the pages (K and V
+    pages and scales of every layer), contiguous.  Give ``block_table`` and
+    ``seq_lens`` to ``verify_attn_rope_append`` and ``verify_attn_with_plan``
+    (with ``block_table_stride`` and ``num_pages`` as plan options)."""
+
+    def __init__(self, block_table, seq_lens, ref_count, free_list, num_free, buffers, flags=None):
+        import torch
+        i32 = (torch.int32,)
+        if block_table.dim() != 2 or ref_count.dim() != 1:
+            raise ValueError("block_table must be [num_seqs, stride] and ref_count [num_pages]")
+        device = block_table.device
+        if flags is None:
+            flags = torch.zeros(1, dtype=torch.int32, device=device)
+        B, stride = block_table.shape
+        P = ref_count.shape[0]
+        self.block_table, self.seq_lens, self.ref_count = block_table, seq_lens, ref_count
+        self.free_list, self.num_free, self.flags = free_list, num_free, flags
+        self.buffers = list(buffers)
+        self.num_seqs, self.num_pages, self.device = B, P, device
+        _same_device(device, seq_lens=seq_lens, ref_count=ref_count, free_list=free_list, num_free=num_free, flags=flags)
+        array = (_PageBuffer * max(1, len(self.buffers)))()
+        for i, t in enumerate(self.buffers):
+            if not t.is_cuda or not t.is_contiguous() or t.device != device or t.dim() < 1 or t.shape[0] != P:
+                raise ValueError(f"buffer {i} must be a contiguous tensor on {device} with {P} pages in its first dimension")
+            array[i].data, array[i].page_bytes = t.data_ptr(), t.numel() // P * t.element_size()
+        size = int(_load().verify_attn_pages_workspace_bytes(B, P))
+        if not size:
+            raise ValueError(f"{B} sequences or {P} pages are out of range")
+        self.workspace = torch.empty(size, dtype=torch.uint8, device=device)
+        self._array = array
+        self._struct = _PagePool(
+            _dev_ptr(block_table, "block_table", i32), _shaped(seq_lens, "seq_lens", i32, (B,)),
+            _shaped(ref_count, "ref_count", i32, (P,)), _shaped(free_list, "free_list", i32, (P,)),
+            _shaped(num_free, "num_free", i32, (1,)), _shaped(flags, "flags", i32, (1,)), stride, B, P,
+            len(self.buffers), array, self.workspace.data_ptr())
+        self._ref = ctypes.byref(self._struct)
+
+    @classmethod
+    def create(cls, num_pages, num_seqs, max_blocks, buffers, device="cuda"):
+        """An empty pool: no sequence holds anything, the lowest page is taken first."""
+        import torch
+        device = torch.device(device)
+        if device.index is None:
+            device = torch.device(device.type, torch.cuda.current_device())
+        kw = dict(dtype=torch.int32, device=device)
+        return cls(torch.full((num_seqs, max_blocks), -1, **kw), torch.zeros(num_seqs, **kw),
+                   torch.zeros(num_pages, **kw), torch.arange(num_pages - 1, -1, -1, **kw),
+                   torch.full((1,), num_pages, **kw), buffers)
+
+
+def verify_attn_pages_resize(pool: PagePool, new_lens, stream=None):
+    """Change the sequences' lengths to ``new_lens`` (int32 ``[num_seqs]`` on the
+    device, negative: left alone): pages past a shorter length go back to the
+    pool, a longer one takes pages, and a growing sequence whose partly filled
+    last page is shared gets a copy of its own."""
+    import torch
+    n = _shaped(new_lens, "new_lens", (torch.int32,), (pool.num_seqs,))
+    _same_device(pool.device, new_lens=new_lens)
+    st, guard = _launch_on(pool.device, stream)
+    with guard:
+        rc = _load().verify_attn_pages_resize(pool._ref, n, st)
+    _check(rc, "verify_attn_pages_resize")
+
+
+def verify_attn_pages_fork(pool: PagePool, parents, children, lens=None, share=True, stream=None):
+    """Make the empty slots ``children`` copies of ``parents`` (int32 ``[F]`` on
+    the device), of their first ``lens`` tokens where given.  ``share``: full
+    pages are held in common and a partly filled last page is copied; otherwise
+    every page is copied."""
+    import torch
+    i32 = (torch.int32,)
+    if parents.dim() != 1:
+        raise ValueError("parents must be [F]")
+    F = parents.shape[0]
+    pa, ch = _shaped(parents, "parents", i32, (F,)), _shaped(children, "children", i32, (F,))
+    ln = None if lens is None else _shaped(lens, "lens", i32, (F,))
+    _same_device(pool.device, parents=parents, children=children, lens=lens)
+    st, guard = _launch_on(pool.device, stream)
+    with guard:
+        rc = _load().verify_attn_pages_fork(pool._ref, pa, ch, ln, F, int(bool(share)), st)
+    _check(rc, "verify_attn_pages_fork")
+
+
+def verify_attn_pages_compact(pool: PagePool, stream=None):
+    """Move the held pages to the front of the pool (block tables and counts
+    follow); the free list then holds the pages behind them, lowest first."""
+    st, guard = _launch_on(pool.device, stream)
+    with guard:
+        rc = _load().verify_attn_pages_compact(pool._ref, st)
+    _check(rc, "verify_attn_pages_compact")
+
+
+def verify_attn_pages_flags(pool: PagePool, clear=True) -> int:
+    """The pool's flag word (``VA_PAGES_*`` bits), cleared by default.  Waits for
+    torch's current stream."""
+    flags = int(pool.flags.item())
+    if clear and flags:
+        pool.flags.zero_()
+    return flags
+
+
 __all__ = [
+    "Rope", "verify_attn_rope_spec", "verify_attn_rope", "verify_attn_rope_append", "verify_attn_accept_probs",
+    "PagePool", "verify_attn_pages_resize", "verify_attn_pages_fork", "verify_attn_pages_compact",
+    "verify_attn_pages_flags",
     "verify_attn_accept",
     "verify_attn_lookup_draft",
     "verify_attn_kv_append",

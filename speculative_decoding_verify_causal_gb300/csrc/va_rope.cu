@@ -1,0 +1,615 @@
+// Rotary positions with several axes: q and k of a batch rotated in one
+// launch (rope_kernel), or rotated and appended to the paged cache in one
+// launch (append_kernel).  Definitions in verify_attn.h.
+//
+// Angles.  A binary32 product position * frequency loses the angle: at
+// position 200,000 its last bit is 1/64 of a radian.  turn[i] holds the part
+// of a turn that one step makes as a 64-bit fraction, so position * turn[i]
+// modulo 2^64 (one integer multiplication, negative positions included) is
+// the angle's part of a turn to 2^-64 times the position.  Its top 32 bits
+// give the nearest quarter turn and a signed remainder of at most 1/8 turn,
+// which binary32 holds to 24 bits; sincospif of the remainder is then within
+// a few ulps, and the quarter turn swaps and negates.
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "va_kv_row.cuh"
+
+namespace va {
+namespace {
+
+// (cos, sin) of position pos * turn / 2^64 of a full turn, times scale
+__device__ __forceinline__ float2 turned(uint64_t turn, int pos, float scale) {
+    const uint64_t phase = turn * (uint64_t)(int64_t)pos;
+    const uint32_t hi = (uint32_t)((phase + 0x80000000ull) >> 32);
+    const uint32_t quarter = (hi + 0x20000000u) >> 30;
+    const int rest = (int)(hi - (quarter << 30));  // in units of 2^-32 turn = 2^-31 pi
+    float s, c;
+    sincospif((float)rest * 4.656612873077392578125e-10f, &s, &c);  // 2^-31
+    c *= scale;
+    s *= scale;
+    float2 r = (quarter & 1u) ? make_float2(-s, c) : make_float2(c, s);
+    if (quarter & 2u) r = make_float2(-r.x, -r.y);
+    return r;
+}
+
+// n / d and n % d for 0 <= n < 2^31 with a multiplication (d >= 1)
+struct FastDiv {
+    uint32_t d, mul, shift;
+};
+FastDiv fast_div(uint32_t d) {
+    FastDiv f{d, 0, 0};
+    while (f.shift < 31 && (1u << f.shift) < d) ++f.shift;
+    f.mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << f.shift) - d)) / d + 1);
+    return f;
+}
+__device__ __forceinline__ uint32_t div(uint32_t n, const FastDiv &f) { return (__umulhi(n, f.mul) + n) >> f.shift; }
+
+// ------------------------------------------------------------------------- rotary alone
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;            // units whose loads a thread has in flight
+constexpr int kTableEntries = 2048;   // (cos, sin) pairs in shared memory: 16 KB
+constexpr int kMinCtas = 304;         // two for each of 152 SMs
+
+struct Tensor {
+    const char *in;
+    char *out;
+    int64_t in_seq, in_token, in_head, out_seq, out_token, out_head;  // bytes
+};
+
+struct RopeParams {
+    va_rope rope;
+    const int32_t *pos;
+    int64_t pos_axis, pos_seq, pos_token;
+    Tensor q, k;
+    int q_heads, heads;      // heads of q, of q and k together
+    int tokens;              // num_seqs * T
+    int tile, head_chunk;    // tokens and heads per CTA
+    int units;               // vectors-pairs per head: pairs / W, then the unrotated vectors
+    int pair_units;
+    float inverse_sign;      // -1 for the inverse
+    FastDiv by_T, by_pairs, by_units, by_chunk;
+};
+
+template <int BYTES>
+struct Raw;
+template <>
+struct Raw<16> {
+    using V = uint4;
+};
+template <>
+struct Raw<8> {
+    using V = uint2;
+};
+template <>
+struct Raw<4> {
+    using V = uint32_t;
+};
+template <>
+struct Raw<2> {
+    using V = uint16_t;
+};
+
+template <int TYPE>
+struct Elem {
+    static constexpr int kBytes = TYPE == VA_FLOAT_FP32 ? 4 : 2;
+};
+
+// W elements of a 16- or 32-bit type <-> fp32
+template <int TYPE, int W, typename V>
+__device__ __forceinline__ void unpack(const V &raw, float (&x)[W]) {
+    if constexpr (TYPE == VA_FLOAT_FP32) {
+        const float *f = reinterpret_cast<const float *>(&raw);
+#pragma unroll
+        for (int e = 0; e < W; ++e) x[e] = f[e];
+    } else {
+        const uint16_t *h = reinterpret_cast<const uint16_t *>(&raw);
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+            x[e] = TYPE == VA_FLOAT_BF16 ? __uint_as_float((uint32_t)h[e] << 16) : __half2float(__ushort_as_half(h[e]));
+    }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <int TYPE, int W, typename V>
+__device__ __forceinline__ V packed(const float (&x)[W]) {
+    V raw;
+    if constexpr (TYPE == VA_FLOAT_FP32) {
+        float *f = reinterpret_cast<float *>(&raw);
+#pragma unroll
+        for (int e = 0; e < W; ++e) f[e] = x[e];
+    } else if constexpr (W == 1) {
+        raw = TYPE == VA_FLOAT_BF16 ? (V)(pack_bf16x2(x[0], 0.f) & 0xFFFFu) : (V)__half_as_ushort(__float2half_rn(x[0]));
+    } else {
+        uint32_t *h = reinterpret_cast<uint32_t *>(&raw);
+#pragma unroll
+        for (int e = 0; e < W; e += 2) {
+            if constexpr (TYPE == VA_FLOAT_BF16) {
+                h[e / 2] = pack_bf16x2(x[e], x[e + 1]);
+            } else {
+                const __half2 p = __floats2half2_rn(x[e], x[e + 1]);
+                h[e / 2] = *reinterpret_cast<const uint32_t *>(&p);
+            }
+        }
+    }
+    return raw;
+}
+
+// A unit is W pairs of one head (two vectors of W elements: one of each half,
+// or 2 W neighbours) or, past the pairs, one vector that is copied.  A CTA
+// turns `tile` tokens x `head_chunk` heads: it first puts the tokens' (cos,
+// sin) into shared memory, once for all the heads, then streams the units.
+template <int TYPE, int W, bool ADJACENT>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+    using V = typename Raw<W * Elem<TYPE>::kBytes>::V;
+    constexpr int kElem = Elem<TYPE>::kBytes;
+    __shared__ float2 table[kTableEntries];
+    const int P = p.rope.num_pairs;
+    const int first = blockIdx.x * p.tile, count = min(p.tile, p.tokens - first);
+    const int h0 = blockIdx.y * p.head_chunk, nh = min(p.head_chunk, p.heads - h0);
+    griddep_wait();
+    for (int i = threadIdx.x; i < count * P; i += kThreads) {
+        const int n = (int)div(i, p.by_pairs), pr = i - n * P;
+        const int b = (int)div(first + n, p.by_T), t = first + n - b * (int)p.by_T.d;
+        const int pos = p.pos[p.rope.axis[pr] * p.pos_axis + b * p.pos_seq + t * p.pos_token];
+        float2 cs = turned(p.rope.turn[pr], pos, p.rope.scale);
+        cs.y *= p.inverse_sign;
+        table[i] = cs;
+    }
+    __syncthreads();
+    const int total = count * p.head_chunk * p.units;
+    const int pair_units = p.pair_units;
+    for (int base = threadIdx.x; base < total; base += kThreads * kUnroll) {
+        V lo[kUnroll], hi[kUnroll];
+        char *to[kUnroll];
+        int at[kUnroll];  // first table entry of the unit; -1: nothing to do, -2: copied
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int i = base + u * kThreads;
+            at[u] = -1;
+            if (i >= total) continue;
+            const int row = (int)div(i, p.by_units), unit = i - row * p.units;
+            const int n = (int)div(row, p.by_chunk), hc = row - n * p.head_chunk;
+            if (hc >= nh) continue;
+            const int b = (int)div(first + n, p.by_T), t = first + n - b * (int)p.by_T.d;
+            int h = h0 + hc;
+            const bool is_k = h >= p.q_heads;
+            if (is_k) h -= p.q_heads;
+            const Tensor &x = is_k ? p.k : p.q;
+            const bool pairs = unit < pair_units;
+            const int elem = ADJACENT ? (pairs ? 2 * W * unit : 2 * P + W * (unit - pair_units))
+                                      : (pairs ? W * unit : 2 * P + W * (unit - pair_units));
+            const char *src = x.in + b * x.in_seq + t * x.in_token + h * x.in_head + (int64_t)elem * kElem;
+            to[u] = x.out + b * x.out_seq + t * x.out_token + h * x.out_head + (int64_t)elem * kElem;
+            at[u] = pairs ? n * P + W * unit : -2;
+            lo[u] = *reinterpret_cast<const V *>(src);
+            if (pairs) hi[u] = *reinterpret_cast<const V *>(src + (ADJACENT ? W : P) * kElem);
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            if (at[u] == -1) continue;
+            if (at[u] == -2) {
+                *reinterpret_cast<V *>(to[u]) = lo[u];
+                continue;
+            }
+            float x0[W], x1[W];
+            unpack<TYPE, W>(lo[u], x0);
+            unpack<TYPE, W>(hi[u], x1);
+            const float2 *cs = table + at[u];
+            if constexpr (ADJACENT) {  // x0, x1 as one run of 2 W: pair j is elements 2 j, 2 j + 1
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    float &a = 2 * j < W ? x0[2 * j < W ? 2 * j : 0] : x1[2 * j < W ? 0 : 2 * j - W];
+                    float &b = 2 * j + 1 < W ? x0[2 * j + 1 < W ? 2 * j + 1 : 0] : x1[2 * j + 1 < W ? 0 : 2 * j + 1 - W];
+                    const float2 r = cs[j];
+                    const float na = fmaf(a, r.x, -b * r.y), nb = fmaf(b, r.x, a * r.y);
+                    a = na;
+                    b = nb;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    const float2 r = cs[j];
+                    const float na = fmaf(x0[j], r.x, -x1[j] * r.y), nb = fmaf(x1[j], r.x, x0[j] * r.y);
+                    x0[j] = na;
+                    x1[j] = nb;
+                }
+            }
+            *reinterpret_cast<V *>(to[u]) = packed<TYPE, W, V>(x0);
+            *reinterpret_cast<V *>(to[u] + (ADJACENT ? W : P) * kElem) = packed<TYPE, W, V>(x1);
+        }
+    }
+}
+
+template <int TYPE, int W>
+cudaError_t launch_rope_w(const RopeParams &p, dim3 grid, cudaStream_t s) {
+    return p.rope.adjacent ? launch_pdl(rope_kernel<TYPE, W, true>, grid, dim3(kThreads), 0, s, p)
+                           : launch_pdl(rope_kernel<TYPE, W, false>, grid, dim3(kThreads), 0, s, p);
+}
+
+template <int TYPE>
+cudaError_t launch_rope(const RopeParams &p, int w, dim3 grid, cudaStream_t s) {
+    constexpr int kWide = 16 / Elem<TYPE>::kBytes;
+    return w == kWide ? launch_rope_w<TYPE, kWide>(p, grid, s)
+           : w == 2   ? launch_rope_w<TYPE, 2>(p, grid, s)
+                      : launch_rope_w<TYPE, 1>(p, grid, s);
+}
+
+// ------------------------------------------------------------------------- rotary and append
+
+struct RopeAppendParams {
+    va_rope rope;
+    const int32_t *pos;  // null: the token's place in its sequence
+    int64_t pos_axis, pos_seq, pos_token;
+    const uint16_t *q, *k, *v;
+    int64_t q_seq, q_token, q_head, k_seq, k_token, k_head, v_seq, v_token, v_head;  // elements
+    uint16_t *q_out;
+    void *k_pages, *v_pages;
+    float *k_scale, *v_scale;
+    const int32_t *block_table;
+    const int32_t *seq_lens;
+    int *flags;
+    int T, Hq, Hkv, bt_stride, num_pages;
+};
+
+constexpr int kRowWarps = kThreads / 32;
+
+// One CTA per token (blockIdx.x) and chunk of its Hq + 2 Hkv rows (blockIdx.y,
+// kRowWarps * ROWS of them), one warp per row, ROWS rows per warp with their
+// loads in flight together.  The token's (cos, sin) are computed once per CTA,
+// one pair a thread, and each lane keeps those of its E elements in registers.
+// Lane l holds elements [l E, l E + E): the other half of a pair is P / E
+// lanes away (halves) or the neighbouring element (adjacent).
+template <int D, int DT, int ROWS>
+__global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_constant__ RopeAppendParams p) {
+    constexpr int E = D / 32;
+    using In = typename RowVec<E>::In;
+    __shared__ float2 table[VA_ROPE_MAX_PAIRS];
+    const int P = p.rope.num_pairs;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = blockIdx.x / p.T, t = blockIdx.x - b * p.T;
+    const int rows = p.Hq + 2 * p.Hkv;
+    const int row0 = blockIdx.y * (kRowWarps * ROWS) + warp;
+    griddep_wait();
+    In raw[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        const int row = row0 + r * kRowWarps;
+        if (row >= rows) continue;
+        const uint16_t *src;
+        if (row < p.Hq) src = p.q + b * p.q_seq + t * p.q_token + row * p.q_head;
+        else if (row < p.Hq + p.Hkv) src = p.k + b * p.k_seq + t * p.k_token + (row - p.Hq) * p.k_head;
+        else src = p.v + b * p.v_seq + t * p.v_token + (row - p.Hq - p.Hkv) * p.v_head;
+        raw[r] = *reinterpret_cast<const In *>(src + lane * E);
+    }
+    const int place = p.seq_lens[b] - p.T + t;
+    if (threadIdx.x < P) {
+        const int axis = p.rope.axis[threadIdx.x];
+        const int pos = p.pos ? p.pos[axis * p.pos_axis + b * p.pos_seq + t * p.pos_token] : place;
+        table[threadIdx.x] = turned(p.rope.turn[threadIdx.x], pos, p.rope.scale);
+    }
+    int page = -1;
+    const int block = place / VA_PAGE_SIZE;
+    if (place >= 0 && block < p.bt_stride) page = p.block_table[(size_t)b * p.bt_stride + block];
+    const bool stored = page >= 0 && (p.num_pages == 0 || page < p.num_pages);
+    __syncthreads();
+    const bool adjacent = p.rope.adjacent != 0;
+    float c[E], s[E];  // x' = x c + partner s
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int i = lane * E + e;
+        c[e] = 1.f;
+        s[e] = 0.f;
+        if (i < 2 * P) {
+            const bool second = adjacent ? (e & 1) : i >= P;
+            const float2 cs = table[adjacent ? i / 2 : (second ? i - P : i)];
+            c[e] = cs.x;
+            s[e] = second ? cs.y : -cs.y;
+        }
+    }
+    const int away = P / E;  // lanes between the halves of a pair
+    const int other = lane < away ? lane + away : lane < 2 * away ? lane - away : lane;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        const int row = row0 + r * kRowWarps;
+        if (row >= rows) continue;
+        const bool is_v = row >= p.Hq + p.Hkv;
+        const uint16_t *h = reinterpret_cast<const uint16_t *>(&raw[r]);
+        float x[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = __uint_as_float((uint32_t)h[e] << 16);
+        if (!is_v) {
+            float y[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float far = __shfl_sync(0xffffffffu, x[e], other);
+                const float partner = adjacent ? x[e ^ 1] : far;
+                y[e] = lane * E + e < 2 * P ? fmaf(x[e], c[e], partner * s[e]) : x[e];
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = y[e];
+        }
+        In turned_raw;
+        if (row < p.Hq || DT == VA_BF16) {
+            uint32_t *w = reinterpret_cast<uint32_t *>(&turned_raw);
+#pragma unroll
+            for (int e = 0; e < E; e += 2) w[e / 2] = pack_bf16x2(x[e], x[e + 1]);
+        }
+        if (row < p.Hq) {
+            *reinterpret_cast<In *>(p.q_out + ((size_t)blockIdx.x * p.Hq + row) * D + lane * E) = turned_raw;
+            continue;
+        }
+        if (!stored) {
+            if (lane == 0 && p.flags) atomicOr(p.flags, kFlagBadPage);
+            continue;
+        }
+        const int g = row - p.Hq - (is_v ? p.Hkv : 0);
+        const size_t dst_row = ((size_t)page * VA_PAGE_SIZE + place % VA_PAGE_SIZE) * p.Hkv + g;
+        void *pages = is_v ? p.v_pages : p.k_pages;
+        if constexpr (DT == VA_BF16) {  // v's bits unchanged, as in the append
+            *reinterpret_cast<In *>(static_cast<uint16_t *>(pages) + dst_row * D + lane * E) = is_v ? raw[r] : turned_raw;
+        } else {
+            store_quantised_row<D, DT>(x, pages, is_v ? p.v_scale : p.k_scale, dst_row, lane);
+        }
+    }
+}
+
+template <int D, int DT>
+cudaError_t launch_append(const RopeAppendParams &p, int tokens, cudaStream_t s) {
+    const int rows = p.Hq + 2 * p.Hkv;
+    constexpr int kMany = 4;
+    // four rows a warp once that still leaves two CTAs for every SM
+    const int wide = (rows + kRowWarps * kMany - 1) / (kRowWarps * kMany);
+    if ((long long)tokens * wide >= kMinCtas)
+        return launch_pdl(rope_append_kernel<D, DT, kMany>, dim3(tokens, wide), dim3(kThreads), 0, s, p);
+    return launch_pdl(rope_append_kernel<D, DT, 1>, dim3(tokens, (rows + kRowWarps - 1) / kRowWarps), dim3(kThreads), 0,
+                      s, p);
+}
+
+template <int D>
+cudaError_t launch_append_d(const RopeAppendParams &p, int dtype, int tokens, cudaStream_t s) {
+    switch (dtype) {
+    case VA_BF16: return launch_append<D, VA_BF16>(p, tokens, s);
+    case VA_FP8_E4M3: return launch_append<D, VA_FP8_E4M3>(p, tokens, s);
+    case VA_INT8: return launch_append<D, VA_INT8>(p, tokens, s);
+    case VA_INT4: return launch_append<D, VA_INT4>(p, tokens, s);
+    default: return launch_append<D, VA_INT2>(p, tokens, s);
+    }
+}
+
+bool rope_ok(const va_rope *r) {
+    if (!r || r->num_pairs < 1 || r->num_pairs > VA_ROPE_MAX_PAIRS || r->num_axes < 1 || r->num_axes > VA_ROPE_MAX_AXES)
+        return false;
+    for (int i = 0; i < r->num_pairs; ++i)
+        if (r->axis[i] >= r->num_axes) return false;
+    return true;
+}
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// Whether the elements of an output lie apart: each dimension's stride clears the extent of those inside it.
+bool apart(const va_heads &x, int num_seqs, int T, int head_dim) {
+    struct Dim {
+        int64_t stride, size;
+    } d[3] = {{x.stride_head, x.num_heads}, {x.stride_token, T}, {x.stride_seq, num_seqs}};
+    std::sort(d, d + 3, [](const Dim &a, const Dim &b) { return a.stride < b.stride; });
+    int64_t extent = head_dim;
+    for (const Dim &k : d) {
+        if (k.size <= 1) continue;
+        if (k.stride < extent) return false;
+        extent = (k.size - 1) * k.stride + extent;
+    }
+    return true;
+}
+
+bool same_strides(const va_heads &a, const va_heads &b, int num_seqs, int T) {
+    return (num_seqs <= 1 || a.stride_seq == b.stride_seq) && (T <= 1 || a.stride_token == b.stride_token) &&
+           (a.num_heads <= 1 || a.stride_head == b.stride_head);
+}
+
+// The strides that matter (of a dimension of more than one) are multiples of w elements and not negative.
+bool strides_ok(const va_heads &x, int num_seqs, int T, int64_t w) {
+    return (num_seqs <= 1 || (x.stride_seq >= 0 && x.stride_seq % w == 0)) &&
+           (T <= 1 || (x.stride_token >= 0 && x.stride_token % w == 0)) &&
+           (x.num_heads <= 1 || (x.stride_head >= 0 && x.stride_head % w == 0));
+}
+
+}  // namespace
+}  // namespace va
+
+extern "C" int verify_attn_rope_init(va_rope *rope, const double *inv_freq, const int32_t *axis, int num_pairs,
+                                     int num_axes, int adjacent, float scale) {
+    if (!rope || !inv_freq || num_pairs < 1 || num_pairs > VA_ROPE_MAX_PAIRS || num_axes < 1 ||
+        num_axes > VA_ROPE_MAX_AXES || !std::isfinite(scale))
+        return VA_ERR_INVALID_ARGUMENT;
+    for (int i = 0; i < num_pairs; ++i) {
+        if (!std::isfinite(inv_freq[i]) || std::fabs(inv_freq[i]) > 1048576.0) return VA_ERR_INVALID_ARGUMENT;
+        if (axis && (axis[i] < 0 || axis[i] >= num_axes)) return VA_ERR_INVALID_ARGUMENT;
+    }
+    // 1 / (2 pi) in units of 2^-66: with inv_freq = m 2^e (m of 53 bits), m times this is exact in
+    // 117 bits, and the part of a turn is that product times 2^(e - 66).
+    constexpr uint64_t kTurn66 = 0xA2F9836E4E44152Aull;
+    *rope = va_rope{};
+    for (int i = 0; i < num_pairs; ++i) {
+        int e = 0;
+        const double m = std::frexp(std::fabs(inv_freq[i]), &e);  // in [0.5, 1), or 0
+        const uint64_t whole = (uint64_t)std::ldexp(m, 53);       // inv_freq = whole 2^(e - 53)
+        const unsigned __int128 product = (unsigned __int128)whole * kTurn66;
+        // turns = product 2^(e - 53 - 66); as a multiple of 2^-64: product 2^(e - 55)
+        const int shift = 55 - e;
+        const uint64_t turn =  // e <= 21, so shift >= 34
+            shift > 120 ? 0 : (uint64_t)((product + ((unsigned __int128)1 << (shift - 1))) >> shift);
+        rope->turn[i] = inv_freq[i] < 0 ? 0 - turn : turn;
+        rope->axis[i] = (uint8_t)(axis ? axis[i] : 0);
+    }
+    rope->num_pairs = num_pairs;
+    rope->num_axes = num_axes;
+    rope->adjacent = adjacent != 0;
+    rope->scale = scale;
+    return VA_OK;
+}
+
+extern "C" int verify_attn_rope(const va_rope *rope, const va_positions *positions, va_float_type type, int num_seqs,
+                                int T, int head_dim, const va_heads *q, const va_heads *q_out, const va_heads *k,
+                                const va_heads *k_out, int inverse, void *stream) {
+    if (!va::rope_ok(rope) || !positions || !q || !q_out || !k != !k_out) return VA_ERR_INVALID_ARGUMENT;
+    if (type != VA_FLOAT_BF16 && type != VA_FLOAT_FP16 && type != VA_FLOAT_FP32) return VA_ERR_UNSUPPORTED;
+    if (num_seqs < 0 || T < 0 || head_dim < 2 * rope->num_pairs || head_dim > 1024) return VA_ERR_INVALID_ARGUMENT;
+    if (q->num_heads < 1 || q->num_heads != q_out->num_heads || (k && (k->num_heads < 1 || k->num_heads != k_out->num_heads)))
+        return VA_ERR_INVALID_ARGUMENT;
+    const long long tokens = (long long)num_seqs * T;
+    const int heads = q->num_heads + (k ? k->num_heads : 0);
+    if (tokens > (1LL << 30) || q->num_heads > 65535 || heads > 65535) return VA_ERR_INVALID_ARGUMENT;
+    if (tokens == 0) return VA_OK;
+    const int bytes = type == VA_FLOAT_FP32 ? 4 : 2;
+    if (!positions->data || !va::aligned(positions->data, 4)) return VA_ERR_INVALID_ARGUMENT;
+    const va_heads *all[4] = {q, q_out, k, k_out};
+    for (int i = 0; i < 4; ++i) {
+        if (!all[i]) continue;
+        if (!all[i]->data || !va::aligned(all[i]->data, bytes) || !va::strides_ok(*all[i], num_seqs, T, 1))
+            return VA_ERR_INVALID_ARGUMENT;
+        if ((i & 1) && !va::apart(*all[i], num_seqs, T, head_dim)) return VA_ERR_INVALID_ARGUMENT;
+        if ((i & 1) && all[i]->data == all[i - 1]->data && !va::same_strides(*all[i], *all[i - 1], num_seqs, T))
+            return VA_ERR_INVALID_ARGUMENT;
+    }
+    // the widest vector, up to 16 bytes, that every pointer, stride and part of the head is a multiple of
+    const int P = rope->num_pairs;
+    int w = 1;
+    for (int cand : {16 / bytes, 2}) {
+        bool ok = P % cand == 0 && (head_dim - 2 * P) % cand == 0;
+        for (const va_heads *x : all)
+            ok = ok && (!x || (va::aligned(x->data, (uintptr_t)cand * bytes) && va::strides_ok(*x, num_seqs, T, cand)));
+        if (ok) {
+            w = cand;
+            break;
+        }
+    }
+    va::RopeParams p{};
+    p.rope = *rope;
+    p.pos = positions->data;
+    p.pos_axis = positions->stride_axis;
+    p.pos_seq = positions->stride_seq;
+    p.pos_token = positions->stride_token;
+    auto tensor = [&](const va_heads *in, const va_heads *out) {
+        return va::Tensor{static_cast<const char *>(in->data), static_cast<char *>(out->data),
+                          in->stride_seq * bytes, in->stride_token * bytes, in->stride_head * bytes,
+                          out->stride_seq * bytes, out->stride_token * bytes, out->stride_head * bytes};
+    };
+    p.q = tensor(q, q_out);
+    if (k) p.k = tensor(k, k_out);
+    p.q_heads = q->num_heads;
+    p.heads = heads;
+    p.tokens = (int)tokens;
+    p.pair_units = P / w;
+    p.units = p.pair_units + (head_dim - 2 * P) / w;
+    p.inverse_sign = inverse ? -1.f : 1.f;
+    // A CTA takes about four units a thread (the loads it has in flight): several tokens, or some of
+    // one token's heads; fewer while the grid is below two CTAs an SM, down to one unit a thread.
+    const int per_cta = va::kThreads * va::kUnroll;
+    const int limit = std::min<long long>(va::kTableEntries / P, tokens);
+    p.tile = std::max(1, std::min(limit, per_cta / (p.units * heads)));
+    p.head_chunk = std::max(1, std::min(heads, per_cta / p.units));
+    auto ctas = [&] {
+        return ((tokens + p.tile - 1) / p.tile) * ((heads + p.head_chunk - 1) / p.head_chunk);
+    };
+    while (ctas() < va::kMinCtas && p.tile > 1) p.tile = (p.tile + 1) / 2;
+    while (ctas() < va::kMinCtas && p.head_chunk > 1 && p.head_chunk * p.units >= 2 * va::kThreads)
+        p.head_chunk = (p.head_chunk + 1) / 2;
+    p.by_T = va::fast_div((uint32_t)T);
+    p.by_pairs = va::fast_div((uint32_t)P);
+    p.by_units = va::fast_div((uint32_t)p.units);
+    p.by_chunk = va::fast_div((uint32_t)p.head_chunk);
+    const dim3 grid((unsigned)((tokens + p.tile - 1) / p.tile), (unsigned)((heads + p.head_chunk - 1) / p.head_chunk));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = type == VA_FLOAT_BF16   ? va::launch_rope<VA_FLOAT_BF16>(p, w, grid, s)
+                          : type == VA_FLOAT_FP16 ? va::launch_rope<VA_FLOAT_FP16>(p, w, grid, s)
+                                                  : va::launch_rope<VA_FLOAT_FP32>(p, w, grid, s);
+    if (e != cudaSuccess) {
+        va::note_cuda_error(e);
+        return VA_ERR_CUDA;
+    }
+    return VA_OK;
+}
+
+extern "C" int verify_attn_rope_append(const va_rope *rope, const va_positions *positions, int num_seqs, int T,
+                                       int head_dim, const va_heads *q, void *q_out, const va_heads *k_new,
+                                       const va_heads *v_new, va_kv_dtype kv_dtype, void *k_pages, void *v_pages,
+                                       float *k_scale, float *v_scale, const int32_t *block_table,
+                                       int block_table_stride, const int32_t *seq_lens, int num_pages, int *flags,
+                                       void *stream) {
+    if (!va::rope_ok(rope) || !q != !q_out || !k_new || !v_new || !k_pages || !v_pages || !block_table || !seq_lens)
+        return VA_ERR_INVALID_ARGUMENT;
+    if (num_seqs < 1 || T < 1 || block_table_stride < 1 || num_pages < 0) return VA_ERR_INVALID_ARGUMENT;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return VA_ERR_UNSUPPORTED;
+    if (kv_dtype < VA_BF16 || kv_dtype > VA_INT2) return VA_ERR_UNSUPPORTED;
+    if (kv_dtype != VA_BF16 && (!k_scale || !v_scale)) return VA_ERR_INVALID_ARGUMENT;
+    if (2 * rope->num_pairs > head_dim) return VA_ERR_INVALID_ARGUMENT;
+    if (!rope->adjacent && rope->num_pairs % (head_dim / 32) != 0) return VA_ERR_UNSUPPORTED;
+    if (k_new->num_heads < 1 || k_new->num_heads != v_new->num_heads || (q && q->num_heads < 1))
+        return VA_ERR_INVALID_ARGUMENT;
+    if (positions && (!positions->data || !va::aligned(positions->data, 4))) return VA_ERR_INVALID_ARGUMENT;
+    // rows move as 16-byte (bf16 in) / 8-byte (codes out) units
+    for (const va_heads *x : {q, k_new, v_new})
+        if (x && (!x->data || !va::aligned(x->data, 16) || !va::strides_ok(*x, num_seqs, T, 8))) return VA_ERR_INVALID_ARGUMENT;
+    if (!va::aligned(k_pages, 16) || !va::aligned(v_pages, 16) || (q_out && !va::aligned(q_out, 16)) ||
+        !va::aligned(block_table, 4) || !va::aligned(seq_lens, 4) || !va::aligned(k_scale, 4) ||
+        !va::aligned(v_scale, 4) || !va::aligned(flags, 4))
+        return VA_ERR_INVALID_ARGUMENT;
+    const long long tokens = (long long)num_seqs * T;
+    if (tokens > (1LL << 30) || (q && q->num_heads > 65535) || k_new->num_heads > 65535) return VA_ERR_INVALID_ARGUMENT;
+    va::RopeAppendParams p{};
+    p.rope = *rope;
+    if (positions) {
+        p.pos = positions->data;
+        p.pos_axis = positions->stride_axis;
+        p.pos_seq = positions->stride_seq;
+        p.pos_token = positions->stride_token;
+    }
+    if (q) {
+        p.q = static_cast<const uint16_t *>(q->data);
+        p.q_seq = q->stride_seq;
+        p.q_token = q->stride_token;
+        p.q_head = q->stride_head;
+        p.Hq = q->num_heads;
+        p.q_out = static_cast<uint16_t *>(q_out);
+    }
+    p.k = static_cast<const uint16_t *>(k_new->data);
+    p.k_seq = k_new->stride_seq;
+    p.k_token = k_new->stride_token;
+    p.k_head = k_new->stride_head;
+    p.v = static_cast<const uint16_t *>(v_new->data);
+    p.v_seq = v_new->stride_seq;
+    p.v_token = v_new->stride_token;
+    p.v_head = v_new->stride_head;
+    p.k_pages = k_pages;
+    p.v_pages = v_pages;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.flags = flags;
+    p.T = T;
+    p.Hkv = k_new->num_heads;
+    p.bt_stride = block_table_stride;
+    p.num_pages = num_pages;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    switch (head_dim) {
+    case 64: e = va::launch_append_d<64>(p, kv_dtype, (int)tokens, s); break;
+    case 128: e = va::launch_append_d<128>(p, kv_dtype, (int)tokens, s); break;
+    default: e = va::launch_append_d<256>(p, kv_dtype, (int)tokens, s); break;
+    }
+    if (e != cudaSuccess) {
+        va::note_cuda_error(e);
+        return VA_ERR_CUDA;
+    }
+    return VA_OK;
+}
