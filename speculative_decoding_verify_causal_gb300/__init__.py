@@ -21,6 +21,7 @@ numbers) and ``PagePool`` with ``verify_attn_pages_resize`` / ``_fork`` /
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -151,9 +152,10 @@ def _load():
         lib.verify_attn_validate_host.argtypes = [P, I, I, P, I, I, ctypes.POINTER(I), ctypes.POINTER(I)]
         lib.verify_attn_validate_host.restype = I
         lib.verify_attn_rope_init.argtypes = [P, P, P, I, I, I, ctypes.c_float]
-        lib.verify_attn_rope.argtypes = [P, P, I, I, I, I, P, P, P, P, I, P]
-        lib.verify_attn_rope_append.argtypes = [P, P, I, I, I, P, P, P, P, I, P, P, P, P, P, I, P, I, P, P]
-        lib.verify_attn_accept_probs.argtypes = [P, P, I, P, P, P, P, I, I, I, P, P, P]
+        H, S, R = ctypes.POINTER(_Heads), ctypes.POINTER(_Positions), ctypes.POINTER(_Rows)
+        lib.verify_attn_rope.argtypes = [P, S, I, I, I, I, H, H, H, H, I, P]
+        lib.verify_attn_rope_append.argtypes = [P, S, I, I, I, H, P, H, H, I, P, P, P, P, P, I, P, I, P, P]
+        lib.verify_attn_accept_probs.argtypes = [R, R, I, P, P, P, P, I, I, I, P, P, P]
         lib.verify_attn_pages_workspace_bytes.argtypes = [I, I]
         lib.verify_attn_pages_workspace_bytes.restype = ctypes.c_size_t
         lib.verify_attn_pages_resize.argtypes = [P, P, P]
@@ -525,25 +527,28 @@ def verify_attn_accept(target_logits, draft_tokens, temperature, seed, draft_log
 
 
 def _float_code(t, name):
-    import torch
-    code = {torch.bfloat16: VA_FLOAT_BF16, torch.float16: VA_FLOAT_FP16, torch.float32: VA_FLOAT_FP32}.get(t.dtype)
+    code = _FLOAT_CODES.get(str(t.dtype))
     if code is None:
         raise ValueError(f"{name} has dtype {t.dtype}, expected bfloat16, float16 or float32")
     return code
+
+
+_FLOAT_CODES = {"torch.bfloat16": VA_FLOAT_BF16, "torch.float16": VA_FLOAT_FP16, "torch.float32": VA_FLOAT_FP32}
+_here = contextlib.nullcontext()
 
 
 def _launch_on(device, stream):
     """(stream handle, guard): a call runs on the tensors' device and on ``stream`` there (a
     torch stream or a raw handle; default: torch's current stream of that device).  What the
     call allocates is allocated inside the guard, so it belongs to that stream."""
-    import contextlib
-
     import torch
     if stream is None:
-        handle = torch.cuda.current_stream(device).cuda_stream
-        if torch.cuda.current_device() == device.index:
-            return handle, contextlib.nullcontext()
-        return handle, torch.cuda.device(device)
+        index = device.index
+        current = torch.cuda.current_device() == index
+        # the current stream's handle without a Stream object around it, where torch offers that
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        handle = raw(index) if raw is not None else torch.cuda.current_stream(device).cuda_stream
+        return handle, _here if current else torch.cuda.device(device)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     elif stream.device != device:
@@ -551,43 +556,59 @@ def _launch_on(device, stream):
     return stream.cuda_stream, torch.cuda.stream(stream)
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+def _device_of(t, name):
+    """The device of a CUDA tensor and its index."""
+    if not getattr(t, "is_cuda", False):
+        raise ValueError(f"{name} must be a CUDA tensor")
+    device = t.device
+    return device, device.index
 
 
-def _shaped(t, name, dtypes, shape):
-    """Device pointer of a contiguous CUDA tensor of that shape."""
-    p = _dev_ptr(t, name, dtypes)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return p
+def _ptr(t, name, dtype, index, shape=None):
+    """Address of a contiguous tensor of that type (and shape) on CUDA device ``index``."""
+    try:
+        if (t.dtype is dtype and t.get_device() == index and t.is_contiguous()
+                and (shape is None or t.shape == shape)):
+            return t.data_ptr()
+    except AttributeError:
+        raise ValueError(f"{name} must be a CUDA tensor") from None
+    want = "" if shape is None else f" of shape {list(shape)}"
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor{want} on cuda:{index}, "
+                     f"got {t.dtype} {list(t.shape)} on {t.device}")
 
 
-def _heads(t, name, dtype, shape=None):
+def _ptr_of(t, name, dtypes, index):
+    """``_ptr`` of a tensor that may have one of several types."""
+    dtype = getattr(t, "dtype", None)
+    if dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {dtype}, expected one of {dtypes}")
+    return _ptr(t, name, dtype, index)
+
+
+def _heads(t, name, dtype, index, shape=None):
     """A [B, T, H, D] tensor, any strides but a contiguous last dimension, as a ``va_heads``."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 4:
-        raise ValueError(f"{name} must be a CUDA tensor [B, T, H, D]")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    s = t.stride()
-    if s[3] != 1 and t.shape[3] > 1:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
-    return _Heads(t.data_ptr(), s[0], s[1], s[2], t.shape[2])
+    try:
+        n, s = t.shape, t.stride()
+        if (t.dtype is dtype and t.get_device() == index and len(n) == 4 and (s[3] == 1 or n[3] <= 1)
+                and (shape is None or n == shape)):
+            return _Heads(t.data_ptr(), s[0], s[1], s[2], n[2])
+    except AttributeError:
+        raise ValueError(f"{name} must be a CUDA tensor") from None
+    want = "[B, T, H, D]" if shape is None else list(shape)
+    raise ValueError(f"{name} must be a {dtype} tensor {want} on cuda:{index}, contiguous in its last dimension, "
+                     f"got {t.dtype} {list(n)} with strides {list(s)} on {t.device}")
 
 
-def _positions(t, rope, B, T):
+def _positions(t, rope, B, T, index):
     import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32:
-        raise ValueError("positions must be an int32 CUDA tensor")
-    if tuple(t.shape) != (rope.num_axes, B, T):
-        raise ValueError(f"positions must be [{rope.num_axes}, {B}, {T}], got {list(t.shape)}")
-    s = t.stride()
-    return _Positions(t.data_ptr(), s[0], s[1], s[2])
+    shape = (rope._struct.num_axes, B, T)
+    try:
+        if t.dtype is torch.int32 and t.get_device() == index and t.shape == shape:
+            s = t.stride()
+            return _Positions(t.data_ptr(), s[0], s[1], s[2])
+    except AttributeError:
+        pass
+    raise ValueError(f"positions must be an int32 tensor {list(shape)} on cuda:{index}")
 
 
 class Rope:
@@ -650,28 +671,32 @@ def verify_attn_rope(rope: Rope, positions, q, k=None, q_out=None, k_out=None, i
     inputs.  ``inverse=True`` rotates back, which is also the gradient's way.
     Returns (q_out, k_out), k_out None without ``k``."""
     import torch
+    device, index = _device_of(q, "q")
     code = _float_code(q, "q")
-    hq = _heads(q, "q", q.dtype)
-    B, T, _, D = q.shape
-    hk = None if k is None else _heads(k, "k", q.dtype, (B, T, k.shape[2] if k.dim() == 4 else -1, D))
-    pos = _positions(positions, rope, B, T)
-    if k is None and k_out is not None:
+    dtype = q.dtype
+    hq = _heads(q, "q", dtype, index)
+    B, T, _, D = n = q.shape
+    hk = None
+    if k is not None:
+        hk = _heads(k, "k", dtype, index)
+        nk = k.shape
+        if nk[0] != B or nk[1] != T or nk[3] != D:
+            raise ValueError(f"k must be [{B}, {T}, heads, {D}], got {list(nk)}")
+    elif k_out is not None:
         raise ValueError("k_out without k")
-    device = q.device
-    _same_device(device, positions=positions, k=k, q_out=q_out, k_out=k_out)
+    pos = _positions(positions, rope, B, T, index)
     st, guard = _launch_on(device, stream)
     with guard:
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=device)
-        if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=q.dtype, device=device)
-        oq = _heads(q_out, "q_out", q.dtype, q.shape)
-        ok = None if k is None else _heads(k_out, "k_out", q.dtype, k.shape)
-        ref = ctypes.byref
-        rc = _load().verify_attn_rope(rope._ref, ref(pos), code, B, T, D, ref(hq), ref(oq),
-                                      None if hk is None else ref(hk), None if ok is None else ref(ok),
-                                      int(bool(inverse)), st)
-    _check(rc, "verify_attn_rope")
+            q_out = torch.empty(n, dtype=dtype, device=device)
+        oq, ok = _heads(q_out, "q_out", dtype, index, n), None
+        if k is not None:
+            if k_out is None:
+                k_out = torch.empty(nk, dtype=dtype, device=device)
+            ok = _heads(k_out, "k_out", dtype, index, nk)
+        rc = (_lib or _load()).verify_attn_rope(rope._ref, pos, code, B, T, D, hq, oq, hk, ok, 1 if inverse else 0, st)
+    if rc:
+        _check(rc, "verify_attn_rope")
     return q_out, k_out
 
 
@@ -687,47 +712,48 @@ def verify_attn_rope_append(rope: Rope, positions, q, k_new, v_new, k_pages, v_p
     the rotated q, contiguous bf16."""
     import torch
     code = _dtype_code(kv_dtype)
-    bf16 = torch.bfloat16
-    hk = _heads(k_new, "k_new", bf16)
-    B, T, Hkv, D = k_new.shape
-    hv = _heads(v_new, "v_new", bf16, k_new.shape)
-    hq = None if q is None else _heads(q, "q", bf16, (B, T, q.shape[2] if q.dim() == 4 else -1, D))
-    pos = None if positions is None else _positions(positions, rope, B, T)
+    device, index = _device_of(k_new, "k_new")
+    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    hk = _heads(k_new, "k_new", bf16, index)
+    B, T, Hkv, D = n = k_new.shape
+    hv = _heads(v_new, "v_new", bf16, index, n)
+    hq = None
+    if q is not None:
+        hq = _heads(q, "q", bf16, index)
+        nq = q.shape
+        if nq[0] != B or nq[1] != T or nq[3] != D:
+            raise ValueError(f"q must be [{B}, {T}, heads, {D}], got {list(nq)}")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    pos = None if positions is None else _positions(positions, rope, B, T, index)
     kvd = _kv_dtypes(code)
-    bits = {VA_BF16: 16, VA_INT4: 4, VA_INT2: 2}.get(code, 8)
-    width = D if code in (VA_BF16, VA_FP8_E4M3, VA_INT8) else D * bits // 8
-    cache = []
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        cache.append(_dev_ptr(t, name, kvd))
-        if t.dim() != 4 or tuple(t.shape[1:]) != (PAGE_SIZE, Hkv, width):
-            raise ValueError(f"{name} must be [num_pages, {PAGE_SIZE}, {Hkv}, {width}], got {list(t.shape)}")
-    pages = min(k_pages.shape[0], v_pages.shape[0])
+    kp, vp = _ptr_of(k_pages, "k_pages", kvd, index), _ptr_of(v_pages, "v_pages", kvd, index)
+    pages = k_pages.shape[0] if k_pages.dim() else 0
+    cache = (pages, PAGE_SIZE, Hkv, {VA_INT4: D // 2, VA_INT2: D // 4}.get(code, D))
+    if k_pages.shape != cache or v_pages.shape != cache:
+        raise ValueError(f"k_pages and v_pages must be [num_pages, {PAGE_SIZE}, {Hkv}, {cache[3]}], got "
+                         f"{list(k_pages.shape)} and {list(v_pages.shape)}")
     if num_pages > pages:
         raise ValueError(f"num_pages is {num_pages}, the cache has {pages}")
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        cache.append(_dev_ptr(t, name, (torch.float32,), allow_none=code == VA_BF16))
-        if t is not None and (t.numel() < pages * PAGE_SIZE * Hkv):
-            raise ValueError(f"{name} must be [num_pages, {PAGE_SIZE}, {Hkv}]")
-    bt = _dev_ptr(block_table, "block_table", (torch.int32,))
-    if block_table.dim() != 2 or block_table.shape[0] < B:
-        raise ValueError("block_table must be [B, stride]")
-    sl = _dev_ptr(seq_lens, "seq_lens", (torch.int32,))
-    if seq_lens.numel() < B:
-        raise ValueError("seq_lens must be [B]")
-    fl = _dev_ptr(flags, "flags", (torch.int32,), allow_none=True)
-    device = k_new.device
-    _same_device(device, q=q, q_out=q_out, v_new=v_new, positions=positions, k_pages=k_pages, v_pages=v_pages,
-                 k_scale=k_scale, v_scale=v_scale, block_table=block_table, seq_lens=seq_lens, flags=flags)
+    ks = vs = None
+    if code != VA_BF16:
+        ks, vs = _ptr(k_scale, "k_scale", f32, index, cache[:3]), _ptr(v_scale, "v_scale", f32, index, cache[:3])
+    bt, sl = _ptr(block_table, "block_table", i32, index), _ptr(seq_lens, "seq_lens", i32, index, (B,))
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must be [{B}, stride], got {list(block_table.shape)}")
+    fl = None if flags is None else _ptr(flags, "flags", i32, index)
     st, guard = _launch_on(device, stream)
     with guard:
-        if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=bf16, device=device)
-        oq = None if q is None else _shaped(q_out, "q_out", (bf16,), q.shape)
-        ref = ctypes.byref
-        rc = _load().verify_attn_rope_append(
-            rope._ref, None if pos is None else ref(pos), B, T, D, None if hq is None else ref(hq), oq, ref(hk),
-            ref(hv), code, *cache, bt, block_table.shape[1], sl, int(num_pages) or pages, fl, st)
-    _check(rc, "verify_attn_rope_append")
+        oq = None
+        if q is not None:
+            if q_out is None:
+                q_out = torch.empty(nq, dtype=bf16, device=device)
+            oq = _ptr(q_out, "q_out", bf16, index, nq)
+        rc = (_lib or _load()).verify_attn_rope_append(
+            rope._ref, pos, B, T, D, hq, oq, hk, hv, code, kp, vp, ks, vs, bt, block_table.shape[1], sl,
+            num_pages or pages, fl, st)
+    if rc:
+        _check(rc, "verify_attn_rope_append")
     return q_out
 
 
@@ -742,45 +768,45 @@ def verify_attn_accept_probs(target_probs, draft_tokens, u_accept, u_emit, draft
     token).  Definition in ``include/verify_attn.h``.  Returns (out_tokens int32
     ``[B, T+1]`` with -1 after the emitted token, num_accepted int32 ``[B]``)."""
     import torch
-    f32, i32 = (torch.float32,), (torch.int32,)
+    f32, i32 = torch.float32, torch.int32
+    device, index = _device_of(target_probs, "target_probs")
     code = _float_code(target_probs, "target_probs")
-
-    def rows(t, name, shape):
-        if not t.is_cuda or t.dtype != target_probs.dtype:
-            raise ValueError(f"{name} must be a CUDA tensor of type {target_probs.dtype}")
-        if t.dim() != 3 or tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-        s = t.stride()
-        if s[2] != 1 and t.shape[2] > 1:
-            raise ValueError(f"{name} must be contiguous in its last dimension")
-        return _Rows(t.data_ptr(), s[0], s[1])
-
-    if target_probs.dim() != 3 or target_probs.shape[1] < 1:
+    dtype, n = target_probs.dtype, target_probs.shape
+    if len(n) != 3 or n[1] < 1:
         raise ValueError("target_probs must be [B, T+1, V]")
-    B, T1, V = target_probs.shape
+    B, T1, V = n
     T = T1 - 1
-    p = rows(target_probs, "target_probs", (B, T1, V))
-    q = None if draft_probs is None or T == 0 else rows(draft_probs, "draft_probs", (B, T, V))
-    device = target_probs.device
-    d = _shaped(draft_tokens, "draft_tokens", i32, (B, T)) if T else None
-    ua = _shaped(u_accept, "u_accept", f32, (B, T)) if T else None
-    ue = _shaped(u_emit, "u_emit", f32, (B,))
-    dl = None if draft_lens is None else _shaped(draft_lens, "draft_lens", i32, (B,))
-    _same_device(device, draft_probs=draft_probs, draft_tokens=draft_tokens if T else None,
-                 u_accept=u_accept if T else None, u_emit=u_emit, draft_lens=draft_lens, out_tokens=out_tokens,
-                 num_accepted=num_accepted)
+    p = _prob_rows(target_probs, "target_probs", dtype, index, n)
+    q = d = ua = None
+    if T:
+        if draft_probs is not None:
+            q = _prob_rows(draft_probs, "draft_probs", dtype, index, (B, T, V))
+        d, ua = _ptr(draft_tokens, "draft_tokens", i32, index, (B, T)), _ptr(u_accept, "u_accept", f32, index, (B, T))
+    ue = _ptr(u_emit, "u_emit", f32, index, (B,))
+    dl = None if draft_lens is None else _ptr(draft_lens, "draft_lens", i32, index, (B,))
     st, guard = _launch_on(device, stream)
     with guard:
         if out_tokens is None:
-            out_tokens = torch.empty((B, T1), dtype=torch.int32, device=device)
+            out_tokens = torch.empty((B, T1), dtype=i32, device=device)
         if num_accepted is None:
-            num_accepted = torch.empty((B,), dtype=torch.int32, device=device)
-        ot = _shaped(out_tokens, "out_tokens", i32, (B, T1))
-        na = _shaped(num_accepted, "num_accepted", i32, (B,))
-        rc = _load().verify_attn_accept_probs(ctypes.byref(p), None if q is None else ctypes.byref(q), code, d, dl, ua,
-                                              ue, B, T, V, ot, na, st)
-    _check(rc, "verify_attn_accept_probs")
+            num_accepted = torch.empty((B,), dtype=i32, device=device)
+        ot, na = _ptr(out_tokens, "out_tokens", i32, index, (B, T1)), _ptr(num_accepted, "num_accepted", i32, index, (B,))
+        rc = (_lib or _load()).verify_attn_accept_probs(p, q, code, d, dl, ua, ue, B, T, V, ot, na, st)
+    if rc:
+        _check(rc, "verify_attn_accept_probs")
     return out_tokens, num_accepted
+
+
+def _prob_rows(t, name, dtype, index, shape):
+    """A [B, positions, V] tensor, any strides but a contiguous last dimension, as a ``va_rows``."""
+    try:
+        s = t.stride()
+        if t.dtype is dtype and t.get_device() == index and t.shape == shape and (s[2] == 1 or shape[2] <= 1):
+            return _Rows(t.data_ptr(), s[0], s[1])
+    except AttributeError:
+        raise ValueError(f"{name} must be a CUDA tensor") from None
+    raise ValueError(f"{name} must be a {dtype} tensor {list(shape)} on cuda:{index}, contiguous in its last dimension, "
+                     f"got {t.dtype} {list(t.shape)} with strides {list(s)} on {t.device}")
 
 
 class PagePool:
@@ -797,22 +823,21 @@ class PagePool:
 
     def __init__(self, block_table, seq_lens, ref_count, free_list, num_free, buffers, flags=None):
         import torch
-        i32 = (torch.int32,)
+        i32 = torch.int32
+        device, index = _device_of(block_table, "block_table")
         if block_table.dim() != 2 or ref_count.dim() != 1:
             raise ValueError("block_table must be [num_seqs, stride] and ref_count [num_pages]")
-        device = block_table.device
         if flags is None:
-            flags = torch.zeros(1, dtype=torch.int32, device=device)
+            flags = torch.zeros(1, dtype=i32, device=device)
         B, stride = block_table.shape
         P = ref_count.shape[0]
         self.block_table, self.seq_lens, self.ref_count = block_table, seq_lens, ref_count
         self.free_list, self.num_free, self.flags = free_list, num_free, flags
         self.buffers = list(buffers)
         self.num_seqs, self.num_pages, self.device = B, P, device
-        _same_device(device, seq_lens=seq_lens, ref_count=ref_count, free_list=free_list, num_free=num_free, flags=flags)
         array = (_PageBuffer * max(1, len(self.buffers)))()
         for i, t in enumerate(self.buffers):
-            if not t.is_cuda or not t.is_contiguous() or t.device != device or t.dim() < 1 or t.shape[0] != P:
+            if not t.is_contiguous() or t.device != device or t.dim() < 1 or t.shape[0] != P:
                 raise ValueError(f"buffer {i} must be a contiguous tensor on {device} with {P} pages in its first dimension")
             array[i].data, array[i].page_bytes = t.data_ptr(), t.numel() // P * t.element_size()
         size = int(_load().verify_attn_pages_workspace_bytes(B, P))
@@ -821,9 +846,9 @@ class PagePool:
         self.workspace = torch.empty(size, dtype=torch.uint8, device=device)
         self._array = array
         self._struct = _PagePool(
-            _dev_ptr(block_table, "block_table", i32), _shaped(seq_lens, "seq_lens", i32, (B,)),
-            _shaped(ref_count, "ref_count", i32, (P,)), _shaped(free_list, "free_list", i32, (P,)),
-            _shaped(num_free, "num_free", i32, (1,)), _shaped(flags, "flags", i32, (1,)), stride, B, P,
+            _ptr(block_table, "block_table", i32, index), _ptr(seq_lens, "seq_lens", i32, index, (B,)),
+            _ptr(ref_count, "ref_count", i32, index), _ptr(free_list, "free_list", i32, index, (P,)),
+            _ptr(num_free, "num_free", i32, index, (1,)), _ptr(flags, "flags", i32, index, (1,)), stride, B, P,
             len(self.buffers), array, self.workspace.data_ptr())
         self._ref = ctypes.byref(self._struct)
 
@@ -846,12 +871,12 @@ def verify_attn_pages_resize(pool: PagePool, new_lens, stream=None):
     pool, a longer one takes pages, and a growing sequence whose partly filled
     last page is shared gets a copy of its own."""
     import torch
-    n = _shaped(new_lens, "new_lens", (torch.int32,), (pool.num_seqs,))
-    _same_device(pool.device, new_lens=new_lens)
+    n = _ptr(new_lens, "new_lens", torch.int32, pool.device.index, (pool.num_seqs,))
     st, guard = _launch_on(pool.device, stream)
     with guard:
-        rc = _load().verify_attn_pages_resize(pool._ref, n, st)
-    _check(rc, "verify_attn_pages_resize")
+        rc = (_lib or _load()).verify_attn_pages_resize(pool._ref, n, st)
+    if rc:
+        _check(rc, "verify_attn_pages_resize")
 
 
 def verify_attn_pages_fork(pool: PagePool, parents, children, lens=None, share=True, stream=None):
@@ -860,17 +885,18 @@ def verify_attn_pages_fork(pool: PagePool, parents, children, lens=None, share=T
     pages are held in common and a partly filled last page is copied; otherwise
     every page is copied."""
     import torch
-    i32 = (torch.int32,)
-    if parents.dim() != 1:
+    i32, index = torch.int32, pool.device.index
+    pa = _ptr(parents, "parents", i32, index)
+    shape = parents.shape
+    if len(shape) != 1:
         raise ValueError("parents must be [F]")
-    F = parents.shape[0]
-    pa, ch = _shaped(parents, "parents", i32, (F,)), _shaped(children, "children", i32, (F,))
-    ln = None if lens is None else _shaped(lens, "lens", i32, (F,))
-    _same_device(pool.device, parents=parents, children=children, lens=lens)
+    ch = _ptr(children, "children", i32, index, shape)
+    ln = None if lens is None else _ptr(lens, "lens", i32, index, shape)
     st, guard = _launch_on(pool.device, stream)
     with guard:
-        rc = _load().verify_attn_pages_fork(pool._ref, pa, ch, ln, F, int(bool(share)), st)
-    _check(rc, "verify_attn_pages_fork")
+        rc = (_lib or _load()).verify_attn_pages_fork(pool._ref, pa, ch, ln, shape[0], 1 if share else 0, st)
+    if rc:
+        _check(rc, "verify_attn_pages_fork")
 
 
 def verify_attn_pages_compact(pool: PagePool, stream=None):
@@ -878,8 +904,9 @@ def verify_attn_pages_compact(pool: PagePool, stream=None):
     follow); the free list then holds the pages behind them, lowest first."""
     st, guard = _launch_on(pool.device, stream)
     with guard:
-        rc = _load().verify_attn_pages_compact(pool._ref, st)
-    _check(rc, "verify_attn_pages_compact")
+        rc = (_lib or _load()).verify_attn_pages_compact(pool._ref, st)
+    if rc:
+        _check(rc, "verify_attn_pages_compact")
 
 
 def verify_attn_pages_flags(pool: PagePool, clear=True) -> int:
