@@ -522,7 +522,7 @@ typedef struct {
  *   the emitted token is the smallest i with w_0 + .. + w_i > u_emit[b] * W,
  *     W the sum of all w (inversion of the cumulative distribution).
  * The weights need not sum to one.  Each p and q counts as a number in [0, 1]
- * (NaN and negative values as 0, larger ones as 1), cut to a multiple of
+ * (NaN and negative values as 0, larger ones as 1), rounded to a multiple of
  * 2^-62; the sums are exact in 128-bit integers, so the token does not depend
  * on how the work is split.  u_emit counts as in [0, 1 - 2^-24] (NaN as 0).
  * A row with no weight at all emits -1.

@@ -68,7 +68,7 @@ def fixed62(p):
     """Probabilities as multiples of 2^-62, Python integers: NaN and negative 0, above one 1."""
     p = np.asarray(p, np.float64)
     p = np.where(np.isnan(p), 0.0, np.clip(p, 0.0, 1.0))
-    return [int(v) for v in (p * 2.0 ** 62).astype(np.uint64)]
+    return [int(v) for v in np.rint(p * 2.0 ** 62).astype(np.uint64)]
 
 
 def accept_probs(p, drafts, u_accept, u_emit, q=None, lens=None):

@@ -3,20 +3,29 @@
 //
 // Mathematics.  The decisions u q < p are products of two binary32 numbers,
 // exact in binary64.  The emitted token inverts the cumulative distribution of
-// the weights, an integer that must not depend on how the sum is split: so
-// every p and q becomes a multiple of 2^-62 (an integer of 63 bits; what is
-// cut off is below 2^-62 an entry, 2^-44 over a whole vocabulary), the
-// residual max(0, p - q) is an exact integer subtraction and the sums are
-// exact 128-bit integers.  The threshold u W is m W / 2^k for u = m 2^-k with
-// m of 24 bits: exact in 128 bits too, and sum > u W holds for integers
-// exactly where sum > floor(m W / 2^k).  The integers also keep the work off
-// the FP64 pipe, which does two lanes a clock and SM here.
+// the weights, a whole number that must not depend on how the sum is split: so
+// every p and q is rounded to a multiple of 2^-62, the residual max(0, p - q)
+// is an exact integer subtraction and the sums are exact 128-bit integers.  The
+// threshold u W is m W / 2^k for u = m 2^-k with m of 24 bits: exact in 128
+// bits too, and sum > u W holds for integers exactly where sum > floor(m W /
+// 2^k).
+//
+// The integers are read off binary32 additions.  x + 12 lies in [8, 16), where
+// binary32 counts in steps of 2^-20: its last bits are x in those steps,
+// rounded, and what the rounding left, x - ((x + 12) - 12), is exact.  Twice
+// more, in steps of 2^-42 and 2^-62, gives x as n1 2^-20 + n2 2^-42 + n3 2^-62
+// with three small signed integers, which are summed as they are (the
+// constants cancel in p - q).  That is seven additions a number, two numbers
+// an instruction (add.f32x2).  Shifting significands into 64-bit integers took
+// about four times the instructions (64 sequences, vocabulary 151,936: 34.8 us
+// with it); binary64 does two lanes a clock and SM here.
 //
 // One thread-block cluster per sequence.  Every CTA evaluates the (at most T)
 // acceptance tests; each then sums its slice of the one row that decides, a
 // contiguous run per warp, and the CTAs exchange their sums through
-// distributed shared memory.  The one warp whose run holds the threshold reads
-// it again (from L2) and finds the entry.  Bound: the bytes of one row of p
+// distributed shared memory.  The CTA whose slice holds the threshold reads the
+// one run that holds it again (from L2), a vector a thread, and finds the
+// entry (one warp alone took 7 us longer at 2,374 entries a run).  Bound: the bytes of one row of p
 // (and one of q) per sequence for a large batch; for one sequence the chain of
 // dependent reads (draft, its probabilities, the row) and two cluster barriers.
 #include <cuda_fp16.h>
@@ -32,11 +41,12 @@ namespace {
 using namespace sm100;
 typedef unsigned __int128 u128;
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;  // portable cluster size
-constexpr int kMinPerCta = 8192;  // entries below which a row is not split further
+constexpr int kMaxCluster = 8;    // portable cluster size
+constexpr int kMinPerCta = 4096;  // entries below which a row is not split further
 constexpr int kSlots = 304;       // resident CTAs of this size: two on each of 152 SMs
+
 
 struct ProbsParams {
     const void *p, *q;  // q null: point mass
@@ -52,38 +62,78 @@ struct Prob;
 template <>
 struct Prob<VA_FLOAT_FP32> {
     using T = uint32_t;
-    static constexpr int kVec = 4;
+    static constexpr int kVec = 4, kUnroll = 4;  // kUnroll: 16-byte pieces of each row that a lane has in flight
     static __device__ __forceinline__ uint32_t bits(uint32_t x) { return x; }
 };
 template <>
 struct Prob<VA_FLOAT_BF16> {
     using T = uint16_t;
-    static constexpr int kVec = 8;
+    static constexpr int kVec = 8, kUnroll = 2;
     static __device__ __forceinline__ uint32_t bits(uint16_t x) { return (uint32_t)x << 16; }
 };
 template <>
 struct Prob<VA_FLOAT_FP16> {
     using T = uint16_t;
-    static constexpr int kVec = 8;
+    static constexpr int kVec = 8, kUnroll = 2;
     static __device__ __forceinline__ uint32_t bits(uint16_t x) {
         return __float_as_uint(__half2float(__ushort_as_half(x)));
     }
 };
 
-// A binary32 probability as a multiple of 2^-62: NaN and negative numbers 0, above one 1.
-__device__ __forceinline__ uint64_t fixed62(uint32_t bits) {
-    const int e = (int)(bits >> 23);
-    const uint64_t m = (bits & 0x7FFFFFu) | (e ? 0x800000u : 0u);  // value m 2^(e - 150)
-    const int s = e - 88;
-    uint64_t v = s >= 0 ? m << min(s, 39) : m >> min(-s, 31);
-    if (bits > 0x3F800000u) v = bits <= 0x7F800000u ? (uint64_t)1 << 62 : 0;
-    return v;
+// NaN and negative numbers count as 0, numbers above one as 1.
+__device__ __forceinline__ uint32_t sane(uint32_t bits) {
+    return bits <= 0x3F800000u ? bits : bits <= 0x7F800000u ? 0x3F800000u : 0u;
 }
 
-__device__ __forceinline__ uint64_t weight(uint32_t p_bits, uint32_t q_bits) {
-    const uint64_t a = fixed62(p_bits), b = fixed62(q_bits);
-    return a > b ? a - b : 0;
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) { return ((uint64_t)hi << 32) | lo; }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+constexpr uint32_t kStep1 = 0x41400000u;  // 12 = 1.5 * 2^3: steps of 2^-20
+constexpr uint32_t kStep2 = 0x36400000u;  // 1.5 * 2^-19: steps of 2^-42
+constexpr uint32_t kStep3 = 0x2C400000u;  // 1.5 * 2^-39: steps of 2^-62
+constexpr uint32_t kSign = 0x80000000u;
+
+__device__ __forceinline__ uint64_t twice(float x) { return pack2(__float_as_uint(x), __float_as_uint(x)); }
+
+// Two numbers in [0, 1] (binary32 bits) in the three steps, each plus the bits of its constant.
+struct Steps {
+    uint64_t n1, n2, n3;
+    __device__ __forceinline__ explicit Steps(uint64_t x) {
+        const uint64_t minus = twice(-1.f);
+        n1 = add2(x, pack2(kStep1, kStep1));
+        const uint64_t x1 = fma2(add2(n1, pack2(kStep1 | kSign, kStep1 | kSign)), minus, x);
+        n2 = add2(x1, pack2(kStep2, kStep2));
+        const uint64_t x2 = fma2(add2(n2, pack2(kStep2 | kSign, kStep2 | kSign)), minus, x1);
+        n3 = add2(x2, pack2(kStep3, kStep3));
+    }
+};
+
+// A sum of weights in the three steps.  One weight adds at most 2^20, 2^22 and 2^20 to them, so they hold kHeld weights
+// before they have to go into wider integers.
+constexpr int kHeld = 256;
+struct Sum {
+    int n1 = 0, n2 = 0, n3 = 0;
+    // Half `HALF` of p - q; without a model q is nothing and the constants are taken off
+    template <int HALF, bool MODEL>
+    __device__ __forceinline__ void add(const Steps &p, const Steps &q) {
+        constexpr int kShift = 32 * HALF;
+        n1 += (int)(uint32_t)(p.n1 >> kShift) - (MODEL ? (int)(uint32_t)(q.n1 >> kShift) : (int)kStep1);
+        n2 += (int)(uint32_t)(p.n2 >> kShift) - (MODEL ? (int)(uint32_t)(q.n2 >> kShift) : (int)kStep2);
+        n3 += (int)(uint32_t)(p.n3 >> kShift) - (MODEL ? (int)(uint32_t)(q.n3 >> kShift) : (int)kStep3);
+    }
+    // in units of 2^-62: not negative, below 2^71
+    __device__ __forceinline__ u128 value() const {
+        return (u128)(((__int128)n1 << 42) + ((int64_t)n2 << 20) + n3);
+    }
+};
 
 __device__ __forceinline__ u128 shfl_up(u128 v, int d) {
     const uint64_t lo = __shfl_up_sync(0xffffffffu, (uint64_t)v, d);
@@ -109,143 +159,205 @@ __device__ __forceinline__ u128 warp_scan(u128 v, int lane) {
 template <int TYPE>
 struct Row {
     using E = typename Prob<TYPE>::T;
-    static constexpr int kVec = Prob<TYPE>::kVec;
+    static constexpr int kVec = Prob<TYPE>::kVec, kUnroll = Prob<TYPE>::kUnroll;
+    union Vec {
+        uint4 raw;
+        E e[kVec];
+    };
     const E *p, *q;
     int drop;
     bool vec;  // both rows start on a 16-byte boundary
 
-    __device__ __forceinline__ uint64_t at(int i) const {
-        const uint32_t pb = Prob<TYPE>::bits(p[i]);
-        if (q) return weight(pb, Prob<TYPE>::bits(q[i]));
-        return i == drop ? 0 : fixed62(pb);
-    }
-    // the weights of entries i .. i + kVec - 1 (i a multiple of kVec), those from `hi` on as 0
-    __device__ __forceinline__ void load(int i, int hi, uint64_t (&w)[kVec]) const {
+    // entries i .. i + kVec - 1 (i a multiple of kVec) of one of the rows, those from `hi` on as 0
+    __device__ __forceinline__ uint4 load(const E *row, int i, int hi) const {
+        Vec v;
+        v.raw = make_uint4(0, 0, 0, 0);
         if (vec && i + kVec <= hi) {
-            const uint4 a = *reinterpret_cast<const uint4 *>(p + i);
-            const E *pe = reinterpret_cast<const E *>(&a);
-            if (q) {
-                const uint4 b = *reinterpret_cast<const uint4 *>(q + i);
-                const E *qe = reinterpret_cast<const E *>(&b);
-#pragma unroll
-                for (int k = 0; k < kVec; ++k) w[k] = weight(Prob<TYPE>::bits(pe[k]), Prob<TYPE>::bits(qe[k]));
-            } else {
-#pragma unroll
-                for (int k = 0; k < kVec; ++k) w[k] = i + k == drop ? 0 : fixed62(Prob<TYPE>::bits(pe[k]));
-            }
+            v.raw = *reinterpret_cast<const uint4 *>(row + i);
         } else {
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) w[k] = i + k < hi ? at(i + k) : 0;
+            for (int k = 0; k < kVec; ++k)
+                if (i + k < hi) v.e[k] = row[i + k];
         }
+        return v.raw;
+    }
+    // their weights, pair by pair: f(k, p's steps, q's steps) for entries i + k and i + k + 1
+    template <bool MODEL, typename F>
+    __device__ __forceinline__ void weights(const uint4 &praw, const uint4 &qraw, int i, F f) const {
+        Vec pv, qv;
+        pv.raw = praw;
+        qv.raw = qraw;
+        uint32_t a[kVec], b[kVec], most = 0;
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) {
+            a[k] = Prob<TYPE>::bits(pv.e[k]);
+            b[k] = MODEL ? Prob<TYPE>::bits(qv.e[k]) : 0;
+            most = max(most, max(a[k], b[k]));
+        }
+        if (most > 0x3F800000u) {  // not probabilities: rare
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) {
+                a[k] = sane(a[k]);
+                b[k] = sane(b[k]);
+            }
+        }
+        if (!MODEL && (unsigned)(drop - i) < kVec) {
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) a[k] = i + k == drop ? 0 : a[k];
+        }
+#pragma unroll
+        for (int k = 0; k < kVec; k += 2) {
+            const Steps p2(pack2(a[k], a[k + 1]));
+            // bits order as the numbers do: the smaller of the two as q leaves 0 where q >= p
+            const Steps q2(MODEL ? pack2(min(a[k], b[k]), min(a[k + 1], b[k + 1])) : 0);
+            f(k, p2, q2);
+        }
+    }
+
+    // this lane's share of the sum over [lo, hi)
+    template <bool MODEL>
+    __device__ u128 sum(int lo, int hi, int lane) const {
+        u128 total = 0;
+        int base = lo + lane * kVec;
+        while (base < hi) {
+            Sum s;
+            for (int r = 0; r < kHeld / (kVec * kUnroll) && base < hi; ++r, base += 32 * kVec * kUnroll) {
+                uint4 pv[kUnroll], qv[kUnroll];
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) {
+                    const int i = base + u * 32 * kVec;
+                    pv[u] = load(p, i, hi);
+                    if (MODEL) qv[u] = load(q, i, hi);
+                    else qv[u] = make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u)
+                    weights<MODEL>(pv[u], qv[u], base + u * 32 * kVec, [&](int, const Steps &p2, const Steps &q2) {
+                        s.template add<0, MODEL>(p2, q2);
+                        s.template add<1, MODEL>(p2, q2);
+                    });
+            }
+            total += s.value();
+        }
+        return total;
+    }
+
+    // The first entry of [lo, hi) where `before` plus the sum from lo passes the threshold, found by the whole CTA, one
+    // vector a thread; exactly one thread gets it, the others -1.
+    template <bool MODEL>
+    __device__ int pass(int lo, int hi, u128 before, u128 threshold, u128 *s_sums) const {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        for (int base = lo; base < hi; base += kThreads * kVec) {
+            const int i = base + threadIdx.x * kVec;
+            const uint4 pv = load(p, i, hi), qv = MODEL ? load(q, i, hi) : make_uint4(0, 0, 0, 0);
+            Sum s;
+            weights<MODEL>(pv, qv, i, [&](int, const Steps &p2, const Steps &q2) {
+                s.template add<0, MODEL>(p2, q2);
+                s.template add<1, MODEL>(p2, q2);
+            });
+            const u128 own = s.value(), inc = warp_scan(own, lane);
+            __syncthreads();  // s_sums may still be read
+            if (lane == 31) s_sums[warp] = inc;
+            __syncthreads();
+            const u128 sums = warp_scan(lane < kWarps ? s_sums[lane] : 0, lane);
+            const u128 chunk = shfl(sums, 31), earlier = shfl(sums, max(warp - 1, 0));
+            const u128 start = before + inc - own + (warp ? earlier : 0);
+            int token = -1;
+            if (start <= threshold && threshold < start + own) {  // one thread
+                Sum upto;
+                weights<MODEL>(pv, qv, i, [&](int k, const Steps &p2, const Steps &q2) {
+                    upto.template add<0, MODEL>(p2, q2);
+                    if (token < 0 && start + upto.value() > threshold) token = i + k;
+                    upto.template add<1, MODEL>(p2, q2);
+                    if (token < 0 && start + upto.value() > threshold) token = i + k + 1;
+                });
+            }
+            before += chunk;
+            if (before > threshold) return token;  // all threads: one of them has it
+        }
+        return -1;
     }
 };
 
 template <int TYPE>
-__global__ void __launch_bounds__(kThreads) accept_probs_kernel(const ProbsParams a) {
+__global__ void __launch_bounds__(kThreads, 2) accept_probs_kernel(const ProbsParams a) {
     using E = typename Prob<TYPE>::T;
     constexpr int kVec = Prob<TYPE>::kVec;
     __shared__ int s_first;
     __shared__ u128 s_warp[kWarps];  // sums of the warps' runs, then the sums before them
-    __shared__ uint64_t s_cta[2];    // this CTA's sum, read by the others
+    __shared__ u128 s_sums[kWarps];
+    __shared__ uint64_t s_cta[2][2];  // this CTA's sum in each pass, read by the others
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rank = (int)cluster_rank(), ctas = (int)cluster_size();
     const int b = blockIdx.y;
+    if (threadIdx.x == 0) s_first = 0x7FFFFFFF;
+    __syncthreads();
     griddep_wait();
     const int count = a.lens ? min(max(a.lens[b], 0), a.T) : a.T;
     const E *p0 = static_cast<const E *>(a.p) + b * a.p_seq;
     const E *q0 = a.q ? static_cast<const E *>(a.q) + b * a.q_seq : nullptr;
-    if (threadIdx.x == 0) s_first = count;
-    __syncthreads();
+    const float u_emit = a.u_emit[b];
+    int32_t *out = a.out + (int64_t)b * (a.T + 1);
     for (int t = threadIdx.x; t < count; t += kThreads) {
         const int d = a.drafts[(int64_t)b * a.T + t];
+        const double u = (double)a.u_accept[(int64_t)b * a.T + t];
         bool ok = d >= 0 && d < a.V;
         if (ok) {
             const double p = (double)__uint_as_float(Prob<TYPE>::bits(p0[t * a.p_pos + d]));
             const double q = q0 ? (double)__uint_as_float(Prob<TYPE>::bits(q0[t * a.q_pos + d])) : 1.0;
-            ok = (double)a.u_accept[(int64_t)b * a.T + t] * q < p;
+            ok = u * q < p;
         }
         if (!ok) atomicMin(&s_first, t);
     }
     __syncthreads();
-    const int n = s_first;
-    const int dn = n < count ? a.drafts[(int64_t)b * a.T + n] : -1;
+    const int n = min(s_first, count);
+    const bool rejected = n < count;
 
     Row<TYPE> row;
     row.p = p0 + n * a.p_pos;
-    row.q = n < count && q0 ? q0 + n * a.q_pos : nullptr;
-    row.drop = n < count && !q0 ? dn : -1;
+    row.q = rejected && q0 ? q0 + n * a.q_pos : nullptr;
+    row.drop = rejected && !q0 ? a.drafts[(int64_t)b * a.T + n] : -1;
     const int per_warp = ((a.V + ctas * kWarps - 1) / (ctas * kWarps) + kVec - 1) / kVec * kVec;
     const int64_t start = (int64_t)(rank * kWarps + warp) * per_warp;
     const int lo = (int)min((int64_t)a.V, start), hi = (int)min((int64_t)a.V, start + per_warp);
 
-    int token = -1;
-    bool mine = false, empty = false;
+    bool empty = false;
     for (int pass = 0; pass < 2; ++pass) {  // the second only where the residual is zero everywhere
         row.vec = ((reinterpret_cast<uintptr_t>(row.p) | reinterpret_cast<uintptr_t>(row.q)) & 15) == 0;
-        u128 sum = 0;
-        for (int i = lo + lane * kVec; i < hi; i += 32 * kVec) {
-            uint64_t w[kVec];
-            row.load(i, hi, w);
-#pragma unroll
-            for (int k = 0; k < kVec; ++k) sum += w[k];
-        }
-        sum = warp_scan(sum, lane);
+        const u128 sum = warp_scan(row.q ? row.template sum<true>(lo, hi, lane) : row.template sum<false>(lo, hi, lane), lane);
         if (lane == 31) s_warp[warp] = sum;
         __syncthreads();
         if (warp == 0) {
-            const u128 v = s_warp[lane], inc = warp_scan(v, lane);
-            s_warp[lane] = inc - v;
+            const u128 v = lane < kWarps ? s_warp[lane] : 0, inc = warp_scan(v, lane);
+            if (lane < kWarps) s_warp[lane] = inc - v;
             if (lane == 31) {
-                s_cta[0] = (uint64_t)inc;
-                s_cta[1] = (uint64_t)(inc >> 64);
+                s_cta[pass][0] = (uint64_t)inc;
+                s_cta[pass][1] = (uint64_t)(inc >> 64);
             }
         }
         cluster_sync();
         u128 before = 0, total = 0;
         for (int r = 0; r < ctas; ++r) {
-            const u128 x = ((u128)ld_cluster_u64(&s_cta[1], r) << 64) | ld_cluster_u64(&s_cta[0], r);
+            const u128 x = ((u128)ld_cluster_u64(&s_cta[pass][1], r) << 64) | ld_cluster_u64(&s_cta[pass][0], r);
             if (r < rank) before += x;
             total += x;
         }
-        cluster_sync();  // s_cta may be rewritten, and the CTA may leave
         if (total != 0) {
-            float u = a.u_emit[b];
-            u = u > 0.f ? fminf(u, 0.999999940395355224609375f) : 0.f;  // 1 - 2^-24; NaN: 0
+            const float u = u_emit > 0.f ? fminf(u_emit, 0.999999940395355224609375f) : 0.f;  // 1 - 2^-24; NaN: 0
             const uint32_t bits = __float_as_uint(u);
             const int e = (int)(bits >> 23);
             const uint32_t m = (bits & 0x7FFFFFu) | (e ? 0x800000u : 0u);
             const int k = 150 - max(e, 1);  // u = m 2^-k, 24 <= k <= 149
             const u128 threshold = k < 128 ? ((u128)m * total) >> k : 0;
-            before += s_warp[warp];
-            const u128 own = shfl(sum, 31);
-            mine = before <= threshold && threshold < before + own;
-            if (mine) {
-                for (int base = lo; base < hi; base += 32 * kVec) {
-                    uint64_t w[kVec];
-                    u128 s = 0;
-                    const int i = base + lane * kVec;
-                    if (i < hi) {
-                        row.load(i, hi, w);
-#pragma unroll
-                        for (int j = 0; j < kVec; ++j) s += w[j];
-                    }
-                    const u128 inc = warp_scan(s, lane);
-                    const unsigned past = __ballot_sync(0xffffffffu, before + inc > threshold);
-                    if (past) {
-                        const int who = __ffs(past) - 1;
-                        if (lane == who) {
-                            u128 c = before + inc - s;
-#pragma unroll
-                            for (int j = 0; j < kVec; ++j) {
-                                c += w[j];
-                                if (token < 0 && c > threshold) token = i + j;
-                            }
-                        }
-                        token = __shfl_sync(0xffffffffu, token, who);
-                        break;
-                    }
-                    before += shfl(inc, 31);
-                }
+            const u128 own = ((u128)s_cta[pass][1] << 64) | s_cta[pass][0];
+            if (before <= threshold && threshold < before + own) {  // in this CTA's slice: in whose run?
+                const int w = 31 - __clz(__ballot_sync(0xffffffffu, lane < kWarps && before + s_warp[lane % kWarps] <= threshold));
+                before += s_warp[w];
+                const int64_t from = (int64_t)(rank * kWarps + w) * per_warp;
+                const int run_lo = (int)min((int64_t)a.V, from), run_hi = (int)min((int64_t)a.V, from + per_warp);
+                const int token = row.q ? row.template pass<true>(run_lo, run_hi, before, threshold, s_sums)
+                                        : row.template pass<false>(run_lo, run_hi, before, threshold, s_sums);
+                if (token >= 0) out[n] = token;
             }
             break;
         }
@@ -254,13 +366,12 @@ __global__ void __launch_bounds__(kThreads) accept_probs_kernel(const ProbsParam
         row.q = nullptr;
         row.drop = -1;
     }
-    int32_t *out = a.out + (int64_t)b * (a.T + 1);
-    if (mine && lane == 0) out[n] = token;
     if (rank == 0) {
         for (int t = threadIdx.x; t <= a.T; t += kThreads)
             if (t != n || empty) out[t] = t < n ? a.drafts[(int64_t)b * a.T + t] : -1;
         if (threadIdx.x == 0) a.nacc[b] = n;
     }
+    cluster_sync();  // no CTA leaves while another may read its sum
 }
 
 template <int TYPE>
