@@ -64,11 +64,11 @@ def rope(x, positions, inv_freq, axis, adjacent=False, scale=1.0, inverse=False)
 # ------------------------------------------------------------------ acceptance
 
 
-def fixed62(p):
-    """Probabilities as multiples of 2^-62, Python integers: NaN and negative 0, above one 1."""
+def fixed54(p):
+    """Probabilities as multiples of 2^-54, Python integers: NaN and negative 0, above one 1."""
     p = np.asarray(p, np.float64)
     p = np.where(np.isnan(p), 0.0, np.clip(p, 0.0, 1.0))
-    return [int(v) for v in np.rint(p * 2.0 ** 62).astype(np.uint64)]
+    return [int(v) for v in np.rint(p * 2.0 ** 54).astype(np.uint64)]
 
 
 def accept_probs(p, drafts, u_accept, u_emit, q=None, lens=None):
@@ -91,13 +91,13 @@ def accept_probs(p, drafts, u_accept, u_emit, q=None, lens=None):
             out[b, n] = d
             n += 1
         nacc[b] = n
-        full = fixed62(p[b, n])
+        full = fixed54(p[b, n])
         weights = full
         if n < count:
             if q is None:
                 weights = [0 if i == int(drafts[b][n]) else w for i, w in enumerate(full)]
             else:
-                weights = [max(0, w - v) for w, v in zip(full, fixed62(q[b][n]))]
+                weights = [max(0, w - v) for w, v in zip(full, fixed54(q[b][n]))]
             if not any(weights):
                 weights = full
         total = sum(weights)

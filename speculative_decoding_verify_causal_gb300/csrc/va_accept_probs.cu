@@ -4,27 +4,29 @@
 // Mathematics.  The decisions u q < p are products of two binary32 numbers,
 // exact in binary64.  The emitted token inverts the cumulative distribution of
 // the weights, a whole number that must not depend on how the sum is split: so
-// every p and q is rounded to a multiple of 2^-62, the residual max(0, p - q)
+// every p and q is rounded to a multiple of 2^-54, the residual max(0, p - q)
 // is an exact integer subtraction and the sums are exact 128-bit integers.  The
 // threshold u W is m W / 2^k for u = m 2^-k with m of 24 bits: exact in 128
 // bits too, and sum > u W holds for integers exactly where sum > floor(m W /
-// 2^k).
+// 2^k).  Rounding each of 152k entries by 2^-55 moves a sum by some 1e-14.
 //
-// The integers are read off binary32 additions.  x + 12 lies in [8, 16), where
-// binary32 counts in steps of 2^-20: its last bits are x in those steps,
-// rounded, and what the rounding left, x - ((x + 12) - 12), is exact.  Twice
-// more, in steps of 2^-42 and 2^-62, gives x as n1 2^-20 + n2 2^-42 + n3 2^-62
-// with three small signed integers, which are summed as they are (the
-// constants cancel in p - q).  That is seven additions a number, two numbers
-// an instruction (add.f32x2).  Shifting significands into 64-bit integers took
-// about four times the instructions (64 sequences, vocabulary 151,936: 34.8 us
-// with it); binary64 does two lanes a clock and SM here.
+// The integers are read off binary32 additions.  x + 1.5 2^-9 lies where
+// binary32 counts in steps of 2^-32: its last bits are x in those steps,
+// rounded, and what the rounding left, x - ((x + 1.5 2^-9) - 1.5 2^-9), is
+// exact.  Once more in steps of 2^-54, and x is n2 2^-32 + n3 2^-54 with two
+// small signed integers, which are summed as they are (the constants cancel in
+// p - q).  That holds for x below 2^-10; the few larger ones first go through
+// steps of 2^-10.  Two numbers an instruction (add.f32x2, fma.f32x2), four or
+// seven of them a number.  64 sequences at a vocabulary of 151,936 (two rows
+// where a model's draft is rejected): 34.8 us with significands shifted into
+// 64-bit integers, which takes about four times the instructions; binary64
+// does two lanes a clock and SM here.
 //
 // One thread-block cluster per sequence.  Every CTA evaluates the (at most T)
 // acceptance tests; each then sums its slice of the one row that decides, a
 // contiguous run per warp, and the CTAs exchange their sums through
 // distributed shared memory.  The CTA whose slice holds the threshold reads the
-// one run that holds it again (from L2), a vector a thread, and finds the
+// one run that holds it again (from L2), eight entries a thread, and finds the
 // entry (one warp alone took 7 us longer at 2,374 entries a run).  Bound: the bytes of one row of p
 // (and one of q) per sequence for a large batch; for one sequence the chain of
 // dependent reads (draft, its probabilities, the row) and two cluster barriers.
@@ -62,19 +64,19 @@ struct Prob;
 template <>
 struct Prob<VA_FLOAT_FP32> {
     using T = uint32_t;
-    static constexpr int kVec = 4, kUnroll = 4;  // kUnroll: 16-byte pieces of each row that a lane has in flight
+    static constexpr int kVec = 4;
     static __device__ __forceinline__ uint32_t bits(uint32_t x) { return x; }
 };
 template <>
 struct Prob<VA_FLOAT_BF16> {
     using T = uint16_t;
-    static constexpr int kVec = 8, kUnroll = 2;
+    static constexpr int kVec = 8;
     static __device__ __forceinline__ uint32_t bits(uint16_t x) { return (uint32_t)x << 16; }
 };
 template <>
 struct Prob<VA_FLOAT_FP16> {
     using T = uint16_t;
-    static constexpr int kVec = 8, kUnroll = 2;
+    static constexpr int kVec = 8;
     static __device__ __forceinline__ uint32_t bits(uint16_t x) {
         return __float_as_uint(__half2float(__ushort_as_half(x)));
     }
@@ -96,42 +98,52 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-constexpr uint32_t kStep1 = 0x41400000u;  // 12 = 1.5 * 2^3: steps of 2^-20
-constexpr uint32_t kStep2 = 0x36400000u;  // 1.5 * 2^-19: steps of 2^-42
-constexpr uint32_t kStep3 = 0x2C400000u;  // 1.5 * 2^-39: steps of 2^-62
 constexpr uint32_t kSign = 0x80000000u;
+constexpr uint32_t kStep1 = 0x46400000u;  // 1.5 * 2^13: steps of 2^-10
+constexpr uint32_t kStep2 = 0x3B400000u;  // 1.5 * 2^-9: steps of 2^-32
+constexpr uint32_t kStep3 = 0x30400000u;  // 1.5 * 2^-31: steps of 2^-54
+constexpr uint32_t kOne = 0x3F800000u;
+constexpr uint32_t kSmall = 0x3A800000u;  // 2^-10: numbers below need no first step
 
-__device__ __forceinline__ uint64_t twice(float x) { return pack2(__float_as_uint(x), __float_as_uint(x)); }
-
-// Two numbers in [0, 1] (binary32 bits) in the three steps, each plus the bits of its constant.
+// Two numbers in [0, 1] (binary32 bits) in the three steps, each plus the bits of its constant; FIRST = false where both are
+// below 2^-10.
+template <bool FIRST>
 struct Steps {
     uint64_t n1, n2, n3;
+    static __device__ __forceinline__ uint64_t left(uint64_t x, uint64_t n, uint32_t step) {  // x - (n - step), exact
+        return fma2(add2(n, pack2(step | kSign, step | kSign)), pack2(kOne | kSign, kOne | kSign), x);
+    }
     __device__ __forceinline__ explicit Steps(uint64_t x) {
-        const uint64_t minus = twice(-1.f);
-        n1 = add2(x, pack2(kStep1, kStep1));
-        const uint64_t x1 = fma2(add2(n1, pack2(kStep1 | kSign, kStep1 | kSign)), minus, x);
-        n2 = add2(x1, pack2(kStep2, kStep2));
-        const uint64_t x2 = fma2(add2(n2, pack2(kStep2 | kSign, kStep2 | kSign)), minus, x1);
-        n3 = add2(x2, pack2(kStep3, kStep3));
+        n1 = 0;
+        if (FIRST) {
+            n1 = add2(x, pack2(kStep1, kStep1));
+            x = left(x, n1, kStep1);
+        }
+        n2 = add2(x, pack2(kStep2, kStep2));
+        n3 = add2(left(x, n2, kStep2), pack2(kStep3, kStep3));
     }
 };
 
-// A sum of weights in the three steps.  One weight adds at most 2^20, 2^22 and 2^20 to them, so they hold kHeld weights
-// before they have to go into wider integers.
+// A sum of weights in the three steps.  One weight adds at most 2^10, 2^22 and 2^22 to them (the first step leaves at most
+// 2^-11, the second 2^-33; without the first, numbers below 2^-10), so they hold kHeld weights before they have to go into
+// wider integers.
 constexpr int kHeld = 256;
 struct Sum {
     int n1 = 0, n2 = 0, n3 = 0;
-    // Half `HALF` of p - q; without a model q is nothing and the constants are taken off
-    template <int HALF, bool MODEL>
-    __device__ __forceinline__ void add(const Steps &p, const Steps &q) {
-        constexpr int kShift = 32 * HALF;
-        n1 += (int)(uint32_t)(p.n1 >> kShift) - (MODEL ? (int)(uint32_t)(q.n1 >> kShift) : (int)kStep1);
-        n2 += (int)(uint32_t)(p.n2 >> kShift) - (MODEL ? (int)(uint32_t)(q.n2 >> kShift) : (int)kStep2);
-        n3 += (int)(uint32_t)(p.n3 >> kShift) - (MODEL ? (int)(uint32_t)(q.n3 >> kShift) : (int)kStep3);
+    template <bool FIRST, bool MODEL>
+    __device__ __forceinline__ void add(const Steps<FIRST> &p, const Steps<FIRST> &q) {  // both halves of p - q, or of p
+        if (FIRST) n1 += both<MODEL>(p.n1, q.n1, kStep1);
+        n2 += both<MODEL>(p.n2, q.n2, kStep2);
+        n3 += both<MODEL>(p.n3, q.n3, kStep3);
     }
-    // in units of 2^-62: not negative, below 2^71
-    __device__ __forceinline__ u128 value() const {
-        return (u128)(((__int128)n1 << 42) + ((int64_t)n2 << 20) + n3);
+    template <bool MODEL>
+    static __device__ __forceinline__ int both(uint64_t p, uint64_t q, uint32_t step) {
+        const int lo = (int)(uint32_t)p - (MODEL ? (int)(uint32_t)q : (int)step);
+        return lo + (int)(uint32_t)(p >> 32) - (MODEL ? (int)(uint32_t)(q >> 32) : (int)step);
+    }
+    // in units of 2^-54: not negative, below 2^63
+    __device__ __forceinline__ uint64_t value() const {
+        return (uint64_t)(((int64_t)n1 << 44) + ((int64_t)n2 << 22) + n3);
     }
 };
 
@@ -159,7 +171,7 @@ __device__ __forceinline__ u128 warp_scan(u128 v, int lane) {
 template <int TYPE>
 struct Row {
     using E = typename Prob<TYPE>::T;
-    static constexpr int kVec = Prob<TYPE>::kVec, kUnroll = Prob<TYPE>::kUnroll;
+    static constexpr int kVec = Prob<TYPE>::kVec;
     union Vec {
         uint4 raw;
         E e[kVec];
@@ -168,22 +180,22 @@ struct Row {
     int drop;
     bool vec;  // both rows start on a 16-byte boundary
 
-    // entries i .. i + kVec - 1 (i a multiple of kVec) of one of the rows, those from `hi` on as 0
-    __device__ __forceinline__ uint4 load(const E *row, int i, int hi) const {
+    // entries i .. i + kVec - 1 (i a multiple of kVec) of a row that starts anywhere, or that ends among them (as 0)
+    static __device__ __forceinline__ uint4 load_slowly(const E *row, int i, int hi) {
         Vec v;
         v.raw = make_uint4(0, 0, 0, 0);
-        if (vec && i + kVec <= hi) {
-            v.raw = *reinterpret_cast<const uint4 *>(row + i);
-        } else {
 #pragma unroll
-            for (int k = 0; k < kVec; ++k)
-                if (i + k < hi) v.e[k] = row[i + k];
-        }
+        for (int k = 0; k < kVec; ++k)
+            if (i + k < hi) v.e[k] = row[i + k];
         return v.raw;
     }
-    // their weights, pair by pair: f(k, p's steps, q's steps) for entries i + k and i + k + 1
-    template <bool MODEL, typename F>
-    __device__ __forceinline__ void weights(const uint4 &praw, const uint4 &qraw, int i, F f) const {
+    __device__ __forceinline__ uint4 load(const E *row, int i, int hi) const {
+        if (i >= hi || !row) return make_uint4(0, 0, 0, 0);
+        if (vec && i + kVec <= hi) return *reinterpret_cast<const uint4 *>(row + i);
+        return load_slowly(row, i, hi);
+    }
+    template <bool MODEL>
+    __device__ __forceinline__ void add(Sum &s, const uint4 &praw, const uint4 &qraw, int i) const {
         Vec pv, qv;
         pv.raw = praw;
         qv.raw = qraw;
@@ -194,67 +206,83 @@ struct Row {
             b[k] = MODEL ? Prob<TYPE>::bits(qv.e[k]) : 0;
             most = max(most, max(a[k], b[k]));
         }
-        if (most > 0x3F800000u) {  // not probabilities: rare
-#pragma unroll
-            for (int k = 0; k < kVec; ++k) {
-                a[k] = sane(a[k]);
-                b[k] = sane(b[k]);
-            }
-        }
         if (!MODEL && (unsigned)(drop - i) < kVec) {
 #pragma unroll
             for (int k = 0; k < kVec; ++k) a[k] = i + k == drop ? 0 : a[k];
         }
+        if (most < kSmall) {
+            add_steps<false, MODEL>(s, a, b);
+        } else {
+            if (most > kOne) {  // not probabilities: rare
 #pragma unroll
-        for (int k = 0; k < kVec; k += 2) {
-            const Steps p2(pack2(a[k], a[k + 1]));
-            // bits order as the numbers do: the smaller of the two as q leaves 0 where q >= p
-            const Steps q2(MODEL ? pack2(min(a[k], b[k]), min(a[k + 1], b[k + 1])) : 0);
-            f(k, p2, q2);
+                for (int k = 0; k < kVec; ++k) {
+                    a[k] = sane(a[k]);
+                    b[k] = sane(b[k]);
+                }
+            }
+            add_steps<true, MODEL>(s, a, b);
         }
+    }
+    template <bool FIRST, bool MODEL>
+    static __device__ __forceinline__ void add_steps(Sum &s, const uint32_t (&a)[kVec], const uint32_t (&b)[kVec]) {
+#pragma unroll
+        for (int k = 0; k < kVec; k += 2) {  // bits order as the numbers do: the smaller of the two as q leaves 0 where q >= p
+            const Steps<FIRST> p2(pack2(a[k], a[k + 1]));
+            if (MODEL) s.add<FIRST, true>(p2, Steps<FIRST>(pack2(min(a[k], b[k]), min(a[k + 1], b[k + 1]))));
+            else s.add<FIRST, false>(p2, p2);
+        }
+    }
+    __device__ __forceinline__ uint64_t one(int i) const {  // the weight of one entry
+        const uint32_t a = sane(Prob<TYPE>::bits(p[i])), b = i == drop ? a : q ? sane(Prob<TYPE>::bits(q[i])) : 0;
+        Sum s;
+        s.add<true, true>(Steps<true>(a), Steps<true>(min(a, b)));
+        return s.value();
     }
 
     // this lane's share of the sum over [lo, hi)
     template <bool MODEL>
-    __device__ u128 sum(int lo, int hi, int lane) const {
+    __device__ __forceinline__ u128 sum(int lo, int hi, int lane) const {
+        constexpr int U = (MODEL ? 16 : 32) / kVec;  // 64 bytes (fp32) of each row in flight, 128 of one row
         u128 total = 0;
         int base = lo + lane * kVec;
         while (base < hi) {
             Sum s;
-            for (int r = 0; r < kHeld / (kVec * kUnroll) && base < hi; ++r, base += 32 * kVec * kUnroll) {
-                uint4 pv[kUnroll], qv[kUnroll];
+            for (int r = 0; r < kHeld / (kVec * U) && base < hi; ++r, base += 32 * kVec * U) {
+                uint4 pv[U], qv[U];
 #pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    const int i = base + u * 32 * kVec;
-                    pv[u] = load(p, i, hi);
-                    if (MODEL) qv[u] = load(q, i, hi);
-                    else qv[u] = make_uint4(0, 0, 0, 0);
+                for (int u = 0; u < U; ++u) {
+                    pv[u] = load(p, base + u * 32 * kVec, hi);
+                    if (MODEL) qv[u] = load(q, base + u * 32 * kVec, hi);
                 }
 #pragma unroll
-                for (int u = 0; u < kUnroll; ++u)
-                    weights<MODEL>(pv[u], qv[u], base + u * 32 * kVec, [&](int, const Steps &p2, const Steps &q2) {
-                        s.template add<0, MODEL>(p2, q2);
-                        s.template add<1, MODEL>(p2, q2);
-                    });
+                for (int u = 0; u < U; ++u)
+                    if (base + u * 32 * kVec < hi) add<MODEL>(s, pv[u], MODEL ? qv[u] : pv[u], base + u * 32 * kVec);
             }
             total += s.value();
         }
         return total;
     }
 
-    // The first entry of [lo, hi) where `before` plus the sum from lo passes the threshold, found by the whole CTA, one
-    // vector a thread; exactly one thread gets it, the others -1.
-    template <bool MODEL>
-    __device__ int pass(int lo, int hi, u128 before, u128 threshold, u128 *s_sums) const {
+    // The first entry of [lo, hi) where `before` plus the sum from lo passes the threshold, found by the whole CTA, kEach
+    // neighbouring entries a thread.  One warp finds it (token >= 0 in all its lanes), the others get -1.
+    __device__ __forceinline__ int pass(int lo, int hi, u128 before, u128 threshold, u128 *s_sums) const {
+        constexpr int kEach = 8;
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        for (int base = lo; base < hi; base += kThreads * kVec) {
-            const int i = base + threadIdx.x * kVec;
-            const uint4 pv = load(p, i, hi), qv = MODEL ? load(q, i, hi) : make_uint4(0, 0, 0, 0);
+        int token = -1;
+        for (int base = lo; base < hi && before <= threshold; base += kThreads * kEach) {
+            const int i = base + threadIdx.x * kEach;
             Sum s;
-            weights<MODEL>(pv, qv, i, [&](int, const Steps &p2, const Steps &q2) {
-                s.template add<0, MODEL>(p2, q2);
-                s.template add<1, MODEL>(p2, q2);
-            });
+            uint4 pv[kEach / kVec], qv[kEach / kVec];
+#pragma unroll
+            for (int u = 0; u < kEach / kVec; ++u) {
+                pv[u] = load(p, i + u * kVec, hi);
+                qv[u] = load(q, i + u * kVec, hi);
+            }
+#pragma unroll
+            for (int u = 0; u < kEach / kVec; ++u) {
+                if (q) add<true>(s, pv[u], qv[u], i + u * kVec);
+                else add<false>(s, pv[u], pv[u], i + u * kVec);
+            }
             const u128 own = s.value(), inc = warp_scan(own, lane);
             __syncthreads();  // s_sums may still be read
             if (lane == 31) s_sums[warp] = inc;
@@ -262,20 +290,15 @@ struct Row {
             const u128 sums = warp_scan(lane < kWarps ? s_sums[lane] : 0, lane);
             const u128 chunk = shfl(sums, 31), earlier = shfl(sums, max(warp - 1, 0));
             const u128 start = before + inc - own + (warp ? earlier : 0);
-            int token = -1;
-            if (start <= threshold && threshold < start + own) {  // one thread
-                Sum upto;
-                weights<MODEL>(pv, qv, i, [&](int k, const Steps &p2, const Steps &q2) {
-                    upto.template add<0, MODEL>(p2, q2);
-                    if (token < 0 && start + upto.value() > threshold) token = i + k;
-                    upto.template add<1, MODEL>(p2, q2);
-                    if (token < 0 && start + upto.value() > threshold) token = i + k + 1;
-                });
-            }
             before += chunk;
-            if (before > threshold) return token;  // all threads: one of them has it
+            const unsigned mine = __ballot_sync(0xffffffffu, start <= threshold && threshold < start + own);
+            if (mine) {  // this warp: the lane's entries one to a lane
+                const int who = __ffs(mine) - 1, first = base + (warp * 32 + who) * kEach;
+                const u128 each = warp_scan(lane < kEach && first + lane < hi ? one(first + lane) : 0, lane);
+                token = first + __ffs(__ballot_sync(0xffffffffu, shfl(start, who) + each > threshold)) - 1;
+            }
         }
-        return -1;
+        return token;
     }
 };
 
@@ -286,12 +309,13 @@ __global__ void __launch_bounds__(kThreads, 2) accept_probs_kernel(const ProbsPa
     __shared__ int s_first;
     __shared__ u128 s_warp[kWarps];  // sums of the warps' runs, then the sums before them
     __shared__ u128 s_sums[kWarps];
-    __shared__ uint64_t s_cta[2][2];  // this CTA's sum in each pass, read by the others
+    __shared__ uint64_t s_ctas[2][kMaxCluster][2];  // the CTAs' sums in each pass, written by them
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rank = (int)cluster_rank(), ctas = (int)cluster_size();
     const int b = blockIdx.y;
     if (threadIdx.x == 0) s_first = 0x7FFFFFFF;
     __syncthreads();
+    cluster_arrive();  // this CTA runs: its shared memory may be written
     griddep_wait();
     const int count = a.lens ? min(max(a.lens[b], 0), a.T) : a.T;
     const E *p0 = static_cast<const E *>(a.p) + b * a.p_seq;
@@ -327,21 +351,20 @@ __global__ void __launch_bounds__(kThreads, 2) accept_probs_kernel(const ProbsPa
         const u128 sum = warp_scan(row.q ? row.template sum<true>(lo, hi, lane) : row.template sum<false>(lo, hi, lane), lane);
         if (lane == 31) s_warp[warp] = sum;
         __syncthreads();
+        if (pass == 0) cluster_wait();
         if (warp == 0) {
             const u128 v = lane < kWarps ? s_warp[lane] : 0, inc = warp_scan(v, lane);
             if (lane < kWarps) s_warp[lane] = inc - v;
-            if (lane == 31) {
-                s_cta[pass][0] = (uint64_t)inc;
-                s_cta[pass][1] = (uint64_t)(inc >> 64);
+            const u128 own = shfl(inc, 31);
+            if (lane < ctas) {
+                st_cluster_u64(&s_ctas[pass][rank][0], lane, (uint64_t)own);
+                st_cluster_u64(&s_ctas[pass][rank][1], lane, (uint64_t)(own >> 64));
             }
         }
-        cluster_sync();
-        u128 before = 0, total = 0;
-        for (int r = 0; r < ctas; ++r) {
-            const u128 x = ((u128)ld_cluster_u64(&s_cta[pass][1], r) << 64) | ld_cluster_u64(&s_cta[pass][0], r);
-            if (r < rank) before += x;
-            total += x;
-        }
+        cluster_sync();  // all sums are here; nothing is written to another CTA after the last one
+        const u128 cta = lane < ctas ? ((u128)s_ctas[pass][lane][1] << 64) | s_ctas[pass][lane][0] : 0;
+        const u128 upto = warp_scan(cta, lane), own = shfl(cta, rank), total = shfl(upto, 31);
+        u128 before = shfl(upto, rank) - own;
         if (total != 0) {
             const float u = u_emit > 0.f ? fminf(u_emit, 0.999999940395355224609375f) : 0.f;  // 1 - 2^-24; NaN: 0
             const uint32_t bits = __float_as_uint(u);
@@ -349,15 +372,13 @@ __global__ void __launch_bounds__(kThreads, 2) accept_probs_kernel(const ProbsPa
             const uint32_t m = (bits & 0x7FFFFFu) | (e ? 0x800000u : 0u);
             const int k = 150 - max(e, 1);  // u = m 2^-k, 24 <= k <= 149
             const u128 threshold = k < 128 ? ((u128)m * total) >> k : 0;
-            const u128 own = ((u128)s_cta[pass][1] << 64) | s_cta[pass][0];
             if (before <= threshold && threshold < before + own) {  // in this CTA's slice: in whose run?
                 const int w = 31 - __clz(__ballot_sync(0xffffffffu, lane < kWarps && before + s_warp[lane % kWarps] <= threshold));
                 before += s_warp[w];
                 const int64_t from = (int64_t)(rank * kWarps + w) * per_warp;
                 const int run_lo = (int)min((int64_t)a.V, from), run_hi = (int)min((int64_t)a.V, from + per_warp);
-                const int token = row.q ? row.template pass<true>(run_lo, run_hi, before, threshold, s_sums)
-                                        : row.template pass<false>(run_lo, run_hi, before, threshold, s_sums);
-                if (token >= 0) out[n] = token;
+                const int token = row.pass(run_lo, run_hi, before, threshold, s_sums);
+                if (token >= 0 && lane == 0) out[n] = token;
             }
             break;
         }
@@ -371,7 +392,6 @@ __global__ void __launch_bounds__(kThreads, 2) accept_probs_kernel(const ProbsPa
             if (t != n || empty) out[t] = t < n ? a.drafts[(int64_t)b * a.T + t] : -1;
         if (threadIdx.x == 0) a.nacc[b] = n;
     }
-    cluster_sync();  // no CTA leaves while another may read its sum
 }
 
 template <int TYPE>

@@ -312,6 +312,10 @@ __device__ __forceinline__ uint32_t cluster_size() {
     return n;
 }
 
+// The cluster barrier in two halves: work between them overlaps the wait.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // Barrier over every thread of every CTA of the cluster, with release /
 // acquire ordering of shared-memory writes across the cluster.
 __device__ __forceinline__ void cluster_sync() {
@@ -325,6 +329,10 @@ __device__ __forceinline__ uint32_t cluster_map(const void *local, uint32_t rank
                  : "=r"(remote)
                  : "r"((uint32_t)__cvta_generic_to_shared(local)), "r"(rank));
     return remote;
+}
+
+__device__ __forceinline__ void st_cluster_u64(const void *local, uint32_t rank, unsigned long long v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(cluster_map(local, rank)), "l"(v) : "memory");
 }
 
 __device__ __forceinline__ unsigned long long ld_cluster_u64(const void *local, uint32_t rank) {

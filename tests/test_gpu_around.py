@@ -470,15 +470,19 @@ def test_accept_probs_borders(va):
     case(half, flat, -1, 0.0, 0.9)          # no such token
     case(half, flat, V, 0.0, 0.9, half)
     case(half, flat, 3, nan, 0.2)           # no comparison with NaN holds
-    odd = [nan, -0.5, inf, 2.0, 1e-45, 2.0 ** -62, 2.0 ** -63, -inf, -0.0] + [0.0] * (V - 9)
+    odd = [nan, -0.5, inf, 2.0, 1e-45, 2.0 ** -54, 2.0 ** -55, -inf, -0.0] + [0.0] * (V - 9)
     for ue in (0.0, 0.49, 0.5, 0.51, 0.9999):
         case(odd, odd, 0, 0.1, ue)          # draft 0 has p = NaN: rejected
         case(odd, odd, 2, 0.1, ue)          # p = inf: accepted
         case(odd, odd, 8, 0.1, ue, odd)
     tiny = [0.0] * V
-    tiny[10], tiny[20] = 2.0 ** -61, 2.0 ** -62
-    for ue in (0.0, 0.66, 0.67, 0.99):
+    tiny[10], tiny[20], tiny[30], tiny[40] = 2.0 ** -53, 2.0 ** -54, 2.0 ** -55, 1.5 * 2.0 ** -54
+    for ue in (0.0, 0.39, 0.41, 0.59, 0.61, 0.99):
         case(tiny, tiny, 20, 0.5, ue)
+    edge = [2.0 ** -10, 2.0 ** -10 - 2.0 ** -34, 2.0 ** -11, 3.0 * 2.0 ** -33, 2.0 ** -32 + 2.0 ** -55] + [0.0] * (V - 5)
+    for ue in (0.0, 0.3, 0.399999, 0.4, 0.7999, 0.8, 0.999999):  # around the steps in which the numbers are read
+        case(edge, edge, 60, 0.5, ue)
+        case(edge, edge, 60, 0.5, ue, [x / 2 for x in edge])
     for model in (False, True):
         some = [r for r in rows if (r[5] is not None) == model]
         p = torch.tensor([[r[0], r[1]] for r in some], dtype=torch.float32)
