@@ -487,10 +487,9 @@ int verify_attn_rope(const va_rope *rope, const va_positions *positions, va_floa
  * positions NULL: every axis is the token's place in its sequence,
  * L_b - T + t.  Cache, block table, seq_lens, num_pages and flags as for
  * verify_attn_kv_append; rows whose block lies outside the block table's row
- * are skipped and flagged as well.  head_dim in {64, 128, 256}; num_pairs a
- * multiple of head_dim / 32 unless the pairs are adjacent; q, k_new and v_new
- * start on a 16-byte boundary and their strides are multiples of 8.  Returns
- * as verify_attn_kv_append. */
+ * are skipped and flagged as well.  head_dim in {64, 128, 256}; q, k_new and
+ * v_new start on a 16-byte boundary and their strides are multiples of 8.
+ * Returns as verify_attn_kv_append. */
 int verify_attn_rope_append(const va_rope *rope, const va_positions *positions, int num_seqs, int T,
                             int head_dim, const va_heads *q, void *q_out, const va_heads *k_new,
                             const va_heads *v_new, va_kv_dtype kv_dtype, void *k_pages,

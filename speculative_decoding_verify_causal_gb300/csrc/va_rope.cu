@@ -11,11 +11,12 @@
 // which binary32 holds to 24 bits; sincospif of the remainder is then within
 // a few ulps, and the quarter turn swaps and negates.
 #include <cuda_fp16.h>
+#include <cuda_fp8.h>
 #include <math.h>
 
 #include <algorithm>
 
-#include "va_kv_row.cuh"
+#include "va_internal.h"
 
 namespace va {
 namespace {
@@ -155,22 +156,12 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     const int P = p.rope.num_pairs;
     const int first = blockIdx.x * p.tile, count = min(p.tile, p.tokens - first);
     const int h0 = blockIdx.y * p.head_chunk, nh = min(p.head_chunk, p.heads - h0);
-    griddep_wait();
-    for (int i = threadIdx.x; i < count * P; i += kThreads) {
-        const int n = (int)div(i, p.by_pairs), pr = i - n * P;
-        const int b = (int)div(first + n, p.by_T), t = first + n - b * (int)p.by_T.d;
-        const int pos = p.pos[p.rope.axis[pr] * p.pos_axis + b * p.pos_seq + t * p.pos_token];
-        float2 cs = turned(p.rope.turn[pr], pos, p.rope.scale);
-        cs.y *= p.inverse_sign;
-        table[i] = cs;
-    }
-    __syncthreads();
     const int total = count * p.head_chunk * p.units;
     const int pair_units = p.pair_units;
-    for (int base = threadIdx.x; base < total; base += kThreads * kUnroll) {
-        V lo[kUnroll], hi[kUnroll];
-        char *to[kUnroll];
-        int at[kUnroll];  // first table entry of the unit; -1: nothing to do, -2: copied
+    V lo[kUnroll], hi[kUnroll];
+    char *to[kUnroll];
+    int at[kUnroll];  // first table entry of the unit; -1: nothing to do, -2: copied
+    auto load = [&](int base) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int i = base + u * kThreads;
@@ -193,6 +184,20 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
             lo[u] = *reinterpret_cast<const V *>(src);
             if (pairs) hi[u] = *reinterpret_cast<const V *>(src + (ADJACENT ? W : P) * kElem);
         }
+    };
+    griddep_wait();
+    load(threadIdx.x);  // under way while the table is made
+    for (int i = threadIdx.x; i < count * P; i += kThreads) {
+        const int n = (int)div(i, p.by_pairs), pr = i - n * P;
+        const int b = (int)div(first + n, p.by_T), t = first + n - b * (int)p.by_T.d;
+        const int pos = p.pos[p.rope.axis[pr] * p.pos_axis + b * p.pos_seq + t * p.pos_token];
+        float2 cs = turned(p.rope.turn[pr], pos, p.rope.scale);
+        cs.y *= p.inverse_sign;
+        table[i] = cs;
+    }
+    __syncthreads();
+    for (int base = threadIdx.x; base < total; base += kThreads * kUnroll) {
+        if (base != threadIdx.x) load(base);
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             if (at[u] == -1) continue;
@@ -261,34 +266,114 @@ struct RopeAppendParams {
 };
 
 constexpr int kRowWarps = kThreads / 32;
+constexpr int kE = 16;  // elements of a lane: two 16-byte vectors of bf16
 
-// One CTA per token (blockIdx.x) and chunk of its Hq + 2 Hkv rows (blockIdx.y,
-// kRowWarps * ROWS of them), one warp per row, ROWS rows per warp with their
-// loads in flight together.  The token's (cos, sin) are computed once per CTA,
-// one pair a thread, and each lane keeps those of its E elements in registers.
-// Lane l holds elements [l E, l E + E): the other half of a pair is P / E
-// lanes away (halves) or the neighbouring element (adjacent).
-template <int D, int DT, int ROWS>
+// Where the two elements of a pair are, as the kernel is built for it.
+enum Pairing : int {
+    kHalves,    // P / 8 lanes hold 8 pairs each: 8 elements of either half (P a multiple of 8)
+    kAdjacent,  // a lane holds 16 neighbours
+    kApart      // halves that begin inside a vector: 16 neighbours a lane, the other element is read again
+};
+
+// Eight codes of the append's rule, element e at bit e * bits of the result.
+template <int DT>
+__device__ __forceinline__ uint64_t codes8(const float *x, float s) {
+    constexpr int kBits = DT == VA_INT4 ? 4 : DT == VA_INT2 ? 2 : 8;
+    constexpr int qm = DT == VA_INT8 ? 127 : DT == VA_INT4 ? 7 : 1, mask = (1 << kBits) - 1;
+    uint64_t codes = 0;
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        const float y0 = __fdiv_rn(x[e], s), y1 = __fdiv_rn(x[e + 1], s);
+        uint32_t two;
+        if constexpr (DT == VA_FP8_E4M3) {
+            two = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(fminf(fmaxf(y0, -448.f), 448.f), fminf(fmaxf(y1, -448.f), 448.f)),
+                                                     __NV_SATFINITE, __NV_E4M3);
+        } else {
+            two = ((uint32_t)max(-qm, min(qm, __float2int_rn(y0))) & mask) |
+                  (((uint32_t)max(-qm, min(qm, __float2int_rn(y1))) & mask) << kBits);
+        }
+        codes |= (uint64_t)two << (e * kBits);
+    }
+    return codes;
+}
+
+// The append's rule (verify_attn_kv_append) on a row that D / 16 lanes hold: absmax over the lanes (exact), the scale and
+// the quotients IEEE binary32 divisions, the codes rounded to nearest even.  x0 and x1 are 8 elements each, from e0 and e1.
+template <int D, int DT>
+__device__ __forceinline__ void store_quantised(const float (&x0)[8], const float (&x1)[8], int e0, int e1, void *pages,
+                                                float *scales, size_t row, bool first, bool write) {
+    float a = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a = fmaxf(a, fmaxf(fabsf(x0[e]), fabsf(x1[e])));
+#pragma unroll
+    for (int o = D / kE / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    if (!write) return;  // a row that is not the cache's, in a warp with one that is
+    constexpr float qmax = DT == VA_FP8_E4M3 ? 448.f : DT == VA_INT8 ? 127.f : DT == VA_INT4 ? 7.f : 1.f;
+    constexpr int kBits = DT == VA_INT4 ? 4 : DT == VA_INT2 ? 2 : 8;
+    const float s = a > 0.f ? __fdiv_rn(a, qmax) : 1.f;
+    unsigned char *dst = static_cast<unsigned char *>(pages) + row * (D * kBits / 8);
+    auto put = [&](int e, uint64_t codes) {
+        unsigned char *to = dst + e * kBits / 8;
+        if constexpr (kBits == 8) *reinterpret_cast<uint2 *>(to) = make_uint2((uint32_t)codes, (uint32_t)(codes >> 32));
+        else if constexpr (kBits == 4) *reinterpret_cast<uint32_t *>(to) = (uint32_t)codes;
+        else *reinterpret_cast<uint16_t *>(to) = (uint16_t)codes;
+    };
+    put(e0, codes8<DT>(x0, s));
+    put(e1, codes8<DT>(x1, s));
+    if (first) scales[row] = s;
+}
+
+__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
+    return ((uint64_t)__float_as_uint(hi) << 32) | __float_as_uint(lo);
+}
+__device__ __forceinline__ float low(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float high(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// One CTA per token (blockIdx.x) and chunk of its Hq + 2 Hkv rows (blockIdx.y).  D / 16 lanes hold a row, so a warp has 512 /
+// D rows at a time, and PASSES of them with their loads in flight together.  The token's (cos, sin) are computed once per
+// CTA, one pair a thread, while the rows are on their way, and each lane keeps those of its 8 pairs in registers.  Both
+// elements of a pair are in the lane, so that a rotation is two multiplications and two fused ones, two pairs an
+// instruction, with no exchange: with pairs spread over lanes (8 elements a lane, the others by shuffles) the kernel issued
+// six times the instructions and was bound by them (8,192 tokens of 32 + 16 heads of 128, bf16: 85 us).
+template <int D, int DT, int PASSES, int PAIRING>
 __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_constant__ RopeAppendParams p) {
-    constexpr int E = D / 32;
-    using In = typename RowVec<E>::In;
+    constexpr int kLanes = D / kE, kRows = 32 / kLanes;  // lanes of a row, rows of a warp
     __shared__ float2 table[VA_ROPE_MAX_PAIRS];
     const int P = p.rope.num_pairs;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % kLanes;
     const int b = blockIdx.x / p.T, t = blockIdx.x - b * p.T;
     const int rows = p.Hq + 2 * p.Hkv;
-    const int row0 = blockIdx.y * (kRowWarps * ROWS) + warp;
+    const int row0 = blockIdx.y * (kRowWarps * kRows * PASSES) + warp * kRows + lane / kLanes;
+    // this lane's elements: 8 from e0, 8 from e1; `turns` of its 8 pairs are turned, the pairs from pair0 on
+    const int pair_lanes = P / 8;
+    const bool tail = PAIRING == kHalves && sub >= pair_lanes;
+    const int e0 = PAIRING != kHalves ? kE * sub : tail ? 2 * P + kE * (sub - pair_lanes) : 8 * sub;
+    const int e1 = PAIRING != kHalves || tail ? e0 + 8 : P + 8 * sub;
+    const int pair0 = 8 * sub, turns = PAIRING == kHalves ? (tail ? 0 : 8) : min(8, max(0, P - pair0));
     griddep_wait();
-    In raw[ROWS];
+    const uint16_t *src[PASSES];
+    uint4 raw0[PASSES], raw1[PASSES];
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-        const int row = row0 + r * kRowWarps;
-        if (row >= rows) continue;
-        const uint16_t *src;
-        if (row < p.Hq) src = p.q + b * p.q_seq + t * p.q_token + row * p.q_head;
-        else if (row < p.Hq + p.Hkv) src = p.k + b * p.k_seq + t * p.k_token + (row - p.Hq) * p.k_head;
-        else src = p.v + b * p.v_seq + t * p.v_token + (row - p.Hq - p.Hkv) * p.v_head;
-        raw[r] = *reinterpret_cast<const In *>(src + lane * E);
+    for (int r = 0; r < PASSES; ++r) {
+        const int row = row0 + r * kRowWarps * kRows;
+        src[r] = row < p.Hq           ? p.q + b * p.q_seq + t * p.q_token + row * p.q_head
+                 : row < p.Hq + p.Hkv ? p.k + b * p.k_seq + t * p.k_token + (row - p.Hq) * p.k_head
+                                      : p.v + b * p.v_seq + t * p.v_token + (row - p.Hq - p.Hkv) * p.v_head;
+        raw0[r] = raw1[r] = make_uint4(0, 0, 0, 0);
+        if (row < rows) {
+            raw0[r] = *reinterpret_cast<const uint4 *>(src[r] + e0);
+            raw1[r] = *reinterpret_cast<const uint4 *>(src[r] + e1);
+        }
     }
     const int place = p.seq_lens[b] - p.T + t;
     if (threadIdx.x < P) {
@@ -301,77 +386,92 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_cons
     if (place >= 0 && block < p.bt_stride) page = p.block_table[(size_t)b * p.bt_stride + block];
     const bool stored = page >= 0 && (p.num_pages == 0 || page < p.num_pages);
     __syncthreads();
-    const bool adjacent = p.rope.adjacent != 0;
-    float c[E], s[E];  // x' = x c + partner s
+    float2 cs[8];
+    if (PAIRING != kApart) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int i = lane * E + e;
-        c[e] = 1.f;
-        s[e] = 0.f;
-        if (i < 2 * P) {
-            const bool second = adjacent ? (e & 1) : i >= P;
-            const float2 cs = table[adjacent ? i / 2 : (second ? i - P : i)];
-            c[e] = cs.x;
-            s[e] = second ? cs.y : -cs.y;
-        }
+        for (int j = 0; j < 8; ++j) cs[j] = j < turns ? table[pair0 + j] : make_float2(1.f, 0.f);
     }
-    const int away = P / E;  // lanes between the halves of a pair
-    const int other = lane < away ? lane + away : lane < 2 * away ? lane - away : lane;
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-        const int row = row0 + r * kRowWarps;
-        if (row >= rows) continue;
+    for (int r = 0; r < PASSES; ++r) {
+        const int row = row0 + r * kRowWarps * kRows;
+        if (row - lane / kLanes >= rows) break;  // none of the warp's rows
         const bool is_v = row >= p.Hq + p.Hkv;
-        const uint16_t *h = reinterpret_cast<const uint16_t *>(&raw[r]);
-        float x[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = __uint_as_float((uint32_t)h[e] << 16);
+        float x0[8], x1[8];
+        unpack<VA_FLOAT_BF16, 8>(raw0[r], x0);
+        unpack<VA_FLOAT_BF16, 8>(raw1[r], x1);
         if (!is_v) {
-            float y[E];
+            if constexpr (PAIRING == kHalves) {
+                if (turns) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float far = __shfl_sync(0xffffffffu, x[e], other);
-                const float partner = adjacent ? x[e ^ 1] : far;
-                y[e] = lane * E + e < 2 * P ? fmaf(x[e], c[e], partner * s[e]) : x[e];
+                    for (int j = 0; j < 8; j += 2) {
+                        const uint64_t a2 = pair2(x0[j], x0[j + 1]), b2 = pair2(x1[j], x1[j + 1]);
+                        const uint64_t c2 = pair2(cs[j].x, cs[j + 1].x), s2 = pair2(cs[j].y, cs[j + 1].y);
+                        const uint64_t na = fma2(a2, c2, mul2(b2, pair2(-cs[j].y, -cs[j + 1].y)));
+                        const uint64_t nb = fma2(b2, c2, mul2(a2, s2));
+                        x0[j] = low(na), x0[j + 1] = high(na);
+                        x1[j] = low(nb), x1[j + 1] = high(nb);
+                    }
+                }
+            } else if constexpr (PAIRING == kAdjacent) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float &u = j < 4 ? x0[2 * (j & 3)] : x1[2 * (j & 3)], &v = j < 4 ? x0[2 * (j & 3) + 1] : x1[2 * (j & 3) + 1];
+                    const float nu = fmaf(u, cs[j].x, -v * cs[j].y), nv = fmaf(v, cs[j].x, u * cs[j].y);
+                    if (j < turns) u = nu, v = nv;
+                }
+            } else {
+#pragma unroll
+                for (int m = 0; m < kE; ++m) {
+                    const int i = e0 + m;
+                    if (i < 2 * P && row < rows) {
+                        const float2 r2 = table[i < P ? i : i - P];
+                        const float far = __uint_as_float((uint32_t)src[r][i < P ? i + P : i - P] << 16);
+                        float &x = m < 8 ? x0[m & 7] : x1[m & 7];
+                        x = fmaf(x, r2.x, i < P ? -far * r2.y : far * r2.y);
+                    }
+                }
             }
-#pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = y[e];
         }
-        In turned_raw;
-        if (row < p.Hq || DT == VA_BF16) {
-            uint32_t *w = reinterpret_cast<uint32_t *>(&turned_raw);
-#pragma unroll
-            for (int e = 0; e < E; e += 2) w[e / 2] = pack_bf16x2(x[e], x[e + 1]);
-        }
+        if (PAIRING == kApart) __syncwarp();  // every lane has read before q is written, where it is q_out itself
         if (row < p.Hq) {
-            *reinterpret_cast<In *>(p.q_out + ((size_t)blockIdx.x * p.Hq + row) * D + lane * E) = turned_raw;
-            continue;
+            uint16_t *dst = p.q_out + ((size_t)blockIdx.x * p.Hq + row) * D;
+            *reinterpret_cast<uint4 *>(dst + e0) = packed<VA_FLOAT_BF16, 8, uint4>(x0);
+            *reinterpret_cast<uint4 *>(dst + e1) = packed<VA_FLOAT_BF16, 8, uint4>(x1);
         }
-        if (!stored) {
-            if (lane == 0 && p.flags) atomicOr(p.flags, kFlagBadPage);
-            continue;
-        }
-        const int g = row - p.Hq - (is_v ? p.Hkv : 0);
-        const size_t dst_row = ((size_t)page * VA_PAGE_SIZE + place % VA_PAGE_SIZE) * p.Hkv + g;
+        const bool cached = row >= p.Hq && row < rows, write = cached && stored;
+        if (cached && !stored && sub == 0 && p.flags) atomicOr(p.flags, kFlagBadPage);
+        const size_t dst_row = write ? ((size_t)page * VA_PAGE_SIZE + place % VA_PAGE_SIZE) * p.Hkv + row - p.Hq - (is_v ? p.Hkv : 0) : 0;
         void *pages = is_v ? p.v_pages : p.k_pages;
         if constexpr (DT == VA_BF16) {  // v's bits unchanged, as in the append
-            *reinterpret_cast<In *>(static_cast<uint16_t *>(pages) + dst_row * D + lane * E) = is_v ? raw[r] : turned_raw;
-        } else {
-            store_quantised_row<D, DT>(x, pages, is_v ? p.v_scale : p.k_scale, dst_row, lane);
+            if (write) {
+                uint16_t *dst = static_cast<uint16_t *>(pages) + dst_row * D;
+                *reinterpret_cast<uint4 *>(dst + e0) = is_v ? raw0[r] : packed<VA_FLOAT_BF16, 8, uint4>(x0);
+                *reinterpret_cast<uint4 *>(dst + e1) = is_v ? raw1[r] : packed<VA_FLOAT_BF16, 8, uint4>(x1);
+            }
+        } else if (__any_sync(0xffffffffu, write)) {
+            store_quantised<D, DT>(x0, x1, e0, e1, pages, is_v ? p.v_scale : p.k_scale, dst_row, sub == 0, write);
         }
     }
 }
 
+template <int D, int DT, int PAIRING>
+cudaError_t launch_append_p(const RopeAppendParams &p, int tokens, cudaStream_t s) {
+    constexpr int kRows = kRowWarps * (32 * kE / D);  // of a CTA at a time
+    const int rows = p.Hq + 2 * p.Hkv;
+    auto chunks = [&](int passes) { return (rows + kRows * passes - 1) / (kRows * passes); };
+    // two passes where that still leaves two CTAs for every SM
+    if constexpr (PAIRING != kApart) {
+        if (rows > kRows && (long long)tokens * chunks(2) >= kMinCtas)
+            return launch_pdl(rope_append_kernel<D, DT, 2, PAIRING>, dim3(tokens, chunks(2)), dim3(kThreads), 0, s, p);
+    }
+    return launch_pdl(rope_append_kernel<D, DT, 1, PAIRING>, dim3(tokens, chunks(1)), dim3(kThreads), 0, s, p);
+}
+
 template <int D, int DT>
 cudaError_t launch_append(const RopeAppendParams &p, int tokens, cudaStream_t s) {
-    const int rows = p.Hq + 2 * p.Hkv;
-    constexpr int kMany = 4;
-    // four rows a warp once that still leaves two CTAs for every SM
-    const int wide = (rows + kRowWarps * kMany - 1) / (kRowWarps * kMany);
-    if ((long long)tokens * wide >= kMinCtas)
-        return launch_pdl(rope_append_kernel<D, DT, kMany>, dim3(tokens, wide), dim3(kThreads), 0, s, p);
-    return launch_pdl(rope_append_kernel<D, DT, 1>, dim3(tokens, (rows + kRowWarps - 1) / kRowWarps), dim3(kThreads), 0,
-                      s, p);
+    if (p.rope.adjacent) return launch_append_p<D, DT, kAdjacent>(p, tokens, s);
+    return p.rope.num_pairs % 8 == 0 ? launch_append_p<D, DT, kHalves>(p, tokens, s)
+                                     : launch_append_p<D, DT, kApart>(p, tokens, s);
 }
 
 template <int D>
@@ -552,7 +652,6 @@ extern "C" int verify_attn_rope_append(const va_rope *rope, const va_positions *
     if (kv_dtype < VA_BF16 || kv_dtype > VA_INT2) return VA_ERR_UNSUPPORTED;
     if (kv_dtype != VA_BF16 && (!k_scale || !v_scale)) return VA_ERR_INVALID_ARGUMENT;
     if (2 * rope->num_pairs > head_dim) return VA_ERR_INVALID_ARGUMENT;
-    if (!rope->adjacent && rope->num_pairs % (head_dim / 32) != 0) return VA_ERR_UNSUPPORTED;
     if (k_new->num_heads < 1 || k_new->num_heads != v_new->num_heads || (q && q->num_heads < 1))
         return VA_ERR_INVALID_ARGUMENT;
     if (positions && (!positions->data || !va::aligned(positions->data, 4))) return VA_ERR_INVALID_ARGUMENT;

@@ -277,8 +277,11 @@ APPEND_CASES = [  # lens, T, Hq, Hkv, D, rotary_dim, pairing
     ([25016], 16, 24, 4, 256, 64, "half"),
     ([100, 16], 16, 6, 2, 128, 128, "half"),
     ([70, 300, 16, 17], 7, 8, 8, 256, 256, "adjacent"),
-    ([40] * 80, 5, 32, 8, 128, 96, "half"),          # four rows a warp
-    ([400, 500, 600], 200, 24, 4, 256, 34, "adjacent"),  # the same, and pairs that end inside a lane
+    ([40] * 80, 5, 32, 8, 128, 96, "half"),              # three passes a warp
+    ([400, 500, 600], 200, 24, 4, 256, 34, "adjacent"),  # four, and pairs that end inside a lane
+    ([400, 500, 600], 200, 5, 2, 256, 22, "half"),       # two, and halves that start inside a lane
+    ([33, 40], 9, 3, 1, 64, 6, "half"),
+    ([500] * 9, 50, 33, 7, 64, 62, "half"),
 ]
 
 
