@@ -50,10 +50,10 @@ __device__ __forceinline__ uint32_t div(uint32_t n, const FastDiv &f) { return (
 
 // ------------------------------------------------------------------------- rotary alone
 
-constexpr int kThreads = 256;
-constexpr int kUnroll = 4;            // units whose loads a thread has in flight
-constexpr int kTableEntries = 2048;   // (cos, sin) pairs in shared memory: 16 KB
-constexpr int kMinCtas = 304;         // two for each of 152 SMs
+constexpr int kThreads = 128;
+constexpr int kUnroll = 2;      // heads whose loads a thread has in flight while it turns as many
+constexpr int kHeads = 16;      // heads of a thread where there is work enough
+constexpr int kMinCtas = 2432;  // sixteen for each of 152 SMs
 
 struct Tensor {
     const char *in;
@@ -68,11 +68,11 @@ struct RopeParams {
     Tensor q, k;
     int q_heads, heads;      // heads of q, of q and k together
     int tokens;              // num_seqs * T
-    int tile, head_chunk;    // tokens and heads per CTA
-    int units;               // vectors-pairs per head: pairs / W, then the unrotated vectors
+    int head_chunk;          // heads per thread
+    int units;               // of a head: pairs / W, then the unrotated vectors
     int pair_units;
     float inverse_sign;      // -1 for the inverse
-    FastDiv by_T, by_pairs, by_units, by_chunk;
+    FastDiv by_T, by_units;
 };
 
 template <int BYTES>
@@ -145,91 +145,84 @@ __device__ __forceinline__ V packed(const float (&x)[W]) {
 }
 
 // A unit is W pairs of one head (two vectors of W elements: one of each half,
-// or 2 W neighbours) or, past the pairs, one vector that is copied.  A CTA
-// turns `tile` tokens x `head_chunk` heads: it first puts the tokens' (cos,
-// sin) into shared memory, once for all the heads, then streams the units.
+// or 2 W neighbours) or, past the pairs, one vector that is copied.  A thread
+// has one unit of one token: it makes the W (cos, sin) once, in registers, and
+// turns that unit of head_chunk heads with them.  No shared memory and no
+// barrier: a first form that made a token's (cos, sin) in shared memory for all
+// its heads issued twice the instructions and waited on the table's bank
+// conflicts (32,768 tokens, 40 heads of 128, bf16: 123.5 us).
 template <int TYPE, int W, bool ADJACENT>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
     using V = typename Raw<W * Elem<TYPE>::kBytes>::V;
     constexpr int kElem = Elem<TYPE>::kBytes;
-    __shared__ float2 table[kTableEntries];
+    const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
+    const uint32_t n = div(i, p.by_units), unit = i - n * p.units;
+    if (n >= (uint32_t)p.tokens) return;
     const int P = p.rope.num_pairs;
-    const int first = blockIdx.x * p.tile, count = min(p.tile, p.tokens - first);
-    const int h0 = blockIdx.y * p.head_chunk, nh = min(p.head_chunk, p.heads - h0);
-    const int total = count * p.head_chunk * p.units;
-    const int pair_units = p.pair_units;
+    const int b = (int)div(n, p.by_T), t = (int)n - b * (int)p.by_T.d;
+    const bool pairs = (int)unit < p.pair_units;
+    const int pair0 = W * (int)unit;
+    const int64_t elem = pairs ? (ADJACENT ? 2 * pair0 : pair0) : 2 * P + W * ((int)unit - p.pair_units);
+    const int64_t off0 = elem * kElem, off1 = off0 + (ADJACENT ? W : P) * kElem;
+    const int h0 = blockIdx.y * p.head_chunk, h1 = min(p.heads, h0 + p.head_chunk);
+    griddep_wait();
+    // heads h0 .. h1 - 1 of q and k, kUnroll at a time
     V lo[kUnroll], hi[kUnroll];
     char *to[kUnroll];
-    int at[kUnroll];  // first table entry of the unit; -1: nothing to do, -2: copied
-    auto load = [&](int base) {
+    auto load = [&](int h) {
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int i = base + u * kThreads;
-            at[u] = -1;
-            if (i >= total) continue;
-            const int row = (int)div(i, p.by_units), unit = i - row * p.units;
-            const int n = (int)div(row, p.by_chunk), hc = row - n * p.head_chunk;
-            if (hc >= nh) continue;
-            const int b = (int)div(first + n, p.by_T), t = first + n - b * (int)p.by_T.d;
-            int h = h0 + hc;
+        for (int u = 0; u < kUnroll; ++u, ++h) {
+            if (h >= h1) continue;
             const bool is_k = h >= p.q_heads;
-            if (is_k) h -= p.q_heads;
             const Tensor &x = is_k ? p.k : p.q;
-            const bool pairs = unit < pair_units;
-            const int elem = ADJACENT ? (pairs ? 2 * W * unit : 2 * P + W * (unit - pair_units))
-                                      : (pairs ? W * unit : 2 * P + W * (unit - pair_units));
-            const char *src = x.in + b * x.in_seq + t * x.in_token + h * x.in_head + (int64_t)elem * kElem;
-            to[u] = x.out + b * x.out_seq + t * x.out_token + h * x.out_head + (int64_t)elem * kElem;
-            at[u] = pairs ? n * P + W * unit : -2;
-            lo[u] = *reinterpret_cast<const V *>(src);
-            if (pairs) hi[u] = *reinterpret_cast<const V *>(src + (ADJACENT ? W : P) * kElem);
+            const int g = is_k ? h - p.q_heads : h;
+            const char *in = x.in + b * x.in_seq + t * x.in_token + g * x.in_head;
+            to[u] = x.out + b * x.out_seq + t * x.out_token + g * x.out_head;
+            lo[u] = *reinterpret_cast<const V *>(in + off0);
+            if (pairs) hi[u] = *reinterpret_cast<const V *>(in + off1);
         }
     };
-    griddep_wait();
-    load(threadIdx.x);  // under way while the table is made
-    for (int i = threadIdx.x; i < count * P; i += kThreads) {
-        const int n = (int)div(i, p.by_pairs), pr = i - n * P;
-        const int b = (int)div(first + n, p.by_T), t = first + n - b * (int)p.by_T.d;
-        const int pos = p.pos[p.rope.axis[pr] * p.pos_axis + b * p.pos_seq + t * p.pos_token];
-        float2 cs = turned(p.rope.turn[pr], pos, p.rope.scale);
-        cs.y *= p.inverse_sign;
-        table[i] = cs;
+    load(h0);  // under way while the angles are computed
+    float2 cs[W];
+    if (pairs) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            const int pos = p.pos[p.rope.axis[pair0 + j] * p.pos_axis + b * p.pos_seq + t * p.pos_token];
+            cs[j] = turned(p.rope.turn[pair0 + j], pos, p.rope.scale);
+            cs[j].y *= p.inverse_sign;
+        }
     }
-    __syncthreads();
-    for (int base = threadIdx.x; base < total; base += kThreads * kUnroll) {
-        if (base != threadIdx.x) load(base);
+    for (int h = h0; h < h1; h += kUnroll) {
+        V x[kUnroll], y[kUnroll];
+        char *out[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            if (at[u] == -1) continue;
-            if (at[u] == -2) {
-                *reinterpret_cast<V *>(to[u]) = lo[u];
-                continue;
-            }
-            float x0[W], x1[W];
-            unpack<TYPE, W>(lo[u], x0);
-            unpack<TYPE, W>(hi[u], x1);
-            const float2 *cs = table + at[u];
-            if constexpr (ADJACENT) {  // x0, x1 as one run of 2 W: pair j is elements 2 j, 2 j + 1
+            x[u] = lo[u];
+            y[u] = hi[u];
+            out[u] = to[u];
+        }
+        load(h + kUnroll);  // under way while these are turned
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            if (h + u >= h1) continue;
+            if (pairs) {
+                float x0[W], x1[W];
+                unpack<TYPE, W>(x[u], x0);
+                unpack<TYPE, W>(y[u], x1);
 #pragma unroll
                 for (int j = 0; j < W; ++j) {
-                    float &a = 2 * j < W ? x0[2 * j < W ? 2 * j : 0] : x1[2 * j < W ? 0 : 2 * j - W];
-                    float &b = 2 * j + 1 < W ? x0[2 * j + 1 < W ? 2 * j + 1 : 0] : x1[2 * j + 1 < W ? 0 : 2 * j + 1 - W];
-                    const float2 r = cs[j];
-                    const float na = fmaf(a, r.x, -b * r.y), nb = fmaf(b, r.x, a * r.y);
-                    a = na;
-                    b = nb;
+                    // adjacent: x0, x1 are one run of 2 W, pair j its elements 2 j and 2 j + 1
+                    float &first = ADJACENT ? (2 * j < W ? x0[2 * j < W ? 2 * j : 0] : x1[2 * j < W ? 0 : 2 * j - W]) : x0[j];
+                    float &second = ADJACENT ? (2 * j + 1 < W ? x0[2 * j + 1 < W ? 2 * j + 1 : 0] : x1[2 * j + 1 < W ? 0 : 2 * j + 1 - W])
+                                             : x1[j];
+                    const float na = fmaf(first, cs[j].x, -second * cs[j].y), nb = fmaf(second, cs[j].x, first * cs[j].y);
+                    first = na;
+                    second = nb;
                 }
-            } else {
-#pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    const float2 r = cs[j];
-                    const float na = fmaf(x0[j], r.x, -x1[j] * r.y), nb = fmaf(x1[j], r.x, x0[j] * r.y);
-                    x0[j] = na;
-                    x1[j] = nb;
-                }
+                x[u] = packed<TYPE, W, V>(x0);
+                *reinterpret_cast<V *>(out[u] + off1) = packed<TYPE, W, V>(x1);
             }
-            *reinterpret_cast<V *>(to[u]) = packed<TYPE, W, V>(x0);
-            *reinterpret_cast<V *>(to[u] + (ADJACENT ? W : P) * kElem) = packed<TYPE, W, V>(x1);
+            *reinterpret_cast<V *>(out[u] + off0) = x[u];
         }
     }
 }
@@ -263,9 +256,11 @@ struct RopeAppendParams {
     const int32_t *seq_lens;
     int *flags;
     int T, Hq, Hkv, bt_stride, num_pages;
+    int tokens, chunk;  // num_seqs * T; rows of a token per thread
 };
 
-constexpr int kRowWarps = kThreads / 32;
+constexpr int kRowsEach = 48;     // rows of a thread where there is work enough
+constexpr int kAppendCtas = 456;  // three CTAs for each of 152 SMs
 constexpr int kE = 16;  // elements of a lane: two 16-byte vectors of bf16
 
 // Where the two elements of a pair are, as the kernel is built for it.
@@ -339,21 +334,21 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     return r;
 }
 
-// One CTA per token (blockIdx.x) and chunk of its Hq + 2 Hkv rows (blockIdx.y).  D / 16 lanes hold a row, so a warp has 512 /
-// D rows at a time, and PASSES of them with their loads in flight together.  The token's (cos, sin) are computed once per
-// CTA, one pair a thread, while the rows are on their way, and each lane keeps those of its 8 pairs in registers.  Both
-// elements of a pair are in the lane, so that a rotation is two multiplications and two fused ones, two pairs an
-// instruction, with no exchange: with pairs spread over lanes (8 elements a lane, the others by shuffles) the kernel issued
-// six times the instructions and was bound by them (8,192 tokens of 32 + 16 heads of 128, bf16: 85 us).
-template <int D, int DT, int PASSES, int PAIRING>
+// D / 16 lanes hold a row of one token, 16 elements each, and turn `chunk` rows of that token (its Hq + 2 Hkv rows: q, k, v)
+// one after the other, kAhead of them with their loads in flight.  Both elements of a pair are in the lane, whose 8 (cos, sin)
+// stay in registers: a rotation is two multiplications and two fused ones, two pairs an instruction, without shared memory,
+// barriers or exchange.  8,192 tokens of 32 + 16 heads of 128, bf16: with pairs spread over lanes (the other element by a
+// shuffle) 85 us, bound by its instructions; with a token's (cos, sin) in shared memory for all its rows 66 us.
+template <int D, int DT, int PAIRING>
 __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_constant__ RopeAppendParams p) {
-    constexpr int kLanes = D / kE, kRows = 32 / kLanes;  // lanes of a row, rows of a warp
-    __shared__ float2 table[VA_ROPE_MAX_PAIRS];
+    constexpr int kLanes = D / kE, kAhead = 2;
     const int P = p.rope.num_pairs;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % kLanes;
-    const int b = blockIdx.x / p.T, t = blockIdx.x - b * p.T;
+    const int lane = threadIdx.x & 31, sub = lane % kLanes;
+    const int n = (blockIdx.x * kThreads + threadIdx.x) / kLanes;
+    const bool here = n < p.tokens;  // whole rows of lanes, so that those past the end only take part in exchanges
+    const int b = here ? n / p.T : 0, t = here ? n - b * p.T : 0;
     const int rows = p.Hq + 2 * p.Hkv;
-    const int row0 = blockIdx.y * (kRowWarps * kRows * PASSES) + warp * kRows + lane / kLanes;
+    const int from = blockIdx.y * p.chunk, to = min(rows, from + p.chunk);
     // this lane's elements: 8 from e0, 8 from e1; `turns` of its 8 pairs are turned, the pairs from pair0 on
     const int pair_lanes = P / 8;
     const bool tail = PAIRING == kHalves && sub >= pair_lanes;
@@ -361,127 +356,135 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_cons
     const int e1 = PAIRING != kHalves || tail ? e0 + 8 : P + 8 * sub;
     const int pair0 = 8 * sub, turns = PAIRING == kHalves ? (tail ? 0 : 8) : min(8, max(0, P - pair0));
     griddep_wait();
-    const uint16_t *src[PASSES];
-    uint4 raw0[PASSES], raw1[PASSES];
-#pragma unroll
-    for (int r = 0; r < PASSES; ++r) {
-        const int row = row0 + r * kRowWarps * kRows;
-        src[r] = row < p.Hq           ? p.q + b * p.q_seq + t * p.q_token + row * p.q_head
-                 : row < p.Hq + p.Hkv ? p.k + b * p.k_seq + t * p.k_token + (row - p.Hq) * p.k_head
-                                      : p.v + b * p.v_seq + t * p.v_token + (row - p.Hq - p.Hkv) * p.v_head;
-        raw0[r] = raw1[r] = make_uint4(0, 0, 0, 0);
-        if (row < rows) {
-            raw0[r] = *reinterpret_cast<const uint4 *>(src[r] + e0);
-            raw1[r] = *reinterpret_cast<const uint4 *>(src[r] + e1);
-        }
-    }
+    auto source = [&](int row) {
+        return row < p.Hq           ? p.q + b * p.q_seq + t * p.q_token + row * p.q_head
+               : row < p.Hq + p.Hkv ? p.k + b * p.k_seq + t * p.k_token + (row - p.Hq) * p.k_head
+                                    : p.v + b * p.v_seq + t * p.v_token + (row - p.Hq - p.Hkv) * p.v_head;
+    };
     const int place = p.seq_lens[b] - p.T + t;
-    if (threadIdx.x < P) {
-        const int axis = p.rope.axis[threadIdx.x];
+    auto angle = [&](int pair) {
+        const int axis = p.rope.axis[pair];
         const int pos = p.pos ? p.pos[axis * p.pos_axis + b * p.pos_seq + t * p.pos_token] : place;
-        table[threadIdx.x] = turned(p.rope.turn[threadIdx.x], pos, p.rope.scale);
-    }
+        return turned(p.rope.turn[pair], pos, p.rope.scale);
+    };
+    uint4 next0[kAhead], next1[kAhead];
+    auto load = [&](int row) {
+#pragma unroll
+        for (int r = 0; r < kAhead; ++r) {
+            next0[r] = next1[r] = make_uint4(0, 0, 0, 0);
+            if (here && row + r < to) {
+                const uint16_t *src = source(row + r);
+                next0[r] = *reinterpret_cast<const uint4 *>(src + e0);
+                next1[r] = *reinterpret_cast<const uint4 *>(src + e1);
+            }
+        }
+    };
+    load(from);  // under way while the angles are computed
     int page = -1;
     const int block = place / VA_PAGE_SIZE;
-    if (place >= 0 && block < p.bt_stride) page = p.block_table[(size_t)b * p.bt_stride + block];
-    const bool stored = page >= 0 && (p.num_pages == 0 || page < p.num_pages);
-    __syncthreads();
+    if (to > p.Hq && place >= 0 && block < p.bt_stride) page = p.block_table[(size_t)b * p.bt_stride + block];
+    const bool stored = here && page >= 0 && (p.num_pages == 0 || page < p.num_pages);
     float2 cs[8];
-    if (PAIRING != kApart) {
+    if (PAIRING != kApart && from < p.Hq + p.Hkv) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) cs[j] = j < turns ? table[pair0 + j] : make_float2(1.f, 0.f);
+        for (int j = 0; j < 8; ++j) cs[j] = j < turns ? angle(pair0 + j) : make_float2(1.f, 0.f);
     }
+    for (int base = from; base < to; base += kAhead) {
+        uint4 raw0[kAhead], raw1[kAhead];
 #pragma unroll
-    for (int r = 0; r < PASSES; ++r) {
-        const int row = row0 + r * kRowWarps * kRows;
-        if (row - lane / kLanes >= rows) break;  // none of the warp's rows
-        const bool is_v = row >= p.Hq + p.Hkv;
-        float x0[8], x1[8];
-        unpack<VA_FLOAT_BF16, 8>(raw0[r], x0);
-        unpack<VA_FLOAT_BF16, 8>(raw1[r], x1);
-        if (!is_v) {
-            if constexpr (PAIRING == kHalves) {
-                if (turns) {
+        for (int r = 0; r < kAhead; ++r) {
+            raw0[r] = next0[r];
+            raw1[r] = next1[r];
+        }
+        load(base + kAhead);  // under way while these are turned
 #pragma unroll
-                    for (int j = 0; j < 8; j += 2) {
-                        const uint64_t a2 = pair2(x0[j], x0[j + 1]), b2 = pair2(x1[j], x1[j + 1]);
-                        const uint64_t c2 = pair2(cs[j].x, cs[j + 1].x), s2 = pair2(cs[j].y, cs[j + 1].y);
-                        const uint64_t na = fma2(a2, c2, mul2(b2, pair2(-cs[j].y, -cs[j + 1].y)));
-                        const uint64_t nb = fma2(b2, c2, mul2(a2, s2));
-                        x0[j] = low(na), x0[j + 1] = high(na);
-                        x1[j] = low(nb), x1[j + 1] = high(nb);
+        for (int r = 0; r < kAhead; ++r) {
+            const int row = base + r;
+            if (row >= to) break;
+            const bool is_v = row >= p.Hq + p.Hkv;
+            float x0[8], x1[8];
+            unpack<VA_FLOAT_BF16, 8>(raw0[r], x0);
+            unpack<VA_FLOAT_BF16, 8>(raw1[r], x1);
+            if (!is_v) {
+                if constexpr (PAIRING == kHalves) {
+                    if (turns) {
+#pragma unroll
+                        for (int j = 0; j < 8; j += 2) {
+                            const uint64_t a2 = pair2(x0[j], x0[j + 1]), b2 = pair2(x1[j], x1[j + 1]);
+                            const uint64_t c2 = pair2(cs[j].x, cs[j + 1].x), s2 = pair2(cs[j].y, cs[j + 1].y);
+                            const uint64_t na = fma2(a2, c2, mul2(b2, pair2(-cs[j].y, -cs[j + 1].y)));
+                            const uint64_t nb = fma2(b2, c2, mul2(a2, s2));
+                            x0[j] = low(na), x0[j + 1] = high(na);
+                            x1[j] = low(nb), x1[j + 1] = high(nb);
+                        }
                     }
-                }
-            } else if constexpr (PAIRING == kAdjacent) {
+                } else if constexpr (PAIRING == kAdjacent) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float &u = j < 4 ? x0[2 * (j & 3)] : x1[2 * (j & 3)], &v = j < 4 ? x0[2 * (j & 3) + 1] : x1[2 * (j & 3) + 1];
-                    const float nu = fmaf(u, cs[j].x, -v * cs[j].y), nv = fmaf(v, cs[j].x, u * cs[j].y);
-                    if (j < turns) u = nu, v = nv;
+                    for (int j = 0; j < 8; ++j) {
+                        float &u = j < 4 ? x0[2 * (j & 3)] : x1[2 * (j & 3)], &v = j < 4 ? x0[2 * (j & 3) + 1] : x1[2 * (j & 3) + 1];
+                        const float nu = fmaf(u, cs[j].x, -v * cs[j].y), nv = fmaf(v, cs[j].x, u * cs[j].y);
+                        if (j < turns) u = nu, v = nv;
+                    }
+                } else {
+                    const uint16_t *src = source(row);
+#pragma unroll
+                    for (int m = 0; m < kE; ++m) {
+                        const int i = e0 + m;
+                        if (i < 2 * P && here) {
+                            const float2 r2 = angle(i < P ? i : i - P);
+                            const float far = __uint_as_float((uint32_t)src[i < P ? i + P : i - P] << 16);
+                            float &x = m < 8 ? x0[m & 7] : x1[m & 7];
+                            x = fmaf(x, r2.x, i < P ? -far * r2.y : far * r2.y);
+                        }
+                    }
+                    __syncwarp();  // every lane has read before q is written, where it is q_out itself
+                }
+            }
+            if (row < p.Hq) {
+                if (here) {
+                    uint16_t *dst = p.q_out + ((size_t)n * p.Hq + row) * D;
+                    *reinterpret_cast<uint4 *>(dst + e0) = packed<VA_FLOAT_BF16, 8, uint4>(x0);
+                    *reinterpret_cast<uint4 *>(dst + e1) = packed<VA_FLOAT_BF16, 8, uint4>(x1);
+                }
+                continue;
+            }
+            if (here && !stored && sub == 0 && p.flags) atomicOr(p.flags, kFlagBadPage);
+            const size_t dst_row = stored ? ((size_t)page * VA_PAGE_SIZE + place % VA_PAGE_SIZE) * p.Hkv + row - p.Hq - (is_v ? p.Hkv : 0) : 0;
+            void *pages = is_v ? p.v_pages : p.k_pages;
+            if constexpr (DT == VA_BF16) {  // v's bits unchanged, as in the append
+                if (stored) {
+                    uint16_t *dst = static_cast<uint16_t *>(pages) + dst_row * D;
+                    *reinterpret_cast<uint4 *>(dst + e0) = is_v ? raw0[r] : packed<VA_FLOAT_BF16, 8, uint4>(x0);
+                    *reinterpret_cast<uint4 *>(dst + e1) = is_v ? raw1[r] : packed<VA_FLOAT_BF16, 8, uint4>(x1);
                 }
             } else {
-#pragma unroll
-                for (int m = 0; m < kE; ++m) {
-                    const int i = e0 + m;
-                    if (i < 2 * P && row < rows) {
-                        const float2 r2 = table[i < P ? i : i - P];
-                        const float far = __uint_as_float((uint32_t)src[r][i < P ? i + P : i - P] << 16);
-                        float &x = m < 8 ? x0[m & 7] : x1[m & 7];
-                        x = fmaf(x, r2.x, i < P ? -far * r2.y : far * r2.y);
-                    }
-                }
+                store_quantised<D, DT>(x0, x1, e0, e1, pages, is_v ? p.v_scale : p.k_scale, dst_row, sub == 0, stored);
             }
         }
-        if (PAIRING == kApart) __syncwarp();  // every lane has read before q is written, where it is q_out itself
-        if (row < p.Hq) {
-            uint16_t *dst = p.q_out + ((size_t)blockIdx.x * p.Hq + row) * D;
-            *reinterpret_cast<uint4 *>(dst + e0) = packed<VA_FLOAT_BF16, 8, uint4>(x0);
-            *reinterpret_cast<uint4 *>(dst + e1) = packed<VA_FLOAT_BF16, 8, uint4>(x1);
-        }
-        const bool cached = row >= p.Hq && row < rows, write = cached && stored;
-        if (cached && !stored && sub == 0 && p.flags) atomicOr(p.flags, kFlagBadPage);
-        const size_t dst_row = write ? ((size_t)page * VA_PAGE_SIZE + place % VA_PAGE_SIZE) * p.Hkv + row - p.Hq - (is_v ? p.Hkv : 0) : 0;
-        void *pages = is_v ? p.v_pages : p.k_pages;
-        if constexpr (DT == VA_BF16) {  // v's bits unchanged, as in the append
-            if (write) {
-                uint16_t *dst = static_cast<uint16_t *>(pages) + dst_row * D;
-                *reinterpret_cast<uint4 *>(dst + e0) = is_v ? raw0[r] : packed<VA_FLOAT_BF16, 8, uint4>(x0);
-                *reinterpret_cast<uint4 *>(dst + e1) = is_v ? raw1[r] : packed<VA_FLOAT_BF16, 8, uint4>(x1);
-            }
-        } else if (__any_sync(0xffffffffu, write)) {
-            store_quantised<D, DT>(x0, x1, e0, e1, pages, is_v ? p.v_scale : p.k_scale, dst_row, sub == 0, write);
-        }
     }
-}
-
-template <int D, int DT, int PAIRING>
-cudaError_t launch_append_p(const RopeAppendParams &p, int tokens, cudaStream_t s) {
-    constexpr int kRows = kRowWarps * (32 * kE / D);  // of a CTA at a time
-    const int rows = p.Hq + 2 * p.Hkv;
-    auto chunks = [&](int passes) { return (rows + kRows * passes - 1) / (kRows * passes); };
-    // two passes where that still leaves two CTAs for every SM
-    if constexpr (PAIRING != kApart) {
-        if (rows > kRows && (long long)tokens * chunks(2) >= kMinCtas)
-            return launch_pdl(rope_append_kernel<D, DT, 2, PAIRING>, dim3(tokens, chunks(2)), dim3(kThreads), 0, s, p);
-    }
-    return launch_pdl(rope_append_kernel<D, DT, 1, PAIRING>, dim3(tokens, chunks(1)), dim3(kThreads), 0, s, p);
 }
 
 template <int D, int DT>
-cudaError_t launch_append(const RopeAppendParams &p, int tokens, cudaStream_t s) {
-    if (p.rope.adjacent) return launch_append_p<D, DT, kAdjacent>(p, tokens, s);
-    return p.rope.num_pairs % 8 == 0 ? launch_append_p<D, DT, kHalves>(p, tokens, s)
-                                     : launch_append_p<D, DT, kApart>(p, tokens, s);
+cudaError_t launch_append(RopeAppendParams p, cudaStream_t s) {
+    // rows of a thread: kRowsEach, fewer while the grid is below kAppendCtas
+    const int rows = p.Hq + 2 * p.Hkv;
+    const unsigned ctas = (unsigned)(((long long)p.tokens * (D / kE) + kThreads - 1) / kThreads);
+    const int chunks = std::min(rows, std::max((rows + kRowsEach - 1) / kRowsEach, (int)((kAppendCtas + ctas - 1) / ctas)));
+    p.chunk = (rows + chunks - 1) / chunks;
+    const dim3 grid(ctas, (rows + p.chunk - 1) / p.chunk), block(kThreads);
+    if (p.rope.adjacent) return launch_pdl(rope_append_kernel<D, DT, kAdjacent>, grid, block, 0, s, p);
+    return p.rope.num_pairs % 8 == 0 ? launch_pdl(rope_append_kernel<D, DT, kHalves>, grid, block, 0, s, p)
+                                     : launch_pdl(rope_append_kernel<D, DT, kApart>, grid, block, 0, s, p);
 }
 
 template <int D>
-cudaError_t launch_append_d(const RopeAppendParams &p, int dtype, int tokens, cudaStream_t s) {
+cudaError_t launch_append_d(const RopeAppendParams &p, int dtype, cudaStream_t s) {
     switch (dtype) {
-    case VA_BF16: return launch_append<D, VA_BF16>(p, tokens, s);
-    case VA_FP8_E4M3: return launch_append<D, VA_FP8_E4M3>(p, tokens, s);
-    case VA_INT8: return launch_append<D, VA_INT8>(p, tokens, s);
-    case VA_INT4: return launch_append<D, VA_INT4>(p, tokens, s);
-    default: return launch_append<D, VA_INT2>(p, tokens, s);
+    case VA_BF16: return launch_append<D, VA_BF16>(p, s);
+    case VA_FP8_E4M3: return launch_append<D, VA_FP8_E4M3>(p, s);
+    case VA_INT8: return launch_append<D, VA_INT8>(p, s);
+    case VA_INT4: return launch_append<D, VA_INT4>(p, s);
+    default: return launch_append<D, VA_INT2>(p, s);
     }
 }
 
@@ -611,23 +614,15 @@ extern "C" int verify_attn_rope(const va_rope *rope, const va_positions *positio
     p.pair_units = P / w;
     p.units = p.pair_units + (head_dim - 2 * P) / w;
     p.inverse_sign = inverse ? -1.f : 1.f;
-    // A CTA takes about four units a thread (the loads it has in flight): several tokens, or some of
-    // one token's heads; fewer while the grid is below two CTAs an SM, down to one unit a thread.
-    const int per_cta = va::kThreads * va::kUnroll;
-    const int limit = std::min<long long>(va::kTableEntries / P, tokens);
-    p.tile = std::max(1, std::min(limit, per_cta / (p.units * heads)));
-    p.head_chunk = std::max(1, std::min(heads, per_cta / p.units));
-    auto ctas = [&] {
-        return ((tokens + p.tile - 1) / p.tile) * ((heads + p.head_chunk - 1) / p.head_chunk);
-    };
-    while (ctas() < va::kMinCtas && p.tile > 1) p.tile = (p.tile + 1) / 2;
-    while (ctas() < va::kMinCtas && p.head_chunk > 1 && p.head_chunk * p.units >= 2 * va::kThreads)
-        p.head_chunk = (p.head_chunk + 1) / 2;
+    if (tokens * p.units >= (1LL << 31)) return VA_ERR_INVALID_ARGUMENT;
+    // heads of a thread: kHeads, fewer while the grid is below kMinCtas
+    const unsigned ctas = (unsigned)((tokens * p.units + va::kThreads - 1) / va::kThreads);
+    const int chunks = std::min<long long>(heads, std::max<long long>((heads + va::kHeads - 1) / va::kHeads,
+                                                                      (va::kMinCtas + ctas - 1) / ctas));
+    p.head_chunk = (heads + chunks - 1) / chunks;
     p.by_T = va::fast_div((uint32_t)T);
-    p.by_pairs = va::fast_div((uint32_t)P);
     p.by_units = va::fast_div((uint32_t)p.units);
-    p.by_chunk = va::fast_div((uint32_t)p.head_chunk);
-    const dim3 grid((unsigned)((tokens + p.tile - 1) / p.tile), (unsigned)((heads + p.head_chunk - 1) / p.head_chunk));
+    const dim3 grid(ctas, (unsigned)((heads + p.head_chunk - 1) / p.head_chunk));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = type == VA_FLOAT_BF16   ? va::launch_rope<VA_FLOAT_BF16>(p, w, grid, s)
                           : type == VA_FLOAT_FP16 ? va::launch_rope<VA_FLOAT_FP16>(p, w, grid, s)
@@ -663,7 +658,7 @@ extern "C" int verify_attn_rope_append(const va_rope *rope, const va_positions *
         !va::aligned(v_scale, 4) || !va::aligned(flags, 4))
         return VA_ERR_INVALID_ARGUMENT;
     const long long tokens = (long long)num_seqs * T;
-    if (tokens > (1LL << 30) || (q && q->num_heads > 65535) || k_new->num_heads > 65535) return VA_ERR_INVALID_ARGUMENT;
+    if (tokens > (1LL << 26) || (q && q->num_heads > 65535) || k_new->num_heads > 65535) return VA_ERR_INVALID_ARGUMENT;
     va::RopeAppendParams p{};
     p.rope = *rope;
     if (positions) {
@@ -696,15 +691,16 @@ extern "C" int verify_attn_rope_append(const va_rope *rope, const va_positions *
     p.seq_lens = seq_lens;
     p.flags = flags;
     p.T = T;
+    p.tokens = (int)tokens;
     p.Hkv = k_new->num_heads;
     p.bt_stride = block_table_stride;
     p.num_pages = num_pages;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     switch (head_dim) {
-    case 64: e = va::launch_append_d<64>(p, kv_dtype, (int)tokens, s); break;
-    case 128: e = va::launch_append_d<128>(p, kv_dtype, (int)tokens, s); break;
-    default: e = va::launch_append_d<256>(p, kv_dtype, (int)tokens, s); break;
+    case 64: e = va::launch_append_d<64>(p, kv_dtype, s); break;
+    case 128: e = va::launch_append_d<128>(p, kv_dtype, s); break;
+    default: e = va::launch_append_d<256>(p, kv_dtype, s); break;
     }
     if (e != cudaSuccess) {
         va::note_cuda_error(e);
