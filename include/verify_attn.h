@@ -578,11 +578,12 @@ int verify_attn_accept_probs(const va_rows *target_probs, const va_rows *draft_p
  * the pages and num_free = num_pages.  Calls on one pool, and those that read
  * its block table, must be ordered on one stream.  Results do not depend on
  * timing: whole numbers, counted and ordered by page and sequence.
- * Limits: num_seqs and num_forks <= VA_PAGES_MAX_SEQS, num_pages <= 2^24,
- * num_seqs * block_table_stride < 2^31.  Every call returns VA_OK when enqueued,
+ * Limits: num_seqs and num_forks <= VA_PAGES_MAX_SEQS, num_pages <=
+ * VA_PAGES_MAX_PAGES, num_seqs * block_table_stride < 2^31.  Every call returns VA_OK when enqueued,
  * VA_ERR_INVALID_ARGUMENT for null or misaligned pointers and sizes out of
  * range, VA_ERR_CUDA if a launch fails. */
 #define VA_PAGES_MAX_SEQS 8192
+#define VA_PAGES_MAX_PAGES (1 << 22)
 #define VA_PAGES_BAD_ENTRY 1
 #define VA_PAGES_EXHAUSTED 8
 #define VA_PAGES_BAD_REQUEST 16

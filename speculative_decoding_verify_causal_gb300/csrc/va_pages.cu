@@ -8,16 +8,18 @@
 //
 // The bookkeeping is integer work whose results do not depend on timing.
 // Counts go down and up by atomics (order-free).  The pages that a call frees
-// are first marked in a bitmap, whose scan then pushes them in ascending
-// order; requests are placed by prefix sums over the sequences, which every
-// CTA computes for itself in shared memory, so that only the bitmap, the counts
-// and the lists are shared (through L2, cluster barriers between the phases).
-// Work is spread over table entries, not sequences: entry i belongs to the
-// sequence whose prefix sum it falls into (a binary search in shared memory),
-// so one long sequence is shared by all threads.  Bound: a chain of dependent
-// L2 round trips and barriers, not bytes.
+// are first marked in a bitmap, which lies in the CTAs' shared memory, a slice
+// each, and is marked there by all of them; its scan then pushes the pages in
+// ascending order.  Requests are placed by prefix sums over the sequences,
+// which every CTA computes for itself, so that only the bitmap, the counts and
+// the lists are shared, with cluster barriers between the phases.  Work is
+// spread over table entries, not sequences: entry i belongs to the sequence
+// whose prefix sum it falls into (a binary search in shared memory), so one
+// long sequence is shared by all threads, each with kBatch entries' loads in
+// flight.  Bound: a chain of dependent L2 round trips and barriers, not bytes.
 //
-// The copy kernel is HBM-bound: every byte of a page is read and written once.
+// The copy kernel is HBM-bound: every byte of a page is read and written once
+// (0.95 GB of traffic in 144 us, 6.6 TB/s).
 #include <algorithm>
 
 #include "va_internal.h"
@@ -31,6 +33,7 @@ using namespace sm100;
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;  // portable cluster size
+constexpr int kBatch = 4;
 
 struct Header {
     int jobs;    // pages to copy
@@ -41,10 +44,9 @@ struct Header {
 struct Pool {
     int32_t *table, *lens, *ref, *free_list, *num_free, *flags;
     int stride, B, P;
+    int slice_bits;  // of the bitmap's 32-bit words: each CTA has 2^slice_bits of them
     // workspace
     Header *head;
-    uint32_t *mask;   // two bitmaps over the pages
-    int32_t *claim;   // [B]
     int32_t *map;     // [P]
     int32_t *movers;  // [P]
     int2 *jobs;       // [P] (source, destination)
@@ -108,38 +110,64 @@ __device__ __forceinline__ int find(const int *pre, int n, int i) {
     return lo;
 }
 
-// Exclusive sum over the cluster's CTAs of one number each; `total` gets the sum of all.
-__device__ int cluster_scan(int v, int &total) {
-    __shared__ unsigned long long slot;
-    if (threadIdx.x == 0) slot = (unsigned long long)(unsigned)v;
+// load(i), then use(i, what it gave), for the items i = me, me + all, .. below `total`: kBatch loads in flight.
+template <typename Load, typename Use>
+__device__ __forceinline__ void for_items(int me, int all, int total, Load load, Use use) {
+    for (int base = me; base < total; base += kBatch * all) {
+        decltype(load(0)) v[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+            if (base + u * all < total) v[u] = load(base + u * all);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+            if (base + u * all < total) use(base + u * all, v[u]);
+    }
+}
+
+// Exclusive sum over the cluster's CTAs of one number each (v of thread 0 .. ctas - 1 of each CTA); `total` gets the sum of
+// all.  One cluster barrier; `slots` of this CTA is written by the others and serves one call.
+__device__ int cluster_scan(int v, int &total, unsigned long long *slots) {
+    const int rank = (int)cluster_rank(), ctas = (int)cluster_size();
+    if ((int)threadIdx.x < ctas) st_cluster_u64(slots + rank, threadIdx.x, (unsigned long long)(unsigned)v);
     cluster_sync();
     int before = 0;
     total = 0;
-    for (int r = 0; r < (int)cluster_size(); ++r) {
-        const int x = (int)ld_cluster_u64(&slot, r);
-        if (r < (int)cluster_rank()) before += x;
+    for (int r = 0; r < ctas; ++r) {
+        const int x = (int)slots[r];
+        if (r < rank) before += x;
         total += x;
     }
-    cluster_sync();
     return before;
 }
 
-// Push the pages marked in `mask` onto the free list, in ascending order, above its first nf entries.  Returns the new
-// count.  The marks must be visible (a cluster barrier before); the entries are visible after the next one.
-__device__ int push_marked(const Pool &p, const uint32_t *mask, int nf) {
-    const int W = mask_words(p.P), n = (int)cluster_size();
-    const int per = (W + n - 1) / n, lo = min(W, (int)cluster_rank() * per), hi = min(W, lo + per);
+// Mark a page in the bitmap, in the shared memory of the CTA that has its word.
+__device__ __forceinline__ void mark(const Pool &p, uint32_t *mask, int page) {
+    const int w = page >> 5;
+    asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(
+                     cluster_map(mask + (w & ((1 << p.slice_bits) - 1)), w >> p.slice_bits)),
+                 "r"(1u << (page & 31))
+                 : "memory");
+}
+
+// Push the marked pages onto the free list, in ascending order, above its first nf entries, and clear the marks.  Returns
+// the new count.  The marks must be complete (a cluster barrier before); the entries are visible after the next one.
+__device__ int push_marked(const Pool &p, uint32_t *mask, int nf, unsigned long long *slots) {
+    const int first = (int)cluster_rank() << p.slice_bits, words = max(0, min(1 << p.slice_bits, mask_words(p.P) - first));
     int mine = 0;
-    for (int w = lo + threadIdx.x; w < hi; w += kThreads) mine += __popc(__ldcg(mask + w));
+    for (int w = threadIdx.x; w < words; w += kThreads) mine += __popc(mask[w]);
     int sum, total;
     block_scan(mine, sum);
-    int at = nf + cluster_scan(sum, total);
-    for (int base = lo; base < hi && sum > 0; base += kThreads) {
+    int at = nf + cluster_scan(sum, total, slots);
+    for (int base = 0; base < words && sum > 0; base += kThreads) {
         const int w = base + threadIdx.x;
-        uint32_t bits = w < hi ? __ldcg(mask + w) : 0;
+        uint32_t bits = 0;
+        if (w < words) {
+            bits = mask[w];
+            mask[w] = 0;
+        }
         int chunk, to = at + block_scan(__popc(bits), chunk);
         while (bits) {
-            if (to < p.P) p.free_list[to] = 32 * w + __ffs(bits) - 1;
+            if (to < p.P) p.free_list[to] = 32 * (first + w) + __ffs(bits) - 1;
             ++to;
             bits &= bits - 1;
         }
@@ -149,15 +177,17 @@ __device__ int push_marked(const Pool &p, const uint32_t *mask, int nf) {
     return min(p.P, nf + total);
 }
 
-__device__ __forceinline__ void drop_reference(const Pool &p, int page, uint32_t *mask) {
-    const int old = atomicSub(p.ref + page, 1);
+__device__ __forceinline__ int take_reference(const Pool &p, int page) { return atomicSub(p.ref + page, 1); }
+__device__ __forceinline__ void dropped(const Pool &p, uint32_t *mask, int page, int old) {
     if (old == 1) {
-        atomicOr(mask + (page >> 5), 1u << (page & 31));
+        mark(p, mask, page);
     } else if (old <= 0) {
         atomicAdd(p.ref + page, 1);
         flag(p, VA_PAGES_BAD_COUNT);
     }
 }
+
+__device__ __forceinline__ bool in_pool(const Pool &p, int page) { return page >= 0 && page < p.P; }
 
 __device__ __forceinline__ int free_count(const Pool &p) {
     const int nf = __ldcg(p.num_free);
@@ -167,97 +197,112 @@ __device__ __forceinline__ int free_count(const Pool &p) {
 
 __global__ void __launch_bounds__(kThreads) resize_kernel(const Pool p, const int32_t *new_lens) {
     extern __shared__ int smem[];
-    int *pre = smem, *len = smem + p.B + 1;
-    unsigned char *own_copy = reinterpret_cast<unsigned char *>(len + p.B);
+    int *pre = smem, *len = pre + p.B + 1, *want = len + p.B, *tail = want + p.B;
+    uint32_t *mask = reinterpret_cast<uint32_t *>(tail + p.B);
+    __shared__ unsigned long long slots[2][kMaxCluster];
     __shared__ int s_taken, s_copies;
     const int me = cluster_thread(), all = cluster_threads();
     const bool first = cluster_rank() == 0;
-    uint32_t *mask2 = p.mask + mask_words(p.P);
     const int64_t most = (int64_t)p.stride * VA_PAGE_SIZE;
+    for (int w = threadIdx.x; w < (1 << p.slice_bits); w += kThreads) mask[w] = 0;
+    if (threadIdx.x == 0) s_taken = s_copies = 0;
+    cluster_arrive();  // the bitmap is clear, and this CTA runs
     griddep_wait();
-    for (int w = me; w < 2 * mask_words(p.P); w += all) __stcg(p.mask + w, 0u);
     if (me == 0) p.head->jobs = 0;
+    int nf = free_count(p);
     for (int b = threadIdx.x; b < p.B; b += kThreads) {
         const int L = p.lens[b], N = new_lens[b];
         const bool ok = L >= 0 && L <= most && N <= most;
         if (!ok && first) flag(p, VA_PAGES_BAD_REQUEST);
         len[b] = ok && N >= 0 ? L : -1;  // -1: left alone
+        want[b] = N;
         pre[b] = ok && N >= 0 && N < L ? blocks_of(L) - blocks_of(N) : 0;
-    }
-    if (threadIdx.x == 0) s_taken = s_copies = 0;
-    prefix_sums(pre, p.B);
-    cluster_sync();  // the bitmaps are clear
-    // 1. shrinking sequences drop their last pages
-    for (int i = me; i < pre[p.B]; i += all) {
-        const int b = find(pre, p.B, i);
-        int32_t *entry = p.table + (size_t)b * p.stride + blocks_of(new_lens[b]) + (i - pre[b]);
-        const int page = *entry;
-        *entry = -1;
-        if (page < 0 || page >= p.P) flag(p, VA_PAGES_BAD_ENTRY);
-        else drop_reference(p, page, p.mask);
-    }
-    cluster_sync();
-    int nf = push_marked(p, p.mask, free_count(p));
-    // 2. what each growing sequence needs, and who can be served
-    for (int b = threadIdx.x; b < p.B; b += kThreads) {
-        const int L = len[b], N = new_lens[b];
-        int need = 0;
-        own_copy[b] = 0;
-        if (L >= 0 && N > L) {
-            need = blocks_of(N) - blocks_of(L);
-            if (L % VA_PAGE_SIZE) {
-                const int page = p.table[(size_t)b * p.stride + L / VA_PAGE_SIZE];
-                if (page < 0 || page >= p.P) {
-                    if (first) flag(p, VA_PAGES_BAD_ENTRY);
-                } else if (__ldcg(p.ref + page) > 1) {
-                    own_copy[b] = 1;
-                    ++need;
-                }
-            }
+        // the partly filled last page of a sequence that grows
+        tail[b] = ok && N > L && L % VA_PAGE_SIZE ? p.table[(size_t)b * p.stride + L / VA_PAGE_SIZE] : -1;
+        if (ok && N > L && L % VA_PAGE_SIZE && !in_pool(p, tail[b])) {
+            if (first) flag(p, VA_PAGES_BAD_ENTRY);
+            tail[b] = -1;
         }
-        pre[b] = need;
+    }
+    prefix_sums(pre, p.B);
+    cluster_wait();
+    // 1. shrinking sequences drop their last pages
+    const int drops = pre[p.B];
+    if (drops) {
+        struct Entry {
+            int32_t *at;
+            int page;
+        };
+        for (int base = me; base < drops; base += kBatch * all) {
+            Entry v[kBatch];
+            int old[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int i = base + u * all;
+                v[u].page = -1;
+                if (i >= drops) continue;
+                const int b = find(pre, p.B, i);
+                v[u].at = p.table + (size_t)b * p.stride + blocks_of(want[b]) + (i - pre[b]);
+                v[u].page = *v[u].at;
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                if (base + u * all >= drops) continue;
+                *v[u].at = -1;
+                if (in_pool(p, v[u].page)) old[u] = take_reference(p, v[u].page);
+                else flag(p, VA_PAGES_BAD_ENTRY);
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                if (base + u * all < drops && in_pool(p, v[u].page)) dropped(p, mask, v[u].page, old[u]);
+        }
+        cluster_sync();
+        nf = push_marked(p, mask, nf, slots[0]);
+    }
+    // 2. what each growing sequence needs, and who can be served
+    __syncthreads();  // pre is read no more
+    for (int b = threadIdx.x; b < p.B; b += kThreads) {
+        const int L = len[b], N = want[b];
+        if (tail[b] >= 0 && __ldcg(p.ref + tail[b]) <= 1) tail[b] = -1;  // its own already
+        pre[b] = L >= 0 && N > L ? blocks_of(N) - blocks_of(L) + (tail[b] >= 0) : 0;
     }
     prefix_sums(pre, p.B);
     for (int b = threadIdx.x; b < p.B; b += kThreads) {
-        const int need = pre[b + 1] - pre[b];
-        if (need == 0) continue;
+        if (pre[b + 1] == pre[b]) continue;
         if (pre[b + 1] <= nf) {
             atomicMax(&s_taken, pre[b + 1]);
-            if (own_copy[b]) s_copies = 1;
+            if (tail[b] >= 0) s_copies = 1;
         } else if (first) {
             flag(p, VA_PAGES_EXHAUSTED);
         }
     }
     cluster_sync();  // everybody has decided; the pushed entries are visible
-    const int taken = s_taken;
-    for (int i = me; i < taken; i += all) {
+    const int taken = s_taken, copies = s_copies;
+    for_items(me, all, taken, [&](int i) { return __ldcg(p.free_list + nf - 1 - i); }, [&](int i, int page) {
         const int b = find(pre, p.B, i), k = i - pre[b], L = len[b];
-        const bool copy = own_copy[b] && k == 0;
-        const int j = copy ? L / VA_PAGE_SIZE : blocks_of(L) + k - own_copy[b];
-        int32_t *entry = p.table + (size_t)b * p.stride + j;
-        int page = __ldcg(p.free_list + nf - 1 - i);
-        if (page < 0 || page >= p.P) {
+        const int own = tail[b] >= 0;
+        const bool copy = own && k == 0;
+        if (in_pool(p, page)) {
+            p.ref[page] = 1;
+        } else {
             flag(p, VA_PAGES_BAD_ENTRY);
             page = -1;
-        } else {
-            p.ref[page] = 1;
         }
         if (copy) {
-            const int old = *entry;
-            p.jobs[atomicAdd(&p.head->jobs, 1)] = make_int2(page < 0 ? -1 : old, page);
-            drop_reference(p, old, mask2);
+            p.jobs[atomicAdd(&p.head->jobs, 1)] = make_int2(page < 0 ? -1 : tail[b], page);
+            dropped(p, mask, tail[b], take_reference(p, tail[b]));
         }
-        *entry = page;
-    }
+        p.table[(size_t)b * p.stride + (copy ? L / VA_PAGE_SIZE : blocks_of(L) + k - own)] = page;
+    });
     if (first) {
         for (int b = threadIdx.x; b < p.B; b += kThreads)
-            if (len[b] >= 0 && (pre[b + 1] == pre[b] || pre[b + 1] <= nf)) p.lens[b] = new_lens[b];
+            if (len[b] >= 0 && (pre[b + 1] == pre[b] || pre[b + 1] <= nf)) p.lens[b] = want[b];
     }
     // 3. shared pages that all their holders replaced
     nf -= taken;
-    if (s_copies) {
+    if (copies) {
         cluster_sync();
-        nf = push_marked(p, mask2, nf);
+        nf = push_marked(p, mask, nf, slots[1]);
     }
     if (me == 0) *p.num_free = nf;
 }
@@ -265,28 +310,30 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const Pool p, const in
 __global__ void __launch_bounds__(kThreads) fork_kernel(const Pool p, const int32_t *parents, const int32_t *children,
                                                         const int32_t *lens, int F, int share) {
     extern __shared__ int smem[];
-    int *held = smem, *need = held + F + 1, *len = need + F + 1;
+    int *held = smem, *need = held + F + 1, *len = need + F + 1, *parent = len + F, *child = parent + F, *claim = child + F;
     __shared__ int s_taken;
     const int me = cluster_thread(), all = cluster_threads();
     const bool first = cluster_rank() == 0;
     const int64_t most = (int64_t)p.stride * VA_PAGE_SIZE;
-    griddep_wait();
-    for (int b = me; b < p.B; b += all) __stcg(p.claim + b, F);
-    cluster_sync();
-    for (int f = me; f < F; f += all) {
-        const int c = children[f];
-        if (c >= 0 && c < p.B) atomicMin(p.claim + c, f);
-    }
+    for (int b = threadIdx.x; b < p.B; b += kThreads) claim[b] = F;
     if (threadIdx.x == 0) s_taken = 0;
-    cluster_sync();
+    __syncthreads();
+    griddep_wait();
     const int nf = free_count(p);
+    // the first fork of the call that wants a slot has it
     for (int f = threadIdx.x; f < F; f += kThreads) {
-        const int from = parents[f], to = children[f];
+        parent[f] = parents[f];
+        child[f] = children[f];
+        if (child[f] >= 0 && child[f] < p.B) atomicMin(claim + child[f], f);
+    }
+    __syncthreads();
+    for (int f = threadIdx.x; f < F; f += kThreads) {
+        const int from = parent[f], to = child[f];
         int n = -1;
-        if (from >= 0 && from < p.B && to >= 0 && to < p.B && p.lens[to] == 0 && __ldcg(p.claim + to) == f) {
-            const int L = p.lens[from];
+        if (from >= 0 && from < p.B && to >= 0 && to < p.B && claim[to] == f) {
+            const int L = p.lens[from], there = p.lens[to];
             n = lens ? lens[f] : L;
-            if (L < 0 || L > most || n < 0 || n > L) n = -1;
+            if (there != 0 || L < 0 || L > most || n < 0 || n > L) n = -1;
         }
         if (n < 0 && first) flag(p, VA_PAGES_BAD_REQUEST);
         len[f] = n;
@@ -300,34 +347,43 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const Pool p, const int3
         if (need[f + 1] <= nf) atomicMax(&s_taken, need[f + 1]);
         else if (first) flag(p, VA_PAGES_EXHAUSTED);
     }
-    cluster_sync();  // everybody has decided
-    for (int i = me; i < held[F]; i += all) {
-        const int f = find(held, F, i), j = i - held[f];
-        if (need[f + 1] > need[f] && need[f + 1] > nf) continue;  // refused
-        int page = p.table[(size_t)parents[f] * p.stride + j];
-        const bool bad = page < 0 || page >= p.P;
-        if (bad) flag(p, VA_PAGES_BAD_ENTRY);
-        const int fresh = share ? len[f] / VA_PAGE_SIZE : 0;  // the first block that is copied
-        if (j < fresh) {
-            if (bad) page = -1;
-            else atomicAdd(p.ref + page, 1);
-        } else {
-            const int k = need[f] + j - fresh;
-            int to = p.free_list[nf - 1 - k];
-            if (to < 0 || to >= p.P) {
-                flag(p, VA_PAGES_BAD_ENTRY);
-                to = -1;
+    cluster_arrive();  // this CTA has read the lengths and the free count
+    struct Entry {
+        int f, j, page, to;
+    };
+    for_items(
+        me, all, held[F],
+        [&](int i) {
+            Entry e;
+            e.f = find(held, F, i);
+            e.j = i - held[e.f];
+            e.page = p.table[(size_t)parent[e.f] * p.stride + e.j];
+            const int fresh = share ? len[e.f] / VA_PAGE_SIZE : 0, k = need[e.f] + e.j - fresh;
+            e.to = e.j >= fresh && need[e.f + 1] <= nf ? p.free_list[nf - 1 - k] : -1;
+            return e;
+        },
+        [&](int, const Entry &e) {
+            if (need[e.f + 1] > need[e.f] && need[e.f + 1] > nf) return;  // refused
+            const bool bad = !in_pool(p, e.page);
+            if (bad) flag(p, VA_PAGES_BAD_ENTRY);
+            const int fresh = share ? len[e.f] / VA_PAGE_SIZE : 0;  // the first block that is copied
+            int page = bad ? -1 : e.page;
+            if (e.j < fresh) {
+                if (!bad) atomicAdd(p.ref + page, 1);
             } else {
-                p.ref[to] = 1;
+                const bool good = in_pool(p, e.to);
+                if (good) p.ref[e.to] = 1;
+                else flag(p, VA_PAGES_BAD_ENTRY);
+                p.jobs[need[e.f] + e.j - fresh] = make_int2(good ? page : -1, good ? e.to : -1);
+                page = good ? e.to : -1;
             }
-            p.jobs[k] = make_int2(bad || to < 0 ? -1 : page, to);
-            page = to;
-        }
-        p.table[(size_t)children[f] * p.stride + j] = page;
-    }
+            p.table[(size_t)child[e.f] * p.stride + e.j] = page;
+        });
+    __syncthreads();
+    cluster_wait();
     if (first) {
         for (int f = threadIdx.x; f < F; f += kThreads)
-            if (len[f] >= 0 && (need[f + 1] == need[f] || need[f + 1] <= nf)) p.lens[children[f]] = len[f];
+            if (len[f] >= 0 && (need[f + 1] == need[f] || need[f + 1] <= nf)) p.lens[child[f]] = len[f];
         if (threadIdx.x == 0) {
             *p.num_free = nf - s_taken;
             p.head->jobs = s_taken;
@@ -337,39 +393,58 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const Pool p, const int3
 
 __global__ void __launch_bounds__(kThreads) compact_kernel(const Pool p) {
     extern __shared__ int smem[];
+    int *pre = smem;
+    uint32_t *mask = reinterpret_cast<uint32_t *>(pre + p.B + 1);
     __shared__ int word_pre[kThreads];
+    __shared__ unsigned long long slots[kMaxCluster];
     const int me = cluster_thread(), all = cluster_threads();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool first = cluster_rank() == 0;
     const int64_t most = (int64_t)p.stride * VA_PAGE_SIZE;
+    cluster_arrive();  // this CTA runs
     griddep_wait();
     if (me == 0) p.head->movers = 0;
     // which pages are held, 32 to a word, and how many before each CTA's words
-    const int W = mask_words(p.P), ncta = (int)cluster_size();
-    const int per = (W + ncta - 1) / ncta, lo = min(W, (int)cluster_rank() * per), hi = min(W, lo + per);
+    const int word0 = (int)cluster_rank() << p.slice_bits, words = max(0, min(1 << p.slice_bits, mask_words(p.P) - word0));
     int mine = 0;
-    for (int w = lo + warp; w < hi; w += kWarps) {
-        const int page = 32 * w + lane;
-        const uint32_t live = __ballot_sync(0xffffffffu, page < p.P && p.ref[page] > 0);
-        if (lane == 0) {
-            p.mask[w] = live;
-            mine += __popc(live);
+    for (int base = warp; base < words; base += kWarps * kBatch) {
+        int held[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int page = 32 * (word0 + base + u * kWarps) + lane;
+            held[u] = base + u * kWarps < words && page < p.P ? p.ref[page] : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const uint32_t live = __ballot_sync(0xffffffffu, held[u] > 0);
+            if (lane == 0 && base + u * kWarps < words) {
+                mask[base + u * kWarps] = live;
+                mine += __popc(live);
+            }
         }
     }
+    for (int b = threadIdx.x; b < p.B; b += kThreads) {
+        const int L = p.lens[b];
+        const bool ok = L >= 0 && L <= most;
+        if (!ok && first) flag(p, VA_PAGES_BAD_REQUEST);
+        pre[b] = ok ? blocks_of(L) : 0;
+    }
+    prefix_sums(pre, p.B);
     int sum, n;
     block_scan(mine, sum);
-    int before = cluster_scan(sum, n);  // n pages are held
+    cluster_wait();
+    int before = cluster_scan(sum, n, slots);  // n pages are held
     // free places below n, held pages from n on
-    for (int base = lo; base < hi; base += kThreads) {
+    for (int base = 0; base < words; base += kThreads) {
         const int w = base + threadIdx.x;
         int chunk;
-        const int at = block_scan(w < hi ? __popc(p.mask[w]) : 0, chunk);
+        const int at = block_scan(w < words ? __popc(mask[w]) : 0, chunk);
         word_pre[threadIdx.x] = before + at;
         before += chunk;
         __syncthreads();
-        for (int v = base + warp; v < min(hi, base + kThreads); v += kWarps) {
-            const uint32_t live = p.mask[v];
-            const int page = 32 * v + lane;
+        for (int v = base + warp; v < min(words, base + kThreads); v += kWarps) {
+            const uint32_t live = mask[v];
+            const int page = 32 * (word0 + v) + lane;
             const int below = word_pre[v - base] + __popc(live & ((1u << lane) - 1));  // held pages below this one
             if (page == n) p.head->movers = page - below;
             if (page < p.P) {
@@ -386,38 +461,43 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const Pool p) {
     }
     cluster_sync();
     const int M = n < p.P ? __ldcg(&p.head->movers) : 0;
-    for (int k = me; k < M; k += all) {
-        const int src = __ldcg(p.movers + M - 1 - k), dst = __ldcg(&p.jobs[k].y);
-        p.jobs[k].x = src;
-        p.map[src] = dst;
-        p.ref[dst] = p.ref[src];
-        p.ref[src] = 0;
-    }
+    for_items(me, all, M, [&](int k) { return make_int2(__ldcg(p.movers + M - 1 - k), __ldcg(&p.jobs[k].y)); },
+              [&](int k, int2 move) {
+                  p.jobs[k].x = move.x;
+                  p.map[move.x] = move.y;
+                  p.ref[move.y] = p.ref[move.x];
+                  p.ref[move.x] = 0;
+              });
     for (int i = me; i < p.P - n; i += all) p.free_list[i] = p.P - 1 - i;
     if (me == 0) {
         if (*p.num_free != p.P - n) flag(p, VA_PAGES_BAD_COUNT);
         *p.num_free = p.P - n;
         p.head->jobs = M;
     }
-    for (int b = threadIdx.x; b < p.B; b += kThreads) {
-        const int L = p.lens[b];
-        const bool ok = L >= 0 && L <= most;
-        if (!ok && first) flag(p, VA_PAGES_BAD_REQUEST);
-        smem[b] = ok ? blocks_of(L) : 0;
-    }
-    prefix_sums(smem, p.B);
     cluster_sync();
-    for (int i = me; i < smem[p.B]; i += all) {
-        const int b = find(smem, p.B, i);
-        int32_t *entry = p.table + (size_t)b * p.stride + (i - smem[b]);
-        const int page = *entry;
-        if (page < 0 || page >= p.P) {
-            flag(p, VA_PAGES_BAD_ENTRY);
-            continue;
+    // the tables
+    const int entries = pre[p.B];
+    for (int base = me; base < entries; base += kBatch * all) {
+        int32_t *at[kBatch];
+        int page[kBatch], to[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int i = base + u * all;
+            if (i >= entries) continue;
+            const int b = find(pre, p.B, i);
+            at[u] = p.table + (size_t)b * p.stride + (i - pre[b]);
+            page[u] = *at[u];
         }
-        const int to = __ldcg(p.map + page);
-        if (to < 0) flag(p, VA_PAGES_BAD_COUNT);
-        else if (to != page) *entry = to;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+            if (base + u * all < entries && in_pool(p, page[u])) to[u] = __ldcg(p.map + page[u]);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (base + u * all >= entries) continue;
+            if (!in_pool(p, page[u])) flag(p, VA_PAGES_BAD_ENTRY);
+            else if (to[u] < 0) flag(p, VA_PAGES_BAD_COUNT);
+            else if (to[u] != page[u]) *at[u] = to[u];
+        }
     }
 }
 
@@ -482,18 +562,16 @@ __global__ void __launch_bounds__(kCopyThreads, 2) copy_kernel(const __grid_cons
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Layout {
-    size_t mask, claim, map, movers, jobs, total;
-    Layout(int B, int P) {
-        mask = align_up(sizeof(Header));
-        claim = mask + align_up(2 * sizeof(uint32_t) * (size_t)mask_words(P));
-        map = claim + align_up(sizeof(int32_t) * (size_t)B);
+    size_t map, movers, jobs, total;
+    explicit Layout(int P) {
+        map = align_up(sizeof(Header));
         movers = map + align_up(sizeof(int32_t) * (size_t)P);
         jobs = movers + align_up(sizeof(int32_t) * (size_t)P);
         total = jobs + align_up(sizeof(int2) * (size_t)P);
     }
 };
 
-bool sizes_ok(int B, int P) { return B >= 1 && B <= VA_PAGES_MAX_SEQS && P >= 1 && P <= (1 << 24); }
+bool sizes_ok(int B, int P) { return B >= 1 && B <= VA_PAGES_MAX_SEQS && P >= 1 && P <= VA_PAGES_MAX_PAGES; }
 
 int check(const va_page_pool *v, Pool *p) {
     if (!v || !v->block_table || !v->seq_lens || !v->ref_count || !v->free_list || !v->num_free || !v->workspace)
@@ -522,19 +600,22 @@ int check(const va_page_pool *v, Pool *p) {
     p->stride = v->block_table_stride;
     p->B = v->num_seqs;
     p->P = v->num_pages;
-    const Layout at(p->B, p->P);
+    const Layout at(p->P);
     char *ws = static_cast<char *>(v->workspace);
     p->head = reinterpret_cast<Header *>(ws);
-    p->mask = reinterpret_cast<uint32_t *>(ws + at.mask);
-    p->claim = reinterpret_cast<int32_t *>(ws + at.claim);
     p->map = reinterpret_cast<int32_t *>(ws + at.map);
     p->movers = reinterpret_cast<int32_t *>(ws + at.movers);
     p->jobs = reinterpret_cast<int2 *>(ws + at.jobs);
     return VA_OK;
 }
 
-// One cluster: a single CTA while the pool and the table are small (its barriers cost least), eight beyond.
-int cluster_for(const Pool &p, long long entries) { return p.P <= 16384 && entries <= 16384 ? 1 : kMaxCluster; }
+// One cluster: a single CTA while the pool and the table are small (its barriers cost least), eight beyond.  Sets the slice
+// of the bitmap that each CTA has.
+int cluster_for(Pool &p, long long entries) {
+    const int ctas = p.P <= 16384 && entries <= 8192 ? 1 : kMaxCluster;
+    while ((ctas << p.slice_bits) < mask_words(p.P)) ++p.slice_bits;
+    return ctas;
+}
 
 template <typename... KArgs, typename... Args>
 cudaError_t launch_book(void (*kernel)(KArgs...), int cluster, size_t smem, cudaStream_t s, Args... args) {
@@ -587,7 +668,7 @@ int done(cudaError_t e) {
 }  // namespace va
 
 extern "C" size_t verify_attn_pages_workspace_bytes(int num_seqs, int num_pages) {
-    return va::sizes_ok(num_seqs, num_pages) ? va::Layout(num_seqs, num_pages).total : 0;
+    return va::sizes_ok(num_seqs, num_pages) ? va::Layout(num_pages).total : 0;
 }
 
 extern "C" int verify_attn_pages_resize(const va_page_pool *pool, const int32_t *new_lens, void *stream) {
@@ -595,8 +676,9 @@ extern "C" int verify_attn_pages_resize(const va_page_pool *pool, const int32_t 
     if (const int rc = va::check(pool, &p)) return rc;
     if (!new_lens || (reinterpret_cast<uintptr_t>(new_lens) & 3)) return VA_ERR_INVALID_ARGUMENT;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const size_t smem = sizeof(int) * (2 * (size_t)p.B + 1) + (size_t)p.B;
-    cudaError_t e = va::launch_book(va::resize_kernel, va::cluster_for(p, (long long)p.B * p.stride), smem, s, p, new_lens);
+    const int ctas = va::cluster_for(p, (long long)p.B * p.stride);
+    const size_t smem = sizeof(int) * (4 * (size_t)p.B + 1 + ((size_t)1 << p.slice_bits));
+    cudaError_t e = va::launch_book(va::resize_kernel, ctas, smem, s, p, new_lens);
     if (e == cudaSuccess) e = va::launch_copies(pool, p, s);
     return va::done(e);
 }
@@ -611,9 +693,9 @@ extern "C" int verify_attn_pages_fork(const va_page_pool *pool, const int32_t *p
     for (const int32_t *x : {parents, children, lens})
         if (reinterpret_cast<uintptr_t>(x) & 3) return VA_ERR_INVALID_ARGUMENT;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const size_t smem = sizeof(int) * (3 * (size_t)num_forks + 2);
-    cudaError_t e = va::launch_book(va::fork_kernel, va::cluster_for(p, (long long)num_forks * p.stride), smem, s, p,
-                                    parents, children, lens, num_forks, share);
+    const int ctas = va::cluster_for(p, (long long)num_forks * p.stride);
+    const size_t smem = sizeof(int) * (5 * (size_t)num_forks + 2 + (size_t)p.B);
+    cudaError_t e = va::launch_book(va::fork_kernel, ctas, smem, s, p, parents, children, lens, num_forks, share);
     if (e == cudaSuccess) e = va::launch_copies(pool, p, s);
     return va::done(e);
 }
@@ -622,8 +704,9 @@ extern "C" int verify_attn_pages_compact(const va_page_pool *pool, void *stream)
     va::Pool p;
     if (const int rc = va::check(pool, &p)) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const size_t smem = sizeof(int) * ((size_t)p.B + 1);
-    cudaError_t e = va::launch_book(va::compact_kernel, va::cluster_for(p, (long long)p.B * p.stride), smem, s, p);
+    const int ctas = va::cluster_for(p, (long long)p.B * p.stride);
+    const size_t smem = sizeof(int) * ((size_t)p.B + 1 + ((size_t)1 << p.slice_bits));
+    cudaError_t e = va::launch_book(va::compact_kernel, ctas, smem, s, p);
     if (e == cudaSuccess) e = va::launch_copies(pool, p, s);
     return va::done(e);
 }

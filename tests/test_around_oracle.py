@@ -127,7 +127,7 @@ def test_rope_refuses_a_description_that_was_never_filled():
 
 
 def _append(**change):
-    a = dict(rope=va.verify_attn_rope_spec(32)._struct, pos=None, B=1, T=2, D=64, q=_heads(4096, 256, 128, 64), q_out=8192,
+    a = dict(rope=va.verify_attn_rope_spec(change.pop("rotary", 32))._struct, pos=None, B=1, T=2, D=64, q=_heads(4096, 256, 128, 64), q_out=8192,
              k=_heads(4096, 256, 128, 64), v=_heads(4096, 256, 128, 64), dtype=2, k_pages=4096, v_pages=4096, k_scale=4096,
              v_scale=4096, table=4096, stride=4, lens=4096, pages=8, flags=None)
     a.update(change)
@@ -143,7 +143,7 @@ def _append(**change):
     (dict(k_pages=None), -1), (dict(v_pages=None), -1), (dict(k_scale=None), -1), (dict(v_scale=None), -1),
     (dict(table=None), -1), (dict(lens=None), -1), (dict(B=0), -1), (dict(T=0), -1), (dict(stride=0), -1),
     (dict(pages=-1), -1), (dict(D=96), -2), (dict(dtype=5), -2), (dict(dtype=-1), -2),
-    (dict(rope=va.verify_attn_rope_spec(128)._struct), -1),   # wider than the head
+    (dict(rotary=128), -1),   # wider than the head
     (dict(v=_heads(4096, 256, 128, 64, n=1)), -1), (dict(q=_heads(4096, 256, 128, 64, n=0)), -1),
     (dict(k=_heads(4104, 256, 128, 64)), -1), (dict(v=_heads(4096, 256, 132, 64)), -1), (dict(q_out=8200), -1),
     (dict(k_pages=4104), -1), (dict(table=4098), -1), (dict(flags=4098), -1), (dict(pos=va._Positions(0, 0, 0, 1)), -1),
@@ -296,7 +296,7 @@ def _pool(**change):
 @pytest.mark.parametrize("change", [
     dict(block_table=None), dict(seq_lens=None), dict(ref_count=None), dict(free_list=None), dict(num_free=None),
     dict(workspace=None), dict(workspace=4104), dict(block_table=4098), dict(flags=4097), dict(block_table_stride=0),
-    dict(num_seqs=0), dict(num_seqs=8193), dict(num_pages=0), dict(num_pages=2 ** 24 + 1), dict(block_table_stride=2 ** 30),
+    dict(num_seqs=0), dict(num_seqs=8193), dict(num_pages=0), dict(num_pages=2 ** 22 + 1), dict(block_table_stride=2 ** 30),
     dict(num_buffers=-1), dict(page=(0, 64)), dict(page=(4104, 64)), dict(page=(4096, 24)), dict(page=(4096, 0)),
 ])
 def test_page_pool_refusals(change):
