@@ -526,29 +526,40 @@ def verify_attn_accept(target_logits, draft_tokens, temperature, seed, draft_log
     return out, nacc
 
 
+_here = contextlib.nullcontext()
+_torch = None
+
+
+def _bind_torch():
+    """What the calls below need of torch, looked up once: a call's checks and marshalling are most of
+    its cost on small batches."""
+    global _torch, _FLOAT_CODES, _CACHE_TYPES, _raw_stream, _current_device
+    import torch
+    _FLOAT_CODES = {torch.bfloat16: VA_FLOAT_BF16, torch.float16: VA_FLOAT_FP16, torch.float32: VA_FLOAT_FP32}
+    _CACHE_TYPES = {code: _kv_dtypes(code) for code in KV_DTYPE_CODES.values()}
+    # the current stream's handle without a Stream object around it, where torch offers that
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _current_device = torch.cuda.current_device
+    _torch = torch
+    return torch
+
+
 def _float_code(t, name):
-    code = _FLOAT_CODES.get(str(t.dtype))
+    code = _FLOAT_CODES.get(t.dtype)
     if code is None:
         raise ValueError(f"{name} has dtype {t.dtype}, expected bfloat16, float16 or float32")
     return code
-
-
-_FLOAT_CODES = {"torch.bfloat16": VA_FLOAT_BF16, "torch.float16": VA_FLOAT_FP16, "torch.float32": VA_FLOAT_FP32}
-_here = contextlib.nullcontext()
 
 
 def _launch_on(device, stream):
     """(stream handle, guard): a call runs on the tensors' device and on ``stream`` there (a
     torch stream or a raw handle; default: torch's current stream of that device).  What the
     call allocates is allocated inside the guard, so it belongs to that stream."""
-    import torch
+    torch = _torch
     if stream is None:
         index = device.index
-        current = torch.cuda.current_device() == index
-        # the current stream's handle without a Stream object around it, where torch offers that
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        handle = raw(index) if raw is not None else torch.cuda.current_stream(device).cuda_stream
-        return handle, _here if current else torch.cuda.device(device)
+        return _raw_stream(index), _here if _current_device() == index else torch.cuda.device(device)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     elif stream.device != device:
@@ -600,10 +611,9 @@ def _heads(t, name, dtype, index, shape=None):
 
 
 def _positions(t, rope, B, T, index):
-    import torch
     shape = (rope._struct.num_axes, B, T)
     try:
-        if t.dtype is torch.int32 and t.get_device() == index and t.shape == shape:
+        if t.dtype is _torch.int32 and t.get_device() == index and t.shape == shape:
             s = t.stride()
             return _Positions(t.data_ptr(), s[0], s[1], s[2])
     except AttributeError:
@@ -670,7 +680,7 @@ def verify_attn_rope(rope: Rope, positions, q, k=None, q_out=None, k_out=None, i
     ``q`` / ``k`` themselves to work in place, otherwise outputs must not overlap
     inputs.  ``inverse=True`` rotates back, which is also the gradient's way.
     Returns (q_out, k_out), k_out None without ``k``."""
-    import torch
+    torch = _torch or _bind_torch()
     device, index = _device_of(q, "q")
     code = _float_code(q, "q")
     dtype = q.dtype
@@ -710,7 +720,7 @@ def verify_attn_rope_append(rope: Rope, positions, q, k_new, v_new, k_pages, v_p
     their unrounded values.  ``positions`` None: every axis is the token's
     place in its sequence, ``seq_lens[b] - T + t``.  ``q`` may be None.  Returns
     the rotated q, contiguous bf16."""
-    import torch
+    torch = _torch or _bind_torch()
     code = _dtype_code(kv_dtype)
     device, index = _device_of(k_new, "k_new")
     bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
@@ -726,10 +736,10 @@ def verify_attn_rope_append(rope: Rope, positions, q, k_new, v_new, k_pages, v_p
     elif q_out is not None:
         raise ValueError("q_out without q")
     pos = None if positions is None else _positions(positions, rope, B, T, index)
-    kvd = _kv_dtypes(code)
+    kvd = _CACHE_TYPES.get(code, ())
     kp, vp = _ptr_of(k_pages, "k_pages", kvd, index), _ptr_of(v_pages, "v_pages", kvd, index)
     pages = k_pages.shape[0] if k_pages.dim() else 0
-    cache = (pages, PAGE_SIZE, Hkv, {VA_INT4: D // 2, VA_INT2: D // 4}.get(code, D))
+    cache = (pages, PAGE_SIZE, Hkv, D // 2 if code == VA_INT4 else D // 4 if code == VA_INT2 else D)
     if k_pages.shape != cache or v_pages.shape != cache:
         raise ValueError(f"k_pages and v_pages must be [num_pages, {PAGE_SIZE}, {Hkv}, {cache[3]}], got "
                          f"{list(k_pages.shape)} and {list(v_pages.shape)}")
@@ -739,8 +749,9 @@ def verify_attn_rope_append(rope: Rope, positions, q, k_new, v_new, k_pages, v_p
     if code != VA_BF16:
         ks, vs = _ptr(k_scale, "k_scale", f32, index, cache[:3]), _ptr(v_scale, "v_scale", f32, index, cache[:3])
     bt, sl = _ptr(block_table, "block_table", i32, index), _ptr(seq_lens, "seq_lens", i32, index, (B,))
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError(f"block_table must be [{B}, stride], got {list(block_table.shape)}")
+    nt = block_table.shape
+    if len(nt) != 2 or nt[0] != B:
+        raise ValueError(f"block_table must be [{B}, stride], got {list(nt)}")
     fl = None if flags is None else _ptr(flags, "flags", i32, index)
     st, guard = _launch_on(device, stream)
     with guard:
@@ -750,7 +761,7 @@ def verify_attn_rope_append(rope: Rope, positions, q, k_new, v_new, k_pages, v_p
                 q_out = torch.empty(nq, dtype=bf16, device=device)
             oq = _ptr(q_out, "q_out", bf16, index, nq)
         rc = (_lib or _load()).verify_attn_rope_append(
-            rope._ref, pos, B, T, D, hq, oq, hk, hv, code, kp, vp, ks, vs, bt, block_table.shape[1], sl,
+            rope._ref, pos, B, T, D, hq, oq, hk, hv, code, kp, vp, ks, vs, bt, nt[1], sl,
             num_pages or pages, fl, st)
     if rc:
         _check(rc, "verify_attn_rope_append")
@@ -767,7 +778,7 @@ def verify_attn_accept_probs(target_probs, draft_tokens, u_accept, u_emit, draft
     ``[B, T]`` (one per draft) and ``u_emit`` fp32 ``[B]`` (for the emitted
     token).  Definition in ``include/verify_attn.h``.  Returns (out_tokens int32
     ``[B, T+1]`` with -1 after the emitted token, num_accepted int32 ``[B]``)."""
-    import torch
+    torch = _torch or _bind_torch()
     f32, i32 = torch.float32, torch.int32
     device, index = _device_of(target_probs, "target_probs")
     code = _float_code(target_probs, "target_probs")
@@ -822,7 +833,7 @@ class PagePool:
     (with ``block_table_stride`` and ``num_pages`` as plan options)."""
 
     def __init__(self, block_table, seq_lens, ref_count, free_list, num_free, buffers, flags=None):
-        import torch
+        torch = _torch or _bind_torch()
         i32 = torch.int32
         device, index = _device_of(block_table, "block_table")
         if block_table.dim() != 2 or ref_count.dim() != 1:
@@ -834,7 +845,7 @@ class PagePool:
         self.block_table, self.seq_lens, self.ref_count = block_table, seq_lens, ref_count
         self.free_list, self.num_free, self.flags = free_list, num_free, flags
         self.buffers = list(buffers)
-        self.num_seqs, self.num_pages, self.device = B, P, device
+        self.num_seqs, self.num_pages, self.device, self._index = B, P, device, index
         array = (_PageBuffer * max(1, len(self.buffers)))()
         for i, t in enumerate(self.buffers):
             if not t.is_contiguous() or t.device != device or t.dim() < 1 or t.shape[0] != P:
@@ -870,8 +881,7 @@ def verify_attn_pages_resize(pool: PagePool, new_lens, stream=None):
     device, negative: left alone): pages past a shorter length go back to the
     pool, a longer one takes pages, and a growing sequence whose partly filled
     last page is shared gets a copy of its own."""
-    import torch
-    n = _ptr(new_lens, "new_lens", torch.int32, pool.device.index, (pool.num_seqs,))
+    n = _ptr(new_lens, "new_lens", _torch.int32, pool._index, (pool.num_seqs,))
     st, guard = _launch_on(pool.device, stream)
     with guard:
         rc = (_lib or _load()).verify_attn_pages_resize(pool._ref, n, st)
@@ -884,8 +894,7 @@ def verify_attn_pages_fork(pool: PagePool, parents, children, lens=None, share=T
     the device), of their first ``lens`` tokens where given.  ``share``: full
     pages are held in common and a partly filled last page is copied; otherwise
     every page is copied."""
-    import torch
-    i32, index = torch.int32, pool.device.index
+    i32, index = _torch.int32, pool._index
     pa = _ptr(parents, "parents", i32, index)
     shape = parents.shape
     if len(shape) != 1:
