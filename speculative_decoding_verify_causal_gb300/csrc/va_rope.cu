@@ -69,7 +69,7 @@ struct RopeParams {
     int q_heads, heads;      // heads of q, of q and k together
     int tokens;              // num_seqs * T
     int head_chunk;          // heads per thread
-    int units;               // of a head: pairs / W, then the unrotated vectors
+    int units;               // of a head: those of the pairs, then the unrotated vectors
     int pair_units;
     float inverse_sign;      // -1 for the inverse
     FastDiv by_T, by_units;
@@ -144,34 +144,35 @@ __device__ __forceinline__ V packed(const float (&x)[W]) {
     return raw;
 }
 
-// A unit is W pairs of one head (two vectors of W elements: one of each half,
-// or 2 W neighbours) or, past the pairs, one vector that is copied.  A thread
-// has one unit of one token: it makes the W (cos, sin) once, in registers, and
-// turns that unit of head_chunk heads with them.  No shared memory and no
-// barrier: a first form that made a token's (cos, sin) in shared memory for all
-// its heads issued twice the instructions and waited on the table's bank
-// conflicts (32,768 tokens, 40 heads of 128, bf16: 123.5 us).
+// A unit is a piece of one head whose pairs are whole: a vector of W elements of each half, or one vector of neighbours (two
+// single elements where W is 1), or, past the pairs, one vector that is copied.  A thread has one unit of one token: it makes
+// its (cos, sin) once, in registers, and turns that unit of head_chunk heads with them.  No shared memory and no barrier: a
+// first form that made a token's (cos, sin) in shared memory for all its heads issued twice the instructions and waited on
+// the table's bank conflicts (32,768 tokens, 40 heads of 128, bf16: 123.5 us; this one 104.4 us, 6.4 TB/s of the 671 MB).
 template <int TYPE, int W, bool ADJACENT>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
     using V = typename Raw<W * Elem<TYPE>::kBytes>::V;
     constexpr int kElem = Elem<TYPE>::kBytes;
+    constexpr bool kOne = ADJACENT && W > 1;      // one vector holds the pairs
+    constexpr int kPairs = kOne ? W / 2 : W;
     const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
     const uint32_t n = div(i, p.by_units), unit = i - n * p.units;
     if (n >= (uint32_t)p.tokens) return;
     const int P = p.rope.num_pairs;
     const int b = (int)div(n, p.by_T), t = (int)n - b * (int)p.by_T.d;
     const bool pairs = (int)unit < p.pair_units;
-    const int pair0 = W * (int)unit;
+    const int pair0 = kPairs * (int)unit;
     const int64_t elem = pairs ? (ADJACENT ? 2 * pair0 : pair0) : 2 * P + W * ((int)unit - p.pair_units);
     const int64_t off0 = elem * kElem, off1 = off0 + (ADJACENT ? W : P) * kElem;
     const int h0 = blockIdx.y * p.head_chunk, h1 = min(p.heads, h0 + p.head_chunk);
     griddep_wait();
-    // heads h0 .. h1 - 1 of q and k, kUnroll at a time
-    V lo[kUnroll], hi[kUnroll];
-    char *to[kUnroll];
+    // heads h0 .. h1 - 1 of q and k, kAhead at a time
+    constexpr int kAhead = kOne ? 2 * kUnroll : kUnroll;
+    V lo[kAhead], hi[kAhead];
+    char *to[kAhead];
     auto load = [&](int h) {
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u, ++h) {
+        for (int u = 0; u < kAhead; ++u, ++h) {
             if (h >= h1) continue;
             const bool is_k = h >= p.q_heads;
             const Tensor &x = is_k ? p.k : p.q;
@@ -179,48 +180,45 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
             const char *in = x.in + b * x.in_seq + t * x.in_token + g * x.in_head;
             to[u] = x.out + b * x.out_seq + t * x.out_token + g * x.out_head;
             lo[u] = *reinterpret_cast<const V *>(in + off0);
-            if (pairs) hi[u] = *reinterpret_cast<const V *>(in + off1);
+            if (!kOne && pairs) hi[u] = *reinterpret_cast<const V *>(in + off1);
         }
     };
     load(h0);  // under way while the angles are computed
-    float2 cs[W];
+    float2 cs[kPairs];
     if (pairs) {
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
+        for (int j = 0; j < kPairs; ++j) {
             const int pos = p.pos[p.rope.axis[pair0 + j] * p.pos_axis + b * p.pos_seq + t * p.pos_token];
             cs[j] = turned(p.rope.turn[pair0 + j], pos, p.rope.scale);
             cs[j].y *= p.inverse_sign;
         }
     }
-    for (int h = h0; h < h1; h += kUnroll) {
-        V x[kUnroll], y[kUnroll];
-        char *out[kUnroll];
+    for (int h = h0; h < h1; h += kAhead) {
+        V x[kAhead], y[kAhead];
+        char *out[kAhead];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
+        for (int u = 0; u < kAhead; ++u) {
             x[u] = lo[u];
             y[u] = hi[u];
             out[u] = to[u];
         }
-        load(h + kUnroll);  // under way while these are turned
+        load(h + kAhead);  // under way while these are turned
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
+        for (int u = 0; u < kAhead; ++u) {
             if (h + u >= h1) continue;
             if (pairs) {
                 float x0[W], x1[W];
                 unpack<TYPE, W>(x[u], x0);
-                unpack<TYPE, W>(y[u], x1);
+                if (!kOne) unpack<TYPE, W>(y[u], x1);
 #pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    // adjacent: x0, x1 are one run of 2 W, pair j its elements 2 j and 2 j + 1
-                    float &first = ADJACENT ? (2 * j < W ? x0[2 * j < W ? 2 * j : 0] : x1[2 * j < W ? 0 : 2 * j - W]) : x0[j];
-                    float &second = ADJACENT ? (2 * j + 1 < W ? x0[2 * j + 1 < W ? 2 * j + 1 : 0] : x1[2 * j + 1 < W ? 0 : 2 * j + 1 - W])
-                                             : x1[j];
+                for (int j = 0; j < kPairs; ++j) {
+                    float &first = x0[kOne ? 2 * j : j], &second = kOne ? x0[(2 * j + 1) % W] : x1[j];
                     const float na = fmaf(first, cs[j].x, -second * cs[j].y), nb = fmaf(second, cs[j].x, first * cs[j].y);
                     first = na;
                     second = nb;
                 }
                 x[u] = packed<TYPE, W, V>(x0);
-                *reinterpret_cast<V *>(out[u] + off1) = packed<TYPE, W, V>(x1);
+                if (!kOne) *reinterpret_cast<V *>(out[u] + off1) = packed<TYPE, W, V>(x1);
             }
             *reinterpret_cast<V *>(out[u] + off0) = x[u];
         }
@@ -260,14 +258,15 @@ struct RopeAppendParams {
 };
 
 constexpr int kRowsEach = 48;     // rows of a thread where there is work enough
-constexpr int kAppendCtas = 456;  // three CTAs for each of 152 SMs
+constexpr int kAppendThreads = 64;
+constexpr int kAppendCtas = 912;  // six for each of 152 SMs
 constexpr int kE = 16;  // elements of a lane: two 16-byte vectors of bf16
 
 // Where the two elements of a pair are, as the kernel is built for it.
 enum Pairing : int {
     kHalves,    // P / 8 lanes hold 8 pairs each: 8 elements of either half (P a multiple of 8)
-    kAdjacent,  // a lane holds 16 neighbours
-    kApart      // halves that begin inside a vector: 16 neighbours a lane, the other element is read again
+    kAdjacent,  // inside a lane's vectors
+    kApart      // halves that begin inside a vector: the other element is read again
 };
 
 // Eight codes of the append's rule, element e at bit e * bits of the result.
@@ -338,23 +337,26 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 // one after the other, kAhead of them with their loads in flight.  Both elements of a pair are in the lane, whose 8 (cos, sin)
 // stay in registers: a rotation is two multiplications and two fused ones, two pairs an instruction, without shared memory,
 // barriers or exchange.  8,192 tokens of 32 + 16 heads of 128, bf16: with pairs spread over lanes (the other element by a
-// shuffle) 85 us, bound by its instructions; with a token's (cos, sin) in shared memory for all its rows 66 us.
+// shuffle) 85 us, bound by its instructions; with a token's (cos, sin) in shared memory for all its rows 66 us; this one 35.4
+// us, 5.7 TB/s, bound by the loads in flight: three rows ahead in eight CTAs an SM (two rows 38.4 us; four 36.4; nine CTAs,
+// with fewer registers, 41.1).  In CTAs of 64 threads, since 128 leave a sixth of the SMs a CTA short here.
 template <int D, int DT, int PAIRING>
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_constant__ RopeAppendParams p) {
-    constexpr int kLanes = D / kE, kAhead = 2;
+__global__ void __launch_bounds__(kAppendThreads, 8) rope_append_kernel(const __grid_constant__ RopeAppendParams p) {
+    constexpr int kLanes = D / kE, kAhead = 3;
     const int P = p.rope.num_pairs;
     const int lane = threadIdx.x & 31, sub = lane % kLanes;
-    const int n = (blockIdx.x * kThreads + threadIdx.x) / kLanes;
+    const int n = (blockIdx.x * kAppendThreads + threadIdx.x) / kLanes;
     const bool here = n < p.tokens;  // whole rows of lanes, so that those past the end only take part in exchanges
     const int b = here ? n / p.T : 0, t = here ? n - b * p.T : 0;
     const int rows = p.Hq + 2 * p.Hkv;
     const int from = blockIdx.y * p.chunk, to = min(rows, from + p.chunk);
-    // this lane's elements: 8 from e0, 8 from e1; `turns` of its 8 pairs are turned, the pairs from pair0 on
+    // this lane's elements, 8 from e0 and 8 from e1: halves of the same 8 pairs (then the rest of the head, two vectors a
+    // lane), or vectors of the head's own halves
     const int pair_lanes = P / 8;
     const bool tail = PAIRING == kHalves && sub >= pair_lanes;
-    const int e0 = PAIRING != kHalves ? kE * sub : tail ? 2 * P + kE * (sub - pair_lanes) : 8 * sub;
-    const int e1 = PAIRING != kHalves || tail ? e0 + 8 : P + 8 * sub;
-    const int pair0 = 8 * sub, turns = PAIRING == kHalves ? (tail ? 0 : 8) : min(8, max(0, P - pair0));
+    const int e0 = tail ? 2 * P + kE * (sub - pair_lanes) : 8 * sub;
+    const int e1 = PAIRING != kHalves ? D / 2 + e0 : tail ? e0 + 8 : P + 8 * sub;
+    auto pair_of = [&](int j) { return PAIRING == kHalves ? 8 * sub + j : (j < 4 ? e0 / 2 + j : e1 / 2 + j - 4); };
     griddep_wait();
     auto source = [&](int row) {
         return row < p.Hq           ? p.q + b * p.q_seq + t * p.q_token + row * p.q_head
@@ -387,7 +389,7 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_cons
     float2 cs[8];
     if (PAIRING != kApart && from < p.Hq + p.Hkv) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) cs[j] = j < turns ? angle(pair0 + j) : make_float2(1.f, 0.f);
+        for (int j = 0; j < 8; ++j) cs[j] = !tail && pair_of(j) < P ? angle(pair_of(j)) : make_float2(1.f, 0.f);
     }
     for (int base = from; base < to; base += kAhead) {
         uint4 raw0[kAhead], raw1[kAhead];
@@ -407,7 +409,7 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_cons
             unpack<VA_FLOAT_BF16, 8>(raw1[r], x1);
             if (!is_v) {
                 if constexpr (PAIRING == kHalves) {
-                    if (turns) {
+                    if (!tail) {
 #pragma unroll
                         for (int j = 0; j < 8; j += 2) {
                             const uint64_t a2 = pair2(x0[j], x0[j + 1]), b2 = pair2(x1[j], x1[j + 1]);
@@ -423,13 +425,13 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_cons
                     for (int j = 0; j < 8; ++j) {
                         float &u = j < 4 ? x0[2 * (j & 3)] : x1[2 * (j & 3)], &v = j < 4 ? x0[2 * (j & 3) + 1] : x1[2 * (j & 3) + 1];
                         const float nu = fmaf(u, cs[j].x, -v * cs[j].y), nv = fmaf(v, cs[j].x, u * cs[j].y);
-                        if (j < turns) u = nu, v = nv;
+                        if (pair_of(j) < P) u = nu, v = nv;
                     }
                 } else {
                     const uint16_t *src = source(row);
 #pragma unroll
                     for (int m = 0; m < kE; ++m) {
-                        const int i = e0 + m;
+                        const int i = m < 8 ? e0 + m : e1 + m - 8;
                         if (i < 2 * P && here) {
                             const float2 r2 = angle(i < P ? i : i - P);
                             const float far = __uint_as_float((uint32_t)src[i < P ? i + P : i - P] << 16);
@@ -468,10 +470,10 @@ template <int D, int DT>
 cudaError_t launch_append(RopeAppendParams p, cudaStream_t s) {
     // rows of a thread: kRowsEach, fewer while the grid is below kAppendCtas
     const int rows = p.Hq + 2 * p.Hkv;
-    const unsigned ctas = (unsigned)(((long long)p.tokens * (D / kE) + kThreads - 1) / kThreads);
+    const unsigned ctas = (unsigned)(((long long)p.tokens * (D / kE) + kAppendThreads - 1) / kAppendThreads);
     const int chunks = std::min(rows, std::max((rows + kRowsEach - 1) / kRowsEach, (int)((kAppendCtas + ctas - 1) / ctas)));
     p.chunk = (rows + chunks - 1) / chunks;
-    const dim3 grid(ctas, (rows + p.chunk - 1) / p.chunk), block(kThreads);
+    const dim3 grid(ctas, (rows + p.chunk - 1) / p.chunk), block(kAppendThreads);
     if (p.rope.adjacent) return launch_pdl(rope_append_kernel<D, DT, kAdjacent>, grid, block, 0, s, p);
     return p.rope.num_pairs % 8 == 0 ? launch_pdl(rope_append_kernel<D, DT, kHalves>, grid, block, 0, s, p)
                                      : launch_pdl(rope_append_kernel<D, DT, kApart>, grid, block, 0, s, p);
@@ -587,7 +589,7 @@ extern "C" int verify_attn_rope(const va_rope *rope, const va_positions *positio
     const int P = rope->num_pairs;
     int w = 1;
     for (int cand : {16 / bytes, 2}) {
-        bool ok = P % cand == 0 && (head_dim - 2 * P) % cand == 0;
+        bool ok = (rope->adjacent ? 2 * P : P) % cand == 0 && (head_dim - 2 * P) % cand == 0;
         for (const va_heads *x : all)
             ok = ok && (!x || (va::aligned(x->data, (uintptr_t)cand * bytes) && va::strides_ok(*x, num_seqs, T, cand)));
         if (ok) {
@@ -611,7 +613,7 @@ extern "C" int verify_attn_rope(const va_rope *rope, const va_positions *positio
     p.q_heads = q->num_heads;
     p.heads = heads;
     p.tokens = (int)tokens;
-    p.pair_units = P / w;
+    p.pair_units = rope->adjacent && w > 1 ? 2 * P / w : P / w;
     p.units = p.pair_units + (head_dim - 2 * P) / w;
     p.inverse_sign = inverse ? -1.f : 1.f;
     if (tokens * p.units >= (1LL << 31)) return VA_ERR_INVALID_ARGUMENT;
