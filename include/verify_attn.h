@@ -466,8 +466,10 @@ typedef struct {
 /* Rotate q and k (k and k_out may both be NULL) of one batch in one launch.
  * Each output is its input's own memory with the same strides (in place), or
  * memory that overlaps neither input; its elements must not overlap each
- * other.  head_dim >= 2 * num_pairs, any size up to 1024; num_seqs, T >= 0 (nothing
- * is launched for 0).  Arithmetic in binary32, one rounding to the type.
+ * other.  head_dim >= 2 * num_pairs, any size up to 1024; num_seqs, T >= 0
+ * (nothing is launched for 0), at most 2^30 vectors of one head's elements in
+ * num_seqs * T tokens (16 bytes each where sizes, strides and pointers allow,
+ * single elements at worst).  Arithmetic in binary32, one rounding to the type.
  * Returns VA_OK when enqueued, VA_ERR_INVALID_ARGUMENT, VA_ERR_UNSUPPORTED
  * for an unknown type, VA_ERR_CUDA. */
 int verify_attn_rope(const va_rope *rope, const va_positions *positions, va_float_type type,
@@ -488,8 +490,8 @@ int verify_attn_rope(const va_rope *rope, const va_positions *positions, va_floa
  * L_b - T + t.  Cache, block table, seq_lens, num_pages and flags as for
  * verify_attn_kv_append; rows whose block lies outside the block table's row
  * are skipped and flagged as well.  head_dim in {64, 128, 256}; q, k_new and
- * v_new start on a 16-byte boundary and their strides are multiples of 8.
- * Returns as verify_attn_kv_append. */
+ * v_new start on a 16-byte boundary and their strides are multiples of 8;
+ * num_seqs * T <= 2^26.  Returns as verify_attn_kv_append. */
 int verify_attn_rope_append(const va_rope *rope, const va_positions *positions, int num_seqs, int T,
                             int head_dim, const va_heads *q, void *q_out, const va_heads *k_new,
                             const va_heads *v_new, va_kv_dtype kv_dtype, void *k_pages,
@@ -534,7 +536,8 @@ typedef struct {
  * [num_seqs] or NULL, u_accept fp32 [num_seqs, T], u_emit fp32 [num_seqs],
  * out_tokens int32 [num_seqs, T + 1], num_accepted int32 [num_seqs].
  * T >= 0 (0: one sample of p_0 per sequence; draft_tokens and u_accept may
- * then be NULL), 1 <= num_seqs <= 65535, vocab >= 1.  No workspace.  Returns
+ * then be NULL), T <= 65535, 1 <= num_seqs <= 65535, 1 <= vocab <= 2^30.  No
+ * workspace.  Returns
  * VA_OK when enqueued, VA_ERR_INVALID_ARGUMENT, VA_ERR_UNSUPPORTED for an
  * unknown type, VA_ERR_CUDA. */
 int verify_attn_accept_probs(const va_rows *target_probs, const va_rows *draft_probs,
@@ -579,7 +582,7 @@ int verify_attn_accept_probs(const va_rows *target_probs, const va_rows *draft_p
  * its block table, must be ordered on one stream.  Results do not depend on
  * timing: whole numbers, counted and ordered by page and sequence.
  * Limits: num_seqs and num_forks <= VA_PAGES_MAX_SEQS, num_pages <=
- * VA_PAGES_MAX_PAGES, num_seqs * block_table_stride < 2^31.  Every call returns VA_OK when enqueued,
+ * VA_PAGES_MAX_PAGES, num_seqs (num_forks) * block_table_stride <= 2^30.  Every call returns VA_OK when enqueued,
  * VA_ERR_INVALID_ARGUMENT for null or misaligned pointers and sizes out of
  * range, VA_ERR_CUDA if a launch fails. */
 #define VA_PAGES_MAX_SEQS 8192

@@ -678,8 +678,9 @@ def verify_attn_rope(rope: Rope, positions, q, k=None, q_out=None, k_out=None, i
     with a contiguous last dimension) by ``positions`` (int32 ``[axes, B, T]``,
     any strides).  ``q_out`` / ``k_out`` default to new contiguous tensors; pass
     ``q`` / ``k`` themselves to work in place, otherwise outputs must not overlap
-    inputs.  ``inverse=True`` rotates back, which is also the gradient's way.
-    Returns (q_out, k_out), k_out None without ``k``."""
+    inputs.  ``inverse=True`` rotates back, which is also the way of the gradient
+    (the call itself is not recorded by autograd).  Returns (q_out, k_out), k_out
+    None without ``k``."""
     torch = _torch or _bind_torch()
     device, index = _device_of(q, "q")
     code = _float_code(q, "q")
@@ -846,14 +847,14 @@ class PagePool:
         self.free_list, self.num_free, self.flags = free_list, num_free, flags
         self.buffers = list(buffers)
         self.num_seqs, self.num_pages, self.device, self._index = B, P, device, index
+        size = int(_load().verify_attn_pages_workspace_bytes(B, P))
+        if not size:
+            raise ValueError(f"{B} sequences or {P} pages are out of range")
         array = (_PageBuffer * max(1, len(self.buffers)))()
         for i, t in enumerate(self.buffers):
             if not t.is_contiguous() or t.device != device or t.dim() < 1 or t.shape[0] != P:
                 raise ValueError(f"buffer {i} must be a contiguous tensor on {device} with {P} pages in its first dimension")
             array[i].data, array[i].page_bytes = t.data_ptr(), t.numel() // P * t.element_size()
-        size = int(_load().verify_attn_pages_workspace_bytes(B, P))
-        if not size:
-            raise ValueError(f"{B} sequences or {P} pages are out of range")
         self.workspace = torch.empty(size, dtype=torch.uint8, device=device)
         self._array = array
         self._struct = _PagePool(

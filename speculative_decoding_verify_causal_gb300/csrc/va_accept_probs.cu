@@ -420,7 +420,8 @@ extern "C" int verify_attn_accept_probs(const va_rows *target_probs, const va_ro
                                         const float *u_accept, const float *u_emit, int num_seqs, int T, int vocab,
                                         int32_t *out_tokens, int32_t *num_accepted, void *stream) {
     if (!target_probs || !target_probs->data || !u_emit || !out_tokens || !num_accepted) return VA_ERR_INVALID_ARGUMENT;
-    if (num_seqs < 1 || num_seqs > 65535 || T < 0 || T > 65535 || vocab < 1) return VA_ERR_INVALID_ARGUMENT;
+    if (num_seqs < 1 || num_seqs > 65535 || T < 0 || T > 65535 || vocab < 1 || vocab > (1 << 30))
+        return VA_ERR_INVALID_ARGUMENT;
     if (T > 0 && (!draft_tokens || !u_accept)) return VA_ERR_INVALID_ARGUMENT;
     if (type != VA_FLOAT_BF16 && type != VA_FLOAT_FP16 && type != VA_FLOAT_FP32) return VA_ERR_UNSUPPORTED;
     const bool model = draft_probs && draft_probs->data && T > 0;

@@ -580,7 +580,7 @@ int check(const va_page_pool *v, Pool *p) {
     if (!v || !v->block_table || !v->seq_lens || !v->ref_count || !v->free_list || !v->num_free || !v->workspace)
         return VA_ERR_INVALID_ARGUMENT;
     if (!sizes_ok(v->num_seqs, v->num_pages) || v->block_table_stride < 1 ||
-        (long long)v->num_seqs * v->block_table_stride >= (1LL << 31) ||
+        (long long)v->num_seqs * v->block_table_stride > (1LL << 30) ||
         (long long)v->block_table_stride * VA_PAGE_SIZE >= (1LL << 31) || v->num_buffers < 0 ||
         (v->num_buffers > 0 && !v->buffers))
         return VA_ERR_INVALID_ARGUMENT;
@@ -690,7 +690,7 @@ extern "C" int verify_attn_pages_fork(const va_page_pool *pool, const int32_t *p
     if (const int rc = va::check(pool, &p)) return rc;
     if (num_forks < 0 || num_forks > VA_PAGES_MAX_SEQS) return VA_ERR_INVALID_ARGUMENT;
     if (num_forks == 0) return VA_OK;
-    if (!parents || !children || (long long)num_forks * p.stride >= (1LL << 31)) return VA_ERR_INVALID_ARGUMENT;
+    if (!parents || !children || (long long)num_forks * p.stride > (1LL << 30)) return VA_ERR_INVALID_ARGUMENT;
     for (const int32_t *x : {parents, children, lens})
         if (reinterpret_cast<uintptr_t>(x) & 3) return VA_ERR_INVALID_ARGUMENT;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

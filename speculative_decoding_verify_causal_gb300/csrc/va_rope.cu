@@ -616,7 +616,7 @@ extern "C" int verify_attn_rope(const va_rope *rope, const va_positions *positio
     p.pair_units = rope->adjacent && w > 1 ? 2 * P / w : P / w;
     p.units = p.pair_units + (head_dim - 2 * P) / w;
     p.inverse_sign = inverse ? -1.f : 1.f;
-    if (tokens * p.units >= (1LL << 31)) return VA_ERR_INVALID_ARGUMENT;
+    if (tokens * p.units > (1LL << 30)) return VA_ERR_INVALID_ARGUMENT;
     // heads of a thread: kHeads, fewer while the grid is below kMinCtas
     const unsigned ctas = (unsigned)((tokens * p.units + va::kThreads - 1) / va::kThreads);
     const int chunks = std::min<long long>(heads, std::max<long long>((heads + va::kHeads - 1) / va::kHeads,

@@ -113,6 +113,7 @@ def _rope(**change):
     (dict(q_out=_heads(8192, token=24)), -1),   # tokens overlap the heads before them
     (dict(q_out=_heads(4096, token=32, seq=96)), -1),   # in place with other strides
     (dict(q=_heads(token=-64)), -1),
+    (dict(B=2 ** 20, T=2 ** 20), -1), (dict(B=2 ** 14, T=2 ** 14, q=_heads(4098), q_out=_heads(8194)), -1),  # too many
     (dict(B=0), 0), (dict(T=0), 0),             # nothing to do
 ])
 def test_rope_refusals(change, status):
@@ -205,7 +206,7 @@ def _accept(**change):
     (dict(p=None), -1), (dict(p=va._Rows(0, 8, 4)), -1), (dict(p=va._Rows(4098, 8, 4)), -1), (dict(p=va._Rows(4096, -8, 4)), -1),
     (dict(q=va._Rows(4098, 4, 4)), -1), (dict(q=va._Rows(4096, 4, -4)), -1), (dict(type=3), -2), (dict(drafts=None), -1),
     (dict(ua=None), -1), (dict(ue=None), -1), (dict(out=None), -1), (dict(n=None), -1), (dict(B=0), -1), (dict(B=65536), -1),
-    (dict(T=-1), -1), (dict(T=65536), -1), (dict(V=0), -1), (dict(drafts=4097), -1), (dict(lens=4098), -1), (dict(out=4099), -1),
+    (dict(T=-1), -1), (dict(T=65536), -1), (dict(V=0), -1), (dict(V=2 ** 30 + 1), -1), (dict(drafts=4097), -1), (dict(lens=4098), -1), (dict(out=4099), -1),
 ])
 def test_accept_probs_refusals(change, status):
     assert _accept(**change) == status
@@ -296,7 +297,7 @@ def _pool(**change):
 @pytest.mark.parametrize("change", [
     dict(block_table=None), dict(seq_lens=None), dict(ref_count=None), dict(free_list=None), dict(num_free=None),
     dict(workspace=None), dict(workspace=4104), dict(block_table=4098), dict(flags=4097), dict(block_table_stride=0),
-    dict(num_seqs=0), dict(num_seqs=8193), dict(num_pages=0), dict(num_pages=2 ** 22 + 1), dict(block_table_stride=2 ** 30),
+    dict(num_seqs=0), dict(num_seqs=8193), dict(num_pages=0), dict(num_pages=2 ** 22 + 1), dict(block_table_stride=2 ** 30), dict(num_seqs=4096, block_table_stride=2 ** 18 + 1),
     dict(num_buffers=-1), dict(page=(0, 64)), dict(page=(4104, 64)), dict(page=(4096, 24)), dict(page=(4096, 0)),
 ])
 def test_page_pool_refusals(change):

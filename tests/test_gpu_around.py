@@ -599,6 +599,24 @@ def test_pages_create_takes_the_lowest_page_first(va):
     assert pool.num_free.item() == 45 and va.verify_attn_pages_flags(pool) == 0
 
 
+def test_pages_at_the_limits(va):
+    """The most sequences, forks and pages that a call takes."""
+    P, B, stride = 2 ** 22, 8192, 40
+    rng = np.random.default_rng(6)
+    pool = around.Pages(P, B, stride, [rng.integers(0, 255, (P, 16)).astype(np.uint8)])
+    pool.stack = rng.permutation(P)
+    dev = gpu_pool(va, pool)
+    lens = rng.integers(0, 640, B)
+    lens[B // 2:] = 0
+    order = rng.permutation(B // 2)
+    for name, args in (("resize", (lens.astype(np.int32),)),
+                       ("fork", (order.astype(np.int32), (B // 2 + order).astype(np.int32), None, True)),
+                       ("fork", (np.arange(B, dtype=np.int32), np.arange(B, dtype=np.int32)[::-1].copy(), None, False)),
+                       ("resize", (np.where(rng.random(B) < 0.5, lens // 2, 640).astype(np.int32),)), ("compact", ())):
+        apply(va, dev, pool, name, args)
+        check_pool(dev, pool)
+
+
 def test_pages_all_of_a_long_sequence_at_once(va):
     """A 262,144-token sequence taken, shared, copied, freed and the rest compacted, on the wide path."""
     P, B, stride = 40000, 3, 16400
@@ -735,6 +753,8 @@ def test_page_pool_argument_errors(va):
         with pytest.raises(ValueError):
             va.PagePool(*[bad if i == at else x for i, x in enumerate(good)])
     with pytest.raises(ValueError):
+        va.PagePool.create(0, 2, 3, [torch.zeros(0, 4, device="cuda")])
+    with pytest.raises(ValueError):
         va.verify_attn_pages_resize(pool, i32(3))
     with pytest.raises(ValueError):
         va.verify_attn_pages_fork(pool, i32(2), i32(3))
@@ -809,6 +829,11 @@ def test_steps_on_a_side_stream_and_captured_are_the_eager_ones(va):
         with torch.cuda.stream(s2):  # torch's own additions there too; the calls are told the raw handle
             explicit.run(stream=s2.cuda_stream)
     for a, b in zip(explicit.state(), want):
+        assert torch.equal(a, b)
+    default = Step(va)
+    for _ in range(3):
+        default.run(stream=0)  # the raw handle of the default stream
+    for a, b in zip(default.state(), want):
         assert torch.equal(a, b)
     torch.cuda.synchronize()
     first, second = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
