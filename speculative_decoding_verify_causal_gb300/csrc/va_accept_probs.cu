@@ -45,6 +45,7 @@ typedef unsigned __int128 u128;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+static_assert(kWarps <= 32, "a warp scans one number per warp of the block");
 constexpr int kMaxCluster = 8;    // portable cluster size
 constexpr int kMinPerCta = 4096;  // entries below which a row is not split further
 constexpr int kSlots = 304;       // resident CTAs of this size: two on each of 152 SMs

@@ -32,6 +32,7 @@ using namespace sm100;
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
+static_assert(kWarps == 32, "a warp scans one number per warp of the block");
 constexpr int kMaxCluster = 8;  // portable cluster size
 constexpr int kBatch = 4;
 
