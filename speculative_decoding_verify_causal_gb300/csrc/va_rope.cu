@@ -51,7 +51,7 @@ __device__ __forceinline__ uint32_t div(uint32_t n, const FastDiv &f) { return (
 // ------------------------------------------------------------------------- rotary alone
 
 constexpr int kThreads = 128;
-constexpr int kUnroll = 2;      // heads whose loads a thread has in flight while it turns as many
+constexpr int kInFlight = 64;   // bytes that a thread has in flight while it turns as many
 constexpr int kHeads = 16;      // heads of a thread where there is work enough
 constexpr int kMinCtas = 2432;  // sixteen for each of 152 SMs
 
@@ -68,6 +68,7 @@ struct RopeParams {
     Tensor q, k;
     int q_heads, heads;      // heads of q, of q and k together
     int tokens;              // num_seqs * T
+    int head_dim;
     int head_chunk;          // heads per thread
     int units;               // of a head: those of the pairs, then the unrotated vectors
     int pair_units;
@@ -145,15 +146,15 @@ __device__ __forceinline__ V packed(const float (&x)[W]) {
 }
 
 // A unit is a piece of one head whose pairs are whole: a vector of W elements of each half, or one vector of neighbours (two
-// single elements where W is 1), or, past the pairs, one vector that is copied.  A thread has one unit of one token: it makes
+// single elements where W is 1), or, past the pairs, as many vectors that are copied.  A thread has one unit of one token: it makes
 // its (cos, sin) once, in registers, and turns that unit of head_chunk heads with them.  No shared memory and no barrier: a
 // first form that made a token's (cos, sin) in shared memory for all its heads issued twice the instructions and waited on
-// the table's bank conflicts (32,768 tokens, 40 heads of 128, bf16: 123.5 us; this one 104.4 us, 6.4 TB/s of the 671 MB).
+// the table's bank conflicts (32,768 tokens, 40 heads of 128, bf16: 123.5 us; this one 103.6 us, 6.5 TB/s).
 template <int TYPE, int W, bool ADJACENT>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
     using V = typename Raw<W * Elem<TYPE>::kBytes>::V;
     constexpr int kElem = Elem<TYPE>::kBytes;
-    constexpr bool kOne = ADJACENT && W > 1;      // one vector holds the pairs
+    constexpr bool kOne = ADJACENT && W > 1;  // one vector holds the pairs; a unit is one vector, else two
     constexpr int kPairs = kOne ? W / 2 : W;
     const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
     const uint32_t n = div(i, p.by_units), unit = i - n * p.units;
@@ -162,12 +163,13 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     const int b = (int)div(n, p.by_T), t = (int)n - b * (int)p.by_T.d;
     const bool pairs = (int)unit < p.pair_units;
     const int pair0 = kPairs * (int)unit;
-    const int64_t elem = pairs ? (ADJACENT ? 2 * pair0 : pair0) : 2 * P + W * ((int)unit - p.pair_units);
-    const int64_t off0 = elem * kElem, off1 = off0 + (ADJACENT ? W : P) * kElem;
+    const int elem = pairs ? (ADJACENT ? 2 * pair0 : pair0) : 2 * P + (kOne ? W : 2 * W) * ((int)unit - p.pair_units);
+    const int64_t off0 = (int64_t)elem * kElem, off1 = off0 + (pairs && !ADJACENT ? P : W) * kElem;
+    const bool two = !kOne && (pairs || elem + W < p.head_dim);
     const int h0 = blockIdx.y * p.head_chunk, h1 = min(p.heads, h0 + p.head_chunk);
     griddep_wait();
-    // heads h0 .. h1 - 1 of q and k, kAhead at a time
-    constexpr int kAhead = kOne ? 2 * kUnroll : kUnroll;
+    // heads h0 .. h1 - 1 of q and k, kAhead at a time: kInFlight bytes of each unit's vectors, eight heads at most
+    constexpr int kBytes = (kOne ? 1 : 2) * W * kElem, kAhead = kInFlight / kBytes < 8 ? kInFlight / kBytes : 8;
     V lo[kAhead], hi[kAhead];
     char *to[kAhead];
     auto load = [&](int h) {
@@ -180,7 +182,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
             const char *in = x.in + b * x.in_seq + t * x.in_token + g * x.in_head;
             to[u] = x.out + b * x.out_seq + t * x.out_token + g * x.out_head;
             lo[u] = *reinterpret_cast<const V *>(in + off0);
-            if (!kOne && pairs) hi[u] = *reinterpret_cast<const V *>(in + off1);
+            if (two) hi[u] = *reinterpret_cast<const V *>(in + off1);
         }
     };
     load(h0);  // under way while the angles are computed
@@ -218,9 +220,10 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
                     second = nb;
                 }
                 x[u] = packed<TYPE, W, V>(x0);
-                if (!kOne) *reinterpret_cast<V *>(out[u] + off1) = packed<TYPE, W, V>(x1);
+                if (!kOne) y[u] = packed<TYPE, W, V>(x1);
             }
             *reinterpret_cast<V *>(out[u] + off0) = x[u];
+            if (two) *reinterpret_cast<V *>(out[u] + off1) = y[u];
         }
     }
 }
@@ -235,6 +238,7 @@ template <int TYPE>
 cudaError_t launch_rope(const RopeParams &p, int w, dim3 grid, cudaStream_t s) {
     constexpr int kWide = 16 / Elem<TYPE>::kBytes;
     return w == kWide ? launch_rope_w<TYPE, kWide>(p, grid, s)
+           : w == 4   ? launch_rope_w<TYPE, 4>(p, grid, s)
            : w == 2   ? launch_rope_w<TYPE, 2>(p, grid, s)
                       : launch_rope_w<TYPE, 1>(p, grid, s);
 }
@@ -342,7 +346,7 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 // with fewer registers, 41.1).  In CTAs of 64 threads, since 128 leave a sixth of the SMs a CTA short here.
 template <int D, int DT, int PAIRING>
 __global__ void __launch_bounds__(kAppendThreads, 8) rope_append_kernel(const __grid_constant__ RopeAppendParams p) {
-    constexpr int kLanes = D / kE, kAhead = 3;
+    constexpr int kLanes = D / kE, kAhead = PAIRING == kApart ? 1 : 3;
     const int P = p.rope.num_pairs;
     const int lane = threadIdx.x & 31, sub = lane % kLanes;
     const int n = (blockIdx.x * kAppendThreads + threadIdx.x) / kLanes;
@@ -391,6 +395,14 @@ __global__ void __launch_bounds__(kAppendThreads, 8) rope_append_kernel(const __
 #pragma unroll
         for (int j = 0; j < 8; ++j) cs[j] = !tail && pair_of(j) < P ? angle(pair_of(j)) : make_float2(1.f, 0.f);
     }
+    float2 each[PAIRING == kApart ? kE : 1];  // of every element
+    if (PAIRING == kApart) {
+#pragma unroll
+        for (int m = 0; m < kE; ++m) {
+            const int i = m < 8 ? e0 + m : e1 + m - 8;
+            each[PAIRING == kApart ? m : 0] = i < 2 * P ? angle(i < P ? i : i - P) : make_float2(1.f, 0.f);
+        }
+    }
     for (int base = from; base < to; base += kAhead) {
         uint4 raw0[kAhead], raw1[kAhead];
 #pragma unroll
@@ -433,7 +445,7 @@ __global__ void __launch_bounds__(kAppendThreads, 8) rope_append_kernel(const __
                     for (int m = 0; m < kE; ++m) {
                         const int i = m < 8 ? e0 + m : e1 + m - 8;
                         if (i < 2 * P && here) {
-                            const float2 r2 = angle(i < P ? i : i - P);
+                            const float2 r2 = each[m];
                             const float far = __uint_as_float((uint32_t)src[i < P ? i + P : i - P] << 16);
                             float &x = m < 8 ? x0[m & 7] : x1[m & 7];
                             x = fmaf(x, r2.x, i < P ? -far * r2.y : far * r2.y);
@@ -588,7 +600,7 @@ extern "C" int verify_attn_rope(const va_rope *rope, const va_positions *positio
     // the widest vector, up to 16 bytes, that every pointer, stride and part of the head is a multiple of
     const int P = rope->num_pairs;
     int w = 1;
-    for (int cand : {16 / bytes, 2}) {
+    for (int cand : {16 / bytes, 4, 2}) {
         bool ok = (rope->adjacent ? 2 * P : P) % cand == 0 && (head_dim - 2 * P) % cand == 0;
         for (const va_heads *x : all)
             ok = ok && (!x || (va::aligned(x->data, (uintptr_t)cand * bytes) && va::strides_ok(*x, num_seqs, T, cand)));
@@ -613,8 +625,10 @@ extern "C" int verify_attn_rope(const va_rope *rope, const va_positions *positio
     p.q_heads = q->num_heads;
     p.heads = heads;
     p.tokens = (int)tokens;
-    p.pair_units = rope->adjacent && w > 1 ? 2 * P / w : P / w;
-    p.units = p.pair_units + (head_dim - 2 * P) / w;
+    const bool one = rope->adjacent && w > 1;  // vectors of a unit: one, else two
+    p.head_dim = head_dim;
+    p.pair_units = one ? 2 * P / w : P / w;
+    p.units = p.pair_units + ((head_dim - 2 * P) / w + (one ? 0 : 1)) / (one ? 1 : 2);
     p.inverse_sign = inverse ? -1.f : 1.f;
     if (tokens * p.units > (1LL << 30)) return VA_ERR_INVALID_ARGUMENT;
     // heads of a thread: kHeads, fewer while the grid is below kMinCtas

@@ -78,6 +78,9 @@ ROPE_CASES = [  # B, T, Hq, Hk, D, rotary_dim, sections, layout, pairing
     (2, 33, 2, 2, 128, 128, [16, 24, 24], "blocked", "half"),
     (1, 2, 3, 1, 515, 256, [128], "blocked", "adjacent"),
     (1, 130, 2, 1, 24, 24, [3, 3, 3, 3], "dealt", "half"),
+    (2, 9, 19, 3, 72, 72, [18, 18], "blocked", "half"),       # 8-byte vectors of 16-bit types
+    (1, 9, 19, 3, 88, 40, None, "blocked", "half"),           # an odd number of vectors past the pairs
+    (1, 9, 19, 3, 90, 36, None, "blocked", "adjacent"),
 ]
 
 
@@ -436,15 +439,17 @@ def test_accept_probs(va, B, T, V, dtype, model):
         assert 0 < n.sum() < B * T  # acceptances and rejections both occur
 
 
-def test_accept_probs_truncated_rows_ragged_counts_and_strides(va):
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("top", [0, 20])
+def test_accept_probs_truncated_rows_ragged_counts_and_strides(va, dtype, top):
     B, T, V = 9, 4, 3001
-    p, q, d, ua, ue = probs(7, B, T, V, torch.float32, True, top=20)
+    p, q, d, ua, ue = probs(7, B, T, V, dtype, True, top=top)
     lens = torch.tensor([0, 1, 2, 3, 4, 5, -1, 100, 2], dtype=torch.int32)
     check_accept(va, p, q, d, ua, ue, lens)
     # rows of a padded vocabulary (aligned and not), and positions before sequences
-    for pad in (5, 7):
-        wide_p = torch.rand(B, T + 1, V + pad).cuda()
-        wide_q = torch.rand(T, B, V + pad).cuda().transpose(0, 1)
+    for pad in (1, 5, 7):
+        wide_p = torch.rand(B, T + 1, V + pad).to(dtype).cuda()
+        wide_q = torch.rand(T, B, V + pad).to(dtype).cuda().transpose(0, 1)
         wide_p[..., :V], wide_q[..., :V] = p.cuda(), q.cuda()
         check_accept(va, p, q, d, ua, ue, lens, stored=(wide_p[..., :V], wide_q[..., :V]))
 
