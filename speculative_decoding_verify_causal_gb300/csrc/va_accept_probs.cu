@@ -27,9 +27,11 @@
 // contiguous run per warp, and the CTAs exchange their sums through
 // distributed shared memory.  The CTA whose slice holds the threshold reads the
 // one run that holds it again (from L2), eight entries a thread, and finds the
-// entry (one warp alone took 7 us longer at 2,374 entries a run).  Bound: the bytes of one row of p
-// (and one of q) per sequence for a large batch; for one sequence the chain of
-// dependent reads (draft, its probabilities, the row) and two cluster barriers.
+// entry (one warp alone took 4 us longer at 2,374 entries a run).  Bound: for one
+// sequence (7.2 us) the chain of dependent reads, draft, its probabilities, the
+// row, the run, with the cluster's barrier between them; for 64 (18.5 us, 61 MB
+// from DRAM) that chain, about 11 us of it, and 5 to 7 us of sums, which run at
+// the memory's rate.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -46,10 +48,12 @@ typedef unsigned __int128 u128;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 static_assert(kWarps <= 32, "a warp scans one number per warp of the block");
-constexpr int kMaxCluster = 8;    // portable cluster size
-constexpr int kMinPerCta = 4096;  // entries below which a row is not split further
-constexpr int kSlots = 304;       // resident CTAs of this size: two on each of 152 SMs
-
+// CTAs of a sequence: the most, up to the portable cluster size, that keep all sequences' CTAs resident together (two of this
+// size on each of 152 SMs) and kMinPerCta entries in each.  64 sequences of 151,936 entries: 4 CTAs 19.4 us, 2 23.2, 8 (two
+// waves) 27.7; one sequence: 8 CTAs 7.7 us, 4 8.7, 1 18.7; one of 8,000: 4 CTAs 6.2 us, 1 7.1, 8 5.9.
+constexpr int kMaxCluster = 8;
+constexpr int kMinPerCta = 2048;
+constexpr int kSlots = 304;
 
 struct ProbsParams {
     const void *p, *q;  // q null: point mass
