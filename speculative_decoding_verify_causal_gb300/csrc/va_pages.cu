@@ -36,6 +36,10 @@ static_assert(kWarps == 32, "a warp scans one number per warp of the block");
 constexpr int kMaxCluster = 8;  // portable cluster size
 constexpr int kBatch = 4;
 
+// The kernel behind this one on the stream, the copies, may take its places on the other SMs now; it waits there for this
+// one's end (griddep_wait), which then costs no launch.
+__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 struct Header {
     int jobs;    // pages to copy
     int movers;  // compaction: pages that move
@@ -159,12 +163,11 @@ __device__ int push_marked(const Pool &p, uint32_t *mask, int nf, unsigned long 
     int mine = 0;
     for (int w = threadIdx.x; w < words; w += kThreads) mine += __popc(mask[w]);
     int sum, total;
-    block_scan(mine, sum);
-    int at = nf + cluster_scan(sum, total, slots);
+    int before = block_scan(mine, sum);  // each word's own where a thread has one word
+    int at = nf + cluster_scan(sum, total, slots), chunk = sum;
     for (int base = 0; base < words && sum > 0; base += kThreads) {
         const int w = base + threadIdx.x;
-        int chunk;
-        const int before = block_scan(w < words ? __popc(mask[w]) : 0, chunk);
+        if (words > kThreads) before = block_scan(w < words ? __popc(mask[w]) : 0, chunk);
         word_pre[threadIdx.x] = at + before;
         at += chunk;
         __syncthreads();
@@ -211,6 +214,7 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const Pool p, const in
     for (int w = threadIdx.x; w < (1 << p.slice_bits); w += kThreads) mask[w] = 0;
     if (threadIdx.x == 0) s_taken = s_copies = 0;
     cluster_arrive();  // the bitmap is clear, and this CTA runs
+    griddep_launch();
     griddep_wait();
     if (me == 0) p.head->jobs = 0;
     int nf = free_count(p);
@@ -322,6 +326,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const Pool p, const int3
     for (int b = threadIdx.x; b < p.B; b += kThreads) claim[b] = F;
     if (threadIdx.x == 0) s_taken = 0;
     __syncthreads();
+    griddep_launch();
     griddep_wait();
     const int nf = free_count(p);
     // the first fork of the call that wants a slot has it
@@ -406,6 +411,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const Pool p) {
     const bool first = cluster_rank() == 0;
     const int64_t most = (int64_t)p.stride * VA_PAGE_SIZE;
     cluster_arrive();  // this CTA runs
+    griddep_launch();
     griddep_wait();
     if (me == 0) p.head->movers = 0;
     // which pages are held, 32 to a word, and how many before each CTA's words
