@@ -567,8 +567,8 @@ int verify_attn_accept_probs(const va_rows *target_probs, const va_rows *draft_p
  *                                        block_table_stride], a sequence
  *                                        index outside [0, num_seqs), a fork
  *                                        into a slot that is not empty or
- *                                        that an earlier fork of the call has
- *                                        taken: not carried out
+ *                                        that an earlier fork of the call
+ *                                        names: not carried out
  *                   VA_PAGES_BAD_COUNT   a held page with no references, or a
  *                                        num_free that disagrees with them
  *     buffers     host array of the pools that the pages lie in: page p of

@@ -1,6 +1,6 @@
 // Rotary positions with several axes: q and k of a batch rotated in one
 // launch (rope_kernel), or rotated and appended to the paged cache in one
-// launch (append_kernel).  Definitions in verify_attn.h.
+// launch (rope_append_kernel).  Definitions in verify_attn.h.
 //
 // Angles.  A binary32 product position * frequency loses the angle: at
 // position 200,000 its last bit is 1/64 of a radian.  turn[i] holds the part
@@ -150,10 +150,10 @@ __device__ __forceinline__ V packed(const float (&x)[W]) {
 }
 
 // A unit is a piece of one head whose pairs are whole: a vector of W elements of each half, or one vector of neighbours (two
-// single elements where W is 1), or, past the pairs, as many vectors that are copied.  A thread has one unit of one token: it makes
-// its (cos, sin) once, in registers, and turns that unit of head_chunk heads with them.  No shared memory and no barrier: a
+// single elements where W is 1), or, past the pairs, as many vectors that are copied.  A thread has one unit of one token: it
+// makes its (cos, sin) once, in registers, and turns that unit of head_chunk heads with them.  No shared memory and no barrier: a
 // first form that made a token's (cos, sin) in shared memory for all its heads issued twice the instructions and waited on
-// the table's bank conflicts (32,768 tokens, 40 heads of 128, bf16: 123.5 us; this one 103.6 us, 6.5 TB/s).
+// the table's bank conflicts (32,768 tokens, 40 heads of 128, bf16: 123.5 us; this one 104.4 us, 6.4 TB/s).
 template <int TYPE, int W, bool ADJACENT>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
     using V = typename Raw<W * Elem<TYPE>::kBytes>::V;
@@ -674,6 +674,10 @@ extern "C" int verify_attn_rope_append(const va_rope *rope, const va_positions *
     // rows move as 16-byte (bf16 in) / 8-byte (codes out) units
     for (const va_heads *x : {q, k_new, v_new})
         if (x && (!x->data || !va::aligned(x->data, 16) || !va::strides_ok(*x, num_seqs, T, 8))) return VA_ERR_INVALID_ARGUMENT;
+    if (q && q_out == q->data) {  // in place: q has to lie as q_out does
+        const va_heads whole{q_out, (int64_t)T * q->num_heads * head_dim, (int64_t)q->num_heads * head_dim, head_dim, q->num_heads};
+        if (!va::same_strides(*q, whole, num_seqs, T)) return VA_ERR_INVALID_ARGUMENT;
+    }
     if (!va::aligned(k_pages, 16) || !va::aligned(v_pages, 16) || (q_out && !va::aligned(q_out, 16)) ||
         !va::aligned(block_table, 4) || !va::aligned(seq_lens, 4) || !va::aligned(k_scale, 4) ||
         !va::aligned(v_scale, 4) || !va::aligned(flags, 4))

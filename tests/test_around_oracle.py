@@ -145,6 +145,7 @@ def _append(**change):
     (dict(table=None), -1), (dict(lens=None), -1), (dict(B=0), -1), (dict(T=0), -1), (dict(stride=0), -1),
     (dict(pages=-1), -1), (dict(D=96), -2), (dict(dtype=5), -2), (dict(dtype=-1), -2),
     (dict(rotary=128), -1),   # wider than the head
+    (dict(q=_heads(8192, 512, 256, 64), q_out=8192), -1),   # in place where q does not lie as q_out does
     (dict(v=_heads(4096, 256, 128, 64, n=1)), -1), (dict(q=_heads(4096, 256, 128, 64, n=0)), -1),
     (dict(k=_heads(4104, 256, 128, 64)), -1), (dict(v=_heads(4096, 256, 132, 64)), -1), (dict(q_out=8200), -1),
     (dict(k_pages=4104), -1), (dict(table=4098), -1), (dict(flags=4098), -1), (dict(pos=va._Positions(0, 0, 0, 1)), -1),

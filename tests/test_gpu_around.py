@@ -854,6 +854,26 @@ def test_steps_on_a_side_stream_and_captured_are_the_eager_ones(va):
         assert torch.equal(a, b)
 
 
+def test_two_steps_at_once_on_two_streams(va):
+    """Pools of their own on streams of their own: nothing is shared."""
+    steps = [Step(va, seed=s) for s in (0, 1)]
+    alone = [Step(va, seed=s) for s in (0, 1)]
+    for st in alone:
+        for _ in range(10):
+            st.run()
+    want = [st.state() for st in alone]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        for st, s in zip(steps, streams):
+            with torch.cuda.stream(s):
+                st.run()
+    for st, w in zip(steps, want):
+        for a, b in zip(st.state(), w):
+            assert torch.equal(a, b)
+
+
 def test_outputs_made_on_a_given_stream_belong_to_it(va):
     """Without outputs given, the call makes them on the stream it runs on: work that is still queued on the current
     stream cannot share their memory."""
