@@ -41,8 +41,8 @@ constexpr int kBatch = 4;
 __device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 struct Header {
-    int jobs;    // pages to copy
-    int movers;  // compaction: pages that move
+    int jobs;  // pages to copy
+    int held;  // compaction: held pages
     int pad[14];
 };
 
@@ -52,9 +52,9 @@ struct Pool {
     int slice_bits;  // of the bitmap's 32-bit words: each CTA has 2^slice_bits of them
     // workspace
     Header *head;
-    int32_t *map;     // [P]
-    int32_t *movers;  // [P]
-    int2 *jobs;       // [P] (source, destination)
+    int32_t *map;     // [P] compaction: -1 for a free page, a moving page's place among the movers
+    int32_t *movers;  // [P] compaction: the pages that move, the last one first
+    int2 *jobs;       // [P] (source, destination); compaction: the destinations, in order
 };
 
 __host__ __device__ inline int mask_words(int P) { return (P + 31) / 32; }
@@ -400,20 +400,18 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const Pool p, const int3
     }
 }
 
+// Which pages move and where to.  What follows from that, counts, lists and tables, is done beside the copies.
 __global__ void __launch_bounds__(kThreads) compact_kernel(const Pool p) {
     extern __shared__ int smem[];
-    int *pre = smem;
-    uint32_t *mask = reinterpret_cast<uint32_t *>(pre + p.B + 1);
+    uint32_t *mask = reinterpret_cast<uint32_t *>(smem);
     __shared__ int word_pre[kThreads];
     __shared__ unsigned long long slots[kMaxCluster];
-    const int me = cluster_thread(), all = cluster_threads();
+    const int me = cluster_thread();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const bool first = cluster_rank() == 0;
-    const int64_t most = (int64_t)p.stride * VA_PAGE_SIZE;
     cluster_arrive();  // this CTA runs
     griddep_launch();
     griddep_wait();
-    if (me == 0) p.head->movers = 0;
+    if (me == 0) p.head->jobs = 0;
     // which pages are held, 32 to a word, and how many before each CTA's words
     const int word0 = (int)cluster_rank() << p.slice_bits, words = max(0, min(1 << p.slice_bits, mask_words(p.P) - word0));
     int mine = 0;
@@ -433,17 +431,11 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const Pool p) {
             }
         }
     }
-    for (int b = threadIdx.x; b < p.B; b += kThreads) {
-        const int L = p.lens[b];
-        const bool ok = L >= 0 && L <= most;
-        if (!ok && first) flag(p, VA_PAGES_BAD_REQUEST);
-        pre[b] = ok ? blocks_of(L) : 0;
-    }
-    prefix_sums(pre, p.B);
     int sum, n;
     block_scan(mine, sum);
     cluster_wait();
     int before = cluster_scan(sum, n, slots);  // n pages are held
+    if (me == 0) p.head->held = n;
     // free places below n, held pages from n on
     for (int base = 0; base < words; base += kThreads) {
         const int w = base + threadIdx.x;
@@ -456,25 +448,30 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const Pool p) {
             const uint32_t live = mask[v];
             const int page = 32 * (word0 + v) + lane;
             const int below = word_pre[v - base] + __popc(live & ((1u << lane) - 1));  // held pages below this one
-            if (page == n) p.head->movers = page - below;
-            if (page < p.P) {
-                if (live >> lane & 1) {
-                    p.map[page] = page;
-                    if (page >= n) p.movers[n - 1 - below] = page;  // counted from the last held page
-                } else {
-                    p.map[page] = -1;
-                    if (page < n) p.jobs[page - below].y = page;
-                }
+            if (page >= p.P) continue;
+            if (page == n) p.head->jobs = page - below;  // as many move as there are free places below n
+            if (live >> lane & 1) {
+                const int last = n - 1 - below;  // counted from the last held page
+                p.map[page] = page < n ? 0 : last;
+                if (page >= n) p.movers[last] = page;
+            } else {
+                p.map[page] = -1;
+                if (page < n) p.jobs[page - below].y = page;
             }
         }
         __syncthreads();
     }
-    cluster_sync();
-    const int M = n < p.P ? __ldcg(&p.head->movers) : 0;
-    for_items(me, all, M, [&](int k) { return make_int2(__ldcg(p.movers + M - 1 - k), __ldcg(&p.jobs[k].y)); },
-              [&](int k, int2 move) {
-                  p.jobs[k].x = move.x;
-                  p.map[move.x] = move.y;
+}
+
+// The rest of a compaction, by the first kSideCtas CTAs of the copy kernel: the k-th mover from below goes to destination k,
+// and is the (M - 1 - k)-th from the last.
+constexpr int kSideCtas = 8;
+__device__ void compact_rest(const Pool &p, int *pre) {
+    const int me = blockIdx.x * kThreads + threadIdx.x, all = kSideCtas * kThreads;
+    const int64_t most = (int64_t)p.stride * VA_PAGE_SIZE;
+    const int M = p.head->jobs, n = p.head->held;
+    for_items(me, all, M, [&](int k) { return make_int2(p.movers[M - 1 - k], p.jobs[k].y); },
+              [&](int, int2 move) {
                   p.ref[move.y] = p.ref[move.x];
                   p.ref[move.x] = 0;
               });
@@ -482,10 +479,14 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const Pool p) {
     if (me == 0) {
         if (*p.num_free != p.P - n) flag(p, VA_PAGES_BAD_COUNT);
         *p.num_free = p.P - n;
-        p.head->jobs = M;
     }
-    cluster_sync();
-    // the tables
+    for (int b = threadIdx.x; b < p.B; b += kThreads) {
+        const int L = p.lens[b];
+        const bool ok = L >= 0 && L <= most;
+        if (!ok && blockIdx.x == 0) flag(p, VA_PAGES_BAD_REQUEST);
+        pre[b] = ok ? blocks_of(L) : 0;
+    }
+    prefix_sums(pre, p.B);
     const int entries = pre[p.B];
     for (int base = me; base < entries; base += kBatch * all) {
         int32_t *at[kBatch];
@@ -500,13 +501,13 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const Pool p) {
         }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u)
-            if (base + u * all < entries && in_pool(p, page[u])) to[u] = __ldcg(p.map + page[u]);
+            if (base + u * all < entries && in_pool(p, page[u])) to[u] = p.map[page[u]];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             if (base + u * all >= entries) continue;
             if (!in_pool(p, page[u])) flag(p, VA_PAGES_BAD_ENTRY);
             else if (to[u] < 0) flag(p, VA_PAGES_BAD_COUNT);
-            else if (to[u] != page[u]) *at[u] = to[u];
+            else if (page[u] >= n) *at[u] = p.jobs[M - 1 - to[u]].y;
         }
     }
 }
@@ -525,20 +526,22 @@ struct CopyParams {
     uint32_t page_16[kMaxBuffers];         // page size in 16-byte pieces
     uint32_t unit_begin[kMaxBuffers + 1];  // units of one page in the buffers before
     int buffers;
+    const int32_t *movers;  // compaction: the sources, the last one first
 };
 
 // A warp copies one unit at a time: (page pair, buffer, 2 KB piece of the page).  Units are dealt round the CTAs, so that
 // a few pages spread over all SMs.
-__global__ void __launch_bounds__(kCopyThreads, 2) copy_kernel(const __grid_constant__ CopyParams p) {
-    griddep_wait();
+template <bool COMPACT>
+__device__ __forceinline__ void copy_pages(const CopyParams &p, uint32_t cta, uint32_t ctas) {
     const int jobs = p.head->jobs;
     const int lane = threadIdx.x & 31;
     const uint32_t units = p.unit_begin[p.buffers];
-    const uint32_t warps = gridDim.x * (kCopyThreads / 32), mine = (threadIdx.x >> 5) * gridDim.x + blockIdx.x;
+    const uint32_t warps = ctas * (kCopyThreads / 32), mine = (threadIdx.x >> 5) * ctas + cta;
     const uint32_t step_job = warps / units, step_unit = warps % units;
     uint32_t job = mine / units, unit = mine % units;
     while (job < (uint32_t)jobs) {
-        const int2 pages = p.jobs[job];
+        int2 pages = p.jobs[job];
+        if (COMPACT) pages.x = p.movers[jobs - 1 - job];
         int lo = 0, hi = p.buffers;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -565,6 +568,20 @@ __global__ void __launch_bounds__(kCopyThreads, 2) copy_kernel(const __grid_cons
             ++job;
         }
     }
+}
+
+__global__ void __launch_bounds__(kCopyThreads, 2) copy_kernel(const __grid_constant__ CopyParams p) {
+    griddep_wait();
+    copy_pages<false>(p, blockIdx.x, gridDim.x);
+}
+
+// A compaction's copies, and in the first CTAs its counts, lists and tables (not again in the launches of further buffers).
+__global__ void __launch_bounds__(kCopyThreads, 2)
+    compact_copy_kernel(const __grid_constant__ CopyParams p, const __grid_constant__ Pool pool, int side) {
+    extern __shared__ int smem[];
+    griddep_wait();
+    if ((int)blockIdx.x < side) compact_rest(pool, smem);
+    else if (p.buffers) copy_pages<true>(p, blockIdx.x - side, gridDim.x - side);
 }
 
 // ------------------------------------------------------------------------- host
@@ -648,19 +665,35 @@ cudaError_t launch_book(void (*kernel)(KArgs...), size_t smem, cudaStream_t s, A
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
+CopyParams copy_params(const va_page_pool *v, const Pool &p, int done) {
+    CopyParams c{};
+    c.head = p.head;
+    c.jobs = p.jobs;
+    c.movers = p.movers;
+    c.buffers = std::min(kMaxBuffers, v->num_buffers - done);
+    for (int i = 0; i < c.buffers; ++i) {
+        const va_page_buffer &b = v->buffers[done + i];
+        c.data[i] = static_cast<char *>(b.data);
+        c.page_16[i] = (uint32_t)(b.page_bytes / 16);
+        c.unit_begin[i + 1] = c.unit_begin[i] + (uint32_t)((b.page_bytes + kUnit - 1) / kUnit);
+    }
+    return c;
+}
+
 cudaError_t launch_copies(const va_page_pool *v, const Pool &p, cudaStream_t s) {
     for (int done = 0; done < v->num_buffers; done += kMaxBuffers) {
-        CopyParams c{};
-        c.head = p.head;
-        c.jobs = p.jobs;
-        c.buffers = std::min(kMaxBuffers, v->num_buffers - done);
-        for (int i = 0; i < c.buffers; ++i) {
-            const va_page_buffer &b = v->buffers[done + i];
-            c.data[i] = static_cast<char *>(b.data);
-            c.page_16[i] = (uint32_t)(b.page_bytes / 16);
-            c.unit_begin[i + 1] = c.unit_begin[i] + (uint32_t)((b.page_bytes + kUnit - 1) / kUnit);
-        }
-        const cudaError_t e = launch_pdl(copy_kernel, dim3(kCopyCtas), dim3(kCopyThreads), 0, s, c);
+        const cudaError_t e = launch_pdl(copy_kernel, dim3(kCopyCtas), dim3(kCopyThreads), 0, s, copy_params(v, p, done));
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+cudaError_t launch_compact_copies(const va_page_pool *v, const Pool &p, cudaStream_t s) {
+    const size_t smem = sizeof(int) * ((size_t)p.B + 1);
+    for (int done = 0; done == 0 || done < v->num_buffers; done += kMaxBuffers) {
+        const int side = done == 0 ? kSideCtas : 0;
+        const cudaError_t e = launch_pdl(compact_copy_kernel, dim3(v->num_buffers ? kCopyCtas : side), dim3(kCopyThreads),
+                                         side ? smem : 0, s, copy_params(v, p, done), p, side);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -713,8 +746,8 @@ extern "C" int verify_attn_pages_compact(const va_page_pool *pool, void *stream)
     if (const int rc = va::check(pool, &p)) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     va::set_slices(p);
-    const size_t smem = sizeof(int) * ((size_t)p.B + 1 + ((size_t)1 << p.slice_bits));
+    const size_t smem = sizeof(int) * ((size_t)1 << p.slice_bits);
     cudaError_t e = va::launch_book(va::compact_kernel, smem, s, p);
-    if (e == cudaSuccess) e = va::launch_copies(pool, p, s);
+    if (e == cudaSuccess) e = va::launch_compact_copies(pool, p, s);
     return va::done(e);
 }

@@ -744,9 +744,18 @@ def test_pages_many_buffers(va):
     for b, w in zip(buffers, want):
         w[2] = w[1]
         assert torch.equal(b, w)
+    va.verify_attn_pages_resize(pool, cuda(np.array([0, -1], np.int32)))
+    va.verify_attn_pages_compact(pool)  # pages 0 and 2, shared and copied, become 0 and 1
+    assert pool.block_table[1, :2].tolist() == [0, 1] and pool.num_free.item() == P - 2
+    for b, w in zip(buffers, want):
+        w[1] = w[2]
+        assert torch.equal(b, w)
     bare = va.PagePool.create(P, 2, 4, [])
     va.verify_attn_pages_resize(bare, cuda(np.array([20, 40], np.int32)))
     assert bare.num_free.item() == P - 5
+    va.verify_attn_pages_resize(bare, cuda(np.array([0, 40], np.int32)))
+    va.verify_attn_pages_compact(bare)
+    assert bare.block_table[1, :3].tolist() == [2, 0, 1] and bare.ref_count.tolist() == [1] * 3 + [0] * (P - 3)
 
 
 def test_page_pool_argument_errors(va):
