@@ -59,7 +59,11 @@ struct Pool {
 
 __host__ __device__ inline int mask_words(int P) { return (P + 31) / 32; }
 __device__ __forceinline__ int blocks_of(int len) { return (int)(((unsigned)len + VA_PAGE_SIZE - 1) / VA_PAGE_SIZE); }
-__device__ __forceinline__ int cluster_thread() { return (int)cluster_rank() * kThreads + threadIdx.x; }
+// Threads are counted warp by warp round the CTAs, so that what a round leaves over spreads over all of them.
+__device__ __forceinline__ int spread_thread(int cta, int ctas) {
+    return (((int)threadIdx.x >> 5) * ctas + cta) * 32 + ((int)threadIdx.x & 31);
+}
+__device__ __forceinline__ int cluster_thread() { return spread_thread((int)cluster_rank(), (int)cluster_size()); }
 __device__ __forceinline__ int cluster_threads() { return (int)cluster_size() * kThreads; }
 __device__ __forceinline__ void flag(const Pool &p, int bit) {
     if (p.flags) atomicOr(p.flags, bit);
@@ -467,7 +471,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const Pool p) {
 // and is the (M - 1 - k)-th from the last.
 constexpr int kSideCtas = 8;
 __device__ void compact_rest(const Pool &p, int *pre) {
-    const int me = blockIdx.x * kThreads + threadIdx.x, all = kSideCtas * kThreads;
+    const int me = spread_thread(blockIdx.x, kSideCtas), all = kSideCtas * kThreads;
     const int64_t most = (int64_t)p.stride * VA_PAGE_SIZE;
     const int M = p.head->jobs, n = p.head->held;
     for_items(me, all, M, [&](int k) { return make_int2(p.movers[M - 1 - k], p.jobs[k].y); },
