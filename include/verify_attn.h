@@ -574,7 +574,8 @@ int verify_attn_accept_probs(const va_rows *target_probs, const va_rows *draft_p
  *     buffers     host array of the pools that the pages lie in: page p of
  *                 buffer i is page_bytes bytes at data + p * page_bytes (the K
  *                 pages, V pages and scales of every layer; 16-byte aligned,
- *                 page_bytes a multiple of 16); all are copied alike
+ *                 page_bytes a multiple of 16, at most 2^30); all are copied
+ *                 alike
  *     workspace   at least verify_attn_pages_workspace_bytes(num_seqs,
  *                 num_pages) bytes, 16-byte aligned; needs no initialisation
  * A pool starts with ref_count and seq_lens 0, free_list any permutation of
