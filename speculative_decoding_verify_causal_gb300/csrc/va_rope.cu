@@ -374,10 +374,13 @@ __global__ void __launch_bounds__(kAppendThreads, 8) rope_append_kernel(const __
                                     : p.v + b * p.v_seq + t * p.v_token + (row - p.Hq - p.Hkv) * p.v_head;
     };
     const int place = p.seq_lens[b] - p.T + t;
+    int at[VA_ROPE_MAX_AXES];  // the token's positions
+#pragma unroll
+    for (int a = 0; a < VA_ROPE_MAX_AXES; ++a)
+        at[a] = !p.pos ? place : a < p.rope.num_axes ? p.pos[a * p.pos_axis + b * p.pos_seq + t * p.pos_token] : 0;
     auto angle = [&](int pair) {
         const int axis = p.rope.axis[pair];
-        const int pos = p.pos ? p.pos[axis * p.pos_axis + b * p.pos_seq + t * p.pos_token] : place;
-        return turned(p.rope.turn[pair], pos, p.rope.scale);
+        return turned(p.rope.turn[pair], axis < 2 ? (axis ? at[1] : at[0]) : (axis == 2 ? at[2] : at[3]), p.rope.scale);
     };
     uint4 next0[kAhead], next1[kAhead];
     auto load = [&](int row) {
