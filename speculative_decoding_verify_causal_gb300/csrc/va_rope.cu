@@ -36,6 +36,40 @@ __device__ __forceinline__ float2 turned(uint64_t turn, int pos, float scale) {
     return r;
 }
 
+// (cos, sin) of the N neighbouring pairs from `first` on (a multiple of N) for a token at the positions `at`.  The description
+// is in the launch's arguments (16-byte aligned there), where reads that differ from lane to lane go one after the other: they
+// are made as wide as they can be (16 tokens of 24 + 8 heads of 256, a quarter turned: 3.6 -> 2.9 us).
+template <int N>
+__device__ __forceinline__ void angles(const va_rope &r, int first, const int (&at)[VA_ROPE_MAX_AXES], float2 *cs) {
+    uint64_t axes;
+    if constexpr (N == 8) axes = *reinterpret_cast<const uint64_t *>(r.axis + first);
+    else if constexpr (N == 4) axes = *reinterpret_cast<const uint32_t *>(r.axis + first);
+    else if constexpr (N == 2) axes = *reinterpret_cast<const uint16_t *>(r.axis + first);
+    else axes = r.axis[first];
+    uint64_t turns[N];
+    if constexpr (N == 1) {
+        turns[0] = r.turn[first];
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; j += 2) {
+            const ulonglong2 two = *reinterpret_cast<const ulonglong2 *>(r.turn + first + j);
+            turns[j] = two.x;
+            turns[j + 1] = two.y;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int axis = (int)(axes >> (8 * j)) & 255;
+        cs[j] = turned(turns[j], axis < 2 ? (axis ? at[1] : at[0]) : (axis == 2 ? at[2] : at[3]), r.scale);
+    }
+}
+
+// The positions of one token.
+__device__ __forceinline__ void positions(const va_rope &r, const int32_t *pos, int64_t stride, int (&at)[VA_ROPE_MAX_AXES]) {
+#pragma unroll
+    for (int a = 0; a < VA_ROPE_MAX_AXES; ++a) at[a] = a < r.num_axes ? pos[a * stride] : 0;
+}
+
 // n / d and n % d for 0 <= n < 2^31 with a multiplication (d >= 1)
 struct FastDiv {
     uint32_t d, mul, shift;
@@ -52,11 +86,13 @@ __device__ __forceinline__ uint32_t div(uint32_t n, const FastDiv &f) { return (
 
 constexpr int kThreads = 128;
 constexpr int kInFlight = 64;   // bytes that a thread has in flight while it turns as many
-// Heads of a thread: kHeads where there is work enough, fewer while the grid is below kMinCtas, two CTAs for each of 152 SMs.
+// Heads of a thread: kHeadBytes of them where there is work enough (8 heads of a 16-byte vector, 32 of a 4-byte one, whose
+// angles cost as much a pair: 46 us instead of 56 with 8 heads of 4-byte vectors, 16,384 tokens of 40 heads of 72), fewer
+// while the grid is below kMinCtas, two CTAs for each of 152 SMs.
 // Fewer heads share a thread's angles: with 912 and 2,432 CTAs wanted, 1,024 tokens of 40 heads of 128 took 6.4 and 8.1 us
 // instead of 5.5, 256 tokens 4.7 instead of 3.3.  With 16 heads a thread the grid of an image tower's 4,110 tokens is 1.06 waves
 // (16.5 us, with 8 heads 15.0); at 32,768 tokens 8 to 40 heads are within 1.5 %.
-constexpr int kHeads = 8;
+constexpr int kHeadBytes = 128;
 constexpr int kMinCtas = 304;
 
 struct Tensor {
@@ -65,7 +101,7 @@ struct Tensor {
     int64_t in_seq, in_token, in_head, out_seq, out_token, out_head;  // bytes
 };
 
-struct RopeParams {
+struct alignas(16) RopeParams {
     va_rope rope;
     const int32_t *pos;
     int64_t pos_axis, pos_seq, pos_token;
@@ -153,7 +189,7 @@ __device__ __forceinline__ V packed(const float (&x)[W]) {
 // single elements where W is 1), or, past the pairs, as many vectors that are copied.  A thread has one unit of one token: it
 // makes its (cos, sin) once, in registers, and turns that unit of head_chunk heads with them.  No shared memory and no barrier: a
 // first form that made a token's (cos, sin) in shared memory for all its heads issued twice the instructions and waited on
-// the table's bank conflicts (32,768 tokens, 40 heads of 128, bf16: 123.5 us; this one 104.4 us, 6.4 TB/s).
+// the table's bank conflicts (32,768 tokens, 40 heads of 128, bf16: 123.5 us; this one 104.2 us, 6.4 TB/s).
 template <int TYPE, int W, bool ADJACENT>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
     using V = typename Raw<W * Elem<TYPE>::kBytes>::V;
@@ -192,12 +228,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     load(h0);  // under way while the angles are computed
     float2 cs[kPairs];
     if (pairs) {
+        int at[VA_ROPE_MAX_AXES];
+        positions(p.rope, p.pos + b * p.pos_seq + t * p.pos_token, p.pos_axis, at);
+        angles<kPairs>(p.rope, pair0, at, cs);
 #pragma unroll
-        for (int j = 0; j < kPairs; ++j) {
-            const int pos = p.pos[p.rope.axis[pair0 + j] * p.pos_axis + b * p.pos_seq + t * p.pos_token];
-            cs[j] = turned(p.rope.turn[pair0 + j], pos, p.rope.scale);
-            cs[j].y *= p.inverse_sign;
-        }
+        for (int j = 0; j < kPairs; ++j) cs[j].y *= p.inverse_sign;
     }
     for (int h = h0; h < h1; h += kAhead) {
         V x[kAhead], y[kAhead];
@@ -249,7 +284,7 @@ cudaError_t launch_rope(const RopeParams &p, int w, dim3 grid, cudaStream_t s) {
 
 // ------------------------------------------------------------------------- rotary and append
 
-struct RopeAppendParams {
+struct alignas(16) RopeAppendParams {
     va_rope rope;
     const int32_t *pos;  // null: the token's place in its sequence
     int64_t pos_axis, pos_seq, pos_token;
@@ -266,7 +301,7 @@ struct RopeAppendParams {
 };
 
 // Rows of a thread: kRowsEach where there is work enough, fewer while the grid is below kAppendCtas, six CTAs for each of 152
-// SMs (320 tokens of 24 + 8 heads of 256, fp8: 5.9 us; with 304 CTAs wanted 9.6, with 9,728 7.6).
+// SMs (320 tokens of 24 + 8 heads of 256, fp8: 5.9 us then; with 304 CTAs wanted 9.6, with 9,728 7.6).
 constexpr int kRowsEach = 48;
 constexpr int kAppendThreads = 64;
 constexpr int kAppendCtas = 912;
@@ -347,8 +382,8 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 // one after the other, kAhead of them with their loads in flight.  Both elements of a pair are in the lane, whose 8 (cos, sin)
 // stay in registers: a rotation is two multiplications and two fused ones, two pairs an instruction, without shared memory,
 // barriers or exchange.  8,192 tokens of 32 + 16 heads of 128, bf16: with pairs spread over lanes (the other element by a
-// shuffle) 85 us, bound by its instructions; with a token's (cos, sin) in shared memory for all its rows 66 us; this one 35.4
-// us, 5.7 TB/s, bound by the loads in flight: three rows ahead in eight CTAs an SM (two rows 38.4 us; four 36.4; nine CTAs,
+// shuffle) 85 us, bound by its instructions; with a token's (cos, sin) in shared memory for all its rows 66 us; this one 34.4
+// us, 5.8 TB/s, bound by the loads in flight: three rows ahead in eight CTAs an SM (two rows 38.4 us; four 36.4; nine CTAs,
 // with fewer registers, 41.1).  In CTAs of 64 threads, since 128 leave a sixth of the SMs a CTA short here.
 template <int D, int DT, int PAIRING>
 __global__ void __launch_bounds__(kAppendThreads, 8) rope_append_kernel(const __grid_constant__ RopeAppendParams p) {
@@ -374,13 +409,12 @@ __global__ void __launch_bounds__(kAppendThreads, 8) rope_append_kernel(const __
                                     : p.v + b * p.v_seq + t * p.v_token + (row - p.Hq - p.Hkv) * p.v_head;
     };
     const int place = p.seq_lens[b] - p.T + t;
-    int at[VA_ROPE_MAX_AXES];  // the token's positions
-#pragma unroll
-    for (int a = 0; a < VA_ROPE_MAX_AXES; ++a)
-        at[a] = !p.pos ? place : a < p.rope.num_axes ? p.pos[a * p.pos_axis + b * p.pos_seq + t * p.pos_token] : 0;
+    int at[VA_ROPE_MAX_AXES] = {place, place, place, place};
+    if (p.pos) positions(p.rope, p.pos + b * p.pos_seq + t * p.pos_token, p.pos_axis, at);
     auto angle = [&](int pair) {
-        const int axis = p.rope.axis[pair];
-        return turned(p.rope.turn[pair], axis < 2 ? (axis ? at[1] : at[0]) : (axis == 2 ? at[2] : at[3]), p.rope.scale);
+        float2 cs;
+        angles<1>(p.rope, pair, at, &cs);
+        return cs;
     };
     uint4 next0[kAhead], next1[kAhead];
     auto load = [&](int row) {
@@ -400,9 +434,10 @@ __global__ void __launch_bounds__(kAppendThreads, 8) rope_append_kernel(const __
     if (to > p.Hq && place >= 0 && block < p.bt_stride) page = p.block_table[(size_t)b * p.bt_stride + block];
     const bool stored = here && page >= 0 && (p.num_pages == 0 || page < p.num_pages);
     float2 cs[8];
-    if (PAIRING != kApart && from < p.Hq + p.Hkv) {
+    if (PAIRING != kApart && from < p.Hq + p.Hkv && !tail) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) cs[j] = !tail && pair_of(j) < P ? angle(pair_of(j)) : make_float2(1.f, 0.f);
+        for (int j = 0; j < 8; j += 4)
+            if (pair_of(j) < P) angles<4>(p.rope, pair_of(j), at, cs + j);
     }
     float2 each[PAIRING == kApart ? kE : 1];  // of every element
     if (PAIRING == kApart) {
@@ -606,7 +641,7 @@ extern "C" int verify_attn_rope(const va_rope *rope, const va_positions *positio
             return VA_ERR_INVALID_ARGUMENT;
     }
     // the widest vector, up to 16 bytes, that every pointer, stride and part of the head is a multiple of (16,384 tokens of 40
-    // heads, bf16: 16 bytes 89-98 % of the copy rate, 4 bytes (head_dim 72, 36 of it turned) 57 %, 2 bytes (34 turned) 36 %)
+    // heads, bf16: 16 bytes 84-99 % of the copy rate, 4 bytes (head_dim 72, 36 of it turned) 60 %, 2 bytes (34 turned) 40 %)
     const int P = rope->num_pairs;
     int w = 1;
     for (int cand : {16 / bytes, 4, 2}) {
@@ -641,7 +676,8 @@ extern "C" int verify_attn_rope(const va_rope *rope, const va_positions *positio
     p.inverse_sign = inverse ? -1.f : 1.f;
     if (tokens * p.units > (1LL << 30)) return VA_ERR_INVALID_ARGUMENT;
     const unsigned ctas = (unsigned)((tokens * p.units + va::kThreads - 1) / va::kThreads);
-    const int chunks = std::min<long long>(heads, std::max<long long>((heads + va::kHeads - 1) / va::kHeads,
+    const int each = va::kHeadBytes / (w * bytes);
+    const int chunks = std::min<long long>(heads, std::max<long long>((heads + each - 1) / each,
                                                                       (va::kMinCtas + ctas - 1) / ctas));
     p.head_chunk = (heads + chunks - 1) / chunks;
     p.by_T = va::fast_div((uint32_t)T);
