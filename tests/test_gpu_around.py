@@ -311,10 +311,27 @@ def test_rope_append(va, case, kv_dtype):
 
 
 @pytest.mark.parametrize("kv_dtype", ["bf16", "fp8_e4m3", "int8", "int4", "int2"])
-def test_rope_append_at_position_zero_is_the_append(va, kv_dtype):
-    B, T, Hkv, D = 3, 4, 2, 128
-    pages, scale, bt, lens, P = cache_case(5, [9, 40, 4], T, Hkv, D, kv_dtype)
-    k, v = normal(12, B, T, Hkv, D, dtype=torch.bfloat16), normal(13, B, T, Hkv, D, dtype=torch.bfloat16)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_rope_append_at_position_zero_is_the_append(va, kv_dtype, D):
+    """Bit for bit, 2,000 rows of every size: ties, tiny and subnormal rows, huge ones, zeros, and rows of one value among
+    them, where a quotient that is not rounded as a division would show."""
+    B, T, Hkv = 3, 334, 2
+    pages, scale, bt, lens, P = cache_case(5, [400, 340, 334], T, Hkv, D, kv_dtype)
+    rng = np.random.default_rng(D)
+
+    def rows(seed):
+        x = normal(seed, B, T, Hkv, D).cpu().numpy().astype(np.float64)
+        x *= 2.0 ** rng.integers(-120, 100, (B, T, Hkv, 1))
+        x[0, 0], x[0, 1, 0], x[0, 2, 1] = 0.0, 2.5, 1e-40
+        x[0, 3] = np.linspace(-1, 1, D)
+        x[0, 4] = np.arange(D) - D // 2
+        x[0, 5, 0] = 3e38 * np.sign(x[0, 5, 0])
+        x[0, 6] = np.where(np.arange(D) % 7 == 0, 1.0, 2.0 ** -rng.integers(0, 30, D))
+        x[1, :200] = rng.integers(-448, 449, (200, Hkv, D)) / 2  # halves of codes: ties where the scale is a power of two
+        x[1, :200, :, 0] = 2.0 ** rng.integers(6, 9, (200, Hkv)) * rng.choice([1.75, 1.984375, 1.0])
+        return torch.from_numpy(np.clip(x, -3e38, 3e38).astype(np.float32)).to(torch.bfloat16).cuda()
+
+    k, v = rows(12), rows(13)
     spec = va.verify_attn_rope_spec(D)
     zero = torch.zeros(1, B, T, dtype=torch.int32, device="cuda")
     out, (kp, vp), (ks, vs), _ = run_append(va, spec, zero, None, k, v, pages, scale, bt, lens, kv_dtype)
