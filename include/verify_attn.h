@@ -622,9 +622,22 @@ size_t verify_attn_pages_workspace_bytes(int num_seqs, int num_pages);
  *      a page are refused.
  *   3. Shared pages that all their holders replaced in step 2 are then given
  *      back, in ascending order.
- * So the call after a verify step is new_lens[b] = accepted length + the next
- * block's tokens. */
+ * A growing sequence keeps all of its old tokens: its next tokens go from its
+ * old length on, and only the page that they start in is made its own.  Tokens
+ * that will be written over below that length, the rejected drafts of a verify
+ * step, have to be cut off first, by verify_attn_pages_resize_ex or a call of
+ * their own: they may lie in full pages that a fork shares. */
 int verify_attn_pages_resize(const va_page_pool *pool, const int32_t *new_lens, void *stream);
+
+/* The same with the sequences first cut back to kept_lens [num_seqs] (device;
+ * each in [0, seq_lens[b]], else VA_PAGES_BAD_REQUEST and the sequence is left
+ * alone; not read where new_lens is negative; NULL: all is kept).  The result
+ * is that of two calls of verify_attn_pages_resize, to min(kept, new) and then
+ * to new.  A sequence that finds the list too short (VA_PAGES_EXHAUSTED) stays
+ * cut back.  So the call after a verify step is kept_lens[b] = accepted length,
+ * new_lens[b] = that + the next block's tokens, whoever shares its pages. */
+int verify_attn_pages_resize_ex(const va_page_pool *pool, const int32_t *kept_lens,
+                                const int32_t *new_lens, void *stream);
 
 /* Fork sequences: fork f makes the empty slot children[f] a copy of the first
  * lens[f] tokens (lens NULL: all) of parents[f], for samples, beams or a
@@ -633,7 +646,11 @@ int verify_attn_pages_resize(const va_page_pool *pool, const int32_t *new_lens, 
  * every page is copied.  Pages are taken in order f = 0, 1, .. and block
  * order; from the first fork on for which the list is too short, all that
  * need a page are refused.  parents, children, lens: device, [num_forks];
- * num_forks >= 0.  The lengths are those before the call. */
+ * num_forks >= 0.  The lengths are those before the call.  Tokens in the full
+ * pages of a shared fork are read by both sequences from then on: a sequence
+ * whose length counts tokens that are still to be written (its next block, or
+ * drafts not yet decided) is forked with lens = the tokens that stand, or both
+ * are cut back to those (verify_attn_pages_resize_ex) before either writes. */
 int verify_attn_pages_fork(const va_page_pool *pool, const int32_t *parents, const int32_t *children,
                            const int32_t *lens, int num_forks, int share, void *stream);
 

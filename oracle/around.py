@@ -148,23 +148,25 @@ class Pages:
             for src, dst in pairs:
                 x[dst] = x[src]
 
-    def resize(self, new_lens):
+    def resize(self, new_lens, kept=None):
         B, stride = self.table.shape
         new = [int(n) for n in new_lens]
+        cut = [int(n) for n in (self.lens if kept is None else kept)]
         for b in range(B):
-            if new[b] > PAGE * stride:
+            if new[b] > PAGE * stride or (new[b] >= 0 and not 0 <= cut[b] <= self.lens[b]):
                 self.flags |= BAD_REQUEST
                 new[b] = -1
+            cut[b] = min(cut[b], new[b])
         gone = []
         for b in range(B):
-            if 0 <= new[b] < self.lens[b]:
-                for j in range(blocks(new[b]), blocks(int(self.lens[b]))):
+            if 0 <= cut[b] < self.lens[b]:
+                for j in range(blocks(cut[b]), blocks(int(self.lens[b]))):
                     page = int(self.table[b, j])
                     self.table[b, j] = -1
                     self.ref[page] -= 1
                     if self.ref[page] == 0:
                         gone.append(page)
-                self.lens[b] = new[b]
+                self.lens[b] = cut[b]
         self._push(gone)
         # what a sequence needs goes by the counts before any sequence has grown
         plan = []

@@ -159,10 +159,12 @@ def _load():
         lib.verify_attn_pages_workspace_bytes.argtypes = [I, I]
         lib.verify_attn_pages_workspace_bytes.restype = ctypes.c_size_t
         lib.verify_attn_pages_resize.argtypes = [P, P, P]
+        lib.verify_attn_pages_resize_ex.argtypes = [P, P, P, P]
         lib.verify_attn_pages_fork.argtypes = [P, P, P, P, I, I, P]
         lib.verify_attn_pages_compact.argtypes = [P, P]
         for f in ("verify_attn_rope_init", "verify_attn_rope", "verify_attn_rope_append", "verify_attn_accept_probs",
-                  "verify_attn_pages_resize", "verify_attn_pages_fork", "verify_attn_pages_compact"):
+                  "verify_attn_pages_resize", "verify_attn_pages_resize_ex", "verify_attn_pages_fork",
+                  "verify_attn_pages_compact"):
             getattr(lib, f).restype = I
         for f in ("verify_attn_plan", "verify_attn_plan_ex", "verify_attn", "verify_attn_with_plan",
                   "verify_attn_plan_get_info", "verify_attn_plan_describe", "verify_attn_plan_device_flags"):
@@ -877,15 +879,21 @@ class PagePool:
                    torch.full((1,), num_pages, **kw), buffers)
 
 
-def verify_attn_pages_resize(pool: PagePool, new_lens, stream=None):
+def verify_attn_pages_resize(pool: PagePool, new_lens, stream=None, kept_lens=None):
     """Change the sequences' lengths to ``new_lens`` (int32 ``[num_seqs]`` on the
     device, negative: left alone): pages past a shorter length go back to the
     pool, a longer one takes pages, and a growing sequence whose partly filled
-    last page is shared gets a copy of its own."""
-    n = _ptr(new_lens, "new_lens", _torch.int32, pool._index, (pool.num_seqs,))
+    last page is shared gets a copy of its own.  ``kept_lens`` (int32
+    ``[num_seqs]``): the sequences are first cut back to these, so that the tokens
+    behind them (rejected drafts) are written anew in pages of their own; after a
+    verify step give the accepted lengths, and in ``new_lens`` those plus the
+    next block."""
+    i32, shape = _torch.int32, (pool.num_seqs,)
+    n = _ptr(new_lens, "new_lens", i32, pool._index, shape)
+    kept = None if kept_lens is None else _ptr(kept_lens, "kept_lens", i32, pool._index, shape)
     st, guard = _launch_on(pool.device, stream)
     with guard:
-        rc = (_lib or _load()).verify_attn_pages_resize(pool._ref, n, st)
+        rc = (_lib or _load()).verify_attn_pages_resize_ex(pool._ref, kept, n, st)
     if rc:
         _check(rc, "verify_attn_pages_resize")
 
@@ -894,7 +902,9 @@ def verify_attn_pages_fork(pool: PagePool, parents, children, lens=None, share=T
     """Make the empty slots ``children`` copies of ``parents`` (int32 ``[F]`` on
     the device), of their first ``lens`` tokens where given.  ``share``: full
     pages are held in common and a partly filled last page is copied; otherwise
-    every page is copied."""
+    every page is copied.  Where a parent's length counts tokens that are still to
+    be written, give ``lens`` without them, or cut both back (``kept_lens`` of
+    ``verify_attn_pages_resize``) before either is written."""
     i32, index = _torch.int32, pool._index
     pa = _ptr(parents, "parents", i32, index)
     shape = parents.shape

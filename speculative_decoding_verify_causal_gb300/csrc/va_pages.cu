@@ -206,7 +206,7 @@ __device__ __forceinline__ int free_count(const Pool &p) {
     return min(max(nf, 0), p.P);
 }
 
-__global__ void __launch_bounds__(kThreads) resize_kernel(const Pool p, const int32_t *new_lens) {
+__global__ void __launch_bounds__(kThreads) resize_kernel(const Pool p, const int32_t *kept_lens, const int32_t *new_lens) {
     extern __shared__ int smem[];
     int *pre = smem, *len = pre + p.B + 1, *want = len + p.B, *tail = want + p.B;
     uint32_t *mask = reinterpret_cast<uint32_t *>(tail + p.B);
@@ -223,22 +223,24 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const Pool p, const in
     if (me == 0) p.head->jobs = 0;
     int nf = free_count(p);
     for (int b = threadIdx.x; b < p.B; b += kThreads) {
-        const int L = p.lens[b], N = new_lens[b];
-        const bool ok = L >= 0 && L <= most && N <= most;
+        const int L = p.lens[b], N = new_lens[b], K = kept_lens && N >= 0 ? kept_lens[b] : L;
+        const bool ok = L >= 0 && L <= most && N <= most && K >= 0 && K <= L;
         if (!ok && first) flag(p, VA_PAGES_BAD_REQUEST);
-        len[b] = ok && N >= 0 ? L : -1;  // -1: left alone
+        const int cut = ok ? min(K, N) : -1;  // what stays of the sequence before it grows
+        len[b] = cut;  // -1: left alone
         want[b] = N;
-        pre[b] = ok && N >= 0 && N < L ? blocks_of(L) - blocks_of(N) : 0;
+        pre[b] = cut >= 0 ? blocks_of(L) - blocks_of(cut) : 0;
         // the partly filled last page of a sequence that grows
-        tail[b] = ok && N > L && L % VA_PAGE_SIZE ? p.table[(size_t)b * p.stride + L / VA_PAGE_SIZE] : -1;
-        if (ok && N > L && L % VA_PAGE_SIZE && !in_pool(p, tail[b])) {
+        const bool part = cut >= 0 && N > cut && cut % VA_PAGE_SIZE;
+        tail[b] = part ? p.table[(size_t)b * p.stride + cut / VA_PAGE_SIZE] : -1;
+        if (part && !in_pool(p, tail[b])) {
             if (first) flag(p, VA_PAGES_BAD_ENTRY);
             tail[b] = -1;
         }
     }
     prefix_sums(pre, p.B);
     cluster_wait();
-    // 1. shrinking sequences drop their last pages
+    // 1. sequences that are cut back drop their last pages
     const int drops = pre[p.B];
     if (drops) {
         struct Entry {
@@ -254,7 +256,7 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const Pool p, const in
                 v[u].page = -1;
                 if (i >= drops) continue;
                 const int b = find(pre, p.B, i);
-                v[u].at = p.table + (size_t)b * p.stride + blocks_of(want[b]) + (i - pre[b]);
+                v[u].at = p.table + (size_t)b * p.stride + blocks_of(len[b]) + (i - pre[b]);
                 v[u].page = *v[u].at;
             }
 #pragma unroll
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const Pool p, const in
     });
     if (first) {
         for (int b = threadIdx.x; b < p.B; b += kThreads)
-            if (len[b] >= 0 && (pre[b + 1] == pre[b] || pre[b + 1] <= nf)) p.lens[b] = want[b];
+            if (len[b] >= 0) p.lens[b] = pre[b + 1] == pre[b] || pre[b + 1] <= nf ? want[b] : len[b];
     }
     // 3. shared pages that all their holders replaced
     nf -= taken;
@@ -716,16 +718,22 @@ extern "C" size_t verify_attn_pages_workspace_bytes(int num_seqs, int num_pages)
     return va::sizes_ok(num_seqs, num_pages) ? va::Layout(num_pages).total : 0;
 }
 
-extern "C" int verify_attn_pages_resize(const va_page_pool *pool, const int32_t *new_lens, void *stream) {
+extern "C" int verify_attn_pages_resize_ex(const va_page_pool *pool, const int32_t *kept_lens, const int32_t *new_lens,
+                                           void *stream) {
     va::Pool p;
     if (const int rc = va::check(pool, &p)) return rc;
-    if (!new_lens || (reinterpret_cast<uintptr_t>(new_lens) & 3)) return VA_ERR_INVALID_ARGUMENT;
+    if (!new_lens || (reinterpret_cast<uintptr_t>(new_lens) & 3) || (reinterpret_cast<uintptr_t>(kept_lens) & 3))
+        return VA_ERR_INVALID_ARGUMENT;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     va::set_slices(p);
     const size_t smem = sizeof(int) * (4 * (size_t)p.B + 1 + ((size_t)1 << p.slice_bits));
-    cudaError_t e = va::launch_book(va::resize_kernel, smem, s, p, new_lens);
+    cudaError_t e = va::launch_book(va::resize_kernel, smem, s, p, kept_lens, new_lens);
     if (e == cudaSuccess) e = va::launch_copies(pool, p, s);
     return va::done(e);
+}
+
+extern "C" int verify_attn_pages_resize(const va_page_pool *pool, const int32_t *new_lens, void *stream) {
+    return verify_attn_pages_resize_ex(pool, nullptr, new_lens, stream);
 }
 
 extern "C" int verify_attn_pages_fork(const va_page_pool *pool, const int32_t *parents, const int32_t *children,

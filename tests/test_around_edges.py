@@ -1,0 +1,96 @@
+"""Edges of the operators around the verify step on the CPU: sequences that are cut back into pages that a fork shares."""
+import ctypes
+
+import numpy as np
+import pytest
+
+from oracle import around
+import speculative_decoding_verify_causal_gb300 as va
+from speculative_decoding_verify_causal_gb300 import build as vbuild
+
+from test_around_oracle import _pool
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    vbuild.build()
+
+
+# ------------------------------------------------------------------ pages
+
+
+class Tokens:
+    """What each sequence of a pool should read: its tokens, written through the table as they come."""
+
+    def __init__(self, pool):
+        self.pool, self.seqs, self.next = pool, [[] for _ in pool.lens], 1
+
+    def write(self, b, kept):
+        """The block of sequence b, tokens kept .. its length - 1, as an append writes it."""
+        self.seqs[b] = self.seqs[b][:kept]
+        for at in range(kept, int(self.pool.lens[b])):
+            self.seqs[b].append(self.next)
+            self.pool.buffers[0][self.pool.table[b, at // 16], at % 16] = self.next
+            self.next += 1
+
+    def check(self):
+        for b, tokens in enumerate(self.seqs):
+            n = int(self.pool.lens[b])
+            assert [self.pool.buffers[0][self.pool.table[b, i // 16], i % 16] for i in range(n)] == tokens[:n], b
+
+
+@pytest.mark.parametrize("kept,new", [([20, 20], [36, 36]), ([20, 27], [36, 31]), ([3, 32], [19, 48]), ([16, 17], [32, 32]),
+                                      ([31, 0], [32, 16]), ([20, 20], [30, 32])])
+def test_a_fork_made_before_the_drafts_were_decided_keeps_its_tokens(kept, new):
+    """32 tokens, the last 16 of them drafts, are forked with their full pages shared; then both sequences keep what was
+    accepted and write their next blocks."""
+    pool = around.Pages(16, 2, 4, [np.zeros((16, 16), np.int64)])
+    tokens = Tokens(pool)
+    pool.resize([32, 0])
+    tokens.write(0, 0)
+    pool.fork([0], [1])
+    tokens.seqs[1] = list(tokens.seqs[0])
+    pool.resize(new, kept=kept)
+    pool.check()
+    for b in (0, 1):
+        tokens.write(b, kept[b])
+    tokens.check()
+    assert pool.flags == 0 and pool.lens.tolist() == new
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_resize_with_kept_lengths_is_two_calls(seed):
+    rng = np.random.default_rng(seed)
+    make = lambda: around.Pages(40, 5, 8, [np.arange(40 * 4).reshape(40, 4)])  # noqa: E731
+    a, b = make(), make()
+    for _ in range(60):
+        if rng.random() < 0.3:
+            args = rng.integers(0, 5, 2), rng.integers(0, 5, 2)
+            a.fork(*args)
+            b.fork(*args)
+        kept = rng.integers(0, a.lens + 1)
+        new = np.where(rng.random(5) < 0.2, -1, np.minimum(kept + rng.integers(-10, 30, 5), 128).clip(0))
+        a.resize(new, kept=kept)
+        b.resize(np.where(new < 0, -1, np.minimum(kept, new)))
+        b.resize(new)
+        a.check()
+        for x, y in zip((a.table, a.lens, a.ref, a.stack[:a.num_free], a.buffers[0], a.flags),
+                        (b.table, b.lens, b.ref, b.stack[:b.num_free], b.buffers[0], b.flags)):
+            assert np.array_equal(x, y)
+
+
+def test_resize_refuses_kept_lengths_that_are_not_there():
+    pool = around.Pages(8, 4, 4)
+    pool.resize([20, 20, 20, 0])
+    pool.resize([30, 30, -1, 5], kept=[21, -1, 99, 0])
+    assert pool.flags == around.BAD_REQUEST and pool.lens.tolist() == [20, 20, 20, 5]
+
+
+def test_resize_ex_refusals():
+    lib, s = va.library(), _pool()
+    ref = ctypes.byref(s)
+    assert lib.verify_attn_pages_resize_ex(None, None, 4096, None) == -1
+    assert lib.verify_attn_pages_resize_ex(ref, None, None, None) == -1
+    assert lib.verify_attn_pages_resize_ex(ref, 4096, None, None) == -1
+    assert lib.verify_attn_pages_resize_ex(ref, 4098, 4096, None) == -1
+    assert lib.verify_attn_pages_resize_ex(ref, 4096, 4098, None) == -1

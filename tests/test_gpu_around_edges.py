@@ -1,0 +1,104 @@
+"""Edges of the operators around the verify step on the GPU: forks whose sequences are cut back before they write."""
+import numpy as np
+import pytest
+
+from oracle import around
+
+from test_gpu_around import check_pool, cuda, gpu_pool
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from speculative_decoding_verify_causal_gb300 import build
+    build.build()
+
+
+@pytest.fixture(scope="module")
+def va():
+    import speculative_decoding_verify_causal_gb300 as va
+    return va
+
+
+def i32(*v):
+    return cuda(np.array(v, np.int32))
+
+
+# ------------------------------------------------------------------ pages
+
+
+@pytest.mark.parametrize("kept", [[20, 20], [20, 27], [3, 32], [16, 17], [31, 0]])
+@pytest.mark.parametrize("calls", [1, 2])
+def test_a_fork_made_before_the_drafts_were_decided_keeps_its_tokens(va, kept, calls):
+    """32 tokens, 16 of them drafts, forked with their full pages shared; both sequences keep what was accepted, take
+    pages for their next block and append it.  Each reads its own tokens afterwards."""
+    T, Hkv, D = 16, 1, 64
+    pages = torch.zeros(16, 16, Hkv, D, dtype=torch.bfloat16, device="cuda")
+    values = torch.zeros_like(pages)
+    pool = va.PagePool.create(16, 2, 4, [pages, values])
+    spec = va.verify_attn_rope_spec(D)
+
+    def append(seed):
+        """T rows before each sequence's end, whole numbers: v is stored as it is."""
+        v = torch.randint(1, 200, (2, T, Hkv, D), generator=torch.Generator().manual_seed(seed)).bfloat16().cuda()
+        va.verify_attn_rope_append(spec, None, None, v, v, pages, values, None, None, pool.block_table, pool.seq_lens, "bf16")
+        return v
+
+    def read(b):
+        n = int(pool.seq_lens[b])
+        return torch.cat([values[p] for p in pool.block_table[b, :-(-n // 16)].tolist()])[:n]
+
+    va.verify_attn_pages_resize(pool, i32(16, 0))
+    first = append(1)[0]
+    va.verify_attn_pages_resize(pool, i32(32, 0))
+    second = append(2)[0]
+    va.verify_attn_pages_fork(pool, i32(0), i32(1))
+    old = torch.cat([first, second])
+    assert torch.equal(read(0), old) and torch.equal(read(1), old)
+    new = [n + T for n in kept]
+    if calls == 1:
+        va.verify_attn_pages_resize(pool, i32(*new), kept_lens=i32(*kept))
+    else:
+        va.verify_attn_pages_resize(pool, i32(*kept))
+        va.verify_attn_pages_resize(pool, i32(*new))
+    for b in (0, 1):
+        assert torch.equal(read(b)[:kept[b]], old[:kept[b]])
+    block = append(3)
+    for b in (0, 1):
+        assert torch.equal(read(b), torch.cat([old[:kept[b]], block[b]])), b
+    assert va.verify_attn_pages_flags(pool) == 0
+
+
+@pytest.mark.parametrize("seed,P,B,stride", [(0, 60, 7, 12), (1, 500, 45, 8), (2, 3000, 300, 20), (3, 40, 9, 6)])
+def test_resize_with_kept_lengths(va, seed, P, B, stride):
+    """Random steps, refused ones and exhausted lists among them, against the sequential definition after each."""
+    rng = np.random.default_rng(seed)
+    pool = around.Pages(P, B, stride, [rng.integers(0, 255, (P, 32)).astype(np.uint8)])
+    pool.stack = rng.permutation(P)
+    dev = gpu_pool(va, pool)
+    for _ in range(40):
+        if rng.random() < 0.4:
+            n = max(1, B // 6)
+            args = [rng.integers(0, B, n).astype(np.int32) for _ in range(2)]
+            pool.fork(*args)
+            va.verify_attn_pages_fork(dev, *map(cuda, args))
+            check_pool(dev, pool)
+        kept = rng.integers(0, pool.lens + 1)
+        kept = np.where(rng.random(B) < 0.05, rng.choice([-1, 10 ** 6], B), kept).astype(np.int32)
+        new = np.minimum(np.maximum(kept, 0) + rng.integers(-8, 40, B), 16 * stride).clip(0)
+        new = np.where(rng.random(B) < 0.15, -1, new).astype(np.int32)
+        pool.resize(new, kept=kept)
+        va.verify_attn_pages_resize(dev, cuda(new), kept_lens=cuda(kept))
+        check_pool(dev, pool)
+        pool.check()
+
+
+def test_resize_kept_lengths_argument_errors(va):
+    pool = va.PagePool.create(8, 2, 3, [])
+    for bad in (i32(1), i32(1, 2).long(), torch.zeros(2, dtype=torch.int32)):
+        with pytest.raises(ValueError):
+            va.verify_attn_pages_resize(pool, i32(1, 2), kept_lens=bad)
