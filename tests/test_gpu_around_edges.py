@@ -1,10 +1,11 @@
-"""Edges of the operators around the verify step on the GPU: forks whose sequences are cut back before they write."""
+"""Edges of the operators around the verify step on the GPU: forks whose sequences are cut back before they write,
+the signs of zeros."""
 import numpy as np
 import pytest
 
 from oracle import around
 
-from test_gpu_around import check_pool, cuda, gpu_pool
+from test_gpu_around import bits16, cache_case, check_pool, cuda, expected_cache, gpu_pool, normal, run_append
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -102,3 +103,39 @@ def test_resize_kept_lengths_argument_errors(va):
     for bad in (i32(1), i32(1, 2).long(), torch.zeros(2, dtype=torch.int32)):
         with pytest.raises(ValueError):
             va.verify_attn_pages_resize(pool, i32(1, 2), kept_lens=bad)
+
+
+# ------------------------------------------------------------------ rotary and append
+
+
+@pytest.mark.parametrize("kv_dtype", ["fp8_e4m3", "int8", "int4", "int2", "bf16"])
+@pytest.mark.parametrize("D,R,pairing", [(64, 64, "half"), (128, 96, "half"), (256, 34, "adjacent"), (128, 22, "half")])
+def test_rope_append_keeps_the_signs_of_zeros(va, kv_dtype, D, R, pairing):
+    """Negative zeros, rows of them, and negative numbers too small for their row's scale: v is stored byte for byte as
+    verify_attn_kv_append stores it, k as the append's rule makes it of the rotated rows."""
+    B, T, Hkv = 2, 40, 2
+    pages, scale, bt, lens, P = cache_case(3, [47, 40], T, Hkv, D, kv_dtype)
+
+    def rows(seed):
+        x = normal(seed, B, T, Hkv, D)
+        kind = torch.randint(0, 5, x.shape, generator=torch.Generator().manual_seed(seed + 1)).cuda()
+        x = torch.where(kind == 0, torch.full_like(x, -0.0), x)
+        x = torch.where(kind == 1, -1e-6 * x.abs(), x)
+        x = torch.where(kind == 2, torch.full_like(x, -1e-38), x)
+        x[0, :4] = -0.0
+        x[1, 5:9] = x[1, 5:9].sign() * 0.0
+        return x.bfloat16()
+
+    k, v = rows(40), rows(42)
+    spec = va.verify_attn_rope_spec(R, pairing=pairing)
+    pos = cuda((np.arange(B * T, dtype=np.int32) // 30).reshape(1, B, T))
+    _, (kp, vp), (ks, vs), _ = run_append(va, spec, pos, None, k, v, pages, scale, bt, lens, kv_dtype)
+    dev = cuda(pages.view(np.int16) if kv_dtype == "bf16" else pages)
+    other, s1, s2 = dev.clone(), None if scale is None else cuda(scale), None if scale is None else cuda(scale)
+    va.verify_attn_kv_append(v, v, dev, other, s1, s2, cuda(bt), cuda(lens), T, kv_dtype)
+    assert np.array_equal(vp, bits16(dev) if kv_dtype == "bf16" else dev.cpu().numpy())
+    _, turned = va.verify_attn_rope(spec, pos, k.float(), k.float())
+    want, _ = expected_cache(turned.cpu().numpy(), pages, scale, bt, lens, kv_dtype, P)
+    assert np.array_equal(kp, want)
+    if kv_dtype == "fp8_e4m3":
+        assert (vp == 0x80).sum() > 1000 and (kp == 0x80).sum() > 100
