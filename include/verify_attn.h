@@ -428,8 +428,8 @@ typedef enum {
  * verify_attn_rope_init and copied into every launch, so it may be changed or
  * freed as soon as a call has returned.  turn[i] is inv_freq[i] / (2 pi), the
  * part of a full turn that one step of position makes, times 2^64 and modulo
- * 2^64: position * turn[i] modulo 2^64 is then the angle's part of a turn to
- * 2^-33 of a turn for every int32 position. */
+ * 2^64, rounded: position * turn[i] modulo 2^64 is then the angle's part of a
+ * turn to 2^-33 of a turn for every int32 position and every inv_freq. */
 #define VA_ROPE_MAX_PAIRS 128
 #define VA_ROPE_MAX_AXES 4
 typedef struct {

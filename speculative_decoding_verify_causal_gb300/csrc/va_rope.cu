@@ -6,7 +6,7 @@
 // position 200,000 its last bit is 1/64 of a radian.  turn[i] holds the part
 // of a turn that one step makes as a 64-bit fraction, so position * turn[i]
 // modulo 2^64 (one integer multiplication, negative positions included) is
-// the angle's part of a turn to 2^-64 times the position.  Its top 32 bits
+// the angle's part of a turn to 2^-65 times the position, at most 2^-34.  Its top 32 bits
 // give the nearest quarter turn and a signed remainder of at most 1/8 turn,
 // which binary32 holds to 24 bits; sincospif of the remainder is then within
 // a few ulps, and the quarter turn swaps and negates.
@@ -621,16 +621,18 @@ extern "C" int verify_attn_rope_init(va_rope *rope, const double *inv_freq, cons
         if (!std::isfinite(inv_freq[i]) || std::fabs(inv_freq[i]) > 1048576.0) return VA_ERR_INVALID_ARGUMENT;
         if (axis && (axis[i] < 0 || axis[i] >= num_axes)) return VA_ERR_INVALID_ARGUMENT;
     }
-    // 1 / (2 pi) in units of 2^-66: with inv_freq = m 2^e (m of 53 bits), m times this is exact in
-    // 117 bits, and the part of a turn is that product times 2^(e - 66).
-    constexpr uint64_t kTurn66 = 0xA2F9836E4E44152Aull;
+    // 1 / (2 pi) in units of 2^-130, in two words: cut there, it is off by less than 2^-130, an angle at any frequency up to
+    // 2^20 and any int32 position by less than 2^-79 of a turn, so that the rounding of turn[i] to 2^-64 is all of its error.
+    // (One word would cost 2^-21 of a turn at the largest of both.)
+    constexpr uint64_t kTurnHigh = 0xA2F9836E4E441529ull, kTurnLow = 0xFC2757D1F534DDC0ull;
     *rope = va_rope{};
     for (int i = 0; i < num_pairs; ++i) {
         int e = 0;
         const double m = std::frexp(std::fabs(inv_freq[i]), &e);  // in [0.5, 1), or 0
         const uint64_t whole = (uint64_t)std::ldexp(m, 53);       // inv_freq = whole 2^(e - 53)
-        const unsigned __int128 product = (unsigned __int128)whole * kTurn66;
-        // turns = product 2^(e - 53 - 66); as a multiple of 2^-64: product 2^(e - 55)
+        // the product of 53 and 128 bits without its last word, which lies below every rounding
+        const unsigned __int128 product = (unsigned __int128)whole * kTurnHigh + (((unsigned __int128)whole * kTurnLow) >> 64);
+        // turns = product 2^(e - 53 - 66); as a multiple of 2^-64: product 2^(e - 55), rounded
         const int shift = 55 - e;
         const uint64_t turn =  // e <= 21, so shift >= 34
             shift > 120 ? 0 : (uint64_t)((product + ((unsigned __int128)1 << (shift - 1))) >> shift);

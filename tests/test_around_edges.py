@@ -1,5 +1,7 @@
-"""Edges of the operators around the verify step on the CPU: sequences that are cut back into pages that a fork shares."""
+"""Edges of the operators around the verify step on the CPU: sequences that are cut back into pages that a fork shares,
+frequencies above one."""
 import ctypes
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -94,3 +96,19 @@ def test_resize_ex_refusals():
     assert lib.verify_attn_pages_resize_ex(ref, 4096, None, None) == -1
     assert lib.verify_attn_pages_resize_ex(ref, 4098, 4096, None) == -1
     assert lib.verify_attn_pages_resize_ex(ref, 4096, 4098, None) == -1
+
+
+# ------------------------------------------------------------------ rotary
+
+
+def test_rope_spec_rounds_the_part_of_a_turn_correctly():
+    """turn[i] is inv_freq / (2 pi) to half a unit of 2^-64, whatever the frequency: at the largest position that is 2^-34
+    of a turn."""
+    rng = np.random.default_rng(1)
+    freq = [2.0 ** 20, -(2.0 ** 20), 3.0e4, 1024.0, 129.0, 7.5, 1.0, 0.37, -0.25, 1e-3, 3e-30, 0.0, 2.0 ** -66, 1e-18]
+    freq += list(2.0 ** rng.uniform(-30, 20, 100) * rng.choice([-1, 1], 100))
+    spec = va.verify_attn_rope_spec(2 * len(freq), inv_freq=freq)
+    for i, f in enumerate(freq):
+        exact = Fraction(f) * Fraction(around._TURN, 2 ** around._BITS) * 2 ** 64
+        err = (Fraction(spec._struct.turn[i]) - exact) % 2 ** 64
+        assert min(err, 2 ** 64 - err) <= Fraction(1, 2) + Fraction(1, 2 ** 20), f

@@ -1,11 +1,11 @@
 """Edges of the operators around the verify step on the GPU: forks whose sequences are cut back before they write,
-the signs of zeros."""
+the signs of zeros, frequencies above one."""
 import numpy as np
 import pytest
 
 from oracle import around
 
-from test_gpu_around import bits16, cache_case, check_pool, cuda, expected_cache, gpu_pool, normal, run_append
+from test_gpu_around import bits16, cache_case, check_pool, cuda, expected_cache, gpu_pool, normal, rope_bound, run_append
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -139,3 +139,17 @@ def test_rope_append_keeps_the_signs_of_zeros(va, kv_dtype, D, R, pairing):
     assert np.array_equal(kp, want)
     if kv_dtype == "fp8_e4m3":
         assert (vp == 0x80).sum() > 1000 and (kp == 0x80).sum() > 100
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rope_at_frequencies_above_one(va, dtype):
+    """Frequencies up to 2^20 at the ends of int32: within the bound of every other angle."""
+    freq = [2.0 ** 20, 3.0e4, 1024.0, 7.5, 1.0, -65536.5, 1e-3, 129.0]
+    spec = va.verify_attn_rope_spec(16, inv_freq=freq)
+    pos = np.array([2 ** 31 - 1, -(2 ** 31), 2 ** 30 + 7, 123456789, -1, 1], np.int32).reshape(1, 1, -1)
+    x = normal(50, 1, 6, 3, 16, dtype=dtype)
+    got, _ = va.verify_attn_rope(spec, cuda(pos), x)
+    xs = x.double().cpu().numpy()
+    ref = around.rope(xs, pos.tolist(), freq, [0] * 8)
+    err = np.abs(got.double().cpu().numpy() - ref)
+    assert (err <= rope_bound(xs, 8, False, 1.0, dtype, ref)).all(), err.max()
