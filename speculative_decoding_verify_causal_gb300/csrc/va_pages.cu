@@ -648,10 +648,17 @@ void set_slices(Pool &p) {
     while ((kMaxCluster << p.slice_bits) < mask_words(p.P)) ++p.slice_bits;
 }
 
+// The most dynamic shared memory that a bookkeeping kernel asks for: fork with all sequences and as many forks, or resize with
+// all sequences and an eighth of the largest bitmap.
+constexpr size_t kMaxBookSmem = sizeof(int) * (6 * (size_t)VA_PAGES_MAX_SEQS + 2);
+static_assert(4 * (size_t)VA_PAGES_MAX_SEQS + 1 + VA_PAGES_MAX_PAGES / 32 / kMaxCluster <= kMaxBookSmem / sizeof(int),
+              "resize's arrays and its slice of the bitmap");
+static_assert(kMaxBookSmem + 16 * 1024 <= kMaxSmemPerBlock, "the kernels' own arrays lie beside it");
+
 template <typename... KArgs, typename... Args>
 cudaError_t launch_book(void (*kernel)(KArgs...), size_t smem, cudaStream_t s, Args... args) {
-    if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (smem > 40 * 1024) {  // always the same limit: it is the function's, and other host threads launch it too
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxBookSmem);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};

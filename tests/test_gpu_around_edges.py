@@ -1,5 +1,5 @@
 """Edges of the operators around the verify step on the GPU: forks whose sequences are cut back before they write,
-the signs of zeros, frequencies above one."""
+host threads at once, the signs of zeros, frequencies above one."""
 import numpy as np
 import pytest
 
@@ -103,6 +103,36 @@ def test_resize_kept_lengths_argument_errors(va):
     for bad in (i32(1), i32(1, 2).long(), torch.zeros(2, dtype=torch.int32)):
         with pytest.raises(ValueError):
             va.verify_attn_pages_resize(pool, i32(1, 2), kept_lens=bad)
+
+
+def test_page_calls_of_several_host_threads(va):
+    """Pools whose bookkeeping wants shared memory past the default, in two different amounts, each used by a host thread
+    and on a stream of its own, as fast as they can: no call changes what a call of another thread may ask for."""
+    import threading
+    pools = [va.PagePool.create(P, B, 2, []) for B, P in 2 * ((8192, 20000), (2700, 64))]
+    streams = [torch.cuda.Stream() for _ in pools]
+    lens = [torch.ones(pool.num_seqs, dtype=torch.int32, device="cuda") for pool in pools]
+    for x in lens:
+        x[50:] = 0
+    torch.cuda.synchronize()
+    resize = va.library().verify_attn_pages_resize
+    codes, start = [set() for _ in pools], threading.Barrier(len(pools))
+
+    def work(i):
+        args = pools[i]._ref, lens[i].data_ptr(), streams[i].cuda_stream
+        start.wait()
+        codes[i] = {resize(*args) for _ in range(4000)}
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(pools))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert codes == [{0}] * len(pools)
+    for pool, want in zip(pools, lens):
+        assert torch.equal(pool.seq_lens, want) and pool.num_free.item() == pool.num_pages - 50
+        assert va.verify_attn_pages_flags(pool) == 0
 
 
 # ------------------------------------------------------------------ rotary and append
