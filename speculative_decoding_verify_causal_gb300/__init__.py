@@ -833,7 +833,12 @@ class PagePool:
     (made).  ``buffers``: tensors whose first dimension is the pages (K and V
     pages and scales of every layer), contiguous.  Give ``block_table`` and
     ``seq_lens`` to ``verify_attn_rope_append`` and ``verify_attn_with_plan``
-    (with ``block_table_stride`` and ``num_pages`` as plan options)."""
+    (with ``block_table_stride`` and ``num_pages`` as plan options).
+
+    The pool's tensors, the workspace among them, are recorded on the torch
+    streams that its calls run on, so a pool may be dropped while calls are
+    queued there.  It has to outlive the work on a raw stream handle (or an
+    ``ExternalStream``) and the replays of a captured graph."""
 
     def __init__(self, block_table, seq_lens, ref_count, free_list, num_free, buffers, flags=None):
         torch = _torch or _bind_torch()
@@ -865,6 +870,21 @@ class PagePool:
             _ptr(num_free, "num_free", i32, index, (1,)), _ptr(flags, "flags", i32, index, (1,)), stride, B, P,
             len(self.buffers), array, self.workspace.data_ptr())
         self._ref = ctypes.byref(self._struct)
+        self._tensors = [block_table, seq_lens, ref_count, free_list, num_free, flags, self.workspace, *self.buffers]
+        self._recorded = set()  # handles of the streams that the tensors are recorded on
+
+    def _launch_on(self, stream):
+        """``_launch_on`` of the pool's device, with the pool's tensors recorded on a torch stream the first time."""
+        st, guard = _launch_on(self.device, stream)
+        if st not in self._recorded:
+            torch = _torch
+            if stream is None:
+                stream = torch.cuda.current_stream(self.device)
+            if isinstance(stream, torch.cuda.Stream) and not isinstance(stream, torch.cuda.ExternalStream):
+                for t in self._tensors:  # no more than a look where a tensor was made on that stream
+                    t.record_stream(stream)
+                self._recorded.add(st)
+        return st, guard
 
     @classmethod
     def create(cls, num_pages, num_seqs, max_blocks, buffers, device="cuda"):
@@ -891,7 +911,7 @@ def verify_attn_pages_resize(pool: PagePool, new_lens, stream=None, kept_lens=No
     i32, shape = _torch.int32, (pool.num_seqs,)
     n = _ptr(new_lens, "new_lens", i32, pool._index, shape)
     kept = None if kept_lens is None else _ptr(kept_lens, "kept_lens", i32, pool._index, shape)
-    st, guard = _launch_on(pool.device, stream)
+    st, guard = pool._launch_on(stream)
     with guard:
         rc = (_lib or _load()).verify_attn_pages_resize_ex(pool._ref, kept, n, st)
     if rc:
@@ -912,7 +932,7 @@ def verify_attn_pages_fork(pool: PagePool, parents, children, lens=None, share=T
         raise ValueError("parents must be [F]")
     ch = _ptr(children, "children", i32, index, shape)
     ln = None if lens is None else _ptr(lens, "lens", i32, index, shape)
-    st, guard = _launch_on(pool.device, stream)
+    st, guard = pool._launch_on(stream)
     with guard:
         rc = (_lib or _load()).verify_attn_pages_fork(pool._ref, pa, ch, ln, shape[0], 1 if share else 0, st)
     if rc:
@@ -922,7 +942,7 @@ def verify_attn_pages_fork(pool: PagePool, parents, children, lens=None, share=T
 def verify_attn_pages_compact(pool: PagePool, stream=None):
     """Move the held pages to the front of the pool (block tables and counts
     follow); the free list then holds the pages behind them, lowest first."""
-    st, guard = _launch_on(pool.device, stream)
+    st, guard = pool._launch_on(stream)
     with guard:
         rc = (_lib or _load()).verify_attn_pages_compact(pool._ref, st)
     if rc:

@@ -1,5 +1,5 @@
 """Edges of the operators around the verify step on the GPU: forks whose sequences are cut back before they write,
-host threads at once, the signs of zeros, frequencies above one."""
+host threads at once, a pool dropped early, the signs of zeros, frequencies above one."""
 import numpy as np
 import pytest
 
@@ -133,6 +133,34 @@ def test_page_calls_of_several_host_threads(va):
     for pool, want in zip(pools, lens):
         assert torch.equal(pool.seq_lens, want) and pool.num_free.item() == pool.num_pages - 50
         assert va.verify_attn_pages_flags(pool) == 0
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_a_dropped_pool_keeps_its_memory_until_its_calls_are_done(va, given):
+    """A pool dropped while its calls are queued on another stream: none of its tensors' memory is handed out before they
+    have run (the tensors here are too large to share a block with anything else)."""
+    big = torch.empty(2 ** 32, dtype=torch.uint8, device="cuda")
+    pages = torch.zeros(2 ** 20, 64, dtype=torch.uint8, device="cuda")
+    pool = va.PagePool.create(2 ** 20, 8, 2 ** 18, [pages])
+    sizes = [(t.data_ptr(), t.numel() * t.element_size()) for t in (pool.workspace, pool.block_table, pool.ref_count,
+                                                                    pool.free_list, pages)]
+    new = i32(100, 2 ** 20, 0, 0, 0, 0, 0, 0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(60):  # some 30 ms before the pool's calls
+            big.fill_(1)
+        if not given:
+            va.verify_attn_pages_resize(pool, new)
+    if given:
+        va.verify_attn_pages_resize(pool, new, stream=side)
+    del pool, pages
+    taken = [torch.empty(n, dtype=torch.uint8, device="cuda") for _, n in sizes for _ in range(2)]
+    waiting = not side.query()
+    reused = {t.data_ptr() for t in taken} & {at for at, _ in sizes}
+    torch.cuda.synchronize()
+    assert waiting and not reused
 
 
 # ------------------------------------------------------------------ rotary and append
