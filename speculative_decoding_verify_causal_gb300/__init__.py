@@ -535,7 +535,7 @@ _torch = None
 def _bind_torch():
     """What the calls below need of torch, looked up once: a call's checks and marshalling are most of
     its cost on small batches."""
-    global _torch, _FLOAT_CODES, _CACHE_TYPES, _raw_stream, _current_device
+    global _torch, _FLOAT_CODES, _CACHE_TYPES, _raw_stream, _current_device, _grad_mode
     import torch
     _FLOAT_CODES = {torch.bfloat16: VA_FLOAT_BF16, torch.float16: VA_FLOAT_FP16, torch.float32: VA_FLOAT_FP32}
     _CACHE_TYPES = {code: _kv_dtypes(code) for code in KV_DTYPE_CODES.values()}
@@ -543,6 +543,7 @@ def _bind_torch():
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda index: torch.cuda.current_stream(index).cuda_stream)
     _current_device = torch.cuda.current_device
+    _grad_mode = torch.is_grad_enabled
     _torch = torch
     return torch
 
@@ -623,6 +624,14 @@ def _positions(t, rope, B, T, index):
     raise ValueError(f"positions must be an int32 tensor {list(shape)} on cuda:{index}")
 
 
+def _no_gradient(what, *tensors):
+    """A result without its gradient is refused, not returned."""
+    if any(getattr(t, "requires_grad", False) for t in tensors):
+        raise ValueError(f"{what} is not recorded by autograd and would lose its inputs' gradient: call it under "
+                         "torch.no_grad(), on detached tensors, or in a torch.autograd.Function whose backward rotates "
+                         "with inverse=True")
+
+
 class Rope:
     """A rotation (``va_rope``): host data, made by ``verify_attn_rope_spec``."""
 
@@ -680,10 +689,14 @@ def verify_attn_rope(rope: Rope, positions, q, k=None, q_out=None, k_out=None, i
     with a contiguous last dimension) by ``positions`` (int32 ``[axes, B, T]``,
     any strides).  ``q_out`` / ``k_out`` default to new contiguous tensors; pass
     ``q`` / ``k`` themselves to work in place, otherwise outputs must not overlap
-    inputs.  ``inverse=True`` rotates back, which is also the way of the gradient
-    (the call itself is not recorded by autograd).  Returns (q_out, k_out), k_out
-    None without ``k``."""
+    inputs.  ``inverse=True`` rotates back, which is also the way of the gradient:
+    a ``torch.autograd.Function`` calls this in its forward and, with
+    ``inverse=True`` on the outputs' gradients, in its backward.  The call itself
+    is not recorded by autograd, and in grad mode tensors that require a gradient
+    are refused.  Returns (q_out, k_out), k_out None without ``k``."""
     torch = _torch or _bind_torch()
+    if _grad_mode():
+        _no_gradient("verify_attn_rope", q, k, q_out, k_out)
     device, index = _device_of(q, "q")
     code = _float_code(q, "q")
     dtype = q.dtype
@@ -721,9 +734,12 @@ def verify_attn_rope_append(rope: Rope, positions, q, k_new, v_new, k_pages, v_p
     Cache arguments, ``num_pages`` and ``flags`` as for
     ``verify_attn_kv_append``; the cache gets the rotated keys, quantised from
     their unrounded values.  ``positions`` None: every axis is the token's
-    place in its sequence, ``seq_lens[b] - T + t``.  ``q`` may be None.  Returns
-    the rotated q, contiguous bf16."""
+    place in its sequence, ``seq_lens[b] - T + t``.  ``q`` may be None.  Not
+    recorded by autograd: in grad mode tensors that require a gradient are
+    refused.  Returns the rotated q, contiguous bf16."""
     torch = _torch or _bind_torch()
+    if _grad_mode():
+        _no_gradient("verify_attn_rope_append", q, k_new, v_new, q_out)
     code = _dtype_code(kv_dtype)
     device, index = _device_of(k_new, "k_new")
     bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32

@@ -1,5 +1,5 @@
 """Edges of the operators around the verify step on the CPU: sequences that are cut back into pages that a fork shares,
-frequencies above one."""
+frequencies above one, inputs that require a gradient."""
 import ctypes
 from fractions import Fraction
 
@@ -112,3 +112,24 @@ def test_rope_spec_rounds_the_part_of_a_turn_correctly():
         exact = Fraction(f) * Fraction(around._TURN, 2 ** around._BITS) * 2 ** 64
         err = (Fraction(spec._struct.turn[i]) - exact) % 2 ** 64
         assert min(err, 2 ** 64 - err) <= Fraction(1, 2) + Fraction(1, 2 ** 20), f
+
+
+def test_calls_that_would_lose_a_gradient_are_refused():
+    """Before anything else is looked at; without grad mode or on detached tensors the call goes on (to the next refusal
+    here, which is that there is no GPU)."""
+    torch = pytest.importorskip("torch")
+    rope = va.verify_attn_rope_spec(16)
+    pos = torch.zeros(1, 1, 2, dtype=torch.int32)
+    x, w = torch.zeros(1, 2, 3, 16), torch.zeros(1, 2, 3, 16, requires_grad=True)
+    for kw in (dict(q=w), dict(q=x, k=w), dict(q=w, q_out=w), dict(q=x, q_out=w), dict(q=x, k=x, k_out=w), dict(q=w * 2)):
+        with pytest.raises(ValueError, match="gradient"):
+            va.verify_attn_rope(rope, pos, **kw)
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+            va.verify_attn_rope(rope, pos, **kw)
+    with pytest.raises(ValueError, match="CUDA"):
+        va.verify_attn_rope(rope, pos, w.detach())
+    for q, k, v in ((w, x, x), (x, w, x), (x, x, w), (None, w, x)):
+        with pytest.raises(ValueError, match="gradient"):
+            va.verify_attn_rope_append(rope, pos, q, k, v, x, x, x, x, pos, pos, "int8")
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+            va.verify_attn_rope_append(rope, pos, q, k, v, x, x, x, x, pos, pos, "int8")

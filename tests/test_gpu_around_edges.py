@@ -1,5 +1,6 @@
 """Edges of the operators around the verify step on the GPU: forks whose sequences are cut back before they write,
-host threads at once, a pool dropped early, the signs of zeros, frequencies above one."""
+host threads at once, a pool dropped early, the signs of zeros, frequencies above one,
+gradients."""
 import numpy as np
 import pytest
 
@@ -197,6 +198,42 @@ def test_rope_append_keeps_the_signs_of_zeros(va, kv_dtype, D, R, pairing):
     assert np.array_equal(kp, want)
     if kv_dtype == "fp8_e4m3":
         assert (vp == 0x80).sum() > 1000 and (kp == 0x80).sum() > 100
+
+
+def test_rope_inside_an_autograd_function_and_refused_outside(va):
+    """The way that the refusal names: forward and inverse calls in a Function.  The gradient of sum(w y) is the transposed
+    map of w, within the bound of a rotated element; it also goes through a broadcast input, whose gradients add up (3
+    heads: three elements and two additions)."""
+    spec = va.verify_attn_rope_spec(16, sections=[3, 5])
+    pos = cuda(np.random.default_rng(2).integers(0, 9000, (2, 2, 5)).astype(np.int32))
+
+    class Rotate(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k):
+            return va.verify_attn_rope(spec, pos, q, k)
+
+        @staticmethod
+        def backward(ctx, dq, dk):
+            return va.verify_attn_rope(spec, pos, dq, dk, inverse=True)
+
+    q, one = normal(1, 2, 5, 4, 20).requires_grad_(), normal(2, 2, 5, 1, 20).requires_grad_()
+    wq, wk = normal(3, 2, 5, 4, 20), normal(4, 2, 5, 3, 20)
+    y, z = Rotate.apply(q, one.expand(2, 5, 3, 20))
+    ((y * wq).sum() + (z * wk).sum()).backward()
+    freq = 1.0e6 ** (-np.arange(8) / 8)
+    for got, w, heads in ((q.grad, wq, 1), (one.grad, wk, 3)):
+        ws = w.double().cpu().numpy()
+        want = around.rope(ws, pos.tolist(), freq, spec.axis, inverse=True)
+        bound = rope_bound(ws, 8, False, 1.0, torch.float32, want)
+        if heads > 1:
+            bound = bound.sum(2, keepdims=True) + 2 * 2.0 ** -24 * np.abs(want).sum(2, keepdims=True) * (1 + 1e-6)
+            want = want.sum(2, keepdims=True)
+        assert (np.abs(got.double().cpu().numpy() - want) <= bound).all()
+    with pytest.raises(ValueError, match="gradient"):
+        va.verify_attn_rope(spec, pos, q)
+    with torch.no_grad():
+        va.verify_attn_rope(spec, pos, q)
+    assert torch.equal(va.verify_attn_rope(spec, pos, q.detach())[0], y.detach())
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
