@@ -588,11 +588,11 @@ bool apart(const va_heads &x, int num_seqs, int T, int head_dim) {
         int64_t stride, size;
     } d[3] = {{x.stride_head, x.num_heads}, {x.stride_token, T}, {x.stride_seq, num_seqs}};
     std::sort(d, d + 3, [](const Dim &a, const Dim &b) { return a.stride < b.stride; });
-    int64_t extent = head_dim;
+    __int128 extent = head_dim;  // strides are any number of 63 bits
     for (const Dim &k : d) {
         if (k.size <= 1) continue;
         if (k.stride < extent) return false;
-        extent = (k.size - 1) * k.stride + extent;
+        extent += (__int128)(k.size - 1) * k.stride;
     }
     return true;
 }
@@ -655,8 +655,8 @@ extern "C" int verify_attn_rope(const va_rope *rope, const va_positions *positio
     if (q->num_heads < 1 || q->num_heads != q_out->num_heads || (k && (k->num_heads < 1 || k->num_heads != k_out->num_heads)))
         return VA_ERR_INVALID_ARGUMENT;
     const long long tokens = (long long)num_seqs * T;
+    if (tokens > (1LL << 30) || (long long)q->num_heads + (k ? k->num_heads : 0) > 65535) return VA_ERR_INVALID_ARGUMENT;
     const int heads = q->num_heads + (k ? k->num_heads : 0);
-    if (tokens > (1LL << 30) || q->num_heads > 65535 || heads > 65535) return VA_ERR_INVALID_ARGUMENT;
     if (tokens == 0) return VA_OK;
     const int bytes = type == VA_FLOAT_FP32 ? 4 : 2;
     if (!positions->data || !va::aligned(positions->data, 4)) return VA_ERR_INVALID_ARGUMENT;

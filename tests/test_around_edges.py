@@ -1,5 +1,5 @@
 """Edges of the operators around the verify step on the CPU: sequences that are cut back into pages that a fork shares,
-frequencies above one, inputs that require a gradient."""
+frequencies above one, inputs that require a gradient, head counts and strides at their limits."""
 import ctypes
 from fractions import Fraction
 
@@ -10,7 +10,7 @@ from oracle import around
 import speculative_decoding_verify_causal_gb300 as va
 from speculative_decoding_verify_causal_gb300 import build as vbuild
 
-from test_around_oracle import _pool
+from test_around_oracle import _heads, _pool, _rope
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -133,3 +133,16 @@ def test_calls_that_would_lose_a_gradient_are_refused():
             va.verify_attn_rope_append(rope, pos, q, k, v, x, x, x, x, pos, pos, "int8")
         with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
             va.verify_attn_rope_append(rope, pos, q, k, v, x, x, x, x, pos, pos, "int8")
+
+
+@pytest.mark.parametrize("change", [
+    dict(k=_heads(4096, 2 ** 40, 2 ** 38, 16, 2 ** 31 - 1), k_out=_heads(8192, 2 ** 40, 2 ** 38, 16, 2 ** 31 - 1)),
+    dict(q=_heads(4096, 2 ** 24, 2 ** 22, 16, 65535), q_out=_heads(8192, 2 ** 24, 2 ** 22, 16, 65535),
+         k=_heads(4096), k_out=_heads(8192)),
+    # outputs whose elements lie on one another, with extents past 63 bits
+    dict(B=5, T=3, q_out=_heads(8192, seq=2 ** 61, token=2 ** 62, head=16)),
+    dict(T=2, B=2 ** 20, q_out=_heads(8192, seq=2 ** 44, token=2 ** 63 - 1, head=16)),
+])
+def test_rope_refuses_counts_and_extents_that_wrap(change):
+    """More than 65,535 heads in sum: their sum once wrapped and ended the process with a division by zero."""
+    assert _rope(**change) == -1
