@@ -478,16 +478,15 @@ def verify_attn_lookup_draft(tokens, lens, num_draft, min_match=6, max_match=12,
     i32 = (torch.int32,)
     tp = _dev_ptr(tokens, "tokens", i32)
     lp = _dev_ptr(lens, "lens", i32)
-    draft = torch.empty((B, int(num_draft)), dtype=torch.int32, device=tokens.device)
-    dlen = torch.empty((B,), dtype=torch.int32, device=tokens.device)
     me = _dev_ptr(match_end, "match_end", i32, allow_none=True)
     ml = _dev_ptr(match_len, "match_len", i32, allow_none=True)
-    if stream is None:
-        stream = torch.cuda.current_stream(tokens.device)
-    st = ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
-    rc = _load().verify_attn_lookup_draft(tp, int(stride), lp, int(B), int(min_match), int(max_match),
-                                          int(num_draft), ctypes.c_void_p(draft.data_ptr()),
-                                          ctypes.c_void_p(dlen.data_ptr()), me, ml, st)
+    st, guard = _launch_on(tokens.device, stream)
+    with guard:
+        draft = torch.empty((B, int(num_draft)), dtype=torch.int32, device=tokens.device)
+        dlen = torch.empty((B,), dtype=torch.int32, device=tokens.device)
+        rc = _load().verify_attn_lookup_draft(tp, int(stride), lp, int(B), int(min_match), int(max_match),
+                                              int(num_draft), ctypes.c_void_p(draft.data_ptr()),
+                                              ctypes.c_void_p(dlen.data_ptr()), me, ml, st)
     _check(rc, "verify_attn_lookup_draft")
     return draft, dlen
 
@@ -514,16 +513,15 @@ def verify_attn_accept(target_logits, draft_tokens, temperature, seed, draft_log
     dp = _dev_ptr(draft_tokens, "draft_tokens", i32)
     tp = _dev_ptr(temperature, "temperature", f32)
     lib = _load()
-    ws = torch.empty(max(16, int(lib.verify_attn_accept_workspace_bytes(int(B), int(T)))), dtype=torch.uint8,
-                     device=target_logits.device)
-    out = torch.empty((B, T1), dtype=torch.int32, device=target_logits.device)
-    nacc = torch.empty((B,), dtype=torch.int32, device=target_logits.device)
-    if stream is None:
-        stream = torch.cuda.current_stream(target_logits.device)
-    st = ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
-    rc = lib.verify_attn_accept(zp, wp, dp, tp, int(B), int(T), int(V), int(seed) & 0xFFFFFFFFFFFFFFFF,
-                                ctypes.c_void_p(ws.data_ptr()), ctypes.c_void_p(out.data_ptr()),
-                                ctypes.c_void_p(nacc.data_ptr()), st)
+    st, guard = _launch_on(target_logits.device, stream)
+    with guard:
+        ws = torch.empty(max(16, int(lib.verify_attn_accept_workspace_bytes(int(B), int(T)))), dtype=torch.uint8,
+                         device=target_logits.device)
+        out = torch.empty((B, T1), dtype=torch.int32, device=target_logits.device)
+        nacc = torch.empty((B,), dtype=torch.int32, device=target_logits.device)
+        rc = lib.verify_attn_accept(zp, wp, dp, tp, int(B), int(T), int(V), int(seed) & 0xFFFFFFFFFFFFFFFF,
+                                    ctypes.c_void_p(ws.data_ptr()), ctypes.c_void_p(out.data_ptr()),
+                                    ctypes.c_void_p(nacc.data_ptr()), st)
     _check(rc, "verify_attn_accept")
     return out, nacc
 
@@ -559,7 +557,7 @@ def _launch_on(device, stream):
     """(stream handle, guard): a call runs on the tensors' device and on ``stream`` there (a
     torch stream or a raw handle; default: torch's current stream of that device).  What the
     call allocates is allocated inside the guard, so it belongs to that stream."""
-    torch = _torch
+    torch = _torch or _bind_torch()
     if stream is None:
         index = device.index
         return _raw_stream(index), _here if _current_device() == index else torch.cuda.device(device)
