@@ -522,9 +522,9 @@ typedef struct {
  *     w_i = p_n(i);
  *   the emitted token is the smallest i with w_0 + .. + w_i > u_emit[b] * W,
  *     W the sum of all w (inversion of the cumulative distribution).
- * The weights need not sum to one.  Each p and q counts as a number in [0, 1]
- * (NaN and negative values as 0, larger ones as 1), rounded to a multiple of
- * 2^-54; the sums are exact in 128-bit integers, so the token does not depend
+ * The acceptance test takes p and q as they are.  The weights need not sum to
+ * one: in them each p and q counts as a number in [0, 1] (NaN and negative
+ * values as 0, larger ones as 1), rounded to a multiple of 2^-54; the sums are exact in 128-bit integers, so the token does not depend
  * on how the work is split.  u_emit counts as in [0, 1 - 2^-24] (NaN as 0).
  * A row with no weight at all emits -1.
  * Outputs as verify_attn_accept: out_tokens[b, 0 .. n-1] = the accepted
