@@ -622,12 +622,15 @@ def _positions(t, rope, B, T, index):
     raise ValueError(f"positions must be an int32 tensor {list(shape)} on cuda:{index}")
 
 
-def _no_gradient(what, *tensors):
-    """A result without its gradient is refused, not returned."""
-    if any(getattr(t, "requires_grad", False) for t in tensors):
-        raise ValueError(f"{what} is not recorded by autograd and would lose its inputs' gradient: call it under "
-                         "torch.no_grad(), on detached tensors, or in a torch.autograd.Function whose backward rotates "
-                         "with inverse=True")
+def _wants_gradient(t):
+    return getattr(t, "requires_grad", False)
+
+
+def _gradient_lost(what):
+    """The error in place of a result without its gradient."""
+    return ValueError(f"{what} is not recorded by autograd and would lose its inputs' gradient: call it under "
+                      "torch.no_grad(), on detached tensors, or in a torch.autograd.Function whose backward rotates "
+                      "with inverse=True")
 
 
 class Rope:
@@ -693,8 +696,8 @@ def verify_attn_rope(rope: Rope, positions, q, k=None, q_out=None, k_out=None, i
     is not recorded by autograd, and in grad mode tensors that require a gradient
     are refused.  Returns (q_out, k_out), k_out None without ``k``."""
     torch = _torch or _bind_torch()
-    if _grad_mode():
-        _no_gradient("verify_attn_rope", q, k, q_out, k_out)
+    if _grad_mode() and (_wants_gradient(q) or _wants_gradient(k) or _wants_gradient(q_out) or _wants_gradient(k_out)):
+        raise _gradient_lost("verify_attn_rope")
     device, index = _device_of(q, "q")
     code = _float_code(q, "q")
     dtype = q.dtype
@@ -736,8 +739,8 @@ def verify_attn_rope_append(rope: Rope, positions, q, k_new, v_new, k_pages, v_p
     recorded by autograd: in grad mode tensors that require a gradient are
     refused.  Returns the rotated q, contiguous bf16."""
     torch = _torch or _bind_torch()
-    if _grad_mode():
-        _no_gradient("verify_attn_rope_append", q, k_new, v_new, q_out)
+    if _grad_mode() and (_wants_gradient(q) or _wants_gradient(k_new) or _wants_gradient(v_new) or _wants_gradient(q_out)):
+        raise _gradient_lost("verify_attn_rope_append")
     code = _dtype_code(kv_dtype)
     device, index = _device_of(k_new, "k_new")
     bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
