@@ -330,25 +330,31 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     return r;
 }
 
+__device__ __forceinline__ uint64_t fma2_down(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rm.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
 // y = x / s, each rounded to nearest as IEEE division rounds it.  With the reciprocal correctly rounded, one correction by the
 // exact remainder gives a quotient within an ulp and a second one the correctly rounded quotient (Markstein, IBM J. Res. Dev.
 // 34, 1990), two elements an instruction: 8,192 tokens of 32 + 16 heads of 128 into an fp8 cache 41.0 us by divisions, 38.8
 // so.  Remainders are exact where the scale is far from both ends of the exponents; else by divisions.  (A remainder that
-// underflows all the same belongs to a quotient below 2^-10, whose code is 0 either way.)  The quotient is kept negated:
-// the remainder x + s (-q) of a zero is +0 whatever the zero's sign, and what is then added to -q, remainder times -r, is -0,
-// which leaves both zeros as they are (+0 would make -0 a +0, whose e4m3 code is another).
+// underflows all the same belongs to a quotient below 2^-10, whose code is 0 either way.)  The remainders are
+// rounded down, which changes no exact one but those that are 0: -0 then, which added to a zero quotient leaves its sign
+// (a +0 would make -0 a +0, whose e4m3 code is another).
 __device__ __forceinline__ void quotients(const float (&x)[8], float s, float (&y)[8]) {
     if (s >= 8.67361737988403547e-19f && s <= 1.152921504606846976e18f) {  // 2^-60, 2^60
         const float r = __frcp_rn(s);
-        const uint64_t minus_r2 = pair2(-r, -r), s2 = pair2(s, s);
+        const uint64_t r2 = pair2(r, r), minus = pair2(-s, -s);
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
             const uint64_t x2 = pair2(x[e], x[e + 1]);
-            uint64_t minus_q = mul2(x2, minus_r2);
-            minus_q = fma2(fma2(s2, minus_q, x2), minus_r2, minus_q);
-            minus_q = fma2(fma2(s2, minus_q, x2), minus_r2, minus_q);
-            y[e] = -low(minus_q);
-            y[e + 1] = -high(minus_q);
+            uint64_t q = mul2(x2, r2);
+            q = fma2(fma2_down(minus, q, x2), r2, q);
+            q = fma2(fma2_down(minus, q, x2), r2, q);
+            y[e] = low(q);
+            y[e + 1] = high(q);
         }
     } else {
 #pragma unroll
