@@ -308,6 +308,13 @@ def verify_attn_plan_describe(seq_lens, T, num_q_heads, num_kv_heads, head_dim, 
     return info.as_dict(), items[:n]
 
 
+_INT_MAX = 0x7FFFFFFF  # ctypes cuts a larger size to its low 32 bits
+
+
+def _too_large(what, shape):
+    return ValueError(f"{what}: {list(shape)} has a size past 32 bits")
+
+
 def _dev_ptr(t, name, dtypes, allow_none=False):
     import torch
     if t is None:
@@ -445,6 +452,8 @@ def verify_attn_kv_append(k_new, v_new, k_pages, v_pages, k_scale, v_scale, bloc
     B, T_, Hkv, D = k_new.shape
     if int(T) != T_ or tuple(v_new.shape) != tuple(k_new.shape):
         raise ValueError("k_new and v_new must both be [B, T, Hkv, D] with the given T")
+    if B | T_ | Hkv | D | block_table.shape[1] > _INT_MAX:
+        raise _too_large("k_new or block_table", (*k_new.shape, block_table.shape[1]))
     q16 = (torch.bfloat16, torch.int16)
     kvd = _kv_dtypes(code)
     ptrs = [_dev_ptr(k_new, "k_new", q16), _dev_ptr(v_new, "v_new", q16)]
@@ -475,6 +484,8 @@ def verify_attn_lookup_draft(tokens, lens, num_draft, min_match=6, max_match=12,
     if tokens.dim() != 2:
         raise ValueError("tokens must be [num_seqs, stride]")
     B, stride = tokens.shape
+    if B | stride > _INT_MAX:
+        raise _too_large("tokens", tokens.shape)
     i32 = (torch.int32,)
     tp = _dev_ptr(tokens, "tokens", i32)
     lp = _dev_ptr(lens, "lens", i32)
@@ -502,6 +513,8 @@ def verify_attn_accept(target_logits, draft_tokens, temperature, seed, draft_log
     if target_logits.dim() != 3 or draft_tokens.dim() != 2:
         raise ValueError("target_logits must be [B, T+1, V] and draft_tokens [B, T]")
     B, T1, V = target_logits.shape
+    if B | T1 | V > _INT_MAX:
+        raise _too_large("target_logits", target_logits.shape)
     T = T1 - 1
     if tuple(draft_tokens.shape) != (B, T):
         raise ValueError("draft_tokens must be [B, T]")
@@ -603,6 +616,8 @@ def _heads(t, name, dtype, index, shape=None):
         n, s = t.shape, t.stride()
         if (t.dtype is dtype and t.get_device() == index and len(n) == 4 and (s[3] == 1 or n[3] <= 1)
                 and (shape is None or n == shape)):
+            if n[0] | n[1] | n[2] | n[3] > _INT_MAX:
+                raise _too_large(name, n)
             return _Heads(t.data_ptr(), s[0], s[1], s[2], n[2])
     except AttributeError:
         raise ValueError(f"{name} must be a CUDA tensor") from None
@@ -772,6 +787,8 @@ def verify_attn_rope_append(rope: Rope, positions, q, k_new, v_new, k_pages, v_p
     nt = block_table.shape
     if len(nt) != 2 or nt[0] != B:
         raise ValueError(f"block_table must be [{B}, stride], got {list(nt)}")
+    if nt[1] | pages > _INT_MAX:
+        raise _too_large("block_table or k_pages", (nt[1], pages))
     fl = None if flags is None else _ptr(flags, "flags", i32, index)
     st, guard = _launch_on(device, stream)
     with guard:
@@ -806,6 +823,8 @@ def verify_attn_accept_probs(target_probs, draft_tokens, u_accept, u_emit, draft
     if len(n) != 3 or n[1] < 1:
         raise ValueError("target_probs must be [B, T+1, V]")
     B, T1, V = n
+    if B | T1 | V > _INT_MAX:
+        raise _too_large("target_probs", n)
     T = T1 - 1
     p = _prob_rows(target_probs, "target_probs", dtype, index, n)
     q = d = ua = None
@@ -867,6 +886,8 @@ class PagePool:
             flags = torch.zeros(1, dtype=i32, device=device)
         B, stride = block_table.shape
         P = ref_count.shape[0]
+        if B | stride | P > _INT_MAX:
+            raise _too_large("block_table or ref_count", (B, stride, P))
         self.block_table, self.seq_lens, self.ref_count = block_table, seq_lens, ref_count
         self.free_list, self.num_free, self.flags = free_list, num_free, flags
         self.buffers = list(buffers)
@@ -947,6 +968,8 @@ def verify_attn_pages_fork(pool: PagePool, parents, children, lens=None, share=T
     shape = parents.shape
     if len(shape) != 1:
         raise ValueError("parents must be [F]")
+    if shape[0] > _INT_MAX:
+        raise _too_large("parents", shape)
     ch = _ptr(children, "children", i32, index, shape)
     ln = None if lens is None else _ptr(lens, "lens", i32, index, shape)
     st, guard = pool._launch_on(stream)

@@ -1,6 +1,7 @@
 """Edges of the operators around the verify step on the GPU: forks whose sequences are cut back before they write,
 host threads at once, a pool dropped early, the signs of zeros, frequencies above one,
-gradients."""
+gradients, q in place,
+sizes past 32 bits."""
 import numpy as np
 import pytest
 
@@ -248,3 +249,54 @@ def test_rope_at_frequencies_above_one(va, dtype):
     ref = around.rope(xs, pos.tolist(), freq, [0] * 8)
     err = np.abs(got.double().cpu().numpy() - ref)
     assert (err <= rope_bound(xs, 8, False, 1.0, dtype, ref)).all(), err.max()
+
+
+@pytest.mark.parametrize("kv_dtype", ["int8", "bf16"])
+@pytest.mark.parametrize("D,R,pairing", [(64, 22, "half"), (256, 34, "half"), (128, 128, "adjacent"), (256, 34, "adjacent"),
+                                         (128, 96, "half")])
+def test_rope_append_in_place(va, kv_dtype, D, R, pairing):
+    """q as its own output, halves that begin inside a vector and adjacent pairs among them; k and v as [B, H, T, D] and
+    as one head for all."""
+    B, T, Hq, Hkv = 3, 70, 5, 2
+    pages, scale, bt, lens, P = cache_case(9, [70, 100, 81], T, Hkv, D, kv_dtype)
+    q, k, v = (normal(60 + i, B, T, h, D, dtype=torch.bfloat16) for i, h in enumerate((Hq, Hkv, Hkv)))
+    spec = va.verify_attn_rope_spec(R, pairing=pairing)
+    want = run_append(va, spec, None, q, k, v, pages, scale, bt, lens, kv_dtype)
+    work = q.clone()
+    lie = lambda x: x.transpose(1, 2).contiguous().transpose(1, 2)  # noqa: E731
+    got = run_append(va, spec, None, work, lie(k), lie(v), pages, scale, bt, lens, kv_dtype, q_out=work)
+    assert got[0] is work and torch.equal(work, want[0])
+    assert all(np.array_equal(a, b) for a, b in zip(got[1] + got[2], want[1] + want[2]))
+    one = k[:, :, :1].expand(B, T, Hkv, D)
+    a = run_append(va, spec, None, None, one, one, pages, scale, bt, lens, kv_dtype)
+    b = run_append(va, spec, None, None, one.contiguous(), one.contiguous(), pages, scale, bt, lens, kv_dtype)
+    assert all(np.array_equal(x, y) for x, y in zip(a[1] + a[2], b[1] + b[2]))
+
+
+def test_sizes_past_32_bits_are_refused(va):
+    """Sizes whose low 32 bits alone would be a small call (tensors of one element here, broadcast)."""
+    far = 2 ** 32 + 3
+    big = lambda *s, dtype=torch.bfloat16: torch.zeros((), dtype=dtype, device="cuda").expand(*s)  # noqa: E731
+    head = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    spec = va.verify_attn_rope_spec(64)
+    pos = big(1, 1, far, dtype=torch.int32)
+    with pytest.raises(ValueError, match="32 bits"):
+        va.verify_attn_rope(spec, pos, head.expand(1, far, 1, 64))
+    with pytest.raises(ValueError, match="32 bits"):
+        va.verify_attn_rope(spec, i32(0).view(1, 1, 1), head, head.expand(1, 1, far, 64))
+    with pytest.raises(ValueError, match="32 bits"):
+        va.verify_attn_rope_append(spec, None, None, head.expand(1, far, 1, 64), head.expand(1, far, 1, 64), head, head, None,
+                                   None, i32(0).view(1, 1), i32(far % 2 ** 31), "bf16")
+    for shape in ((1, 2, far), (1, far, 4), (far, 1, 4)):
+        with pytest.raises(ValueError, match="32 bits"):
+            va.verify_attn_accept_probs(big(*shape), i32(0).view(1, 1), torch.zeros(1, 1, device="cuda"), torch.zeros(1, device="cuda"))
+    with pytest.raises(ValueError, match="32 bits"):
+        va.PagePool(big(1, far, dtype=torch.int32), i32(0), i32(0), i32(0), i32(1), [])
+    with pytest.raises(ValueError, match="32 bits"):
+        va.PagePool(i32(0).view(1, 1), i32(0), big(far, dtype=torch.int32), big(far, dtype=torch.int32), i32(1), [])
+    with pytest.raises(ValueError, match="32 bits"):
+        va.verify_attn_accept(big(1, 2, far, dtype=torch.float32), i32(0).view(1, 1), torch.zeros(1, device="cuda"), 1)
+    with pytest.raises(ValueError, match="32 bits"):
+        va.verify_attn_lookup_draft(big(1, far, dtype=torch.int32), i32(5), 4)
+    with pytest.raises(ValueError, match="32 bits"):
+        va.verify_attn_kv_append(head, head, head, head, None, None, big(1, far, dtype=torch.int32), i32(1), 1, "bf16")
