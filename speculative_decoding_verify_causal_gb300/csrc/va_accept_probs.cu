@@ -29,9 +29,11 @@
 // one run that holds it again (from L2), eight entries a thread, and finds the
 // entry (one warp alone took 4 us longer at 2,374 entries a run).  Bound: for one
 // sequence (7.2 us) the chain of dependent reads, draft, its probabilities, the
-// row, the run, with the cluster's barrier between them; for 64 (18.5 us, 61 MB
-// from DRAM) that chain, about 11 us of it, and 5 to 7 us of sums, which run at
-// the memory's rate.
+// row, the run, with the cluster's barrier between them.  For 64 (18.5 us, 61 MB
+// from DRAM) the rows: by stamps in a copy of the kernel a CTA's sums take 8 us
+// where one row is read, 12 where two are (medians, all CTAs at once); before
+// them 2 us of drafts and their probabilities, behind them 2.5 us of barriers
+// and, in the CTA that holds the threshold, 2 to 3 us of search.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -49,8 +51,10 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 static_assert(kWarps <= 32, "a warp scans one number per warp of the block");
 // CTAs of a sequence: the most, up to the portable cluster size, that keep all sequences' CTAs resident together (two of this
-// size on each of 152 SMs) and kMinPerCta entries in each.  64 sequences of 151,936 entries: 4 CTAs 19.4 us, 2 23.2, 8 (two
-// waves) 27.7; one sequence: 8 CTAs 7.7 us, 4 8.7, 1 18.7; one of 8,000: 4 CTAs 6.2 us, 1 7.1, 8 5.9.
+// size on each of 152 SMs) and kMinPerCta entries in each.  Measured with a model's drafts, fp32, the rule's choice first:
+// 64 sequences of 152,064 entries 4 CTAs 20.8 us, 2 23.8, 8 (two waves) 26.2; one of them 8 CTAs 8.5 us, 4 10.9, 1 27.2; one
+// of 8,000 entries 2 CTAs 6.6 us, 1 7.3, 4 6.2, 8 6.1; 64 of 8,000 2 CTAs 6.9 us, 1 7.4, 4 8.5.  It is not the best count
+// everywhere: 64 of 16,000 get 4 CTAs (8.9 us) where 2 take 7.5, 16 of 32,000 get 8 (7.8 us) where 4 take 7.2.
 constexpr int kMaxCluster = 8;
 constexpr int kMinPerCta = 2048;
 constexpr int kSlots = 304;
