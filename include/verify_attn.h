@@ -312,9 +312,10 @@ int verify_attn_noalloc_flags(int clear, int *flags, void *stream);
  * Layouts: k_new, v_new bf16 [num_seqs, T, Hkv, D] on the device; the cache,
  * block table (row stride block_table_stride >= 1) and device seq_lens as for
  * verify_attn.  head_dim in {64, 128, 256}.  Checks: rows whose position is
- * negative (seq_lens[b] < T) or whose page is outside [0, num_pages) (when
- * num_pages > 0) are skipped and set bit 0 of *flags (a device int, may be
- * NULL; the library only ORs into it).  Returns VA_OK when enqueued on
+ * negative (seq_lens[b] < T), whose block lies outside the block table's row or
+ * whose page is negative or, when num_pages > 0, not below it, are skipped and
+ * set bit 0 of *flags (a device int, may be NULL; the library only ORs into
+ * it).  Returns VA_OK when enqueued on
  * stream, VA_ERR_INVALID_ARGUMENT for null or non-positive arguments,
  * VA_ERR_UNSUPPORTED for another head_dim or dtype, VA_ERR_CUDA if the launch
  * fails.  Rows of one call write disjoint cache slots as long as the block
@@ -488,8 +489,7 @@ int verify_attn_rope(const va_rope *rope, const va_positions *positions, va_floa
  * a bf16 copy of it.  v is stored as verify_attn_kv_append stores it.
  * positions NULL: every axis is the token's place in its sequence,
  * L_b - T + t.  Cache, block table, seq_lens, num_pages and flags as for
- * verify_attn_kv_append; rows whose block lies outside the block table's row
- * are skipped and flagged as well.  head_dim in {64, 128, 256}; q, k_new and
+ * verify_attn_kv_append.  head_dim in {64, 128, 256}; q, k_new and
  * v_new start on a 16-byte boundary and their strides are multiples of 8;
  * num_seqs * T <= 2^26.  Returns as verify_attn_kv_append. */
 int verify_attn_rope_append(const va_rope *rope, const va_positions *positions, int num_seqs, int T,
@@ -524,8 +524,9 @@ typedef struct {
  *     W the sum of all w (inversion of the cumulative distribution).
  * The acceptance test takes p and q as they are.  The weights need not sum to
  * one: in them each p and q counts as a number in [0, 1] (NaN and negative
- * values as 0, larger ones as 1), rounded to a multiple of 2^-54; the sums are exact in 128-bit integers, so the token does not depend
- * on how the work is split.  u_emit counts as in [0, 1 - 2^-24] (NaN as 0).
+ * values as 0, larger ones as 1), rounded to a multiple of 2^-54; the sums are
+ * exact in 128-bit integers, so the token does not depend on how the work is
+ * split.  u_emit counts as in [0, 1 - 2^-24] (NaN as 0).
  * A row with no weight at all emits -1.
  * Outputs as verify_attn_accept: out_tokens[b, 0 .. n-1] = the accepted
  * drafts, out_tokens[b, n] = the emitted token, -1 after it; num_accepted[b]
@@ -583,9 +584,9 @@ int verify_attn_accept_probs(const va_rows *target_probs, const va_rows *draft_p
  * its block table, must be ordered on one stream.  Results do not depend on
  * timing: whole numbers, counted and ordered by page and sequence.
  * Limits: num_seqs and num_forks <= VA_PAGES_MAX_SEQS, num_pages <=
- * VA_PAGES_MAX_PAGES, num_seqs (num_forks) * block_table_stride <= 2^30.  Every call returns VA_OK when enqueued,
- * VA_ERR_INVALID_ARGUMENT for null or misaligned pointers and sizes out of
- * range, VA_ERR_CUDA if a launch fails. */
+ * VA_PAGES_MAX_PAGES, num_seqs (num_forks) * block_table_stride <= 2^30.
+ * Every call returns VA_OK when enqueued, VA_ERR_INVALID_ARGUMENT for null or
+ * misaligned pointers and sizes out of range, VA_ERR_CUDA if a launch fails. */
 #define VA_PAGES_MAX_SEQS 8192
 #define VA_PAGES_MAX_PAGES (1 << 22)
 #define VA_PAGES_BAD_ENTRY 1

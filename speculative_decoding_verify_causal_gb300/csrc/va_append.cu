@@ -61,9 +61,10 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
     const int g = rem % p.Hkv, bt_row = rem / p.Hkv;
     const int b = bt_row / p.T, t = bt_row % p.T;
     const int pos = p.seq_lens[b] - p.T + t;
+    const bool in_row = pos >= 0 && pos / VA_PAGE_SIZE < p.bt_stride;
     int page = -1;
-    if (pos >= 0) page = p.block_table[(size_t)b * p.bt_stride + pos / VA_PAGE_SIZE];
-    if (pos < 0 || (p.num_pages > 0 && (page < 0 || page >= p.num_pages))) {
+    if (in_row) page = p.block_table[(size_t)b * p.bt_stride + pos / VA_PAGE_SIZE];
+    if (page < 0 || (p.num_pages > 0 && page >= p.num_pages)) {
         if (lane == 0 && p.flags) atomicOr(p.flags, 1);
         return;
     }

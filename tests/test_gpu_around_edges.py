@@ -1,7 +1,7 @@
 """Edges of the operators around the verify step on the GPU: forks whose sequences are cut back before they write,
 host threads at once, a pool dropped early, the signs of zeros, frequencies above one,
 gradients, q in place,
-sizes past 32 bits."""
+sizes past 32 bits, lengths past the block table."""
 import numpy as np
 import pytest
 
@@ -300,3 +300,29 @@ def test_sizes_past_32_bits_are_refused(va):
         va.verify_attn_lookup_draft(big(1, far, dtype=torch.int32), i32(5), 4)
     with pytest.raises(ValueError, match="32 bits"):
         va.verify_attn_kv_append(head, head, head, head, None, None, big(1, far, dtype=torch.int32), i32(1), 1, "bf16")
+
+
+@pytest.mark.parametrize("kv_dtype", ["int8", "bf16"])
+@pytest.mark.parametrize("num_pages", [0, 8])
+def test_append_rows_without_a_page_are_skipped_and_flagged(va, kv_dtype, num_pages):
+    """A device length past what the table's row holds, whose rows do not go by the next row's entries, and an entry of -1,
+    as a page pool's table has it where nothing is held; with and without the count of pages."""
+    T, Hkv, D = 4, 2, 64
+    kind = torch.bfloat16 if kv_dtype == "bf16" else torch.int8
+    kp, vp = (torch.zeros(8, 16, Hkv, D, dtype=kind, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros(8, 16, Hkv, device="cuda") for _ in range(2))
+    flags = i32(0)
+    x = normal(1, 2, T, Hkv, D, dtype=torch.bfloat16)
+    table = i32(0, 1, 2, 3, 4, 5).view(2, 3)[:, :2].contiguous()  # rows of two blocks: 0 1, 3 4
+    va.verify_attn_kv_append(x, x, kp, vp, ks, vs, table, i32(34, 10), T, kv_dtype, num_pages=num_pages, flags=flags)
+    torch.cuda.synchronize()
+    assert flags.item() == 1
+    written = (vp.float().abs().amax((2, 3)) > 0).nonzero().tolist()
+    assert written == [[1, 14], [1, 15], [3, 6], [3, 7], [3, 8], [3, 9]]
+    flags.zero_()
+    va.verify_attn_kv_append(x, x, kp, vp, ks, vs, i32(-1, 5, 6, -1).view(2, 2), i32(18, 18), T, kv_dtype, num_pages=num_pages,
+                             flags=flags)
+    torch.cuda.synchronize()
+    assert flags.item() == 1
+    written = (vp[4:].float().abs().amax((2, 3)) > 0).nonzero().tolist()
+    assert written == [[1, 0], [1, 1], [2, 14], [2, 15]]
