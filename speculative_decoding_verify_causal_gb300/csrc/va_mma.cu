@@ -1099,28 +1099,26 @@ bool make_map(CUtensorMap *m, const void *base, int D, int bits, int Hkv, int nu
 
 template <int D, int DT>
 cudaError_t launch_one(const PartialParams &p, int n, cudaStream_t s) {
-    int nst = 0;
-    if (Cfg<D, DT>::kQuant) {
-        nst = kMaxRawStages;
-        while (nst > kMinRawStages && Smem<D, DT>(p.Hkv, nst).total + 1024 > kMaxSmemPerBlock) --nst;
-    }
-    const Smem<D, DT> L(p.Hkv, nst);
-    const size_t smem = L.total + 1024;  // + alignment slack
-    if (smem > kMaxSmemPerBlock) return cudaErrorInvalidConfiguration;
-    auto k = mma_partial_kernel<D, DT>;
-    // before the tensor maps: they are made by the driver, which needs the context that this first runtime call binds to a
-    // host thread that has made none
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
     MmaParams mp;
     mp.p = p;
-    mp.raw_stages = nst;
     if (!make_map(&mp.tm_k, p.k_pages, D, Cfg<D, DT>::kBits, p.Hkv, p.num_pages) ||
         !make_map(&mp.tm_v, p.v_pages, D, Cfg<D, DT>::kBits, p.Hkv, p.num_pages))
         return cudaErrorInvalidValue;
     memset(&mp.tm_o, 0, sizeof(mp.tm_o));
     if (p.num_parts > 0 && !make_part_map(&mp.tm_o, p.o_part, D, p.rows_per_group, p.num_parts))
         return cudaErrorInvalidValue;
+    int nst = 0;
+    if (Cfg<D, DT>::kQuant) {
+        nst = kMaxRawStages;
+        while (nst > kMinRawStages && Smem<D, DT>(p.Hkv, nst).total + 1024 > kMaxSmemPerBlock) --nst;
+    }
+    mp.raw_stages = nst;
+    const Smem<D, DT> L(p.Hkv, nst);
+    const size_t smem = L.total + 1024;  // + alignment slack
+    if (smem > kMaxSmemPerBlock) return cudaErrorInvalidConfiguration;
+    auto k = mma_partial_kernel<D, DT>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
     return launch_pdl(k, dim3(n), dim3(Cfg<D, DT>::kThreads), smem, s, mp);
 }
 

@@ -538,6 +538,19 @@ int verify_attn_with_plan(const va_plan *p, const void *q, const void *k_pages,
     if (!va::aligned_for(p->path, p->kv_dtype, q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens,
                          out, lse))
         return VA_ERR_INVALID_ARGUMENT;
+    // The tensor maps of the tcgen05 path are made by the driver, which needs a context; a host thread has one from its first
+    // runtime call on.  A question about the stream is one that is allowed while it is captured.
+    thread_local bool bound = false;
+    cudaStreamCaptureStatus capture;
+    if (!bound) {
+        const cudaError_t asked = cudaStreamIsCapturing(s, &capture);
+        if (asked != cudaSuccess) {
+            va::note_cuda_error(asked);
+            cudaGetLastError();
+            return VA_ERR_CUDA;
+        }
+        bound = true;
+    }
     if (p->ev_before && cudaEventRecordWithFlags(p->ev_before, s, cudaEventRecordExternal) != cudaSuccess)
         return VA_ERR_CUDA;
     cudaError_t e = p->path == VA_PATH_MMA
