@@ -662,6 +662,54 @@ int verify_attn_pages_fork(const va_page_pool *pool, const int32_t *parents, con
  * can be given to something else. */
 int verify_attn_pages_compact(const va_page_pool *pool, void *stream);
 
+/* Attention of chunks of new tokens over the paged cache: a prompt that is
+ * worked in chunks, and batches in which some requests add a chunk and others
+ * one token.  Sequence b ends with n_b = chunk_lens[b] new tokens (0: it takes
+ * no part) whose keys and values are in the cache already, L_b = seq_lens[b]
+ * tokens with them.  The new tokens of all sequences lie one after the other:
+ * token t of sequence b is row n_0 + .. + n_(b-1) + t of q, out and lse.
+ *     s_j = (1/sqrt(head_dim)) <q[row, h, :], Khat[j]>,  j <= L_b - n_b + t
+ *     lse = ln sum_j exp(s_j),   out = sum_j exp(s_j - lse) Vhat[j]
+ * with kv head h / G, decode, cache layouts and scales as for verify_attn.
+ * out depends on no key that its token does not see, whatever lies there.
+ *
+ * A plan is made from the lengths on the host, as verify_attn_plan's, and owns
+ * its work list and the partials' workspace on the current device; calls on one
+ * plan must be ordered on one stream.  0 <= n_b <= L_b <= 2^30, the sum of n_b
+ * at most 2^30, num_q_heads a multiple of num_kv_heads and at most 128 times
+ * it, head_dim in {64, 128, 256}.  num_sms 0: the current device's. */
+typedef struct va_chunk_plan va_chunk_plan;
+typedef struct {
+    int num_seqs, num_q_heads, num_kv_heads, head_dim, kv_dtype;
+    int num_tokens;       /* new tokens of all sequences */
+    int max_blocks;       /* block-table entries that a row must have */
+    int num_items;        /* CTAs of the attention kernel */
+    int num_split_groups; /* tiles of rows whose keys are split, merged by a second kernel */
+    int max_item_keys;    /* the longest range of keys of a CTA */
+    int num_sms;
+    long long workspace_bytes;
+} va_chunk_plan_info;
+int verify_attn_chunk_plan(const int32_t *chunk_lens_host, const int32_t *seq_lens_host, int num_seqs,
+                           int num_q_heads, int num_kv_heads, int head_dim, va_kv_dtype kv_dtype,
+                           int num_sms, va_chunk_plan **out_plan);
+/* As verify_attn_plan_destroy, _get_info and _device_flags (bits 0 and 2). */
+void verify_attn_chunk_plan_destroy(va_chunk_plan *plan);
+int verify_attn_chunk_plan_get_info(const va_chunk_plan *plan, va_chunk_plan_info *info);
+int verify_attn_chunk_plan_device_flags(const va_chunk_plan *plan, int clear, int *flags, void *stream);
+
+/* q: bf16, num_heads = num_q_heads; strides positive multiples of 8, data on a
+ * 16-byte boundary (stride_seq is not used).  out bf16 [tokens, num_q_heads,
+ * head_dim] on a 16-byte boundary, lse fp32 [tokens, num_q_heads] or NULL; rows
+ * behind the last sequence's are left as they are.  out may not overlap q.
+ * block_table int32 [num_seqs, block_table_stride].  num_pages > 0: entries
+ * outside [0, num_pages) are skipped (their keys read as absent; a row without
+ * any key is 0 with lse -inf) and flagged; 0: unchecked.  Returns VA_OK when
+ * enqueued, VA_ERR_NO_PLAN, VA_ERR_INVALID_ARGUMENT, VA_ERR_CUDA. */
+int verify_attn_chunk(const va_chunk_plan *plan, const va_heads *q, const void *k_pages,
+                      const void *v_pages, const float *k_scale, const float *v_scale,
+                      const int32_t *block_table, int block_table_stride, int num_pages, void *out,
+                      float *lse, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -74,6 +74,14 @@ class PlanInfo(ctypes.Structure):
         return {n: getattr(self, n) for n, _ in self._fields_}
 
 
+class ChunkPlanInfo(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "num_seqs", "num_q_heads", "num_kv_heads", "head_dim", "kv_dtype", "num_tokens", "max_blocks", "num_items",
+        "num_split_groups", "max_item_keys", "num_sms")] + [("workspace_bytes", ctypes.c_longlong)]
+
+    as_dict = PlanInfo.as_dict
+
+
 class _Rope(ctypes.Structure):
     _fields_ = [("turn", ctypes.c_uint64 * ROPE_MAX_PAIRS), ("axis", ctypes.c_uint8 * ROPE_MAX_PAIRS),
                 ("num_pairs", ctypes.c_int32), ("num_axes", ctypes.c_int32), ("adjacent", ctypes.c_int32),
@@ -162,6 +170,15 @@ def _load():
         lib.verify_attn_pages_resize_ex.argtypes = [P, P, P, P]
         lib.verify_attn_pages_fork.argtypes = [P, P, P, P, I, I, P]
         lib.verify_attn_pages_compact.argtypes = [P, P]
+        lib.verify_attn_chunk_plan.argtypes = [P, P, I, I, I, I, I, I, ctypes.POINTER(P)]
+        lib.verify_attn_chunk_plan_destroy.argtypes = [P]
+        lib.verify_attn_chunk_plan_destroy.restype = None
+        lib.verify_attn_chunk_plan_get_info.argtypes = [P, ctypes.POINTER(ChunkPlanInfo)]
+        lib.verify_attn_chunk_plan_device_flags.argtypes = [P, I, ctypes.POINTER(I), P]
+        lib.verify_attn_chunk.argtypes = [P, H, P, P, P, P, P, I, I, P, P, P]
+        for f in ("verify_attn_chunk_plan", "verify_attn_chunk_plan_get_info", "verify_attn_chunk_plan_device_flags",
+                  "verify_attn_chunk"):
+            getattr(lib, f).restype = I
         for f in ("verify_attn_rope_init", "verify_attn_rope", "verify_attn_rope_append", "verify_attn_accept_probs",
                   "verify_attn_pages_resize", "verify_attn_pages_resize_ex", "verify_attn_pages_fork",
                   "verify_attn_pages_compact"):
@@ -648,6 +665,11 @@ def _gradient_lost(what):
                       "with inverse=True")
 
 
+def _gradient_refused(what):
+    return ValueError(f"{what} is not recorded by autograd and would lose its inputs' gradient: call it under "
+                      "torch.no_grad() or on detached tensors")
+
+
 class Rope:
     """A rotation (``va_rope``): host data, made by ``verify_attn_rope_spec``."""
 
@@ -998,7 +1020,145 @@ def verify_attn_pages_flags(pool: PagePool, clear=True) -> int:
     return flags
 
 
+class ChunkPlan:
+    """Owning handle of a ``va_chunk_plan`` (freed on ``destroy()`` or collection)."""
+
+    def __init__(self, handle, shape, index):
+        self._h = ctypes.c_void_p(handle)
+        self._index = index  # CUDA device that the plan's memory is on
+        self.num_seqs, self.num_q_heads, self.num_kv_heads, self.head_dim, self.kv_dtype, self.num_tokens = shape
+
+    @property
+    def handle(self):
+        return self._h
+
+    def info(self) -> dict:
+        info = ChunkPlanInfo()
+        _check(_load().verify_attn_chunk_plan_get_info(self._h, ctypes.byref(info)), "verify_attn_chunk_plan_get_info")
+        return info.as_dict()
+
+    def destroy(self):
+        if self._h and self._h.value:
+            _load().verify_attn_chunk_plan_destroy(self._h)
+            self._h = ctypes.c_void_p(0)
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass
+
+
+def verify_attn_chunk_plan(chunk_lens, seq_lens, num_q_heads, num_kv_heads, head_dim, kv_dtype, num_sms=0) -> ChunkPlan:
+    """Plan a batch in which sequence b ends with ``chunk_lens[b]`` new tokens (0: it
+    takes no part) of its ``seq_lens[b]`` cached ones, both on the host.  The plan
+    owns its workspace on the current CUDA device; calls on it must be ordered on
+    one stream."""
+    lib = _load()
+    torch = _torch or _bind_torch()
+    new, lens = _host_lens(chunk_lens), _host_lens(seq_lens)
+    if len(new) != len(lens):
+        raise ValueError(f"{len(new)} chunk_lens and {len(lens)} seq_lens")
+    code = _dtype_code(kv_dtype)
+    out = ctypes.c_void_p()
+    _check(lib.verify_attn_chunk_plan(new.ctypes.data, lens.ctypes.data, len(new), int(num_q_heads), int(num_kv_heads),
+                                      int(head_dim), code, int(num_sms), ctypes.byref(out)), "verify_attn_chunk_plan")
+    return ChunkPlan(out.value, (len(new), int(num_q_heads), int(num_kv_heads), int(head_dim), code, int(new.sum())),
+                     torch.cuda.current_device())
+
+
+def verify_attn_chunk_plan_destroy(plan: ChunkPlan):
+    plan.destroy()
+
+
+def verify_attn_chunk_plan_device_flags(plan: ChunkPlan, clear=True, stream=None) -> int:
+    """The plan's flag word (bit 0: a block-table entry outside the pool was
+    skipped, bit 2: a wait gave up), cleared by default.  Waits for the stream."""
+    st, guard = _launch_on(_torch.device("cuda", plan._index), stream)
+    flags = ctypes.c_int(0)
+    with guard:
+        rc = _load().verify_attn_chunk_plan_device_flags(plan._h, int(bool(clear)), ctypes.byref(flags), st)
+    _check(rc, "verify_attn_chunk_plan_device_flags")
+    return flags.value
+
+
+def _chunk_q(plan, q):
+    """q [tokens or more, Hq, D] as a ``va_heads``, its device and the device's index."""
+    device, index = _device_of(q, "q")
+    n, s = q.shape, q.stride()
+    if (q.dtype is not _torch.bfloat16 or len(n) != 3 or n[0] < plan.num_tokens or n[1] != plan.num_q_heads
+            or n[2] != plan.head_dim or s[2] != 1):
+        raise ValueError(f"q must be a bfloat16 tensor [{plan.num_tokens}, {plan.num_q_heads}, {plan.head_dim}], contiguous "
+                         f"in its last dimension, got {q.dtype} {list(n)} with strides {list(s)}")
+    if index != plan._index:
+        raise ValueError(f"q is on cuda:{index}, the plan on cuda:{plan._index}")
+    return _Heads(q.data_ptr(), 0, s[0], s[1], n[1]), device, index
+
+
+def _chunk_cache(plan, pages, scale, what, index):
+    """Addresses of one of the cache's pools and its scales, and the number of pages."""
+    code = plan.kv_dtype
+    ptr = _ptr_of(pages, f"{what}_pages", _CACHE_TYPES[code], index)
+    row = plan.head_dim * (16 if code == VA_BF16 else 4 if code == VA_INT4 else 2 if code == VA_INT2 else 8) // 8
+    n = pages.shape
+    cache = (n[0] if len(n) else 0, PAGE_SIZE, plan.num_kv_heads, row // 2 if code == VA_BF16 else row)
+    if n != cache:
+        raise ValueError(f"{what}_pages must be [num_pages, {PAGE_SIZE}, {plan.num_kv_heads}, {cache[3]}], got {list(n)}")
+    if cache[0] > _INT_MAX:
+        raise _too_large(f"{what}_pages", n)
+    return ptr, None if code == VA_BF16 else _ptr(scale, f"{what}_scale", _torch.float32, index, cache[:3]), cache[0]
+
+
+def _chunk_table(plan, block_table, index):
+    ptr = _ptr(block_table, "block_table", _torch.int32, index)
+    n = block_table.shape
+    if len(n) != 2 or n[0] != plan.num_seqs:
+        raise ValueError(f"block_table must be [{plan.num_seqs}, stride], got {list(n)}")
+    if n[1] > _INT_MAX:
+        raise _too_large("block_table", n)
+    return ptr, n[1]
+
+
+def verify_attn_chunk(plan: ChunkPlan, q, k_pages, v_pages, k_scale, v_scale, block_table, out=None, lse=None,
+                      num_pages=0, stream=None):
+    """Attention of chunks of new tokens over the paged cache: ``q`` bf16 ``[tokens,
+    Hq, D]``, the new tokens of all sequences one after the other (any strides that
+    are multiples of 8 elements with a contiguous last dimension, for instance a
+    slice of a fused projection; rows behind the plan's tokens are not read).  The
+    new keys and values are in the cache already.  ``num_pages``: pages that the
+    block table may name (default: all of the pool's); others are skipped and
+    flagged.  ``out`` (bf16) and ``lse`` (fp32 ``[tokens, Hq]``) default to new tensors
+    with as many rows as ``q``; rows behind the plan's tokens are left as they are.
+    Not recorded by autograd: in grad mode tensors that require a gradient are
+    refused.  Returns (out, lse)."""
+    torch = _torch or _bind_torch()
+    if _grad_mode() and (_wants_gradient(q) or _wants_gradient(k_pages) or _wants_gradient(v_pages)
+                         or _wants_gradient(k_scale) or _wants_gradient(v_scale) or _wants_gradient(out)):
+        raise _gradient_refused("verify_attn_chunk")
+    heads, device, index = _chunk_q(plan, q)
+    kp, ks, pages = _chunk_cache(plan, k_pages, k_scale, "k", index)
+    vp, vs, pages_v = _chunk_cache(plan, v_pages, v_scale, "v", index)
+    if pages_v != pages or num_pages > pages:
+        raise ValueError(f"k_pages has {pages} pages, v_pages {pages_v}, num_pages is {num_pages}")
+    bt, stride = _chunk_table(plan, block_table, index)
+    n = q.shape
+    st, guard = _launch_on(device, stream)
+    with guard:
+        if out is None:
+            out = torch.empty(n, dtype=torch.bfloat16, device=device)
+        if lse is None:
+            lse = torch.empty(n[:2], dtype=torch.float32, device=device)
+        rc = (_lib or _load()).verify_attn_chunk(
+            plan._h, heads, kp, vp, ks, vs, bt, stride, num_pages or pages, _ptr(out, "out", torch.bfloat16, index, n),
+            _ptr(lse, "lse", torch.float32, index, n[:2]), st)
+    if rc:
+        _check(rc, "verify_attn_chunk")
+    return out, lse
+
+
 __all__ = [
+    "ChunkPlan", "verify_attn_chunk_plan", "verify_attn_chunk_plan_destroy", "verify_attn_chunk_plan_device_flags",
+    "verify_attn_chunk",
     "Rope", "verify_attn_rope_spec", "verify_attn_rope", "verify_attn_rope_append", "verify_attn_accept_probs",
     "PagePool", "verify_attn_pages_resize", "verify_attn_pages_fork", "verify_attn_pages_compact",
     "verify_attn_pages_flags",

@@ -1,0 +1,863 @@
+// Attention of ragged chunks of new tokens over the paged cache, for sm_103a (tcgen05 + TMEM + TMA).
+//
+// For token t of a chunk of n that ends a sequence of L cached tokens, and query head h of kv head g:
+//     s_j = <q, K_j> / sqrt(D), j <= L - n + t;   lse = ln sum_j exp(s_j);   out = sum_j exp(s_j - lse) V_j.
+// A tile is 128 packed rows: `tpt` tokens of one sequence with all query heads of one kv head (row = token * G +
+// head), so each key and value is read once for all of them.  A CTA takes one item: one tile of rows (head_dim 256)
+// or up to two (64, 128) over a range of keys.
+//
+// The MMA warp walks "steps".  Step k of a two-tile item is (rows k % 2, keys k / 2); of a one-tile item it is (keys
+// k).  Either way scores alternate between two tensor-memory slots, and the order is S(0), S(1), then P(k) V(k),
+// S(k + 2): while the softmax of one slot runs, the tensor pipe works on the other.  P overwrites S in its slot; S(k
+// + 2) is issued behind P(k) V(k) by the same thread, and tensor instructions run in their order.
+//   producer warp   page ids from the block table, then TMA boxes (16 slots of one page and head) into the ring
+//   dequant warps   (quantised caches) raw panel -> fp16 panel, exact, in the MMA's swizzled layout; keys' scales
+//   MMA warp        one thread issues everything
+//   softmax warps   four per tile of rows, a thread per row: k scale, mask, running maximum (moved, and O rescaled,
+//                   only when it grows by more than 2^8), P * v_scale * 2^beta back over S; at the end O / l and lse
+// A panel is 128 keys by min(D, 128) elements: what one ring slot holds.
+//
+// P is rounded to the type of the values' tile: bf16 for a bf16 cache, fp16 for codes (with v_scale; 2^beta, a power
+// of two by each row's largest v scale in the tile, keeps that product in fp16's normal range).  Scores, maxima,
+// sums and O are binary32.
+//
+// Keys that a row must not see: their scores are replaced, not multiplied, and elements of V that are not finite are
+// taken out of the tiles that the mask cuts (0 times infinity is not 0); rows that do see them get them back at the
+// end.  Waits give up after 2 s (flag bit 2).
+#include <math.h>
+
+#include <cstring>
+
+#include "va_chunk.h"
+#include "va_convert.cuh"
+
+namespace va {
+namespace {
+
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr float kRescaleLog2 = 8.0f;
+constexpr int kKeys = kChunkKeys;
+constexpr int kPages = kKeys / VA_PAGE_SIZE;  // pages of a tile of keys
+constexpr int kScaleRing = 4;
+constexpr int kScaleFloats = 2 * kKeys + 4;   // k scales, v scales, the largest v scale of each 32 keys
+constexpr int kBadRing = 16;                  // tiles whose bad pages are remembered: more than the ring holds ahead
+constexpr int kMaxStages = 8;
+
+template <int D, int DT>
+struct Cfg {
+    static constexpr bool kQuant = DT != VA_BF16;
+    static constexpr int kTiles = chunk_tiles(D);
+    static constexpr int kPanelD = D < 128 ? D : 128;
+    static constexpr int kPanels = D / kPanelD;       // panels of a K or V tile
+    static constexpr int kChunks = kPanelD / 64;      // 64-element chunks of a panel
+    static constexpr int kChunkBytes = kKeys * 128;
+    static constexpr int kPanelBytes = kChunks * kChunkBytes;
+    static constexpr int kBits = DT == VA_BF16 ? 16 : DT == VA_INT4 ? 4 : DT == VA_INT2 ? 2 : 8;
+    static constexpr int kRawRow = kPanelD * kBits / 8;  // bytes of a row of a raw panel
+    static constexpr int kRawBytes = kKeys * kRawRow;
+    static constexpr int kQBytes = kMmaRows * D * 2;
+    static constexpr int kStages = kQuant ? (D == 64 ? 6 : 3) : (D == 64 ? 8 : 5);
+    static constexpr int kRawStages = kQuant ? (D == 64 ? 6 : 3) : 0;
+    static constexpr int kSoftmaxWarps = 4 * kTiles;
+    static constexpr int kDequantWarps = kQuant ? 4 : 0;
+    static constexpr int kProducerWarp = kSoftmaxWarps + kDequantWarps;
+    static constexpr int kMmaWarp = kProducerWarp + 1;
+    static constexpr int kThreads = (kMmaWarp + 1) * 32;
+    // all of a row's scores stay in registers where the block's threads leave 200 of them
+    static constexpr bool kKeep = kThreads <= 320;
+    static constexpr uint32_t kOCol = 2 * kKeys;  // S slots at 0 and 128
+    static constexpr int kQ = 0;
+    static constexpr int kConv = kTiles * kQBytes;
+    static constexpr int kRaw = kConv + kStages * kPanelBytes;
+    static constexpr int kScale = kRaw + kRawStages * kRawBytes;
+    static constexpr int kBad = kScale + (kQuant ? kScaleRing * kScaleFloats * 4 : 0);
+    static constexpr int kBars = kBad + kBadRing * 4;
+    static constexpr int kSmem = kBars + 64 * 8 + 1024;  // and slack for the alignment
+    static_assert(kSmem <= (int)kMaxSmemPerBlock, "shared memory");
+};
+
+enum Bar : int {
+    kFull = 0,                       // panel in the MMA's layout
+    kEmpty = kFull + kMaxStages,     // and read
+    kRawFull = kEmpty + kMaxStages,
+    kRawEmpty = kRawFull + kMaxStages,
+    kSFull = kRawEmpty + kMaxStages,  // scores of a slot
+    kPFull = kSFull + 2,              // its probabilities
+    kODone = kPFull + 2,              // its product with V
+    kOFinal = kODone + 2,
+    kQFull = kOFinal + 1,             // q from memory
+    kQReady = kQFull + 1,             // q as the MMA takes it
+    kScaleFree = kQReady + 1,
+    kSwept = kScaleFree + kScaleRing,  // the softmax warps have gone through an edge tile's values
+    kNumBars = kSwept + 1,
+    kTmemSlot = 62,
+    kPoison = 63,
+};
+static_assert(kNumBars <= kTmemSlot, "barrier block");
+
+struct Args {
+    CUtensorMap tm_q, tm_k, tm_v;  // 64-byte aligned members first
+    ChunkParams p;
+};
+
+// Place of a panel in the order in which the MMA warp uses them: K0 V0 K1 V1 .. with two tiles of rows, K0 K1 V0 K2
+// V1 .. with one (its next scores are issued before the product).
+__device__ __forceinline__ int k_entry(int i, bool two) { return two ? 2 * i : (i == 0 ? 0 : 2 * i - 1); }
+__device__ __forceinline__ int v_entry(int i, bool two, int n) {
+    return two ? 2 * i + 1 : (i == n - 1 ? 2 * n - 1 : 2 * i + 2);
+}
+// The reverse: which tile, and whether it is V.
+__device__ __forceinline__ int entry_tile(int e, bool two, int n, bool &v) {
+    if (two) {
+        v = e & 1;
+        return e >> 1;
+    }
+    if (e == 0) return v = false, 0;
+    if (e == 2 * n - 1) return v = true, n - 1;
+    v = !(e & 1);
+    return v ? (e - 2) >> 1 : (e + 1) >> 1;
+}
+
+__device__ __forceinline__ bool half_finite(uint32_t w, uint32_t exponent) {  // both 16-bit elements of a word
+    return (w & exponent) != exponent && ((w >> 16) & exponent) != exponent;
+}
+
+// Element d of a cached row, as a number (the slow path of values that are not finite).
+template <int D, int DT>
+__device__ float cached_value(const void *pages, const float *scale, size_t row, int d) {
+    if constexpr (DT == VA_BF16) {
+        return bf16_bits_to_float(static_cast<const uint16_t *>(pages)[row * D + d]);
+    } else if constexpr (DT == VA_FP8_E4M3) {
+        const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<const __nv_fp8_storage_t *>(pages)[row * D + d], __NV_E4M3);
+        return __half2float(*reinterpret_cast<const __half *>(&h)) * scale[row];
+    } else {
+        return 0.f;  // codes are always finite
+    }
+}
+
+template <int D, int DT>
+__global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __grid_constant__ Args args) {
+    using C = Cfg<D, DT>;
+    const ChunkParams &p = args.p;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                            ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = smem_u32(smem);
+    auto bar = [&](int i) { return sbase + C::kBars + 8u * i; };
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    griddep_wait();
+    const ChunkItem it = p.items[blockIdx.x];
+    const int G = p.G, tpt = p.tpt;
+    const bool two = C::kTiles == 2 && it.nt > tpt;  // both tiles of rows hold something
+    const int nq = two ? 2 : 1;
+    const int ntiles = (it.k_end - it.k_begin + kKeys - 1) / kKeys;
+    const int lp0 = it.k_begin / VA_PAGE_SIZE;  // k_begin is a multiple of a tile
+    const int npages = (it.k_end + VA_PAGE_SIZE - 1) / VA_PAGE_SIZE - lp0;
+    const int32_t *bt = p.block_table + (size_t)it.b * p.bt_stride + lp0;
+
+    if (warp == C::kProducerWarp && lane == 0) {
+        prefetch_tensormap(&args.tm_q);
+        prefetch_tensormap(&args.tm_k);
+        prefetch_tensormap(&args.tm_v);
+        for (int i = 0; i < kMaxStages; ++i) {
+            mbar_init(bar(kFull + i), C::kQuant ? C::kDequantWarps : 1);
+            mbar_init(bar(kEmpty + i), 1);
+            mbar_init(bar(kRawFull + i), 1);
+            mbar_init(bar(kRawEmpty + i), C::kQuant ? C::kDequantWarps : 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(kSFull + i), 1);
+            mbar_init(bar(kPFull + i), 4);
+            mbar_init(bar(kODone + i), 1);
+        }
+        mbar_init(bar(kOFinal), 1);
+        mbar_init(bar(kQFull), 1);
+        mbar_init(bar(kQReady), 4 * nq);
+        mbar_init(bar(kSwept), 4 * nq);
+        for (int i = 0; i < kScaleRing; ++i) mbar_init(bar(kScaleFree + i), 4 * nq);
+        sts_u32(bar(kPoison), 0u);
+        fence_barrier_init();
+    } else if (warp == C::kMmaWarp) {
+        tmem_alloc(bar(kTmemSlot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = lds_u32(bar(kTmemSlot));
+    bool ok = true;
+
+    if (warp == C::kProducerWarp) {
+        // ------------------------------------------------------------ producer
+        // q: one box of 64 elements x G heads x tpt tokens per tile of rows and chunk; tokens past q's end read 0
+        if (lane == 0) mbar_arrive_expect_tx(bar(kQFull), (uint32_t)(nq * (D / 64) * G * tpt * 128));
+        __syncwarp();
+        if (lane < nq * (D / 64)) {
+            const int q = lane / (D / 64), c = lane % (D / 64);
+            tma_load_3d(sbase + C::kQ + q * C::kQBytes + c * C::kChunkBytes, &args.tm_q, c * 64, it.kvh * G,
+                        it.q0 + q * tpt, bar(kQFull));
+        }
+        // page ids: 32 at a time, one batch ahead
+        auto load_ids = [&](int i0) -> int {  // of the tiles i0 .. i0 + 3
+            const int k = i0 * kPages + lane;
+            return k < npages ? __ldg(bt + k) : 0;
+        };
+        int ids_k = load_ids(0), next_k = load_ids(4), at_k = 0;  // K and V walk the table apart
+        int ids_v = ids_k, next_v = next_k, at_v = 0;
+        const int total = 2 * ntiles * C::kPanels;
+        int issued = 0;
+        for (int e = 0; e < total; ++e) {
+            bool v;
+            const int i = entry_tile(e / C::kPanels, two, ntiles, v);
+            const int pp = e % C::kPanels;
+            int &ids = v ? ids_v : ids_k, &next = v ? next_v : next_k, &at = v ? at_v : at_k;
+            if (i / 4 != at) {
+                at = i / 4;
+                ids = next;
+                next = load_ids(4 * at + 4);
+            }
+            const int npg = min(kPages, npages - i * kPages);
+            int page = __shfl_sync(0xffffffffu, ids, (i % 4) * kPages + lane % kPages);
+            const bool bad = p.num_pages > 0 && (page < 0 || page >= p.num_pages) && lane < npg;
+            const uint32_t bads = __ballot_sync(0xffffffffu, bad);
+            if (bad) page = 0;
+            const int slot = C::kQuant ? e % (C::kRawStages ? C::kRawStages : 1) : e % C::kStages;
+            const int use = C::kQuant ? e / (C::kRawStages ? C::kRawStages : 1) : e / C::kStages;
+            if (use > 0) {
+                ok = mbar_wait(bar((C::kQuant ? kRawEmpty : kEmpty) + slot), (use & 1) ^ 1, kWaitNs);
+                ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+                if (!ok) break;
+            }
+            page = __shfl_sync(0xffffffffu, page, lane % kPages);
+            const CUtensorMap *map = v ? &args.tm_v : &args.tm_k;
+            const uint32_t full = bar((C::kQuant ? kRawFull : kFull) + slot);
+            if (lane == 0) {
+                if (!v && pp == 0) {
+                    sts_u32(sbase + C::kBad + 4u * (i % kBadRing), bads);
+                    if (bads) atomicOr(p.flags, kFlagBadPage);
+                }
+                mbar_arrive_expect_tx(full, (uint32_t)npg * (C::kQuant ? VA_PAGE_SIZE * C::kRawRow
+                                                                       : VA_PAGE_SIZE * 128 * C::kChunks));
+            }
+            __syncwarp();
+            if constexpr (C::kQuant) {
+                if (lane < npg)
+                    tma_load_4d(sbase + C::kRaw + slot * C::kRawBytes + lane * VA_PAGE_SIZE * C::kRawRow, map,
+                                pp * C::kRawRow, it.kvh, 0, page, full);
+            } else {
+                const int pg = lane % kPages, c = lane / kPages;
+                if (pg < npg && c < C::kChunks)
+                    tma_load_4d(sbase + C::kConv + slot * C::kPanelBytes + c * C::kChunkBytes + pg * VA_PAGE_SIZE * 128, map,
+                                pp * C::kPanelD + c * 64, it.kvh, 0, page, full);
+            }
+            __syncwarp();
+            issued = e + 1;
+        }
+        // every issued copy lands before the CTA ends
+        if (lane == 0) {
+            const int n = C::kQuant ? C::kRawStages : C::kStages;
+            for (int e = max(0, issued - n); e < issued; ++e)
+                if (!mbar_wait(bar((C::kQuant ? kRawFull : kFull) + e % n), (e / n) & 1, kWaitNs)) ok = false;
+            if (!mbar_wait(bar(kQFull), 0, kWaitNs)) ok = false;
+        }
+    } else if (warp == C::kMmaWarp) {
+        // ------------------------------------------------------------ MMA issue
+        if (lane == 0) {
+            constexpr int kAB = C::kQuant ? 0 : 1;
+            constexpr uint32_t idS = idesc_f16(128, kKeys, kAB, 0, 0);
+            constexpr uint32_t idO = idesc_f16(128, C::kPanelD, kAB, 0, 1);
+            // K-major operands: 8-row groups 1024 bytes apart; V is MN-major, its 64-element chunks kChunkBytes apart
+            const uint64_t qdesc = smem_desc(sbase + C::kQ, 16, 1024, 2);
+            const uint64_t kdesc = smem_desc(sbase + C::kConv, 16, 1024, 2);
+            const uint64_t vdesc = smem_desc(sbase + C::kConv, C::kChunkBytes, 1024, 2);
+            const int steps = nq * ntiles;
+            auto scores = [&](int k) -> bool {
+                const int q = two ? k & 1 : 0, i = two ? k >> 1 : k;
+                for (int pp = 0; pp < C::kPanels; ++pp) {
+                    const int e = k_entry(i, two) * C::kPanels + pp, slot = e % C::kStages;
+                    if (!mbar_wait(bar(kFull + slot), (e / C::kStages) & 1, kWaitNs)) return false;
+                    tc_fence_after();
+                    const uint64_t kd = kdesc + (uint64_t)(slot * (C::kPanelBytes >> 4));
+                    const uint64_t qd = qdesc + (uint64_t)((q * C::kQBytes + pp * C::kPanelBytes) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < C::kPanelD / 16; ++kk) {
+                        const uint64_t off = (uint64_t)((kk / 4) * (C::kChunkBytes >> 4) + (kk % 4) * 2);
+                        mma_ss(tmem + (k & 1) * kKeys, qd + off, kd + off, idS, pp > 0 || kk > 0);
+                    }
+                    if (!two || q == 1) mma_commit(bar(kEmpty + slot));
+                }
+                mma_commit(bar(kSFull + (k & 1)));
+                return true;
+            };
+            auto product = [&](int k) -> bool {
+                const int q = two ? k & 1 : 0, i = two ? k >> 1 : k;
+                if (!mbar_wait(bar(kPFull + (k & 1)), (k >> 1) & 1, kWaitNs)) return false;
+                for (int pp = 0; pp < C::kPanels; ++pp) {
+                    const int e = v_entry(i, two, ntiles) * C::kPanels + pp, slot = e % C::kStages;
+                    if (!mbar_wait(bar(kFull + slot), (e / C::kStages) & 1, kWaitNs)) return false;
+                    tc_fence_after();
+                    const uint64_t vd = vdesc + (uint64_t)(slot * (C::kPanelBytes >> 4));
+#pragma unroll
+                    for (int kk = 0; kk < kKeys / 16; ++kk)
+                        mma_ts(tmem + C::kOCol + q * D + pp * C::kPanelD, tmem + (k & 1) * kKeys + kk * 8,
+                               vd + (uint64_t)(kk * (16 * 128 >> 4)), idO, i > 0 || kk > 0);
+                    if (!two || q == 1) mma_commit(bar(kEmpty + slot));
+                }
+                mma_commit(bar(kODone + (k & 1)));
+                return true;
+            };
+            ok = mbar_wait(bar(kQReady), 0, kWaitNs);
+            tc_fence_after();
+            ok = ok && scores(0) && (steps < 2 || scores(1));
+            for (int k = 0; k < steps && ok; ++k) ok = product(k) && (k + 2 >= steps || scores(k + 2));
+            mma_commit(bar(kOFinal));
+            if (!mbar_wait(bar(kOFinal), 0, kWaitNs)) ok = false;
+        }
+    } else if (warp < C::kSoftmaxWarps) {
+        // ------------------------------------------------------------ softmax
+        const int w = warp >> 2;  // tile of rows
+        const int r = (warp & 3) * 32 + lane;
+        const int nt = max(0, min(tpt, it.nt - w * tpt));
+        const bool row_ok = r < nt * G;
+        if (w < nq) {
+            const int token = w * tpt + r / G;  // of the item
+            const int head = it.kvh * G + r % G;
+            const int vis = it.vis0 + token;
+            const uint32_t lane_tm = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+            // q as the MMA takes it: rows without a token are zero; for a cache of codes, fp16 scaled by a power of
+            // two that brings the row's largest element into [2^14, 2^15)
+            float prescale = 1.f;
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(kQFull), 0, kWaitNs));
+            {
+                const uint32_t row = sbase + C::kQ + w * C::kQBytes;
+                auto unit = [&](int u) { return row + (u / 8) * C::kChunkBytes + sw128(r, u % 8); };
+                if (!row_ok) {
+#pragma unroll 4
+                    for (int u = 0; u < D / 8; ++u) sts_u4(unit(u), make_uint4(0, 0, 0, 0));
+                } else if (C::kQuant) {
+                    float amax = 0.f;
+#pragma unroll 4
+                    for (int u = 0; u < D / 8; ++u) {
+                        const uint4 x = lds_u4(unit(u));
+                        const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            amax = fmaxf(amax, fmaxf(fabsf(bf16_bits_to_float(ws[e] & 0xFFFFu)),
+                                                     fabsf(__uint_as_float(ws[e] & 0xFFFF0000u))));
+                    }
+                    if (amax > 0.f && amax < INFINITY) {
+                        int e;
+                        frexpf(amax, &e);
+                        prescale = __uint_as_float((uint32_t)(127 + max(-126, min(127, 15 - e))) << 23);
+                    }
+#pragma unroll 4
+                    for (int u = 0; u < D / 8; ++u) {
+                        const uint4 x = lds_u4(unit(u));
+                        const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
+                        uint32_t h[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            h[e] = pack_half2(bf16_bits_to_float(ws[e] & 0xFFFFu) * prescale,
+                                              __uint_as_float(ws[e] & 0xFFFF0000u) * prescale);
+                        sts_u4(unit(u), make_uint4(h[0], h[1], h[2], h[3]));
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kQReady));
+            }
+            const float c_r = p.sm_scale_log2 / prescale;
+            const uint64_t c2 = f2_pack(__float_as_uint(c_r), __float_as_uint(c_r));
+            float m_run = -INFINITY, l_run = 0.f;
+            int beta = 0, swept = 0;
+            const int first_vis = it.vis0 + w * tpt;  // of the tile's first token
+            for (int i = 0; i < ntiles && ok; ++i) {
+                const int k = two ? 2 * i + w : i, sl = k & 1;
+                ok = __all_sync(0xffffffffu, ok && mbar_wait(bar(kSFull + sl), (k >> 1) & 1, kWaitNs));
+                if (!ok) break;
+                tc_fence_after();
+                const int key0 = it.k_begin + i * kKeys;
+                const uint32_t bads = lds_u32(sbase + C::kBad + 4u * (i % kBadRing));
+                // an edge tile hides some key from some row of the item; both tiles of rows take the same view of it
+                const bool edge = key0 + kKeys > it.k_end || key0 + kKeys - 1 > it.vis0 || bads != 0;
+                const bool cut = edge && (key0 + kKeys > it.k_end || key0 + kKeys - 1 > first_vis || bads != 0);
+                const int last = row_ok ? min(vis, it.k_end - 1) - key0 : -1;  // last key of the tile that the row sees
+                const uint32_t s_tm = lane_tm + sl * kKeys;
+                const uint32_t ring = sbase + C::kScale + (i % kScaleRing) * kScaleFloats * 4;
+                auto visible = [&](int j) { return j <= last && !((bads >> (j / VA_PAGE_SIZE)) & 1u); };
+                // raw scores times k scale, hidden keys at -inf; mx: four chains of maxima
+                auto take = [&](int c, uint32_t (&s)[32], float (&mx)[4]) {
+                    if constexpr (C::kQuant) {
+#pragma unroll
+                        for (int j4 = 0; j4 < 8; ++j4) {
+                            const uint4 sc = lds_u4(ring + 128u * c + 16 * j4);
+                            f2_unpack(f2_mul(f2_pack(s[4 * j4], s[4 * j4 + 1]), f2_pack(sc.x, sc.y)), s[4 * j4],
+                                      s[4 * j4 + 1]);
+                            f2_unpack(f2_mul(f2_pack(s[4 * j4 + 2], s[4 * j4 + 3]), f2_pack(sc.z, sc.w)), s[4 * j4 + 2],
+                                      s[4 * j4 + 3]);
+                        }
+                    }
+                    if (cut) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (!visible(32 * c + j)) s[j] = 0xFF800000u;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2)
+                        mx[(j / 2) & 3] = fmax3(mx[(j / 2) & 3], __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+                };
+                uint32_t s[C::kKeep ? 4 : 1][32];
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                if constexpr (C::kKeep) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + 32 * c, s[c]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) take(c, s[c], mx);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_ld32(s_tm + 32 * c, s[0]);
+                        tmem_wait_ld();
+                        take(c, s[0], mx);
+                    }
+                }
+                const float m_tile = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * c_r;
+                const bool grow = m_tile > m_run + kRescaleLog2;
+                float alpha = 1.f;
+                if (grow) {
+                    if (m_run != -INFINITY) alpha = ex2_approx(m_run - m_tile);
+                    m_run = m_tile;
+                    l_run *= alpha;
+                }
+                int dbeta = 0;
+                if constexpr (C::kQuant) {
+                    float mv;
+                    if (!cut) {
+                        const float4 x = lds_f4(ring + 8u * kKeys);
+                        mv = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w));
+                    } else {  // of the keys that the row sees
+                        mv = 0.f;
+#pragma unroll 8
+                        for (int j = 0; j < kKeys; ++j)
+                            if (visible(j)) mv = fmaxf(mv, lds_f32(ring + 4u * (kKeys + j)));
+                    }
+                    if (mv > 0.f) {
+                        const float rr = mv * __uint_as_float((uint32_t)(127 + beta) << 23);
+                        if (!(rr >= 0x1p-6f && rr < 4.f)) {
+                            // mv in [2^(E-127), 2^(E-126)); beta at most 118, so that p 2^beta stays finite
+                            const int E = max(9, min(253, (int)((__float_as_uint(mv) >> 23) & 0xFFu)));
+                            dbeta = (127 - E) - beta;
+                            beta = 127 - E;
+                        }
+                    }
+                }
+                const float fo =
+                    dbeta == 0 ? alpha : alpha * __uint_as_float((uint32_t)(127 + max(-126, min(127, dbeta))) << 23);
+                if (i > 0 && __any_sync(0xffffffffu, fo != 1.f)) {
+                    // O holds the tiles before: their last product has to have landed
+                    const int kp = two ? k - 2 : k - 1;
+                    if (!__all_sync(0xffffffffu, mbar_wait(bar(kODone + (kp & 1)), (kp >> 1) & 1, kWaitNs))) ok = false;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(lane_tm + C::kOCol + w * D + c0, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fo);
+                        tmem_st32(lane_tm + C::kOCol + w * D + c0, o);
+                    }
+                    tmem_wait_st();
+                }
+                const float neg_m = (m_run == -INFINITY ? 0.f : -m_run) + (float)beta;
+                const uint64_t nm2 = f2_pack(__float_as_uint(neg_m), __float_as_uint(neg_m));
+                uint64_t ls[2] = {0ull, 0ull};
+                auto give = [&](int c, uint32_t (&x)[32]) {  // probabilities of 32 keys, over the slot's columns
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int j4 = 0; j4 < 8; ++j4) {
+                        uint32_t a[4];
+                        f2_unpack(f2_fma(f2_pack(x[4 * j4], x[4 * j4 + 1]), c2, nm2), a[0], a[1]);
+                        f2_unpack(f2_fma(f2_pack(x[4 * j4 + 2], x[4 * j4 + 3]), c2, nm2), a[2], a[3]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) a[e] = __float_as_uint(ex2_approx(__uint_as_float(a[e])));
+                        const uint64_t p01 = f2_pack(a[0], a[1]), p23 = f2_pack(a[2], a[3]);
+                        ls[0] = f2_add(ls[0], p01);
+                        ls[1] = f2_add(ls[1], p23);
+                        if constexpr (C::kQuant) {
+                            const uint4 sc = lds_u4(ring + 4u * kKeys + 128u * c + 16 * j4);
+                            f2_unpack(f2_mul(p01, f2_pack(sc.x, sc.y)), a[0], a[1]);
+                            f2_unpack(f2_mul(p23, f2_pack(sc.z, sc.w)), a[2], a[3]);
+                            if (cut) {  // a hidden key's scale may be anything
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (!visible(32 * c + 4 * j4 + e)) a[e] = 0u;
+                            }
+                            pk[2 * j4] = pack_half2(__uint_as_float(a[0]), __uint_as_float(a[1]));
+                            pk[2 * j4 + 1] = pack_half2(__uint_as_float(a[2]), __uint_as_float(a[3]));
+                        } else {
+                            pk[2 * j4] = pack_bf162(__uint_as_float(a[0]), __uint_as_float(a[1]));
+                            pk[2 * j4 + 1] = pack_bf162(__uint_as_float(a[2]), __uint_as_float(a[3]));
+                        }
+                    }
+                    tmem_st16(s_tm + 16 * c, pk);
+                };
+                if constexpr (C::kKeep) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) give(c, s[c]);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float none[4] = {0.f, 0.f, 0.f, 0.f};
+                        tmem_ld32(s_tm + 32 * c, s[0]);
+                        tmem_wait_ld();
+                        take(c, s[0], none);
+                        give(c, s[0]);
+                    }
+                }
+                uint32_t l0, l1;
+                f2_unpack(f2_add(ls[0], ls[1]), l0, l1);
+                l_run += (__uint_as_float(l0) + __uint_as_float(l1)) * __uint_as_float((uint32_t)(127 - beta) << 23);
+                if constexpr (C::kQuant) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kScaleFree + i % kScaleRing));
+                }
+                tmem_wait_st();
+                if (edge && (DT == VA_BF16 || DT == VA_FP8_E4M3)) {
+                    // values that are not finite, in a tile that the mask cuts: out of the product (0 * inf is not 0).
+                    // All softmax threads share the sweep and leave it together.
+                    const int valid = min(kKeys, it.k_end - key0);
+                    bool found = false;
+                    for (int pp = 0; pp < C::kPanels; ++pp) {
+                        const int e = v_entry(i, two, ntiles) * C::kPanels + pp, slot = e % C::kStages;
+                        if (!__all_sync(0xffffffffu, mbar_wait(bar(kFull + slot), (e / C::kStages) & 1, kWaitNs))) ok = false;
+                        const uint32_t panel = sbase + C::kConv + slot * C::kPanelBytes;
+                        for (int u = w * 128 + r; u < kKeys * C::kPanelD / 8; u += nq * 128) {
+                            const int row = u / (C::kPanelD / 8), cu = u % (C::kPanelD / 8);
+                            const uint32_t a = panel + (cu / 8) * C::kChunkBytes + sw128(row, cu % 8);
+                            constexpr uint32_t kExp = DT == VA_BF16 ? 0x7F80u : 0x7C00u;
+                            uint4 x = lds_u4(a);
+                            if (row >= valid) {
+                                sts_u4(a, make_uint4(0, 0, 0, 0));
+                            } else if (!(half_finite(x.x, kExp) && half_finite(x.y, kExp) && half_finite(x.z, kExp) &&
+                                         half_finite(x.w, kExp))) {
+                                uint32_t ws[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                                for (int n = 0; n < 4; ++n) {
+                                    if ((ws[n] & kExp) == kExp) ws[n] &= 0xFFFF0000u;
+                                    if (((ws[n] >> 16) & kExp) == kExp) ws[n] &= 0x0000FFFFu;
+                                }
+                                sts_u4(a, make_uint4(ws[0], ws[1], ws[2], ws[3]));
+                                found = true;
+                            }
+                        }
+                    }
+                    if (found) sts_u32(bar(kPoison), 1u);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kSwept));
+                    if (!__all_sync(0xffffffffu, mbar_wait(bar(kSwept), swept & 1, kWaitNs))) ok = false;
+                    ++swept;
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kPFull + sl));
+            }
+            // epilogue
+            if (!__all_sync(0xffffffffu, mbar_wait(bar(kOFinal), 0, kWaitNs))) ok = false;
+            tc_fence_after();
+            const bool poison = lds_u32(bar(kPoison)) != 0;
+            const float inv = l_run == 0.f ? 0.f : (1.f / l_run) * __uint_as_float((uint32_t)(127 - beta) << 23);
+            const float lse = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
+            const size_t orow = (size_t)(it.q0 + token) * p.Hq + head;
+            if (row_ok && ok) {
+                if (it.part < 0) {
+                    if (p.lse) p.lse[orow] = lse;
+                } else {
+                    p.lse_part[(size_t)(it.part + w) * kMmaRows + r] = lse;
+                }
+            }
+            // what was taken out comes back to the rows that see it
+            auto give_back = [&](int d) -> float {
+                float add = 0.f;
+                for (int i = 0; i < ntiles; ++i) {
+                    const int key0 = it.k_begin + i * kKeys;
+                    bool edge = key0 + kKeys > it.k_end || key0 + kKeys - 1 > it.vis0;
+                    for (int n = 0; n < kPages && !edge; ++n) {
+                        const int page = bt[i * kPages + n];
+                        edge = p.num_pages > 0 && (page < 0 || page >= p.num_pages);
+                    }
+                    if (!edge) continue;
+                    for (int key = key0; key < min(key0 + kKeys, min(it.k_end, vis + 1)); ++key) {
+                        const int page = bt[key / VA_PAGE_SIZE - lp0];
+                        if (page < 0 || (p.num_pages > 0 && page >= p.num_pages)) continue;
+                        const float x = cached_value<D, DT>(
+                            p.v_pages, p.v_scale, ((size_t)page * VA_PAGE_SIZE + key % VA_PAGE_SIZE) * p.Hkv + it.kvh, d);
+                        if (!(fabsf(x) < INFINITY)) add += x;
+                    }
+                }
+                return add;
+            };
+            if (it.part < 0) {
+                // bf16 rows staged over this tile of q, units exchanged by row, then written 16 bytes a lane
+                const uint32_t stage = sbase + C::kQ + w * C::kQBytes;
+                auto unit = [&](int row, int u) { return stage + row * (D * 2) + (((u & ~7) | ((u ^ row) & 7)) << 4); };
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(lane_tm + C::kOCol + w * D + c0, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * inv);
+                    if (poison && row_ok) {
+#pragma unroll 1
+                        for (int j = 0; j < 32; ++j) {
+                            const float add = give_back(c0 + j);
+                            if (add != 0.f) {
+#pragma unroll
+                                for (int n = 0; n < 32; ++n)
+                                    if (n == j) o[n] = __float_as_uint(__uint_as_float(o[n]) + add);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+                        sts_u4(unit(r, c0 / 8 + n),
+                               make_uint4(pack_bf162(__uint_as_float(o[8 * n]), __uint_as_float(o[8 * n + 1])),
+                                          pack_bf162(__uint_as_float(o[8 * n + 2]), __uint_as_float(o[8 * n + 3])),
+                                          pack_bf162(__uint_as_float(o[8 * n + 4]), __uint_as_float(o[8 * n + 5])),
+                                          pack_bf162(__uint_as_float(o[8 * n + 6]), __uint_as_float(o[8 * n + 7]))));
+                }
+                named_bar_sync(2 + w, 128);
+                if (ok) {
+                    for (int e = r; e < nt * G * (D / 8); e += 128) {
+                        const int row = e / (D / 8), u = e % (D / 8);
+                        const size_t to = (size_t)(it.q0 + w * tpt + row / G) * p.Hq + it.kvh * G + row % G;
+                        reinterpret_cast<uint4 *>(p.out)[to * (D / 8) + u] = lds_u4(unit(row, u));
+                    }
+                }
+            } else {
+                float *o_part = p.o_part + (size_t)(it.part + w) * D * kMmaRows + r;
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(lane_tm + C::kOCol + w * D + c0, o);
+                    tmem_wait_ld();
+                    if (!row_ok || !ok) continue;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o_part[(size_t)(c0 + j) * kMmaRows] = __uint_as_float(o[j]) * inv;
+#pragma unroll 1
+                    for (int j = 0; poison && j < 32; ++j) {
+                        const float add = give_back(c0 + j);
+                        if (add != 0.f) o_part[(size_t)(c0 + j) * kMmaRows] += add;
+                    }
+                }
+            }
+        }
+    } else if constexpr (C::kQuant) {
+        // ------------------------------------------------------------ dequant
+        // A panel is 16-element pieces; each thread takes kPer of them, kStep rows (a multiple of the swizzle's 8) apart.
+        constexpr int kPieces = C::kPanelD / 16;  // of a row
+        constexpr int kPer = kKeys * kPieces / 128;
+        constexpr int kStep = 128 / kPieces;
+        constexpr int kPieceBytes = C::kBits * 2;
+        static_assert(kStep % 8 == 0, "rows apart");
+        const int dt = tid - C::kSoftmaxWarps * 32;  // 0 .. 127, also the key whose scales it carries
+        const int n0 = dt / kPieces, d0 = (dt % kPieces) * 16;
+        const uint32_t lo_at = (d0 / 64) * C::kChunkBytes + sw128(n0, (d0 % 64) / 8);
+        const uint32_t hi_at = (d0 / 64) * C::kChunkBytes + sw128(n0, (d0 % 64) / 8 + 1);
+        const bool odd = (d0 / 64) & 1;  // the other unit first, so that a quarter of a warp hits no bank twice
+        auto load_id = [&](int i) -> int {
+            const int n = i * kPages + dt / VA_PAGE_SIZE;
+            if (i >= ntiles || n >= npages || it.k_begin + i * kKeys + dt >= it.k_end) return -1;
+            const int page = __ldg(bt + n);
+            return p.num_pages > 0 && page >= p.num_pages ? -1 : page;
+        };
+        auto load_scale = [&](const float *from, int page) -> float {
+            return page < 0 ? 0.f : __ldg(from + ((size_t)page * VA_PAGE_SIZE + dt % VA_PAGE_SIZE) * p.Hkv + it.kvh);
+        };
+        // scales two tiles ahead, page ids three
+        int id0 = load_id(0), id1 = load_id(1), id2 = load_id(2);
+        float ks0 = load_scale(p.k_scale, id0), vs0 = load_scale(p.v_scale, id0);
+        float ks1 = load_scale(p.k_scale, id1), vs1 = load_scale(p.v_scale, id1);
+        constexpr int kRawN = C::kRawStages ? C::kRawStages : 1;
+        const int total = 2 * ntiles * C::kPanels;
+        for (int e = 0; e < total && ok; ++e) {
+            bool v;
+            const int i = entry_tile(e / C::kPanels, two, ntiles, v);
+            const int rs = e % kRawN, slot = e % C::kStages;
+            if (!mbar_wait(bar(kRawFull + rs), (e / kRawN) & 1, kWaitNs)) { ok = false; break; }
+            const uint32_t src = sbase + C::kRaw + rs * C::kRawBytes + dt * kPieceBytes;
+            const uint32_t dst = sbase + C::kConv + slot * C::kPanelBytes;
+            RawPiece<DT> raw[kPer];
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) raw[j].load(src + j * 128 * kPieceBytes);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kRawEmpty + rs));
+            const int nvalid = it.k_end - (it.k_begin + i * kKeys);
+            if (e / C::kStages > 0 &&
+                !mbar_wait(bar(kEmpty + slot), ((e / C::kStages) & 1) ^ 1, kWaitNs)) { ok = false; break; }
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                uint32_t h[8];
+                raw[j].to_half(h);
+                uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+                if (n0 + j * kStep >= nvalid) lo = hi = make_uint4(0, 0, 0, 0);
+                const uint32_t at = dst + j * kStep * 128;
+                if (odd) {
+                    sts_u4(at + hi_at, hi);
+                    sts_u4(at + lo_at, lo);
+                } else {
+                    sts_u4(at + lo_at, lo);
+                    sts_u4(at + hi_at, hi);
+                }
+            }
+            if (!v && e % C::kPanels == 0) {
+                if (i >= kScaleRing &&
+                    !mbar_wait(bar(kScaleFree + i % kScaleRing), ((i / kScaleRing) & 1) ^ 1, kWaitNs)) { ok = false; break; }
+                const uint32_t ring = sbase + C::kScale + (i % kScaleRing) * kScaleFloats * 4;
+                sts_f32(ring + 4u * dt, ks0);
+                sts_f32(ring + 4u * (kKeys + dt), vs0);
+                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(vs0)));
+                if (lane == 0) sts_u32(ring + 4u * (2 * kKeys + dt / 32), top);
+                ks0 = ks1, vs0 = vs1;
+                ks1 = load_scale(p.k_scale, id2), vs1 = load_scale(p.v_scale, id2);
+                id2 = load_id(i + 3);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kFull + slot));
+        }
+    }
+
+    if (!ok) atomicOr(p.flags, kFlagTimeoutBit);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == C::kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Log-sum-exp merge of a tile's partials.  A CTA takes kCols elements of all 128 rows: thread = row, so that the
+// partials (rows innermost) are read in whole segments; the merged piece goes through shared memory, so that rows
+// of `out` are written in pieces of kCols elements.
+constexpr int kCombineCols = 16;
+
+__global__ void __launch_bounds__(kMmaRows) chunk_combine_kernel(const ChunkCombineParams p) {
+    __shared__ uint32_t tile[kMmaRows][kCombineCols / 2 + 1];
+    griddep_wait();
+    const ChunkGroup g = p.groups[blockIdx.x];
+    const int r = threadIdx.x, d0 = blockIdx.y * kCombineCols;
+    const int rows = g.nt * p.G;
+    if (r < rows) {
+        const float *lse = p.lse_part + (size_t)g.first_part * kMmaRows + r;
+        const size_t step = (size_t)g.step * kMmaRows;
+        float m = -INFINITY;
+        for (int n = 0; n < g.n; ++n) m = fmaxf(m, lse[n * step]);
+        float z = 0.f, acc[kCombineCols];
+#pragma unroll
+        for (int d = 0; d < kCombineCols; ++d) acc[d] = 0.f;
+        const float *o = p.o_part + ((size_t)g.first_part * p.D + d0) * kMmaRows + r;
+        for (int n = 0; n < g.n; ++n) {
+            const float l = lse[n * step];
+            const float e = l == -INFINITY ? 0.f : expf(l - m);
+            z += e;
+#pragma unroll
+            for (int d = 0; d < kCombineCols; ++d) {
+                const float x = o[n * step * p.D + d * kMmaRows];
+                acc[d] = l == -INFINITY ? acc[d] : fmaf(e, x, acc[d]);
+            }
+        }
+        const float inv = z == 0.f ? 0.f : 1.f / z;
+#pragma unroll
+        for (int d = 0; d < kCombineCols / 2; ++d) tile[r][d] = pack_bf162(acc[2 * d] * inv, acc[2 * d + 1] * inv);
+        if (blockIdx.y == 0 && p.lse)
+            p.lse[(size_t)(g.q0 + r / p.G) * p.Hq + g.kvh * p.G + r % p.G] = z == 0.f ? -INFINITY : m + logf(z);
+    }
+    __syncthreads();
+    constexpr int kUnits = kCombineCols / 8;
+    for (int e = r; e < rows * kUnits; e += kMmaRows) {
+        const int row = e / kUnits, u = e % kUnits;
+        const size_t to = (size_t)(g.q0 + row / p.G) * p.Hq + g.kvh * p.G + row % p.G;
+        reinterpret_cast<uint4 *>(p.out)[(to * p.D + d0) / 8 + u] =
+            make_uint4(tile[row][4 * u], tile[row][4 * u + 1], tile[row][4 * u + 2], tile[row][4 * u + 3]);
+    }
+}
+
+// A page pool [pages, 16, Hkv, row] by boxes of one page and head: 64 elements (bf16, swizzled) or one panel's bytes.
+bool make_cache_map(CUtensorMap *m, const void *base, int D, int bits, int box_row, int Hkv, int num_pages) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const bool bf16 = bits == 16;
+    const cuuint64_t bytes = (cuuint64_t)D * bits / 8;
+    const cuuint64_t pages = num_pages > 0 ? (cuuint64_t)num_pages : (cuuint64_t)1 << 30;
+    cuuint64_t dims[4] = {bf16 ? (cuuint64_t)D : bytes, (cuuint64_t)Hkv, (cuuint64_t)VA_PAGE_SIZE, pages};
+    cuuint64_t strides[3] = {bytes, bytes * Hkv, bytes * Hkv * VA_PAGE_SIZE};
+    cuuint32_t box[4] = {(cuuint32_t)box_row, 1u, (cuuint32_t)VA_PAGE_SIZE, 1u};
+    cuuint32_t one[4] = {1, 1, 1, 1};
+    return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(base),
+               dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               bf16 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// q [N, heads, D] by boxes of 64 elements x G heads x tpt tokens.
+bool make_q_map(CUtensorMap *m, const va_heads &q, int N, int D, int G, int tpt) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)q.num_heads, (cuuint64_t)N};
+    cuuint64_t strides[2] = {(cuuint64_t)q.stride_head * 2, (cuuint64_t)q.stride_token * 2};
+    cuuint32_t box[3] = {64u, (cuuint32_t)G, (cuuint32_t)tpt};
+    cuuint32_t one[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q.data, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int DT>
+cudaError_t launch_one(const ChunkParams &p, const va_heads &q, int N, int n, cudaStream_t s) {
+    using C = Cfg<D, DT>;
+    Args a;
+    a.p = p;
+    const int box = C::kQuant ? C::kRawRow : 64;
+    if (!make_q_map(&a.tm_q, q, N, D, p.G, p.tpt) ||
+        !make_cache_map(&a.tm_k, p.k_pages, D, C::kBits, box, p.Hkv, p.num_pages) ||
+        !make_cache_map(&a.tm_v, p.v_pages, D, C::kBits, box, p.Hkv, p.num_pages))
+        return cudaErrorInvalidValue;
+    auto k = chunk_kernel<D, DT>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(k, dim3(n), dim3(C::kThreads), C::kSmem, s, a);
+}
+
+template <int D>
+cudaError_t launch_d(const ChunkParams &p, const va_heads &q, int N, int dtype, int n, cudaStream_t s) {
+    switch (dtype) {
+    case VA_BF16: return launch_one<D, VA_BF16>(p, q, N, n, s);
+    case VA_FP8_E4M3: return launch_one<D, VA_FP8_E4M3>(p, q, N, n, s);
+    case VA_INT8: return launch_one<D, VA_INT8>(p, q, N, n, s);
+    case VA_INT4: return launch_one<D, VA_INT4>(p, q, N, n, s);
+    default: return launch_one<D, VA_INT2>(p, q, N, n, s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_chunk(const ChunkParams &p, const va_heads &q, int N, int D, int dtype, int num_items, cudaStream_t s) {
+    if (num_items <= 0) return cudaSuccess;
+    switch (D) {
+    case 64: return launch_d<64>(p, q, N, dtype, num_items, s);
+    case 128: return launch_d<128>(p, q, N, dtype, num_items, s);
+    default: return launch_d<256>(p, q, N, dtype, num_items, s);
+    }
+}
+
+cudaError_t launch_chunk_combine(const ChunkCombineParams &p, int num_groups, cudaStream_t s) {
+    if (num_groups <= 0) return cudaSuccess;
+    return launch_pdl(chunk_combine_kernel, dim3(num_groups, p.D / kCombineCols), dim3(kMmaRows), 0, s, p);
+}
+
+}  // namespace va
