@@ -710,6 +710,26 @@ int verify_attn_chunk(const va_chunk_plan *plan, const va_heads *q, const void *
                       const int32_t *block_table, int block_table_stride, int num_pages, void *out,
                       float *lse, void *stream);
 
+/* The attention weight that the cached tokens gather from the chunks: for kv
+ * head g and key j < L_b of every sequence that takes part,
+ *     w = sum over t with j <= L_b - n_b + t and the query heads h of g of
+ *         exp(s_j - lse[row, h])
+ *     weights[b, g, j] = w, or weights[b, g, j] + w for accumulate != 0 and
+ *                        j < L_b - n_b (the new tokens start from nothing)
+ * with lse as verify_attn_chunk gives it (a row with lse -inf gives nothing).
+ * Entry (b, g, j) of weights is weights[b * weights_stride_seq + g *
+ * weights_stride_head + j]; entries from L_b on are left as they are.  slot_pos
+ * (int32, strides as weights; NULL: not kept) receives positions[row] (int32
+ * [tokens]) at the new tokens' places: the order of age in a cache whose rows
+ * verify_attn_evict has moved.  Plan, q, cache, block table and num_pages as for
+ * verify_attn_chunk, on the same stream order.  The sums do not depend on
+ * timing. */
+int verify_attn_chunk_weights(const va_chunk_plan *plan, const va_heads *q, const void *k_pages,
+                              const float *k_scale, const int32_t *block_table, int block_table_stride,
+                              int num_pages, const float *lse, float *weights, int64_t weights_stride_seq,
+                              int64_t weights_stride_head, int accumulate, int32_t *slot_pos,
+                              const int32_t *positions, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

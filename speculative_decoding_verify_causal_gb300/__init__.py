@@ -176,8 +176,9 @@ def _load():
         lib.verify_attn_chunk_plan_get_info.argtypes = [P, ctypes.POINTER(ChunkPlanInfo)]
         lib.verify_attn_chunk_plan_device_flags.argtypes = [P, I, ctypes.POINTER(I), P]
         lib.verify_attn_chunk.argtypes = [P, H, P, P, P, P, P, I, I, P, P, P]
+        lib.verify_attn_chunk_weights.argtypes = [P, H, P, P, P, I, I, P, P, ctypes.c_int64, ctypes.c_int64, I, P, P, P]
         for f in ("verify_attn_chunk_plan", "verify_attn_chunk_plan_get_info", "verify_attn_chunk_plan_device_flags",
-                  "verify_attn_chunk"):
+                  "verify_attn_chunk", "verify_attn_chunk_weights"):
             getattr(lib, f).restype = I
         for f in ("verify_attn_rope_init", "verify_attn_rope", "verify_attn_rope_append", "verify_attn_accept_probs",
                   "verify_attn_pages_resize", "verify_attn_pages_resize_ex", "verify_attn_pages_fork",
@@ -1026,7 +1027,8 @@ class ChunkPlan:
     def __init__(self, handle, shape, index):
         self._h = ctypes.c_void_p(handle)
         self._index = index  # CUDA device that the plan's memory is on
-        self.num_seqs, self.num_q_heads, self.num_kv_heads, self.head_dim, self.kv_dtype, self.num_tokens = shape
+        (self.num_seqs, self.num_q_heads, self.num_kv_heads, self.head_dim, self.kv_dtype, self.num_tokens,
+         self.max_len) = shape  # max_len: the longest sequence that takes part
 
     @property
     def handle(self):
@@ -1063,7 +1065,8 @@ def verify_attn_chunk_plan(chunk_lens, seq_lens, num_q_heads, num_kv_heads, head
     out = ctypes.c_void_p()
     _check(lib.verify_attn_chunk_plan(new.ctypes.data, lens.ctypes.data, len(new), int(num_q_heads), int(num_kv_heads),
                                       int(head_dim), code, int(num_sms), ctypes.byref(out)), "verify_attn_chunk_plan")
-    return ChunkPlan(out.value, (len(new), int(num_q_heads), int(num_kv_heads), int(head_dim), code, int(new.sum())),
+    return ChunkPlan(out.value, (len(new), int(num_q_heads), int(num_kv_heads), int(head_dim), code, int(new.sum()),
+                                 int(lens[new > 0].max(initial=0))),
                      torch.cuda.current_device())
 
 
@@ -1156,7 +1159,63 @@ def verify_attn_chunk(plan: ChunkPlan, q, k_pages, v_pages, k_scale, v_scale, bl
     return out, lse
 
 
+def _per_slot(t, name, dtype, index, shape):
+    """Address and the strides of a [B, Hkv, slots] tensor, contiguous in its last dimension."""
+    try:
+        n, s = t.shape, t.stride()
+        if (t.dtype is dtype and t.get_device() == index and len(n) == 3 and n[:2] == shape[:2] and n[2] >= shape[2]
+                and (s[2] == 1 or n[2] <= 1)):
+            return t.data_ptr(), s[0], s[1]
+    except AttributeError:
+        raise ValueError(f"{name} must be a CUDA tensor") from None
+    raise ValueError(f"{name} must be a {dtype} tensor {list(shape)} (or more slots) on cuda:{index}, contiguous in its "
+                     f"last dimension, got {t.dtype} {list(n)} with strides {list(s)} on {t.device}")
+
+
+def verify_attn_chunk_weights(plan: ChunkPlan, q, k_pages, k_scale, block_table, lse, weights, accumulate=True,
+                              slot_pos=None, positions=None, num_pages=0, stream=None):
+    """The attention weight that each cached token gathers from the chunks: ``weights``
+    (fp32 ``[num_seqs, Hkv, slots]``, any strides with a contiguous last dimension)
+    is added to at the tokens that were cached before (``accumulate=False``: set) and
+    set at the new ones; slots past a sequence's length are left as they are.
+    ``lse``: what ``verify_attn_chunk`` returned for the same queries.  ``slot_pos``
+    (int32, shape and strides as ``weights``) with ``positions`` (int32 ``[tokens]``): also
+    keeps the new tokens' positions, for ``verify_attn_evict``.  Other arguments as
+    for ``verify_attn_chunk``.  Returns ``weights``."""
+    torch = _torch or _bind_torch()
+    if _grad_mode() and (_wants_gradient(q) or _wants_gradient(k_pages) or _wants_gradient(k_scale)
+                         or _wants_gradient(lse) or _wants_gradient(weights)):
+        raise _gradient_refused("verify_attn_chunk_weights")
+    heads, device, index = _chunk_q(plan, q)
+    kp, ks, pages = _chunk_cache(plan, k_pages, k_scale, "k", index)
+    if num_pages > pages:
+        raise ValueError(f"num_pages is {num_pages}, the cache has {pages}")
+    bt, stride = _chunk_table(plan, block_table, index)
+    n = lse.shape
+    if len(n) != 2 or n[0] < plan.num_tokens or n[1] != plan.num_q_heads:
+        raise ValueError(f"lse must be [{plan.num_tokens}, {plan.num_q_heads}], got {list(n)}")
+    lp = _ptr(lse, "lse", torch.float32, index)
+    shape = (plan.num_seqs, plan.num_kv_heads, plan.max_len)
+    wp, seq, head = _per_slot(weights, "weights", torch.float32, index, shape)
+    sp = pos = None
+    if slot_pos is not None:
+        sp, *strides = _per_slot(slot_pos, "slot_pos", torch.int32, index, shape)
+        if strides != [seq, head]:
+            raise ValueError("slot_pos must have the strides of weights")
+        if positions is None or positions.dim() != 1 or positions.shape[0] < plan.num_tokens:
+            raise ValueError(f"slot_pos needs positions [{plan.num_tokens}]")
+        pos = _ptr(positions, "positions", torch.int32, index)
+    st, guard = _launch_on(device, stream)
+    with guard:
+        rc = (_lib or _load()).verify_attn_chunk_weights(plan._h, heads, kp, ks, bt, stride, num_pages or pages, lp, wp,
+                                                         seq, head, 1 if accumulate else 0, sp, pos, st)
+    if rc:
+        _check(rc, "verify_attn_chunk_weights")
+    return weights
+
+
 __all__ = [
+    "verify_attn_chunk_weights",
     "ChunkPlan", "verify_attn_chunk_plan", "verify_attn_chunk_plan_destroy", "verify_attn_chunk_plan_device_flags",
     "verify_attn_chunk",
     "Rope", "verify_attn_rope_spec", "verify_attn_rope", "verify_attn_rope_append", "verify_attn_accept_probs",

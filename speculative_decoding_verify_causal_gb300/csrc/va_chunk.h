@@ -60,10 +60,13 @@ struct WeightParams {
 };
 
 constexpr int kChunkKeys = 128;  // keys of one tile of scores
+constexpr int kWeightClusters = 8;  // most CTAs that share a block of keys
+constexpr int weight_keys(int D) { return D == 256 ? 128 : 256; }  // keys of a block
 constexpr int kFlagTimeoutBit = 4;
 constexpr int chunk_tiles(int D) { return D == 256 ? 1 : 2; }  // tiles of packed rows that a CTA takes
 
 cudaError_t launch_chunk(const ChunkParams &p, const va_heads &q, int N, int D, int dtype, int num_items, cudaStream_t s);
+cudaError_t launch_weights(const WeightParams &p, const va_heads &q, int N, int D, int dtype, int num_blocks, cudaStream_t s);
 cudaError_t launch_chunk_combine(const ChunkCombineParams &p, int num_groups, cudaStream_t s);
 
 }  // namespace va

@@ -68,7 +68,7 @@ struct Geometry {
     std::vector<va::ChunkItem> items;
     std::vector<va::ChunkGroup> groups;
     std::vector<va::WeightItem> blocks;
-    int num_parts = 0, max_tiles = 0;
+    int num_parts = 0, max_tiles = 0, cluster = 1;
 };
 
 // One row item of one kv head before it is split: `nt` tokens, `tiles` tiles of keys.
@@ -146,6 +146,26 @@ void plan_geometry(const int32_t *chunk_lens, const int32_t *seq_lens, int B, in
     for (const auto &x : items) g.items.push_back(x.second);
 }
 
+// Blocks of keys for the gathered weights, the ones that most tiles of rows pass by first, and how many CTAs share one.
+void plan_blocks(const int32_t *chunk_lens, const int32_t *seq_lens, int B, int Hkv, int G, int D, int num_sms, Geometry &g) {
+    const int tpt = va::kMmaRows / G, keys = va::weight_keys(D);
+    std::vector<std::pair<int, va::WeightItem>> blocks;
+    int at = 0;
+    for (int b = 0; b < B; at += chunk_lens[b], ++b) {
+        const int n = chunk_lens[b], L = seq_lens[b];
+        for (int key0 = 0; n > 0 && key0 < L; key0 += keys) {
+            const int tiles = (n - std::max(0, key0 - (L - n)) + tpt - 1) / tpt;
+            for (int h = 0; h < Hkv; ++h) blocks.push_back({tiles, {b, h, key0, at, n, L, 0, 0}});
+        }
+    }
+    std::stable_sort(blocks.begin(), blocks.end(), [](const auto &a, const auto &b) { return a.first > b.first; });
+    for (const auto &x : blocks) g.blocks.push_back(x.second);
+    // a cluster where that fills SMs that would be idle, and where its CTAs have several tiles each
+    while (!blocks.empty() && g.cluster < va::kWeightClusters && (long long)blocks.size() * g.cluster * 2 <= num_sms &&
+           blocks.front().first >= 4 * g.cluster)
+        g.cluster *= 2;
+}
+
 int fail(cudaError_t e) {
     va::note_cuda_error(e);
     cudaGetLastError();
@@ -199,6 +219,7 @@ int verify_attn_chunk_plan(const int32_t *chunk_lens, const int32_t *seq_lens, i
     va_chunk_plan *p = nullptr;
     try {
         plan_geometry(chunk_lens, seq_lens, num_seqs, num_kv_heads, num_q_heads / num_kv_heads, head_dim, num_sms, g);
+        plan_blocks(chunk_lens, seq_lens, num_seqs, num_kv_heads, num_q_heads / num_kv_heads, head_dim, num_sms, g);
         p = new va_chunk_plan();
     } catch (const std::exception &) {
         return VA_ERR_OUT_OF_MEMORY;
@@ -221,6 +242,7 @@ int verify_attn_chunk_plan(const int32_t *chunk_lens, const int32_t *seq_lens, i
     p->num_parts = g.num_parts;
     p->max_tiles = g.max_tiles;
     p->num_blocks = (int)g.blocks.size();
+    p->cluster = g.cluster;
     const size_t items = align_up(sizeof(va::ChunkItem) * g.items.size());
     const size_t groups = align_up(sizeof(va::ChunkGroup) * g.groups.size());
     const size_t blocks = align_up(sizeof(va::WeightItem) * g.blocks.size());
@@ -306,6 +328,33 @@ int verify_attn_chunk(const va_chunk_plan *p, const va_heads *q, const void *k_p
         const va::ChunkCombineParams mp = {p->groups, p->o_part, p->lse_part, cp.out, lse, p->Hq, p->G, p->D};
         e = va::launch_chunk_combine(mp, p->num_groups, s);
     }
+    return e == cudaSuccess ? VA_OK : fail(e);
+}
+
+int verify_attn_chunk_weights(const va_chunk_plan *p, const va_heads *q, const void *k_pages, const float *k_scale,
+                              const int32_t *block_table, int block_table_stride, int num_pages, const float *lse,
+                              float *weights, int64_t weights_stride_seq, int64_t weights_stride_head, int accumulate,
+                              int32_t *slot_pos, const int32_t *positions, void *stream) {
+    if (!p) return VA_ERR_NO_PLAN;
+    va_heads qv;
+    int rc = check_q(p, q, qv);
+    if (rc != VA_OK) return rc;
+    if (!k_pages || !block_table || !lse || !weights || num_pages < 0 || block_table_stride < p->max_blocks ||
+        (slot_pos && !positions) || weights_stride_seq < 0 || weights_stride_head < 0)
+        return VA_ERR_INVALID_ARGUMENT;
+    if (p->kv_dtype != VA_BF16 && !k_scale) return VA_ERR_INVALID_ARGUMENT;
+    if (!aligned(k_pages, 16) || !aligned(block_table, 4) || !aligned(k_scale, 4) || !aligned(lse, 4) ||
+        !aligned(weights, 4) || !aligned(slot_pos, 4) || !aligned(positions, 4))
+        return VA_ERR_INVALID_ARGUMENT;
+    if (p->num_blocks == 0) return VA_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    rc = bind_thread(s);
+    if (rc != VA_OK) return rc;
+    const float scale = (float)(1.4426950408889634 / std::sqrt((double)p->D));
+    const va::WeightParams wp = {k_pages, k_scale, lse, block_table, p->blocks, weights, slot_pos, positions,
+                                 weights_stride_seq, weights_stride_head, p->flags, block_table_stride, p->Hq, p->Hkv,
+                                 p->G, p->tpt, num_pages, accumulate != 0, p->cluster, scale};
+    const cudaError_t e = va::launch_weights(wp, qv, p->total, p->D, p->kv_dtype, p->num_blocks, s);
     return e == cudaSuccess ? VA_OK : fail(e);
 }
 

@@ -179,7 +179,7 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t
                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-EncodeTiledFn encode_fn() {
+inline EncodeTiledFn encode_fn() {
     static std::once_flag once;
     static EncodeTiledFn fn = nullptr;
     std::call_once(once, [] {
@@ -193,6 +193,19 @@ EncodeTiledFn encode_fn() {
             cudaGetLastError();
     });
     return fn;
+}
+
+// q [N, heads, D] by boxes of 64 elements x G heads x tpt tokens.
+inline bool make_q_map(CUtensorMap *m, const va_heads &q, int N, int D, int G, int tpt) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)q.num_heads, (cuuint64_t)N};
+    cuuint64_t strides[2] = {(cuuint64_t)q.stride_head * 2, (cuuint64_t)q.stride_token * 2};
+    cuuint32_t box[3] = {64u, (cuuint32_t)G, (cuuint32_t)tpt};
+    cuuint32_t one[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q.data, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace

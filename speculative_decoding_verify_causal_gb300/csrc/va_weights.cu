@@ -1,0 +1,372 @@
+// The attention weight that each cached token gathers from a chunk of new tokens, for sm_103a (tcgen05 + TMEM + TMA).
+//
+//     w[b, g, j] = sum over tokens t with j <= L - n + t, and query heads h of kv head g, of exp(s_j - lse[t, h]),
+//     s_j = <q[t, h], K_j> / sqrt(D),
+// with the log-sum-exp of the attention itself, so that a token's weights over the keys sum to one.
+//
+// A CTA holds a block of keys in shared memory (one tile of 128 at head_dim 256, else two) and lets the packed rows of
+// q (128 at a time, as chunk attention packs them) pass by: S^T = K Q^T, keys on the tensor memory's lanes.  A thread
+// then owns a key: its sum runs along its own lane, so nothing is exchanged, and -lse of the rows is a broadcast read.
+// Half of the attention's products, the same exponentials, no maximum, no second product.
+// Where there are few blocks of keys, a cluster shares one: its CTAs take the tiles of rows in turn and their sums
+// are added in rank order, so that the result does not depend on timing.  No atomics.
+//
+// Arithmetic: the keys' codes are exact in bf16, products exact, sums binary32; a thread adds a tile's exponentials
+// first and the tiles' sums with a compensation, so that 32,768 rows cost no more bits than 128.
+#include <math.h>
+
+#include "va_chunk.h"
+#include "va_convert.cuh"
+
+namespace va {
+namespace {
+
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kRows = kMmaRows;  // packed rows of one tile of q
+constexpr int kLseRing = 16;     // tiles whose lse is held: the stages of q, two tiles of scores, one being written
+
+template <int D>
+struct Cfg {
+    static constexpr int kKeyTiles = weight_keys(D) / 128;
+    static constexpr int kChunkBytes = 128 * 128;  // 64 elements of 128 rows
+    static constexpr int kTileBytes = D / 64 * kChunkBytes;
+    static constexpr int kStages = D == 64 ? 8 : D == 128 ? 4 : 2;
+    static constexpr int kSumWarps = 4 * kKeyTiles;
+    static constexpr int kThreads = (kSumWarps + 2) * 32;
+    static constexpr int kK = 0;
+    static constexpr int kQ = kKeyTiles * kTileBytes;
+    static constexpr int kLse = kQ + kStages * kTileBytes;
+    static constexpr int kSum = kLse + kLseRing * kRows * 4;
+    static constexpr int kBars = kSum + kKeyTiles * 128 * 4;
+    static constexpr int kSmem = kBars + 32 * 8 + 1024;
+    static_assert(kSmem <= (int)kMaxSmemPerBlock && kLseRing >= kStages + 3, "shared memory");
+};
+
+enum Bar : int {
+    kQFull = 0,              // stages
+    kQEmpty = 8,             // stages
+    kSFull = 16,             // key tile * 2 + buffer
+    kSEmpty = kSFull + 4,
+    kDone = kSEmpty + 4,
+    kTmemSlot = 31,
+};
+
+struct Args {
+    CUtensorMap tm_q;
+    WeightParams p;
+};
+
+// 16 elements of a cached row as 8 words of two bf16, exact.
+template <int DT>
+struct KeyPiece {
+    static constexpr int kBytes = DT == VA_BF16 ? 32 : DT == VA_INT4 ? 8 : DT == VA_INT2 ? 4 : 16;
+    uint32_t w[kBytes / 4];
+    __device__ __forceinline__ void load(const void *from) {
+        if constexpr (kBytes == 32) {
+            const uint4 a = __ldg(static_cast<const uint4 *>(from)), b = __ldg(static_cast<const uint4 *>(from) + 1);
+            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+        } else if constexpr (kBytes == 16) {
+            const uint4 a = __ldg(static_cast<const uint4 *>(from));
+            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+        } else if constexpr (kBytes == 8) {
+            const uint2 a = __ldg(static_cast<const uint2 *>(from));
+            w[0] = a.x, w[1] = a.y;
+        } else {
+            w[0] = __ldg(static_cast<const uint32_t *>(from));
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kBytes / 4; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ void store(uint32_t lo, uint32_t hi) const {
+        uint32_t h[8];
+        if constexpr (DT == VA_BF16) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[i] = w[i];
+        } else {
+            RawPiece<DT> raw;
+#pragma unroll
+            for (int i = 0; i < kBytes / 4; ++i) raw.w[i] = w[i];
+            raw.to_half(h);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+                h[i] = pack_bf162(f.x, f.y);
+            }
+        }
+        sts_u4(lo, make_uint4(h[0], h[1], h[2], h[3]));
+        sts_u4(hi, make_uint4(h[4], h[5], h[6], h[7]));
+    }
+};
+
+template <int D, int DT>
+__global__ void __launch_bounds__(Cfg<D>::kThreads, 1) weights_kernel(const __grid_constant__ Args args) {
+    using C = Cfg<D>;
+    const WeightParams &p = args.p;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                            ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = smem_u32(smem);
+    auto bar = [&](int i) { return sbase + C::kBars + 8u * i; };
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int ranks = p.cluster, rank = blockIdx.x % ranks;
+
+    griddep_wait();
+    const WeightItem it = p.items[blockIdx.x / ranks];
+    const int G = p.G, tpt = p.tpt;
+    const int before = it.L - it.n;                     // keys that every token of the chunk sees
+    const int t_first = max(0, it.key0 - before);       // the first token that sees one of the block's keys
+    const int all = (it.n - t_first + tpt - 1) / tpt;   // tiles of rows
+    const int tiles = all > rank ? (all - rank + ranks - 1) / ranks : 0;
+    auto tile_t0 = [&](int m) { return t_first + (m * ranks + rank) * tpt; };
+    constexpr int kProducerWarp = C::kSumWarps, kMmaWarp = C::kSumWarps + 1;
+
+    if (warp == kProducerWarp && lane == 0) {
+        prefetch_tensormap(&args.tm_q);
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(bar(kQFull + i), 1);
+            mbar_init(bar(kQEmpty + i), 1);
+        }
+        for (int i = 0; i < 2 * C::kKeyTiles; ++i) {
+            mbar_init(bar(kSFull + i), 1);
+            mbar_init(bar(kSEmpty + i), 4);
+        }
+        mbar_init(bar(kDone), 1);
+        fence_barrier_init();
+    } else if (warp == kMmaWarp) {
+        tmem_alloc(bar(kTmemSlot), 256 * C::kKeyTiles);
+        tmem_relinquish();
+    }
+    const int32_t *bt = p.block_table + (size_t)it.b * p.bt_stride;
+    auto page_of = [&](int key) -> int {  // -1: no such key
+        if (key >= it.L) return -1;
+        const int page = __ldg(bt + key / VA_PAGE_SIZE);
+        return page < 0 || (p.num_pages > 0 && page >= p.num_pages) ? -1 : page;
+    };
+    if (warp < C::kSumWarps) {
+        // the block's keys, 16 elements a piece
+        constexpr int kPieces = D / 16, kBatch = 4;
+        constexpr int kTotal = C::kKeyTiles * 128 * kPieces, kStride = C::kSumWarps * 32;
+        const unsigned char *pages = static_cast<const unsigned char *>(p.k_pages);
+#pragma unroll 1
+        for (int e0 = tid; e0 < kTotal; e0 += kBatch * kStride) {
+            KeyPiece<DT> x[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int e = e0 + i * kStride, key = it.key0 + e / kPieces;
+                const int page = page_of(key);
+                if (page < 0)
+                    x[i].zero();
+                else
+                    x[i].load(pages + ((((size_t)page * VA_PAGE_SIZE + key % VA_PAGE_SIZE) * p.Hkv + it.kvh) * kPieces +
+                                       e % kPieces) * KeyPiece<DT>::kBytes);
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int e = e0 + i * kStride, row = e / kPieces, u = e % kPieces * 2;
+                const uint32_t at = sbase + C::kK + (row / 128) * C::kTileBytes + (u / 8) * C::kChunkBytes;
+                x[i].store(at + sw128(row % 128, u % 8), at + sw128(row % 128, u % 8 + 1));
+            }
+        }
+        static_assert(kTotal % (kBatch * kStride) == 0, "whole batches");
+        fence_proxy_async_smem();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = lds_u32(bar(kTmemSlot));
+    bool ok = true;
+
+    if (warp == kProducerWarp) {
+        // ------------------------------------------------------------ producer: rows of q, and their -lse in units of ln 2
+        auto load_lse = [&](int m, float (&x)[4]) {
+            const int t0 = tile_t0(m);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 32 * i + lane, t = t0 + r / G;
+                const bool in = m < tiles && r < tpt * G && t < it.n;
+                const float l = in ? __ldg(p.lse + (size_t)(it.q0 + t) * p.Hq + it.kvh * G + r % G) : INFINITY;
+                x[i] = l == -INFINITY ? -INFINITY : -l * 1.4426950408889634f;  // a row without keys gives nothing
+            }
+        };
+        float next[4];
+        load_lse(0, next);
+        int issued = 0;
+        for (int m = 0; m < tiles; ++m) {
+            const int st = m % C::kStages;
+            if (m >= C::kStages) {
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(kQEmpty + st), ((m / C::kStages) & 1) ^ 1, kWaitNs));
+                if (!ok) break;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                sts_f32(sbase + C::kLse + 4u * ((m % kLseRing) * kRows + 32 * i + lane), next[i]);
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar(kQFull + st), (uint32_t)(D / 64 * G * tpt * 128));
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load_3d(sbase + C::kQ + st * C::kTileBytes + c * C::kChunkBytes, &args.tm_q, c * 64, it.kvh * G,
+                                it.q0 + tile_t0(m), bar(kQFull + st));
+            }
+            __syncwarp();
+            issued = m + 1;
+            load_lse(m + 1, next);
+        }
+        if (lane == 0)
+            for (int m = max(0, issued - C::kStages); m < issued; ++m)
+                if (!mbar_wait(bar(kQFull + m % C::kStages), (m / C::kStages) & 1, kWaitNs)) ok = false;
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------ MMA issue
+        if (lane == 0) {
+            constexpr uint32_t id = idesc_f16(128, kRows, 1, 0, 0);
+            const uint64_t kdesc = smem_desc(sbase + C::kK, 16, 1024, 2), qdesc = smem_desc(sbase + C::kQ, 16, 1024, 2);
+            for (int m = 0; m < tiles && ok; ++m) {
+                const int st = m % C::kStages;
+                ok = mbar_wait(bar(kQFull + st), (m / C::kStages) & 1, kWaitNs);
+                for (int kt = 0; kt < C::kKeyTiles && ok; ++kt) {
+                    const int s = kt * 2 + (m & 1);
+                    if (m >= 2) ok = mbar_wait(bar(kSEmpty + s), ((m >> 1) & 1) ^ 1, kWaitNs);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t off = (uint64_t)((kk / 4) * (C::kChunkBytes >> 4) + (kk % 4) * 2);
+                        mma_ss(tmem + s * kRows, kdesc + (uint64_t)(kt * (C::kTileBytes >> 4)) + off,
+                               qdesc + (uint64_t)(st * (C::kTileBytes >> 4)) + off, id, kk > 0);
+                    }
+                    mma_commit(bar(kSFull + s));
+                }
+                mma_commit(bar(kQEmpty + st));
+            }
+            mma_commit(bar(kDone));
+            if (!mbar_wait(bar(kDone), 0, kWaitNs)) ok = false;
+        }
+    } else {
+        // ------------------------------------------------------------ sums
+        const int kt = warp >> 2, row = (warp & 3) * 32 + lane;
+        const int key = it.key0 + kt * 128 + row;
+        const uint32_t lane_tm = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const int page = page_of(key);
+        float scale = p.sm_scale_log2;
+        if (DT != VA_BF16 && page >= 0)
+            scale *= __ldg(p.k_scale + ((size_t)page * VA_PAGE_SIZE + key % VA_PAGE_SIZE) * p.Hkv + it.kvh);
+        const uint64_t c2 = f2_pack(__float_as_uint(scale), __float_as_uint(scale));
+        float sum = 0.f, lost = 0.f;
+        const int last_key = it.key0 + C::kKeyTiles * 128 - 1;  // of the block: both of a CTA's tiles take one view
+        for (int m = 0; m < tiles; ++m) {
+            const int s = kt * 2 + (m & 1), t0 = tile_t0(m);
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(kSFull + s), (m >> 1) & 1, kWaitNs));
+            if (!ok) break;
+            tc_fence_after();
+            // columns [from, to) of the tile are rows that see this key
+            const int to = min(tpt, it.n - t0) * G;
+            const bool cut = to < kRows || last_key > before + t0;
+            const int from = max(0, key - before - t0) * G;
+            const uint32_t nl = sbase + C::kLse + 4u * ((m % kLseRing) * kRows);
+            uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t x[32];
+                tmem_ld32(lane_tm + s * kRows + 32 * c, x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const uint4 l = lds_u4(nl + 128u * c + 4u * j);
+                    f2_unpack(f2_fma(f2_pack(x[j], x[j + 1]), c2, f2_pack(l.x, l.y)), x[j], x[j + 1]);
+                    f2_unpack(f2_fma(f2_pack(x[j + 2], x[j + 3]), c2, f2_pack(l.z, l.w)), x[j + 2], x[j + 3]);
+                    if (cut) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (32 * c + j + e < from || 32 * c + j + e >= to) x[j + e] = 0xFF800000u;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[j + e] = __float_as_uint(ex2_approx(__uint_as_float(x[j + e])));
+                    acc[(j / 4) & 1] = f2_add(acc[(j / 4) & 1], f2_pack(x[j], x[j + 1]));
+                    acc[2 + ((j / 4) & 1)] = f2_add(acc[2 + ((j / 4) & 1)], f2_pack(x[j + 2], x[j + 3]));
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kSEmpty + s));
+            uint32_t a, b;
+            f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), a, b);
+            const float y = __fsub_rn(__fadd_rn(__uint_as_float(a), __uint_as_float(b)), lost);
+            const float t = __fadd_rn(sum, y);
+            lost = __fsub_rn(__fsub_rn(t, sum), y);
+            if (!(fabsf(lost) < INFINITY)) lost = 0.f;  // of a sum that is not finite
+            sum = t;
+        }
+        sts_f32(sbase + C::kSum + 4u * tid, page < 0 ? 0.f : sum);
+    }
+    if (!ok) atomicOr(p.flags, kFlagTimeoutBit);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 256 * C::kKeyTiles);
+    }
+    if (ranks > 1) cluster_sync();
+    if (rank == 0 && warp < C::kSumWarps) {
+        const int key = it.key0 + tid;
+        float sum = lds_f32(sbase + C::kSum + 4u * tid);
+        for (int r = 1; r < ranks; ++r) sum += ld_cluster_f32(smem + C::kSum + 4 * tid, r);
+        if (key < it.L) {
+            const int64_t at = it.b * p.stride_seq + it.kvh * p.stride_head + key;
+            if (p.accumulate && key < before) sum += p.weights[at];
+            p.weights[at] = sum;
+            if (p.slot_pos && key >= before) p.slot_pos[at] = p.positions[it.q0 + key - before];
+            if (page_of(key) < 0) atomicOr(p.flags, kFlagBadPage);
+        }
+    }
+    if (ranks > 1) cluster_sync();  // the sums are read
+}
+
+template <int D, int DT>
+cudaError_t launch_one(const WeightParams &p, const va_heads &q, int N, int n, cudaStream_t s) {
+    using C = Cfg<D>;
+    Args a;
+    a.p = p;
+    if (!make_q_map(&a.tm_q, q, N, D, p.G, p.tpt)) return cudaErrorInvalidValue;
+    auto k = weights_kernel<D, DT>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(n * p.cluster);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, k, a);
+}
+
+template <int D>
+cudaError_t launch_d(const WeightParams &p, const va_heads &q, int N, int dtype, int n, cudaStream_t s) {
+    switch (dtype) {
+    case VA_BF16: return launch_one<D, VA_BF16>(p, q, N, n, s);
+    case VA_FP8_E4M3: return launch_one<D, VA_FP8_E4M3>(p, q, N, n, s);
+    case VA_INT8: return launch_one<D, VA_INT8>(p, q, N, n, s);
+    case VA_INT4: return launch_one<D, VA_INT4>(p, q, N, n, s);
+    default: return launch_one<D, VA_INT2>(p, q, N, n, s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_weights(const WeightParams &p, const va_heads &q, int N, int D, int dtype, int num_blocks, cudaStream_t s) {
+    if (num_blocks <= 0) return cudaSuccess;
+    switch (D) {
+    case 64: return launch_d<64>(p, q, N, dtype, num_blocks, s);
+    case 128: return launch_d<128>(p, q, N, dtype, num_blocks, s);
+    default: return launch_d<256>(p, q, N, dtype, num_blocks, s);
+    }
+}
+
+}  // namespace va
