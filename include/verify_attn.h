@@ -730,6 +730,69 @@ int verify_attn_chunk_weights(const va_chunk_plan *plan, const va_heads *q, cons
                               int64_t weights_stride_head, int accumulate, int32_t *slot_pos,
                               const int32_t *positions, void *stream);
 
+/* Log probabilities of given tokens: what a caller reports beside the tokens
+ * that the acceptance step emits, or for a prompt's own tokens.  For row n with
+ * logits x[0 .. vocab-1] and p = softmax(x):
+ *     logprobs[n]  = ln p(tokens[n])
+ *     ranks[n]     = how many entries come before the token in descending order,
+ *                    equal ones by index (0: it is the top one)
+ *     entropy[n]   = - sum p ln p
+ *     top_tokens[n, k], top_logprobs[n, k]: the first num_top entries of that
+ *                    order
+ * in binary32, relative to small values too: ln p near 0 and the entropy of a
+ * row with one likely token keep their bits.  Entries of -inf have no weight; a
+ * row of nothing else gives log probabilities of -inf and entropy 0.  A NaN or
+ * +inf makes the row's logprobs, entropy and top_logprobs NaN; NaN comes last in
+ * the order.  A token outside [0, vocab) has log probability -inf and rank -1.
+ * Layouts (device): logits [num_rows, vocab] of `type`, rows `stride` elements
+ * apart (any alignment of its type; rows of 16-byte alignment are read as they
+ * lie), tokens int32 [num_rows], outputs contiguous; logprobs, ranks and
+ * entropy may be NULL, top_tokens and top_logprobs where num_top is 0.
+ * 0 <= num_rows <= 2^27, 1 <= vocab <= 2^30, 0 <= num_top <=
+ * min(VA_LOGPROBS_MAX_TOP, vocab).  Returns VA_OK when enqueued,
+ * VA_ERR_INVALID_ARGUMENT, VA_ERR_UNSUPPORTED for an unknown type,
+ * VA_ERR_CUDA. */
+#define VA_LOGPROBS_MAX_TOP 32
+int verify_attn_logprobs(const void *logits, int64_t stride, va_float_type type, const int32_t *tokens,
+                         int num_rows, int vocab, int num_top, float *logprobs, int32_t *ranks,
+                         float *entropy, int32_t *top_tokens, float *top_logprobs, void *stream);
+
+/* Cut sequences back to keep_lens[b] cached tokens each, by the weight that
+ * the tokens have gathered.  Every kv head keeps min(keep_lens[b], seq_lens[b])
+ * tokens of its own choice: first the protected ones, whose position is below
+ * num_sinks or at least recent_from[b] (NULL: none), then the heaviest; of equal
+ * ones the lower slot (NaN weighs least).  The position of slot j is slot_pos[b,
+ * g, j], or j where slot_pos is NULL.  The kept tokens end up in the first slots
+ * of the sequence, each head's rows of K and V with their scales moved in place:
+ * in ascending order, the k-th kept slot at or above keep_lens[b] goes to the
+ * k-th slot below it whose token goes; all others stay.  weights and slot_pos
+ * move with them (their entries from keep_lens[b] on are left as they are).
+ * new_lens[b] receives the new length: give it to verify_attn_pages_resize after
+ * the call of the last layer (each layer chooses for itself; seq_lens is only
+ * read), and from then on give rotary positions to new tokens explicitly, since
+ * a token's slot is no longer its position.  keep_lens[b] negative or not below
+ * seq_lens[b]: the sequence is left alone.
+ * A sequence with a page that others hold too (ref_count[page] > 1; ref_count
+ * NULL: not looked at) or with a length outside [0, num_slots] or past its
+ * block table's row is left alone and sets VA_PAGES_BAD_REQUEST in *flags, one
+ * with a block-table entry that is negative or, for num_pages > 0, not below
+ * it sets VA_PAGES_BAD_ENTRY (flags may be NULL; the call only ORs into it).
+ * Layouts: cache, block table and seq_lens as for verify_attn; weights fp32 and
+ * slot_pos int32 [num_seqs, num_kv_heads, num_slots] with the strides given;
+ * keep_lens, recent_from, new_lens int32 [num_seqs]; workspace: at least
+ * verify_attn_evict_workspace_bytes (0 for sizes that are rejected), 16-byte
+ * aligned, no initialisation; calls that share one must be ordered on one
+ * stream.  num_seqs * num_kv_heads <= 65535, num_slots <= 2^30.  Returns VA_OK
+ * when enqueued, VA_ERR_INVALID_ARGUMENT, VA_ERR_UNSUPPORTED, VA_ERR_CUDA. */
+size_t verify_attn_evict_workspace_bytes(int num_seqs, int num_kv_heads, int num_slots);
+int verify_attn_evict(void *k_pages, void *v_pages, float *k_scale, float *v_scale, va_kv_dtype kv_dtype,
+                      const int32_t *block_table, int block_table_stride, const int32_t *seq_lens,
+                      int num_seqs, int num_kv_heads, int head_dim, int num_pages, float *weights,
+                      int32_t *slot_pos, int64_t stride_seq, int64_t stride_head, int num_slots,
+                      const int32_t *keep_lens, int num_sinks, const int32_t *recent_from,
+                      const int32_t *ref_count, int32_t *new_lens, void *workspace, int32_t *flags,
+                      void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -38,6 +38,7 @@ PATH_CODES = {"auto": VA_PATH_AUTO, "warp": VA_PATH_WARP, "mma": VA_PATH_MMA}
 PAGE_SIZE = 16
 VA_FLOAT_BF16, VA_FLOAT_FP16, VA_FLOAT_FP32 = 0, 1, 2
 ROPE_MAX_PAIRS, ROPE_MAX_AXES = 128, 4
+LOGPROBS_MAX_TOP = 32
 # bits of a page pool's flag word
 VA_PAGES_BAD_ENTRY, VA_PAGES_EXHAUSTED, VA_PAGES_BAD_REQUEST, VA_PAGES_BAD_COUNT = 1, 8, 16, 32
 
@@ -177,8 +178,13 @@ def _load():
         lib.verify_attn_chunk_plan_device_flags.argtypes = [P, I, ctypes.POINTER(I), P]
         lib.verify_attn_chunk.argtypes = [P, H, P, P, P, P, P, I, I, P, P, P]
         lib.verify_attn_chunk_weights.argtypes = [P, H, P, P, P, I, I, P, P, ctypes.c_int64, ctypes.c_int64, I, P, P, P]
+        lib.verify_attn_logprobs.argtypes = [P, ctypes.c_int64, I, P, I, I, I, P, P, P, P, P, P]
+        lib.verify_attn_evict_workspace_bytes.argtypes = [I, I, I]
+        lib.verify_attn_evict_workspace_bytes.restype = ctypes.c_size_t
+        lib.verify_attn_evict.argtypes = [P, P, P, P, I, P, I, P, I, I, I, I, P, P, ctypes.c_int64, ctypes.c_int64, I, P, I,
+                                          P, P, P, P, P, P]
         for f in ("verify_attn_chunk_plan", "verify_attn_chunk_plan_get_info", "verify_attn_chunk_plan_device_flags",
-                  "verify_attn_chunk", "verify_attn_chunk_weights"):
+                  "verify_attn_chunk", "verify_attn_chunk_weights", "verify_attn_logprobs", "verify_attn_evict"):
             getattr(lib, f).restype = I
         for f in ("verify_attn_rope_init", "verify_attn_rope", "verify_attn_rope_append", "verify_attn_accept_probs",
                   "verify_attn_pages_resize", "verify_attn_pages_resize_ex", "verify_attn_pages_fork",
@@ -1214,7 +1220,114 @@ def verify_attn_chunk_weights(plan: ChunkPlan, q, k_pages, k_scale, block_table,
     return weights
 
 
+def verify_attn_logprobs(logits, tokens, num_top=0, stream=None):
+    """Log probabilities of ``tokens`` (int32 ``[N]``) under ``softmax(logits)`` (``[N,
+    V]`` fp32, bf16 or fp16, any row stride), their place in the descending order,
+    the rows' entropy and the ``num_top`` (at most ``LOGPROBS_MAX_TOP``) likeliest
+    tokens.  Definition in ``include/verify_attn.h``.  Not recorded by autograd: in
+    grad mode logits that require a gradient are refused.  Returns (logprobs fp32
+    ``[N]``, ranks int32 ``[N]``, entropy fp32 ``[N]``, top_tokens int32 ``[N, num_top]``,
+    top_logprobs fp32 ``[N, num_top]``)."""
+    torch = _torch or _bind_torch()
+    if _grad_mode() and _wants_gradient(logits):
+        raise _gradient_refused("verify_attn_logprobs")
+    f32, i32 = torch.float32, torch.int32
+    device, index = _device_of(logits, "logits")
+    code = _float_code(logits, "logits")
+    n = logits.shape
+    if len(n) != 2 or (n[1] > 1 and logits.stride(1) != 1):
+        raise ValueError(f"logits must be [N, V], contiguous in its last dimension, got {list(n)} with strides "
+                         f"{list(logits.stride())}")
+    N, V = n
+    if N | V > _INT_MAX:
+        raise _too_large("logits", n)
+    K = int(num_top)
+    if not 0 <= K <= min(LOGPROBS_MAX_TOP, V):
+        raise ValueError(f"num_top must be between 0 and {min(LOGPROBS_MAX_TOP, V)}")
+    tp = _ptr(tokens, "tokens", i32, index, (N,))
+    st, guard = _launch_on(device, stream)
+    with guard:
+        logprobs, entropy = torch.empty((N,), dtype=f32, device=device), torch.empty((N,), dtype=f32, device=device)
+        ranks = torch.empty((N,), dtype=i32, device=device)
+        top_tokens = torch.empty((N, K), dtype=i32, device=device)
+        top_logprobs = torch.empty((N, K), dtype=f32, device=device)
+        rc = 0
+        if N:
+            rc = (_lib or _load()).verify_attn_logprobs(
+                logits.data_ptr(), logits.stride(0), code, tp, N, V, K, logprobs.data_ptr(), ranks.data_ptr(),
+                entropy.data_ptr(), top_tokens.data_ptr(), top_logprobs.data_ptr(), st)
+    if rc:
+        _check(rc, "verify_attn_logprobs")
+    return logprobs, ranks, entropy, top_tokens, top_logprobs
+
+
+def verify_attn_evict(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, weights, keep_lens, kv_dtype, slot_pos=None,
+                      num_sinks=0, recent_from=None, ref_count=None, new_lens=None, flags=None, num_pages=0, stream=None):
+    """Cut sequences back to ``keep_lens`` (int32 ``[num_seqs]`` on the device; negative
+    or not below the length: left alone) cached tokens: every kv head keeps the
+    protected tokens (positions below ``num_sinks`` or from ``recent_from``, int32
+    ``[num_seqs]``, on) and then those with the largest ``weights`` (fp32 ``[num_seqs,
+    Hkv, slots]``, as ``verify_attn_chunk_weights`` gathers them).  Rows of K and V,
+    scales, ``weights`` and ``slot_pos`` (int32 like ``weights``: the position of each
+    slot's token; None: the slot) move into the first slots, in place.  Pass
+    ``ref_count`` of a page pool whose sequences may share pages: sequences that do
+    are left alone and flagged.  Call it for every layer, then give the result to
+    ``verify_attn_pages_resize``.  Definition in ``include/verify_attn.h``.  Returns the
+    new lengths, int32 ``[num_seqs]``."""
+    torch = _torch or _bind_torch()
+    code = _dtype_code(kv_dtype)
+    device, index = _device_of(k_pages, "k_pages")
+    f32, i32 = torch.float32, torch.int32
+    kvd = _CACHE_TYPES.get(code, ())
+    kp, vp = _ptr_of(k_pages, "k_pages", kvd, index), _ptr_of(v_pages, "v_pages", kvd, index)
+    n = k_pages.shape
+    if len(n) != 4 or n[1] != PAGE_SIZE or v_pages.shape != n:
+        raise ValueError(f"k_pages and v_pages must be [num_pages, {PAGE_SIZE}, Hkv, row], got {list(n)} and "
+                         f"{list(v_pages.shape)}")
+    pages, _, Hkv, D = n
+    D = D * 2 if code == VA_INT4 else D * 4 if code == VA_INT2 else D
+    bt, sl = _ptr(block_table, "block_table", i32, index), _ptr(seq_lens, "seq_lens", i32, index)
+    nt = block_table.shape
+    if len(nt) != 2 or seq_lens.shape != nt[:1]:
+        raise ValueError(f"block_table must be [num_seqs, stride] and seq_lens [num_seqs], got {list(nt)} and "
+                         f"{list(seq_lens.shape)}")
+    B, stride = nt
+    if pages | B | Hkv | stride | weights.shape[-1] > _INT_MAX:
+        raise _too_large("k_pages, block_table or weights", (*n, *nt, *weights.shape))
+    if num_pages > pages:
+        raise ValueError(f"num_pages is {num_pages}, the cache has {pages}")
+    ks = vs = None
+    if code != VA_BF16:
+        ks, vs = _ptr(k_scale, "k_scale", f32, index, n[:3]), _ptr(v_scale, "v_scale", f32, index, n[:3])
+    wp, seq, head = _per_slot(weights, "weights", f32, index, (B, Hkv, 0))
+    slots = weights.shape[2]
+    sp = None
+    if slot_pos is not None:
+        sp, *strides = _per_slot(slot_pos, "slot_pos", i32, index, (B, Hkv, slots))
+        if strides != [seq, head]:
+            raise ValueError("slot_pos must have the strides of weights")
+    kl = _ptr(keep_lens, "keep_lens", i32, index, (B,))
+    rf = None if recent_from is None else _ptr(recent_from, "recent_from", i32, index, (B,))
+    rc_ = None if ref_count is None else _ptr(ref_count, "ref_count", i32, index, (pages,))
+    fl = None if flags is None else _ptr(flags, "flags", i32, index)
+    lib = _lib or _load()
+    size = lib.verify_attn_evict_workspace_bytes(B, Hkv, slots)
+    st, guard = _launch_on(device, stream)
+    with guard:
+        workspace = torch.empty(max(1, size), dtype=torch.uint8, device=device)
+        if new_lens is None:
+            new_lens = torch.empty((B,), dtype=i32, device=device)
+        rc = lib.verify_attn_evict(kp, vp, ks, vs, code, bt, stride, sl, B, Hkv, D, num_pages or pages, wp, sp, seq, head,
+                                   slots, kl, int(num_sinks), rf, rc_, _ptr(new_lens, "new_lens", i32, index, (B,)),
+                                   workspace.data_ptr(), fl, st)
+    if rc:
+        _check(rc, "verify_attn_evict")
+    return new_lens
+
+
 __all__ = [
+    "verify_attn_evict",
+    "verify_attn_logprobs", "LOGPROBS_MAX_TOP",
     "verify_attn_chunk_weights",
     "ChunkPlan", "verify_attn_chunk_plan", "verify_attn_chunk_plan_destroy", "verify_attn_chunk_plan_device_flags",
     "verify_attn_chunk",
