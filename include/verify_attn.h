@@ -692,6 +692,13 @@ typedef struct {
 int verify_attn_chunk_plan(const int32_t *chunk_lens_host, const int32_t *seq_lens_host, int num_seqs,
                            int num_q_heads, int num_kv_heads, int head_dim, va_kv_dtype kv_dtype,
                            int num_sms, va_chunk_plan **out_plan);
+/* Pure host planning (no CUDA call): fills *info and, when items != NULL, up to
+ * max_items work items as 6 ints each (seq, kv_head, first row of q, tokens,
+ * key_begin, key_end), in launch order. */
+int verify_attn_chunk_plan_describe(const int32_t *chunk_lens_host, const int32_t *seq_lens_host,
+                                    int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                    va_kv_dtype kv_dtype, int num_sms, va_chunk_plan_info *info,
+                                    int32_t *items, int max_items);
 /* As verify_attn_plan_destroy, _get_info and _device_flags (bits 0 and 2). */
 void verify_attn_chunk_plan_destroy(va_chunk_plan *plan);
 int verify_attn_chunk_plan_get_info(const va_chunk_plan *plan, va_chunk_plan_info *info);

@@ -172,6 +172,8 @@ def _load():
         lib.verify_attn_pages_fork.argtypes = [P, P, P, P, I, I, P]
         lib.verify_attn_pages_compact.argtypes = [P, P]
         lib.verify_attn_chunk_plan.argtypes = [P, P, I, I, I, I, I, I, ctypes.POINTER(P)]
+        lib.verify_attn_chunk_plan_describe.argtypes = [P, P, I, I, I, I, I, I, ctypes.POINTER(ChunkPlanInfo), P, I]
+        lib.verify_attn_chunk_plan_describe.restype = I
         lib.verify_attn_chunk_plan_destroy.argtypes = [P]
         lib.verify_attn_chunk_plan_destroy.restype = None
         lib.verify_attn_chunk_plan_get_info.argtypes = [P, ctypes.POINTER(ChunkPlanInfo)]
@@ -1076,6 +1078,23 @@ def verify_attn_chunk_plan(chunk_lens, seq_lens, num_q_heads, num_kv_heads, head
                      torch.cuda.current_device())
 
 
+def verify_attn_chunk_plan_describe(chunk_lens, seq_lens, num_q_heads, num_kv_heads, head_dim, kv_dtype, num_sms):
+    """Host-only planning (no GPU needed): (info dict, items int32 [n, 6]) with
+    items = (seq, kv_head, first row of q, tokens, key_begin, key_end)."""
+    lib = _load()
+    new, lens = _host_lens(chunk_lens), _host_lens(seq_lens)
+    if len(new) != len(lens):
+        raise ValueError(f"{len(new)} chunk_lens and {len(lens)} seq_lens")
+    args = (new.ctypes.data, lens.ctypes.data, len(new), int(num_q_heads), int(num_kv_heads), int(head_dim),
+            _dtype_code(kv_dtype), int(num_sms))
+    info = ChunkPlanInfo()
+    _check(lib.verify_attn_chunk_plan_describe(*args, ctypes.byref(info), None, 0), "verify_attn_chunk_plan_describe")
+    items = np.zeros((max(info.num_items, 1), 6), np.int32)
+    _check(lib.verify_attn_chunk_plan_describe(*args, ctypes.byref(info), items.ctypes.data, info.num_items),
+           "verify_attn_chunk_plan_describe")
+    return info.as_dict(), items[:info.num_items]
+
+
 def verify_attn_chunk_plan_destroy(plan: ChunkPlan):
     plan.destroy()
 
@@ -1329,7 +1348,7 @@ __all__ = [
     "verify_attn_evict",
     "verify_attn_logprobs", "LOGPROBS_MAX_TOP",
     "verify_attn_chunk_weights",
-    "ChunkPlan", "verify_attn_chunk_plan", "verify_attn_chunk_plan_destroy", "verify_attn_chunk_plan_device_flags",
+    "ChunkPlan", "verify_attn_chunk_plan", "verify_attn_chunk_plan_describe", "verify_attn_chunk_plan_destroy", "verify_attn_chunk_plan_device_flags",
     "verify_attn_chunk",
     "Rope", "verify_attn_rope_spec", "verify_attn_rope", "verify_attn_rope_append", "verify_attn_accept_probs",
     "PagePool", "verify_attn_pages_resize", "verify_attn_pages_fork", "verify_attn_pages_compact",

@@ -13,7 +13,7 @@
 struct va_chunk_plan {
     int num_seqs, Hq, Hkv, G, D, kv_dtype, tpt, num_sms, device;
     int total;       // rows of q, out and lse that the chunks take
-    int max_blocks;  // block-table entries of the longest sequence
+    int max_blocks;  // block-table entries of the longest sequence that takes part
     int num_items, num_groups, num_parts, max_tiles, num_blocks, cluster;
     void *dev_mem;
     va::ChunkItem *items;
@@ -166,6 +166,37 @@ void plan_blocks(const int32_t *chunk_lens, const int32_t *seq_lens, int B, int 
         g.cluster *= 2;
 }
 
+// Everything of a plan but its device memory.
+int plan_host(const int32_t *chunk_lens, const int32_t *seq_lens, int B, int Hq, int Hkv, int D, int dtype, int num_sms,
+              va_chunk_plan &p, Geometry &g) {
+    try {
+        plan_geometry(chunk_lens, seq_lens, B, Hkv, Hq / Hkv, D, num_sms, g);
+        plan_blocks(chunk_lens, seq_lens, B, Hkv, Hq / Hkv, D, num_sms, g);
+    } catch (const std::exception &) {
+        return VA_ERR_OUT_OF_MEMORY;
+    }
+    p = {};
+    p.num_seqs = B, p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv, p.D = D, p.kv_dtype = dtype;
+    p.tpt = va::kMmaRows / p.G;
+    p.num_sms = num_sms;
+    for (int b = 0; b < B; ++b) {
+        p.total += chunk_lens[b];
+        if (chunk_lens[b] > 0) p.max_blocks = std::max(p.max_blocks, (seq_lens[b] + VA_PAGE_SIZE - 1) / VA_PAGE_SIZE);
+    }
+    p.num_items = (int)g.items.size();
+    p.num_groups = (int)g.groups.size();
+    p.num_parts = g.num_parts;
+    p.max_tiles = g.max_tiles;
+    p.num_blocks = (int)g.blocks.size();
+    p.cluster = g.cluster;
+    return VA_OK;
+}
+
+void fill_info(const va_chunk_plan &p, va_chunk_plan_info *info) {
+    *info = {p.num_seqs, p.Hq, p.Hkv, p.D, p.kv_dtype, p.total, p.max_blocks, p.num_items, p.num_groups,
+             p.max_tiles * va::kChunkKeys, p.num_sms, p.workspace_bytes};
+}
+
 int fail(cudaError_t e) {
     va::note_cuda_error(e);
     cudaGetLastError();
@@ -216,33 +247,14 @@ int verify_attn_chunk_plan(const int32_t *chunk_lens, const int32_t *seq_lens, i
     }
     if (num_sms == 0) num_sms = sms;
     Geometry g;
-    va_chunk_plan *p = nullptr;
-    try {
-        plan_geometry(chunk_lens, seq_lens, num_seqs, num_kv_heads, num_q_heads / num_kv_heads, head_dim, num_sms, g);
-        plan_blocks(chunk_lens, seq_lens, num_seqs, num_kv_heads, num_q_heads / num_kv_heads, head_dim, num_sms, g);
-        p = new va_chunk_plan();
-    } catch (const std::exception &) {
-        return VA_ERR_OUT_OF_MEMORY;
+    va_chunk_plan *p = new (std::nothrow) va_chunk_plan();
+    if (!p) return VA_ERR_OUT_OF_MEMORY;
+    const int made = plan_host(chunk_lens, seq_lens, num_seqs, num_q_heads, num_kv_heads, head_dim, kv_dtype, num_sms, *p, g);
+    if (made != VA_OK) {
+        delete p;
+        return made;
     }
-    p->num_seqs = num_seqs;
-    p->Hq = num_q_heads;
-    p->Hkv = num_kv_heads;
-    p->G = num_q_heads / num_kv_heads;
-    p->D = head_dim;
-    p->kv_dtype = kv_dtype;
-    p->tpt = va::kMmaRows / p->G;
-    p->num_sms = num_sms;
     p->device = device;
-    for (int b = 0; b < num_seqs; ++b) {
-        p->total += chunk_lens[b];
-        if (chunk_lens[b] > 0) p->max_blocks = std::max(p->max_blocks, (seq_lens[b] + VA_PAGE_SIZE - 1) / VA_PAGE_SIZE);
-    }
-    p->num_items = (int)g.items.size();
-    p->num_groups = (int)g.groups.size();
-    p->num_parts = g.num_parts;
-    p->max_tiles = g.max_tiles;
-    p->num_blocks = (int)g.blocks.size();
-    p->cluster = g.cluster;
     const size_t items = align_up(sizeof(va::ChunkItem) * g.items.size());
     const size_t groups = align_up(sizeof(va::ChunkGroup) * g.groups.size());
     const size_t blocks = align_up(sizeof(va::WeightItem) * g.blocks.size());
@@ -277,6 +289,25 @@ int verify_attn_chunk_plan(const int32_t *chunk_lens, const int32_t *seq_lens, i
     return VA_OK;
 }
 
+int verify_attn_chunk_plan_describe(const int32_t *chunk_lens, const int32_t *seq_lens, int num_seqs, int num_q_heads,
+                                    int num_kv_heads, int head_dim, va_kv_dtype kv_dtype, int num_sms,
+                                    va_chunk_plan_info *info, int32_t *out, int max_items) {
+    const int rc = validate(chunk_lens, seq_lens, num_seqs, num_q_heads, num_kv_heads, head_dim, kv_dtype);
+    if (rc != VA_OK) return rc;
+    if (num_sms < 1 || !info || (out && max_items < 0)) return VA_ERR_INVALID_ARGUMENT;
+    Geometry g;
+    va_chunk_plan p;
+    const int made = plan_host(chunk_lens, seq_lens, num_seqs, num_q_heads, num_kv_heads, head_dim, kv_dtype, num_sms, p, g);
+    if (made != VA_OK) return made;
+    fill_info(p, info);
+    for (int i = 0; out && i < std::min(max_items, p.num_items); ++i) {
+        const va::ChunkItem &it = g.items[i];
+        const int32_t x[6] = {it.b, it.kvh, it.q0, it.nt, it.k_begin, it.k_end};
+        std::copy(x, x + 6, out + 6 * i);
+    }
+    return VA_OK;
+}
+
 void verify_attn_chunk_plan_destroy(va_chunk_plan *p) {
     if (!p) return;
     cudaFree(p->dev_mem);
@@ -285,8 +316,7 @@ void verify_attn_chunk_plan_destroy(va_chunk_plan *p) {
 
 int verify_attn_chunk_plan_get_info(const va_chunk_plan *p, va_chunk_plan_info *info) {
     if (!p || !info) return VA_ERR_INVALID_ARGUMENT;
-    *info = {p->num_seqs, p->Hq, p->Hkv, p->D, p->kv_dtype, p->total, p->max_blocks, p->num_items, p->num_groups,
-             p->max_tiles * va::kChunkKeys, p->num_sms, p->workspace_bytes};
+    fill_info(*p, info);
     return VA_OK;
 }
 
