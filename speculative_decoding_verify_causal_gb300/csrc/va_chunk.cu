@@ -6,16 +6,20 @@
 // head), so each key and value is read once for all of them.  A CTA takes one item: one tile of rows (head_dim 256)
 // or up to two (64, 128) over a range of keys.
 //
-// The MMA warp walks "steps".  Step k of a two-tile item is (rows k % 2, keys k / 2); of a one-tile item it is (keys
-// k).  Either way scores alternate between two tensor-memory slots, and the order is S(0), S(1), then P(k) V(k),
-// S(k + 2): while the softmax of one slot runs, the tensor pipe works on the other.  P overwrites S in its slot; S(k
-// + 2) is issued behind P(k) V(k) by the same thread, and tensor instructions run in their order.
-//   producer warp   page ids from the block table, then TMA boxes (16 slots of one page and head) into the ring
+// Steps.  Step k of a two-tile item is (rows k % 2, keys k / 2); of a one-tile item it is (keys k).  Scores alternate
+// between two tensor-memory slots.  Of two tiles each has its slot and a warp that issues its instructions: S(i + 1) as
+// soon as the softmax has read S(i), then P(i) V(i).  Of one tile one warp issues P(k) V(k), S(k + 2): while the softmax
+// of one slot runs, the tensor pipe works on the other.  At head_dim 256 P overwrites S in its slot; S(k + 2) is issued
+// behind P(k) V(k) by the same thread, and tensor instructions run in their order.
+//   producer warps  page ids from the block table, then TMA boxes (16 slots of one page and head) into the ring
 //   dequant warps   (quantised caches) raw panel -> fp16 panel, exact, in the MMA's swizzled layout; keys' scales
-//   MMA warp        one thread issues everything
-//   softmax warps   four per tile of rows, a thread per row: k scale, mask, running maximum (moved, and O rescaled,
-//                   only when it grows by more than 2^8), P * v_scale * 2^beta back over S; at the end O / l and lse
-// A panel is 128 keys by min(D, 128) elements: what one ring slot holds.
+//   MMA warps       as above; panels are used in the order of the ring
+//   softmax warps   four per tile of rows: k scale, mask, running maximum (moved, and O rescaled, only when it grows by
+//                   more than 2^8), P * v_scale * 2^beta; at the end O / l and lse
+// A softmax thread holds four rows of a quarter of the columns (the 16x256b layout of the tensor memory), so a key's
+// scales are read from shared memory by 8 lanes for 32 rows at once; with a row per lane every lane reads every scale,
+// and those reads alone were half of the shared memory's bandwidth.
+// A panel is one tile of keys by min(D, 128) elements: what one ring slot holds.
 //
 // P is rounded to the type of the values' tile: bf16 for a bf16 cache, fp16 for codes (with v_scale; 2^beta, a power
 // of two by each row's largest v scale in the tile, keeps that product in fp16's normal range).  Scores, maxima,
@@ -27,6 +31,7 @@
 #include <math.h>
 
 #include <cstring>
+#include <type_traits>
 
 #include "va_chunk.h"
 #include "va_convert.cuh"
@@ -36,17 +41,18 @@ namespace {
 
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kRescaleLog2 = 8.0f;
-constexpr int kKeys = kChunkKeys;
-constexpr int kPages = kKeys / VA_PAGE_SIZE;  // pages of a tile of keys
 constexpr int kScaleRing = 4;
-constexpr int kScaleFloats = 2 * kKeys + 4;   // k scales, v scales, the largest v scale of each 32 keys
-constexpr int kBadRing = 16;                  // tiles whose bad pages are remembered: more than the ring holds ahead
+constexpr int kBadRing = 16;   // tiles whose bad pages are remembered: more than the ring holds ahead
 constexpr int kMaxStages = 8;
+constexpr int kProducers = 2;  // warps that issue panels in turn: one alone takes longer than the tensor pipe needs for them
 
 template <int D, int DT>
 struct Cfg {
     static constexpr bool kQuant = DT != VA_BF16;
     static constexpr int kTiles = chunk_tiles(D);
+    static constexpr int kKeys = chunk_keys(D);
+    static constexpr int kPages = kKeys / VA_PAGE_SIZE;
+    static constexpr bool kOver = kTiles == 1;        // probabilities overwrite scores
     static constexpr int kPanelD = D < 128 ? D : 128;
     static constexpr int kPanels = D / kPanelD;       // panels of a K or V tile
     static constexpr int kChunks = kPanelD / 64;      // 64-element chunks of a panel
@@ -55,23 +61,35 @@ struct Cfg {
     static constexpr int kBits = DT == VA_BF16 ? 16 : DT == VA_INT4 ? 4 : DT == VA_INT2 ? 2 : 8;
     static constexpr int kRawRow = kPanelD * kBits / 8;  // bytes of a row of a raw panel
     static constexpr int kRawBytes = kKeys * kRawRow;
-    static constexpr int kQBytes = kMmaRows * D * 2;
-    static constexpr int kStages = kQuant ? (D == 64 ? 6 : 3) : (D == 64 ? 8 : 5);
-    static constexpr int kRawStages = kQuant ? (D == 64 ? 6 : 3) : 0;
+    static constexpr int kQChunk = kMmaRows * 128;       // 64-element chunk of a tile of q
+    static constexpr int kQBytes = D / 64 * kQChunk;
+    static constexpr int kStages = kQuant ? (D == 64 ? 6 : D == 128 ? 5 : 3) : (D == 256 ? 5 : D == 128 ? 7 : 8);
+    static constexpr int kRawStages = kQuant ? (D == 64 ? 6 : D == 128 ? 5 : 3) : 0;
+    static constexpr int kScaleFloats = 2 * kKeys + 4;   // k scales, v scales, the largest v scale of each dequant warp
     static constexpr int kSoftmaxWarps = 4 * kTiles;
     static constexpr int kDequantWarps = kQuant ? 4 : 0;
-    static constexpr int kProducerWarp = kSoftmaxWarps + kDequantWarps;
-    static constexpr int kMmaWarp = kProducerWarp + 1;
-    static constexpr int kThreads = (kMmaWarp + 1) * 32;
-    // all of a row's scores stay in registers where the block's threads leave 200 of them
-    static constexpr bool kKeep = kThreads <= 320;
-    static constexpr uint32_t kOCol = 2 * kKeys;  // S slots at 0 and 128
+    static constexpr int kProducerWarp = kSoftmaxWarps + kDequantWarps;  // and the ones behind it
+    static constexpr int kMmaWarp = kProducerWarp + kProducers;          // one for each tile of rows
+    static constexpr int kThreads = (kMmaWarp + kTiles + 3) / 4 * 128;  // whole warpgroups
+    // Registers of a thread, where the block's even share (kLaunchRegs) is too few for a softmax thread's scores: its
+    // warpgroups take what the others, which need few, give back.
+    static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
+    static constexpr int kSoftmaxRegs = kTiles == 2 ? 168 : 240;
+    static constexpr int kDequantRegs = kTiles == 2 ? 104 : 136;
+    static constexpr int kOtherRegs = kTiles == 2 ? 72 : 120;
+    static_assert(!kQuant || (kSoftmaxWarps * kSoftmaxRegs + kDequantWarps * kDequantRegs + 4 * kOtherRegs) * 32 <=
+                                 kThreads * kLaunchRegs, "registers that the block was launched with");
+    static constexpr uint32_t kPCol = 2 * kKeys;                  // S slots at 0 and kKeys, P slots behind them
+    static constexpr uint32_t kOCol = kOver ? 2 * kKeys : 3 * kKeys;
+    static_assert(kOCol + kTiles * D <= 512, "tensor memory");
     static constexpr int kQ = 0;
     static constexpr int kConv = kTiles * kQBytes;
     static constexpr int kRaw = kConv + kStages * kPanelBytes;
     static constexpr int kScale = kRaw + kRawStages * kRawBytes;
     static constexpr int kBad = kScale + (kQuant ? kScaleRing * kScaleFloats * 4 : 0);
-    static constexpr int kBars = kBad + kBadRing * 4;
+    static constexpr int kStats = kQuant ? 3 : 2;      // values of each row that the softmax hands from thread to thread
+    static constexpr int kStat = kBad + kBadRing * 4;
+    static constexpr int kBars = kStat + kTiles * kStats * kMmaRows * 4;
     static constexpr int kSmem = kBars + 64 * 8 + 1024;  // and slack for the alignment
     static_assert(kSmem <= (int)kMaxSmemPerBlock, "shared memory");
 };
@@ -82,7 +100,8 @@ enum Bar : int {
     kRawFull = kEmpty + kMaxStages,
     kRawEmpty = kRawFull + kMaxStages,
     kSFull = kRawEmpty + kMaxStages,  // scores of a slot
-    kPFull = kSFull + 2,              // its probabilities
+    kSRead = kSFull + 2,              // the softmax has them in registers
+    kPFull = kSRead + 2,              // its probabilities
     kODone = kPFull + 2,              // its product with V
     kOFinal = kODone + 2,
     kQFull = kOFinal + 1,             // q from memory
@@ -100,18 +119,10 @@ struct Args {
     ChunkParams p;
 };
 
-// Place of a panel in the order in which the MMA warp uses them: K0 V0 K1 V1 .. with two tiles of rows, K0 K1 V0 K2
-// V1 .. with one (its next scores are issued before the product).
-__device__ __forceinline__ int k_entry(int i, bool two) { return two ? 2 * i : (i == 0 ? 0 : 2 * i - 1); }
-__device__ __forceinline__ int v_entry(int i, bool two, int n) {
-    return two ? 2 * i + 1 : (i == n - 1 ? 2 * n - 1 : 2 * i + 2);
-}
-// The reverse: which tile, and whether it is V.
-__device__ __forceinline__ int entry_tile(int e, bool two, int n, bool &v) {
-    if (two) {
-        v = e & 1;
-        return e >> 1;
-    }
+// Place of a V tile in the order in which tiles are used, K0 K1 V0 K2 V1 .. (the next scores are issued before the
+// product), n tiles of keys; and the reverse, which tile, and whether it is V.
+__device__ __forceinline__ int v_entry(int i, int n) { return i == n - 1 ? 2 * n - 1 : 2 * i + 2; }
+__device__ __forceinline__ int entry_tile(int e, int n, bool &v) {
     if (e == 0) return v = false, 0;
     if (e == 2 * n - 1) return v = true, n - 1;
     v = !(e & 1);
@@ -138,6 +149,7 @@ __device__ float cached_value(const void *pages, const float *scale, size_t row,
 template <int D, int DT>
 __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __grid_constant__ Args args) {
     using C = Cfg<D, DT>;
+    constexpr int kKeys = C::kKeys, kPages = C::kPages;
     const ChunkParams &p = args.p;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -162,16 +174,17 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
         prefetch_tensormap(&args.tm_v);
         for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(bar(kFull + i), C::kQuant ? C::kDequantWarps : 1);
-            mbar_init(bar(kEmpty + i), 1);
+            mbar_init(bar(kEmpty + i), nq);
             mbar_init(bar(kRawFull + i), 1);
             mbar_init(bar(kRawEmpty + i), C::kQuant ? C::kDequantWarps : 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(kSFull + i), 1);
+            mbar_init(bar(kSRead + i), 4);
             mbar_init(bar(kPFull + i), 4);
             mbar_init(bar(kODone + i), 1);
         }
-        mbar_init(bar(kOFinal), 1);
+        mbar_init(bar(kOFinal), nq);
         mbar_init(bar(kQFull), 1);
         mbar_init(bar(kQReady), 4 * nq);
         mbar_init(bar(kSwept), 4 * nq);
@@ -188,134 +201,169 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
     const uint32_t tmem = lds_u32(bar(kTmemSlot));
     bool ok = true;
 
-    if (warp == C::kProducerWarp) {
-        // ------------------------------------------------------------ producer
-        // q: one box of 64 elements x G heads x tpt tokens per tile of rows and chunk; tokens past q's end read 0
-        if (lane == 0) mbar_arrive_expect_tx(bar(kQFull), (uint32_t)(nq * (D / 64) * G * tpt * 128));
-        __syncwarp();
-        if (lane < nq * (D / 64)) {
-            const int q = lane / (D / 64), c = lane % (D / 64);
-            tma_load_3d(sbase + C::kQ + q * C::kQBytes + c * C::kChunkBytes, &args.tm_q, c * 64, it.kvh * G,
-                        it.q0 + q * tpt, bar(kQFull));
-        }
-        // page ids: 32 at a time, one batch ahead
-        auto load_ids = [&](int i0) -> int {  // of the tiles i0 .. i0 + 3
-            const int k = i0 * kPages + lane;
-            return k < npages ? __ldg(bt + k) : 0;
-        };
-        int ids_k = load_ids(0), next_k = load_ids(4), at_k = 0;  // K and V walk the table apart
-        int ids_v = ids_k, next_v = next_k, at_v = 0;
-        const int total = 2 * ntiles * C::kPanels;
-        int issued = 0;
-        for (int e = 0; e < total; ++e) {
-            bool v;
-            const int i = entry_tile(e / C::kPanels, two, ntiles, v);
-            const int pp = e % C::kPanels;
-            int &ids = v ? ids_v : ids_k, &next = v ? next_v : next_k, &at = v ? at_v : at_k;
-            if (i / 4 != at) {
-                at = i / 4;
-                ids = next;
-                next = load_ids(4 * at + 4);
-            }
-            const int npg = min(kPages, npages - i * kPages);
-            int page = __shfl_sync(0xffffffffu, ids, (i % 4) * kPages + lane % kPages);
-            const bool bad = p.num_pages > 0 && (page < 0 || page >= p.num_pages) && lane < npg;
-            const uint32_t bads = __ballot_sync(0xffffffffu, bad);
-            if (bad) page = 0;
-            const int slot = C::kQuant ? e % (C::kRawStages ? C::kRawStages : 1) : e % C::kStages;
-            const int use = C::kQuant ? e / (C::kRawStages ? C::kRawStages : 1) : e / C::kStages;
-            if (use > 0) {
-                ok = mbar_wait(bar((C::kQuant ? kRawEmpty : kEmpty) + slot), (use & 1) ^ 1, kWaitNs);
-                ok = __shfl_sync(0xffffffffu, (int)ok, 0);
-                if (!ok) break;
-            }
-            page = __shfl_sync(0xffffffffu, page, lane % kPages);
-            const CUtensorMap *map = v ? &args.tm_v : &args.tm_k;
-            const uint32_t full = bar((C::kQuant ? kRawFull : kFull) + slot);
-            if (lane == 0) {
-                if (!v && pp == 0) {
-                    sts_u32(sbase + C::kBad + 4u * (i % kBadRing), bads);
-                    if (bads) atomicOr(p.flags, kFlagBadPage);
+    if (warp >= C::kProducerWarp) {
+        if constexpr (C::kQuant) regs_down<C::kOtherRegs>();
+        if (warp < C::kMmaWarp) {
+            // ------------------------------------------------------------ producers
+            const int pw = warp - C::kProducerWarp;
+            // q: one box of 64 elements x G heads x tpt tokens per tile of rows and chunk; tokens past q's end read 0
+            if (pw == 0) {
+                if (lane == 0) mbar_arrive_expect_tx(bar(kQFull), (uint32_t)(nq * (D / 64) * G * tpt * 128));
+                __syncwarp();
+                if (lane < nq * (D / 64)) {
+                    const int q = lane / (D / 64), c = lane % (D / 64);
+                    tma_load_3d(sbase + C::kQ + q * C::kQBytes + c * C::kQChunk, &args.tm_q, c * 64, it.kvh * G,
+                                it.q0 + q * tpt, bar(kQFull));
                 }
-                mbar_arrive_expect_tx(full, (uint32_t)npg * (C::kQuant ? VA_PAGE_SIZE * C::kRawRow
-                                                                       : VA_PAGE_SIZE * 128 * C::kChunks));
+                __syncwarp();
             }
-            __syncwarp();
-            if constexpr (C::kQuant) {
-                if (lane < npg)
-                    tma_load_4d(sbase + C::kRaw + slot * C::kRawBytes + lane * VA_PAGE_SIZE * C::kRawRow, map,
-                                pp * C::kRawRow, it.kvh, 0, page, full);
-            } else {
-                const int pg = lane % kPages, c = lane / kPages;
-                if (pg < npg && c < C::kChunks)
-                    tma_load_4d(sbase + C::kConv + slot * C::kPanelBytes + c * C::kChunkBytes + pg * VA_PAGE_SIZE * 128, map,
-                                pp * C::kPanelD + c * 64, it.kvh, 0, page, full);
-            }
-            __syncwarp();
-            issued = e + 1;
-        }
-        // every issued copy lands before the CTA ends
-        if (lane == 0) {
-            const int n = C::kQuant ? C::kRawStages : C::kStages;
-            for (int e = max(0, issued - n); e < issued; ++e)
-                if (!mbar_wait(bar((C::kQuant ? kRawFull : kFull) + e % n), (e / n) & 1, kWaitNs)) ok = false;
-            if (!mbar_wait(bar(kQFull), 0, kWaitNs)) ok = false;
-        }
-    } else if (warp == C::kMmaWarp) {
-        // ------------------------------------------------------------ MMA issue
-        if (lane == 0) {
-            constexpr int kAB = C::kQuant ? 0 : 1;
-            constexpr uint32_t idS = idesc_f16(128, kKeys, kAB, 0, 0);
-            constexpr uint32_t idO = idesc_f16(128, C::kPanelD, kAB, 0, 1);
-            // K-major operands: 8-row groups 1024 bytes apart; V is MN-major, its 64-element chunks kChunkBytes apart
-            const uint64_t qdesc = smem_desc(sbase + C::kQ, 16, 1024, 2);
-            const uint64_t kdesc = smem_desc(sbase + C::kConv, 16, 1024, 2);
-            const uint64_t vdesc = smem_desc(sbase + C::kConv, C::kChunkBytes, 1024, 2);
-            const int steps = nq * ntiles;
-            auto scores = [&](int k) -> bool {
-                const int q = two ? k & 1 : 0, i = two ? k >> 1 : k;
-                for (int pp = 0; pp < C::kPanels; ++pp) {
-                    const int e = k_entry(i, two) * C::kPanels + pp, slot = e % C::kStages;
-                    if (!mbar_wait(bar(kFull + slot), (e / C::kStages) & 1, kWaitNs)) return false;
-                    tc_fence_after();
-                    const uint64_t kd = kdesc + (uint64_t)(slot * (C::kPanelBytes >> 4));
-                    const uint64_t qd = qdesc + (uint64_t)((q * C::kQBytes + pp * C::kPanelBytes) >> 4);
-#pragma unroll
-                    for (int kk = 0; kk < C::kPanelD / 16; ++kk) {
-                        const uint64_t off = (uint64_t)((kk / 4) * (C::kChunkBytes >> 4) + (kk % 4) * 2);
-                        mma_ss(tmem + (k & 1) * kKeys, qd + off, kd + off, idS, pp > 0 || kk > 0);
+            // page ids: 32 at a time, one batch ahead
+            constexpr int kIdTiles = 32 / kPages;
+            auto load_ids = [&](int i0) -> int {  // of the tiles i0 .. i0 + kIdTiles - 1
+                const int k = i0 * kPages + lane;
+                return k < npages ? __ldg(bt + k) : 0;
+            };
+            int ids_k = load_ids(0), next_k = load_ids(kIdTiles), at_k = 0;  // K and V walk the table apart
+            int ids_v = ids_k, next_v = next_k, at_v = 0;
+            constexpr int kRing = C::kQuant ? C::kRawStages : C::kStages;
+            constexpr int kFullBar = C::kQuant ? kRawFull : kFull, kEmptyBar = C::kQuant ? kRawEmpty : kEmpty;
+            const int total = 2 * ntiles * C::kPanels;
+            int end = total;
+            for (int e = pw; e < total; e += kProducers) {
+                bool v;
+                const int i = entry_tile(e / C::kPanels, ntiles, v);
+                const int pp = e % C::kPanels;
+                int &ids = v ? ids_v : ids_k, &next = v ? next_v : next_k, &at = v ? at_v : at_k;
+                if (i / kIdTiles != at) {
+                    at = i / kIdTiles;
+                    ids = next;
+                    next = load_ids(kIdTiles * (at + 1));
+                }
+                const int npg = min(kPages, npages - i * kPages);
+                int page = __shfl_sync(0xffffffffu, ids, (i % kIdTiles) * kPages + lane % kPages);
+                const bool bad = p.num_pages > 0 && (page < 0 || page >= p.num_pages) && lane < npg;
+                const uint32_t bads = __ballot_sync(0xffffffffu, bad);
+                if (bad) page = 0;
+                const int slot = e % kRing, use = e / kRing;
+                if (use > 0) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(bar(kEmptyBar + slot), (use & 1) ^ 1, kWaitNs));
+                    if (!ok) {
+                        end = e;
+                        break;
                     }
-                    if (!two || q == 1) mma_commit(bar(kEmpty + slot));
                 }
-                mma_commit(bar(kSFull + (k & 1)));
-                return true;
-            };
-            auto product = [&](int k) -> bool {
-                const int q = two ? k & 1 : 0, i = two ? k >> 1 : k;
-                if (!mbar_wait(bar(kPFull + (k & 1)), (k >> 1) & 1, kWaitNs)) return false;
-                for (int pp = 0; pp < C::kPanels; ++pp) {
-                    const int e = v_entry(i, two, ntiles) * C::kPanels + pp, slot = e % C::kStages;
-                    if (!mbar_wait(bar(kFull + slot), (e / C::kStages) & 1, kWaitNs)) return false;
-                    tc_fence_after();
-                    const uint64_t vd = vdesc + (uint64_t)(slot * (C::kPanelBytes >> 4));
+                const CUtensorMap *map = v ? &args.tm_v : &args.tm_k;
+                const uint32_t full = bar(kFullBar + slot);
+                if (lane == 0) {
+                    if (!v && pp == 0) {
+                        sts_u32(sbase + C::kBad + 4u * (i % kBadRing), bads);
+                        if (bads) atomicOr(p.flags, kFlagBadPage);
+                    }
+                    mbar_arrive_expect_tx(full, (uint32_t)npg * (C::kQuant ? VA_PAGE_SIZE * C::kRawRow
+                                                                           : VA_PAGE_SIZE * 128 * C::kChunks));
+                }
+                __syncwarp();
 #pragma unroll
-                    for (int kk = 0; kk < kKeys / 16; ++kk)
-                        mma_ts(tmem + C::kOCol + q * D + pp * C::kPanelD, tmem + (k & 1) * kKeys + kk * 8,
-                               vd + (uint64_t)(kk * (16 * 128 >> 4)), idO, i > 0 || kk > 0);
-                    if (!two || q == 1) mma_commit(bar(kEmpty + slot));
+                for (int pg = 0; pg < kPages; ++pg) {
+                    if (pg >= npg) break;
+                    const int at_page = __shfl_sync(0xffffffffu, page, pg);
+                    if constexpr (C::kQuant) {
+                        tma_load_4d_warp(sbase + C::kRaw + slot * C::kRawBytes + pg * VA_PAGE_SIZE * C::kRawRow, map,
+                                         pp * C::kRawRow, it.kvh, 0, at_page, full);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < C::kChunks; ++c)
+                            tma_load_4d_warp(sbase + C::kConv + slot * C::kPanelBytes + c * C::kChunkBytes +
+                                                 pg * VA_PAGE_SIZE * 128,
+                                             map, pp * C::kPanelD + c * 64, it.kvh, 0, at_page, full);
+                    }
                 }
-                mma_commit(bar(kODone + (k & 1)));
-                return true;
-            };
-            ok = mbar_wait(bar(kQReady), 0, kWaitNs);
-            tc_fence_after();
-            ok = ok && scores(0) && (steps < 2 || scores(1));
-            for (int k = 0; k < steps && ok; ++k) ok = product(k) && (k + 2 >= steps || scores(k + 2));
-            mma_commit(bar(kOFinal));
-            if (!mbar_wait(bar(kOFinal), 0, kWaitNs)) ok = false;
+            }
+            // every issued copy lands before the CTA ends
+            for (int e = max(0, end - kRing); e < end; ++e)
+                if (e % kProducers == pw && !mbar_wait(bar(kFullBar + e % kRing), (e / kRing) & 1, kWaitNs)) ok = false;
+            if (pw == 0 && !mbar_wait(bar(kQFull), 0, kWaitNs)) ok = false;
+        } else {
+            // ------------------------------------------------------------ MMA issue, by a whole warp
+            const int w = warp - C::kMmaWarp;  // of two tiles of rows, the one that this warp issues
+            if (w < nq) {
+                constexpr int kAB = C::kQuant ? 0 : 1;
+                constexpr uint32_t idS = idesc_f16(128, kKeys, kAB, 0, 0);
+                constexpr uint32_t idO = idesc_f16(128, C::kPanelD, kAB, 0, 1);
+                // K-major operands: 8-row groups 1024 bytes apart; V is MN-major, its 64-element chunks kChunkBytes apart
+                const uint64_t qdesc = smem_desc(sbase + C::kQ + w * C::kQBytes, 16, 1024, 2);
+                const uint64_t kdesc = smem_desc(sbase + C::kConv, 16, 1024, 2);
+                const uint64_t vdesc = smem_desc(sbase + C::kConv, C::kChunkBytes, 1024, 2);
+                auto wait = [&](int b, int parity) -> bool {
+                    return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, kWaitNs));
+                };
+                int stage = 0, phase = 0;  // of the next panel
+                auto pass = [&] {
+                    mma_commit_warp(bar(kEmpty + stage));
+                    if (++stage == C::kStages) stage = 0, phase ^= 1;
+                };
+                auto scores = [&](int slot) -> bool {  // of the next tile of keys, whose first panel is here
+#pragma unroll
+                    for (int pp = 0; pp < C::kPanels; ++pp) {
+                        if (pp > 0 && !wait(kFull + stage, phase)) return false;
+                        const uint64_t kd = kdesc + (uint64_t)(stage * (C::kPanelBytes >> 4));
+                        const uint64_t qd = qdesc + (uint64_t)(pp * (C::kPanelD / 64 * C::kQChunk) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < C::kPanelD / 16; ++kk)
+                            mma_ss_warp(tmem + slot * kKeys, qd + (uint64_t)((kk / 4) * (C::kQChunk >> 4) + (kk % 4) * 2),
+                                        kd + (uint64_t)((kk / 4) * (C::kChunkBytes >> 4) + (kk % 4) * 2), idS, pp > 0 || kk > 0);
+                        if (pp + 1 < C::kPanels) pass();
+                    }
+                    mma_commit_warp(bar(kSFull + slot));
+                    pass();
+                    return true;
+                };
+                auto product = [&](int slot, bool first) -> bool {
+                    const uint32_t from = tmem + (C::kOver ? slot * kKeys : C::kPCol + slot * (kKeys / 2));
+#pragma unroll
+                    for (int pp = 0; pp < C::kPanels; ++pp) {
+                        if (pp > 0 && !wait(kFull + stage, phase)) return false;
+                        const uint64_t vd = vdesc + (uint64_t)(stage * (C::kPanelBytes >> 4));
+#pragma unroll
+                        for (int kk = 0; kk < kKeys / 16; ++kk)
+                            mma_ts_warp(tmem + C::kOCol + w * D + pp * C::kPanelD, from + kk * 8,
+                                        vd + (uint64_t)(kk * (16 * 128 >> 4)), idO, !first || kk > 0);
+                        if (pp + 1 < C::kPanels) pass();
+                    }
+                    mma_commit_warp(bar(kODone + slot));
+                    pass();
+                    return true;
+                };
+                ok = wait(kQReady, 0) && wait(kFull + stage, phase);
+                tc_fence_after();
+                if (two) {
+                    ok = ok && scores(w);
+                    for (int i = 0; i < ntiles && ok; ++i) {
+                        if (i + 1 < ntiles) {
+                            ok = wait(kFull + stage, phase) && wait(kSRead + w, i & 1);
+                            tc_fence_after();
+                            ok = ok && scores(w);
+                        }
+                        ok = ok && wait(kFull + stage, phase) && wait(kPFull + w, i & 1);
+                        tc_fence_after();
+                        ok = ok && product(w, i == 0);
+                    }
+                } else {
+                    ok = ok && scores(0) && (ntiles < 2 || (wait(kFull + stage, phase) && scores(1)));
+                    for (int k = 0; k < ntiles && ok; ++k) {
+                        ok = wait(kFull + stage, phase) && wait(kPFull + (k & 1), (k >> 1) & 1);
+                        tc_fence_after();
+                        ok = ok && product(k & 1, k == 0);
+                        if (ok && k + 2 < ntiles) ok = wait(kFull + stage, phase) && scores(k & 1);
+                    }
+                }
+                mma_commit_warp(bar(kOFinal));
+                if (!wait(kOFinal, 0)) ok = false;
+            }
         }
     } else if (warp < C::kSoftmaxWarps) {
         // ------------------------------------------------------------ softmax
+        if constexpr (C::kQuant) regs_up<C::kSoftmaxRegs>();
         const int w = warp >> 2;  // tile of rows
         const int r = (warp & 3) * 32 + lane;
         const int nt = max(0, min(tpt, it.nt - w * tpt));
@@ -325,13 +373,14 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
             const int head = it.kvh * G + r % G;
             const int vis = it.vis0 + token;
             const uint32_t lane_tm = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+            const uint32_t stat = sbase + C::kStat + w * (C::kStats * kMmaRows * 4);
             // q as the MMA takes it: rows without a token are zero; for a cache of codes, fp16 scaled by a power of
             // two that brings the row's largest element into [2^14, 2^15)
-            float prescale = 1.f;
             ok = __all_sync(0xffffffffu, mbar_wait(bar(kQFull), 0, kWaitNs));
             {
+                float prescale = 1.f;
                 const uint32_t row = sbase + C::kQ + w * C::kQBytes;
-                auto unit = [&](int u) { return row + (u / 8) * C::kChunkBytes + sw128(r, u % 8); };
+                auto unit = [&](int u) { return row + (u / 8) * C::kQChunk + sw128(r, u % 8); };
                 if (!row_ok) {
 #pragma unroll 4
                     for (int u = 0; u < D / 8; ++u) sts_u4(unit(u), make_uint4(0, 0, 0, 0));
@@ -363,18 +412,29 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                         sts_u4(unit(u), make_uint4(h[0], h[1], h[2], h[3]));
                     }
                 }
+                sts_f32(stat + 4u * r, p.sm_scale_log2 / prescale);
+                sts_u32(stat + 4u * (kMmaRows + r), (uint32_t)(row_ok ? vis : -1));
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kQReady));
             }
-            const float c_r = p.sm_scale_log2 / prescale;
-            const uint64_t c2 = f2_pack(__float_as_uint(c_r), __float_as_uint(c_r));
-            float m_run = -INFINITY, l_run = 0.f;
-            int beta = 0, swept = 0;
+            // this thread's rows of the warp's 32: 16 h + lane / 4 + 8 j, as row 2 h + j; its columns of each 8: c, c + 1
+            const int c = 2 * (lane & 3);
+            auto my_row = [&](int x) { return (warp & 3) * 32 + 16 * (x >> 1) + 8 * (x & 1) + (lane >> 2); };
+            float c_r[4], m_run[4], l_run[4];
+            int beta[4], seen[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {  // written by this warp
+                c_r[x] = lds_f32(stat + 4u * my_row(x));
+                seen[x] = (int)lds_u32(stat + 4u * (kMmaRows + my_row(x)));
+                m_run[x] = -INFINITY, l_run[x] = 0.f, beta[x] = 0;
+            }
+            constexpr int kU = kKeys / 8;
             const int first_vis = it.vis0 + w * tpt;  // of the tile's first token
+            int swept = 0;
             for (int i = 0; i < ntiles && ok; ++i) {
-                const int k = two ? 2 * i + w : i, sl = k & 1;
-                ok = __all_sync(0xffffffffu, ok && mbar_wait(bar(kSFull + sl), (k >> 1) & 1, kWaitNs));
+                const int sl = two ? w : i & 1, ph = two ? i : i >> 1;
+                ok = __all_sync(0xffffffffu, ok && mbar_wait(bar(kSFull + sl), ph & 1, kWaitNs));
                 if (!ok) break;
                 tc_fence_after();
                 const int key0 = it.k_begin + i * kKeys;
@@ -382,144 +442,196 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                 // an edge tile hides some key from some row of the item; both tiles of rows take the same view of it
                 const bool edge = key0 + kKeys > it.k_end || key0 + kKeys - 1 > it.vis0 || bads != 0;
                 const bool cut = edge && (key0 + kKeys > it.k_end || key0 + kKeys - 1 > first_vis || bads != 0);
-                const int last = row_ok ? min(vis, it.k_end - 1) - key0 : -1;  // last key of the tile that the row sees
                 const uint32_t s_tm = lane_tm + sl * kKeys;
-                const uint32_t ring = sbase + C::kScale + (i % kScaleRing) * kScaleFloats * 4;
-                auto visible = [&](int j) { return j <= last && !((bads >> (j / VA_PAGE_SIZE)) & 1u); };
-                // raw scores times k scale, hidden keys at -inf; mx: four chains of maxima
-                auto take = [&](int c, uint32_t (&s)[32], float (&mx)[4]) {
-                    if constexpr (C::kQuant) {
+                const uint32_t ring = sbase + C::kScale + (i % kScaleRing) * C::kScaleFloats * 4;
+                uint32_t s[2][4 * kU];
 #pragma unroll
-                        for (int j4 = 0; j4 < 8; ++j4) {
-                            const uint4 sc = lds_u4(ring + 128u * c + 16 * j4);
-                            f2_unpack(f2_mul(f2_pack(s[4 * j4], s[4 * j4 + 1]), f2_pack(sc.x, sc.y)), s[4 * j4],
-                                      s[4 * j4 + 1]);
-                            f2_unpack(f2_mul(f2_pack(s[4 * j4 + 2], s[4 * j4 + 3]), f2_pack(sc.z, sc.w)), s[4 * j4 + 2],
-                                      s[4 * j4 + 3]);
-                        }
-                    }
-                    if (cut) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (!visible(32 * c + j)) s[j] = 0xFF800000u;
-                    }
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2)
-                        mx[(j / 2) & 3] = fmax3(mx[(j / 2) & 3], __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
-                };
-                uint32_t s[C::kKeep ? 4 : 1][32];
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                if constexpr (C::kKeep) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + 32 * c, s[c]);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) take(c, s[c], mx);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        tmem_ld32(s_tm + 32 * c, s[0]);
-                        tmem_wait_ld();
-                        take(c, s[0], mx);
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t at = s_tm + ((uint32_t)(16 * h) << 16);
+                    if constexpr (kU == 16) {
+                        tmem_ld_16x256b(at, s[h]);
+                    } else {
+                        tmem_ld_16x256b(at, reinterpret_cast<uint32_t(&)[32]>(s[h][0]));
+                        tmem_ld_16x256b(at + 64, reinterpret_cast<uint32_t(&)[8]>(s[h][32]));
                     }
                 }
-                const float m_tile = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * c_r;
-                const bool grow = m_tile > m_run + kRescaleLog2;
-                float alpha = 1.f;
-                if (grow) {
-                    if (m_run != -INFINITY) alpha = ex2_approx(m_run - m_tile);
-                    m_run = m_tile;
-                    l_run *= alpha;
+                tmem_wait_ld();
+                if constexpr (!C::kOver) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kSRead + sl));
                 }
-                int dbeta = 0;
+                // raw scores times k scale, hidden keys at -inf, and the rows' maxima
                 if constexpr (C::kQuant) {
-                    float mv;
-                    if (!cut) {
-                        const float4 x = lds_f4(ring + 8u * kKeys);
-                        mv = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w));
-                    } else {  // of the keys that the row sees
-                        mv = 0.f;
-#pragma unroll 8
-                        for (int j = 0; j < kKeys; ++j)
-                            if (visible(j)) mv = fmaxf(mv, lds_f32(ring + 4u * (kKeys + j)));
-                    }
-                    if (mv > 0.f) {
-                        const float rr = mv * __uint_as_float((uint32_t)(127 + beta) << 23);
-                        if (!(rr >= 0x1p-6f && rr < 4.f)) {
-                            // mv in [2^(E-127), 2^(E-126)); beta at most 118, so that p 2^beta stays finite
-                            const int E = max(9, min(253, (int)((__float_as_uint(mv) >> 23) & 0xFFu)));
-                            dbeta = (127 - E) - beta;
-                            beta = 127 - E;
+#pragma unroll
+                    for (int u = 0; u < kU; ++u) {
+                        const uint2 sc = lds_u2(ring + 4u * (8 * u + c));
+                        const uint64_t ks = f2_pack(sc.x, sc.y);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            uint32_t *y = &s[x >> 1][4 * u + 2 * (x & 1)];
+                            f2_unpack(f2_mul(f2_pack(y[0], y[1]), ks), y[0], y[1]);
                         }
                     }
                 }
-                const float fo =
-                    dbeta == 0 ? alpha : alpha * __uint_as_float((uint32_t)(127 + max(-126, min(127, dbeta))) << 23);
-                if (i > 0 && __any_sync(0xffffffffu, fo != 1.f)) {
-                    // O holds the tiles before: their last product has to have landed
-                    const int kp = two ? k - 2 : k - 1;
-                    if (!__all_sync(0xffffffffu, mbar_wait(bar(kODone + (kp & 1)), (kp >> 1) & 1, kWaitNs))) ok = false;
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int c0 = 0; c0 < D; c0 += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(lane_tm + C::kOCol + w * D + c0, o);
-                        tmem_wait_ld();
+                float mx[4], mv[4];
+                if (cut) {  // rows' own maxima of the value scales too: of the keys that they see
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fo);
-                        tmem_st32(lane_tm + C::kOCol + w * D + c0, o);
-                    }
-                    tmem_wait_st();
-                }
-                const float neg_m = (m_run == -INFINITY ? 0.f : -m_run) + (float)beta;
-                const uint64_t nm2 = f2_pack(__float_as_uint(neg_m), __float_as_uint(neg_m));
-                uint64_t ls[2] = {0ull, 0ull};
-                auto give = [&](int c, uint32_t (&x)[32]) {  // probabilities of 32 keys, over the slot's columns
-                    uint32_t pk[16];
+                    for (int x = 0; x < 4; ++x) {
+                        const int last = min(seen[x], it.k_end - 1) - key0;
+                        mv[x] = 0.f;
 #pragma unroll
-                    for (int j4 = 0; j4 < 8; ++j4) {
-                        uint32_t a[4];
-                        f2_unpack(f2_fma(f2_pack(x[4 * j4], x[4 * j4 + 1]), c2, nm2), a[0], a[1]);
-                        f2_unpack(f2_fma(f2_pack(x[4 * j4 + 2], x[4 * j4 + 3]), c2, nm2), a[2], a[3]);
+                        for (int u = 0; u < kU; ++u) {
+                            const bool bad = (bads >> (u / 2)) & 1u;  // a page is two units
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) a[e] = __float_as_uint(ex2_approx(__uint_as_float(a[e])));
-                        const uint64_t p01 = f2_pack(a[0], a[1]), p23 = f2_pack(a[2], a[3]);
-                        ls[0] = f2_add(ls[0], p01);
-                        ls[1] = f2_add(ls[1], p23);
-                        if constexpr (C::kQuant) {
-                            const uint4 sc = lds_u4(ring + 4u * kKeys + 128u * c + 16 * j4);
-                            f2_unpack(f2_mul(p01, f2_pack(sc.x, sc.y)), a[0], a[1]);
-                            f2_unpack(f2_mul(p23, f2_pack(sc.z, sc.w)), a[2], a[3]);
-                            if (cut) {  // a hidden key's scale may be anything
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    if (!visible(32 * c + 4 * j4 + e)) a[e] = 0u;
+                            for (int e = 0; e < 2; ++e) {
+                                uint32_t &y = s[x >> 1][4 * u + 2 * (x & 1) + e];
+                                if (bad || 8 * u + c + e > last)
+                                    y = 0xFF800000u;
+                                else if (C::kQuant)
+                                    mv[x] = fmaxf(mv[x], fabsf(lds_f32(ring + 4u * (kKeys + 8 * u + c + e))));
                             }
-                            pk[2 * j4] = pack_half2(__uint_as_float(a[0]), __uint_as_float(a[1]));
-                            pk[2 * j4 + 1] = pack_half2(__uint_as_float(a[2]), __uint_as_float(a[3]));
-                        } else {
-                            pk[2 * j4] = pack_bf162(__uint_as_float(a[0]), __uint_as_float(a[1]));
-                            pk[2 * j4 + 1] = pack_bf162(__uint_as_float(a[2]), __uint_as_float(a[3]));
                         }
+#pragma unroll
+                        for (int o = 1; o <= 2; o <<= 1) mv[x] = fmaxf(mv[x], __shfl_xor_sync(0xffffffffu, mv[x], o));
                     }
-                    tmem_st16(s_tm + 16 * c, pk);
-                };
-                if constexpr (C::kKeep) {
+                } else if constexpr (C::kQuant) {
+                    const float4 y = lds_f4(ring + 8u * kKeys);
+                    mv[0] = mv[1] = mv[2] = mv[3] = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w));
+                }
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) give(c, s[c]);
-                } else {
+                for (int x = 0; x < 4; ++x) mx[x] = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float none[4] = {0.f, 0.f, 0.f, 0.f};
-                        tmem_ld32(s_tm + 32 * c, s[0]);
-                        tmem_wait_ld();
-                        take(c, s[0], none);
-                        give(c, s[0]);
+                for (int u = 0; u < kU; ++u) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const uint32_t *y = &s[x >> 1][4 * u + 2 * (x & 1)];
+                        mx[x] = fmax3(mx[x], __uint_as_float(y[0]), __uint_as_float(y[1]));
                     }
                 }
-                uint32_t l0, l1;
-                f2_unpack(f2_add(ls[0], ls[1]), l0, l1);
-                l_run += (__uint_as_float(l0) + __uint_as_float(l1)) * __uint_as_float((uint32_t)(127 - beta) << 23);
+#pragma unroll
+                for (int o = 1; o <= 2; o <<= 1) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], o));
+                }
+                // does a row's maximum, or its value scales' power of two, have to move?
+                bool move = false;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    mx[x] *= c_r[x];
+                    move |= mx[x] > m_run[x] + kRescaleLog2;
+                    if constexpr (C::kQuant) {
+                        const float rr = mv[x] * __uint_as_float((uint32_t)(127 + beta[x]) << 23);
+                        move |= !(rr >= 0x1p-6f && rr < 4.f);
+                    }
+                }
+                // the product before this one: P's slot is free and O holds it
+                if (!C::kOver && (two ? i > 0 : i > 1)) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(bar(kODone + sl), (ph - 1) & 1, kWaitNs))) ok = false;
+                    tc_fence_after();
+                }
+                if (__any_sync(0xffffffffu, move)) {
+                    float fo[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        fo[x] = 1.f;
+                        if (mx[x] > m_run[x] + kRescaleLog2) {
+                            if (m_run[x] != -INFINITY) fo[x] = ex2_approx(m_run[x] - mx[x]);
+                            m_run[x] = mx[x];
+                            l_run[x] *= fo[x];
+                        }
+                        if (C::kQuant && mv[x] > 0.f && mv[x] < INFINITY) {
+                            const float rr = mv[x] * __uint_as_float((uint32_t)(127 + beta[x]) << 23);
+                            if (!(rr >= 0x1p-6f && rr < 4.f)) {
+                                // mv in [2^(E-127), 2^(E-126)); beta at most 118 and at least -73, so that p 2^beta
+                                // stays finite, and the sums, which take it, lose nothing above 2^-53
+                                const int E = max(9, min(200, (int)((__float_as_uint(mv[x]) >> 23) & 0xFFu)));
+                                fo[x] *= __uint_as_float((uint32_t)(127 + max(-126, min(127, 127 - E - beta[x]))) << 23);
+                                beta[x] = 127 - E;
+                            }
+                        }
+                    }
+                    if (i > 0 && __any_sync(0xffffffffu, fo[0] != 1.f || fo[1] != 1.f || fo[2] != 1.f || fo[3] != 1.f)) {
+                        // (of one tile, the product before this one is the one of the other slot)
+                        if (!two &&
+                            !__all_sync(0xffffffffu, mbar_wait(bar(kODone + ((i - 1) & 1)), ((i - 1) >> 1) & 1, kWaitNs)))
+                            ok = false;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c0 = 0; c0 < D; c0 += 32) {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const uint32_t at = lane_tm + ((uint32_t)(16 * h) << 16) + C::kOCol + w * D + c0;
+                                uint32_t o[16];
+                                tmem_ld_16x256b(at, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    o[j] = __float_as_uint(__uint_as_float(o[j]) * fo[2 * h + ((j >> 1) & 1)]);
+                                tmem_st_16x256b(at, o);
+                            }
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                const uint32_t p_tm = lane_tm + (C::kOver ? sl * kKeys : C::kPCol + sl * (kKeys / 2));
+                auto give = [&](auto cut_tile) {  // probabilities, over the slot's columns or beside them
+                    constexpr bool kCut = decltype(cut_tile)::value;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t pk[4];  // of two units
+                        uint64_t ls[2] = {0ull, 0ull}, c2[2], nm2[2];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int x = 2 * h + j;
+                            const float nm = (m_run[x] == -INFINITY ? 0.f : -m_run[x]) + (float)beta[x];
+                            c2[j] = f2_pack(__float_as_uint(c_r[x]), __float_as_uint(c_r[x]));
+                            nm2[j] = f2_pack(__float_as_uint(nm), __float_as_uint(nm));
+                        }
+#pragma unroll
+                        for (int u = 0; u < kU; ++u) {
+                            uint64_t vs = 0ull;
+                            if constexpr (C::kQuant) {
+                                const uint2 sc = lds_u2(ring + 4u * (kKeys + 8 * u + c));
+                                vs = f2_pack(sc.x, sc.y);
+                            }
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const uint32_t s0 = s[h][4 * u + 2 * j], s1 = s[h][4 * u + 2 * j + 1];
+                                uint32_t a, b;
+                                f2_unpack(f2_fma(f2_pack(s0, s1), c2[j], nm2[j]), a, b);
+                                a = __float_as_uint(ex2_approx(__uint_as_float(a)));
+                                b = __float_as_uint(ex2_approx(__uint_as_float(b)));
+                                const uint64_t pr = f2_pack(a, b);
+                                ls[j] = f2_add(ls[j], pr);
+                                if constexpr (C::kQuant) {
+                                    f2_unpack(f2_mul(pr, vs), a, b);
+                                    if (kCut) {  // a hidden key's scale may be anything
+                                        const int last = min(seen[2 * h + j], it.k_end - 1) - key0;
+                                        const bool bad = (bads >> (u / 2)) & 1u;
+                                        if (bad || 8 * u + c > last) a = 0u;
+                                        if (bad || 8 * u + c + 1 > last) b = 0u;
+                                    }
+                                    pk[2 * (u & 1) + j] = pack_half2(__uint_as_float(a), __uint_as_float(b));
+                                } else {
+                                    pk[2 * (u & 1) + j] = pack_bf162(__uint_as_float(a), __uint_as_float(b));
+                                }
+                            }
+                            if (u & 1) tmem_st_16x128b(p_tm + ((uint32_t)(16 * h) << 16) + 4 * (u - 1), pk);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            uint32_t a, b;
+                            f2_unpack(ls[j], a, b);
+                            l_run[2 * h + j] += (__uint_as_float(a) + __uint_as_float(b)) *
+                                                __uint_as_float((uint32_t)(127 - beta[2 * h + j]) << 23);
+                        }
+                    }
+                };
+                if (C::kQuant && cut)
+                    give(std::true_type{});
+                else
+                    give(std::false_type{});
                 if constexpr (C::kQuant) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(kScaleFree + i % kScaleRing));
@@ -531,7 +643,7 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                     const int valid = min(kKeys, it.k_end - key0);
                     bool found = false;
                     for (int pp = 0; pp < C::kPanels; ++pp) {
-                        const int e = v_entry(i, two, ntiles) * C::kPanels + pp, slot = e % C::kStages;
+                        const int e = v_entry(i, ntiles) * C::kPanels + pp, slot = e % C::kStages;
                         if (!__all_sync(0xffffffffu, mbar_wait(bar(kFull + slot), (e / C::kStages) & 1, kWaitNs))) ok = false;
                         const uint32_t panel = sbase + C::kConv + slot * C::kPanelBytes;
                         for (int u = w * 128 + r; u < kKeys * C::kPanelD / 8; u += nq * 128) {
@@ -565,12 +677,26 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kPFull + sl));
             }
+            // the rows' sums over the four lanes that share them, and all of a row to its own lane
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+#pragma unroll
+                for (int o = 1; o <= 2; o <<= 1) l_run[x] += __shfl_xor_sync(0xffffffffu, l_run[x], o);
+                if ((lane & 3) == 0) {
+                    sts_f32(stat + 4u * my_row(x), m_run[x]);
+                    sts_f32(stat + 4u * (kMmaRows + my_row(x)), l_run[x]);
+                    if (C::kQuant) sts_u32(stat + 4u * (2 * kMmaRows + my_row(x)), (uint32_t)beta[x]);
+                }
+            }
+            __syncwarp();
+            const float m_row = lds_f32(stat + 4u * r), l_row = lds_f32(stat + 4u * (kMmaRows + r));
+            const int beta_row = !C::kQuant ? 0 : (int)lds_u32(stat + 4u * (2 * kMmaRows + r));
             // epilogue
             if (!__all_sync(0xffffffffu, mbar_wait(bar(kOFinal), 0, kWaitNs))) ok = false;
             tc_fence_after();
             const bool poison = lds_u32(bar(kPoison)) != 0;
-            const float inv = l_run == 0.f ? 0.f : (1.f / l_run) * __uint_as_float((uint32_t)(127 - beta) << 23);
-            const float lse = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
+            const float inv = l_row == 0.f ? 0.f : (1.f / l_row) * __uint_as_float((uint32_t)(127 - beta_row) << 23);
+            const float lse = l_row == 0.f ? -INFINITY : (m_row + log2f(l_row)) * 0.69314718055994531f;
             const size_t orow = (size_t)(it.q0 + token) * p.Hq + head;
             if (row_ok && ok) {
                 if (it.part < 0) {
@@ -658,12 +784,14 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
         }
     } else if constexpr (C::kQuant) {
         // ------------------------------------------------------------ dequant
+        regs_down<C::kDequantRegs>();
         // A panel is 16-element pieces; each thread takes kPer of them, kStep rows (a multiple of the swizzle's 8) apart.
         constexpr int kPieces = C::kPanelD / 16;  // of a row
-        constexpr int kPer = kKeys * kPieces / 128;
+        constexpr int kPer = (kKeys * kPieces + 127) / 128;
         constexpr int kStep = 128 / kPieces;
         constexpr int kPieceBytes = C::kBits * 2;
         static_assert(kStep % 8 == 0, "rows apart");
+        constexpr bool kEven = kKeys * kPieces % 128 == 0;  // else some threads have one less
         const int dt = tid - C::kSoftmaxWarps * 32;  // 0 .. 127, also the key whose scales it carries
         const int n0 = dt / kPieces, d0 = (dt % kPieces) * 16;
         const uint32_t lo_at = (d0 / 64) * C::kChunkBytes + sw128(n0, (d0 % 64) / 8);
@@ -671,7 +799,7 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
         const bool odd = (d0 / 64) & 1;  // the other unit first, so that a quarter of a warp hits no bank twice
         auto load_id = [&](int i) -> int {
             const int n = i * kPages + dt / VA_PAGE_SIZE;
-            if (i >= ntiles || n >= npages || it.k_begin + i * kKeys + dt >= it.k_end) return -1;
+            if (dt >= kKeys || i >= ntiles || n >= npages || it.k_begin + i * kKeys + dt >= it.k_end) return -1;
             const int page = __ldg(bt + n);
             return p.num_pages > 0 && page >= p.num_pages ? -1 : page;
         };
@@ -686,14 +814,15 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
         const int total = 2 * ntiles * C::kPanels;
         for (int e = 0; e < total && ok; ++e) {
             bool v;
-            const int i = entry_tile(e / C::kPanels, two, ntiles, v);
+            const int i = entry_tile(e / C::kPanels, ntiles, v);
             const int rs = e % kRawN, slot = e % C::kStages;
             if (!mbar_wait(bar(kRawFull + rs), (e / kRawN) & 1, kWaitNs)) { ok = false; break; }
             const uint32_t src = sbase + C::kRaw + rs * C::kRawBytes + dt * kPieceBytes;
             const uint32_t dst = sbase + C::kConv + slot * C::kPanelBytes;
             RawPiece<DT> raw[kPer];
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) raw[j].load(src + j * 128 * kPieceBytes);
+            for (int j = 0; j < kPer; ++j)
+                if (kEven || n0 + j * kStep < kKeys) raw[j].load(src + j * 128 * kPieceBytes);
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kRawEmpty + rs));
             const int nvalid = it.k_end - (it.k_begin + i * kKeys);
@@ -701,6 +830,7 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                 !mbar_wait(bar(kEmpty + slot), ((e / C::kStages) & 1) ^ 1, kWaitNs)) { ok = false; break; }
 #pragma unroll
             for (int j = 0; j < kPer; ++j) {
+                if (!kEven && n0 + j * kStep >= kKeys) break;
                 uint32_t h[8];
                 raw[j].to_half(h);
                 uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
@@ -717,9 +847,11 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
             if (!v && e % C::kPanels == 0) {
                 if (i >= kScaleRing &&
                     !mbar_wait(bar(kScaleFree + i % kScaleRing), ((i / kScaleRing) & 1) ^ 1, kWaitNs)) { ok = false; break; }
-                const uint32_t ring = sbase + C::kScale + (i % kScaleRing) * kScaleFloats * 4;
-                sts_f32(ring + 4u * dt, ks0);
-                sts_f32(ring + 4u * (kKeys + dt), vs0);
+                const uint32_t ring = sbase + C::kScale + (i % kScaleRing) * C::kScaleFloats * 4;
+                if (dt < kKeys) {
+                    sts_f32(ring + 4u * dt, ks0);
+                    sts_f32(ring + 4u * (kKeys + dt), vs0);
+                }
                 const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(vs0)));
                 if (lane == 0) sts_u32(ring + 4u * (2 * kKeys + dt / 32), top);
                 ks0 = ks1, vs0 = vs1;

@@ -78,7 +78,7 @@ struct Rows {
 
 void plan_geometry(const int32_t *chunk_lens, const int32_t *seq_lens, int B, int Hkv, int G, int D, int num_sms,
                    Geometry &g) {
-    const int tpt = va::kMmaRows / G, most = tpt * va::chunk_tiles(D);
+    const int tpt = va::kMmaRows / G, most = tpt * va::chunk_tiles(D), keys = va::chunk_keys(D);
     std::vector<Rows> rows;
     int at = 0;
     for (int b = 0; b < B; ++b) {
@@ -86,7 +86,7 @@ void plan_geometry(const int32_t *chunk_lens, const int32_t *seq_lens, int B, in
         for (int t = 0; t < n; t += most) {
             const int nt = std::min(most, n - t), vis0 = L - n + t;
             const int k_end = vis0 + nt;  // the last token of the item sees the keys below
-            rows.push_back({b, at + t, nt, vis0, k_end, (k_end + va::kChunkKeys - 1) / va::kChunkKeys});
+            rows.push_back({b, at + t, nt, vis0, k_end, (k_end + keys - 1) / keys});
         }
         at += n;
     }
@@ -130,8 +130,8 @@ void plan_geometry(const int32_t *chunk_lens, const int32_t *seq_lens, int B, in
             const int first = g.num_parts;
             for (int i = 0; i < pieces; ++i) {
                 const int t0 = (int)((long long)r.tiles * i / pieces), t1 = (int)((long long)r.tiles * (i + 1) / pieces);
-                const va::ChunkItem it = {r.b, h, r.q0, r.nt, r.vis0, t0 * va::kChunkKeys,
-                                          std::min(t1 * va::kChunkKeys, r.k_end), pieces > 1 ? first + i * tiles : -1};
+                const va::ChunkItem it = {r.b, h, r.q0, r.nt, r.vis0, t0 * keys,
+                                          std::min(t1 * keys, r.k_end), pieces > 1 ? first + i * tiles : -1};
                 items.push_back({(t1 - t0) * weight(r), it});
             }
             if (pieces > 1) {
@@ -194,7 +194,7 @@ int plan_host(const int32_t *chunk_lens, const int32_t *seq_lens, int B, int Hq,
 
 void fill_info(const va_chunk_plan &p, va_chunk_plan_info *info) {
     *info = {p.num_seqs, p.Hq, p.Hkv, p.D, p.kv_dtype, p.total, p.max_blocks, p.num_items, p.num_groups,
-             p.max_tiles * va::kChunkKeys, p.num_sms, p.workspace_bytes};
+             p.max_tiles * va::chunk_keys(p.D), p.num_sms, p.workspace_bytes};
 }
 
 int fail(cudaError_t e) {

@@ -217,31 +217,33 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) weights_kernel(const __gr
             for (int m = max(0, issued - C::kStages); m < issued; ++m)
                 if (!mbar_wait(bar(kQFull + m % C::kStages), (m / C::kStages) & 1, kWaitNs)) ok = false;
     } else if (warp == kMmaWarp) {
-        // ------------------------------------------------------------ MMA issue
-        if (lane == 0) {
-            constexpr uint32_t id = idesc_f16(128, kRows, 1, 0, 0);
-            const uint64_t kdesc = smem_desc(sbase + C::kK, 16, 1024, 2), qdesc = smem_desc(sbase + C::kQ, 16, 1024, 2);
-            for (int m = 0; m < tiles && ok; ++m) {
-                const int st = m % C::kStages;
-                ok = mbar_wait(bar(kQFull + st), (m / C::kStages) & 1, kWaitNs);
-                for (int kt = 0; kt < C::kKeyTiles && ok; ++kt) {
-                    const int s = kt * 2 + (m & 1);
-                    if (m >= 2) ok = mbar_wait(bar(kSEmpty + s), ((m >> 1) & 1) ^ 1, kWaitNs);
-                    if (!ok) break;
-                    tc_fence_after();
+        // ------------------------------------------------------------ MMA issue, by the whole warp
+        constexpr uint32_t id = idesc_f16(128, kRows, 1, 0, 0);
+        const uint64_t kdesc = smem_desc(sbase + C::kK, 16, 1024, 2), qdesc = smem_desc(sbase + C::kQ, 16, 1024, 2);
+        auto wait = [&](int b, int parity) -> bool {
+            const bool done = __all_sync(0xffffffffu, mbar_wait(bar(b), parity, kWaitNs));
+            tc_fence_after();
+            return done;
+        };
+        for (int m = 0; m < tiles && ok; ++m) {
+            const int st = m % C::kStages;
+            ok = wait(kQFull + st, (m / C::kStages) & 1);
+            for (int kt = 0; kt < C::kKeyTiles && ok; ++kt) {
+                const int s = kt * 2 + (m & 1);
+                if (m >= 2) ok = wait(kSEmpty + s, ((m >> 1) & 1) ^ 1);
+                if (!ok) break;
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint64_t off = (uint64_t)((kk / 4) * (C::kChunkBytes >> 4) + (kk % 4) * 2);
-                        mma_ss(tmem + s * kRows, kdesc + (uint64_t)(kt * (C::kTileBytes >> 4)) + off,
-                               qdesc + (uint64_t)(st * (C::kTileBytes >> 4)) + off, id, kk > 0);
-                    }
-                    mma_commit(bar(kSFull + s));
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint64_t off = (uint64_t)((kk / 4) * (C::kChunkBytes >> 4) + (kk % 4) * 2);
+                    mma_ss_warp(tmem + s * kRows, kdesc + (uint64_t)(kt * (C::kTileBytes >> 4)) + off,
+                                qdesc + (uint64_t)(st * (C::kTileBytes >> 4)) + off, id, kk > 0);
                 }
-                mma_commit(bar(kQEmpty + st));
+                mma_commit_warp(bar(kSFull + s));
             }
-            mma_commit(bar(kDone));
-            if (!mbar_wait(bar(kDone), 0, kWaitNs)) ok = false;
+            mma_commit_warp(bar(kQEmpty + st));
         }
+        mma_commit_warp(bar(kDone));
+        if (!wait(kDone, 0)) ok = false;
     } else {
         // ------------------------------------------------------------ sums
         const int kt = warp >> 2, row = (warp & 3) * 32 + lane;

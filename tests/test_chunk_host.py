@@ -134,7 +134,7 @@ def test_plan_covers_every_token_and_key_once(seed):
     seen = {}
     for b, h, q0, nt, k0, k1 in items.tolist():
         t = q0 - starts[b]
-        assert 0 <= t and t + nt <= new[b] and 1 <= nt <= tpt * (1 if D == 256 else 2) and k0 % 128 == 0 and k0 < k1
+        assert 0 <= t and t + nt <= new[b] and 1 <= nt <= tpt * (1 if D == 256 else 2) and k0 % 16 == 0 and k0 < k1
         seen.setdefault((b, h, t, nt), []).append((k0, k1))
     for b in range(B):
         for h in range(Hkv):
