@@ -14,11 +14,12 @@
 //   producer warps  page ids from the block table, then TMA boxes (16 slots of one page and head) into the ring
 //   dequant warps   (quantised caches) raw panel -> fp16 panel, exact, in the MMA's swizzled layout; keys' scales
 //   MMA warps       as above; panels are used in the order of the ring
-//   softmax warps   four per tile of rows: k scale, mask, running maximum (moved, and O rescaled, only when it grows by
+//   softmax warps   eight per tile of rows: k scale, mask, running maximum (moved, and O rescaled, only when it grows by
 //                   more than 2^8), P * v_scale * 2^beta; at the end O / l and lse
-// A softmax thread holds four rows of a quarter of the columns (the 16x256b layout of the tensor memory), so a key's
-// scales are read from shared memory by 8 lanes for 32 rows at once; with a row per lane every lane reads every scale,
-// and those reads alone were half of the shared memory's bandwidth.
+// A softmax warp has 16 rows, and a thread two of them in a quarter of the columns (the 16x256b layout of the tensor
+// memory), so a key's scales are read from shared memory by 4 lanes for 16 rows; with a row per lane every lane reads
+// every scale, and those reads alone were half of the shared memory's bandwidth.  Four such warps in each quarter of
+// the SM hide each other's waits.
 // A panel is one tile of keys by min(D, 128) elements: what one ring slot holds.
 //
 // P is rounded to the type of the values' tile: bf16 for a bf16 cache, fp16 for codes (with v_scale; 2^beta, a power
@@ -66,19 +67,11 @@ struct Cfg {
     static constexpr int kStages = kQuant ? (D == 64 ? 6 : D == 128 ? 5 : 3) : (D == 256 ? 5 : D == 128 ? 7 : 8);
     static constexpr int kRawStages = kQuant ? (D == 64 ? 6 : D == 128 ? 5 : 3) : 0;
     static constexpr int kScaleFloats = 2 * kKeys + 4;   // k scales, v scales, the largest v scale of each dequant warp
-    static constexpr int kSoftmaxWarps = 4 * kTiles;
+    static constexpr int kSoftmaxWarps = 8 * kTiles;
     static constexpr int kDequantWarps = kQuant ? 4 : 0;
     static constexpr int kProducerWarp = kSoftmaxWarps + kDequantWarps;  // and the ones behind it
     static constexpr int kMmaWarp = kProducerWarp + kProducers;          // one for each tile of rows
     static constexpr int kThreads = (kMmaWarp + kTiles + 3) / 4 * 128;  // whole warpgroups
-    // Registers of a thread, where the block's even share (kLaunchRegs) is too few for a softmax thread's scores: its
-    // warpgroups take what the others, which need few, give back.
-    static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
-    static constexpr int kSoftmaxRegs = kTiles == 2 ? 168 : 240;
-    static constexpr int kDequantRegs = kTiles == 2 ? 104 : 136;
-    static constexpr int kOtherRegs = kTiles == 2 ? 72 : 120;
-    static_assert(!kQuant || (kSoftmaxWarps * kSoftmaxRegs + kDequantWarps * kDequantRegs + 4 * kOtherRegs) * 32 <=
-                                 kThreads * kLaunchRegs, "registers that the block was launched with");
     static constexpr uint32_t kPCol = 2 * kKeys;                  // S slots at 0 and kKeys, P slots behind them
     static constexpr uint32_t kOCol = kOver ? 2 * kKeys : 3 * kKeys;
     static_assert(kOCol + kTiles * D <= 512, "tensor memory");
@@ -180,15 +173,15 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(kSFull + i), 1);
-            mbar_init(bar(kSRead + i), 4);
-            mbar_init(bar(kPFull + i), 4);
+            mbar_init(bar(kSRead + i), 8);
+            mbar_init(bar(kPFull + i), 8);
             mbar_init(bar(kODone + i), 1);
         }
         mbar_init(bar(kOFinal), nq);
         mbar_init(bar(kQFull), 1);
         mbar_init(bar(kQReady), 4 * nq);
-        mbar_init(bar(kSwept), 4 * nq);
-        for (int i = 0; i < kScaleRing; ++i) mbar_init(bar(kScaleFree + i), 4 * nq);
+        mbar_init(bar(kSwept), 8 * nq);
+        for (int i = 0; i < kScaleRing; ++i) mbar_init(bar(kScaleFree + i), 8 * nq);
         sts_u32(bar(kPoison), 0u);
         fence_barrier_init();
     } else if (warp == C::kMmaWarp) {
@@ -202,7 +195,6 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
     bool ok = true;
 
     if (warp >= C::kProducerWarp) {
-        if constexpr (C::kQuant) regs_down<C::kOtherRegs>();
         if (warp < C::kMmaWarp) {
             // ------------------------------------------------------------ producers
             const int pw = warp - C::kProducerWarp;
@@ -363,8 +355,8 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
         }
     } else if (warp < C::kSoftmaxWarps) {
         // ------------------------------------------------------------ softmax
-        if constexpr (C::kQuant) regs_up<C::kSoftmaxRegs>();
-        const int w = warp >> 2;  // tile of rows
+        const int w = warp >> 3;         // tile of rows
+        const int h = (warp >> 2) & 1;   // half of the 32 rows of this quarter; half of the elements at the end
         const int r = (warp & 3) * 32 + lane;
         const int nt = max(0, min(tpt, it.nt - w * tpt));
         const bool row_ok = r < nt * G;
@@ -377,7 +369,7 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
             // q as the MMA takes it: rows without a token are zero; for a cache of codes, fp16 scaled by a power of
             // two that brings the row's largest element into [2^14, 2^15)
             ok = __all_sync(0xffffffffu, mbar_wait(bar(kQFull), 0, kWaitNs));
-            {
+            if (h == 0) {
                 float prescale = 1.f;
                 const uint32_t row = sbase + C::kQ + w * C::kQBytes;
                 auto unit = [&](int u) { return row + (u / 8) * C::kQChunk + sw128(r, u % 8); };
@@ -418,13 +410,15 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kQReady));
             }
-            // this thread's rows of the warp's 32: 16 h + lane / 4 + 8 j, as row 2 h + j; its columns of each 8: c, c + 1
+            named_bar_sync(2 + w, 256);  // the rows' data
+            // this thread's rows of the warp's 16: lane / 4 and 8 further, as row x; its columns of each 8: c, c + 1
             const int c = 2 * (lane & 3);
-            auto my_row = [&](int x) { return (warp & 3) * 32 + 16 * (x >> 1) + 8 * (x & 1) + (lane >> 2); };
-            float c_r[4], m_run[4], l_run[4];
-            int beta[4], seen[4];
+            auto my_row = [&](int x) { return (warp & 3) * 32 + 16 * h + 8 * x + (lane >> 2); };
+            const uint32_t half_tm = lane_tm + ((uint32_t)(16 * h) << 16);
+            float c_r[2], m_run[2], l_run[2];
+            int beta[2], seen[2];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {  // written by this warp
+            for (int x = 0; x < 2; ++x) {
                 c_r[x] = lds_f32(stat + 4u * my_row(x));
                 seen[x] = (int)lds_u32(stat + 4u * (kMmaRows + my_row(x)));
                 m_run[x] = -INFINITY, l_run[x] = 0.f, beta[x] = 0;
@@ -442,18 +436,14 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                 // an edge tile hides some key from some row of the item; both tiles of rows take the same view of it
                 const bool edge = key0 + kKeys > it.k_end || key0 + kKeys - 1 > it.vis0 || bads != 0;
                 const bool cut = edge && (key0 + kKeys > it.k_end || key0 + kKeys - 1 > first_vis || bads != 0);
-                const uint32_t s_tm = lane_tm + sl * kKeys;
+                const uint32_t s_tm = half_tm + sl * kKeys;
                 const uint32_t ring = sbase + C::kScale + (i % kScaleRing) * C::kScaleFloats * 4;
-                uint32_t s[2][4 * kU];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t at = s_tm + ((uint32_t)(16 * h) << 16);
-                    if constexpr (kU == 16) {
-                        tmem_ld_16x256b(at, s[h]);
-                    } else {
-                        tmem_ld_16x256b(at, reinterpret_cast<uint32_t(&)[32]>(s[h][0]));
-                        tmem_ld_16x256b(at + 64, reinterpret_cast<uint32_t(&)[8]>(s[h][32]));
-                    }
+                uint32_t s[4 * kU];  // row x, unit u of 8 columns: s[4 u + 2 x], s[4 u + 2 x + 1]
+                if constexpr (kU == 16) {
+                    tmem_ld_16x256b(s_tm, s);
+                } else {
+                    tmem_ld_16x256b(s_tm, reinterpret_cast<uint32_t(&)[32]>(s[0]));
+                    tmem_ld_16x256b(s_tm + 64, reinterpret_cast<uint32_t(&)[8]>(s[32]));
                 }
                 tmem_wait_ld();
                 if constexpr (!C::kOver) {
@@ -468,16 +458,16 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                         const uint2 sc = lds_u2(ring + 4u * (8 * u + c));
                         const uint64_t ks = f2_pack(sc.x, sc.y);
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            uint32_t *y = &s[x >> 1][4 * u + 2 * (x & 1)];
+                        for (int x = 0; x < 2; ++x) {
+                            uint32_t *y = &s[4 * u + 2 * x];
                             f2_unpack(f2_mul(f2_pack(y[0], y[1]), ks), y[0], y[1]);
                         }
                     }
                 }
-                float mx[4], mv[4];
+                float mx[2], mv[2];
                 if (cut) {  // rows' own maxima of the value scales too: of the keys that they see
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
+                    for (int x = 0; x < 2; ++x) {
                         const int last = min(seen[x], it.k_end - 1) - key0;
                         mv[x] = 0.f;
 #pragma unroll
@@ -485,7 +475,7 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                             const bool bad = (bads >> (u / 2)) & 1u;  // a page is two units
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                uint32_t &y = s[x >> 1][4 * u + 2 * (x & 1) + e];
+                                uint32_t &y = s[4 * u + 2 * x + e];
                                 if (bad || 8 * u + c + e > last)
                                     y = 0xFF800000u;
                                 else if (C::kQuant)
@@ -497,27 +487,27 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                     }
                 } else if constexpr (C::kQuant) {
                     const float4 y = lds_f4(ring + 8u * kKeys);
-                    mv[0] = mv[1] = mv[2] = mv[3] = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w));
+                    mv[0] = mv[1] = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w));
                 }
 #pragma unroll
-                for (int x = 0; x < 4; ++x) mx[x] = -INFINITY;
+                for (int x = 0; x < 2; ++x) mx[x] = -INFINITY;
 #pragma unroll
                 for (int u = 0; u < kU; ++u) {
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const uint32_t *y = &s[x >> 1][4 * u + 2 * (x & 1)];
+                    for (int x = 0; x < 2; ++x) {
+                        const uint32_t *y = &s[4 * u + 2 * x];
                         mx[x] = fmax3(mx[x], __uint_as_float(y[0]), __uint_as_float(y[1]));
                     }
                 }
 #pragma unroll
                 for (int o = 1; o <= 2; o <<= 1) {
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], o));
+                    for (int x = 0; x < 2; ++x) mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], o));
                 }
                 // does a row's maximum, or its value scales' power of two, have to move?
                 bool move = false;
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
+                for (int x = 0; x < 2; ++x) {
                     mx[x] *= c_r[x];
                     move |= mx[x] > m_run[x] + kRescaleLog2;
                     if constexpr (C::kQuant) {
@@ -531,9 +521,9 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                     tc_fence_after();
                 }
                 if (__any_sync(0xffffffffu, move)) {
-                    float fo[4];
+                    float fo[2];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
+                    for (int x = 0; x < 2; ++x) {
                         fo[x] = 1.f;
                         if (mx[x] > m_run[x] + kRescaleLog2) {
                             if (m_run[x] != -INFINITY) fo[x] = ex2_approx(m_run[x] - mx[x]);
@@ -551,7 +541,7 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                             }
                         }
                     }
-                    if (i > 0 && __any_sync(0xffffffffu, fo[0] != 1.f || fo[1] != 1.f || fo[2] != 1.f || fo[3] != 1.f)) {
+                    if (i > 0 && __any_sync(0xffffffffu, fo[0] != 1.f || fo[1] != 1.f)) {
                         // (of one tile, the product before this one is the one of the other slot)
                         if (!two &&
                             !__all_sync(0xffffffffu, mbar_wait(bar(kODone + ((i - 1) & 1)), ((i - 1) >> 1) & 1, kWaitNs)))
@@ -559,73 +549,64 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                         tc_fence_after();
 #pragma unroll 1
                         for (int c0 = 0; c0 < D; c0 += 32) {
+                            const uint32_t at = half_tm + C::kOCol + w * D + c0;
+                            uint32_t o[16];
+                            tmem_ld_16x256b(at, o);
+                            tmem_wait_ld();
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const uint32_t at = lane_tm + ((uint32_t)(16 * h) << 16) + C::kOCol + w * D + c0;
-                                uint32_t o[16];
-                                tmem_ld_16x256b(at, o);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int j = 0; j < 16; ++j)
-                                    o[j] = __float_as_uint(__uint_as_float(o[j]) * fo[2 * h + ((j >> 1) & 1)]);
-                                tmem_st_16x256b(at, o);
-                            }
+                            for (int j = 0; j < 16; ++j)
+                                o[j] = __float_as_uint(__uint_as_float(o[j]) * fo[(j >> 1) & 1]);
+                            tmem_st_16x256b(at, o);
                         }
                         tmem_wait_st();
                     }
                 }
-                const uint32_t p_tm = lane_tm + (C::kOver ? sl * kKeys : C::kPCol + sl * (kKeys / 2));
+                const uint32_t p_tm = half_tm + (C::kOver ? sl * kKeys : C::kPCol + sl * (kKeys / 2));
                 auto give = [&](auto cut_tile) {  // probabilities, over the slot's columns or beside them
                     constexpr bool kCut = decltype(cut_tile)::value;
+                    uint32_t pk[4];  // of two units
+                    uint64_t ls[2] = {0ull, 0ull}, c2[2], nm2[2];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t pk[4];  // of two units
-                        uint64_t ls[2] = {0ull, 0ull}, c2[2], nm2[2];
+                    for (int x = 0; x < 2; ++x) {
+                        const float nm = (m_run[x] == -INFINITY ? 0.f : -m_run[x]) + (float)beta[x];
+                        c2[x] = f2_pack(__float_as_uint(c_r[x]), __float_as_uint(c_r[x]));
+                        nm2[x] = f2_pack(__float_as_uint(nm), __float_as_uint(nm));
+                    }
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const int x = 2 * h + j;
-                            const float nm = (m_run[x] == -INFINITY ? 0.f : -m_run[x]) + (float)beta[x];
-                            c2[j] = f2_pack(__float_as_uint(c_r[x]), __float_as_uint(c_r[x]));
-                            nm2[j] = f2_pack(__float_as_uint(nm), __float_as_uint(nm));
+                    for (int u = 0; u < kU; ++u) {
+                        uint64_t vs = 0ull;
+                        if constexpr (C::kQuant) {
+                            const uint2 sc = lds_u2(ring + 4u * (kKeys + 8 * u + c));
+                            vs = f2_pack(sc.x, sc.y);
                         }
 #pragma unroll
-                        for (int u = 0; u < kU; ++u) {
-                            uint64_t vs = 0ull;
-                            if constexpr (C::kQuant) {
-                                const uint2 sc = lds_u2(ring + 4u * (kKeys + 8 * u + c));
-                                vs = f2_pack(sc.x, sc.y);
-                            }
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const uint32_t s0 = s[h][4 * u + 2 * j], s1 = s[h][4 * u + 2 * j + 1];
-                                uint32_t a, b;
-                                f2_unpack(f2_fma(f2_pack(s0, s1), c2[j], nm2[j]), a, b);
-                                a = __float_as_uint(ex2_approx(__uint_as_float(a)));
-                                b = __float_as_uint(ex2_approx(__uint_as_float(b)));
-                                const uint64_t pr = f2_pack(a, b);
-                                ls[j] = f2_add(ls[j], pr);
-                                if constexpr (C::kQuant) {
-                                    f2_unpack(f2_mul(pr, vs), a, b);
-                                    if (kCut) {  // a hidden key's scale may be anything
-                                        const int last = min(seen[2 * h + j], it.k_end - 1) - key0;
-                                        const bool bad = (bads >> (u / 2)) & 1u;
-                                        if (bad || 8 * u + c > last) a = 0u;
-                                        if (bad || 8 * u + c + 1 > last) b = 0u;
-                                    }
-                                    pk[2 * (u & 1) + j] = pack_half2(__uint_as_float(a), __uint_as_float(b));
-                                } else {
-                                    pk[2 * (u & 1) + j] = pack_bf162(__uint_as_float(a), __uint_as_float(b));
-                                }
-                            }
-                            if (u & 1) tmem_st_16x128b(p_tm + ((uint32_t)(16 * h) << 16) + 4 * (u - 1), pk);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
+                        for (int x = 0; x < 2; ++x) {
                             uint32_t a, b;
-                            f2_unpack(ls[j], a, b);
-                            l_run[2 * h + j] += (__uint_as_float(a) + __uint_as_float(b)) *
-                                                __uint_as_float((uint32_t)(127 - beta[2 * h + j]) << 23);
+                            f2_unpack(f2_fma(f2_pack(s[4 * u + 2 * x], s[4 * u + 2 * x + 1]), c2[x], nm2[x]), a, b);
+                            a = __float_as_uint(ex2_approx(__uint_as_float(a)));
+                            b = __float_as_uint(ex2_approx(__uint_as_float(b)));
+                            const uint64_t pr = f2_pack(a, b);
+                            ls[x] = f2_add(ls[x], pr);
+                            if constexpr (C::kQuant) {
+                                f2_unpack(f2_mul(pr, vs), a, b);
+                                if (kCut) {  // a hidden key's scale may be anything
+                                    const int last = min(seen[x], it.k_end - 1) - key0;
+                                    const bool bad = (bads >> (u / 2)) & 1u;
+                                    if (bad || 8 * u + c > last) a = 0u;
+                                    if (bad || 8 * u + c + 1 > last) b = 0u;
+                                }
+                                pk[2 * (u & 1) + x] = pack_half2(__uint_as_float(a), __uint_as_float(b));
+                            } else {
+                                pk[2 * (u & 1) + x] = pack_bf162(__uint_as_float(a), __uint_as_float(b));
+                            }
                         }
+                        if (u & 1) tmem_st_16x128b(p_tm + 4 * (u - 1), pk);
+                    }
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        uint32_t a, b;
+                        f2_unpack(ls[x], a, b);
+                        l_run[x] += (__uint_as_float(a) + __uint_as_float(b)) * __uint_as_float((uint32_t)(127 - beta[x]) << 23);
                     }
                 };
                 if (C::kQuant && cut)
@@ -646,7 +627,7 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                         const int e = v_entry(i, ntiles) * C::kPanels + pp, slot = e % C::kStages;
                         if (!__all_sync(0xffffffffu, mbar_wait(bar(kFull + slot), (e / C::kStages) & 1, kWaitNs))) ok = false;
                         const uint32_t panel = sbase + C::kConv + slot * C::kPanelBytes;
-                        for (int u = w * 128 + r; u < kKeys * C::kPanelD / 8; u += nq * 128) {
+                        for (int u = w * 256 + h * 128 + r; u < kKeys * C::kPanelD / 8; u += nq * 256) {
                             const int row = u / (C::kPanelD / 8), cu = u % (C::kPanelD / 8);
                             const uint32_t a = panel + (cu / 8) * C::kChunkBytes + sw128(row, cu % 8);
                             constexpr uint32_t kExp = DT == VA_BF16 ? 0x7F80u : 0x7C00u;
@@ -679,7 +660,7 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
             }
             // the rows' sums over the four lanes that share them, and all of a row to its own lane
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
+            for (int x = 0; x < 2; ++x) {
 #pragma unroll
                 for (int o = 1; o <= 2; o <<= 1) l_run[x] += __shfl_xor_sync(0xffffffffu, l_run[x], o);
                 if ((lane & 3) == 0) {
@@ -688,7 +669,7 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                     if (C::kQuant) sts_u32(stat + 4u * (2 * kMmaRows + my_row(x)), (uint32_t)beta[x]);
                 }
             }
-            __syncwarp();
+            named_bar_sync(2 + w, 256);  // a row's lane is in another warp, or in two
             const float m_row = lds_f32(stat + 4u * r), l_row = lds_f32(stat + 4u * (kMmaRows + r));
             const int beta_row = !C::kQuant ? 0 : (int)lds_u32(stat + 4u * (2 * kMmaRows + r));
             // epilogue
@@ -698,7 +679,7 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
             const float inv = l_row == 0.f ? 0.f : (1.f / l_row) * __uint_as_float((uint32_t)(127 - beta_row) << 23);
             const float lse = l_row == 0.f ? -INFINITY : (m_row + log2f(l_row)) * 0.69314718055994531f;
             const size_t orow = (size_t)(it.q0 + token) * p.Hq + head;
-            if (row_ok && ok) {
+            if (row_ok && ok && h == 0) {
                 if (it.part < 0) {
                     if (p.lse) p.lse[orow] = lse;
                 } else {
@@ -731,7 +712,7 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                 const uint32_t stage = sbase + C::kQ + w * C::kQBytes;
                 auto unit = [&](int row, int u) { return stage + row * (D * 2) + (((u & ~7) | ((u ^ row) & 7)) << 4); };
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32) {
+                for (int c0 = h * (D / 2); c0 < (h + 1) * (D / 2); c0 += 32) {
                     uint32_t o[32];
                     tmem_ld32(lane_tm + C::kOCol + w * D + c0, o);
                     tmem_wait_ld();
@@ -756,9 +737,9 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                                           pack_bf162(__uint_as_float(o[8 * n + 4]), __uint_as_float(o[8 * n + 5])),
                                           pack_bf162(__uint_as_float(o[8 * n + 6]), __uint_as_float(o[8 * n + 7]))));
                 }
-                named_bar_sync(2 + w, 128);
+                named_bar_sync(2 + w, 256);
                 if (ok) {
-                    for (int e = r; e < nt * G * (D / 8); e += 128) {
+                    for (int e = h * 128 + r; e < nt * G * (D / 8); e += 256) {
                         const int row = e / (D / 8), u = e % (D / 8);
                         const size_t to = (size_t)(it.q0 + w * tpt + row / G) * p.Hq + it.kvh * G + row % G;
                         reinterpret_cast<uint4 *>(p.out)[to * (D / 8) + u] = lds_u4(unit(row, u));
@@ -767,7 +748,7 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
             } else {
                 float *o_part = p.o_part + (size_t)(it.part + w) * D * kMmaRows + r;
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32) {
+                for (int c0 = h * (D / 2); c0 < (h + 1) * (D / 2); c0 += 32) {
                     uint32_t o[32];
                     tmem_ld32(lane_tm + C::kOCol + w * D + c0, o);
                     tmem_wait_ld();
@@ -784,7 +765,6 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
         }
     } else if constexpr (C::kQuant) {
         // ------------------------------------------------------------ dequant
-        regs_down<C::kDequantRegs>();
         // A panel is 16-element pieces; each thread takes kPer of them, kStep rows (a multiple of the swizzle's 8) apart.
         constexpr int kPieces = C::kPanelD / 16;  // of a row
         constexpr int kPer = (kKeys * kPieces + 127) / 128;
