@@ -209,33 +209,33 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                 }
                 __syncwarp();
             }
-            // page ids: 32 at a time, one batch ahead
-            constexpr int kIdTiles = 32 / kPages;
-            auto load_ids = [&](int i0) -> int {  // of the tiles i0 .. i0 + kIdTiles - 1
-                const int k = i0 * kPages + lane;
-                return k < npages ? __ldg(bt + k) : 0;
-            };
-            int ids_k = load_ids(0), next_k = load_ids(kIdTiles), at_k = 0;  // K and V walk the table apart
-            int ids_v = ids_k, next_v = next_k, at_v = 0;
             constexpr int kRing = C::kQuant ? C::kRawStages : C::kStages;
             constexpr int kFullBar = C::kQuant ? kRawFull : kFull, kEmptyBar = C::kQuant ? kRawEmpty : kEmpty;
             const int total = 2 * ntiles * C::kPanels;
             int end = total;
+            // page ids of a panel, alike in all lanes: one panel ahead
+            int ids[kPages];
+            auto load_ids = [&](int e) {
+                bool v;
+                const int i = e < total ? entry_tile(e / C::kPanels, ntiles, v) : ntiles;
+#pragma unroll
+                for (int pg = 0; pg < kPages; ++pg) ids[pg] = i * kPages + pg < npages ? __ldg(bt + i * kPages + pg) : 0;
+            };
+            load_ids(pw);
             for (int e = pw; e < total; e += kProducers) {
                 bool v;
                 const int i = entry_tile(e / C::kPanels, ntiles, v);
                 const int pp = e % C::kPanels;
-                int &ids = v ? ids_v : ids_k, &next = v ? next_v : next_k, &at = v ? at_v : at_k;
-                if (i / kIdTiles != at) {
-                    at = i / kIdTiles;
-                    ids = next;
-                    next = load_ids(kIdTiles * (at + 1));
-                }
                 const int npg = min(kPages, npages - i * kPages);
-                int page = __shfl_sync(0xffffffffu, ids, (i % kIdTiles) * kPages + lane % kPages);
-                const bool bad = p.num_pages > 0 && (page < 0 || page >= p.num_pages) && lane < npg;
-                const uint32_t bads = __ballot_sync(0xffffffffu, bad);
-                if (bad) page = 0;
+                uint32_t bads = 0;
+                int page[kPages];
+#pragma unroll
+                for (int pg = 0; pg < kPages; ++pg) {
+                    const bool bad = p.num_pages > 0 && (uint32_t)ids[pg] >= (uint32_t)p.num_pages;
+                    bads |= bad ? 1u << pg : 0u;
+                    page[pg] = bad ? 0 : ids[pg];
+                }
+                load_ids(e + kProducers);
                 const int slot = e % kRing, use = e / kRing;
                 if (use > 0) {
                     ok = __all_sync(0xffffffffu, mbar_wait(bar(kEmptyBar + slot), (use & 1) ^ 1, kWaitNs));
@@ -246,30 +246,29 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                 }
                 const CUtensorMap *map = v ? &args.tm_v : &args.tm_k;
                 const uint32_t full = bar(kFullBar + slot);
-                if (lane == 0) {
+                if (elect_one()) {
                     if (!v && pp == 0) {
                         sts_u32(sbase + C::kBad + 4u * (i % kBadRing), bads);
                         if (bads) atomicOr(p.flags, kFlagBadPage);
                     }
                     mbar_arrive_expect_tx(full, (uint32_t)npg * (C::kQuant ? VA_PAGE_SIZE * C::kRawRow
                                                                            : VA_PAGE_SIZE * 128 * C::kChunks));
-                }
-                __syncwarp();
 #pragma unroll
-                for (int pg = 0; pg < kPages; ++pg) {
-                    if (pg >= npg) break;
-                    const int at_page = __shfl_sync(0xffffffffu, page, pg);
-                    if constexpr (C::kQuant) {
-                        tma_load_4d_warp(sbase + C::kRaw + slot * C::kRawBytes + pg * VA_PAGE_SIZE * C::kRawRow, map,
-                                         pp * C::kRawRow, it.kvh, 0, at_page, full);
-                    } else {
+                    for (int pg = 0; pg < kPages; ++pg) {
+                        if (pg >= npg) break;
+                        if constexpr (C::kQuant) {
+                            tma_load_4d(sbase + C::kRaw + slot * C::kRawBytes + pg * VA_PAGE_SIZE * C::kRawRow, map,
+                                        pp * C::kRawRow, it.kvh, 0, page[pg], full);
+                        } else {
 #pragma unroll
-                        for (int c = 0; c < C::kChunks; ++c)
-                            tma_load_4d_warp(sbase + C::kConv + slot * C::kPanelBytes + c * C::kChunkBytes +
-                                                 pg * VA_PAGE_SIZE * 128,
-                                             map, pp * C::kPanelD + c * 64, it.kvh, 0, at_page, full);
+                            for (int c = 0; c < C::kChunks; ++c)
+                                tma_load_4d(sbase + C::kConv + slot * C::kPanelBytes + c * C::kChunkBytes +
+                                                pg * VA_PAGE_SIZE * 128,
+                                            map, pp * C::kPanelD + c * 64, it.kvh, 0, page[pg], full);
+                        }
                     }
                 }
+                __syncwarp();
             }
             // every issued copy lands before the CTA ends
             for (int e = max(0, end - kRing); e < end; ++e)
@@ -283,74 +282,78 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                 constexpr uint32_t idS = idesc_f16(128, kKeys, kAB, 0, 0);
                 constexpr uint32_t idO = idesc_f16(128, C::kPanelD, kAB, 0, 1);
                 // K-major operands: 8-row groups 1024 bytes apart; V is MN-major, its 64-element chunks kChunkBytes apart
-                const uint64_t qdesc = smem_desc(sbase + C::kQ + w * C::kQBytes, 16, 1024, 2);
-                const uint64_t kdesc = smem_desc(sbase + C::kConv, 16, 1024, 2);
-                const uint64_t vdesc = smem_desc(sbase + C::kConv, C::kChunkBytes, 1024, 2);
-                auto wait = [&](int b, int parity) -> bool {
-                    return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, kWaitNs));
-                };
+                constexpr uint32_t kHi = smem_desc_hi(1024, 2);
+                const uint32_t qlo = smem_desc_lo(sbase + C::kQ + w * C::kQBytes, 16);
+                const uint32_t klo = smem_desc_lo(sbase + C::kConv, 16);
+                const uint32_t vlo = smem_desc_lo(sbase + C::kConv, C::kChunkBytes);
                 int stage = 0, phase = 0;  // of the next panel
                 auto pass = [&] {
-                    mma_commit_warp(bar(kEmpty + stage));
                     if (++stage == C::kStages) stage = 0, phase ^= 1;
+                };
+                auto here = [&]() -> bool {  // the next panel
+                    return __all_sync(0xffffffffu, mbar_wait(bar(kFull + stage), phase, kWaitNs));
+                };
+                auto here_and = [&](int b, int parity) -> bool {  // and another barrier
+                    const bool done = __all_sync(
+                        0xffffffffu, mbar_wait2(bar(kFull + stage), phase, bar(b), parity, kWaitNs));
+                    tc_fence_after();
+                    return done;
                 };
                 auto scores = [&](int slot) -> bool {  // of the next tile of keys, whose first panel is here
 #pragma unroll
                     for (int pp = 0; pp < C::kPanels; ++pp) {
-                        if (pp > 0 && !wait(kFull + stage, phase)) return false;
-                        const uint64_t kd = kdesc + (uint64_t)(stage * (C::kPanelBytes >> 4));
-                        const uint64_t qd = qdesc + (uint64_t)(pp * (C::kPanelD / 64 * C::kQChunk) >> 4);
+                        if (pp > 0 && !here()) return false;
+                        if (elect_one()) {
+                            const uint32_t kd = klo + (uint32_t)(stage * (C::kPanelBytes >> 4));
+                            const uint32_t qd = qlo + (uint32_t)(pp * (C::kPanelD / 64 * C::kQChunk) >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < C::kPanelD / 16; ++kk)
-                            mma_ss_warp(tmem + slot * kKeys, qd + (uint64_t)((kk / 4) * (C::kQChunk >> 4) + (kk % 4) * 2),
-                                        kd + (uint64_t)((kk / 4) * (C::kChunkBytes >> 4) + (kk % 4) * 2), idS, pp > 0 || kk > 0);
-                        if (pp + 1 < C::kPanels) pass();
+                            for (int kk = 0; kk < C::kPanelD / 16; ++kk)
+                                mma_ss_lo<kHi>(tmem + slot * kKeys, qd + (kk / 4) * (C::kQChunk >> 4) + (kk % 4) * 2,
+                                               kd + (kk / 4) * (C::kChunkBytes >> 4) + (kk % 4) * 2, idS, pp > 0 || kk > 0);
+                            if (pp == C::kPanels - 1) mma_commit(bar(kSFull + slot));
+                            mma_commit(bar(kEmpty + stage));
+                        }
+                        __syncwarp();
+                        pass();
                     }
-                    mma_commit_warp(bar(kSFull + slot));
-                    pass();
                     return true;
                 };
                 auto product = [&](int slot, bool first) -> bool {
                     const uint32_t from = tmem + (C::kOver ? slot * kKeys : C::kPCol + slot * (kKeys / 2));
 #pragma unroll
                     for (int pp = 0; pp < C::kPanels; ++pp) {
-                        if (pp > 0 && !wait(kFull + stage, phase)) return false;
-                        const uint64_t vd = vdesc + (uint64_t)(stage * (C::kPanelBytes >> 4));
+                        if (pp > 0 && !here()) return false;
+                        if (elect_one()) {
+                            const uint32_t vd = vlo + (uint32_t)(stage * (C::kPanelBytes >> 4));
 #pragma unroll
-                        for (int kk = 0; kk < kKeys / 16; ++kk)
-                            mma_ts_warp(tmem + C::kOCol + w * D + pp * C::kPanelD, from + kk * 8,
-                                        vd + (uint64_t)(kk * (16 * 128 >> 4)), idO, !first || kk > 0);
-                        if (pp + 1 < C::kPanels) pass();
+                            for (int kk = 0; kk < kKeys / 16; ++kk)
+                                mma_ts_lo<kHi>(tmem + C::kOCol + w * D + pp * C::kPanelD, from + kk * 8,
+                                               vd + kk * (16 * 128 >> 4), idO, !first || kk > 0);
+                            if (pp == C::kPanels - 1) mma_commit(bar(kODone + slot));
+                            mma_commit(bar(kEmpty + stage));
+                        }
+                        __syncwarp();
+                        pass();
                     }
-                    mma_commit_warp(bar(kODone + slot));
-                    pass();
                     return true;
                 };
-                ok = wait(kQReady, 0) && wait(kFull + stage, phase);
-                tc_fence_after();
+                ok = here_and(kQReady, 0);
                 if (two) {
                     ok = ok && scores(w);
                     for (int i = 0; i < ntiles && ok; ++i) {
-                        if (i + 1 < ntiles) {
-                            ok = wait(kFull + stage, phase) && wait(kSRead + w, i & 1);
-                            tc_fence_after();
-                            ok = ok && scores(w);
-                        }
-                        ok = ok && wait(kFull + stage, phase) && wait(kPFull + w, i & 1);
-                        tc_fence_after();
-                        ok = ok && product(w, i == 0);
+                        if (i + 1 < ntiles) ok = here_and(kSRead + w, i & 1) && scores(w);
+                        ok = ok && here_and(kPFull + w, i & 1) && product(w, i == 0);
                     }
                 } else {
-                    ok = ok && scores(0) && (ntiles < 2 || (wait(kFull + stage, phase) && scores(1)));
+                    ok = ok && scores(0) && (ntiles < 2 || (here() && scores(1)));
                     for (int k = 0; k < ntiles && ok; ++k) {
-                        ok = wait(kFull + stage, phase) && wait(kPFull + (k & 1), (k >> 1) & 1);
-                        tc_fence_after();
-                        ok = ok && product(k & 1, k == 0);
-                        if (ok && k + 2 < ntiles) ok = wait(kFull + stage, phase) && scores(k & 1);
+                        ok = here_and(kPFull + (k & 1), (k >> 1) & 1) && product(k & 1, k == 0);
+                        if (ok && k + 2 < ntiles) ok = here() && scores(k & 1);
                     }
                 }
-                mma_commit_warp(bar(kOFinal));
-                if (!wait(kOFinal, 0)) ok = false;
+                if (elect_one()) mma_commit(bar(kOFinal));
+                __syncwarp();
+                if (!__all_sync(0xffffffffu, mbar_wait(bar(kOFinal), 0, kWaitNs))) ok = false;
             }
         }
     } else if (warp < C::kSoftmaxWarps) {

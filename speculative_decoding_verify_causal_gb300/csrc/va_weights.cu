@@ -219,7 +219,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) weights_kernel(const __gr
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issue, by the whole warp
         constexpr uint32_t id = idesc_f16(128, kRows, 1, 0, 0);
-        const uint64_t kdesc = smem_desc(sbase + C::kK, 16, 1024, 2), qdesc = smem_desc(sbase + C::kQ, 16, 1024, 2);
+        constexpr uint32_t kHi = smem_desc_hi(1024, 2);
+        const uint32_t klo = smem_desc_lo(sbase + C::kK, 16), qlo = smem_desc_lo(sbase + C::kQ, 16);
         auto wait = [&](int b, int parity) -> bool {
             const bool done = __all_sync(0xffffffffu, mbar_wait(bar(b), parity, kWaitNs));
             tc_fence_after();
@@ -232,17 +233,21 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) weights_kernel(const __gr
                 const int s = kt * 2 + (m & 1);
                 if (m >= 2) ok = wait(kSEmpty + s, ((m >> 1) & 1) ^ 1);
                 if (!ok) break;
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint64_t off = (uint64_t)((kk / 4) * (C::kChunkBytes >> 4) + (kk % 4) * 2);
-                    mma_ss_warp(tmem + s * kRows, kdesc + (uint64_t)(kt * (C::kTileBytes >> 4)) + off,
-                                qdesc + (uint64_t)(st * (C::kTileBytes >> 4)) + off, id, kk > 0);
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (kk / 4) * (C::kChunkBytes >> 4) + (kk % 4) * 2;
+                        mma_ss_lo<kHi>(tmem + s * kRows, klo + kt * (C::kTileBytes >> 4) + off,
+                                       qlo + st * (C::kTileBytes >> 4) + off, id, kk > 0);
+                    }
+                    mma_commit(bar(kSFull + s));
+                    if (kt == C::kKeyTiles - 1) mma_commit(bar(kQEmpty + st));
                 }
-                mma_commit_warp(bar(kSFull + s));
+                __syncwarp();
             }
-            mma_commit_warp(bar(kQEmpty + st));
         }
-        mma_commit_warp(bar(kDone));
+        if (elect_one()) mma_commit(bar(kDone));
+        __syncwarp();
         if (!wait(kDone, 0)) ok = false;
     } else {
         // ------------------------------------------------------------ sums
