@@ -7,10 +7,10 @@
 // or up to two (64, 128) over a range of keys.
 //
 // Steps.  Step k of a two-tile item is (rows k % 2, keys k / 2); of a one-tile item it is (keys k).  Scores alternate
-// between two tensor-memory slots.  Of two tiles each has its slot and a warp that issues its instructions: S(i + 1) as
-// soon as the softmax has read S(i), then P(i) V(i).  Of one tile one warp issues P(k) V(k), S(k + 2): while the softmax
-// of one slot runs, the tensor pipe works on the other.  At head_dim 256 P overwrites S in its slot; S(k + 2) is issued
-// behind P(k) V(k) by the same thread, and tensor instructions run in their order.
+// between two tensor-memory slots of 80 columns, probabilities between two of 40: 2 x 128 columns (or 256) of O and
+// these are all 512, so that the next scores need not wait for the product of these.  Of two tiles each has its slot
+// and a warp that issues its instructions: S(i + 1) as soon as the softmax has read S(i), then P(i) V(i).  Of one tile
+// one warp issues P(k) V(k), S(k + 2): while the softmax of one slot runs, the tensor pipe works on the other.
 //   producer warps  page ids from the block table, then TMA boxes (16 slots of one page and head) into the ring
 //   dequant warps   (quantised caches) raw panel -> fp16 panel, exact, in the MMA's swizzled layout; keys' scales
 //   MMA warps       as above; panels are used in the order of the ring
@@ -51,9 +51,8 @@ template <int D, int DT>
 struct Cfg {
     static constexpr bool kQuant = DT != VA_BF16;
     static constexpr int kTiles = chunk_tiles(D);
-    static constexpr int kKeys = chunk_keys(D);
+    static constexpr int kKeys = kChunkKeys;
     static constexpr int kPages = kKeys / VA_PAGE_SIZE;
-    static constexpr bool kOver = kTiles == 1;        // probabilities overwrite scores
     static constexpr int kPanelD = D < 128 ? D : 128;
     static constexpr int kPanels = D / kPanelD;       // panels of a K or V tile
     static constexpr int kChunks = kPanelD / 64;      // 64-element chunks of a panel
@@ -64,16 +63,20 @@ struct Cfg {
     static constexpr int kRawBytes = kKeys * kRawRow;
     static constexpr int kQChunk = kMmaRows * 128;       // 64-element chunk of a tile of q
     static constexpr int kQBytes = D / 64 * kQChunk;
-    static constexpr int kStages = kQuant ? (D == 64 ? 6 : D == 128 ? 5 : 3) : (D == 256 ? 5 : D == 128 ? 7 : 8);
-    static constexpr int kRawStages = kQuant ? (D == 64 ? 6 : D == 128 ? 5 : 3) : 0;
+    static constexpr int kStages = kQuant ? (D == 64 ? 6 : 5) : (D == 128 ? 7 : 8);
+    // Even, so that a raw slot belongs to one producer and one dequant group: a barrier's parity tells a phase from the
+    // next, not from the one after that, and nothing holds two producers or two groups within a ring of each other.
+    // (The ring of whole panels is given back by the MMA warps, in order, so there the others cannot be a phase ahead.)
+    static constexpr int kRawStages = kQuant ? (D == 64 ? 6 : 4) : 0;
+    static_assert(kRawStages % 2 == 0 && kProducers == 2, "a slot's owner");
     static constexpr int kScaleFloats = 2 * kKeys + 4;   // k scales, v scales, the largest v scale of each dequant warp
     static constexpr int kSoftmaxWarps = 8 * kTiles;
-    static constexpr int kDequantWarps = kQuant ? 4 : 0;
+    static constexpr int kDequantWarps = kQuant ? 8 : 0;  // two groups, which take panels in turn
     static constexpr int kProducerWarp = kSoftmaxWarps + kDequantWarps;  // and the ones behind it
     static constexpr int kMmaWarp = kProducerWarp + kProducers;          // one for each tile of rows
     static constexpr int kThreads = (kMmaWarp + kTiles + 3) / 4 * 128;  // whole warpgroups
     static constexpr uint32_t kPCol = 2 * kKeys;                  // S slots at 0 and kKeys, P slots behind them
-    static constexpr uint32_t kOCol = kOver ? 2 * kKeys : 3 * kKeys;
+    static constexpr uint32_t kOCol = 3 * kKeys;
     static_assert(kOCol + kTiles * D <= 512, "tensor memory");
     static constexpr int kQ = 0;
     static constexpr int kConv = kTiles * kQBytes;
@@ -166,10 +169,10 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
         prefetch_tensormap(&args.tm_k);
         prefetch_tensormap(&args.tm_v);
         for (int i = 0; i < kMaxStages; ++i) {
-            mbar_init(bar(kFull + i), C::kQuant ? C::kDequantWarps : 1);
+            mbar_init(bar(kFull + i), C::kQuant ? 4 : 1);
             mbar_init(bar(kEmpty + i), nq);
             mbar_init(bar(kRawFull + i), 1);
-            mbar_init(bar(kRawEmpty + i), C::kQuant ? C::kDequantWarps : 1);
+            mbar_init(bar(kRawEmpty + i), C::kQuant ? 4 : 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(kSFull + i), 1);
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                     return true;
                 };
                 auto product = [&](int slot, bool first) -> bool {
-                    const uint32_t from = tmem + (C::kOver ? slot * kKeys : C::kPCol + slot * (kKeys / 2));
+                    const uint32_t from = tmem + C::kPCol + slot * (kKeys / 2);
 #pragma unroll
                     for (int pp = 0; pp < C::kPanels; ++pp) {
                         if (pp > 0 && !here()) return false;
@@ -442,18 +445,13 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                 const uint32_t s_tm = half_tm + sl * kKeys;
                 const uint32_t ring = sbase + C::kScale + (i % kScaleRing) * C::kScaleFloats * 4;
                 uint32_t s[4 * kU];  // row x, unit u of 8 columns: s[4 u + 2 x], s[4 u + 2 x + 1]
-                if constexpr (kU == 16) {
-                    tmem_ld_16x256b(s_tm, s);
-                } else {
-                    tmem_ld_16x256b(s_tm, reinterpret_cast<uint32_t(&)[32]>(s[0]));
-                    tmem_ld_16x256b(s_tm + 64, reinterpret_cast<uint32_t(&)[8]>(s[32]));
-                }
+                static_assert(kU == 10, "80 columns in two loads");
+                tmem_ld_16x256b(s_tm, reinterpret_cast<uint32_t(&)[32]>(s[0]));
+                tmem_ld_16x256b(s_tm + 64, reinterpret_cast<uint32_t(&)[8]>(s[32]));
                 tmem_wait_ld();
-                if constexpr (!C::kOver) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(kSRead + sl));
-                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kSRead + sl));
                 // raw scores times k scale, hidden keys at -inf, and the rows' maxima
                 if constexpr (C::kQuant) {
 #pragma unroll
@@ -519,7 +517,7 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                     }
                 }
                 // the product before this one: P's slot is free and O holds it
-                if (!C::kOver && (two ? i > 0 : i > 1)) {
+                if (two ? i > 0 : i > 1) {
                     if (!__all_sync(0xffffffffu, mbar_wait(bar(kODone + sl), (ph - 1) & 1, kWaitNs))) ok = false;
                     tc_fence_after();
                 }
@@ -564,8 +562,8 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                         tmem_wait_st();
                     }
                 }
-                const uint32_t p_tm = half_tm + (C::kOver ? sl * kKeys : C::kPCol + sl * (kKeys / 2));
-                auto give = [&](auto cut_tile) {  // probabilities, over the slot's columns or beside them
+                const uint32_t p_tm = half_tm + C::kPCol + sl * (kKeys / 2);
+                auto give = [&](auto cut_tile) {
                     constexpr bool kCut = decltype(cut_tile)::value;
                     uint32_t pk[4];  // of two units
                     uint64_t ls[2] = {0ull, 0ull}, c2[2], nm2[2];
@@ -775,14 +773,19 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
         constexpr int kPieceBytes = C::kBits * 2;
         static_assert(kStep % 8 == 0, "rows apart");
         constexpr bool kEven = kKeys * kPieces % 128 == 0;  // else some threads have one less
-        const int dt = tid - C::kSoftmaxWarps * 32;  // 0 .. 127, also the key whose scales it carries
+        const int dt = (tid - C::kSoftmaxWarps * 32) & 127;  // in the group, also the key whose scales it carries
+        const int group = (warp - C::kSoftmaxWarps) >> 2;
         const int n0 = dt / kPieces, d0 = (dt % kPieces) * 16;
         const uint32_t lo_at = (d0 / 64) * C::kChunkBytes + sw128(n0, (d0 % 64) / 8);
         const uint32_t hi_at = (d0 / 64) * C::kChunkBytes + sw128(n0, (d0 % 64) / 8 + 1);
         const bool odd = (d0 / 64) & 1;  // the other unit first, so that a quarter of a warp hits no bank twice
+        // The scales of a tile of keys go with its first K panel.  Of one panel a tile that is group 0 for tile 0 and
+        // group 1 for the others (K0 K1 V0 K2 V1 ..), of two panels always group 0.
+        const int first = C::kPanels == 1 ? group : 0;
+        const int beyond = C::kPanels == 1 ? (group == 0 ? 1 : ntiles) : (group == 0 ? ntiles : 0);
         auto load_id = [&](int i) -> int {
             const int n = i * kPages + dt / VA_PAGE_SIZE;
-            if (dt >= kKeys || i >= ntiles || n >= npages || it.k_begin + i * kKeys + dt >= it.k_end) return -1;
+            if (dt >= kKeys || i >= beyond || i >= ntiles || n >= npages || it.k_begin + i * kKeys + dt >= it.k_end) return -1;
             const int page = __ldg(bt + n);
             return p.num_pages > 0 && page >= p.num_pages ? -1 : page;
         };
@@ -790,12 +793,12 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
             return page < 0 ? 0.f : __ldg(from + ((size_t)page * VA_PAGE_SIZE + dt % VA_PAGE_SIZE) * p.Hkv + it.kvh);
         };
         // scales two tiles ahead, page ids three
-        int id0 = load_id(0), id1 = load_id(1), id2 = load_id(2);
+        int id0 = load_id(first), id1 = load_id(first + 1), id2 = load_id(first + 2);
         float ks0 = load_scale(p.k_scale, id0), vs0 = load_scale(p.v_scale, id0);
         float ks1 = load_scale(p.k_scale, id1), vs1 = load_scale(p.v_scale, id1);
         constexpr int kRawN = C::kRawStages ? C::kRawStages : 1;
         const int total = 2 * ntiles * C::kPanels;
-        for (int e = 0; e < total && ok; ++e) {
+        for (int e = group; e < total && ok; e += 2) {
             bool v;
             const int i = entry_tile(e / C::kPanels, ntiles, v);
             const int rs = e % kRawN, slot = e % C::kStages;

@@ -59,10 +59,7 @@ struct WeightParams {
     float sm_scale_log2;
 };
 
-// Keys of one tile of scores.  80 leaves room in the tensor memory for probabilities beside the scores (2 tiles of
-// rows: 2 x 128 columns of O, 2 x 80 of scores, 2 x 40 of probabilities), so that the next scores need not wait for the
-// product of these; at head_dim 256 O takes 256 columns and probabilities overwrite their scores.
-constexpr __host__ __device__ int chunk_keys(int D) { return D == 256 ? 128 : 80; }
+constexpr int kChunkKeys = 80;  // keys of one tile of scores
 constexpr int kWeightClusters = 8;  // most CTAs that share a block of keys
 constexpr int weight_keys(int D) { return D == 256 ? 128 : 256; }  // keys of a block
 constexpr int kFlagTimeoutBit = 4;

@@ -78,7 +78,7 @@ struct Rows {
 
 void plan_geometry(const int32_t *chunk_lens, const int32_t *seq_lens, int B, int Hkv, int G, int D, int num_sms,
                    Geometry &g) {
-    const int tpt = va::kMmaRows / G, most = tpt * va::chunk_tiles(D), keys = va::chunk_keys(D);
+    const int tpt = va::kMmaRows / G, most = tpt * va::chunk_tiles(D), keys = va::kChunkKeys;
     std::vector<Rows> rows;
     int at = 0;
     for (int b = 0; b < B; ++b) {
@@ -194,7 +194,7 @@ int plan_host(const int32_t *chunk_lens, const int32_t *seq_lens, int B, int Hq,
 
 void fill_info(const va_chunk_plan &p, va_chunk_plan_info *info) {
     *info = {p.num_seqs, p.Hq, p.Hkv, p.D, p.kv_dtype, p.total, p.max_blocks, p.num_items, p.num_groups,
-             p.max_tiles * va::chunk_keys(p.D), p.num_sms, p.workspace_bytes};
+             p.max_tiles * va::kChunkKeys, p.num_sms, p.workspace_bytes};
 }
 
 int fail(cudaError_t e) {
