@@ -75,6 +75,13 @@ struct Cfg {
     static constexpr int kProducerWarp = kSoftmaxWarps + kDequantWarps;  // and the ones behind it
     static constexpr int kMmaWarp = kProducerWarp + kProducers;          // one for each tile of rows
     static constexpr int kThreads = (kMmaWarp + kTiles + 3) / 4 * 128;  // whole warpgroups
+    // Registers of a thread.  With dequant warps and two tiles of rows the block's even share is too few for a softmax
+    // thread's scores; its warpgroups take what the others give back.
+    static constexpr bool kShare = kQuant && kTiles == 2;
+    static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
+    static constexpr int kSoftmaxRegs = 88, kDequantRegs = 56, kOtherRegs = 40;
+    static_assert(!kShare || (kSoftmaxWarps * kSoftmaxRegs + kDequantWarps * kDequantRegs + 4 * kOtherRegs) * 32 <=
+                                 kThreads * kLaunchRegs, "registers that the block was launched with");
     static constexpr uint32_t kPCol = 2 * kKeys;                  // S slots at 0 and kKeys, P slots behind them
     static constexpr uint32_t kOCol = 3 * kKeys;
     static_assert(kOCol + kTiles * D <= 512, "tensor memory");
@@ -198,6 +205,7 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
     bool ok = true;
 
     if (warp >= C::kProducerWarp) {
+        if constexpr (C::kShare) regs_down<C::kOtherRegs>();
         if (warp < C::kMmaWarp) {
             // ------------------------------------------------------------ producers
             const int pw = warp - C::kProducerWarp;
@@ -361,6 +369,7 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
         }
     } else if (warp < C::kSoftmaxWarps) {
         // ------------------------------------------------------------ softmax
+        if constexpr (C::kShare) regs_up<C::kSoftmaxRegs>();
         const int w = warp >> 3;         // tile of rows
         const int h = (warp >> 2) & 1;   // half of the 32 rows of this quarter; half of the elements at the end
         const int r = (warp & 3) * 32 + lane;
@@ -766,6 +775,7 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
         }
     } else if constexpr (C::kQuant) {
         // ------------------------------------------------------------ dequant
+        if constexpr (C::kShare) regs_down<C::kDequantRegs>();
         // A panel is 16-element pieces; each thread takes kPer of them, kStep rows (a multiple of the swizzle's 8) apart.
         constexpr int kPieces = C::kPanelD / 16;  // of a row
         constexpr int kPer = (kKeys * kPieces + 127) / 128;
