@@ -786,9 +786,11 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
         const int dt = (tid - C::kSoftmaxWarps * 32) & 127;  // in the group, also the key whose scales it carries
         const int group = (warp - C::kSoftmaxWarps) >> 2;
         const int n0 = dt / kPieces, d0 = (dt % kPieces) * 16;
-        const uint32_t lo_at = (d0 / 64) * C::kChunkBytes + sw128(n0, (d0 % 64) / 8);
-        const uint32_t hi_at = (d0 / 64) * C::kChunkBytes + sw128(n0, (d0 % 64) / 8 + 1);
-        const bool odd = (d0 / 64) & 1;  // the other unit first, so that a quarter of a warp hits no bank twice
+        // In odd chunks the piece's second half goes first, so that a quarter of a warp hits no bank twice: the raw words
+        // are exchanged, not the stores' order, which would be a branch within the warp and twice the stores.
+        const bool odd = (d0 / 64) & 1;
+        const uint32_t first_at = (d0 / 64) * C::kChunkBytes + sw128(n0, (d0 % 64) / 8 + (odd ? 1 : 0));
+        const uint32_t second_at = (d0 / 64) * C::kChunkBytes + sw128(n0, (d0 % 64) / 8 + (odd ? 0 : 1));
         // The scales of a tile of keys go with its first K panel.  Of one panel a tile that is group 0 for tile 0 and
         // group 1 for the others (K0 K1 V0 K2 V1 ..), of two panels always group 0.
         const int first = C::kPanels == 1 ? group : 0;
@@ -828,17 +830,15 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
             for (int j = 0; j < kPer; ++j) {
                 if (!kEven && n0 + j * kStep >= kKeys) break;
                 uint32_t h[8];
+                raw[j].exchange(odd);
                 raw[j].to_half(h);
-                uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-                if (n0 + j * kStep >= nvalid) lo = hi = make_uint4(0, 0, 0, 0);
-                const uint32_t at = dst + j * kStep * 128;
-                if (odd) {
-                    sts_u4(at + hi_at, hi);
-                    sts_u4(at + lo_at, lo);
-                } else {
-                    sts_u4(at + lo_at, lo);
-                    sts_u4(at + hi_at, hi);
+                if (n0 + j * kStep >= nvalid) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) h[k] = 0;
                 }
+                const uint32_t at = dst + j * kStep * 128;
+                sts_u4(at + first_at, make_uint4(h[0], h[1], h[2], h[3]));
+                sts_u4(at + second_at, make_uint4(h[4], h[5], h[6], h[7]));
             }
             if (!v && e % C::kPanels == 0) {
                 if (i >= kScaleRing &&

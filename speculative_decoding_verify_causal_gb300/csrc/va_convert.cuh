@@ -149,6 +149,18 @@ struct RawPiece {
             w[0] = lds_u32(a);
         }
     }
+    // the halves of the piece in the other order
+    __device__ __forceinline__ void exchange(bool yes) {
+        if constexpr (kWords == 1) {
+            w[0] = __funnelshift_l(w[0], w[0], yes ? 16 : 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords / 2; ++i) {
+                const uint32_t a = w[i], b = w[i + kWords / 2];
+                w[i] = yes ? b : a, w[i + kWords / 2] = yes ? a : b;
+            }
+        }
+    }
     __device__ __forceinline__ void to_half(uint32_t (&hw)[8]) const {
         if constexpr (DT == VA_INT2) {
             int2x16_to_half2x8(w[0], hw);
