@@ -117,7 +117,7 @@ void plan_geometry(const int32_t *chunk_lens, const int32_t *seq_lens, int B, in
     }
     int chosen = longest;
     double best = rows.empty() ? 0.0 : cost_of(longest);
-    for (double waves : {0.5, 0.75, 1.0, 1.5, 2.0, 3.0, 4.0}) {
+    for (double waves : {0.5, 0.75, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0, 8.0, 12.0}) {
         const int c = std::max(2, (int)std::ceil(units / (num_sms * waves)));
         if (c >= longest) continue;
         const double x = cost_of(c);
@@ -160,9 +160,12 @@ void plan_blocks(const int32_t *chunk_lens, const int32_t *seq_lens, int B, int 
     }
     std::stable_sort(blocks.begin(), blocks.end(), [](const auto &a, const auto &b) { return a.first > b.first; });
     for (const auto &x : blocks) g.blocks.push_back(x.second);
-    // a cluster where that fills SMs that would be idle, and where its CTAs have several tiles each
-    while (!blocks.empty() && g.cluster < va::kWeightClusters && (long long)blocks.size() * g.cluster * 2 <= num_sms &&
-           blocks.front().first >= 4 * g.cluster)
+    // CTAs of a block: as many as leave the longest one half of an SM's share of all tiles, where they have several each
+    // (the last CTAs to end then leave few SMs idle; a CTA's start costs about two tiles)
+    long long tiles = 0;
+    for (const auto &x : blocks) tiles += x.first;
+    while (!blocks.empty() && g.cluster < va::kWeightClusters && blocks.front().first >= 8 * g.cluster &&
+           2ll * blocks.front().first * num_sms > tiles * g.cluster)
         g.cluster *= 2;
 }
 

@@ -5,8 +5,8 @@
 // with the log-sum-exp of the attention itself, so that a token's weights over the keys sum to one.
 //
 // A CTA holds a block of keys in shared memory (one tile of 128 at head_dim 256, else two) and lets the packed rows of
-// q (128 at a time, as chunk attention packs them) pass by: S^T = K Q^T, keys on the tensor memory's lanes.  A thread
-// then owns a key: its sum runs along its own lane, so nothing is exchanged, and -lse of the rows is a broadcast read.
+// q (128 at a time, as chunk attention packs them) pass by: S^T = K Q^T, keys on the tensor memory's lanes.  The sums
+// then run along lanes: four threads share a key until the end, and -lse of the rows is read from shared memory.
 // Half of the attention's products, the same exponentials, no maximum, no second product.
 // Where there are few blocks of keys, a cluster shares one: its CTAs take the tiles of rows in turn and their sums
 // are added in rank order, so that the result does not depend on timing.  No atomics.
@@ -31,8 +31,9 @@ struct Cfg {
     static constexpr int kChunkBytes = 128 * 128;  // 64 elements of 128 rows
     static constexpr int kTileBytes = D / 64 * kChunkBytes;
     static constexpr int kStages = D == 64 ? 8 : D == 128 ? 4 : 2;
-    static constexpr int kSumWarps = 4 * kKeyTiles;
-    static constexpr int kThreads = (kSumWarps + 2) * 32;
+    static constexpr int kSumWarps = 8 * kKeyTiles;
+    static constexpr int kProducerWarp = kSumWarps, kMmaWarp = kSumWarps + 1;  // one issuing warp for each tile of keys
+    static constexpr int kThreads = (kMmaWarp + kKeyTiles) * 32;
     static constexpr int kK = 0;
     static constexpr int kQ = kKeyTiles * kTileBytes;
     static constexpr int kLse = kQ + kStages * kTileBytes;
@@ -120,19 +121,19 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) weights_kernel(const __gr
     const int all = (it.n - t_first + tpt - 1) / tpt;   // tiles of rows
     const int tiles = all > rank ? (all - rank + ranks - 1) / ranks : 0;
     auto tile_t0 = [&](int m) { return t_first + (m * ranks + rank) * tpt; };
-    constexpr int kProducerWarp = C::kSumWarps, kMmaWarp = C::kSumWarps + 1;
+    constexpr int kProducerWarp = C::kProducerWarp, kMmaWarp = C::kMmaWarp;
 
     if (warp == kProducerWarp && lane == 0) {
         prefetch_tensormap(&args.tm_q);
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(bar(kQFull + i), 1);
-            mbar_init(bar(kQEmpty + i), 1);
+            mbar_init(bar(kQEmpty + i), C::kKeyTiles);
         }
         for (int i = 0; i < 2 * C::kKeyTiles; ++i) {
             mbar_init(bar(kSFull + i), 1);
-            mbar_init(bar(kSEmpty + i), 4);
+            mbar_init(bar(kSEmpty + i), 8);
         }
-        mbar_init(bar(kDone), 1);
+        mbar_init(bar(kDone), C::kKeyTiles);
         fence_barrier_init();
     } else if (warp == kMmaWarp) {
         tmem_alloc(bar(kTmemSlot), 256 * C::kKeyTiles);
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) weights_kernel(const __gr
     };
     if (warp < C::kSumWarps) {
         // the block's keys, 16 elements a piece
-        constexpr int kPieces = D / 16, kBatch = 4;
+        constexpr int kPieces = D / 16, kBatch = D == 64 ? 2 : 4;
         constexpr int kTotal = C::kKeyTiles * 128 * kPieces, kStride = C::kSumWarps * 32;
         const unsigned char *pages = static_cast<const unsigned char *>(p.k_pages);
 #pragma unroll 1
@@ -216,95 +217,114 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) weights_kernel(const __gr
         if (lane == 0)
             for (int m = max(0, issued - C::kStages); m < issued; ++m)
                 if (!mbar_wait(bar(kQFull + m % C::kStages), (m / C::kStages) & 1, kWaitNs)) ok = false;
-    } else if (warp == kMmaWarp) {
-        // ------------------------------------------------------------ MMA issue, by the whole warp
+    } else if (warp >= kMmaWarp) {
+        // ------------------------------------------------------------ MMA issue, by a whole warp: its tile of keys
+        const int kt = warp - kMmaWarp;
         constexpr uint32_t id = idesc_f16(128, kRows, 1, 0, 0);
         constexpr uint32_t kHi = smem_desc_hi(1024, 2);
-        const uint32_t klo = smem_desc_lo(sbase + C::kK, 16), qlo = smem_desc_lo(sbase + C::kQ, 16);
-        auto wait = [&](int b, int parity) -> bool {
-            const bool done = __all_sync(0xffffffffu, mbar_wait(bar(b), parity, kWaitNs));
-            tc_fence_after();
-            return done;
-        };
+        const uint32_t klo = smem_desc_lo(sbase + C::kK + kt * C::kTileBytes, 16), qlo = smem_desc_lo(sbase + C::kQ, 16);
         for (int m = 0; m < tiles && ok; ++m) {
-            const int st = m % C::kStages;
-            ok = wait(kQFull + st, (m / C::kStages) & 1);
-            for (int kt = 0; kt < C::kKeyTiles && ok; ++kt) {
-                const int s = kt * 2 + (m & 1);
-                if (m >= 2) ok = wait(kSEmpty + s, ((m >> 1) & 1) ^ 1);
-                if (!ok) break;
-                if (elect_one()) {
+            const int st = m % C::kStages, s = kt * 2 + (m & 1);
+            ok = __all_sync(0xffffffffu, m < 2 ? mbar_wait(bar(kQFull + st), (m / C::kStages) & 1, kWaitNs)
+                                               : mbar_wait2(bar(kQFull + st), (m / C::kStages) & 1, bar(kSEmpty + s),
+                                                            ((m >> 1) & 1) ^ 1, kWaitNs));
+            tc_fence_after();
+            if (!ok) break;
+            if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (kk / 4) * (C::kChunkBytes >> 4) + (kk % 4) * 2;
-                        mma_ss_lo<kHi>(tmem + s * kRows, klo + kt * (C::kTileBytes >> 4) + off,
-                                       qlo + st * (C::kTileBytes >> 4) + off, id, kk > 0);
-                    }
-                    mma_commit(bar(kSFull + s));
-                    if (kt == C::kKeyTiles - 1) mma_commit(bar(kQEmpty + st));
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = (kk / 4) * (C::kChunkBytes >> 4) + (kk % 4) * 2;
+                    mma_ss_lo<kHi>(tmem + s * kRows, klo + off, qlo + st * (C::kTileBytes >> 4) + off, id, kk > 0);
                 }
-                __syncwarp();
+                mma_commit(bar(kSFull + s));
+                mma_commit(bar(kQEmpty + st));
             }
+            __syncwarp();
         }
         if (elect_one()) mma_commit(bar(kDone));
         __syncwarp();
-        if (!wait(kDone, 0)) ok = false;
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(kDone), 0, kWaitNs))) ok = false;
     } else {
         // ------------------------------------------------------------ sums
-        const int kt = warp >> 2, row = (warp & 3) * 32 + lane;
-        const int key = it.key0 + kt * 128 + row;
-        const uint32_t lane_tm = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const int page = page_of(key);
-        float scale = p.sm_scale_log2;
-        if (DT != VA_BF16 && page >= 0)
-            scale *= __ldg(p.k_scale + ((size_t)page * VA_PAGE_SIZE + key % VA_PAGE_SIZE) * p.Hkv + it.kvh);
-        const uint64_t c2 = f2_pack(__float_as_uint(scale), __float_as_uint(scale));
-        float sum = 0.f, lost = 0.f;
+        // A warp has 16 keys; a thread two of them, row x (8 apart), in a quarter of the columns: c and c + 1 of each 8.
+        const int kt = warp >> 3, h = (warp >> 2) & 1, c = 2 * (lane & 3);
+        const uint32_t half_tm = tmem + ((uint32_t)((warp & 3) * 32 + 16 * h) << 16);
+        auto my_row = [&](int x) { return kt * 128 + (warp & 3) * 32 + 16 * h + 8 * x + (lane >> 2); };
+        uint64_t c2[2];
+        float sum[2] = {0.f, 0.f}, lost[2] = {0.f, 0.f};
+        int key[2], page[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            key[x] = it.key0 + my_row(x);
+            page[x] = page_of(key[x]);
+            float scale = p.sm_scale_log2;
+            if (DT != VA_BF16 && page[x] >= 0)
+                scale *= __ldg(p.k_scale + ((size_t)page[x] * VA_PAGE_SIZE + key[x] % VA_PAGE_SIZE) * p.Hkv + it.kvh);
+            c2[x] = f2_pack(__float_as_uint(scale), __float_as_uint(scale));
+        }
         const int last_key = it.key0 + C::kKeyTiles * 128 - 1;  // of the block: both of a CTA's tiles take one view
         for (int m = 0; m < tiles; ++m) {
             const int s = kt * 2 + (m & 1), t0 = tile_t0(m);
             ok = __all_sync(0xffffffffu, mbar_wait(bar(kSFull + s), (m >> 1) & 1, kWaitNs));
             if (!ok) break;
             tc_fence_after();
-            // columns [from, to) of the tile are rows that see this key
+            uint32_t x[64];
+            tmem_ld_16x256b(half_tm + s * kRows, x);
+            tmem_wait_ld();
+            const uint32_t nl = sbase + C::kLse + 4u * ((m % kLseRing) * kRows + c);
             const int to = min(tpt, it.n - t0) * G;
             const bool cut = to < kRows || last_key > before + t0;
-            const int from = max(0, key - before - t0) * G;
-            const uint32_t nl = sbase + C::kLse + 4u * ((m % kLseRing) * kRows);
-            uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t x[32];
-                tmem_ld32(lane_tm + s * kRows + 32 * c, x);
-                tmem_wait_ld();
+            for (int u = 0; u < 16; ++u) {
+                const uint2 l = lds_u2(nl + 32u * u);
+                const uint64_t l2 = f2_pack(l.x, l.y);
 #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const uint4 l = lds_u4(nl + 128u * c + 4u * j);
-                    f2_unpack(f2_fma(f2_pack(x[j], x[j + 1]), c2, f2_pack(l.x, l.y)), x[j], x[j + 1]);
-                    f2_unpack(f2_fma(f2_pack(x[j + 2], x[j + 3]), c2, f2_pack(l.z, l.w)), x[j + 2], x[j + 3]);
-                    if (cut) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (32 * c + j + e < from || 32 * c + j + e >= to) x[j + e] = 0xFF800000u;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[j + e] = __float_as_uint(ex2_approx(__uint_as_float(x[j + e])));
-                    acc[(j / 4) & 1] = f2_add(acc[(j / 4) & 1], f2_pack(x[j], x[j + 1]));
-                    acc[2 + ((j / 4) & 1)] = f2_add(acc[2 + ((j / 4) & 1)], f2_pack(x[j + 2], x[j + 3]));
-                }
+                for (int y = 0; y < 2; ++y)
+                    f2_unpack(f2_fma(f2_pack(x[4 * u + 2 * y], x[4 * u + 2 * y + 1]), c2[y], l2), x[4 * u + 2 * y],
+                              x[4 * u + 2 * y + 1]);
             }
+            // the slot and the tile's lse are read
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kSEmpty + s));
-            uint32_t a, b;
-            f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), a, b);
-            const float y = __fsub_rn(__fadd_rn(__uint_as_float(a), __uint_as_float(b)), lost);
-            const float t = __fadd_rn(sum, y);
-            lost = __fsub_rn(__fsub_rn(t, sum), y);
-            if (!(fabsf(lost) < INFINITY)) lost = 0.f;  // of a sum that is not finite
-            sum = t;
+            if (cut) {  // columns [from, to) of the tile are rows that see the key
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int from = max(0, key[y] - before - t0) * G;
+#pragma unroll
+                    for (int u = 0; u < 16; ++u)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (8 * u + c + e < from || 8 * u + c + e >= to) x[4 * u + 2 * y + e] = 0xFF800000u;
+                }
+            }
+            uint64_t acc[2][2] = {{0ull, 0ull}, {0ull, 0ull}};
+#pragma unroll
+            for (int u = 0; u < 16; ++u)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    uint32_t *z = &x[4 * u + 2 * y];
+                    acc[y][u & 1] = f2_add(acc[y][u & 1], f2_pack(__float_as_uint(ex2_approx(__uint_as_float(z[0]))),
+                                                                  __float_as_uint(ex2_approx(__uint_as_float(z[1])))));
+                }
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                uint32_t a, b;
+                f2_unpack(f2_add(acc[y][0], acc[y][1]), a, b);
+                const float z = __fsub_rn(__fadd_rn(__uint_as_float(a), __uint_as_float(b)), lost[y]);
+                const float t = __fadd_rn(sum[y], z);
+                lost[y] = __fsub_rn(__fsub_rn(t, sum[y]), z);
+                if (!(fabsf(lost[y]) < INFINITY)) lost[y] = 0.f;  // of a sum that is not finite
+                sum[y] = t;
+            }
         }
-        sts_f32(sbase + C::kSum + 4u * tid, page < 0 ? 0.f : sum);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            float z = sum[y];
+            z += __shfl_xor_sync(0xffffffffu, z, 1);
+            z += __shfl_xor_sync(0xffffffffu, z, 2);
+            if ((lane & 3) == 0) sts_f32(sbase + C::kSum + 4u * my_row(y), page[y] < 0 ? 0.f : z);
+        }
     }
     if (!ok) atomicOr(p.flags, kFlagTimeoutBit);
     tc_fence_before();
@@ -314,7 +334,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) weights_kernel(const __gr
         tmem_dealloc(tmem, 256 * C::kKeyTiles);
     }
     if (ranks > 1) cluster_sync();
-    if (rank == 0 && warp < C::kSumWarps) {
+    if (rank == 0 && tid < C::kKeyTiles * 128) {
         const int key = it.key0 + tid;
         float sum = lds_f32(sbase + C::kSum + 4u * tid);
         for (int r = 1; r < ranks; ++r) sum += ld_cluster_f32(smem + C::kSum + 4 * tid, r);
