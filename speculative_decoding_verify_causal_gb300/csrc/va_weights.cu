@@ -23,7 +23,7 @@ namespace {
 
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kRows = kMmaRows;  // packed rows of one tile of q
-constexpr int kLseRing = 16;     // tiles whose lse is held: the stages of q, two tiles of scores, one being written
+constexpr int kLseRing = 16;     // tiles whose lse is held: the stages of q, three tiles of scores, one being written
 
 template <int D>
 struct Cfg {
@@ -40,7 +40,7 @@ struct Cfg {
     static constexpr int kSum = kLse + kLseRing * kRows * 4;
     static constexpr int kBars = kSum + kKeyTiles * 128 * 4;
     static constexpr int kSmem = kBars + 32 * 8 + 1024;
-    static_assert(kSmem <= (int)kMaxSmemPerBlock && kLseRing >= kStages + 3, "shared memory");
+    static_assert(kSmem <= (int)kMaxSmemPerBlock && kLseRing >= kStages + 4, "shared memory");
 };
 
 enum Bar : int {
@@ -171,6 +171,12 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) weights_kernel(const __gr
             }
         }
         static_assert(kTotal % (kBatch * kStride) == 0, "whole batches");
+        // rows of q's tiles that no box fills: with -lse of -inf they add nothing, as long as they are numbers
+        const int full = tpt * G;
+        for (int e = tid; e < C::kStages * (D / 8) * (kRows - full); e += kStride) {
+            const int row = full + e % (kRows - full), u = e / (kRows - full) % (D / 8), st = e / (kRows - full) / (D / 8);
+            sts_u4(sbase + C::kQ + st * C::kTileBytes + (u / 8) * C::kChunkBytes + sw128(row, u % 8), make_uint4(0, 0, 0, 0));
+        }
         fence_proxy_async_smem();
     }
     tc_fence_before();
@@ -263,19 +269,15 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) weights_kernel(const __gr
             c2[x] = f2_pack(__float_as_uint(scale), __float_as_uint(scale));
         }
         const int last_key = it.key0 + C::kKeyTiles * 128 - 1;  // of the block: both of a CTA's tiles take one view
-        for (int m = 0; m < tiles; ++m) {
-            const int s = kt * 2 + (m & 1), t0 = tile_t0(m);
-            ok = __all_sync(0xffffffffu, mbar_wait(bar(kSFull + s), (m >> 1) & 1, kWaitNs));
-            if (!ok) break;
-            tc_fence_after();
-            uint32_t x[64];
-            tmem_ld_16x256b(half_tm + s * kRows, x);
-            tmem_wait_ld();
-            const uint32_t nl = sbase + C::kLse + 4u * ((m % kLseRing) * kRows + c);
+        // Half a tile of columns at a time: while one half's exponentials run, the next one is on its way from the
+        // tensor memory.
+        uint64_t acc[2][2];
+        auto add = [&](int m, int half, uint32_t (&x)[32]) {
+            const int t0 = tile_t0(m);
+            const uint32_t nl = sbase + C::kLse + 4u * ((m % kLseRing) * kRows + 64 * half + c);
             const int to = min(tpt, it.n - t0) * G;
-            const bool cut = to < kRows || last_key > before + t0;
 #pragma unroll
-            for (int u = 0; u < 16; ++u) {
+            for (int u = 0; u < 8; ++u) {
                 const uint2 l = lds_u2(nl + 32u * u);
                 const uint64_t l2 = f2_pack(l.x, l.y);
 #pragma unroll
@@ -283,30 +285,52 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) weights_kernel(const __gr
                     f2_unpack(f2_fma(f2_pack(x[4 * u + 2 * y], x[4 * u + 2 * y + 1]), c2[y], l2), x[4 * u + 2 * y],
                               x[4 * u + 2 * y + 1]);
             }
-            // the slot and the tile's lse are read
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kSEmpty + s));
-            if (cut) {  // columns [from, to) of the tile are rows that see the key
+            if (to < tpt * G || last_key > before + t0) {  // columns [from, to) are rows that see the key
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     const int from = max(0, key[y] - before - t0) * G;
 #pragma unroll
-                    for (int u = 0; u < 16; ++u)
+                    for (int u = 0; u < 8; ++u)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            if (8 * u + c + e < from || 8 * u + c + e >= to) x[4 * u + 2 * y + e] = 0xFF800000u;
+                        for (int e = 0; e < 2; ++e) {
+                            const int col = 64 * half + 8 * u + c + e;
+                            if (col < from || col >= to) x[4 * u + 2 * y + e] = 0xFF800000u;
+                        }
                 }
             }
-            uint64_t acc[2][2] = {{0ull, 0ull}, {0ull, 0ull}};
 #pragma unroll
-            for (int u = 0; u < 16; ++u)
+            for (int u = 0; u < 8; ++u)
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    uint32_t *z = &x[4 * u + 2 * y];
-                    acc[y][u & 1] = f2_add(acc[y][u & 1], f2_pack(__float_as_uint(ex2_approx(__uint_as_float(z[0]))),
-                                                                  __float_as_uint(ex2_approx(__uint_as_float(z[1])))));
+                    const uint64_t e2 = f2_pack(__float_as_uint(ex2_approx(__uint_as_float(x[4 * u + 2 * y]))),
+                                                __float_as_uint(ex2_approx(__uint_as_float(x[4 * u + 2 * y + 1]))));
+                    acc[y][u & 1] = half == 0 && u < 2 ? e2 : f2_add(acc[y][u & 1], e2);
                 }
+        };
+        auto scores_of = [&](int m) {
+            const bool done = __all_sync(0xffffffffu, mbar_wait(bar(kSFull + kt * 2 + (m & 1)), (m >> 1) & 1, kWaitNs));
+            tc_fence_after();
+            return done;
+        };
+        uint32_t x0[32], x1[32];
+        if (tiles > 0) {
+            ok = scores_of(0);
+            if (ok) tmem_ld_16x256b(half_tm + kt * 2 * kRows, x0);
+        }
+        for (int m = 0; m < tiles && ok; ++m) {
+            const int s = kt * 2 + (m & 1);
+            tmem_wait_ld();
+            tmem_ld_16x256b(half_tm + s * kRows + 64, x1);
+            add(m, 0, x0);
+            tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kSEmpty + s));
+            if (m + 1 < tiles) {
+                ok = scores_of(m + 1);
+                if (ok) tmem_ld_16x256b(half_tm + (s ^ 1) * kRows, x0);
+            }
+            add(m, 1, x1);
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
                 uint32_t a, b;
