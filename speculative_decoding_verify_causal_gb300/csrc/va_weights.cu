@@ -187,15 +187,19 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) weights_kernel(const __gr
 
     if (warp == kProducerWarp) {
         // ------------------------------------------------------------ producer: rows of q, and their -lse in units of ln 2
+        int token[4];     // of a tile, of this lane's four rows; past every chunk where there is no such row
+        int64_t place[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 32 * i + lane;
+            token[i] = r < tpt * G ? r / G : 0x40000000;
+            place[i] = (int64_t)(it.q0 + r / G) * p.Hq + it.kvh * G + r % G;
+        }
         auto load_lse = [&](int m, float (&x)[4]) {
             const int t0 = tile_t0(m);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 32 * i + lane, t = t0 + r / G;
-                const bool in = m < tiles && r < tpt * G && t < it.n;
-                const float l = in ? __ldg(p.lse + (size_t)(it.q0 + t) * p.Hq + it.kvh * G + r % G) : INFINITY;
-                x[i] = l == -INFINITY ? -INFINITY : -l * 1.4426950408889634f;  // a row without keys gives nothing
-            }
+            for (int i = 0; i < 4; ++i)
+                x[i] = m < tiles && token[i] < it.n - t0 ? __ldg(p.lse + place[i] + (int64_t)t0 * p.Hq) : INFINITY;
         };
         float next[4];
         load_lse(0, next);
@@ -207,8 +211,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) weights_kernel(const __gr
                 if (!ok) break;
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                sts_f32(sbase + C::kLse + 4u * ((m % kLseRing) * kRows + 32 * i + lane), next[i]);
+            for (int i = 0; i < 4; ++i)  // a row without keys, or none, gives nothing
+                sts_f32(sbase + C::kLse + 4u * ((m % kLseRing) * kRows + 32 * i + lane),
+                        fabsf(next[i]) == INFINITY ? -INFINITY : -next[i] * 1.4426950408889634f);
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive_expect_tx(bar(kQFull + st), (uint32_t)(D / 64 * G * tpt * 128));
