@@ -7,15 +7,21 @@
 // come before the token.  Z is held in two parts, the batch of 16 that holds the maximum and the rest; only the threads
 // that hold the row's maximum read that batch again and sum it without it.
 //
+// The terms are taken as 2^(x log2(e) - C) with C = M log2(e) rounded, one multiplication-addition each, and the sums
+// corrected by 2^(C - M log2(e)), which is near one while M is of ordinary size.  Entries below -1e30 (fp16: -60000;
+// masks) have no weight beside such an M and are raised to that beforehand; a CTA whose maximum is beyond +-4096 (a row
+// of masks, infinity) reads its entries once more and takes each as exp(x - M).
+//
 // The top alternatives are found by a threshold: of the maxima of 32 groups of threads the K-th largest is a lower
 // bound of the K-th largest entry.  Threads whose maximum reaches it go through their entries again (from L2) and list
 // what reaches it, some 30 to 130 entries; those are ranked by counting.  Rows whose list overflows (many equal
 // entries) are searched K times instead.  Order: larger first, equal ones by index, NaN below -inf.
 //
-// A cluster of up to 8 CTAs shares a row where there are few rows; states and lists are merged in rank order.
+// A cluster of up to 8 CTAs shares a row where there are few rows: they write states and lists to the first one, which
+// merges them in rank order.
 #include <math.h>
 
-#include <cstring>
+#include <algorithm>
 
 #include "va_convert.cuh"
 #include "va_internal.h"
@@ -28,16 +34,27 @@ struct LogprobParams {
     const int32_t *tokens;
     float *logprobs, *entropy, *top_logprobs;
     int32_t *ranks, *top_tokens;
-    int vocab, top, cluster;
+    int rows, vocab, top, cluster;
 };
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
-constexpr int kBatch = 16;   // entries whose maximum is taken at once
-constexpr int kList = 4096;  // candidates: more than a sorted row has (32 groups x 16 threads x 8 entries)
 constexpr int kMaxTop = 32;
+constexpr int kMaxCluster = 8;
+constexpr int kThreads = 512, kWarps = kThreads / 32;  // and a warp that loads
+constexpr int kVecs = 4;                               // 16-byte vectors of a thread in a chunk
+constexpr int kChunk = kThreads * kVecs;               // vectors
+constexpr int kStages = 3;
+constexpr int kCtas = 2;     // of an SM
+constexpr int kList = 1024;  // candidates
+constexpr int kTake = 16;    // chunks between takes of the packed counts
+constexpr uint32_t kRingBytes = kStages * kChunk * 16;
+constexpr uint64_t kWaitNs = 2000000000ull;
+static_assert(kWarps * 32 <= kList && kTake * 4 * kVecs <= 256, "bounds go through the list; packed counts are exact");
+
+// Beyond this a maximum has too few bits behind the point for C; see above.  Reference points below -4 kWide are
+// replaced by 0: their entries have no weight then, and none beside a maximum that is not below -kWide either.
+constexpr float kWide = 4096.f;
 
 typedef unsigned long long u64;
 
@@ -62,91 +79,171 @@ __device__ __forceinline__ u64 key_of(float x, int i) { return (u64)order_of(x) 
 // exp(d) for d <= 0, |relative error| about 2^-22 + 2^-24 |d|: 0 for d of -1e30
 __device__ __forceinline__ float exp_neg(float d) { return ex2_approx(d * 1.4426950408889634f); }
 
-// 16 bytes of the row as floats.
+// The bits of the next value below (a type of `sign` + 1 bits; not -0).
+__device__ __forceinline__ uint32_t next_below(uint32_t b, int sign) {
+    return b >> sign ? b + 1 : b ? b - 1 : (1u << sign) + 1;
+}
+
+// What a type needs: kN entries in 16 bytes; the larger of packed entries, NaN left out, and the larger of a word's; a word
+// with what is below a floor raised to it, which is finite; entries as floats; a bound, the next value below one (so
+// that "at least x" is "greater than below(x)"), and a count of entries that are greater than a bound.
 template <typename T>
-struct Vec;
+struct Type;
 template <>
-struct Vec<float> {
+struct Type<float> {
     static constexpr int kN = 4;
-    static __device__ __forceinline__ void unpack(const uint4 &v, float *x) {
-        x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
-    }
+    static constexpr uint32_t kLowest = 0xFF800000u;
     static __device__ __forceinline__ float one(const float *p) { return __ldg(p); }
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    }
+    static __device__ __forceinline__ float top(uint32_t w) { return __uint_as_float(w); }
+    static __device__ __forceinline__ uint32_t raise(uint32_t w) { return __float_as_uint(max_nan(__uint_as_float(w), -1e30f)); }
+    static __device__ __forceinline__ void floats(const uint32_t (&w)[4], float *x) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(w[i]);
+    }
+    static __device__ __forceinline__ uint32_t bound(float x) { return __float_as_uint(x + 0.f); }
+    static __device__ __forceinline__ uint32_t below(uint32_t b) { return next_below(b, 31); }
+    struct Count {
+        int n = 0;
+        __device__ __forceinline__ void add(const uint32_t (&w)[4], uint32_t bound) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) n += __uint_as_float(w[i]) > __uint_as_float(bound);
+        }
+        __device__ __forceinline__ int take() {
+            const int t = n;
+            n = 0;
+            return t;
+        }
+    };
 };
 template <>
-struct Vec<__nv_bfloat16> {
+struct Type<__nv_bfloat16> {
     static constexpr int kN = 8;
-    static __device__ __forceinline__ void unpack(const uint4 &v, float *x) {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            x[2 * i] = bf16_bits_to_float(w[i] & 0xFFFFu), x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+    static constexpr uint32_t kLowest = 0xFF80FF80u;
     static __device__ __forceinline__ float one(const __nv_bfloat16 *p) {
         return bf16_bits_to_float(__ldg(reinterpret_cast<const unsigned short *>(p)));
     }
-};
-template <>
-struct Vec<__half> {
-    static constexpr int kN = 8;
-    static __device__ __forceinline__ void unpack(const uint4 &v, float *x) {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-            x[2 * i] = f.x, x[2 * i + 1] = f.y;
-        }
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+        uint32_t d;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
     }
-    static __device__ __forceinline__ float one(const __half *p) { return __half2float(*p); }
-};
-
-// The entries of one CTA: the row's 16-byte vectors [v0, v1), dealt to the threads one by one, and single entries: of
-// those before the first vector boundary the first `head`, from `tail0` on the last ones.
-template <typename T>
-struct Slice {
-    static constexpr int kN = Vec<T>::kN;
-    static constexpr int kVecs = kBatch / kN;  // vectors of a batch
-    const T *row;
-    const uint4 *body;
-    int head, v0, v1, tail0, tail1;  // entries of vector v: head_all + v * kN ..
-    int head_all;
-
-    // calls f(x[16], first index of the batch's vectors, batch number, count) for each batch of this thread
-    template <typename F>
-    __device__ __forceinline__ void batches(F f) const {
-        constexpr int kLoads = 64 / 16;  // vectors in flight
-        for (int v = v0 + (int)threadIdx.x, n = 0; v < v1; v += kLoads * kThreads, n += kLoads / kVecs) {
-            uint4 raw[kLoads];
+    static __device__ __forceinline__ float top(uint32_t w) {
+        return fmaxf(bf16_bits_to_float(w & 0xFFFFu), __uint_as_float(w & 0xFFFF0000u));
+    }
+    static __device__ __forceinline__ uint32_t raise(uint32_t w) {
+        uint32_t d;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(w), "r"(0xF14AF14Au));
+        return d;
+    }
+    static __device__ __forceinline__ void floats(const uint32_t (&w)[4], float *x) {
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-                if (v + i * kThreads < v1) raw[i] = __ldg(body + v + i * kThreads);
+        for (int i = 0; i < 4; ++i)
+            x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+    static __device__ __forceinline__ uint32_t bound(float x) { return (__float_as_uint(x + 0.f) >> 16) * 0x10001u; }
+    static __device__ __forceinline__ uint32_t below(uint32_t b) { return next_below(b & 0xFFFFu, 15) * 0x10001u; }
+    struct Count {
+        uint32_t n = 0;  // two counts in bf16, exact up to 256
+        __device__ __forceinline__ void add(const uint32_t (&w)[4], uint32_t bound) {
 #pragma unroll
-            for (int b = 0; b < kLoads / kVecs; ++b) {
-                if (v + b * kVecs * kThreads >= v1) break;
-                float x[kBatch];
-#pragma unroll
-                for (int i = 0; i < kVecs; ++i) {
-                    if (v + (b * kVecs + i) * kThreads < v1) {
-                        Vec<T>::unpack(raw[b * kVecs + i], x + i * kN);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < kN; ++j) x[i * kN + j] = -INFINITY;
-                    }
-                }
-                f(x, v + b * kVecs * kThreads, n + b);
+            for (int i = 0; i < 4; ++i) {
+                uint32_t m;
+                asm("set.gt.bf16x2.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(w[i]), "r"(bound));
+                asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(n) : "r"(m), "r"(0x3F803F80u));
             }
         }
+        __device__ __forceinline__ int take() {
+            const int t = (int)__uint_as_float(n << 16) + (int)__uint_as_float(n & 0xFFFF0000u);
+            n = 0;
+            return t;
+        }
+    };
+};
+template <>
+struct Type<__half> {
+    static constexpr int kN = 8;
+    static constexpr uint32_t kLowest = 0xFC00FC00u;
+    static __device__ __forceinline__ float one(const __half *p) { return __half2float(*p); }
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+        uint32_t d;
+        asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
     }
-    // entry j of a batch whose first vector is v; kN-th vectors are kThreads apart.  A missing vector's entries: past v1
-    __device__ __forceinline__ int index(int v, int j) const { return head_all + (v + j / kN * kThreads) * kN + j % kN; }
-    __device__ __forceinline__ bool has(int v, int j) const { return v + j / kN * kThreads < v1; }
-    // the first vector of batch n of this thread
-    __device__ __forceinline__ int first_vector(int n) const { return v0 + (int)threadIdx.x + n * kVecs * kThreads; }
+    static __device__ __forceinline__ float2 pair(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
+    static __device__ __forceinline__ float top(uint32_t w) { return fmaxf(pair(w).x, pair(w).y); }
+    static __device__ __forceinline__ uint32_t raise(uint32_t w) {
+        uint32_t d;
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(w), "r"(0xFBFFFBFFu));
+        return d;
+    }
+    static __device__ __forceinline__ void floats(const uint32_t (&w)[4], float *x) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[2 * i] = pair(w[i]).x, x[2 * i + 1] = pair(w[i]).y;
+    }
+    static __device__ __forceinline__ uint32_t bound(float x) {
+        const __half h = __float2half_rn(x + 0.f);  // it is one
+        return *reinterpret_cast<const unsigned short *>(&h) * 0x10001u;
+    }
+    static __device__ __forceinline__ uint32_t below(uint32_t b) { return next_below(b & 0xFFFFu, 15) * 0x10001u; }
+    struct Count {
+        uint32_t n = 0;  // two counts in fp16
+        __device__ __forceinline__ void add(const uint32_t (&w)[4], uint32_t bound) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t m;
+                asm("set.gt.f16x2.f16x2 %0, %1, %2;" : "=r"(m) : "r"(w[i]), "r"(bound));
+                asm("add.rn.f16x2 %0, %1, %0;" : "+r"(n) : "r"(m));
+            }
+        }
+        __device__ __forceinline__ int take() {
+            const int t = (int)pair(n).x + (int)pair(n).y;
+            n = 0;
+            return t;
+        }
+    };
+};
+
+// The entries of a row that a CTA has: the row's vectors [v0, v1), in chunks, each dealt to the threads one by one, and
+// single entries: those before the row's first 16-byte boundary and those behind its last whole vector.
+template <typename T>
+struct Slice {
+    static constexpr int kN = Type<T>::kN;
+    const T *row;
+    const uint4 *body;
+    int lead;  // entries before the first vector
+    int head, v0, v1, tail0, tail1;
+
+    __device__ __forceinline__ Slice(const LogprobParams &p, int64_t n, int rank) {
+        row = static_cast<const T *>(p.logits) + n * p.stride;
+        const int skip = (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (int)sizeof(T);
+        lead = min(skip, p.vocab);
+        body = reinterpret_cast<const uint4 *>(row + lead);
+        const int vectors = (p.vocab - lead) / kN, per = (vectors + p.cluster - 1) / p.cluster;
+        v0 = min(vectors, rank * per), v1 = min(vectors, v0 + per);
+        head = rank == 0 ? lead : 0;
+        tail0 = lead + vectors * kN, tail1 = rank == p.cluster - 1 ? p.vocab : 0;
+    }
+    __device__ __forceinline__ int chunks() const { return (v1 - v0 + kChunk - 1) / kChunk; }
+    __device__ __forceinline__ int vector(int c, int i) const { return v0 + c * kChunk + i * kThreads + (int)threadIdx.x; }
+    __device__ __forceinline__ int index(int v) const { return lead + v * kN; }  // of its first entry
+    // calls f(words, vector) for each vector of this thread, from global memory
+    template <typename F>
+    __device__ __forceinline__ void vectors(F f) const {
+#pragma unroll 1
+        for (int v = v0 + (int)threadIdx.x; v < v1; v += kThreads) {
+            const uint4 x = __ldg(body + v);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            f(w, v);
+        }
+    }
     // calls f(index) for each single entry of this thread
     template <typename F>
     __device__ __forceinline__ void singles(F f) const {
-        for (int i = threadIdx.x; i < head; i += kThreads) f(i);
-        for (int i = tail0 + (int)threadIdx.x; i < tail1; i += kThreads) f(i);
+        if ((int)threadIdx.x < head) f((int)threadIdx.x);  // at most seven each
+        if (tail0 + (int)threadIdx.x < tail1) f(tail0 + (int)threadIdx.x);
     }
 };
 
@@ -160,336 +257,438 @@ __device__ __forceinline__ State merge(State a, State b) {
         a = b, b = t;
     }
     const bool none = b.m == -INFINITY;
-    const float d = none ? 0.f : b.m - a.m, e = none ? 0.f : exp_neg(max_nan(d, -1e30f));
+    const float d = none ? 0.f : max_nan(b.m - a.m, -1e30f), e = none ? 0.f : exp_neg(d);
     const float w = 1.f + b.z;
-    a.s += none ? b.s * 0.f : e * (b.s + max_nan(d, -1e30f) * w);
+    a.s += none ? b.s * 0.f : e * (b.s + d * w);
     a.z += none ? b.z * 0.f : e * w;  // NaN stays
     return a;
 }
 
-template <typename F>
-__device__ __forceinline__ float warp_sum(float x, F) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
+// A thread's running state: the maximum, and the sums of the entries against it in two parts, the chunk that holds it
+// (which counts the maximum itself, 1) and the rest.
+struct Running {
+    float m = -INFINITY, rest = 0.f, held = 0.f, s = 0.f;
+    int chunk = 0;  // that chunk; ~i: the single entry i
+    __device__ __forceinline__ void move(float to, int c) {
+        const float d = m == -INFINITY ? -1e30f : fmaxf(m - to, -1e30f), e = exp_neg(d);
+        const float w = rest + held;
+        s = e * (s + d * w);
+        rest = e * w;
+        held = 0.f;
+        m = to;
+        chunk = c;
+    }
+};
+
+// An entry by itself.
+__device__ __forceinline__ void take_one(Running &r, float x, int i) {
+    if (x > r.m) {
+        r.move(x, ~i);
+        r.held = 1.f;
+    } else {
+        const float d = max_nan(x - (r.m == -INFINITY ? 0.f : r.m), -1e30f), e = exp_neg(d);
+        r.rest += e;
+        r.s += e * d;
+    }
 }
 
+// What the CTAs of a cluster give to the first one.
+struct Given {
+    State state;
+    int before;
+    u64 best[kMaxTop];
+};
+
+__device__ __forceinline__ void sync_rows() { named_bar_sync(1, kThreads); }  // the threads that take entries
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const LogprobParams p) {
+__global__ void __launch_bounds__(kThreads + 32, kCtas) logprobs_kernel(const LogprobParams p) {
+    using Ty = Type<T>;
+    constexpr int kN = Ty::kN;
+    extern __shared__ __align__(128) unsigned char ring[];
+    __shared__ __align__(8) uint64_t bars[2 * kStages];
     __shared__ float red_m[kWarps], red_z[kWarps], red_s[kWarps];
-    __shared__ int red_c[kWarps], red_w[kWarps];
-    __shared__ u64 group[32], list[kList], best[kMaxTop];
-    __shared__ int count;
-    __shared__ float out_m, out_z, out_s;
-    __shared__ int out_c;
+    __shared__ int red_c[kWarps], red_w[kWarps], count, threads, broken;
+    __shared__ u64 best_of[kWarps], list[kList];
+    __shared__ unsigned short who[kThreads];
+    __shared__ Given given[kMaxCluster];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ranks = p.cluster, rank = blockIdx.x % ranks, V = p.vocab, K = p.top;
-    const int64_t n = blockIdx.x / ranks;
+    const int n0 = blockIdx.x / ranks, step = gridDim.x / ranks;
+    auto full = [&](int i) { return smem_u32(&bars[i]); };
+    auto empty = [&](int i) { return smem_u32(&bars[kStages + i]); };
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) mbar_init(full(i), 1), mbar_init(empty(i), kWarps);
+        fence_barrier_init();
+        broken = 0;
+    }
+    __syncthreads();
+    if (ranks > 1) cluster_arrive();  // this CTA has begun: see cluster_wait below
     griddep_wait();
 
-    Slice<T> sl;
-    constexpr int kN = Slice<T>::kN;
-    sl.row = static_cast<const T *>(p.logits) + n * p.stride;
-    const int skip = (int)((16 - (reinterpret_cast<uintptr_t>(sl.row) & 15)) & 15) / (int)sizeof(T);
-    sl.head_all = min(skip, V);
-    sl.body = reinterpret_cast<const uint4 *>(sl.row + sl.head_all);
-    const int vectors = (V - sl.head_all) / kN, per = (vectors + ranks - 1) / ranks;
-    sl.v0 = min(vectors, rank * per), sl.v1 = min(vectors, sl.v0 + per);
-    sl.head = rank == 0 ? sl.head_all : 0;
-    sl.tail0 = sl.head_all + vectors * kN, sl.tail1 = rank == ranks - 1 ? V : 0;
+    if (warp == kWarps) {
+        // ------------------------------------------------------------ loads, ahead into the next row
+        int g = 0;
+        if (lane == 0) {
+            bool ok = true;
+            for (int n = n0; n < p.rows && ok; n += step) {
+                const Slice<T> sl(p, n, rank);
+                for (int v = sl.v0; v < sl.v1 && ok; v += kChunk, ++g) {
+                    const int st = g % kStages;
+                    if (g >= kStages) ok = mbar_wait(empty(st), (g / kStages - 1) & 1, kWaitNs);
+                    if (!ok) break;
+                    const uint32_t bytes = 16u * min(kChunk, sl.v1 - v);
+                    mbar_arrive_expect_tx(full(st), bytes);
+                    bulk_load(smem_u32(ring) + 16u * kChunk * st, sl.body + v, bytes, full(st));
+                }
+            }
+            if (!ok) broken = 1;
+        }
+        __syncwarp();
+        if (ranks > 1) {
+            cluster_wait();
+            cluster_sync();
+        }
+        return;
+    }
 
-    const int token = p.tokens[n];
-    const bool known = token >= 0 && token < V;
-    const float mine = known ? Vec<T>::one(sl.row + token) : 0.f;
-    const uint32_t mine_order = order_of(mine);
-    // entries before the token count where they are not less, those behind it where they are greater; "not less than
-    // mine" is "greater than the next float below"; NaN and -inf, which have none, by their order
-    const bool by_order = !(mine > -INFINITY);
-    const float below = by_order ? 0.f : mine == 0.f ? -__int_as_float(1) : value_of(mine_order - 1);  // 0 is both zeros
-    auto precedes = [&](float x, int i) { const uint32_t o = order_of(x); return o > mine_order || (o == mine_order && i < token); };
+    int g = 0;
+    int token = n0 < p.rows ? __ldg(p.tokens + n0) : -1;
+    float mine = token >= 0 && token < V ? Ty::one(static_cast<const T *>(p.logits) + n0 * p.stride + token) : 0.f;
+    for (int n = n0; n < p.rows; n += step) {
+        const Slice<T> sl(p, n, rank);
+        const bool known = token >= 0 && token < V;
+        const int after = n + step, next_token = after < p.rows ? __ldg(p.tokens + after) : -1;
+        // entries before the token come before it where they are at least its logit, those behind it where they are
+        // greater; beside the lowest and NaN by their order
+        const bool by_order = known && !(mine > -INFINITY);
+        const uint32_t bound_behind = Ty::bound(by_order || !known ? 0.f : mine), bound_before = Ty::below(bound_behind);
+        const uint32_t mine_order = order_of(mine);
+        auto precedes = [&](float x, int i) {
+            const uint32_t o = order_of(x);
+            return o > mine_order || (o == mine_order && i < token);
+        };
+        // vectors below this are before the token; its own counts as behind, but for the entries up to it
+        const int token_vector = token < sl.lead ? -1 : (token - sl.lead) / kN;
+        int before = 0;
+        if (known && !by_order && tid < kN && token_vector >= sl.v0 && token_vector < sl.v1 && sl.index(token_vector) + tid < token)
+            before = Ty::one(sl.row + sl.index(token_vector) + tid) == mine;
+        if (tid == 0) count = threads = 0;
 
-    float m = -INFINITY, rest = 0.f, held = 0.f, s = 0.f;  // held: the sum of the batch with the maximum, which counts 1
-    int held_batch = -1, held_at = 0, before = 0;          // and the vector of it that has the maximum; -1: entry held_at
-    sl.batches([&](const float (&x)[kBatch], int v, int b) {
-        constexpr int kVecs = Slice<T>::kVecs;
-        float mx[kVecs];  // of each vector
-        float mb = -INFINITY;
+        Running r;
+        typename Ty::Count counted;
+        const int chunks = sl.chunks();
+        auto take_chunk = [&](int c) {
+            const uint32_t at = smem_u32(ring) + 16u * (kChunk * (g % kStages) + tid);
+            const bool whole = sl.v1 - sl.v0 - c * kChunk >= kChunk;
+            uint32_t w[kVecs][4], top[4] = {Ty::kLowest, Ty::kLowest, Ty::kLowest, Ty::kLowest};
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            mx[i] = x[i * kN];
+            for (int i = 0; i < kVecs; ++i) {
+                const bool has = whole || sl.vector(c, i) < sl.v1;
+                const uint4 x = has ? lds_u4(at + 16u * kThreads * i) : make_uint4(Ty::kLowest, Ty::kLowest, Ty::kLowest, Ty::kLowest);
+                w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
+            }
 #pragma unroll
-            for (int j = 1; j + 1 < kN; j += 2) mx[i] = fmax3(mx[i], x[i * kN + j], x[i * kN + j + 1]);
-            mx[i] = fmaxf(mx[i], x[i * kN + kN - 1]);
-            mb = fmaxf(mb, mx[i]);
+            for (int i = 0; i < kVecs; ++i) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top[k] = Ty::larger(top[k], w[i][k]);
+                counted.add(w[i], sl.vector(c, i) < token_vector ? bound_before : bound_behind);
+            }
+            const float mb = Ty::top(Ty::larger(Ty::larger(top[0], top[1]), Ty::larger(top[2], top[3])));
+            const bool moved = mb > r.m;
+            if (moved) r.move(mb, c);
+            // 2^(x log2(e) - C) = exp(x - m) 2^off, off what C is below m log2(e)
+            const float m = r.m < -4.f * kWide ? 0.f : r.m;
+            const float l2e = 1.4426950408889634f, C = m * l2e;
+            const float off = fmaf(m, l2e, -C);
+            const uint64_t l2 = f2_pack(__float_as_uint(l2e), __float_as_uint(l2e));
+            const uint64_t c2 = f2_pack(__float_as_uint(-C), __float_as_uint(-C));
+            float z, s;
+#pragma unroll 1
+            for (bool again = false;; again = true) {
+                uint64_t z2[2] = {0ull, 0ull}, s2[2] = {0ull, 0ull};
+#pragma unroll
+                for (int i = 0; i < kVecs; ++i) {
+                    float x[kN];
+                    Ty::floats(w[i], x);
+#pragma unroll
+                    for (int j = 0; j < kN; j += 2) {
+                        const uint64_t t2 = f2_fma(f2_pack(__float_as_uint(x[j]), __float_as_uint(x[j + 1])), l2, c2);
+                        uint32_t a, b;
+                        f2_unpack(t2, a, b);
+                        const uint64_t e2 = f2_pack(__float_as_uint(ex2_approx(__uint_as_float(a))),
+                                                    __float_as_uint(ex2_approx(__uint_as_float(b))));
+                        z2[(j / 2) & 1] = f2_add(z2[(j / 2) & 1], e2);
+                        s2[(j / 2) & 1] = f2_fma(e2, t2, s2[(j / 2) & 1]);
+                    }
+                }
+                uint32_t a, b;
+                f2_unpack(f2_add(z2[0], z2[1]), a, b);
+                z = __uint_as_float(a) + __uint_as_float(b);
+                f2_unpack(f2_add(s2[0], s2[1]), a, b);
+                s = __uint_as_float(a) + __uint_as_float(b);
+                if (s == s || again) break;
+                // 0 * -inf, or NaN
+#pragma unroll
+                for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[i][j] = Ty::raise(w[i][j]);
+            }
+            const float by = 1.f - 0.69314718f * off;  // 2^-off but for 2^-24: off is 2^-12 at most for kWide
+            if (moved)
+                r.held = z * by;
+            else
+                r.rest += z * by;
+            r.s += (s - off * z) * (0.69314718f * by);
+        };
+        for (int c = 0; c < chunks; ++c, ++g) {
+            const int st = g % kStages;
+            if (!mbar_wait(full(st), (g / kStages) & 1, kWaitNs)) {
+                broken = 1;
+                break;
+            }
+            take_chunk(c);
+            if (c % kTake == kTake - 1) before += counted.take();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty(st));
         }
-        const bool moved = mb > m;
-        if (moved) {
-            const float d = m == -INFINITY ? -1e30f : fmaxf(m - mb, -1e30f), e = exp_neg(d);
-            const float w = rest + held;
-            s = e * (s + d * w);
-            rest = e * w;
-            m = mb;
-            held_batch = b;
-            held_at = 0;
-#pragma unroll
-            for (int i = kVecs - 1; i > 0; --i) held_at = mx[i] == mb ? i : held_at;
-            if (mx[0] == mb) held_at = 0;
-        }
-        const float ref = m == -INFINITY ? 0.f : m;
-        const uint64_t nm2 = f2_pack(__float_as_uint(-ref), __float_as_uint(-ref));
-        const uint32_t l2e = __float_as_uint(1.4426950408889634f);
-        const uint64_t l2 = f2_pack(l2e, l2e);
-        uint64_t z2[2] = {0ull, 0ull}, s2[2] = {0ull, 0ull};
-#pragma unroll
-        for (int j = 0; j < kBatch; j += 2) {
-            uint32_t a, c, ea, ec;
-            f2_unpack(f2_add(f2_pack(__float_as_uint(x[j]), __float_as_uint(x[j + 1])), nm2), a, c);
-            a = __float_as_uint(max_nan(__uint_as_float(a), -1e30f));  // -inf: 0 times it is to be 0
-            c = __float_as_uint(max_nan(__uint_as_float(c), -1e30f));
-            const uint64_t d2 = f2_pack(a, c);
-            f2_unpack(f2_mul(d2, l2), ea, ec);
-            const uint64_t e2 = f2_pack(__float_as_uint(ex2_approx(__uint_as_float(ea))),
-                                        __float_as_uint(ex2_approx(__uint_as_float(ec))));
-            z2[(j / 2) & 1] = f2_add(z2[(j / 2) & 1], e2);
-            s2[(j / 2) & 1] = f2_fma(e2, d2, s2[(j / 2) & 1]);
-        }
-        uint32_t a, c;
-        f2_unpack(f2_add(z2[0], z2[1]), a, c);
-        const float zb = __uint_as_float(a) + __uint_as_float(c);
-        if (moved)
-            held = zb;
-        else
-            rest += zb;
-        f2_unpack(f2_add(s2[0], s2[1]), a, c);
-        s += __uint_as_float(a) + __uint_as_float(c);
+        before += counted.take();
         if (by_order) {
-#pragma unroll 1
-            for (int j = 0; j < kBatch; ++j) {
-                float y = x[0];
-#pragma unroll
-                for (int q = 1; q < kBatch; ++q) y = q == j ? x[q] : y;
-                before += known && sl.has(v, j) && precedes(y, sl.index(v, j));
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < Slice<T>::kVecs; ++i) {
-                const int first = sl.index(v, i * kN);
-                if (first <= token && token < first + kN) {
-#pragma unroll
-                    for (int j = 0; j < kN; ++j) before += x[i * kN + j] > (first + j < token ? below : mine);
-                } else {
-                    const float t = first < token ? below : mine;
-#pragma unroll
-                    for (int j = 0; j < kN; ++j) before += x[i * kN + j] > t;
-                }
-            }
-        }
-    });
-    sl.singles([&](int i) {
-        const float x = Vec<T>::one(sl.row + i);
-        if (x > m) {
-            const float d = m == -INFINITY ? -1e30f : fmaxf(m - x, -1e30f), e = exp_neg(d);
-            const float w = rest + held;
-            s = e * (s + d * w);
-            rest = e * w;
-            held = 1.f;
-            m = x;
-            held_batch = -1, held_at = i;
-        } else {
-            const float d = max_nan(x - (m == -INFINITY ? 0.f : m), -1e30f), e = exp_neg(d);
-            rest += e;
-            s += e * d;
-        }
-        before += known && precedes(x, i);
-    });
-
-    // the CTA's maximum
-    float M = m;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (lane == 0) red_m[warp] = M;
-    if (tid == 0) count = 0;
-    u64 top_key = 0, sure_key = 0;  // bounds of the key of the thread's maximum: its index is somewhere in the vector
-    if (K > 0) {
-        if (m > -INFINITY) {
-            const int first = held_batch < 0 ? held_at : sl.index(sl.first_vector(held_batch), held_at * kN);
-            top_key = key_of(m, first);
-            sure_key = key_of(m, held_batch < 0 ? first : first + kN - 1);
-        } else if (sl.has(sl.first_vector(0), 0)) {  // nothing but -inf, or NaN
-            const int first = sl.index(sl.first_vector(0), 0);
-            const float least = rest == rest ? -INFINITY : rest;
-            top_key = key_of(-INFINITY, first);
-            sure_key = key_of(least, first + kN - 1);
-        }
-        u64 g = sure_key;
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) {
-            const u64 other = __shfl_xor_sync(0xffffffffu, g, o);
-            g = other > g ? other : g;
-        }
-        if ((lane & 15) == 0) group[tid / 16] = g;
-    }
-    __syncthreads();
-    M = red_m[0];
-#pragma unroll
-    for (int i = 1; i < kWarps; ++i) M = fmaxf(M, red_m[i]);
-
-    // sums against the CTA's maximum; those who hold it sum its batch again without it
-    const bool holds = m == M && M > -INFINITY;
-    float z = rest;
-    if (holds) {
-        if (held_batch >= 0) {
-            const int v = sl.first_vector(held_batch);
-            bool out = false;
-#pragma unroll 1
-            for (int i = 0; i < Slice<T>::kVecs; ++i) {
-                if (v + i * kThreads >= sl.v1) break;
+            before = 0;
+            sl.vectors([&](const uint32_t (&w)[4], int v) {
                 float x[kN];
-                Vec<T>::unpack(__ldg(sl.body + v + i * kThreads), x);
+                Ty::floats(w, x);
 #pragma unroll
-                for (int j = 0; j < kN; ++j) {
-                    if (!out && x[j] == m)
-                        out = true;
-                    else
-                        z += exp_neg(max_nan(x[j] - m, -1e30f));
+                for (int j = 0; j < kN; ++j) before += precedes(x[j], sl.index(v) + j);
+            });
+        }
+        sl.singles([&](int i) {
+            const float x = Ty::one(sl.row + i);
+            take_one(r, x, i);
+            before += known && precedes(x, i);
+        });
+
+        // The CTA's maximum.  A thread's largest key is at least `sure`: its maximum's index is somewhere in its chunk,
+        // and without one above -inf it has entries of -inf or NaN, or none.  Group i has lane i of each warp.
+        float M = r.m;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        if (lane == 0) red_m[warp] = M;
+        u64 top_key = key_of(-INFINITY, 0);
+        if (r.m > -INFINITY) top_key = key_of(r.m, r.chunk < 0 ? ~r.chunk : sl.index(sl.vector(r.chunk, 0)));
+        if (K > 0) {
+            u64 sure = 0;
+            if (r.m > -INFINITY)
+                sure = key_of(r.m, r.chunk < 0 ? ~r.chunk : sl.index(sl.vector(r.chunk, kVecs)));
+            else if (sl.vector(0, 0) < sl.v1 || tid < sl.head || sl.tail0 + tid < sl.tail1)
+                sure = key_of(r.rest == r.rest ? -INFINITY : __uint_as_float(0x7FFFFFFFu), 0x7FFFFFFF);
+            list[tid] = sure;
+        }
+        sync_rows();
+        M = red_m[0];
+#pragma unroll
+        for (int i = 1; i < kWarps; ++i) M = fmaxf(M, red_m[i]);
+        u64 bound = 0;
+        if (K > 0) {
+            // the K-th largest of the groups' bounds (0 where fewer groups have one: then everything is a candidate)
+            u64 mine_g = list[lane];
+#pragma unroll
+            for (int i = 1; i < kWarps; ++i) mine_g = max(mine_g, list[32 * i + lane]);
+            int above = 0;
+#pragma unroll 8
+            for (int i = 0; i < 32; ++i) {
+                const u64 other = __shfl_sync(0xffffffffu, mine_g, i);
+                above += other > mine_g || (other == mine_g && i < lane);
+            }
+            bound = __shfl_sync(0xffffffffu, mine_g, __ffs(__ballot_sync(0xffffffffu, above == K - 1)) - 1);
+            if (sl.vector(0, 0) < sl.v1 && top_key >= bound) who[atomicAdd(&threads, 1)] = (unsigned short)tid;
+            if (tid < kMaxTop) given[0].best[tid] = 0;
+        }
+        if (!(fabsf(M) <= kWide)) {  // alike in the CTA: every entry by itself
+            r = Running();
+            sl.vectors([&](const uint32_t (&w)[4], int v) {
+                float x[kN];
+                Ty::floats(w, x);
+#pragma unroll
+                for (int j = 0; j < kN; ++j) take_one(r, x[j], sl.index(v) + j);
+            });
+            sl.singles([&](int i) { take_one(r, Ty::one(sl.row + i), i); });
+        }
+
+        // sums against the CTA's maximum; those who hold it sum its chunk again without it
+        const bool holds = r.m == M && M > -INFINITY;
+        float z = r.rest, s = r.s;
+        if (holds) {
+            if (r.chunk >= 0) {
+                uint4 y[kVecs];
+#pragma unroll
+                for (int i = 0; i < kVecs; ++i)
+                    if (sl.vector(r.chunk, i) < sl.v1) y[i] = __ldg(sl.body + sl.vector(r.chunk, i));
+                bool out = false;
+#pragma unroll
+                for (int i = 0; i < kVecs; ++i) {
+                    if (sl.vector(r.chunk, i) >= sl.v1) continue;
+                    const uint32_t w[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+                    float x[kN];
+                    Ty::floats(w, x);
+#pragma unroll
+                    for (int j = 0; j < kN; ++j) {
+                        const bool it = !out && x[j] == M;
+                        out |= it;
+                        z += it ? 0.f : exp_neg(max_nan(x[j] - M, -1e30f));
+                    }
                 }
             }
+        } else if (r.m > -INFINITY) {
+            const float d = max_nan(r.m - M, -1e30f), e = exp_neg(d), w = r.rest + r.held;
+            s = e * (s + d * w);
+            z = e * w;
+        } else {
+            z += r.held;  // nothing, or NaN
         }
-    } else if (m > -INFINITY) {
-        const float d = max_nan(m - M, -1e30f), e = exp_neg(d), w = rest + held;
-        s = e * (s + d * w);
-        z = e * w;
-    } else {
-        z += held;  // nothing, or NaN
-    }
-    int c = before, w = holds;
+        int c = before, w = holds;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        z += __shfl_xor_sync(0xffffffffu, z, o);
-        s += __shfl_xor_sync(0xffffffffu, s, o);
-        c += __shfl_xor_sync(0xffffffffu, c, o);
-        w += __shfl_xor_sync(0xffffffffu, w, o);
-    }
-    if (lane == 0) red_z[warp] = z, red_s[warp] = s, red_c[warp] = c, red_w[warp] = w;
+        for (int o = 16; o > 0; o >>= 1) {
+            z += __shfl_xor_sync(0xffffffffu, z, o);
+            s += __shfl_xor_sync(0xffffffffu, s, o);
+            c += __shfl_xor_sync(0xffffffffu, c, o);
+            w += __shfl_xor_sync(0xffffffffu, w, o);
+        }
+        if (lane == 0) red_z[warp] = z, red_s[warp] = s, red_c[warp] = c, red_w[warp] = w;
+        if (after < p.rows && next_token >= 0 && next_token < V)
+            mine = Ty::one(static_cast<const T *>(p.logits) + after * p.stride + next_token);
+        const int this_token = token;
+        token = next_token;
+        sync_rows();
 
-    if (K > 0) {
-        // the K-th largest of the groups' maxima (0 where fewer groups have one: then everything is a candidate)
-        u64 mine_g = group[lane], bound = 0;
-        int above = 0;
-        for (int i = 0; i < 32; ++i) above += group[i] > mine_g || (group[i] == mine_g && i < lane);
-        const uint32_t who = __ballot_sync(0xffffffffu, above == K - 1);
-        bound = __shfl_sync(0xffffffffu, mine_g, __ffs(who) - 1);
-        auto offer = [&](u64 key) {
-            if (key >= bound) {
-                const int at = atomicAdd(&count, 1);
-                if (at < kList) list[at] = key;
+        // of `have` keys in `list`, in any order, the K largest to put(0 .. K-1, key), largest first: eight threads
+        // count what is above a key
+        auto rank_list = [&](int have, auto put) {
+            for (int i0 = 0; i0 < have; i0 += kThreads / 8) {
+                const int i = i0 + tid / 8;
+                const u64 key = i < have ? list[i] : 0;
+                int above = 0;
+                for (int j = tid % 8; j < have; j += 8) above += list[j] > key;
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1) above += __shfl_xor_sync(0xffffffffu, above, o);
+                if (i < have && tid % 8 == 0 && above < K) put(above, key);
             }
         };
-        if (bound == 0 || top_key >= bound) {
-            sl.batches([&](const float (&x)[kBatch], int v, int) {
-#pragma unroll
-                for (int j = 0; j < kBatch; ++j)
-                    if (sl.has(v, j)) offer(key_of(x[j], sl.index(v, j)));
-            });
-            sl.singles([&](int i) { offer(key_of(Vec<T>::one(sl.row + i), i)); });
-        }
-        __syncthreads();
-        int have = count;
-        if (have > kList) {
-            // too many reach the bound: the largest key below the last one found, K times
-            u64 last = ~0ull;
-            for (int k = 0; k < K; ++k) {
-                u64 g = 0;
-                sl.batches([&](const float (&x)[kBatch], int v, int) {
-#pragma unroll
-                    for (int j = 0; j < kBatch; ++j) {
-                        const u64 key = sl.has(v, j) ? key_of(x[j], sl.index(v, j)) : 0;
-                        if (key < last && key > g) g = key;
-                    }
-                });
-                sl.singles([&](int i) {
-                    const u64 key = key_of(Vec<T>::one(sl.row + i), i);
-                    if (key < last && key > g) g = key;
-                });
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    const u64 other = __shfl_xor_sync(0xffffffffu, g, o);
-                    g = other > g ? other : g;
+        if (K > 0) {
+            const float least = value_of((uint32_t)(bound >> 32));  // of a candidate; NaN: any
+            auto offer = [&](u64 key) {
+                if (key >= bound) {
+                    const int at = atomicAdd(&count, 1);
+                    if (at < kList) list[at] = key;
                 }
-                __syncthreads();
-                if (lane == 0) group[warp] = g;
-                __syncthreads();
-                last = 0;
-                for (int i = 0; i < kWarps; ++i) last = group[i] > last ? group[i] : last;
-                if (tid == 0) best[k] = last;
+            };
+            const int found = threads, each = (sl.v1 - sl.v0 + kThreads - 1) / kThreads;
+            for (int i = tid; i < found * each; i += kThreads) {
+                const int j = i / found, v = sl.v0 + j * kThreads + who[i - j * found];
+                if (v >= sl.v1) continue;
+                const uint4 y = __ldg(sl.body + v);
+                const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+                if (Ty::top(Ty::larger(Ty::larger(y.x, y.y), Ty::larger(y.z, y.w))) < least) continue;
+                float x[kN];
+                Ty::floats(w, x);
+#pragma unroll
+                for (int k = 0; k < kN; ++k) offer(key_of(x[k], sl.index(v) + k));
             }
-        } else {
-            if (tid < kMaxTop) best[tid] = 0;
-            __syncthreads();
-            for (int i = tid; i < have; i += kThreads) {
-                const u64 key = list[i];
-                int at = 0;
-                for (int j = 0; j < have && at < K; ++j) at += list[j] > key;
-                if (at < K) best[at] = key;
+            sl.singles([&](int i) { offer(key_of(Ty::one(sl.row + i), i)); });
+            sync_rows();
+            const int have = count;
+            if (have > kList) {
+                // too many reach the bound: the largest key below the last one found, K times
+                u64 last = ~0ull;
+                for (int k = 0; k < K; ++k) {
+                    u64 best = 0;
+                    auto look = [&](float x, int i) {
+                        const u64 key = key_of(x, i);
+                        if (key < last && key > best) best = key;
+                    };
+                    sl.vectors([&](const uint32_t (&w)[4], int v) {
+                        float x[kN];
+                        Ty::floats(w, x);
+#pragma unroll
+                        for (int j = 0; j < kN; ++j) look(x[j], sl.index(v) + j);
+                    });
+                    sl.singles([&](int i) { look(Ty::one(sl.row + i), i); });
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) best = max(best, (u64)__shfl_xor_sync(0xffffffffu, best, o));
+                    sync_rows();
+                    if (lane == 0) best_of[warp] = best;
+                    sync_rows();
+                    last = 0;
+                    for (int i = 0; i < kWarps; ++i) last = max(last, best_of[i]);
+                    if (tid == 0) given[0].best[k] = last;
+                }
+            } else {
+                rank_list(have, [&](int at, u64 key) { given[0].best[at] = key; });
             }
         }
-    }
-    __syncthreads();
-    if (tid == 0) {
-        float zt = red_z[0], st = red_s[0];
-        int ct = red_c[0], wt = red_w[0];
-        for (int i = 1; i < kWarps; ++i) zt += red_z[i], st += red_s[i], ct += red_c[i], wt += red_w[i];
-        out_m = M, out_s = st, out_c = ct;
-        out_z = wt > 1 ? zt + (float)(wt - 1) : zt;  // of several that attain the maximum one is left out
-    }
-    State all;
-    if (ranks > 1) {
-        cluster_sync();
-        if (rank != 0) {
+        if (tid == 0) {
+            float zt = red_z[0], st = red_s[0];
+            int ct = red_c[0], wt = red_w[0];
+            for (int i = 1; i < kWarps; ++i) zt += red_z[i], st += red_s[i], ct += red_c[i], wt += red_w[i];
+            // of several that attain the maximum one is left out
+            given[0].state = {M, wt > 1 ? zt + (float)(wt - 1) : zt, st};
+            given[0].before = ct;
+        }
+        sync_rows();
+        if (ranks > 1) {
+            cluster_wait();  // the first CTA has begun
+            if (rank > 0) {
+                constexpr int kWords = sizeof(Given) / 8;
+                static_assert(sizeof(Given) % 8 == 0, "whole words");
+                for (int i = tid; i < kWords; i += kThreads)
+                    st_cluster_u64(reinterpret_cast<u64 *>(&given[rank]) + i, 0, reinterpret_cast<const u64 *>(&given[0])[i]);
+            }
             cluster_sync();
-            return;
+            if (rank > 0) return;
         }
-    } else {
-        __syncthreads();
-    }
-    all = {out_m, out_z, out_s};
-    int ahead = out_c;
-    for (int r = 1; r < ranks; ++r) {
-        all = merge(all, {ld_cluster_f32(&out_m, r), ld_cluster_f32(&out_z, r), ld_cluster_f32(&out_s, r)});
-        ahead += __float_as_int(ld_cluster_f32(reinterpret_cast<const float *>(&out_c), r));
-    }
-    const bool empty = all.m == -INFINITY && all.z == all.z;  // nothing has any weight
-    if (all.m == INFINITY) all.z = __uint_as_float(0x7FFFFFFFu);
-    const float log_z = log1pf(all.z);
-    auto log_prob = [&](float x) { return empty ? -INFINITY : (x - all.m) - log_z; };
-    if (tid == 0) {
-        if (p.logprobs) p.logprobs[n] = known ? log_prob(mine) : -INFINITY;
-        if (p.ranks) p.ranks[n] = known ? ahead : -1;
-        if (p.entropy) p.entropy[n] = empty ? 0.f : log_z - all.s / (1.f + all.z);
-    }
-    if (K > 0) {
-        const int lists = ranks * K;
-        for (int i = tid; i < lists; i += kThreads) list[i] = ld_cluster_u64(&best[i % K], i / K);
-        __syncthreads();
-        for (int i = tid; i < lists; i += kThreads) {
-            const u64 key = list[i];
-            if (key == 0) continue;
-            int at = 0;
-            for (int j = 0; j < lists && at < K; ++j) at += list[j] > key;
-            if (at < K) {
-                p.top_tokens[n * K + at] = (int32_t)(0xFFFFFFFFu - (uint32_t)key);
-                p.top_logprobs[n * K + at] = log_prob(value_of((uint32_t)(key >> 32)));
+        State all = given[0].state;
+        int ahead = given[0].before;
+        for (int q = 1; q < ranks; ++q) {
+            all = merge(all, given[q].state);
+            ahead += given[q].before;
+        }
+        if (broken) all.m = all.z = __uint_as_float(0x7FFFFFFFu);  // a wait ran out
+        const bool empty_row = all.m == -INFINITY && all.z == all.z;  // nothing has any weight
+        if (all.m == INFINITY) all.z = __uint_as_float(0x7FFFFFFFu);
+        const float log_z = log1pf(all.z);
+        auto log_prob = [&](float x) { return empty_row ? -INFINITY : (x - all.m) - log_z; };
+        if (tid == 0) {
+            const float x = known ? Ty::one(sl.row + this_token) : 0.f;
+            if (p.logprobs) p.logprobs[n] = known ? log_prob(x) : -INFINITY;
+            if (p.ranks) p.ranks[n] = known ? ahead : -1;
+            if (p.entropy) p.entropy[n] = empty_row ? 0.f : log_z - all.s / (1.f + all.z);
+        }
+        if (K > 0) {
+            auto put = [&](int at, u64 key) {
+                if (key == 0) return;
+                p.top_tokens[(int64_t)n * K + at] = (int32_t)(0xFFFFFFFFu - (uint32_t)key);
+                p.top_logprobs[(int64_t)n * K + at] = log_prob(value_of((uint32_t)(key >> 32)));
+            };
+            if (ranks == 1) {
+                if (tid < K) put(tid, given[0].best[tid]);
+            } else {
+                const int lists = ranks * K;
+                for (int i = tid; i < lists; i += kThreads) list[i] = given[i / K].best[i % K];
+                sync_rows();
+                rank_list(lists, put);
             }
         }
     }
-    if (ranks > 1) cluster_sync();  // the others' lists are read
 }
 
 template <typename T>
-cudaError_t launch_t(const LogprobParams &p, int64_t rows, cudaStream_t s) {
+cudaError_t launch_t(const LogprobParams &p, int sms, cudaStream_t s) {
+    cudaError_t e = cudaFuncSetAttribute(logprobs_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(rows * p.cluster));
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3((unsigned)(p.cluster > 1 ? p.rows * p.cluster : std::min(p.rows, kCtas * sms)));
+    cfg.blockDim = dim3(kThreads + 32);
+    cfg.dynamicSmemBytes = kRingBytes;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -519,15 +718,20 @@ extern "C" int verify_attn_logprobs(const void *logits, int64_t stride, va_float
         if (reinterpret_cast<uintptr_t>(x) % 4) return VA_ERR_INVALID_ARGUMENT;
     if (num_rows > (1 << 27)) return VA_ERR_INVALID_ARGUMENT;
     if (num_rows == 0) return VA_OK;
+    int device = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
     // a cluster of CTAs a row while the rows are fewer than the CTAs that the GPU holds
     int cluster = 1;
-    while (cluster < 8 && (int64_t)num_rows * cluster * 2 <= 2 * 152 && vocab / (cluster * 2) >= 4096) cluster *= 2;
+    while (cluster < va::kMaxCluster && (int64_t)num_rows * cluster * 2 <= va::kCtas * sms && vocab / (cluster * 2) >= 4096)
+        cluster *= 2;
     const va::LogprobParams p = {logits, stride, tokens, logprobs, entropy, top_logprobs, ranks, top_tokens,
-                                 vocab, num_top, cluster};
+                                 num_rows, vocab, num_top, cluster};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = type == VA_FLOAT_FP32   ? va::launch_t<float>(p, num_rows, s)
-                    : type == VA_FLOAT_BF16 ? va::launch_t<__nv_bfloat16>(p, num_rows, s)
-                                            : va::launch_t<__half>(p, num_rows, s);
+    if (e == cudaSuccess)
+        e = type == VA_FLOAT_FP32   ? va::launch_t<float>(p, sms, s)
+            : type == VA_FLOAT_BF16 ? va::launch_t<__nv_bfloat16>(p, sms, s)
+                                    : va::launch_t<__half>(p, sms, s);
     if (e == cudaSuccess) return VA_OK;
     va::note_cuda_error(e);
     cudaGetLastError();
