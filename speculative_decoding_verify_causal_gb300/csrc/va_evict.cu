@@ -12,6 +12,8 @@
 // the result does not depend on timing.
 #include <math.h>
 
+#include <algorithm>
+
 #include "va_internal.h"
 #include "va_sm100.cuh"
 
@@ -27,8 +29,8 @@ struct EvictParams {
     int2 *moves;     // [num_seqs * Hkv][half]: from, to
     int32_t *count;  // [num_seqs * Hkv]
     int bt_stride, num_seqs, Hkv, num_pages, num_sinks, cluster, half, slots;
-    int units;  // 16-byte units of a row (0: rows of fewer bytes, row_bytes)
-    int row_bytes;
+    int units;   // 16-byte units of a row
+    int cached;  // slots of a CTA whose weights lie in shared memory
 };
 
 namespace {
@@ -39,6 +41,8 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMoveThreads = 256;
+constexpr int kMaxCluster = 8;
+constexpr int kMaxCached = 40960;  // 160 KB
 
 // Weights in an order of unsigned integers: NaN lowest, then -inf .. +inf; protected tokens above all.
 __device__ __forceinline__ uint32_t weight_order(float x) {
@@ -47,21 +51,29 @@ __device__ __forceinline__ uint32_t weight_order(float x) {
     return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
+__device__ __forceinline__ void st_cluster_u32(const void *local, uint32_t rank, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_map(local, rank)), "r"(v) : "memory");
+}
 __device__ __forceinline__ uint32_t ld_cluster_u32(const void *local, uint32_t rank) {
     uint32_t v;
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_map(local, rank)) : "memory");
     return v;
 }
 
-// Sum over the block of a pair of counts, and the sums before this warp.
+// What a warp's slots hold: above the threshold from `keep` on and below it under `keep`, and at it on either side.
 struct Counts {
-    int a, b;
+    int up, down, tied_low, tied_high;
+    __device__ __forceinline__ void add(const Counts &x) {
+        up += x.up, down += x.down, tied_low += x.tied_low, tied_high += x.tied_high;
+    }
 };
 
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParams p) {
+    extern __shared__ uint32_t keys[];
     __shared__ uint32_t bins[kBins], total[kBins];
-    __shared__ uint32_t warp_sum[kWarps + 1], found[2];
-    __shared__ int warp_a[kWarps], warp_b[kWarps], cta_a, cta_b, bad;
+    __shared__ uint32_t warp_sum[kWarps], found[2];
+    __shared__ Counts of_warp[kWarps], of_cta;
+    __shared__ int bad;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ranks = p.cluster, rank = (int)(blockIdx.x % ranks);
     const int bg = blockIdx.x / ranks, b = bg / p.Hkv, g = bg % p.Hkv;
@@ -75,63 +87,72 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
     const int L = p.seq_lens[b], want = p.keep[b];
     const int32_t *bt = p.block_table + (size_t)b * p.bt_stride;
     // requests that are not carried out: the sequence stays as it is
-    int wrong = 0;
-    if (tid == 0) bad = 0;
-    __syncthreads();
-    if (L < 0 || L > p.slots || (int64_t)L > (int64_t)p.bt_stride * VA_PAGE_SIZE) wrong = VA_PAGES_BAD_REQUEST;
-    const bool cut = wrong == 0 && want >= 0 && want < L;
-    if (cut) {
-        for (int i = tid; i < (L + VA_PAGE_SIZE - 1) / VA_PAGE_SIZE; i += kThreads) {
-            const int page = bt[i];
-            if (page < 0 || (p.num_pages > 0 && page >= p.num_pages))
-                atomicOr(&bad, VA_PAGES_BAD_ENTRY);
-            else if (p.ref_count && p.ref_count[page] > 1)
-                atomicOr(&bad, VA_PAGES_BAD_REQUEST);
+    const int wrong = L < 0 || L > p.slots || (int64_t)L > (int64_t)p.bt_stride * VA_PAGE_SIZE ? VA_PAGES_BAD_REQUEST : 0;
+    if (wrong || want < 0 || want >= L) {  // alike in all CTAs of the cluster
+        if (rank == 0 && tid == 0) {
+            if (wrong && p.flags) atomicOr(p.flags, wrong);
+            p.new_lens[b] = L;  // the same from every head
+            p.count[bg] = 0;
         }
+        return;
     }
-    __syncthreads();
-    wrong |= bad;
-    if (rank == 0 && tid == 0) {
-        if (wrong && p.flags) atomicOr(p.flags, wrong);
-        p.new_lens[b] = cut && wrong == 0 ? want : L;  // the same from every head
-        if (!cut || wrong) p.count[bg] = 0;
-    }
-    if (!cut || wrong) return;  // alike in all CTAs of the cluster
 
     const int64_t row = b * p.stride_seq + g * p.stride_head;
     const float *weights = p.weights + row;
     const int recent = p.recent_from ? p.recent_from[b] : 0x7FFFFFFF;
     // a CTA's slots, whole warps' worth
     const int per = ((L + ranks - 1) / ranks + 31) / 32 * 32;
-    const int s0 = min(L, rank * per), s1 = min(L, s0 + per);
+    const int s0 = min(L, rank * per), s1 = min(L, s0 + per), cached = min(s1, s0 + p.cached);
     auto order = [&](int s) -> uint32_t {
         const int pos = p.slot_pos ? p.slot_pos[row + s] : s;
-        if (pos < p.num_sinks || pos >= recent) return 0xFFFFFFFFu;
-        return weight_order(weights[s]);
+        const uint32_t o = weight_order(weights[s]);
+        return pos < p.num_sinks || pos >= recent ? 0xFFFFFFFFu : o;
     };
+    auto key = [&](int s) { return s < cached ? keys[s - s0] : order(s); };
+#pragma unroll 8
+    for (int s = s0 + tid; s < cached; s += kThreads) keys[s - s0] = order(s);
+    if (tid == 0) bad = 0;
+    for (int i = tid; i < kBins; i += kThreads) bins[i] = 0;
+    __syncthreads();
+    for (int i = rank * kThreads + tid; i < (L + VA_PAGE_SIZE - 1) / VA_PAGE_SIZE; i += ranks * kThreads) {
+        const int page = bt[i];
+        if (page < 0 || (p.num_pages > 0 && page >= p.num_pages))
+            atomicOr(&bad, VA_PAGES_BAD_ENTRY);
+        else if (p.ref_count && p.ref_count[page] > 1)
+            atomicOr(&bad, VA_PAGES_BAD_REQUEST);
+    }
 
     // the keep-th largest: from the top, the digit in which the count reaches `left`
     uint32_t prefix = 0, mask = 0;
     int left = want;
     for (int round = 0; round < 3 && want > 0; ++round) {
         const int shift = round == 0 ? 21 : round == 1 ? 10 : 0, width = round == 2 ? 10 : 11, n = 1 << width;
-        for (int i = tid; i < n; i += kThreads) bins[i] = 0;
-        __syncthreads();
+#pragma unroll 4
         for (int s = s0 + tid; s < s1; s += kThreads) {
-            const uint32_t o = order(s);
+            const uint32_t o = key(s);
             if ((o & mask) == prefix) atomicAdd(&bins[(o >> shift) & (n - 1)], 1u);
         }
         sync();
-        for (int i = tid; i < n; i += kThreads) {
-            uint32_t t = 0;
-            for (int r = 0; r < ranks; ++r) t += ranks > 1 ? ld_cluster_u32(&bins[i], r) : bins[i];
-            total[i] = t;
+        const uint32_t *sums = bins;
+        if (ranks > 1) {
+            // each CTA adds up its share of the bins and tells all of them
+            const int share = n / ranks;
+            for (int i = tid; i < share; i += kThreads) {
+                uint32_t t = 0;
+#pragma unroll
+                for (int q = 0; q < kMaxCluster; ++q)
+                    if (q < ranks) t += ld_cluster_u32(&bins[rank * share + i], q);
+#pragma unroll
+                for (int q = 0; q < kMaxCluster; ++q)
+                    if (q < ranks) st_cluster_u32(&total[rank * share + i], q, t);
+            }
+            cluster_sync();
+            sums = total;
         }
-        sync();  // the bins are read
-        // from the top: thread t has bins n - 1 - 4 t ..
-        uint32_t mine = 0;
+        // from the top: thread t has bins n - 1 - each t ..
         const int each = n / kThreads;  // 4 or 2
-        for (int i = 0; i < each; ++i) mine += total[n - 1 - (tid * each + i)];
+        uint32_t mine = 0;
+        for (int i = 0; i < each; ++i) mine += sums[n - 1 - (tid * each + i)];
         uint32_t upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -141,74 +162,95 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
         if (lane == 31) warp_sum[warp] = upto;
         __syncthreads();
         uint32_t before = upto - mine;
-        for (int i = 0; i < warp; ++i) before += warp_sum[i];
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) before += i < warp ? warp_sum[i] : 0u;
         if (before < (uint32_t)left && before + mine >= (uint32_t)left) {
             uint32_t above = before;
             for (int i = 0; i < each; ++i) {
                 const int bin = n - 1 - (tid * each + i);
-                if (above + total[bin] >= (uint32_t)left) {
+                if (above + sums[bin] >= (uint32_t)left) {
                     found[0] = bin, found[1] = above;
                     break;
                 }
-                above += total[bin];
+                above += sums[bin];
             }
         }
         __syncthreads();
         prefix |= found[0] << shift;
         mask |= (uint32_t)(n - 1) << shift;
         left -= (int)found[1];
+        for (int i = tid; i < kBins; i += kThreads) bins[i] = 0;
         __syncthreads();
     }
-    // kept: above the threshold, and of those at it the first `left`.  A slot at the threshold needs the count of
-    // those before it: over the CTAs of lower rank, the warps of lower slots, and in the warp.
+    // Kept: above the threshold, and of those at it the first `left`.  The places of a warp's moves and holes follow
+    // from the counts before it: over the CTAs of lower rank and the warps of lower slots.
     const uint32_t threshold = prefix;
     const int each = ((s1 - s0 + kWarps - 1) / kWarps + 31) / 32 * 32;  // slots of a warp, one after the other
     const int w0 = min(s1, s0 + warp * each), w1 = min(s1, w0 + each);
-    auto place = [&](int in_warp_a, int in_warp_b) -> Counts {  // counts before this warp, over the cluster
-        if (lane == 0) warp_a[warp] = in_warp_a, warp_b[warp] = in_warp_b;
-        __syncthreads();
-        if (tid == 0) {
-            int a = 0, c = 0;
-            for (int i = 0; i < kWarps; ++i) a += warp_a[i], c += warp_b[i];
-            cta_a = a, cta_b = c;
+    Counts mine = {0, 0, 0, 0};
+    for (int s = w0 + lane; s < w1; s += 32) {
+        const uint32_t o = key(s);
+        const bool above = want > 0 && o > threshold, tie = want > 0 && o == threshold;
+        mine.up += above && s >= want;
+        mine.down += !above && !tie && s < want;
+        mine.tied_low += tie && s < want;
+        mine.tied_high += tie && s >= want;
+    }
+    mine.up = __reduce_add_sync(0xffffffffu, mine.up);
+    mine.down = __reduce_add_sync(0xffffffffu, mine.down);
+    mine.tied_low = __reduce_add_sync(0xffffffffu, mine.tied_low);
+    mine.tied_high = __reduce_add_sync(0xffffffffu, mine.tied_high);
+    if (lane == 0) of_warp[warp] = mine;
+    __syncthreads();
+    Counts before = {0, 0, 0, 0}, all = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) before.add(of_warp[i]);
+        all.add(of_warp[i]);
+    }
+    int refused = bad, low = all.tied_low;
+    if (ranks > 1) {
+        if (tid == 0) of_cta = all;
+        cluster_sync();
+#pragma unroll
+        for (int q = 0; q < kMaxCluster; ++q) {
+            if (q >= ranks || q == rank) continue;
+            const int tied_low = ld_cluster_u32(&of_cta.tied_low, q);
+            low += tied_low;
+            refused |= ld_cluster_u32(&bad, q);
+            if (q < rank)
+                before.add({(int)ld_cluster_u32(&of_cta.up, q), (int)ld_cluster_u32(&of_cta.down, q), tied_low,
+                            (int)ld_cluster_u32(&of_cta.tied_high, q)});
         }
-        sync();
-        Counts x = {0, 0};
-        for (int r = 0; r < rank; ++r) x.a += ld_cluster_u32(&cta_a, r), x.b += ld_cluster_u32(&cta_b, r);
-        for (int i = 0; i < warp; ++i) x.a += warp_a[i], x.b += warp_b[i];
-        sync();  // read, before the next use
-        return x;
-    };
-    int at_threshold = 0;
-    for (int s = w0 + lane; s - lane < w1; s += 32)
-        at_threshold += __popc(__ballot_sync(0xffffffffu, s < w1 && want > 0 && order(s) == threshold));
-    const int ties_before = place(at_threshold, 0).a;
-    // two walks: count the moves and holes of this warp, then list them
-    Counts base = {0, 0};
-    for (int walk = 0; walk < 2; ++walk) {
-        int ties = ties_before, movers = base.a, holes = base.b;
+        cluster_arrive();  // read: no CTA ends before cluster_wait
+    }
+    if (rank == 0 && tid == 0) {
+        if (refused && p.flags) atomicOr(p.flags, refused);
+        p.new_lens[b] = refused ? L : want;  // the same from every head
+    }
+    if (refused) {
+        if (rank == 0 && tid == 0) p.count[bg] = 0;
+    } else {
+        const int high = max(0, left - low);  // kept of those at the threshold from `keep` on
+        int ties_low = before.tied_low, ties_high = before.tied_high;
+        int movers = before.up + min(ties_high, high), holes = before.down + ties_low - min(ties_low, left);
         for (int s = w0 + lane; s - lane < w1; s += 32) {
-            const uint32_t o = s < w1 ? order(s) : 0u;
+            const uint32_t o = s < w1 ? key(s) : 0u, lower = (1u << lane) - 1u;
             const bool tie = s < w1 && want > 0 && o == threshold;
-            const uint32_t tied = __ballot_sync(0xffffffffu, tie);
-            const uint32_t lower = (1u << lane) - 1u;
-            const bool kept = s < w1 && want > 0 && (o > threshold || (tie && ties + __popc(tied & lower) < left));
+            const uint32_t tl = __ballot_sync(0xffffffffu, tie && s < want), th = __ballot_sync(0xffffffffu, tie && s >= want);
+            const bool kept = s < w1 && want > 0 &&
+                              (o > threshold || (tie && (s < want ? ties_low + __popc(tl & lower) < left
+                                                                  : ties_high + __popc(th & lower) < high)));
             const bool mover = kept && s >= want, hole = s < w1 && !kept && s < want;
             const uint32_t mv = __ballot_sync(0xffffffffu, mover), hl = __ballot_sync(0xffffffffu, hole);
-            if (walk == 1) {
-                if (mover) p.moves[(size_t)bg * p.half + movers + __popc(mv & lower)].x = s;
-                if (hole) p.moves[(size_t)bg * p.half + holes + __popc(hl & lower)].y = s;
-            }
-            ties += __popc(tied);
-            movers += __popc(mv);
-            holes += __popc(hl);
+            if (mover) p.moves[(size_t)bg * p.half + movers + __popc(mv & lower)].x = s;
+            if (hole) p.moves[(size_t)bg * p.half + holes + __popc(hl & lower)].y = s;
+            ties_low += __popc(tl), ties_high += __popc(th);
+            movers += __popc(mv), holes += __popc(hl);
         }
-        if (walk == 0) {
-            base = place(movers, holes);
-        } else if (rank == ranks - 1 && warp == kWarps - 1 && lane == 0) {
-            p.count[bg] = movers;  // as many as holes
-        }
+        if (rank == ranks - 1 && warp == kWarps - 1 && lane == 0) p.count[bg] = movers;  // as many as holes
     }
+    if (ranks > 1) cluster_wait();
 }
 
 // Rows of K and V: thread = 16 bytes of a row; scales, weights and positions with the row's first thread.
@@ -218,7 +260,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
     const int n = p.count[bg];
     const int32_t *bt = p.block_table + (size_t)b * p.bt_stride;
     const int64_t row = b * p.stride_seq + g * p.stride_head;
-    const int units = p.units > 0 ? p.units : 1;
+    const int units = p.units;
     for (int64_t e = (int64_t)blockIdx.x * kMoveThreads + threadIdx.x; e < (int64_t)n * units;
          e += (int64_t)gridDim.x * kMoveThreads) {
         const int i = (int)(e / units), u = (int)(e % units);
@@ -289,14 +331,16 @@ int verify_attn_evict(void *k_pages, void *v_pages, float *k_scale, float *v_sca
     p.moves = reinterpret_cast<int2 *>(static_cast<char *>(workspace) + align_up((size_t)heads * 4));
     p.bt_stride = block_table_stride, p.num_seqs = num_seqs, p.Hkv = num_kv_heads, p.num_pages = num_pages;
     p.num_sinks = num_sinks, p.half = num_slots / 2, p.slots = num_slots;
-    p.units = row / 16, p.row_bytes = row;
+    p.units = row / 16;
     // CTAs of a cluster: one for each 4,096 slots, as long as there are SMs for all
     p.cluster = 1;
-    while (p.cluster < 8 && num_slots > 4096 * p.cluster && heads * p.cluster * 2 <= 2 * 152) p.cluster *= 2;
+    while (p.cluster < va::kMaxCluster && num_slots > 4096 * p.cluster && heads * p.cluster * 2 <= 2 * 152) p.cluster *= 2;
+    p.cached = std::min(va::kMaxCached, ((num_slots + p.cluster - 1) / p.cluster + 31) / 32 * 32);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(heads * p.cluster));
     cfg.blockDim = dim3(va::kThreads);
+    cfg.dynamicSmemBytes = p.cached * sizeof(uint32_t);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -306,7 +350,9 @@ int verify_attn_evict(void *k_pages, void *v_pages, float *k_scale, float *v_sca
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, va::evict_select_kernel, p);
+    cudaError_t e = cudaFuncSetAttribute(va::evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         va::kMaxCached * (int)sizeof(uint32_t));
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, va::evict_select_kernel, p);
     if (e == cudaSuccess) {
         const int64_t most = (int64_t)p.half * p.units;  // threads' worth of work of a head, at most
         int64_t blocks = (most + va::kMoveThreads - 1) / va::kMoveThreads;

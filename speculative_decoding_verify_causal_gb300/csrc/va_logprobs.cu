@@ -3,19 +3,23 @@
 // With M = max x and Z' = the sum of exp(x - M) over all entries but one that attains M,
 //     log p(i) = (x_i - M) - log1p(Z'),     entropy = log1p(Z') - S / (1 + Z'),  S = sum exp(x - M) (x - M),
 // so that a token of probability near one keeps the bits of its small log, and the entropy is a sum of terms of one
-// sign.  One read of the logits from HBM: each thread keeps the running (M, Z, S) of its entries and counts those that
-// come before the token.  Z is held in two parts, the batch of 16 that holds the maximum and the rest; only the threads
-// that hold the row's maximum read that batch again and sum it without it.
+// sign.  One read of the logits from HBM: a warp copies a CTA's rows to a ring in shared memory, ahead into the next
+// row; each thread keeps the running (M, Z, S) of its entries and counts those that come before the token, in packed
+// bf16 or fp16.  Z is held in two parts, the chunk of 32 entries (fp32: 16) that holds the maximum and the rest; only the
+// threads that hold the row's maximum read that chunk again and sum it without it.
 //
 // The terms are taken as 2^(x log2(e) - C) with C = M log2(e) rounded, one multiplication-addition each, and the sums
-// corrected by 2^(C - M log2(e)), which is near one while M is of ordinary size.  Entries below -1e30 (fp16: -60000;
-// masks) have no weight beside such an M and are raised to that beforehand; a CTA whose maximum is beyond +-4096 (a row
-// of masks, infinity) reads its entries once more and takes each as exp(x - M).
+// corrected by 2^(C - M log2(e)), which is near one while M is of ordinary size.  A CTA whose maximum is beyond +-4096 (a
+// row of masks, infinity) reads its entries once more and takes each as exp(x - M).
 //
 // The top alternatives are found by a threshold: of the maxima of 32 groups of threads the K-th largest is a lower
-// bound of the K-th largest entry.  Threads whose maximum reaches it go through their entries again (from L2) and list
-// what reaches it, some 30 to 130 entries; those are ranked by counting.  Rows whose list overflows (many equal
-// entries) are searched K times instead.  Order: larger first, equal ones by index, NaN below -inf.
+// bound of the K-th largest entry.  The vectors of threads whose maximum reaches it are searched again (from L2) by the
+// whole CTA, which lists what reaches it, some 30 to 130 entries; those are ranked by counting.  Rows whose list
+// overflows (many equal entries) are searched K times instead.  Order: larger first, equal ones by index, NaN below -inf.
+//
+// Bound: instructions, about 7 an entry of bf16 (packed maximum and count 1.5, conversions 1, exponential and sums 2.5),
+// with 16 exponentials a clock of an SM next: 2,048 rows of 151,936 take 129 us, 4.8 TB/s; 256 rows 27 us, where 104 of
+// the SMs have two rows and the others one; 17 rows of fp32 17 us, mostly the chain from the first load to the result.
 //
 // A cluster of up to 8 CTAs shares a row where there are few rows: they write states and lists to the first one, which
 // merges them in rank order.
@@ -41,11 +45,13 @@ namespace {
 
 constexpr int kMaxTop = 32;
 constexpr int kMaxCluster = 8;
-constexpr int kThreads = 512, kWarps = kThreads / 32;  // and a warp that loads
+// Small CTAs, three of an SM, so that one's search at its row's end runs beside the others' sums: 2,048 rows of 151,936
+// bf16 took 165 us with 2 x 512 threads, 129 with 3 x 256, 130 with 5 x 128 (whose 17 rows in fp32 took 23 us, not 17).
+constexpr int kThreads = 256, kWarps = kThreads / 32;  // and a warp that loads
 constexpr int kVecs = 4;                               // 16-byte vectors of a thread in a chunk
 constexpr int kChunk = kThreads * kVecs;               // vectors
-constexpr int kStages = 3;
-constexpr int kCtas = 2;     // of an SM
+constexpr int kStages = 4;
+constexpr int kCtas = 3;     // of an SM
 constexpr int kList = 1024;  // candidates
 constexpr int kTake = 16;    // chunks between takes of the packed counts
 constexpr uint32_t kRingBytes = kStages * kChunk * 16;
