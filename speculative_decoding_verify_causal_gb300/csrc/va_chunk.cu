@@ -869,46 +869,70 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
     }
 }
 
-// Log-sum-exp merge of a tile's partials.  A CTA takes kCols elements of all 128 rows: thread = row, so that the
-// partials (rows innermost) are read in whole segments; the merged piece goes through shared memory, so that rows
-// of `out` are written in pieces of kCols elements.
-constexpr int kCombineCols = 16;
-
-__global__ void __launch_bounds__(kMmaRows) chunk_combine_kernel(const ChunkCombineParams p) {
-    __shared__ uint32_t tile[kMmaRows][kCombineCols / 2 + 1];
+// Log-sum-exp merge of a tile's partials.  A CTA takes kCols elements of all 128 rows: thread = row, so that the partials
+// (rows innermost) are read in whole segments; the merged piece goes through shared memory, so that rows of `out` are
+// written in pieces of kCols elements.  kWays threads share a row's partials: one after the other, each waiting for its
+// loads, ten partials of a question of 45 tokens (24 heads of 256) took longer than the attention itself, 30 us in all
+// against 22 with 8 x 4.  A merge that fills the GPU prefers wider pieces and fewer ways: 384 tiles' 5 partials, 2,000
+// tokens on 23,000, took 1,523 us in all with 8 x 4, 1,495 with 16 x 1, 1,485 with 16 x 2.
+template <int kCols, int kWays>
+__global__ void __launch_bounds__(kMmaRows * kWays) chunk_combine_kernel(const ChunkCombineParams p) {
+    __shared__ uint32_t tile[kMmaRows][kCols / 2 + 1];
+    __shared__ float part[kWays - 1][kCols][kMmaRows], top[kWays][kMmaRows], sum[kWays][kMmaRows];
     griddep_wait();
     const ChunkGroup g = p.groups[blockIdx.x];
-    const int r = threadIdx.x, d0 = blockIdx.y * kCombineCols;
+    const int r = threadIdx.x % kMmaRows, w = threadIdx.x / kMmaRows, d0 = blockIdx.y * kCols;
     const int rows = g.nt * p.G;
+    const size_t step = (size_t)g.step * kMmaRows;
+    float m = -INFINITY, z = 0.f, acc[kCols] = {};
     if (r < rows) {
         const float *lse = p.lse_part + (size_t)g.first_part * kMmaRows + r;
-        const size_t step = (size_t)g.step * kMmaRows;
-        float m = -INFINITY;
-        for (int n = 0; n < g.n; ++n) m = fmaxf(m, lse[n * step]);
-        float z = 0.f, acc[kCombineCols];
-#pragma unroll
-        for (int d = 0; d < kCombineCols; ++d) acc[d] = 0.f;
         const float *o = p.o_part + ((size_t)g.first_part * p.D + d0) * kMmaRows + r;
-        for (int n = 0; n < g.n; ++n) {
+        for (int n = w; n < g.n; n += kWays) {
             const float l = lse[n * step];
-            const float e = l == -INFINITY ? 0.f : expf(l - m);
-            z += e;
+            float x[kCols];
 #pragma unroll
-            for (int d = 0; d < kCombineCols; ++d) {
-                const float x = o[n * step * p.D + d * kMmaRows];
-                acc[d] = l == -INFINITY ? acc[d] : fmaf(e, x, acc[d]);
-            }
+            for (int d = 0; d < kCols; ++d) x[d] = o[n * step * p.D + d * kMmaRows];
+            if (l == -INFINITY) continue;  // no keys: the partial has zeros, or nothing
+            const float to = fmaxf(m, l), e = expf(l - to), old = m == -INFINITY ? 0.f : expf(m - to);
+            m = to;
+            z = z * old + e;
+#pragma unroll
+            for (int d = 0; d < kCols; ++d) acc[d] = fmaf(acc[d], old, e * x[d]);
         }
-        const float inv = z == 0.f ? 0.f : 1.f / z;
+    }
+    top[w][r] = m;
+    __syncthreads();
+    float M = top[0][r];
 #pragma unroll
-        for (int d = 0; d < kCombineCols / 2; ++d) tile[r][d] = pack_bf162(acc[2 * d] * inv, acc[2 * d + 1] * inv);
-        if (blockIdx.y == 0 && p.lse)
-            p.lse[(size_t)(g.q0 + r / p.G) * p.Hq + g.kvh * p.G + r % p.G] = z == 0.f ? -INFINITY : m + logf(z);
+    for (int i = 1; i < kWays; ++i) M = fmaxf(M, top[i][r]);
+    const float e = m == -INFINITY ? 0.f : expf(m - M);
+    sum[w][r] = z * e;
+    if (w > 0) {
+#pragma unroll
+        for (int d = 0; d < kCols; ++d) part[w - 1][d][r] = acc[d] * e;
     }
     __syncthreads();
-    constexpr int kUnits = kCombineCols / 8;
-    for (int e = r; e < rows * kUnits; e += kMmaRows) {
-        const int row = e / kUnits, u = e % kUnits;
+    if (w == 0 && r < rows) {
+        z = sum[0][r];
+#pragma unroll
+        for (int i = 1; i < kWays; ++i) z += sum[i][r];
+        const float inv = z == 0.f ? 0.f : 1.f / z;
+#pragma unroll
+        for (int d = 0; d < kCols; ++d) {
+            acc[d] *= e;
+#pragma unroll
+            for (int i = 1; i < kWays; ++i) acc[d] += part[i - 1][d][r];
+        }
+#pragma unroll
+        for (int d = 0; d < kCols / 2; ++d) tile[r][d] = pack_bf162(acc[2 * d] * inv, acc[2 * d + 1] * inv);
+        if (blockIdx.y == 0 && p.lse)
+            p.lse[(size_t)(g.q0 + r / p.G) * p.Hq + g.kvh * p.G + r % p.G] = z == 0.f ? -INFINITY : M + logf(z);
+    }
+    __syncthreads();
+    constexpr int kUnits = kCols / 8;
+    for (int i = threadIdx.x; i < rows * kUnits; i += kMmaRows * kWays) {
+        const int row = i / kUnits, u = i % kUnits;
         const size_t to = (size_t)(g.q0 + row / p.G) * p.Hq + g.kvh * p.G + row % p.G;
         reinterpret_cast<uint4 *>(p.out)[(to * p.D + d0) / 8 + u] =
             make_uint4(tile[row][4 * u], tile[row][4 * u + 1], tile[row][4 * u + 2], tile[row][4 * u + 3]);
@@ -970,9 +994,10 @@ cudaError_t launch_chunk(const ChunkParams &p, const va_heads &q, int N, int D, 
     }
 }
 
-cudaError_t launch_chunk_combine(const ChunkCombineParams &p, int num_groups, cudaStream_t s) {
-    if (num_groups <= 0) return cudaSuccess;
-    return launch_pdl(chunk_combine_kernel, dim3(num_groups, p.D / kCombineCols), dim3(kMmaRows), 0, s, p);
+cudaError_t launch_chunk_combine(const ChunkCombineParams &p, int num_groups, int num_sms, cudaStream_t s) {
+    if (num_groups * (p.D / 16) <= 4 * num_sms)
+        return launch_pdl(chunk_combine_kernel<8, 4>, dim3(num_groups, p.D / 8), dim3(kMmaRows * 4), 0, s, p);
+    return launch_pdl(chunk_combine_kernel<16, 2>, dim3(num_groups, p.D / 16), dim3(kMmaRows * 2), 0, s, p);
 }
 
 }  // namespace va

@@ -67,6 +67,6 @@ constexpr int chunk_tiles(int D) { return D == 256 ? 1 : 2; }  // tiles of packe
 
 cudaError_t launch_chunk(const ChunkParams &p, const va_heads &q, int N, int D, int dtype, int num_items, cudaStream_t s);
 cudaError_t launch_weights(const WeightParams &p, const va_heads &q, int N, int D, int dtype, int num_blocks, cudaStream_t s);
-cudaError_t launch_chunk_combine(const ChunkCombineParams &p, int num_groups, cudaStream_t s);
+cudaError_t launch_chunk_combine(const ChunkCombineParams &p, int num_groups, int num_sms, cudaStream_t s);
 
 }  // namespace va

@@ -359,7 +359,7 @@ int verify_attn_chunk(const va_chunk_plan *p, const va_heads *q, const void *k_p
     cudaError_t e = va::launch_chunk(cp, qv, p->total, p->D, p->kv_dtype, p->num_items, s);
     if (e == cudaSuccess && p->num_groups > 0) {
         const va::ChunkCombineParams mp = {p->groups, p->o_part, p->lse_part, cp.out, lse, p->Hq, p->G, p->D};
-        e = va::launch_chunk_combine(mp, p->num_groups, s);
+        e = va::launch_chunk_combine(mp, p->num_groups, p->num_sms, s);
     }
     return e == cudaSuccess ? VA_OK : fail(e);
 }
