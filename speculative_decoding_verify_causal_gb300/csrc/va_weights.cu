@@ -62,23 +62,26 @@ template <int DT>
 struct KeyPiece {
     static constexpr int kBytes = DT == VA_BF16 ? 32 : DT == VA_INT4 ? 8 : DT == VA_INT2 ? 4 : 16;
     uint32_t w[kBytes / 4];
-    __device__ __forceinline__ void load(const void *from) {
-        if constexpr (kBytes == 32) {
-            const uint4 a = __ldg(static_cast<const uint4 *>(from)), b = __ldg(static_cast<const uint4 *>(from) + 1);
-            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-        } else if constexpr (kBytes == 16) {
-            const uint4 a = __ldg(static_cast<const uint4 *>(from));
-            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
-        } else if constexpr (kBytes == 8) {
-            const uint2 a = __ldg(static_cast<const uint2 *>(from));
-            w[0] = a.x, w[1] = a.y;
-        } else {
-            w[0] = __ldg(static_cast<const uint32_t *>(from));
-        }
-    }
-    __device__ __forceinline__ void zero() {
+    // from `from`, or zeros: without a branch, so that a thread's loads are in flight together
+    __device__ __forceinline__ void load(const void *from, bool there) {
 #pragma unroll
         for (int i = 0; i < kBytes / 4; ++i) w[i] = 0;
+#pragma unroll
+        for (int i = 0; i < kBytes; i += 16) {
+            const char *at = static_cast<const char *>(from) + i;
+            if constexpr (kBytes >= 16)
+                asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+                             : "+r"(w[i / 4]), "+r"(w[i / 4 + 1]), "+r"(w[i / 4 + 2]), "+r"(w[i / 4 + 3])
+                             : "l"(at), "r"((uint32_t)there));
+            else if constexpr (kBytes == 8)
+                asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\t@p ld.global.nc.v2.u32 {%0, %1}, [%2];\n\t}"
+                             : "+r"(w[0]), "+r"(w[1])
+                             : "l"(at), "r"((uint32_t)there));
+            else
+                asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p ld.global.nc.u32 %0, [%1];\n\t}"
+                             : "+r"(w[0])
+                             : "l"(at), "r"((uint32_t)there));
+        }
     }
     __device__ __forceinline__ void store(uint32_t lo, uint32_t hi) const {
         uint32_t h[8];
@@ -123,45 +126,99 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) weights_kernel(const __gr
     auto tile_t0 = [&](int m) { return t_first + (m * ranks + rank) * tpt; };
     constexpr int kProducerWarp = C::kProducerWarp, kMmaWarp = C::kMmaWarp;
 
-    if (warp == kProducerWarp && lane == 0) {
-        prefetch_tensormap(&args.tm_q);
-        for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(bar(kQFull + i), 1);
-            mbar_init(bar(kQEmpty + i), C::kKeyTiles);
+    // The producer's: rows of q, and their -lse in units of ln 2.
+    int token[4];  // of a tile, of this lane's four rows; past every chunk where there is no such row
+    int64_t place[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 32 * i + lane;
+        token[i] = r < tpt * G ? r / G : 0x40000000;
+        place[i] = (int64_t)(it.q0 + r / G) * p.Hq + it.kvh * G + r % G;
+    }
+    auto load_lse = [&](int m, float (&x)[4]) {
+        const int t0 = tile_t0(m);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            x[i] = m < tiles && token[i] < it.n - t0 ? __ldg(p.lse + place[i] + (int64_t)t0 * p.Hq) : INFINITY;
+    };
+    float next[4];
+    auto load_tile = [&](int m) {
+        const int st = m % C::kStages;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // a row without keys, or none, gives nothing
+            sts_f32(sbase + C::kLse + 4u * ((m % kLseRing) * kRows + 32 * i + lane),
+                    fabsf(next[i]) == INFINITY ? -INFINITY : -next[i] * 1.4426950408889634f);
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive_expect_tx(bar(kQFull + st), (uint32_t)(D / 64 * G * tpt * 128));
+            for (int c = 0; c < D / 64; ++c)
+                tma_load_3d(sbase + C::kQ + st * C::kTileBytes + c * C::kChunkBytes, &args.tm_q, c * 64, it.kvh * G,
+                            it.q0 + tile_t0(m), bar(kQFull + st));
         }
-        for (int i = 0; i < 2 * C::kKeyTiles; ++i) {
-            mbar_init(bar(kSFull + i), 1);
-            mbar_init(bar(kSEmpty + i), 8);
+        __syncwarp();
+        load_lse(m + 1, next);
+    };
+    int issued = 0;
+    if (warp == kProducerWarp) {
+        if (lane == 0) {
+            prefetch_tensormap(&args.tm_q);
+            for (int i = 0; i < C::kStages; ++i) {
+                mbar_init(bar(kQFull + i), 1);
+                mbar_init(bar(kQEmpty + i), C::kKeyTiles);
+            }
+            for (int i = 0; i < 2 * C::kKeyTiles; ++i) {
+                mbar_init(bar(kSFull + i), 1);
+                mbar_init(bar(kSEmpty + i), 8);
+            }
+            mbar_init(bar(kDone), C::kKeyTiles);
+            fence_barrier_init();
         }
-        mbar_init(bar(kDone), C::kKeyTiles);
-        fence_barrier_init();
+        __syncwarp();
+        load_lse(0, next);
+        for (; issued < min(tiles, C::kStages); ++issued) load_tile(issued);
     } else if (warp == kMmaWarp) {
         tmem_alloc(bar(kTmemSlot), 256 * C::kKeyTiles);
         tmem_relinquish();
     }
     const int32_t *bt = p.block_table + (size_t)it.b * p.bt_stride;
     auto page_of = [&](int key) -> int {  // -1: no such key
-        if (key >= it.L) return -1;
-        const int page = __ldg(bt + key / VA_PAGE_SIZE);
-        return page < 0 || (p.num_pages > 0 && page >= p.num_pages) ? -1 : page;
+        const int page = __ldg(bt + min(key, it.L - 1) / VA_PAGE_SIZE);
+        return key >= it.L || page < 0 || (p.num_pages > 0 && page >= p.num_pages) ? -1 : page;
     };
+    // A sum warp has 16 keys; a thread two of them, row x (8 apart), in a quarter of the columns: c and c + 1 of each 8.
+    const int kt = warp >> 3, h = (warp >> 2) & 1, c = 2 * (lane & 3);
+    auto my_row = [&](int x) { return kt * 128 + (warp & 3) * 32 + 16 * h + 8 * x + (lane >> 2); };
+    uint64_t c2[2];
+    int key[2], page[2];
+    float old = 0.f;  // what the block's keys have already, of the first threads
     if (warp < C::kSumWarps) {
+        float scale[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            key[x] = it.key0 + my_row(x);
+            page[x] = page_of(key[x]);
+        }
+        // what is not needed before the keys are there, is asked for before them
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            scale[x] = DT != VA_BF16 && page[x] >= 0
+                           ? __ldg(p.k_scale + ((size_t)page[x] * VA_PAGE_SIZE + key[x] % VA_PAGE_SIZE) * p.Hkv + it.kvh)
+                           : 1.f;
         // the block's keys, 16 elements a piece
-        constexpr int kPieces = D / 16, kBatch = D == 64 ? 2 : 4;
+        constexpr int kPieces = D / 16, kBatch = D == 64 ? 2 : D == 128 ? 4 : 8;  // all of a thread's: one trip
         constexpr int kTotal = C::kKeyTiles * 128 * kPieces, kStride = C::kSumWarps * 32;
         const unsigned char *pages = static_cast<const unsigned char *>(p.k_pages);
 #pragma unroll 1
         for (int e0 = tid; e0 < kTotal; e0 += kBatch * kStride) {
             KeyPiece<DT> x[kBatch];
+            int from[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) from[i] = page_of(it.key0 + (e0 + i * kStride) / kPieces);
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
                 const int e = e0 + i * kStride, key = it.key0 + e / kPieces;
-                const int page = page_of(key);
-                if (page < 0)
-                    x[i].zero();
-                else
-                    x[i].load(pages + ((((size_t)page * VA_PAGE_SIZE + key % VA_PAGE_SIZE) * p.Hkv + it.kvh) * kPieces +
-                                       e % kPieces) * KeyPiece<DT>::kBytes);
+                x[i].load(pages + ((((int64_t)from[i] * VA_PAGE_SIZE + key % VA_PAGE_SIZE) * p.Hkv + it.kvh) * kPieces +
+                                   e % kPieces) * KeyPiece<DT>::kBytes, from[i] >= 0);
             }
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
@@ -171,6 +228,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) weights_kernel(const __gr
             }
         }
         static_assert(kTotal % (kBatch * kStride) == 0, "whole batches");
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const uint32_t by = __float_as_uint(p.sm_scale_log2 * scale[x]);
+            c2[x] = f2_pack(by, by);
+        }
         // rows of q's tiles that no box fills: with -lse of -inf they add nothing, as long as they are numbers
         const int full = tpt * G;
         for (int e = tid; e < C::kStages * (D / 8) * (kRows - full); e += kStride) {
@@ -186,56 +248,24 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) weights_kernel(const __gr
     bool ok = true;
 
     if (warp == kProducerWarp) {
-        // ------------------------------------------------------------ producer: rows of q, and their -lse in units of ln 2
-        int token[4];     // of a tile, of this lane's four rows; past every chunk where there is no such row
-        int64_t place[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 32 * i + lane;
-            token[i] = r < tpt * G ? r / G : 0x40000000;
-            place[i] = (int64_t)(it.q0 + r / G) * p.Hq + it.kvh * G + r % G;
-        }
-        auto load_lse = [&](int m, float (&x)[4]) {
-            const int t0 = tile_t0(m);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                x[i] = m < tiles && token[i] < it.n - t0 ? __ldg(p.lse + place[i] + (int64_t)t0 * p.Hq) : INFINITY;
-        };
-        float next[4];
-        load_lse(0, next);
-        int issued = 0;
-        for (int m = 0; m < tiles; ++m) {
-            const int st = m % C::kStages;
-            if (m >= C::kStages) {
-                ok = __all_sync(0xffffffffu, mbar_wait(bar(kQEmpty + st), ((m / C::kStages) & 1) ^ 1, kWaitNs));
-                if (!ok) break;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)  // a row without keys, or none, gives nothing
-                sts_f32(sbase + C::kLse + 4u * ((m % kLseRing) * kRows + 32 * i + lane),
-                        fabsf(next[i]) == INFINITY ? -INFINITY : -next[i] * 1.4426950408889634f);
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar(kQFull + st), (uint32_t)(D / 64 * G * tpt * 128));
-                for (int c = 0; c < D / 64; ++c)
-                    tma_load_3d(sbase + C::kQ + st * C::kTileBytes + c * C::kChunkBytes, &args.tm_q, c * 64, it.kvh * G,
-                                it.q0 + tile_t0(m), bar(kQFull + st));
-            }
-            __syncwarp();
-            issued = m + 1;
-            load_lse(m + 1, next);
+        // ------------------------------------------------------------ producer, once the first stages are on their way
+        for (; issued < tiles; ++issued) {
+            const int st = issued % C::kStages;
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(kQEmpty + st), ((issued / C::kStages) & 1) ^ 1, kWaitNs));
+            if (!ok) break;
+            load_tile(issued);
         }
         if (lane == 0)
             for (int m = max(0, issued - C::kStages); m < issued; ++m)
                 if (!mbar_wait(bar(kQFull + m % C::kStages), (m / C::kStages) & 1, kWaitNs)) ok = false;
     } else if (warp >= kMmaWarp) {
         // ------------------------------------------------------------ MMA issue, by a whole warp: its tile of keys
-        const int kt = warp - kMmaWarp;
+        const int tile = warp - kMmaWarp;
         constexpr uint32_t id = idesc_f16(128, kRows, 1, 0, 0);
         constexpr uint32_t kHi = smem_desc_hi(1024, 2);
-        const uint32_t klo = smem_desc_lo(sbase + C::kK + kt * C::kTileBytes, 16), qlo = smem_desc_lo(sbase + C::kQ, 16);
+        const uint32_t klo = smem_desc_lo(sbase + C::kK + tile * C::kTileBytes, 16), qlo = smem_desc_lo(sbase + C::kQ, 16);
         for (int m = 0; m < tiles && ok; ++m) {
-            const int st = m % C::kStages, s = kt * 2 + (m & 1);
+            const int st = m % C::kStages, s = tile * 2 + (m & 1);
             ok = __all_sync(0xffffffffu, m < 2 ? mbar_wait(bar(kQFull + st), (m / C::kStages) & 1, kWaitNs)
                                                : mbar_wait2(bar(kQFull + st), (m / C::kStages) & 1, bar(kSEmpty + s),
                                                             ((m >> 1) & 1) ^ 1, kWaitNs));
@@ -257,22 +287,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) weights_kernel(const __gr
         if (!__all_sync(0xffffffffu, mbar_wait(bar(kDone), 0, kWaitNs))) ok = false;
     } else {
         // ------------------------------------------------------------ sums
-        // A warp has 16 keys; a thread two of them, row x (8 apart), in a quarter of the columns: c and c + 1 of each 8.
         const int kt = warp >> 3, h = (warp >> 2) & 1, c = 2 * (lane & 3);
         const uint32_t half_tm = tmem + ((uint32_t)((warp & 3) * 32 + 16 * h) << 16);
-        auto my_row = [&](int x) { return kt * 128 + (warp & 3) * 32 + 16 * h + 8 * x + (lane >> 2); };
-        uint64_t c2[2];
         float sum[2] = {0.f, 0.f}, lost[2] = {0.f, 0.f};
-        int key[2], page[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            key[x] = it.key0 + my_row(x);
-            page[x] = page_of(key[x]);
-            float scale = p.sm_scale_log2;
-            if (DT != VA_BF16 && page[x] >= 0)
-                scale *= __ldg(p.k_scale + ((size_t)page[x] * VA_PAGE_SIZE + key[x] % VA_PAGE_SIZE) * p.Hkv + it.kvh);
-            c2[x] = f2_pack(__float_as_uint(scale), __float_as_uint(scale));
-        }
         const int last_key = it.key0 + C::kKeyTiles * 128 - 1;  // of the block: both of a CTA's tiles take one view
         // Half a tile of columns at a time: while one half's exponentials run, the next one is on its way from the
         // tensor memory.
@@ -322,6 +339,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) weights_kernel(const __gr
             ok = scores_of(0);
             if (ok) tmem_ld_16x256b(half_tm + kt * 2 * kRows, x0);
         }
+#pragma unroll 1
         for (int m = 0; m < tiles && ok; ++m) {
             const int s = kt * 2 + (m & 1);
             tmem_wait_ld();
