@@ -90,7 +90,7 @@ struct Cfg {
     static constexpr int kRaw = kConv + kStages * kPanelBytes;
     static constexpr int kScale = kRaw + kRawStages * kRawBytes;
     static constexpr int kBad = kScale + (kQuant ? kScaleRing * kScaleFloats * 4 : 0);
-    static constexpr int kStats = kQuant ? 3 : 2;      // values of each row that the softmax hands from thread to thread
+    static constexpr int kStats = kQuant ? 4 : 2;      // values of each row that the softmax hands from thread to thread
     static constexpr int kStat = kBad + kBadRing * 4;
     static constexpr int kBars = kStat + kTiles * kStats * kMmaRows * 4;
     static constexpr int kSmem = kBars + 64 * 8 + 1024;  // and slack for the alignment
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
         }
         mbar_init(bar(kOFinal), nq);
         mbar_init(bar(kQFull), 1);
-        mbar_init(bar(kQReady), 4 * nq);
+        mbar_init(bar(kQReady), 8 * nq);
         mbar_init(bar(kSwept), 8 * nq);
         for (int i = 0; i < kScaleRing; ++i) mbar_init(bar(kScaleFree + i), 8 * nq);
         sts_u32(bar(kPoison), 0u);
@@ -384,17 +384,15 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
             // q as the MMA takes it: rows without a token are zero; for a cache of codes, fp16 scaled by a power of
             // two that brings the row's largest element into [2^14, 2^15)
             ok = __all_sync(0xffffffffu, mbar_wait(bar(kQFull), 0, kWaitNs));
-            if (h == 0) {
-                float prescale = 1.f;
-                const uint32_t row = sbase + C::kQ + w * C::kQBytes;
-                auto unit = [&](int u) { return row + (u / 8) * C::kQChunk + sw128(r, u % 8); };
-                if (!row_ok) {
-#pragma unroll 4
-                    for (int u = 0; u < D / 8; ++u) sts_u4(unit(u), make_uint4(0, 0, 0, 0));
-                } else if (C::kQuant) {
-                    float amax = 0.f;
-#pragma unroll 4
-                    for (int u = 0; u < D / 8; ++u) {
+            // two threads of a row, each half of its elements
+            float prescale = 1.f;
+            const uint32_t row = sbase + C::kQ + w * C::kQBytes;
+            auto unit = [&](int u) { return row + ((h * (D / 16) + u) / 8) * C::kQChunk + sw128(r, (h * (D / 16) + u) % 8); };
+            if constexpr (C::kQuant) {
+                float amax = 0.f;
+                if (row_ok) {
+#pragma unroll 2
+                    for (int u = 0; u < D / 16; ++u) {
                         const uint4 x = lds_u4(unit(u));
                         const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -402,29 +400,36 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                             amax = fmaxf(amax, fmaxf(fabsf(bf16_bits_to_float(ws[e] & 0xFFFFu)),
                                                      fabsf(__uint_as_float(ws[e] & 0xFFFF0000u))));
                     }
-                    if (amax > 0.f && amax < INFINITY) {
-                        int e;
-                        frexpf(amax, &e);
-                        prescale = __uint_as_float((uint32_t)(127 + max(-126, min(127, 15 - e))) << 23);
-                    }
-#pragma unroll 4
-                    for (int u = 0; u < D / 8; ++u) {
-                        const uint4 x = lds_u4(unit(u));
-                        const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
-                        uint32_t h[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            h[e] = pack_half2(bf16_bits_to_float(ws[e] & 0xFFFFu) * prescale,
-                                              __uint_as_float(ws[e] & 0xFFFF0000u) * prescale);
-                        sts_u4(unit(u), make_uint4(h[0], h[1], h[2], h[3]));
-                    }
                 }
+                sts_f32(stat + 4u * ((2 + h) * kMmaRows + r), amax);
+                named_bar_sync(2 + w, 256);
+                amax = fmaxf(amax, lds_f32(stat + 4u * ((3 - h) * kMmaRows + r)));
+                if (amax > 0.f && amax < INFINITY)
+                    prescale = __uint_as_float(min(254u, 268u - (__float_as_uint(amax) >> 23)) << 23);
+            }
+            if (!row_ok) {
+#pragma unroll 2
+                for (int u = 0; u < D / 16; ++u) sts_u4(unit(u), make_uint4(0, 0, 0, 0));
+            } else if (C::kQuant) {
+#pragma unroll 2
+                for (int u = 0; u < D / 16; ++u) {
+                    const uint4 x = lds_u4(unit(u));
+                    const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
+                    uint32_t y[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        y[e] = pack_half2(bf16_bits_to_float(ws[e] & 0xFFFFu) * prescale,
+                                          __uint_as_float(ws[e] & 0xFFFF0000u) * prescale);
+                    sts_u4(unit(u), make_uint4(y[0], y[1], y[2], y[3]));
+                }
+            }
+            if (h == 0) {
                 sts_f32(stat + 4u * r, p.sm_scale_log2 / prescale);
                 sts_u32(stat + 4u * (kMmaRows + r), (uint32_t)(row_ok ? vis : -1));
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kQReady));
             }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kQReady));
             named_bar_sync(2 + w, 256);  // the rows' data
             // this thread's rows of the warp's 16: lane / 4 and 8 further, as row x; its columns of each 8: c, c + 1
             const int c = 2 * (lane & 3);
