@@ -638,6 +638,11 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                     // All softmax threads share the sweep and leave it together.
                     const int valid = min(kKeys, it.k_end - key0);
                     bool found = false;
+                    // With two panels a tile and five stages a panel's slot held one of the tile before: done with, so that
+                    // the wait's parity means this panel.
+                    if (!two && i > 0 &&
+                        !__all_sync(0xffffffffu, mbar_wait(bar(kODone + ((i - 1) & 1)), ((i - 1) >> 1) & 1, kWaitNs)))
+                        ok = false;
                     for (int pp = 0; pp < C::kPanels; ++pp) {
                         const int e = v_entry(i, ntiles) * C::kPanels + pp, slot = e % C::kStages;
                         if (!__all_sync(0xffffffffu, mbar_wait(bar(kFull + slot), (e / C::kStages) & 1, kWaitNs))) ok = false;
@@ -826,6 +831,9 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
 #pragma unroll
             for (int j = 0; j < kPer; ++j)
                 if (kEven || n0 + j * kStep < kKeys) raw[j].load(src + j * 128 * kPieceBytes);
+            // The loads are done before the slot is given back: nothing below needs their values before the arrival, which
+            // does not wait for them by itself, and with a cold TLB the copy of a later panel came first.
+            fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kRawEmpty + rs));
             const int nvalid = it.k_end - (it.k_begin + i * kKeys);

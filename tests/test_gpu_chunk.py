@@ -157,6 +157,32 @@ def test_chunk(va, shape, D, kv):
     assert va.verify_attn_chunk_plan_device_flags(plan) == 0
 
 
+@pytest.mark.parametrize("shape", [([100], [6000], 24, 4), ([40] * 40, [900] * 40, 12, 4)], ids=["split", "whole"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("kv", KINDS)
+def test_chunk_and_weights_of_many_tiles_of_keys(va, kv, D, shape):
+    """Every ring of the kernel is gone through several times: an odd number of stages between its two producers once let
+    one of them pass a barrier two phases ahead."""
+    b = Batch(*shape, D, kv, seed=D + 7)
+    plan = b.plan(va)
+    out, lse = b.run(va, plan)
+    b.check(out, lse)
+    w = torch.zeros(len(b.new), b.Hkv, max(b.lens), device="cuda")
+    check_weights(b, b.weigh(va, plan, lse, w), lse, None)
+    assert va.verify_attn_chunk_plan_device_flags(plan) == 0
+
+
+def test_weights_of_many_tiles_of_rows(va):
+    for D, kv in ((64, "bf16"), (128, "fp8_e4m3"), (256, "int8"), (256, "bf16")):
+        b = Batch([1500, 30], [1600, 300], 8, 1, D, kv, seed=D)
+        plan = b.plan(va)
+        _, lse = b.run(va, plan)
+        old = normal(2, 2, 1, 1600).abs()
+        w = old.clone()
+        check_weights(b, b.weigh(va, plan, lse, w), lse, old)
+        assert va.verify_attn_chunk_plan_device_flags(plan) == 0
+
+
 @pytest.mark.parametrize("kv", ["bf16", "int8", "int4"])
 @pytest.mark.parametrize("k_std,v_std", [(3.0, 1e-4), (0.05, 40.0), (1e-3, 1e4), (30.0, 1e-30)])
 def test_chunk_rows_of_any_size(va, kv, k_std, v_std):
@@ -442,6 +468,11 @@ def test_evict_lengths(va, L, keep, ties):
     evict_both(va, 1, 2, 64, "int8", [L], [keep], L, L + keep, ties=ties, pos=False, sinks=2, recent=[L - 3])
 
 
+def test_evict_more_slots_than_shared_memory_holds(va):
+    evict_both(va, 1, 1, 64, "int2", [400_000], [150_000], 400_003, 11, sinks=3)
+    evict_both(va, 1, 1, 64, "int2", [400_000], [399_000], 400_000, 12, ties=True)
+
+
 def test_evict_more_protected_than_kept_all_equal_and_nothing_to_do(va):
     evict_both(va, 2, 2, 64, "bf16", [90, 70], [20, 30], 90, 3, sinks=200)                # everything is protected
     evict_both(va, 2, 2, 64, "bf16", [90, 70], [20, 30], 90, 4, recent=[-5, 0])
@@ -560,6 +591,56 @@ def test_logprobs_special_rows(va, N):
                 many = va.verify_attn_logprobs(z, t.expand(N).contiguous(), K)
                 assert torch.equal(many[1], one[1].expand(N)) and torch.equal(many[3], one[3].expand(N, K)), i
                 assert torch.allclose(many[0], one[0].expand(N), rtol=1e-5, atol=1e-5, equal_nan=True)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_logprobs_of_more_rows_than_ctas_and_of_several_chunks(va, dtype):
+    N, V = 1000, 17_003
+    z = (normal(5, N, V) * 3).to(dtype)
+    t = torch.randint(-1, V + 1, (N,), generator=torch.Generator().manual_seed(6), dtype=torch.int32).cuda()
+    got = va.verify_attn_logprobs(z, t, 3)
+    some = list(range(0, N, 97)) + [N - 1]
+    check_logprobs(va, z[some].contiguous(), t[some].contiguous(), 3)
+    one = [va.verify_attn_logprobs(z[i:i + 1], t[i:i + 1], 3) for i in range(N)]  # by a cluster each
+    for k in (1, 3):
+        assert torch.equal(got[k], torch.cat([x[k] for x in one]))
+    for k in (0, 2, 4):  # each within 2^-13 Z' / (1 + Z') + 2^-21 |x|, the entropy 2^-13 (|S| + Z') / (1 + Z'), |S| < 16 Z'
+        x, y = got[k], torch.cat([x[k] for x in one])
+        assert torch.equal(x.isinf(), y.isinf())
+        assert ((x - y).nan_to_num(0.0).abs() <= 2.0 ** -12 * (17 if k == 2 else 1) + 2.0 ** -20 * y.nan_to_num(0, 0, 0).abs()).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("N", [1, 500])
+def test_logprobs_of_large_and_masked_values(va, dtype, N):
+    """Around the size from which a row is taken entry by entry, with parts of a row on either side of it."""
+    V = 20_000
+    base = normal(8, V).cpu() * 2
+    low = torch.finfo(dtype).min
+    rows = [base + x for x in (4090.0, 4100.0, -4090.0, -4100.0, 20_000.0, -20_000.0, 60_000.0, -60_000.0)] + [base * 500, base * 8000]
+    if dtype != torch.float16:
+        rows += [base + 1e30, base - 1e30, base * 1e30, base * 1e37]
+    for at, x in ((0, -5000.0), (9_000, -17_000.0), (15_000, low), (19_000, -float("inf"))):
+        masked = torch.full((V,), x)
+        masked[at:at + 300] = base[:300]
+        rows.append(masked)
+        part = base.clone()
+        part[at:at + 4000] = x
+        rows.append(part)
+        last = torch.full((V,), x)
+        last[V - 2] = -4000.0
+        rows.append(last)
+    for row in rows:
+        z = row.to(dtype)[None].cuda()
+        for token in (1, 9_050, V - 2):
+            t = torch.full((1,), token, dtype=torch.int32).cuda()
+            check_logprobs(va, z, t, 20)
+            if N > 1 and token == 1:  # and by one CTA a row
+                one = va.verify_attn_logprobs(z, t, 20)
+                many = va.verify_attn_logprobs(z.expand(N, V), t.expand(N).contiguous(), 20)
+                assert torch.equal(many[1], one[1].expand(N)) and torch.equal(many[3], one[3].expand(N, 20))
+                for k in (0, 2, 4):
+                    assert torch.allclose(many[k], one[k].expand(many[k].shape), rtol=2.0 ** -12, atol=2.0 ** -9, equal_nan=True)
 
 
 def test_logprobs_past_32_bits_and_argument_errors(va):
