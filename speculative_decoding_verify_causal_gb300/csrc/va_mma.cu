@@ -826,6 +826,7 @@ mma_partial_kernel(const __grid_constant__ MmaParams mp) {
             RawPiece<DT> raw[kPer];
 #pragma unroll
             for (int jj = 0; jj < kPer; ++jj) raw[jj].load(st + jj * kGT * kPieceBytes);
+            fence_proxy_async_smem();  // the loads are done: the arrival by itself does not wait for their values
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kRawEmpty + slot));
             // the tile's scales move up the pipeline and the load two tiles
