@@ -271,16 +271,16 @@ __device__ __forceinline__ State merge(State a, State b) {
 }
 
 // A thread's running state: the maximum, and the sums of the entries against it in two parts, the chunk that holds it
-// (which counts the maximum itself, 1) and the rest.
+// (which counts the maximum itself, 1, and in S what rounding leaves of its 0) and the rest.
 struct Running {
-    float m = -INFINITY, rest = 0.f, held = 0.f, s = 0.f;
+    float m = -INFINITY, rest = 0.f, held = 0.f, s = 0.f, s_held = 0.f;
     int chunk = 0;  // that chunk; ~i: the single entry i
     __device__ __forceinline__ void move(float to, int c) {
         const float d = m == -INFINITY ? -1e30f : fmaxf(m - to, -1e30f), e = exp_neg(d);
         const float w = rest + held;
-        s = e * (s + d * w);
+        s = e * (s + s_held + d * w);
         rest = e * w;
-        held = 0.f;
+        held = s_held = 0.f;
         m = to;
         chunk = c;
     }
@@ -441,11 +441,11 @@ __global__ void __launch_bounds__(kThreads + 32, kCtas) logprobs_kernel(const Lo
                     for (int j = 0; j < 4; ++j) w[i][j] = Ty::raise(w[i][j]);
             }
             const float by = 1.f - 0.69314718f * off;  // 2^-off but for 2^-24: off is 2^-12 at most for kWide
+            s = (s - off * z) * (0.69314718f * by), z *= by;
             if (moved)
-                r.held = z * by;
+                r.held = z, r.s_held = s;
             else
-                r.rest += z * by;
-            r.s += (s - off * z) * (0.69314718f * by);
+                r.rest += z, r.s += s;
         };
         for (int c = 0; c < chunks; ++c, ++g) {
             const int st = g % kStages;
@@ -541,13 +541,14 @@ __global__ void __launch_bounds__(kThreads + 32, kCtas) logprobs_kernel(const Lo
                     for (int j = 0; j < kN; ++j) {
                         const bool it = !out && x[j] == M;
                         out |= it;
-                        z += it ? 0.f : exp_neg(max_nan(x[j] - M, -1e30f));
+                        const float d = max_nan(x[j] - M, -1e30f), e = it ? 0.f : exp_neg(d);
+                        z += e, s += e * d;
                     }
                 }
             }
         } else if (r.m > -INFINITY) {
             const float d = max_nan(r.m - M, -1e30f), e = exp_neg(d), w = r.rest + r.held;
-            s = e * (s + d * w);
+            s = e * (s + r.s_held + d * w);
             z = e * w;
         } else {
             z += r.held;  // nothing, or NaN

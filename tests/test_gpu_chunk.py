@@ -157,14 +157,14 @@ def test_chunk(va, shape, D, kv):
     assert va.verify_attn_chunk_plan_device_flags(plan) == 0
 
 
-@pytest.mark.parametrize("shape", [([100], [6000], 24, 4), ([40] * 40, [900] * 40, 12, 4)], ids=["split", "whole"])
+@pytest.mark.parametrize("shape,sms", [(([100], [1500], 6, 1), 2), (([40], [2500], 12, 2), 16)], ids=["whole", "split"])
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("kv", KINDS)
-def test_chunk_and_weights_of_many_tiles_of_keys(va, kv, D, shape):
+def test_chunk_and_weights_of_many_tiles_of_keys(va, kv, D, shape, sms):
     """Every ring of the kernel is gone through several times: an odd number of stages between its two producers once let
-    one of them pass a barrier two phases ahead."""
+    one of them pass a barrier two phases ahead, and a slot was once given back before its loads were done."""
     b = Batch(*shape, D, kv, seed=D + 7)
-    plan = b.plan(va)
+    plan = b.plan(va, num_sms=sms)
     out, lse = b.run(va, plan)
     b.check(out, lse)
     w = torch.zeros(len(b.new), b.Hkv, max(b.lens), device="cuda")
@@ -174,10 +174,10 @@ def test_chunk_and_weights_of_many_tiles_of_keys(va, kv, D, shape):
 
 def test_weights_of_many_tiles_of_rows(va):
     for D, kv in ((64, "bf16"), (128, "fp8_e4m3"), (256, "int8"), (256, "bf16")):
-        b = Batch([1500, 30], [1600, 300], 8, 1, D, kv, seed=D)
+        b = Batch([700, 30], [800, 300], 16, 1, D, kv, seed=D)
         plan = b.plan(va)
         _, lse = b.run(va, plan)
-        old = normal(2, 2, 1, 1600).abs()
+        old = normal(2, 2, 1, 800).abs()
         w = old.clone()
         check_weights(b, b.weigh(va, plan, lse, w), lse, old)
         assert va.verify_attn_chunk_plan_device_flags(plan) == 0
@@ -523,7 +523,9 @@ def test_evict_argument_errors(va):
 
 def check_logprobs(va, z, t, top):
     """Z' is a sum of V terms exp(d), each off by 2^-22 and 2^-23 |d| of itself (|d| <= 104, then it is 0), added at most
-    2^10 in a row: 2^-13 of itself.  log1p and the subtractions: 2^-22 of their results and of x - M."""
+    2^10 in a row: 2^-13 of itself.  log1p and the subtractions: 2^-22 of their results and of x - M.  What is below
+    binary32's smallest normal number, 2^-126, may be 0: a term exp(d) below it has |d| exp(d) < 2^-126 * 88 (x exp(-x)
+    falls from there on), so V < 2^19 of them are worth less than 2^-126 * 2^7 * 2^19 = 2^-100."""
     got = va.verify_attn_logprobs(z, t, top)
     lp, ranks, ent, tt, tl, parts = chunks.logprobs(z.float().cpu().numpy(), t.cpu().numpy(), top)
     assert got[1].tolist() == ranks.tolist()
@@ -536,7 +538,7 @@ def check_logprobs(va, z, t, top):
         assert np.array_equal(np.isnan(x), np.isnan(y)) and np.array_equal(np.isneginf(x), np.isneginf(y))
         ok = np.isfinite(y)
         with np.errstate(invalid="ignore"):
-            bad = np.abs(x - y) > more
+            bad = np.abs(x - y) > more + 2.0 ** -100
         assert not bad[ok].any(), (np.abs(x - y)[ok & bad].max())
     with np.errstate(invalid="ignore"):
         close(got[0], lp, moved + 2.0 ** -21 * np.abs(lp))
