@@ -18,6 +18,12 @@ Around the verify step: ``verify_attn_rope`` and ``verify_attn_rope_append``
 ``verify_attn_accept_probs`` (acceptance from given probabilities and random
 numbers) and ``PagePool`` with ``verify_attn_pages_resize`` / ``_fork`` /
 ``_compact`` (the pages behind the block table).
+
+A prompt in chunks: ``verify_attn_chunk`` over a ``verify_attn_chunk_plan``
+(attention of ragged chunks of new tokens), ``verify_attn_chunk_weights`` (the
+attention weight that cached tokens gather), ``verify_attn_evict`` (cutting
+sequences back to their heaviest tokens) and ``verify_attn_logprobs`` (log
+probabilities, places, entropy and top alternatives).
 """
 from __future__ import annotations
 

@@ -10,6 +10,12 @@
 // the same order, three rounds of a histogram of 11, 11 and 10 bits give the keep-th largest, and counts before each
 // CTA's and warp's slots give the places in the list of moves.  The second moves the rows.  Whole numbers throughout:
 // the result does not depend on timing.
+//
+// Bound: latency.  4 sequences of 25,000 slots, 4 heads of 256, int8, cut to 4,096: 20 us for both kernels, 8.7 us of
+// bytes at the copy rate; most is the chain of the first one: a read of the weights (kept in shared memory as integers),
+// three rounds with two cluster barriers each, one exchange of counts (with the weights read again in each of six
+// passes and two exchanges more: 36 us).  Each CTA adds up a share of the bins and tells the others: eight times fewer remote reads than all of them
+// by all.  Two kernels, since eight CTAs of a head cannot move long lists of rows at the copy rate.
 #include <math.h>
 
 #include <algorithm>

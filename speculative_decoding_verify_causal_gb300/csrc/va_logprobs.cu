@@ -12,13 +12,16 @@
 // corrected by 2^(C - M log2(e)), which is near one while M is of ordinary size.  A CTA whose maximum is beyond +-4096 (a
 // row of masks, infinity) reads its entries once more and takes each as exp(x - M).
 //
+// The sums are kept against a reference that is at most 8 below the running maximum, so that they are scaled once or
+// twice a row.
+//
 // The top alternatives are found by a threshold: of the maxima of 32 groups of threads the K-th largest is a lower
 // bound of the K-th largest entry.  The vectors of threads whose maximum reaches it are searched again (from L2) by the
 // whole CTA, which lists what reaches it, some 30 to 130 entries; those are ranked by counting.  Rows whose list
 // overflows (many equal entries) are searched K times instead.  Order: larger first, equal ones by index, NaN below -inf.
 //
 // Bound: instructions, about 7 an entry of bf16 (packed maximum and count 1.5, conversions 1, exponential and sums 2.5),
-// with 16 exponentials a clock of an SM next: 2,048 rows of 151,936 take 129 us, 4.8 TB/s; 256 rows 27 us, where 104 of
+// with the exponentials next: 2,048 rows of 151,936 take 125 us, 5.0 TB/s; 256 rows 27 us, where 104 of
 // the SMs have two rows and the others one; 17 rows of fp32 17 us, mostly the chain from the first load to the result.
 //
 // A cluster of up to 8 CTAs shares a row where there are few rows: they write states and lists to the first one, which
@@ -270,29 +273,35 @@ __device__ __forceinline__ State merge(State a, State b) {
     return a;
 }
 
-// A thread's running state: the maximum, and the sums of the entries against it in two parts, the chunk that holds it
-// (which counts the maximum itself, 1, and in S what rounding leaves of its 0) and the rest.
+// A thread's running state: the maximum m, and the sums of the entries against `ref`, which is at most kLag below it (so
+// that they are rarely scaled), in two parts: the chunk that holds the maximum and the rest.
 struct Running {
-    float m = -INFINITY, rest = 0.f, held = 0.f, s = 0.f, s_held = 0.f;
+    float m = -INFINITY, ref = -INFINITY, rest = 0.f, held = 0.f, s = 0.f, s_held = 0.f;
     int chunk = 0;  // that chunk; ~i: the single entry i
-    __device__ __forceinline__ void move(float to, int c) {
-        const float d = m == -INFINITY ? -1e30f : fmaxf(m - to, -1e30f), e = exp_neg(d);
-        const float w = rest + held;
-        s = e * (s + s_held + d * w);
-        rest = e * w;
-        held = s_held = 0.f;
-        m = to;
+    __device__ __forceinline__ void move(float to) {  // the reference
+        const float d = ref == -INFINITY ? -1e30f : fmaxf(ref - to, -1e30f), e = exp_neg(d);
+        s = e * (s + d * rest);
+        s_held = e * (s_held + d * held);
+        rest *= e;
+        held *= e;
+        ref = to;
+    }
+    __device__ __forceinline__ void hold(float top, int c, float z, float sum) {  // c has the maximum now
+        rest += held, s += s_held;
+        held = z, s_held = sum;
+        m = top;
         chunk = c;
     }
 };
+constexpr float kLag = 8.f;
 
 // An entry by itself.
 __device__ __forceinline__ void take_one(Running &r, float x, int i) {
     if (x > r.m) {
-        r.move(x, ~i);
-        r.held = 1.f;
+        r.move(x);
+        r.hold(x, ~i, 1.f, 0.f);
     } else {
-        const float d = max_nan(x - (r.m == -INFINITY ? 0.f : r.m), -1e30f), e = exp_neg(d);
+        const float d = max_nan(x - (r.ref == -INFINITY ? 0.f : r.ref), -1e30f), e = exp_neg(d);
         r.rest += e;
         r.s += e * d;
     }
@@ -402,9 +411,9 @@ __global__ void __launch_bounds__(kThreads + 32, kCtas) logprobs_kernel(const Lo
             }
             const float mb = Ty::top(Ty::larger(Ty::larger(top[0], top[1]), Ty::larger(top[2], top[3])));
             const bool moved = mb > r.m;
-            if (moved) r.move(mb, c);
+            if (mb > r.ref + kLag) r.move(mb);
             // 2^(x log2(e) - C) = exp(x - m) 2^off, off what C is below m log2(e)
-            const float m = r.m < -4.f * kWide ? 0.f : r.m;
+            const float m = r.ref < -4.f * kWide ? 0.f : r.ref;
             const float l2e = 1.4426950408889634f, C = m * l2e;
             const float off = fmaf(m, l2e, -C);
             const uint64_t l2 = f2_pack(__float_as_uint(l2e), __float_as_uint(l2e));
@@ -443,7 +452,7 @@ __global__ void __launch_bounds__(kThreads + 32, kCtas) logprobs_kernel(const Lo
             const float by = 1.f - 0.69314718f * off;  // 2^-off but for 2^-24: off is 2^-12 at most for kWide
             s = (s - off * z) * (0.69314718f * by), z *= by;
             if (moved)
-                r.held = z, r.s_held = s;
+                r.hold(mb, c, z, s);
             else
                 r.rest += z, r.s += s;
         };
@@ -474,40 +483,33 @@ __global__ void __launch_bounds__(kThreads + 32, kCtas) logprobs_kernel(const Lo
             before += known && precedes(x, i);
         });
 
-        // The CTA's maximum.  A thread's largest key is at least `sure`: its maximum's index is somewhere in its chunk,
-        // and without one above -inf it has entries of -inf or NaN, or none.  Group i has lane i of each warp.
+        // The CTA's maximum, and in `order_of`'s order the largest entry of each thread; without one above -inf it has
+        // entries of -inf or NaN, or none (0).  Group i has lane i of each warp.
         float M = r.m;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         if (lane == 0) red_m[warp] = M;
-        u64 top_key = key_of(-INFINITY, 0);
-        if (r.m > -INFINITY) top_key = key_of(r.m, r.chunk < 0 ? ~r.chunk : sl.index(sl.vector(r.chunk, 0)));
-        if (K > 0) {
-            u64 sure = 0;
-            if (r.m > -INFINITY)
-                sure = key_of(r.m, r.chunk < 0 ? ~r.chunk : sl.index(sl.vector(r.chunk, kVecs)));
-            else if (sl.vector(0, 0) < sl.v1 || tid < sl.head || sl.tail0 + tid < sl.tail1)
-                sure = key_of(r.rest == r.rest ? -INFINITY : __uint_as_float(0x7FFFFFFFu), 0x7FFFFFFF);
-            list[tid] = sure;
-        }
+        uint32_t *tops = reinterpret_cast<uint32_t *>(list);
+        const uint32_t top = r.m > -INFINITY || (r.rest == r.rest && (sl.vector(0, 0) < sl.v1 || tid < sl.head || sl.tail0 + tid < sl.tail1))
+                                 ? order_of(r.m) : 0u;
+        if (K > 0) tops[tid] = top;
         sync_rows();
         M = red_m[0];
 #pragma unroll
         for (int i = 1; i < kWarps; ++i) M = fmaxf(M, red_m[i]);
-        u64 bound = 0;
+        uint32_t bound = 0;
         if (K > 0) {
-            // the K-th largest of the groups' bounds (0 where fewer groups have one: then everything is a candidate)
-            u64 mine_g = list[lane];
+            // the K-th largest of the groups' (0 where fewer groups have one: then everything is a candidate)
+            uint32_t mine_g = tops[lane];
 #pragma unroll
-            for (int i = 1; i < kWarps; ++i) mine_g = max(mine_g, list[32 * i + lane]);
-            int above = 0;
-#pragma unroll 8
-            for (int i = 0; i < 32; ++i) {
-                const u64 other = __shfl_sync(0xffffffffu, mine_g, i);
-                above += other > mine_g || (other == mine_g && i < lane);
+            for (int i = 1; i < kWarps; ++i) mine_g = max(mine_g, tops[32 * i + lane]);
+            for (int k = 0;; ++k) {
+                bound = __reduce_max_sync(0xffffffffu, mine_g);
+                if (k == K - 1) break;
+                const uint32_t has = __ballot_sync(0xffffffffu, mine_g == bound);
+                if (lane == __ffs(has) - 1) mine_g = 0;
             }
-            bound = __shfl_sync(0xffffffffu, mine_g, __ffs(__ballot_sync(0xffffffffu, above == K - 1)) - 1);
-            if (sl.vector(0, 0) < sl.v1 && top_key >= bound) who[atomicAdd(&threads, 1)] = (unsigned short)tid;
+            if (sl.vector(0, 0) < sl.v1 && (top >= bound || r.m == -INFINITY)) who[atomicAdd(&threads, 1)] = (unsigned short)tid;
             if (tid < kMaxTop) given[0].best[tid] = 0;
         }
         if (!(fabsf(M) <= kWide)) {  // alike in the CTA: every entry by itself
@@ -523,8 +525,11 @@ __global__ void __launch_bounds__(kThreads + 32, kCtas) logprobs_kernel(const Lo
 
         // sums against the CTA's maximum; those who hold it sum its chunk again without it
         const bool holds = r.m == M && M > -INFINITY;
+        const float by = max_nan(r.ref - M, -1e30f), e0 = exp_neg(by);  // the reference's distance
         float z = r.rest, s = r.s;
         if (holds) {
+            s = e0 * (s + by * z);
+            z *= e0;
             if (r.chunk >= 0) {
                 uint4 y[kVecs];
 #pragma unroll
@@ -547,9 +552,9 @@ __global__ void __launch_bounds__(kThreads + 32, kCtas) logprobs_kernel(const Lo
                 }
             }
         } else if (r.m > -INFINITY) {
-            const float d = max_nan(r.m - M, -1e30f), e = exp_neg(d), w = r.rest + r.held;
-            s = e * (s + r.s_held + d * w);
-            z = e * w;
+            const float w = z + r.held;
+            s = e0 * (s + r.s_held + by * w);
+            z = e0 * w;
         } else {
             z += r.held;  // nothing, or NaN
         }
@@ -582,9 +587,9 @@ __global__ void __launch_bounds__(kThreads + 32, kCtas) logprobs_kernel(const Lo
             }
         };
         if (K > 0) {
-            const float least = value_of((uint32_t)(bound >> 32));  // of a candidate; NaN: any
+            const float least = value_of(bound);  // of a candidate; NaN: any
             auto offer = [&](u64 key) {
-                if (key >= bound) {
+                if ((uint32_t)(key >> 32) >= bound) {
                     const int at = atomicAdd(&count, 1);
                     if (at < kList) list[at] = key;
                 }
