@@ -649,9 +649,9 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                     // All softmax threads share the sweep and leave it together.
                     const int valid = min(kKeys, it.k_end - key0);
                     bool found = false;
-                    // With two panels a tile and five stages a panel's slot held one of the tile before: done with, so that
-                    // the wait's parity means this panel.
-                    if (!two && i > 0 &&
+                    // With two panels a tile (one-tile items) and five stages a panel's slot may have held one of the tile
+                    // before, which these scores do not show to be done: so that the wait's parity means this panel.
+                    if (C::kPanels > 1 && i > 0 &&
                         !__all_sync(0xffffffffu, mbar_wait(bar(kODone + ((i - 1) & 1)), ((i - 1) >> 1) & 1, kWaitNs)))
                         ok = false;
                     for (int pp = 0; pp < C::kPanels; ++pp) {

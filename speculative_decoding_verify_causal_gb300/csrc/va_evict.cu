@@ -356,8 +356,10 @@ int verify_attn_evict(void *k_pages, void *v_pages, float *k_scale, float *v_sca
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    cudaError_t e = cudaFuncSetAttribute(va::evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         va::kMaxCached * (int)sizeof(uint32_t));
+    cudaError_t e = cudaSuccess;
+    if (p.cached > 4096)  // with the static part past 32 KB: it has to be asked for
+        e = cudaFuncSetAttribute(va::evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 va::kMaxCached * (int)sizeof(uint32_t));
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, va::evict_select_kernel, p);
     if (e == cudaSuccess) {
         const int64_t most = (int64_t)p.half * p.units;  // threads' worth of work of a head, at most
