@@ -725,7 +725,8 @@ int verify_attn_chunk(const va_chunk_plan *plan, const va_heads *q, const void *
  *                        j < L_b - n_b (the new tokens start from nothing)
  * with lse as verify_attn_chunk gives it (a row with lse -inf gives nothing).
  * Entry (b, g, j) of weights is weights[b * weights_stride_seq + g *
- * weights_stride_head + j]; entries from L_b on are left as they are.  slot_pos
+ * weights_stride_head + j]; rows (b, g) may not lie on one another; entries from
+ * L_b on are left as they are.  slot_pos
  * (int32, strides as weights; NULL: not kept) receives positions[row] (int32
  * [tokens]) at the new tokens' places: the order of age in a cache whose rows
  * verify_attn_evict has moved.  Plan, q, cache, block table and num_pages as for
@@ -785,8 +786,9 @@ int verify_attn_logprobs(const void *logits, int64_t stride, va_float_type type,
  * with a block-table entry that is negative or, for num_pages > 0, not below
  * it sets VA_PAGES_BAD_ENTRY (flags may be NULL; the call only ORs into it).
  * Layouts: cache, block table and seq_lens as for verify_attn; weights fp32 and
- * slot_pos int32 [num_seqs, num_kv_heads, num_slots] with the strides given;
- * keep_lens, recent_from, new_lens int32 [num_seqs]; workspace: at least
+ * slot_pos int32 [num_seqs, num_kv_heads, num_slots] with the strides given, rows
+ * not on one another; keep_lens, recent_from, new_lens int32 [num_seqs], new_lens
+ * apart from the others and from seq_lens; workspace: at least
  * verify_attn_evict_workspace_bytes (0 for sizes that are rejected), 16-byte
  * aligned, no initialisation; calls that share one must be ordered on one
  * stream.  num_seqs * num_kv_heads <= 65535, num_slots <= 2^30.  Returns VA_OK

@@ -14,6 +14,7 @@ struct va_chunk_plan {
     int num_seqs, Hq, Hkv, G, D, kv_dtype, tpt, num_sms, device;
     int total;       // rows of q, out and lse that the chunks take
     int max_blocks;  // block-table entries of the longest sequence that takes part
+    int max_len;     // and its length
     int num_items, num_groups, num_parts, max_tiles, num_blocks, cluster;
     void *dev_mem;
     va::ChunkItem *items;
@@ -184,8 +185,9 @@ int plan_host(const int32_t *chunk_lens, const int32_t *seq_lens, int B, int Hq,
     p.num_sms = num_sms;
     for (int b = 0; b < B; ++b) {
         p.total += chunk_lens[b];
-        if (chunk_lens[b] > 0) p.max_blocks = std::max(p.max_blocks, (seq_lens[b] + VA_PAGE_SIZE - 1) / VA_PAGE_SIZE);
+        if (chunk_lens[b] > 0) p.max_len = std::max(p.max_len, seq_lens[b]);
     }
+    p.max_blocks = (p.max_len + VA_PAGE_SIZE - 1) / VA_PAGE_SIZE;
     p.num_items = (int)g.items.size();
     p.num_groups = (int)g.groups.size();
     p.num_parts = g.num_parts;
@@ -373,7 +375,8 @@ int verify_attn_chunk_weights(const va_chunk_plan *p, const va_heads *q, const v
     int rc = check_q(p, q, qv);
     if (rc != VA_OK) return rc;
     if (!k_pages || !block_table || !lse || !weights || num_pages < 0 || block_table_stride < p->max_blocks ||
-        (slot_pos && !positions) || weights_stride_seq < 0 || weights_stride_head < 0)
+        (slot_pos && !positions) || weights_stride_seq < 0 || weights_stride_head < 0 ||
+        va::rows_overlap(weights_stride_seq, weights_stride_head, p->num_seqs, p->Hkv, p->max_len))
         return VA_ERR_INVALID_ARGUMENT;
     if (p->kv_dtype != VA_BF16 && !k_scale) return VA_ERR_INVALID_ARGUMENT;
     if (!aligned(k_pages, 16) || !aligned(block_table, 4) || !aligned(k_scale, 4) || !aligned(lse, 4) ||

@@ -324,7 +324,11 @@ int verify_attn_evict(void *k_pages, void *v_pages, float *k_scale, float *v_sca
                           (const void *)weights, (const void *)slot_pos, (const void *)keep_lens, (const void *)recent_from,
                           (const void *)ref_count, (const void *)new_lens, (const void *)flags})
         if (reinterpret_cast<uintptr_t>(x) % 4) return VA_ERR_INVALID_ARGUMENT;
-    if (num_slots > (1 << 30)) return VA_ERR_INVALID_ARGUMENT;
+    if (num_slots > (1 << 30) || va::rows_overlap(stride_seq, stride_head, num_seqs, num_kv_heads, num_slots))
+        return VA_ERR_INVALID_ARGUMENT;
+    // every head of a sequence reads these, and one writes new_lens
+    for (const int32_t *x : {seq_lens, keep_lens, recent_from})
+        if (x && x < new_lens + num_seqs && new_lens < x + num_seqs) return VA_ERR_INVALID_ARGUMENT;
     const int bits = kv_dtype == VA_BF16 ? 16 : kv_dtype == VA_INT4 ? 4 : kv_dtype == VA_INT2 ? 2 : 8;
     const int heads = num_seqs * num_kv_heads, row = head_dim * bits / 8;
     va::EvictParams p = {};

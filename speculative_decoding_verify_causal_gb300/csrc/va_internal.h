@@ -78,6 +78,17 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 // the stream has completed and its writes are visible.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Whether rows of `n` elements, B x H of them with these strides (not negative), lie on one another.
+inline bool rows_overlap(int64_t stride_seq, int64_t stride_head, int B, int H, int64_t n) {
+    typedef __int128 wide;
+    if (n < 1 || (B < 2 && H < 2)) return false;
+    if (B < 2) return stride_head < n;
+    if (H < 2) return stride_seq < n;
+    const bool heads_inside = stride_head >= n && stride_seq >= (wide)(H - 1) * stride_head + n;
+    const bool seqs_inside = stride_seq >= n && stride_head >= (wide)(B - 1) * stride_seq + n;
+    return !heads_inside && !seqs_inside;
+}
+
 // Remember a failing CUDA call for verify_attn_last_cuda_error (thread-local).
 void note_cuda_error(cudaError_t e);
 

@@ -180,7 +180,7 @@ def test_calls_without_a_plan():
 
 EVICT = dict(k_pages=4096, v_pages=4096, k_scale=4096, v_scale=4096, kv_dtype=2, block_table=4096, block_table_stride=4,
              seq_lens=4096, num_seqs=2, num_kv_heads=2, head_dim=64, num_pages=8, weights=4096, slot_pos=None, stride_seq=128,
-             stride_head=64, num_slots=64, keep_lens=4096, num_sinks=0, recent_from=None, ref_count=None, new_lens=4096,
+             stride_head=64, num_slots=64, keep_lens=4096, num_sinks=0, recent_from=None, ref_count=None, new_lens=8192,
              workspace=4096, flags=None, stream=None)
 
 
@@ -188,6 +188,10 @@ EVICT = dict(k_pages=4096, v_pages=4096, k_scale=4096, v_scale=4096, kv_dtype=2,
     (dict(head_dim=96), -2), (dict(kv_dtype=9), -2), (dict(num_seqs=0), -1), (dict(num_seqs=40000), -1),
     (dict(num_kv_heads=0), -1), (dict(num_slots=-1), -1), (dict(num_slots=2 ** 30 + 2), -1), (dict(num_sinks=-1), -1),
     (dict(block_table_stride=-1), -1), (dict(num_pages=-1), -1), (dict(stride_seq=-1), -1), (dict(stride_head=-1), -1),
+    # rows of weights on one another, with extents past 63 bits too; new lengths over what other heads still read
+    (dict(stride_seq=0), -1), (dict(stride_head=0), -1), (dict(stride_head=63), -1), (dict(stride_seq=127), -1),
+    (dict(stride_seq=64, stride_head=127), -1), (dict(stride_seq=2 ** 62, stride_head=2 ** 62), -1),
+    (dict(new_lens=4096), -1), (dict(new_lens=4100), -1), (dict(new_lens=4092), -1), (dict(recent_from=8188), -1),
     *[(dict([(n, None)]), -1) for n in ("k_pages", "v_pages", "k_scale", "v_scale", "block_table", "seq_lens", "weights",
                                         "keep_lens", "new_lens", "workspace")],
     *[(dict([(n, 4104)]), -1) for n in ("k_pages", "v_pages", "workspace")],

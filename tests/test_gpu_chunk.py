@@ -350,6 +350,11 @@ def test_chunk_argument_errors(va):
                    dict(weights=w.transpose(1, 2).contiguous().transpose(1, 2)), dict(num_pages=b.P + 1)):
         with pytest.raises(ValueError):
             va.verify_attn_chunk_weights(plan, **dict(good, **change))
+    for on_one_another in (w[:1].expand(2, 2, 60), w[:, :1].expand(2, 2, 60), torch.as_strided(w, (2, 2, 60), (59, 120, 1))):
+        with pytest.raises(va.VerifyAttnError):
+            va.verify_attn_chunk_weights(plan, **dict(good, weights=on_one_another))
+    heads_first = torch.zeros(2, 2, 60, device="cuda").transpose(0, 1)  # and what does not
+    va.verify_attn_chunk_weights(plan, **dict(good, weights=heads_first))
 
 
 # ------------------------------------------------------------------ gathered weights
