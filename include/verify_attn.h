@@ -751,7 +751,8 @@ int verify_attn_chunk_weights(const va_chunk_plan *plan, const va_heads *q, cons
  * row with one likely token keep their bits.  Entries of -inf have no weight; a
  * row of nothing else gives log probabilities of -inf and entropy 0.  A NaN or
  * +inf makes the row's logprobs, entropy and top_logprobs NaN; NaN comes last in
- * the order.  A token outside [0, vocab) has log probability -inf and rank -1.
+ * the order.  (NaN also stands for a wait in the kernel that gave up after 2 s.)
+ * A token outside [0, vocab) has log probability -inf and rank -1.
  * Layouts (device): logits [num_rows, vocab] of `type`, rows `stride` elements
  * apart (any alignment of its type; rows of 16-byte alignment are read as they
  * lie), tokens int32 [num_rows], outputs contiguous; logprobs, ranks and
