@@ -29,8 +29,8 @@
 // Bound.  Two tiles of rows by 80 keys at head_dim 128 are 1,470 clocks of the tensor pipe.  bf16, 8,192 tokens of 32
 // heads of 128: 368 us, 78 % of the measured bf16 rate: the tensor pipe, less the tiles on the diagonal, items' starts
 // and ends.  Codes: the warps' issue slots (71 % taken; a softmax warp about 400 instructions a tile, of which 20 each
-// for the two scales) at head_dim 128, 48 sequences, 947 us; the shared memory's bandwidth at 256, where a tile has one
-// of rows and so twice the panels a product, 2,000 on 23,000 tokens, 1,517 us.
+// for the two scales) at head_dim 128, 48 sequences, 952 us; the shared memory's bandwidth at 256, where a tile has one
+// of rows and so twice the panels a product, 2,000 on 23,000 tokens, 1,522 us.
 // Why 80 keys: probabilities that take the place of their scores (64 keys, the first kernel) hold the next scores back
 // until their product is done; with 80 keys both have slots of their own beside O, which with an issuing warp for each
 // tile of rows took the prompt from 477 to 417 us and the 48 sequences from 1,498 to 1,145.  Sixteen softmax warps
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
         }
         mbar_init(bar(kOFinal), nq);
         mbar_init(bar(kQFull), 1);
-        mbar_init(bar(kQReady), 8 * nq);
+        mbar_init(bar(kQReady), (C::kQuant ? 8 : 4) * nq);
         mbar_init(bar(kSwept), 8 * nq);
         for (int i = 0; i < kScaleRing; ++i) mbar_init(bar(kScaleFree + i), 8 * nq);
         sts_u32(bar(kPoison), 0u);
@@ -395,15 +395,16 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
             // q as the MMA takes it: rows without a token are zero; for a cache of codes, fp16 scaled by a power of
             // two that brings the row's largest element into [2^14, 2^15)
             ok = __all_sync(0xffffffffu, mbar_wait(bar(kQFull), 0, kWaitNs));
-            // two threads of a row, each half of its elements
+            // Codes: two threads of a row, each half of its elements; else one, for the rows without a token.
             float prescale = 1.f;
             const uint32_t row = sbase + C::kQ + w * C::kQBytes;
-            auto unit = [&](int u) { return row + ((h * (D / 16) + u) / 8) * C::kQChunk + sw128(r, (h * (D / 16) + u) % 8); };
+            constexpr int kUnits = C::kQuant ? D / 16 : D / 8;
+            auto unit = [&](int u) { return row + ((h * kUnits + u) / 8) * C::kQChunk + sw128(r, (h * kUnits + u) % 8); };
             if constexpr (C::kQuant) {
                 float amax = 0.f;
                 if (row_ok) {
 #pragma unroll 2
-                    for (int u = 0; u < D / 16; ++u) {
+                    for (int u = 0; u < kUnits; ++u) {
                         const uint4 x = lds_u4(unit(u));
                         const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -418,12 +419,12 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                 if (amax > 0.f && amax < INFINITY)
                     prescale = __uint_as_float(min(254u, 268u - (__float_as_uint(amax) >> 23)) << 23);
             }
-            if (!row_ok) {
+            if (!row_ok && (C::kQuant || h == 0)) {
 #pragma unroll 2
-                for (int u = 0; u < D / 16; ++u) sts_u4(unit(u), make_uint4(0, 0, 0, 0));
-            } else if (C::kQuant) {
+                for (int u = 0; u < kUnits; ++u) sts_u4(unit(u), make_uint4(0, 0, 0, 0));
+            } else if (C::kQuant && row_ok) {
 #pragma unroll 2
-                for (int u = 0; u < D / 16; ++u) {
+                for (int u = 0; u < kUnits; ++u) {
                     const uint4 x = lds_u4(unit(u));
                     const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
                     uint32_t y[4];
@@ -438,9 +439,11 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                 sts_f32(stat + 4u * r, p.sm_scale_log2 / prescale);
                 sts_u32(stat + 4u * (kMmaRows + r), (uint32_t)(row_ok ? vis : -1));
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kQReady));
+            if (C::kQuant || h == 0) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kQReady));
+            }
             named_bar_sync(2 + w, 256);  // the rows' data
             // this thread's rows of the warp's 16: lane / 4 and 8 further, as row x; its columns of each 8: c, c + 1
             const int c = 2 * (lane & 3);
