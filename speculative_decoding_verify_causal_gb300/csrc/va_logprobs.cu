@@ -17,8 +17,9 @@
 //
 // The top alternatives are found by a threshold: of the maxima of 32 groups of threads the K-th largest is a lower
 // bound of the K-th largest entry.  The vectors of threads whose maximum reaches it are searched again (from L2) by the
-// whole CTA, which lists what reaches it, some 30 to 130 entries; those are ranked by counting.  Rows whose list
-// overflows (many equal entries) are searched K times instead.  Order: larger first, equal ones by index, NaN below -inf.
+// whole CTA, which lists what reaches it, some 30 to 130 entries; those are ranked by counting.  Where the list
+// overflows (many equal entries: masks), those above the bound and the first ones equal to it are listed instead; where
+// that does not do either, K searches.  Order: larger first, equal ones by index, NaN below -inf.
 //
 // Bound: instructions, about 7 an entry of bf16 (packed maximum and count 1.5, conversions 1, exponential and sums 2.5),
 // with the exponentials next: 2,048 rows of 151,936 take 125 us, 5.0 TB/s; 256 rows 27 us, where 104 of
@@ -56,6 +57,7 @@ constexpr int kChunk = kThreads * kVecs;               // vectors
 constexpr int kStages = 4;
 constexpr int kCtas = 3;     // of an SM
 constexpr int kList = 1024;  // candidates
+constexpr int kFirst = 512;  // entries of a slice whose ties with the bound are taken where there are too many
 constexpr int kTake = 16;    // chunks between takes of the packed counts
 constexpr uint32_t kRingBytes = kStages * kChunk * 16;
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -588,28 +590,52 @@ __global__ void __launch_bounds__(kThreads + 32, kCtas) logprobs_kernel(const Lo
         };
         if (K > 0) {
             const float least = value_of(bound);  // of a candidate; NaN: any
-            auto offer = [&](u64 key) {
-                if ((uint32_t)(key >> 32) >= bound) {
-                    const int at = atomicAdd(&count, 1);
-                    if (at < kList) list[at] = key;
-                }
-            };
             const int found = threads, each = (sl.v1 - sl.v0 + kThreads - 1) / kThreads;
-            for (int i = tid; i < found * each; i += kThreads) {
-                const int j = i / found, v = sl.v0 + j * kThreads + who[i - j * found];
-                if (v >= sl.v1) continue;
-                const uint4 y = __ldg(sl.body + v);
-                const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-                if (Ty::top(Ty::larger(Ty::larger(y.x, y.y), Ty::larger(y.z, y.w))) < least) continue;
-                float x[kN];
-                Ty::floats(w, x);
+            int have = 0;
+            bool above = false;
+#pragma unroll 1
+            for (;; above = true) {
+                // `above`: of what lies above the bound everything, of what is equal to it the first entries
+                const uint32_t from = bound + (above ? 1u : 0u);
+                auto offer = [&](float x, int i) {
+                    const uint32_t o = order_of(x);
+                    if (o >= from && *static_cast<volatile int *>(&count) <= kList) {  // else it has overflowed
+                        const int at = atomicAdd(&count, 1);
+                        if (at < kList) list[at] = (u64)o << 32 | (0xFFFFFFFFu - (uint32_t)i);
+                    }
+                };
+                for (int i = tid; i < found * each; i += kThreads) {
+                    const int j = i / found, v = sl.v0 + j * kThreads + who[i - j * found];
+                    if (v >= sl.v1) continue;
+                    const uint4 y = __ldg(sl.body + v);
+                    const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+                    if (Ty::top(Ty::larger(Ty::larger(y.x, y.y), Ty::larger(y.z, y.w))) < least) continue;
+                    float x[kN];
+                    Ty::floats(w, x);
 #pragma unroll
-                for (int k = 0; k < kN; ++k) offer(key_of(x[k], sl.index(v) + k));
+                    for (int k = 0; k < kN; ++k) offer(x[k], sl.index(v) + k);
+                }
+                sl.singles([&](int i) { offer(Ty::one(sl.row + i), i); });
+                if (above) {
+                    const int first = rank == 0 ? 0 : sl.index(sl.v0);
+                    for (int i = first + tid; i < min(first + kFirst, rank == 0 ? V : sl.index(sl.v1)); i += kThreads) {
+                        const uint32_t o = order_of(Ty::one(sl.row + i));
+                        if (o == bound) {
+                            const int at = atomicAdd(&count, 1);
+                            if (at < kList) list[at] = (u64)o << 32 | (0xFFFFFFFFu - (uint32_t)i);
+                        }
+                    }
+                }
+                sync_rows();
+                have = count;
+                if (above || have <= kList) break;
+                sync_rows();  // it is read
+                if (tid == 0) count = 0;
+                sync_rows();
             }
-            sl.singles([&](int i) { offer(key_of(Ty::one(sl.row + i), i)); });
-            sync_rows();
-            const int have = count;
-            if (have > kList) {
+            // (the second time the list holds the K largest if it holds as many)
+            const bool search = have > kList || (above && have < K);
+            if (search) {
                 // too many reach the bound: the largest key below the last one found, K times
                 u64 last = ~0ull;
                 for (int k = 0; k < K; ++k) {

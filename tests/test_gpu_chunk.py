@@ -650,6 +650,27 @@ def test_logprobs_of_large_and_masked_values(va, dtype, N):
                     assert torch.allclose(many[k], one[k].expand(many[k].shape), rtol=2.0 ** -12, atol=2.0 ** -9, equal_nan=True)
 
 
+@pytest.mark.parametrize("dtype,n", [(torch.float32, 4), (torch.bfloat16, 8), (torch.float16, 8)])
+def test_logprobs_alternatives_among_many_equal_entries(va, dtype, n):
+    """Ties with the threshold past every list: masks but for a few entries, and entries above it that one lane of each warp
+    has, more than the list holds, and NaN at a row's start."""
+    V, K = 60_000, 20
+    i = torch.arange(V)
+    rows = [torch.zeros(V), torch.full((V,), -float("inf")), torch.full((V,), torch.finfo(dtype).min),
+            torch.where(i // n % 32 == 0, 1.0 + (i * 7919 % V) / V, 0.0), torch.zeros(V)]
+    for row, at in ((0, 59_999), (1, 30_000), (2, 700)):
+        rows[row][at], rows[row][at // 2] = 2.0, 3.0
+    rows[4][:3000] = float("nan")
+    rows[4][40_000] = 1.0
+    for row in rows:
+        z = row.to(dtype)[None].cuda()
+        t = torch.full((1,), 40_000, dtype=torch.int32).cuda()
+        check_logprobs(va, z, t, K)
+        many = va.verify_attn_logprobs(z.expand(300, V), t.expand(300).contiguous(), K)  # one CTA a row
+        one = va.verify_attn_logprobs(z, t, K)
+        assert torch.equal(many[3], one[3].expand(300, K)) and torch.equal(many[1], one[1].expand(300))
+
+
 def test_logprobs_past_32_bits_and_argument_errors(va):
     N, V = 9, 300_000_000
     z = torch.zeros(N, V, dtype=torch.bfloat16, device="cuda")
