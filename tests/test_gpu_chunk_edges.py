@@ -6,7 +6,7 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from test_gpu_chunk import Batch  # noqa: E402
+from test_gpu_chunk import Batch, check_rows, cuda  # noqa: E402
 
 MOST = {"fp8_e4m3": 448.0, "int8": 127.0, "int4": 7.0, "int2": 1.0}
 
@@ -57,3 +57,22 @@ def test_chunk_sums_of_the_smallest_value_scales(va, kv, D):
     out, lse = b.run(va, plan)
     assert (out != 0).any(-1).all()
     b.check(out, lse)
+
+
+def verify(va, b, path="mma"):
+    """The verify step on a batch whose chunks are of one length: (out, lse)."""
+    plan = va.verify_attn_plan(b.lens, b.new[0], b.Hq, b.Hkv, b.D, b.kv, num_sms=1, path=path, block_table_stride=b.bt.shape[1])
+    out, lse = torch.empty_like(b.q), torch.empty(b.N, b.Hq, device="cuda")
+    va.verify_attn_with_plan(plan, b.q, b.kp, b.vp, b.ks, b.vs, b.bt, cuda(np.array(b.lens, np.int32)), b.new[0], out, lse)
+    return out, lse
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("kv", ["fp8_e4m3", "int8", "int4", "int2"])
+def test_verify_sums_of_the_smallest_value_scales(va, kv, D):
+    b = Batch([16, 16], [700, 250], 8, 2, D, kv, seed=32, v_std=2.0 ** -118 * MOST[kv] / 3)
+    for s in range(2):
+        score_of_key(b, s, 80, 7.75)
+    ref, ref_lse, size, reach = b.want()
+    out, lse = verify(va, b)
+    check_rows(kv, D, out.double().cpu().numpy(), lse.double().cpu().numpy(), ref, ref_lse, size, reach)
