@@ -53,10 +53,9 @@ namespace {
 
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kRescaleLog2 = 8.0f;
-// From this power of the values' scales on the running maximum does not lag: a thread adds 20 probabilities of up to
-// 2^(8 + beta) before the sum is scaled back, and 20 x 2^123 is the last that binary32 holds; without the lag they are
-// 2^118 at most.
-constexpr int kNoLagBeta = 115;
+// The largest power of two that the values' scales are brought up by: a thread adds 20 probabilities of up to 2^(8 + beta)
+// before the sum is scaled back, and 20 x 2^123 is the last that binary32 holds.
+constexpr int kMaxBeta = 115;
 constexpr int kScaleRing = 4;
 constexpr int kBadRing = 16;   // tiles whose bad pages are remembered: more than the ring holds ahead
 constexpr int kMaxStages = 8;
@@ -542,7 +541,7 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     mx[x] *= c_r[x];
-                    move |= mx[x] > m_run[x] + (C::kQuant && beta[x] > kNoLagBeta ? 0.f : kRescaleLog2);
+                    move |= mx[x] > m_run[x] + kRescaleLog2;
                     if constexpr (C::kQuant) {
                         const float rr = mv[x] * __uint_as_float((uint32_t)(127 + beta[x]) << 23);
                         move |= !(rr >= 0x1p-6f && rr < 4.f);
@@ -558,22 +557,20 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         fo[x] = 1.f;
-                        int to = beta[x];
-                        if (C::kQuant && mv[x] > 0.f && mv[x] < INFINITY) {
-                            const float rr = mv[x] * __uint_as_float((uint32_t)(127 + beta[x]) << 23);
-                            // mv in [2^(E-127), 2^(E-126)); beta at most 118 and at least -73, so that p 2^beta
-                            // stays finite, and the sums, which take it, lose nothing above 2^-53
-                            if (!(rr >= 0x1p-6f && rr < 4.f))
-                                to = 127 - max(9, min(200, (int)((__float_as_uint(mv[x]) >> 23) & 0xFFu)));
-                        }
-                        if (mx[x] > m_run[x] + (to > kNoLagBeta ? 0.f : kRescaleLog2)) {
+                        if (mx[x] > m_run[x] + kRescaleLog2) {
                             if (m_run[x] != -INFINITY) fo[x] = ex2_approx(m_run[x] - mx[x]);
                             m_run[x] = mx[x];
                             l_run[x] *= fo[x];
                         }
-                        if (to != beta[x]) {
-                            fo[x] *= __uint_as_float((uint32_t)(127 + max(-126, min(127, to - beta[x]))) << 23);
-                            beta[x] = to;
+                        if (C::kQuant && mv[x] > 0.f && mv[x] < INFINITY) {
+                            const float rr = mv[x] * __uint_as_float((uint32_t)(127 + beta[x]) << 23);
+                            if (!(rr >= 0x1p-6f && rr < 4.f)) {
+                                // mv in [2^(E-127), 2^(E-126)); beta at least -73, so that the sums, which take it, lose
+                                // nothing above 2^-53
+                                const int E = max(127 - kMaxBeta, min(200, (int)((__float_as_uint(mv[x]) >> 23) & 0xFFu)));
+                                fo[x] *= __uint_as_float((uint32_t)(127 + max(-126, min(127, 127 - E - beta[x]))) << 23);
+                                beta[x] = 127 - E;
+                            }
                         }
                     }
                     if (i > 0 && __any_sync(0xffffffffu, fo[0] != 1.f || fo[1] != 1.f)) {

@@ -71,9 +71,9 @@ constexpr int kMinRawStages = 3;
 constexpr int kBfStages = 3;        // bf16: 64-key stages TMA'd straight into MMA layout
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kRescaleLog2 = 8.0f;
-// From this power of the value scales on the running maximum does not lag: a thread adds 32 probabilities of up to
-// 2^(8 + beta) before the sum is scaled back, and 32 x 2^122 is the last that binary32 holds.
-constexpr int kNoLagBeta = 114;
+// The largest power of two that the value scales are brought up by: a thread adds 32 probabilities of up to 2^(8 + beta)
+// before the sum is scaled back, and 32 x 2^122 is the last that binary32 holds.
+constexpr int kMaxBeta = 114;
 constexpr int kScaleRing = 4;       // per-tile k/v scales handed to the softmax warps
 constexpr int kRingFloats = 2 * kTile + 4;  // one ring slot: k[64], v[64], largest v scale of each half, pad
 constexpr int kMaxItemPages = kMmaMaxItemTokens / VA_PAGE_SIZE;  // page ids staged in smem
@@ -568,6 +568,14 @@ mma_partial_kernel(const __grid_constant__ MmaParams mp) {
                 named_bar_sync(pair_bar, 64);
                 mt = fmaxf(mt, lds_f32(xmax + 4u * ((b * 2 + 1 - half) * 128 + r)));
                 const float m_tile = mt * c_r;  // -inf stays -inf (c_r > 0)
+                const bool grow = m_tile > m_run + kRescaleLog2;
+                const bool rescale = grow && m_run != -INFINITY;
+                float alpha = 1.f;
+                if (grow) {
+                    if (rescale) alpha = ex2_approx(m_run - m_tile);
+                    m_run = m_tile;
+                    l_run *= alpha;
+                }
                 // Value normaliser (quantised caches): P carries p * v_scale * 2^beta
                 // with 2^beta bringing the tile's largest v scale into [1, 2); beta
                 // is kept while that product stays in [2^-6, 4), so that P stays in
@@ -580,21 +588,12 @@ mma_partial_kernel(const __grid_constant__ MmaParams mp) {
                     if (mv > 0.f) {
                         const float rr = mv * __uint_as_float((uint32_t)(127 + beta) << 23);
                         if (i == 0 || !(rr >= 0x1p-6f && rr < 4.f)) {
-                            // mv in [2^(E-127), 2^(E-126)): beta = 127 - E, capped at 118
-                            // so that p 2^beta stays finite in fp32
-                            const int E = max(9, min(253, (int)((__float_as_uint(mv) >> 23) & 0xFFu)));
+                            // mv in [2^(E-127), 2^(E-126)): beta = 127 - E
+                            const int E = max(127 - kMaxBeta, min(253, (int)((__float_as_uint(mv) >> 23) & 0xFFu)));
                             dbeta = i == 0 ? 0 : (127 - E) - beta;
                             beta = 127 - E;
                         }
                     }
-                }
-                const bool grow = m_tile > m_run + (C::kQuant && beta > kNoLagBeta ? 0.f : kRescaleLog2);
-                const bool rescale = grow && m_run != -INFINITY;
-                float alpha = 1.f;
-                if (grow) {
-                    if (rescale) alpha = ex2_approx(m_run - m_tile);
-                    m_run = m_tile;
-                    l_run *= alpha;
                 }
                 // powers of two: exact
                 const float fo =
