@@ -56,6 +56,9 @@ constexpr float kRescaleLog2 = 8.0f;
 // The largest power of two that the values' scales are brought up by: a thread adds 20 probabilities of up to 2^(8 + beta)
 // before the sum is scaled back, and 20 x 2^123 is the last that binary32 holds.
 constexpr int kMaxBeta = 115;
+// A raise of beta looks at what O holds, and leaves it below 2^kHeld (the products to come add 2^49 at most: p vs 2^beta
+// is below 2^10, codes below 2^9).  Products that beta does not bring into fp16's reach then are below 2^-90 of what O holds.
+constexpr int kHeld = 120;
 constexpr int kScaleRing = 4;
 constexpr int kBadRing = 16;   // tiles whose bad pages are remembered: more than the ring holds ahead
 constexpr int kMaxStages = 8;
@@ -553,7 +556,8 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                     tc_fence_after();
                 }
                 if (__any_sync(0xffffffffu, move)) {
-                    float fo[2];
+                    float fo[2];  // what O is multiplied by
+                    bool raise = false;
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         fo[x] = 1.f;
@@ -568,8 +572,11 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                                 // mv in [2^(E-127), 2^(E-126)); beta at least -73, so that the sums, which take it, lose
                                 // nothing above 2^-53
                                 const int E = max(127 - kMaxBeta, min(200, (int)((__float_as_uint(mv[x]) >> 23) & 0xFFu)));
-                                fo[x] *= __uint_as_float((uint32_t)(127 + max(-126, min(127, 127 - E - beta[x]))) << 23);
-                                beta[x] = 127 - E;
+                                const int up = min(kHeld, 127 - E - beta[x]);  // down to -188: in two factors
+                                fo[x] = fo[x] * __uint_as_float((uint32_t)(127 + (up >> 1)) << 23) *
+                                        __uint_as_float((uint32_t)(127 + up - (up >> 1)) << 23);
+                                beta[x] += up;
+                                raise |= up > 0;
                             }
                         }
                     }
@@ -579,6 +586,27 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                             !__all_sync(0xffffffffu, mbar_wait(bar(kODone + ((i - 1) & 1)), ((i - 1) >> 1) & 1, kWaitNs)))
                             ok = false;
                         tc_fence_after();
+                        if (C::kQuant && __any_sync(0xffffffffu, raise)) {
+                            float top[2] = {0.f, 0.f};
+#pragma unroll 1
+                            for (int c0 = 0; c0 < D; c0 += 32) {
+                                uint32_t o[16];
+                                tmem_ld_16x256b(half_tm + C::kOCol + w * D + c0, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    top[(j >> 1) & 1] = fmaxf(top[(j >> 1) & 1], fabsf(__uint_as_float(o[j])));
+                            }
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {  // a row's four lanes: what it holds is below 2^held
+#pragma unroll
+                                for (int n = 1; n <= 2; n <<= 1) top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], n));
+                                const int held = (int)(__float_as_uint(top[x]) >> 23) + (int)(__float_as_uint(fo[x]) >> 23) - 252;
+                                const int cut = max(0, min(126, held - kHeld));
+                                fo[x] *= __uint_as_float((uint32_t)(127 - cut) << 23);
+                                beta[x] -= cut;
+                            }
+                        }
 #pragma unroll 1
                         for (int c0 = 0; c0 < D; c0 += 32) {
                             const uint32_t at = half_tm + C::kOCol + w * D + c0;

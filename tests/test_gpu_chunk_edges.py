@@ -25,21 +25,27 @@ def va():
     return va
 
 
-def score_of_key(b, s, first, value):
+def cells(b, s, first=0, last=None):
+    """Pages and slots of the keys [first, last) of sequence s."""
+    j = torch.arange(first, b.lens[s] if last is None else last)
+    return torch.from_numpy(b.table)[s][j // 16].long().cuda(), (j % 16).cuda()
+
+
+def ones(b, pages, at):
+    """The largest code in an element or all of a row."""
+    code = {"fp8_e4m3": 0x7E, "int8": 127, "int4": 7, "int2": 1}[b.kv]
+    if at is not None:
+        pages[(*at, slice(None), 0)] = code  # of the packed types the first element of the row's first byte
+    return {"int4": 0x77, "int2": 0x55}.get(b.kv, code)
+
+
+def score_of_keys(b, s, first, value):
     """Keys of sequence s from `first` on: zero but for element 0, whose product with q (also zero but there) makes the
     softmax's exponent, in powers of two, `value` at q[0] = sqrt(D); the keys before them: all zero."""
-    most = MOST[b.kv]
-    code = most if b.kv == "fp8_e4m3" else int(most)
-    for j in range(b.lens[s]):
-        page, slot = b.table[s, j // 16], j % 16
-        b.kp[page, slot] = 0
-        b.ks[page, slot] = 1.0
-        if j >= first:
-            if b.kv == "fp8_e4m3":
-                b.kp.view(torch.float8_e4m3fn)[page, slot, :, 0] = code
-            else:
-                b.kp[page, slot, :, 0] = code  # of the packed types the low bits of the first byte
-            b.ks[page, slot] = value * np.log(2.0) / code
+    b.kp[cells(b, s)] = 0
+    b.ks[cells(b, s)] = 1.0
+    ones(b, b.kp, cells(b, s, first))
+    b.ks[cells(b, s, first)] = value * np.log(2.0) / MOST[b.kv]
     b.q.zero_()
     b.q[..., 0] = b.D ** 0.5
 
@@ -51,7 +57,7 @@ def test_chunk_sums_of_the_smallest_value_scales(va, kv, D):
     2^8 against it, times the largest power of two that the scales are brought up by."""
     b = Batch([20, 3], [700, 250], 8, 2, D, kv, seed=31, v_std=2.0 ** -118 * MOST[kv] / 3)
     for s in range(2):
-        score_of_key(b, s, 80, 7.75)
+        score_of_keys(b, s, 80, 7.75)
     plan = b.plan(va, num_sms=1)  # keys not split: the first tile sets the maximum
     assert plan.info()["num_split_groups"] == 0
     out, lse = b.run(va, plan)
@@ -72,7 +78,44 @@ def verify(va, b, path="mma"):
 def test_verify_sums_of_the_smallest_value_scales(va, kv, D):
     b = Batch([16, 16], [700, 250], 8, 2, D, kv, seed=32, v_std=2.0 ** -118 * MOST[kv] / 3)
     for s in range(2):
-        score_of_key(b, s, 80, 7.75)
+        score_of_keys(b, s, 80, 7.75)
     ref, ref_lse, size, reach = b.want()
     out, lse = verify(va, b)
     check_rows(kv, D, out.double().cpu().numpy(), lse.double().cpu().numpy(), ref, ref_lse, size, reach)
+
+
+def values_of_two_sizes(kv, D, where, large, step, seed):
+    """Values of `large` but for the keys of `where`, which have value scales of 2^-118 and scores larger by `step` powers of
+    two."""
+    b = Batch([16], [4200], 4, 1, D, kv, seed=seed)
+    score_of_keys(b, 0, 4200, 0.0)
+    b.vp[:] = ones(b, b.vp, None)
+    b.vs[:] = large / MOST[kv]
+    at = cells(b, 0, *where)
+    b.vs[at] = 2.0 ** -118
+    if step:
+        ones(b, b.kp, at)
+        b.ks[at] = step * np.log(2.0) / MOST[kv]
+    return b
+
+
+# Nearly 4,000 keys make a sum of as many times the codes; then come more than a tile of either kernel's tiny values, which
+# are next to nothing beside the others (0), or all that counts (250), or not of fp16's reach from them (60: a key of a
+# probability of 2^-60 has no part, however large its value; the bound's second part).
+SIZES = [((3840, 4160), (3840, 4200), (0, 320)), [0.0, 60.0, 250.0], [1.0, 2.0 ** 20]]  # whole tiles of 64 and 80
+
+
+def check_two_sizes(b, out, lse, step):
+    ref, ref_lse, (size, small), reach = b.want()
+    check_rows(b.kv, b.D, out.double().cpu().numpy(), lse.double().cpu().numpy(), ref, ref_lse,
+               (size, small if step == 60 else 0 * small), reach)
+
+
+@pytest.mark.parametrize("kv", ["fp8_e4m3", "int8", "int4", "int2"])
+@pytest.mark.parametrize("step", SIZES[1])
+@pytest.mark.parametrize("large", SIZES[2])
+def test_chunk_tiles_of_tiny_values_among_ordinary_ones(va, kv, step, large):
+    for D in (64, 256):
+        for where in SIZES[0]:
+            b = values_of_two_sizes(kv, D, where, large, step, 33)
+            check_two_sizes(b, *b.run(va, b.plan(va, num_sms=1)), step)
