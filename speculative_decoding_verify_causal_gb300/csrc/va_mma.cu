@@ -74,6 +74,9 @@ constexpr float kRescaleLog2 = 8.0f;
 // The largest power of two that the value scales are brought up by: a thread adds 32 probabilities of up to 2^(8 + beta)
 // before the sum is scaled back, and 32 x 2^122 is the last that binary32 holds.
 constexpr int kMaxBeta = 114;
+// A raise of beta looks at what O holds, and leaves it below 2^kHeld (the products to come add 2^49 at most: p vs 2^beta
+// is below 2^10, codes below 2^9).  Products that beta does not bring into fp16's reach then are below 2^-90 of what O holds.
+constexpr int kHeld = 120;
 constexpr int kScaleRing = 4;       // per-tile k/v scales handed to the softmax warps
 constexpr int kRingFloats = 2 * kTile + 4;  // one ring slot: k[64], v[64], largest v scale of each half, pad
 constexpr int kMaxItemPages = kMmaMaxItemTokens / VA_PAGE_SIZE;  // page ids staged in smem
@@ -569,12 +572,11 @@ mma_partial_kernel(const __grid_constant__ MmaParams mp) {
                 mt = fmaxf(mt, lds_f32(xmax + 4u * ((b * 2 + 1 - half) * 128 + r)));
                 const float m_tile = mt * c_r;  // -inf stays -inf (c_r > 0)
                 const bool grow = m_tile > m_run + kRescaleLog2;
-                const bool rescale = grow && m_run != -INFINITY;
-                float alpha = 1.f;
+                float fo = 1.f;  // what O is multiplied by
                 if (grow) {
-                    if (rescale) alpha = ex2_approx(m_run - m_tile);
+                    if (m_run != -INFINITY) fo = ex2_approx(m_run - m_tile);
                     m_run = m_tile;
-                    l_run *= alpha;
+                    l_run *= fo;
                 }
                 // Value normaliser (quantised caches): P carries p * v_scale * 2^beta
                 // with 2^beta bringing the tile's largest v scale into [1, 2); beta
@@ -582,7 +584,7 @@ mma_partial_kernel(const __grid_constant__ MmaParams mp) {
                 // fp16's normal range whatever the values' magnitude.  Every thread
                 // takes the same decision from the same two maxima; O, which holds
                 // the earlier tiles at the previous beta, follows a change.
-                int dbeta = 0;
+                bool raise = false;
                 if (C::kQuant) {
                     const float mv = fmaxf(lds_f32(slot + 4u * (2 * kTile)), lds_f32(slot + 4u * (2 * kTile + 1)));
                     if (mv > 0.f) {
@@ -590,19 +592,39 @@ mma_partial_kernel(const __grid_constant__ MmaParams mp) {
                         if (i == 0 || !(rr >= 0x1p-6f && rr < 4.f)) {
                             // mv in [2^(E-127), 2^(E-126)): beta = 127 - E
                             const int E = max(127 - kMaxBeta, min(253, (int)((__float_as_uint(mv) >> 23) & 0xFFu)));
-                            dbeta = i == 0 ? 0 : (127 - E) - beta;
-                            beta = 127 - E;
+                            if (i == 0) {
+                                beta = 127 - E;
+                            } else {
+                                const int up = min(kHeld, 127 - E - beta);  // down to -240: in two factors
+                                fo = fo * __uint_as_float((uint32_t)(127 + (up >> 1)) << 23) *
+                                     __uint_as_float((uint32_t)(127 + up - (up >> 1)) << 23);
+                                beta += up;
+                                raise = up > 0;
+                            }
                         }
                     }
                 }
-                // powers of two: exact
-                const float fo =
-                    dbeta == 0 ? alpha : alpha * __uint_as_float((uint32_t)(127 + max(-126, min(127, dbeta))) << 23);
                 if (__any_sync(0xffffffffu, fo != 1.f) && i > 0) {
                     // O holds the earlier tiles: wait until PV(i-1) has landed
                     // (its commit completes the ((i-1)/2)-th phase of P buffer (i-1)%2)
                     if (!mbar_wait(bar(kPEmpty + ((i - 1) & 1)), ((i - 1) >> 1) & 1, kWaitNs)) { ok = false; }
                     tc_fence_after();
+                    if (C::kQuant && __any_sync(0xffffffffu, raise)) {  // alike in both warps of the pair
+                        float top = 0.f;
+#pragma unroll 1
+                        for (int c0 = 0; c0 < D; c0 += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(lane_tm + C::kOCol + c0, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) top = fmaxf(top, fabsf(__uint_as_float(o[k])));
+                        }
+                        named_bar_sync(pair_bar, 64);  // the other half is read
+                        const int held = (int)(__float_as_uint(top) >> 23) + (int)(__float_as_uint(fo) >> 23) - 252;
+                        const int cut = max(0, min(126, held - kHeld));  // what O holds is below 2^held
+                        fo *= __uint_as_float((uint32_t)(127 - cut) << 23);
+                        beta -= cut;
+                    }
 #pragma unroll 1
                     for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
                         uint32_t o[32];

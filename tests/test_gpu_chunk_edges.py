@@ -119,3 +119,13 @@ def test_chunk_tiles_of_tiny_values_among_ordinary_ones(va, kv, step, large):
         for where in SIZES[0]:
             b = values_of_two_sizes(kv, D, where, large, step, 33)
             check_two_sizes(b, *b.run(va, b.plan(va, num_sms=1)), step)
+
+
+@pytest.mark.parametrize("kv", ["fp8_e4m3", "int8", "int4", "int2"])
+@pytest.mark.parametrize("step", SIZES[1])
+@pytest.mark.parametrize("large", SIZES[2])
+def test_verify_tiles_of_tiny_values_among_ordinary_ones(va, kv, step, large):
+    for D in (64, 256):
+        for where in SIZES[0]:
+            b = values_of_two_sizes(kv, D, where, large, step, 34)
+            check_two_sizes(b, *verify(va, b), step)
