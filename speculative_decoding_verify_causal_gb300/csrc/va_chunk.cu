@@ -569,10 +569,10 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
                         if (C::kQuant && mv[x] > 0.f && mv[x] < INFINITY) {
                             const float rr = mv[x] * __uint_as_float((uint32_t)(127 + beta[x]) << 23);
                             if (!(rr >= 0x1p-6f && rr < 4.f)) {
-                                // mv in [2^(E-127), 2^(E-126)); beta at least -73, so that the sums, which take it, lose
-                                // nothing above 2^-53
-                                const int E = max(127 - kMaxBeta, min(200, (int)((__float_as_uint(mv[x]) >> 23) & 0xFFu)));
-                                const int up = min(kHeld, 127 - E - beta[x]);  // down to -188: in two factors
+                                // mv in [2^(E-127), 2^(E-126)); beta at least -100, so that the sums, which take it, lose
+                                // no key above 2^-26 of the largest (scales up to 2^107 then are in fp16's reach)
+                                const int E = max(127 - kMaxBeta, min(227, (int)((__float_as_uint(mv[x]) >> 23) & 0xFFu)));
+                                const int up = min(kHeld, 127 - E - beta[x]);  // down to -215: in two factors
                                 fo[x] = fo[x] * __uint_as_float((uint32_t)(127 + (up >> 1)) << 23) *
                                         __uint_as_float((uint32_t)(127 + up - (up >> 1)) << 23);
                                 beta[x] += up;

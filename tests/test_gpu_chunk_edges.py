@@ -65,6 +65,16 @@ def test_chunk_sums_of_the_smallest_value_scales(va, kv, D):
     b.check(out, lse)
 
 
+@pytest.mark.parametrize("kv", ["fp8_e4m3", "int8", "int4", "int2"])
+@pytest.mark.parametrize("scale", [2.0 ** 79, 2.0 ** 85, 2.0 ** 103])
+def test_chunk_of_the_largest_value_scales(va, kv, scale):
+    for D in (64, 256):
+        b = Batch([20, 3], [700, 250], 8, 2, D, kv, seed=35, v_std=scale * MOST[kv] / 4)
+        for s in range(2):
+            score_of_keys(b, s, 80, 7.75)
+        b.check(*b.run(va, b.plan(va, num_sms=1)))
+
+
 def verify(va, b, path="mma"):
     """The verify step on a batch whose chunks are of one length: (out, lse)."""
     plan = va.verify_attn_plan(b.lens, b.new[0], b.Hq, b.Hkv, b.D, b.kv, num_sms=1, path=path, block_table_stride=b.bt.shape[1])
