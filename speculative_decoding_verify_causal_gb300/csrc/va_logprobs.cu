@@ -60,7 +60,14 @@ constexpr int kList = 1024;  // candidates
 constexpr int kFirst = 512;  // entries of a slice whose ties with the bound are taken where there are too many
 constexpr int kTake = 16;    // chunks between takes of the packed counts
 constexpr uint32_t kRingBytes = kStages * kChunk * 16;
-constexpr uint64_t kWaitNs = 2000000000ull;
+// A wait that runs out leaves NaN.  The tests build a copy of this file in which a cluster's CTA of one rank loads only
+// the first chunk of its first row, so that its waits run out, and soon.
+#ifndef VA_LOGPROBS_WITHHELD
+#define VA_LOGPROBS_WITHHELD -1
+#define VA_LOGPROBS_WAIT_NS 2000000000ull
+#endif
+constexpr int kWithheld = VA_LOGPROBS_WITHHELD;
+constexpr uint64_t kWaitNs = VA_LOGPROBS_WAIT_NS;
 static_assert(kWarps * 32 <= kList && kTake * 4 * kVecs <= 256, "bounds go through the list; packed counts are exact");
 
 // Beyond this a maximum has too few bits behind the point for C; see above.  Reference points below -4 kWide are
@@ -351,6 +358,10 @@ __global__ void __launch_bounds__(kThreads + 32, kCtas) logprobs_kernel(const Lo
             for (int n = n0; n < p.rows && ok; n += step) {
                 const Slice<T> sl(p, n, rank);
                 for (int v = sl.v0; v < sl.v1 && ok; v += kChunk, ++g) {
+                    if (rank == kWithheld && v > sl.v0) {
+                        n = p.rows;
+                        break;
+                    }
                     const int st = g % kStages;
                     if (g >= kStages) ok = mbar_wait(empty(st), (g / kStages - 1) & 1, kWaitNs);
                     if (!ok) break;
@@ -359,6 +370,8 @@ __global__ void __launch_bounds__(kThreads + 32, kCtas) logprobs_kernel(const Lo
                     bulk_load(smem_u32(ring) + 16u * kChunk * st, sl.body + v, bytes, full(st));
                 }
             }
+            // every issued copy lands before the CTA ends
+            for (int i = max(0, g - kStages); i < g; ++i) ok &= mbar_wait(full(i % kStages), (i / kStages) & 1, kWaitNs);
             if (!ok) broken = 1;
         }
         __syncwarp();
@@ -394,7 +407,7 @@ __global__ void __launch_bounds__(kThreads + 32, kCtas) logprobs_kernel(const Lo
 
         Running r;
         typename Ty::Count counted;
-        const int chunks = sl.chunks();
+        const int chunks = broken ? 0 : sl.chunks();  // a wait ran out in an earlier row
         auto take_chunk = [&](int c) {
             const uint32_t at = smem_u32(ring) + 16u * (kChunk * (g % kStages) + tid);
             const bool whole = sl.v1 - sl.v0 - c * kChunk >= kChunk;
@@ -670,6 +683,8 @@ __global__ void __launch_bounds__(kThreads + 32, kCtas) logprobs_kernel(const Lo
             for (int i = 1; i < kWarps; ++i) zt += red_z[i], st += red_s[i], ct += red_c[i], wt += red_w[i];
             // of several that attain the maximum one is left out
             given[0].state = {M, wt > 1 ? zt + (float)(wt - 1) : zt, st};
+            const float none = __uint_as_float(0x7FFFFFFFu);
+            if (broken) given[0].state = {none, none, none};  // a wait ran out: NaN through every merge
             given[0].before = ct;
         }
         sync_rows();
@@ -690,7 +705,6 @@ __global__ void __launch_bounds__(kThreads + 32, kCtas) logprobs_kernel(const Lo
             all = merge(all, given[q].state);
             ahead += given[q].before;
         }
-        if (broken) all.m = all.z = __uint_as_float(0x7FFFFFFFu);  // a wait ran out
         const bool empty_row = all.m == -INFINITY && all.z == all.z;  // nothing has any weight
         if (all.m == INFINITY) all.z = __uint_as_float(0x7FFFFFFFu);
         const float log_z = log1pf(all.z);

@@ -1,12 +1,16 @@
 """GPU: ends of the ranges of the operators of a prompt worked in chunks.  Definitions, tolerances and helpers are those of
 ``test_gpu_chunk``."""
+import ctypes
+import os
+import subprocess
+
 import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from test_gpu_chunk import Batch, check_rows, cuda  # noqa: E402
+from test_gpu_chunk import Batch, check_rows, cuda, normal  # noqa: E402
 
 MOST = {"fp8_e4m3": 448.0, "int8": 127.0, "int4": 7.0, "int2": 1.0}
 
@@ -139,3 +143,39 @@ def test_verify_tiles_of_tiny_values_among_ordinary_ones(va, kv, step, large):
         for where in SIZES[0]:
             b = values_of_two_sizes(kv, D, where, large, step, 34)
             check_two_sizes(b, *verify(va, b), step)
+
+def with_loads_withheld(rank, where):
+    """The library with log probabilities in which the CTAs of one rank of a cluster get the first chunk of their first row only:
+    their next wait runs out after 5 ms."""
+    from speculative_decoding_verify_causal_gb300 import build
+    src, obj, out = os.path.join(build.CSRC, "va_logprobs.cu"), str(where / f"l{rank}.o"), str(where / f"l{rank}.so")
+    subprocess.run([build._nvcc(), *build.ARCH, "-O3", "-std=c++17", "-Xcompiler", "-fPIC", f"-DVA_LOGPROBS_WITHHELD={rank}",
+                    "-DVA_LOGPROBS_WAIT_NS=5000000ull", "-I", build.INCLUDE, "-I", build.CSRC, "-c", src, "-o", obj], check=True)
+    others = [os.path.join(build.BUILD_DIR, f) for f in os.listdir(build.BUILD_DIR)
+              if f.endswith(".o") and f != "va_logprobs.cu.o"]
+    subprocess.run([build._nvcc(), *build.ARCH, "-shared", "-cudart", "static", "-o", out, obj, *others], check=True)
+    call = ctypes.CDLL(out).verify_attn_logprobs
+    P, I = ctypes.c_void_p, ctypes.c_int
+    call.argtypes, call.restype = [P, ctypes.c_int64, I, P, I, I, I, P, P, P, P, P, P], I
+    return call
+
+
+@pytest.mark.parametrize("rank", [0, 1, 7])
+def test_logprobs_of_a_wait_that_ran_out(va, rank, tmp_path):
+    """NaN, whichever CTA of a row's cluster it was; and in all further rows of the CTA."""
+    call = with_loads_withheld(rank, tmp_path)
+    for N, V in ((3, 70_000), (2, 9_000), (1000, 6_000)):  # clusters of 8 and 2; two rows and more a CTA
+        x = normal(40, N, V)
+        tokens = torch.arange(N, dtype=torch.int32, device="cuda")
+        want = va.verify_attn_logprobs(x, tokens, 3)
+        got = [torch.empty_like(t) for t in want]
+        p = [t.data_ptr() for t in got]
+        rc = call(x.data_ptr(), V, va.VA_FLOAT_FP32, tokens.data_ptr(), N, V, 3, *p, torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        assert rc == 0
+        hit = rank < {3: 8, 2: 2, 1000: 1}[N]
+        for i in (0, 2, 4):
+            if hit:
+                assert torch.isnan(got[i]).all(), (N, V, i)
+            else:
+                assert torch.equal(got[i], want[i]), (N, V, i)
