@@ -285,6 +285,8 @@ int verify_attn_chunk_plan(const int32_t *chunk_lens, const int32_t *seq_lens, i
     if (e == cudaSuccess) e = copy(p->groups, g.groups.data(), sizeof(va::ChunkGroup) * g.groups.size());
     if (e == cudaSuccess) e = copy(p->blocks, g.blocks.data(), sizeof(va::WeightItem) * g.blocks.size());
     if (e == cudaSuccess) e = cudaMemset(p->flags, 0, 256);
+    // copies and the memset may still be under way, and streams that do not wait for the legacy one come next
+    if (e == cudaSuccess) e = cudaStreamSynchronize(cudaStreamLegacy);
     if (e != cudaSuccess) {
         cudaFree(p->dev_mem);
         delete p;

@@ -179,3 +179,27 @@ def test_logprobs_of_a_wait_that_ran_out(va, rank, tmp_path):
                 assert torch.isnan(got[i]).all(), (N, V, i)
             else:
                 assert torch.equal(got[i], want[i]), (N, V, i)
+
+
+@pytest.mark.parametrize("which", ["chunk"])
+def test_a_plan_is_on_the_device_when_it_is_returned(va, which):
+    """Nothing of it is under way on the legacy stream, which a side stream's first call does not wait for; on an idle
+    and on a full GPU."""
+    side, busy = torch.cuda.Stream(), normal(50, 4096, 4096)
+    legacy = torch.cuda.default_stream()
+    lib, code = va.library(), va.KV_DTYPE_CODES["int8"]
+    for B, full in [(1, 0), (4, 0), (64, 0), (1, 4), (64, 4)] * 20:
+        new, host = np.ones(B, np.int32), np.full(B, 3000, np.int32)
+        with torch.cuda.stream(side):
+            for _ in range(full):
+                busy @ busy
+        plan = ctypes.c_void_p()
+        if which == "chunk":
+            rc = lib.verify_attn_chunk_plan(new.ctypes.data, host.ctypes.data, B, 8, 8, 64, code, 0, ctypes.byref(plan))
+        else:
+            rc = lib.verify_attn_plan_ex(host.ctypes.data, B, 1, 8, 8, 64, code, 0, None, ctypes.byref(plan))
+        done = legacy.query()
+        assert rc == 0
+        (lib.verify_attn_chunk_plan_destroy if which == "chunk" else lib.verify_attn_plan_destroy)(plan)
+        assert done
+    torch.cuda.synchronize()
