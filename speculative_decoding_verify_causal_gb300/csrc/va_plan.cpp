@@ -453,6 +453,8 @@ int verify_attn_plan_ex(const int32_t *seq_lens, int B, int T, int Hq, int Hkv, 
         ok = cudaMemcpy(p->groups, g.groups.data(), sizeof(va::Group) * g.groups.size(),
                         cudaMemcpyHostToDevice) == cudaSuccess;
     if (ok) ok = cudaMemset(p->flags, 0, 256) == cudaSuccess;
+    // copies and the memset may still be under way, and streams that do not wait for the legacy one come next
+    if (ok) ok = cudaStreamSynchronize(cudaStreamLegacy) == cudaSuccess;
     if (!ok) {
         cudaGetLastError();
         cudaFree(mem);

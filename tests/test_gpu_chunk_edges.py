@@ -181,7 +181,7 @@ def test_logprobs_of_a_wait_that_ran_out(va, rank, tmp_path):
                 assert torch.equal(got[i], want[i]), (N, V, i)
 
 
-@pytest.mark.parametrize("which", ["chunk"])
+@pytest.mark.parametrize("which", ["chunk", "verify"])
 def test_a_plan_is_on_the_device_when_it_is_returned(va, which):
     """Nothing of it is under way on the legacy stream, which a side stream's first call does not wait for; on an idle
     and on a full GPU."""
