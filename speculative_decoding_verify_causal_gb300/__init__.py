@@ -1167,7 +1167,8 @@ def verify_attn_chunk(plan: ChunkPlan, q, k_pages, v_pages, k_scale, v_scale, bl
     refused.  Returns (out, lse)."""
     torch = _torch or _bind_torch()
     if _grad_mode() and (_wants_gradient(q) or _wants_gradient(k_pages) or _wants_gradient(v_pages)
-                         or _wants_gradient(k_scale) or _wants_gradient(v_scale) or _wants_gradient(out)):
+                         or _wants_gradient(k_scale) or _wants_gradient(v_scale) or _wants_gradient(out)
+                         or _wants_gradient(lse)):
         raise _gradient_refused("verify_attn_chunk")
     heads, device, index = _chunk_q(plan, q)
     kp, ks, pages = _chunk_cache(plan, k_pages, k_scale, "k", index)
@@ -1212,7 +1213,8 @@ def verify_attn_chunk_weights(plan: ChunkPlan, q, k_pages, k_scale, block_table,
     ``lse``: what ``verify_attn_chunk`` returned for the same queries.  ``slot_pos``
     (int32, shape and strides as ``weights``) with ``positions`` (int32 ``[tokens]``): also
     keeps the new tokens' positions, for ``verify_attn_evict``.  Other arguments as
-    for ``verify_attn_chunk``.  Returns ``weights``."""
+    for ``verify_attn_chunk``; in grad mode tensors that require a gradient are
+    refused.  Returns ``weights``."""
     torch = _torch or _bind_torch()
     if _grad_mode() and (_wants_gradient(q) or _wants_gradient(k_pages) or _wants_gradient(k_scale)
                          or _wants_gradient(lse) or _wants_gradient(weights)):
@@ -1297,9 +1299,13 @@ def verify_attn_evict(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens,
     slot's token; None: the slot) move into the first slots, in place.  Pass
     ``ref_count`` of a page pool whose sequences may share pages: sequences that do
     are left alone and flagged.  Call it for every layer, then give the result to
-    ``verify_attn_pages_resize``.  Definition in ``include/verify_attn.h``.  Returns the
-    new lengths, int32 ``[num_seqs]``."""
+    ``verify_attn_pages_resize``.  Definition in ``include/verify_attn.h``.  In grad mode
+    tensors that require a gradient are refused.  Returns the new lengths, int32
+    ``[num_seqs]``."""
     torch = _torch or _bind_torch()
+    if _grad_mode() and (_wants_gradient(weights) or _wants_gradient(k_pages) or _wants_gradient(v_pages)
+                         or _wants_gradient(k_scale) or _wants_gradient(v_scale)):
+        raise _gradient_refused("verify_attn_evict")
     code = _dtype_code(kv_dtype)
     device, index = _device_of(k_pages, "k_pages")
     f32, i32 = torch.float32, torch.int32
