@@ -710,8 +710,9 @@ int verify_attn_chunk_plan_device_flags(const va_chunk_plan *plan, int clear, in
  * behind the last sequence's are left as they are.  out may not overlap q.
  * block_table int32 [num_seqs, block_table_stride].  num_pages > 0: entries
  * outside [0, num_pages) are skipped (their keys read as absent; a row without
- * any key is 0 with lse -inf) and flagged; 0: unchecked.  Returns VA_OK when
- * enqueued, VA_ERR_NO_PLAN, VA_ERR_INVALID_ARGUMENT, VA_ERR_CUDA. */
+ * any key is 0 with lse -inf) and flagged; 0: unchecked.  A plan without
+ * tokens: nothing is looked at or done, here and in verify_attn_chunk_weights.
+ * Returns VA_OK when enqueued, VA_ERR_NO_PLAN, VA_ERR_INVALID_ARGUMENT, VA_ERR_CUDA. */
 int verify_attn_chunk(const va_chunk_plan *plan, const va_heads *q, const void *k_pages,
                       const void *v_pages, const float *k_scale, const float *v_scale,
                       const int32_t *block_table, int block_table_stride, int num_pages, void *out,

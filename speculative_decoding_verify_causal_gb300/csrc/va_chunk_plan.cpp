@@ -343,6 +343,7 @@ int verify_attn_chunk(const va_chunk_plan *p, const va_heads *q, const void *k_p
                       const float *k_scale, const float *v_scale, const int32_t *block_table, int block_table_stride,
                       int num_pages, void *out, float *lse, void *stream) {
     if (!p) return VA_ERR_NO_PLAN;
+    if (p->total == 0) return VA_OK;  // tensors without elements have no addresses
     va_heads qv;
     int rc = check_q(p, q, qv);
     if (rc != VA_OK) return rc;
@@ -352,7 +353,6 @@ int verify_attn_chunk(const va_chunk_plan *p, const va_heads *q, const void *k_p
     if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16) || !aligned(block_table, 4) ||
         !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(lse, 4))
         return VA_ERR_INVALID_ARGUMENT;
-    if (p->num_items == 0) return VA_OK;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     rc = bind_thread(s);
     if (rc != VA_OK) return rc;
@@ -373,6 +373,7 @@ int verify_attn_chunk_weights(const va_chunk_plan *p, const va_heads *q, const v
                               float *weights, int64_t weights_stride_seq, int64_t weights_stride_head, int accumulate,
                               int32_t *slot_pos, const int32_t *positions, void *stream) {
     if (!p) return VA_ERR_NO_PLAN;
+    if (p->total == 0) return VA_OK;  // tensors without elements have no addresses
     va_heads qv;
     int rc = check_q(p, q, qv);
     if (rc != VA_OK) return rc;
@@ -384,7 +385,6 @@ int verify_attn_chunk_weights(const va_chunk_plan *p, const va_heads *q, const v
     if (!aligned(k_pages, 16) || !aligned(block_table, 4) || !aligned(k_scale, 4) || !aligned(lse, 4) ||
         !aligned(weights, 4) || !aligned(slot_pos, 4) || !aligned(positions, 4))
         return VA_ERR_INVALID_ARGUMENT;
-    if (p->num_blocks == 0) return VA_OK;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     rc = bind_thread(s);
     if (rc != VA_OK) return rc;

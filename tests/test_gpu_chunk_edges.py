@@ -203,3 +203,18 @@ def test_a_plan_is_on_the_device_when_it_is_returned(va, which):
         (lib.verify_attn_chunk_plan_destroy if which == "chunk" else lib.verify_attn_plan_destroy)(plan)
         assert done
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "int8"])
+def test_a_batch_without_new_tokens(va, kv):
+    """Tensors without rows, which have no address; the outputs that the call makes."""
+    b = Batch([0, 0, 0], [0, 30, 17], 4, 2, 64, kv, seed=51)
+    plan = b.plan(va)
+    assert b.q.shape == (0, 4, 64)
+    out, lse = b.run(va, plan)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    w = torch.full((3, 2, 30), 2.0, device="cuda")
+    pos = torch.full((3, 2, 30), 7, dtype=torch.int32, device="cuda")
+    b.weigh(va, plan, lse, w, slot_pos=pos, positions=torch.empty(0, dtype=torch.int32, device="cuda"))
+    b.weigh(va, plan, lse, torch.empty(3, 2, 0, device="cuda"))
+    assert (w == 2).all() and (pos == 7).all() and va.verify_attn_chunk_plan_device_flags(plan) == 0
