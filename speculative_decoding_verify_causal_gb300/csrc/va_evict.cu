@@ -300,7 +300,9 @@ size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 extern "C" {
 
 size_t verify_attn_evict_workspace_bytes(int num_seqs, int num_kv_heads, int num_slots) {
-    if (num_seqs < 1 || num_kv_heads < 1 || num_slots < 0 || (int64_t)num_seqs * num_kv_heads > 65535) return 0;
+    if (num_seqs < 1 || num_kv_heads < 1 || num_slots < 0 || num_slots > (1 << 30) ||
+        (int64_t)num_seqs * num_kv_heads > 65535)
+        return 0;
     const size_t heads = (size_t)num_seqs * num_kv_heads;
     return align_up(heads * 4) + heads * (num_slots / 2) * sizeof(int2) + 16;
 }
@@ -324,7 +326,7 @@ int verify_attn_evict(void *k_pages, void *v_pages, float *k_scale, float *v_sca
                           (const void *)weights, (const void *)slot_pos, (const void *)keep_lens, (const void *)recent_from,
                           (const void *)ref_count, (const void *)new_lens, (const void *)flags})
         if (reinterpret_cast<uintptr_t>(x) % 4) return VA_ERR_INVALID_ARGUMENT;
-    if (num_slots > (1 << 30) || va::rows_overlap(stride_seq, stride_head, num_seqs, num_kv_heads, num_slots))
+    if (va::rows_overlap(stride_seq, stride_head, num_seqs, num_kv_heads, num_slots))
         return VA_ERR_INVALID_ARGUMENT;
     // every head of a sequence reads these, and one writes new_lens
     for (const int32_t *x : {seq_lens, keep_lens, recent_from})

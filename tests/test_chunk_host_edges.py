@@ -25,3 +25,8 @@ def test_outputs_and_moved_tensors_that_require_a_gradient_are_refused():
             call(w)
         with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
             call(w)
+
+
+def test_evict_workspace_of_more_slots_than_a_call_takes():
+    size = va.library().verify_attn_evict_workspace_bytes
+    assert size(1, 1, 2 ** 30) >= 2 ** 32 + 4 and size(1, 1, 2 ** 30 + 1) == size(1, 1, 2 ** 31 - 1) == 0
