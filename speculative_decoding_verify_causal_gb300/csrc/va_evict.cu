@@ -344,9 +344,12 @@ int verify_attn_evict(void *k_pages, void *v_pages, float *k_scale, float *v_sca
     p.bt_stride = block_table_stride, p.num_seqs = num_seqs, p.Hkv = num_kv_heads, p.num_pages = num_pages;
     p.num_sinks = num_sinks, p.half = num_slots / 2, p.slots = num_slots;
     p.units = row / 16;
+    int device = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
     // CTAs of a cluster: one for each 4,096 slots, as long as there are SMs for all
     p.cluster = 1;
-    while (p.cluster < va::kMaxCluster && num_slots > 4096 * p.cluster && heads * p.cluster * 2 <= 2 * 152) p.cluster *= 2;
+    while (p.cluster < va::kMaxCluster && num_slots > 4096 * p.cluster && heads * p.cluster * 2 <= 2 * sms) p.cluster *= 2;
     p.cached = std::min(va::kMaxCached, ((num_slots + p.cluster - 1) / p.cluster + 31) / 32 * 32);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaLaunchConfig_t cfg = {};
@@ -362,15 +365,14 @@ int verify_attn_evict(void *k_pages, void *v_pages, float *k_scale, float *v_sca
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    cudaError_t e = cudaSuccess;
-    if (p.cached > 4096)  // with the static part past 32 KB: it has to be asked for
+    if (e == cudaSuccess && p.cached > 4096)  // with the static part past 32 KB: it has to be asked for
         e = cudaFuncSetAttribute(va::evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  va::kMaxCached * (int)sizeof(uint32_t));
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, va::evict_select_kernel, p);
     if (e == cudaSuccess) {
         const int64_t most = (int64_t)p.half * p.units;  // threads' worth of work of a head, at most
         int64_t blocks = (most + va::kMoveThreads - 1) / va::kMoveThreads;
-        const int64_t cap = (8 * 152 + heads - 1) / heads;
+        const int64_t cap = (8 * sms + heads - 1) / heads;
         if (blocks > cap) blocks = cap;
         if (blocks < 1) blocks = 1;
         e = va::launch_pdl(va::evict_move_kernel, dim3((unsigned)blocks, heads), dim3(va::kMoveThreads), 0, s, p);
