@@ -789,7 +789,7 @@ int verify_attn_logprobs(const void *logits, int64_t stride, va_float_type type,
  * it sets VA_PAGES_BAD_ENTRY (flags may be NULL; the call only ORs into it).
  * Layouts: cache, block table and seq_lens as for verify_attn; weights fp32 and
  * slot_pos int32 [num_seqs, num_kv_heads, num_slots] with the strides given, rows
- * not on one another; keep_lens, recent_from, new_lens int32 [num_seqs], new_lens
+ * not on one another (weights may be NULL for no slots); keep_lens, recent_from, new_lens int32 [num_seqs], new_lens
  * apart from the others and from seq_lens; workspace: at least
  * verify_attn_evict_workspace_bytes (0 for sizes that are rejected), 16-byte
  * aligned, no initialisation; calls that share one must be ordered on one

@@ -317,7 +317,8 @@ int verify_attn_evict(void *k_pages, void *v_pages, float *k_scale, float *v_sca
     if (kv_dtype < VA_BF16 || kv_dtype > VA_INT2) return VA_ERR_UNSUPPORTED;
     const size_t need = verify_attn_evict_workspace_bytes(num_seqs, num_kv_heads, num_slots);
     if (need == 0 || block_table_stride < 0 || num_pages < 0 || num_sinks < 0 || stride_seq < 0 || stride_head < 0 ||
-        !k_pages || !v_pages || !block_table || !seq_lens || !weights || !keep_lens || !new_lens || !workspace)
+        !k_pages || !v_pages || !block_table || !seq_lens || (!weights && num_slots > 0) || !keep_lens || !new_lens ||
+        !workspace)
         return VA_ERR_INVALID_ARGUMENT;
     if (kv_dtype != VA_BF16 && (!k_scale || !v_scale)) return VA_ERR_INVALID_ARGUMENT;
     for (const void *x : {(const void *)k_pages, (const void *)v_pages, (const void *)workspace})

@@ -218,3 +218,14 @@ def test_a_batch_without_new_tokens(va, kv):
     b.weigh(va, plan, lse, w, slot_pos=pos, positions=torch.empty(0, dtype=torch.int32, device="cuda"))
     b.weigh(va, plan, lse, torch.empty(3, 2, 0, device="cuda"))
     assert (w == 2).all() and (pos == 7).all() and va.verify_attn_chunk_plan_device_flags(plan) == 0
+
+
+def test_evict_of_no_slots(va):
+    """Sequences of no tokens, whose weights have no address; one that says otherwise is flagged."""
+    kp, vp = (torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table = torch.zeros(3, 2, dtype=torch.int32, device="cuda")
+    lens, keep = cuda(np.array([0, 0, 5], np.int32)), cuda(np.array([0, 3, 2], np.int32))
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    new = va.verify_attn_evict(kp, vp, None, None, table, lens, torch.empty(3, 2, 0, device="cuda"), keep, "bf16", flags=flags)
+    assert new.tolist() == [0, 0, 5] and flags.item() == va.VA_PAGES_BAD_REQUEST
+    assert (kp == 0).all() and (vp == 0).all()
