@@ -1224,10 +1224,10 @@ def verify_attn_chunk_weights(plan: ChunkPlan, q, k_pages, k_scale, block_table,
     if num_pages > pages:
         raise ValueError(f"num_pages is {num_pages}, the cache has {pages}")
     bt, stride = _chunk_table(plan, block_table, index)
+    lp = _ptr(lse, "lse", torch.float32, index)
     n = lse.shape
     if len(n) != 2 or n[0] < plan.num_tokens or n[1] != plan.num_q_heads:
         raise ValueError(f"lse must be [{plan.num_tokens}, {plan.num_q_heads}], got {list(n)}")
-    lp = _ptr(lse, "lse", torch.float32, index)
     shape = (plan.num_seqs, plan.num_kv_heads, plan.max_len)
     wp, seq, head = _per_slot(weights, "weights", torch.float32, index, shape)
     sp = pos = None
@@ -1235,9 +1235,9 @@ def verify_attn_chunk_weights(plan: ChunkPlan, q, k_pages, k_scale, block_table,
         sp, *strides = _per_slot(slot_pos, "slot_pos", torch.int32, index, shape)
         if strides != [seq, head]:
             raise ValueError("slot_pos must have the strides of weights")
-        if positions is None or positions.dim() != 1 or positions.shape[0] < plan.num_tokens:
-            raise ValueError(f"slot_pos needs positions [{plan.num_tokens}]")
         pos = _ptr(positions, "positions", torch.int32, index)
+        if positions.dim() != 1 or positions.shape[0] < plan.num_tokens:
+            raise ValueError(f"slot_pos needs positions [{plan.num_tokens}], got {list(positions.shape)}")
     st, guard = _launch_on(device, stream)
     with guard:
         rc = (_lib or _load()).verify_attn_chunk_weights(plan._h, heads, kp, ks, bt, stride, num_pages or pages, lp, wp,
@@ -1323,15 +1323,15 @@ def verify_attn_evict(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens,
         raise ValueError(f"block_table must be [num_seqs, stride] and seq_lens [num_seqs], got {list(nt)} and "
                          f"{list(seq_lens.shape)}")
     B, stride = nt
-    if pages | B | Hkv | stride | weights.shape[-1] > _INT_MAX:
+    wp, seq, head = _per_slot(weights, "weights", f32, index, (B, Hkv, 0))
+    slots = weights.shape[2]
+    if pages | B | Hkv | stride | slots > _INT_MAX:
         raise _too_large("k_pages, block_table or weights", (*n, *nt, *weights.shape))
     if num_pages > pages:
         raise ValueError(f"num_pages is {num_pages}, the cache has {pages}")
     ks = vs = None
     if code != VA_BF16:
         ks, vs = _ptr(k_scale, "k_scale", f32, index, n[:3]), _ptr(v_scale, "v_scale", f32, index, n[:3])
-    wp, seq, head = _per_slot(weights, "weights", f32, index, (B, Hkv, 0))
-    slots = weights.shape[2]
     sp = None
     if slot_pos is not None:
         sp, *strides = _per_slot(slot_pos, "slot_pos", i32, index, (B, Hkv, slots))

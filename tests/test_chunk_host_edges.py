@@ -30,3 +30,38 @@ def test_outputs_and_moved_tensors_that_require_a_gradient_are_refused():
 def test_evict_workspace_of_more_slots_than_a_call_takes():
     size = va.library().verify_attn_evict_workspace_bytes
     assert size(1, 1, 2 ** 30) >= 2 ** 32 + 4 and size(1, 1, 2 ** 30 + 1) == size(1, 1, 2 ** 31 - 1) == 0
+
+
+class Cuda(torch.Tensor):
+    """A tensor that says it is on the current GPU: for checks that come before any address is used."""
+    is_cuda = True
+    device = torch.device("cuda", 0)
+
+    def get_device(self):
+        return 0
+
+
+def on_gpu(*shape, dtype=torch.float32):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(Cuda)
+
+
+@pytest.mark.parametrize("wrong", [None, [0, 1], 3.0, torch.zeros(2)])
+def test_arguments_that_are_no_gpu_tensors_are_refused_by_name(wrong):
+    plan = va.ChunkPlan(None, (1, 8, 2, 64, 2, 2, 2), 0)
+    i32 = torch.int32
+    good = dict(plan=plan, q=on_gpu(2, 8, 64, dtype=torch.bfloat16), k_pages=on_gpu(3, 16, 2, 64, dtype=torch.int8), k_scale=on_gpu(3, 16, 2),
+                block_table=on_gpu(1, 2, dtype=i32), lse=on_gpu(2, 8), weights=on_gpu(1, 2, 5), slot_pos=on_gpu(1, 2, 5, dtype=i32),
+                positions=on_gpu(2, dtype=i32))
+    for name in ("q", "k_pages", "k_scale", "block_table", "lse", "weights", "slot_pos", "positions"):
+        if name == "slot_pos" and wrong is None:
+            continue
+        with pytest.raises(ValueError, match=name):
+            va.verify_attn_chunk_weights(**dict(good, **{name: wrong}))
+    pages, lens = good["k_pages"], on_gpu(1, dtype=i32)
+    good = dict(k_pages=pages, v_pages=pages, k_scale=good["k_scale"], v_scale=good["k_scale"], block_table=good["block_table"],
+                seq_lens=lens, weights=good["weights"], keep_lens=lens, kv_dtype="int8")
+    for name in ("k_pages", "v_pages", "k_scale", "v_scale", "block_table", "seq_lens", "weights", "keep_lens"):
+        with pytest.raises(ValueError, match=name):
+            va.verify_attn_evict(**dict(good, **{name: wrong}))
+    with pytest.raises(ValueError, match="tokens"):
+        va.verify_attn_logprobs(on_gpu(2, 9), wrong)
