@@ -197,7 +197,6 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) weights_kernel(const __gr
     auto my_row = [&](int x) { return kt * 128 + (warp & 3) * 32 + 16 * h + 8 * x + (lane >> 2); };
     uint64_t c2[2];
     int key[2], page[2];
-    float old = 0.f;  // what the block's keys have already, of the first threads
     if (warp < C::kSumWarps) {
         float scale[2];
 #pragma unroll
@@ -294,7 +293,6 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) weights_kernel(const __gr
         if (!__all_sync(0xffffffffu, mbar_wait(bar(kDone), 0, kWaitNs))) ok = false;
     } else {
         // ------------------------------------------------------------ sums
-        const int kt = warp >> 3, h = (warp >> 2) & 1, c = 2 * (lane & 3);
         const uint32_t half_tm = tmem + ((uint32_t)((warp & 3) * 32 + 16 * h) << 16);
         float sum[2] = {0.f, 0.f}, lost[2] = {0.f, 0.f};
         const int last_key = it.key0 + C::kKeyTiles * 128 - 1;  // of the block: both of a CTA's tiles take one view
