@@ -479,6 +479,7 @@ __global__ void __launch_bounds__(kThreads + 32, kCtas) logprobs_kernel(const Lo
             }
             take_chunk(c);
             if (c % kTake == kTake - 1) before += counted.take();
+            fence_proxy_async_smem();  // the loads are done: the arrival by itself does not wait for their values
             __syncwarp();
             if (lane == 0) mbar_arrive(empty(st));
         }
