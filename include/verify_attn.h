@@ -710,7 +710,11 @@ int verify_attn_chunk_plan_device_flags(const va_chunk_plan *plan, int clear, in
  * behind the last sequence's are left as they are.  out may not overlap q.
  * block_table int32 [num_seqs, block_table_stride].  num_pages > 0: entries
  * outside [0, num_pages) are skipped (their keys read as absent; a row without
- * any key is 0 with lse -inf) and flagged; 0: unchecked.  A plan without
+ * any key is 0 with lse -inf) and flagged; 0: unchecked.  Scores, sums and out's
+ * sum are binary32; a probability (with its value's scale) is rounded to bf16 for
+ * a bf16 cache, to fp16 for codes, before it meets the value, as in verify_attn:
+ * at most 2^-8 or 2^-11 of sum_j exp(s_j - lse) |Vhat[j]|, beside out's own
+ * rounding.  Value scales of codes: up to 2^107.  A plan without
  * tokens: nothing is looked at or done, here and in verify_attn_chunk_weights.
  * Returns VA_OK when enqueued, VA_ERR_NO_PLAN, VA_ERR_INVALID_ARGUMENT, VA_ERR_CUDA. */
 int verify_attn_chunk(const va_chunk_plan *plan, const va_heads *q, const void *k_pages,
@@ -724,7 +728,8 @@ int verify_attn_chunk(const va_chunk_plan *plan, const va_heads *q, const void *
  *         exp(s_j - lse[row, h])
  *     weights[b, g, j] = w, or weights[b, g, j] + w for accumulate != 0 and
  *                        j < L_b - n_b (the new tokens start from nothing)
- * with lse as verify_attn_chunk gives it (a row with lse -inf gives nothing).
+ * with lse as verify_attn_chunk gives it (a row with lse -inf gives nothing; one
+ * that a caller mutes by setting its lse to -inf needs finite queries).
  * Entry (b, g, j) of weights is weights[b * weights_stride_seq + g *
  * weights_stride_head + j]; rows (b, g) may not lie on one another; entries from
  * L_b on are left as they are.  slot_pos
