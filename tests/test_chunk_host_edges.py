@@ -65,3 +65,20 @@ def test_arguments_that_are_no_gpu_tensors_are_refused_by_name(wrong):
             va.verify_attn_evict(**dict(good, **{name: wrong}))
     with pytest.raises(ValueError, match="tokens"):
         va.verify_attn_logprobs(on_gpu(2, 9), wrong)
+
+
+def test_numbers_past_32_bits_are_refused_not_cut():
+    """2^32 + 5 is 5 in its low 32 bits."""
+    for far in (torch.tensor([2 ** 32 + 5]), [2 ** 32 + 5], torch.tensor([-2 ** 32 + 5])):
+        for new, lens in ((far, [100]), ([5], far)):
+            with pytest.raises((ValueError, OverflowError)):
+                va.verify_attn_chunk_plan_describe(new, lens, 8, 2, 64, "int8", 152)
+            with pytest.raises((ValueError, OverflowError)):
+                va.verify_attn_chunk_plan(new, lens, 8, 2, 64, "int8")
+        with pytest.raises((ValueError, OverflowError)):
+            va.verify_attn_plan_describe(far, 4, 8, 2, 64, "int8", 152)
+    assert va.verify_attn_chunk_plan_describe(torch.tensor([5]), torch.tensor([100]), 8, 2, 64, "int8", 152)[0]["num_tokens"] == 5
+    pages, lens = on_gpu(3, 16, 2, 64, dtype=torch.bfloat16), on_gpu(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="num_sinks"):
+        va.verify_attn_evict(pages, pages, None, None, on_gpu(1, 2, dtype=torch.int32), lens, on_gpu(1, 2, 5), lens, "bf16",
+                             num_sinks=2 ** 32)
