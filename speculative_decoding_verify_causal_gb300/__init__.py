@@ -235,7 +235,10 @@ def _host_lens(seq_lens):
             seq_lens = seq_lens.detach().cpu().numpy()
     except ImportError:  # pragma: no cover
         pass
-    return np.ascontiguousarray(np.asarray(seq_lens, dtype=np.int32).reshape(-1))
+    lens = np.asarray(seq_lens)
+    if lens.size and not (-2 ** 31 <= lens.min() and lens.max() < 2 ** 31):
+        raise ValueError(f"lengths between {lens.min()} and {lens.max()} are past 32 bits")
+    return np.ascontiguousarray(lens.astype(np.int32, copy=False).reshape(-1))
 
 
 class Plan:
@@ -1329,6 +1332,8 @@ def verify_attn_evict(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens,
         raise _too_large("k_pages, block_table or weights", (*n, *nt, *weights.shape))
     if num_pages > pages:
         raise ValueError(f"num_pages is {num_pages}, the cache has {pages}")
+    if num_sinks > _INT_MAX:
+        raise ValueError(f"num_sinks is {num_sinks}, past 32 bits")
     ks = vs = None
     if code != VA_BF16:
         ks, vs = _ptr(k_scale, "k_scale", f32, index, n[:3]), _ptr(v_scale, "v_scale", f32, index, n[:3])
