@@ -27,10 +27,11 @@
 // sums and O are binary32.
 //
 // Bound.  Two tiles of rows by 80 keys at head_dim 128 are 1,470 clocks of the tensor pipe.  bf16, 8,192 tokens of 32
-// heads of 128: 368 us, 78 % of the measured bf16 rate: the tensor pipe, less the tiles on the diagonal, items' starts
-// and ends.  Codes: the warps' issue slots (71 % taken; a softmax warp about 400 instructions a tile, of which 20 each
-// for the two scales) at head_dim 128, 48 sequences, 952 us; the shared memory's bandwidth at 256, where a tile has one
-// of rows and so twice the panels a product, 2,000 on 23,000 tokens, 1,522 us.
+// heads of 128: 365 us at 2,070 MHz, 78 % of the measured bf16 rate, 389 us in a long run under the power cap (1,912 MHz):
+// the tensor pipe, less the tiles on the diagonal, items' starts and ends.  Codes: the warps' issue slots (74 % taken; a
+// softmax warp about 400 instructions a tile, of which 20 each for the two scales) at head_dim 128, 48 sequences, 948 us;
+// the shared memory's bandwidth at 256, where a tile has one of rows and so twice the panels a product, 2,000 on 23,000
+// tokens, 1,520 us (951 with a bf16 cache, which needs no conversion).
 // Why 80 keys: probabilities that take the place of their scores (64 keys, the first kernel) hold the next scores back
 // until their product is done; with 80 keys both have slots of their own beside O, which with an issuing warp for each
 // tile of rows took the prompt from 477 to 417 us and the 48 sequences from 1,498 to 1,145.  Sixteen softmax warps
@@ -932,7 +933,11 @@ __global__ void __launch_bounds__(Cfg<D, DT>::kThreads, 1) chunk_kernel(const __
 // written in pieces of kCols elements.  kWays threads share a row's partials: one after the other, each waiting for its
 // loads, ten partials of a question of 45 tokens (24 heads of 256) took longer than the attention itself, 30 us in all
 // against 22 with 8 x 4.  A merge that fills the GPU prefers wider pieces and fewer ways: 384 tiles' 5 partials, 2,000
-// tokens on 23,000, took 1,523 us in all with 8 x 4, 1,495 with 16 x 1, 1,485 with 16 x 2.
+// tokens on 23,000, took 1,523 us in all with 8 x 4, 1,495 with 16 x 1, 1,485 with 16 x 2.  The border is where the CTAs of
+// the second are four to an SM.  Verify blocks of 16 on 6,000 tokens, whole calls, 8 x 4 against 16 x 2, by tiles times
+// pieces of 16: head_dim 64, bf16: 32: 15 and 27 us, 320: 41 and 43, 512: 51.3 both, 768: 82 and 80; 128, int8: 64: 19 and 29,
+// 256: 27 and 29, 512: 53.3 both, 768: 70 and 68, 1,408: 162 and 155; 256, int8: 64: 23 and 41, 512: 46 and 45, 640: 59.5 both,
+// 1,024: 83 and 80, 2,048: 134 and 125.
 template <int kCols, int kWays>
 __global__ void __launch_bounds__(kMmaRows * kWays) chunk_combine_kernel(const ChunkCombineParams p) {
     __shared__ uint32_t tile[kMmaRows][kCols / 2 + 1];
