@@ -228,6 +228,9 @@ def _options(block_table_stride=0, tokens_per_split=0, path="auto", num_pages=0)
                     PATH_CODES[path] if isinstance(path, str) else int(path), int(num_pages))
 
 
+_current = threading.local()  # .table: rows and stride of the table of this thread's current plan
+
+
 def _host_lens(seq_lens):
     try:
         import torch
@@ -241,14 +244,28 @@ def _host_lens(seq_lens):
     return np.ascontiguousarray(lens.astype(np.int32, copy=False).reshape(-1))
 
 
+def _table_stride(lens, stride):
+    """Entries between a block table's rows: as given, or the longest sequence's pages."""
+    return int(stride) if stride > 0 else (int(lens.max(initial=0)) + PAGE_SIZE - 1) // PAGE_SIZE
+
+
+def _check_table(block_table, num_seqs, stride):
+    """The kernels step through the table by ``stride``; of one sequence a wider row will do.  (A table that is not
+    [num_seqs, stride] is taken as it lies.)"""
+    n = getattr(block_table, "shape", ())
+    if len(n) == 2 and (n[0] < num_seqs or n[1] < stride or (n[1] != stride and num_seqs > 1)):
+        raise ValueError(f"block_table is {list(n)}, the call goes by [{num_seqs}, {stride}]: give its width as block_table_stride")
+
+
 class Plan:
     """Owning handle of a ``va_plan`` (freed on ``destroy()`` or collection)."""
 
-    def __init__(self, handle, seq_lens, T, kv_dtype):
+    def __init__(self, handle, seq_lens, T, kv_dtype, block_table_stride=0):
         self._h = ctypes.c_void_p(handle)
         self.seq_lens = seq_lens
         self.T = T
         self.kv_dtype = kv_dtype
+        self.block_table_stride = _table_stride(seq_lens, block_table_stride)
 
     @property
     def handle(self):
@@ -283,7 +300,9 @@ def verify_attn_plan(seq_lens, T, num_q_heads, num_kv_heads, head_dim, kv_dtype,
                                  int(num_kv_heads), int(head_dim), _dtype_code(kv_dtype), int(num_sms),
                                  ctypes.byref(opts), ctypes.byref(out))
     _check(rc, "verify_attn_plan")
-    return Plan(out.value, lens, int(T), _dtype_code(kv_dtype))
+    plan = Plan(out.value, lens, int(T), _dtype_code(kv_dtype), opts.block_table_stride)
+    _current.table = len(lens), plan.block_table_stride
+    return plan
 
 
 def verify_attn_plan_destroy(plan: Plan):
@@ -400,6 +419,7 @@ def verify_attn_with_plan(plan: Plan, q, k_pages, v_pages, k_scale, v_scale, blo
                           out, lse=None, stream=None):
     """Enqueue verify attention with an explicit plan on ``stream`` (default:
     torch's current stream).  Writes ``out`` (and ``lse`` if given)."""
+    _check_table(block_table, len(plan.seq_lens), plan.block_table_stride)
     args, tail, s = _marshal(plan.kv_dtype, q, k_pages, v_pages, k_scale, v_scale, block_table,
                              seq_lens, out, lse, stream)
     _check(_load().verify_attn_with_plan(plan.handle, *args, int(T), *tail, s), "verify_attn_with_plan")
@@ -420,6 +440,9 @@ def verify_attn(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, T,
             kv_code = {D // 2: VA_INT4, D // 4: VA_INT2}.get(k_pages.shape[-1], kv_code)
     else:
         kv_code = _dtype_code(kv_dtype)
+    table = getattr(_current, "table", None)
+    if table is not None:
+        _check_table(block_table, *table)
     args, tail, s = _marshal(kv_code, q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens,
                              out, lse, stream)
     _check(_load().verify_attn(*args, int(T), *tail, s), "verify_attn")
@@ -456,6 +479,7 @@ def verify_attn_noalloc(seq_lens_host, T, num_q_heads, num_kv_heads, head_dim, k
     ``verify_attn_noalloc_flags``)."""
     lens = _host_lens(seq_lens_host)
     code = _dtype_code(kv_dtype)
+    _check_table(block_table, len(lens), _table_stride(lens, block_table_stride))
     args, tail, s = _marshal(code, q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, out, lse,
                              stream)
     rc = _load().verify_attn_noalloc(lens.ctypes.data_as(ctypes.c_void_p), len(lens), int(T), int(num_q_heads),

@@ -1,4 +1,5 @@
 """Host: refusals and empty calls of the operators of a prompt worked in chunks, beside those of ``test_chunk_host``."""
+import numpy as np
 import pytest
 
 import speculative_decoding_verify_causal_gb300 as va
@@ -82,3 +83,25 @@ def test_numbers_past_32_bits_are_refused_not_cut():
     with pytest.raises(ValueError, match="num_sinks"):
         va.verify_attn_evict(pages, pages, None, None, on_gpu(1, 2, dtype=torch.int32), lens, on_gpu(1, 2, 5), lens, "bf16",
                              num_sinks=2 ** 32)
+
+
+def test_a_block_table_of_another_width_than_the_plan_is_refused():
+    """The kernels step through the table by the plan's stride: rows of another width are read from the wrong places."""
+    bf, i32 = torch.bfloat16, torch.int32
+    q, pages, lens = on_gpu(2, 4, 8, 64, dtype=bf), on_gpu(9, 16, 2, 64, dtype=bf), on_gpu(2, dtype=i32)
+    plan = va.Plan(None, np.array([40, 100], np.int32), 4, 0)
+    assert plan.block_table_stride == 7
+    assert va.Plan(None, np.array([40, 100], np.int32), 4, 0, 12).block_table_stride == 12
+    for table in (on_gpu(2, 8, dtype=i32), on_gpu(2, 6, dtype=i32), on_gpu(1, 7, dtype=i32)):
+        with pytest.raises(ValueError, match="block_table.*7"):
+            va.verify_attn_with_plan(plan, q, pages, pages, None, None, table, lens, 4, q)
+        with pytest.raises(ValueError, match="block_table.*7"):
+            va.verify_attn_noalloc([40, 100], 4, 8, 2, 64, "bf16", q, pages, pages, None, None, table, lens, q)
+        with pytest.raises(ValueError, match="block_table.*9"):
+            va.verify_attn_noalloc([40, 100], 4, 8, 2, 64, "bf16", q, pages, pages, None, None, table, lens, q, block_table_stride=9)
+    one = va.Plan(None, np.array([40], np.int32), 4, 0)  # one sequence: a wider row is read no further than it has to be
+    with pytest.raises(ValueError, match="block_table.*3"):
+        va.verify_attn_with_plan(one, q[:1], pages, pages, None, None, on_gpu(1, 2, dtype=i32), lens, 4, q)
+    for table in (on_gpu(1, 8, dtype=i32), on_gpu(1, 3, dtype=i32), on_gpu(5, dtype=i32)):
+        with pytest.raises(va.VerifyAttnError):  # no handle: past the check
+            va.verify_attn_with_plan(one, q[:1], pages, pages, None, None, table, lens, 4, q, stream=0)
